@@ -3,16 +3,16 @@
 Four kinds of pass, over 32 query heads, 8 KV heads and head_dim 128:
 
   decode  attention of 1 to 4 query tokens a request over a cache held in 4
-          bits (int4 codes, one bf16 scale for every 32 dims of a row),
-          contiguous or paged
+          bits (e2m1 codes, an e4m3 scale for every 16 dims of a row and an
+          fp32 scale for all keys and one for all values), contiguous or paged
   write   norm, rotary embedding (one position axis, or time, height and
           width) and the cache write of many tokens at once, 16-bit cache
-  store   the same write into an int4, int8 or e4m3 cache, then the rows read
+  store   the same write into an fp4, int8 or e4m3 cache, then the rows read
           back to 16 bits, as a prompt taken in chunks does
   read    the rows of a cache of any format read back to a dense 16-bit cache
 
 A 4-bit row is 64 bytes: byte j holds dims 2j (low nibble) and 2j + 1 (high
-nibble) as two's complement codes; kv_scales holds 4 bf16 scales a row.
+nibble) as e2m1 codes; kv_scales holds 8 e4m3 scales a row.
 """
 import math
 
@@ -20,8 +20,10 @@ import torch
 
 own = False
 
-HQ, HKV, D, GROUP = 32, 8, 128, 32
+HQ, HKV, D, GROUP = 32, 8, 128, 16
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+# the scales of all keys and of all values that a program has from its calibration
+SCALES = {"fp4": (10 / 1024, 9 / 1024), "e4m3": (1 / 32, 1 / 32)}
 
 
 # ------------------------------------------------------------------- cases
@@ -51,13 +53,13 @@ def listed():
         {"name": "write 8192 image", "kind": "write", "dtype": "f16", "fmt": "f16", "tokens": 8192, "batch": 4,
          "capacity": 2112, "page": 0, "axes": 3, "interleaved": True, "fused": True, "norm": True},
         # a chunk of a prompt into a paged 4-bit cache, then the whole prefix back for the chunk's attention
-        {"name": "store int4 4096", "kind": "store", "dtype": "bf16", "fmt": "i4", "tokens": 4096, "batch": 4,
+        {"name": "store fp4 4096", "kind": "store", "dtype": "bf16", "fmt": "fp4", "tokens": 4096, "batch": 4,
          "capacity": 4096, "page": 64, "axes": 3, "interleaved": True, "fused": True, "norm": True},
         # the same of an int8 cache with odd sizes, positions in blocks of the axes, no norm
         {"name": "store int8 1531", "kind": "store", "dtype": "f16", "fmt": "i8", "tokens": 1531, "batch": 3,
          "capacity": 1000, "page": 0, "axes": 3, "interleaved": False, "fused": False, "norm": False},
         # the prefixes of long contexts read back from a 4-bit pool
-        {"name": "read int4 8x32768 paged", "kind": "read", "dtype": "bf16", "fmt": "i4", "batch": 8,
+        {"name": "read fp4 8x32768 paged", "kind": "read", "dtype": "bf16", "fmt": "fp4", "batch": 8,
          "capacity": 32768, "len_lo": 16384, "len_hi": 32768, "page": 256, "starts": False},
         # one short request's e4m3 cache: latency
         {"name": "read e4m3 1x1024", "kind": "read", "dtype": "f16", "fmt": "e4m3", "batch": 1, "capacity": 1024,
@@ -91,7 +93,7 @@ def draw(rng):
         per = -(-tokens // batch)
         capacity = -(-(per + rng.randint(0, max(1, per // 2))) // (page or 8)) * (page or 8)
         axes = rng.choice([1, 3])
-        return {"kind": kind, "dtype": dtype, "fmt": dtype if kind == "write" else rng.choice(["i4", "i4", "i8", "e4m3"]),
+        return {"kind": kind, "dtype": dtype, "fmt": dtype if kind == "write" else rng.choice(["fp4", "fp4", "i8", "e4m3"]),
                 "tokens": tokens, "batch": batch, "capacity": capacity, "page": page, "axes": axes,
                 "interleaved": axes == 3 and rng.random() < 0.5, "fused": rng.random() < 0.5,
                 "norm": rng.random() < 0.8}
@@ -99,7 +101,7 @@ def draw(rng):
     capacity = _log(rng, 16, max(16, (1 << 17) // batch))
     capacity = -(-capacity // (page or 8)) * (page or 8)
     hi = rng.randint(1, capacity)
-    fmt = rng.choice(["i4", "i4", "i8", "e4m3", dtype])
+    fmt = rng.choice(["fp4", "fp4", "i8", "e4m3", dtype])
     return {"kind": kind, "dtype": dtype, "fmt": fmt, "batch": batch, "capacity": capacity,
             "len_lo": rng.choice([hi, 0]), "len_hi": hi, "page": page, "starts": rng.random() < 0.5}
 
@@ -120,7 +122,7 @@ def _share(case):
 
 
 def _row_bytes(fmt):
-    return {"f16": 256, "bf16": 256, "e4m3": 128, "i8": 130, "i4": 72}[fmt]
+    return {"f16": 256, "bf16": 256, "e4m3": 128, "i8": 130, "fp4": 72}[fmt]
 
 
 def work(case):
@@ -129,7 +131,7 @@ def work(case):
         tokens = B * (case["len_lo"] + case["len_hi"]) / 2
     if kind == "decode":
         T = case["q_len"]
-        return {"bytes": tokens * 16 * _row_bytes("i4") + 2 * B * T * HQ * D * 2 + 4 * B,
+        return {"bytes": tokens * 16 * _row_bytes("fp4") + 2 * B * T * HQ * D * 2 + 4 * B,
                 "flops": 4 * tokens * T * HQ * D}
     if kind == "read":
         if case["starts"]:
@@ -161,33 +163,40 @@ def _randn(shape, seed, k, dtype=torch.float32):
     return torch.randn(shape, generator=_gen(seed, k), device="cuda", dtype=dtype)
 
 
-def _quantise(x, fmt):
-    """(codes, scales) of rows x [..., 128] in 32 or 64 bits."""
-    if fmt == "i4":
-        g = x.unflatten(-1, (D // GROUP, GROUP))
-        s = (g.abs().amax(-1) / 7).to(torch.bfloat16)
-        s = torch.where(s == 0, torch.ones_like(s), s)
-        c = (g / s.to(x.dtype).unsqueeze(-1)).round().clamp(-7, 7).to(torch.int8).flatten(-2) & 15
-        return (c[..., 0::2] | (c[..., 1::2] << 4)).view(torch.uint8), s
+def _quantise(x, fmt, scale):
+    """(codes, scales) of rows x [..., 128] in 32 or 64 bits; `scale` is the one of all of them."""
+    if fmt == "fp4":
+        g = (x / scale).unflatten(-1, (D // GROUP, GROUP))
+        s = (g.abs().amax(-1) / 6).clamp(max=448).to(torch.float32).to(torch.float8_e4m3fn)
+        wide = s.to(x.dtype).unsqueeze(-1)
+        t = torch.where(wide > 0, g / wide, torch.zeros_like(g))
+        m = t.abs().clamp(max=6)
+        step = torch.where(m < 2, 0.5, torch.where(m < 4, 1.0, 2.0)).to(x.dtype)
+        m = (m / step).round() * step  # 0, 0.5, 1, 1.5, 2, 3, 4, 6: to the nearest, ties to the even code
+        c = torch.where(m < 2, 2 * m, torch.where(m < 4, m + 2, m / 2 + 4)).to(torch.uint8)
+        c = (c | ((t < 0).to(torch.uint8) << 3)).flatten(-2)
+        return c[..., 0::2] | (c[..., 1::2] << 4), s.view(torch.uint8)
     if fmt == "i8":
         s = (x.abs().amax(-1) / 127).to(torch.bfloat16)
         s = torch.where(s == 0, torch.ones_like(s), s)
         return (x / s.to(x.dtype).unsqueeze(-1)).round().clamp(-127, 127).to(torch.int8), s
     if fmt == "e4m3":
-        return x.clamp(-448, 448).to(torch.float32).to(torch.float8_e4m3fn).view(torch.uint8), None
+        return (x / scale).clamp(-448, 448).to(torch.float32).to(torch.float8_e4m3fn).view(torch.uint8), None
     return x.to(TYPES[fmt]), None
 
 
-def _values(codes, scales, fmt):
+def _values(codes, scales, fmt, scale):
     """The rows that codes and scales stand for, in 32 bits."""
-    if fmt == "i4":
-        n = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).to(torch.int8)
-        x = torch.where(n > 7, n - 16, n).to(torch.float32).unflatten(-1, (D // GROUP, GROUP))
-        return (x * scales.to(torch.float32).unsqueeze(-1)).flatten(-2)
+    if fmt == "fp4":
+        n = torch.stack((codes & 15, codes >> 4), -1).flatten(-2)
+        m = (n & 7).to(torch.float32)
+        m = torch.where(m < 4, 0.5 * m, torch.where(m < 6, m - 2, 2 * m - 8))
+        x = torch.where(n > 7, -m, m).unflatten(-1, (D // GROUP, GROUP))
+        return (x * (scales.view(torch.float8_e4m3fn).to(torch.float32) * scale).unsqueeze(-1)).flatten(-2)
     if fmt == "i8":
         return codes.to(torch.float32) * scales.to(torch.float32).unsqueeze(-1)
     if fmt == "e4m3":
-        return codes.view(torch.float8_e4m3fn).to(torch.float32)
+        return codes.view(torch.float8_e4m3fn).to(torch.float32) * scale
     return codes.to(torch.float32)
 
 
@@ -196,23 +205,25 @@ def _cache(case, fmt, seed):
     Contiguous [B,2,8,C,...], or a pool of shuffled pages with its block table."""
     B, C, page = case["batch"], case["capacity"], case["page"]
     units, rows = (B * C // page, page) if page else (B, C)
-    width = {"i4": 64, "i8": D, "e4m3": D, "f16": D, "bf16": D}[fmt]
-    kind = {"i4": torch.uint8, "i8": torch.int8, "e4m3": torch.uint8}.get(fmt) or TYPES[fmt]
+    width = 64 if fmt == "fp4" else D
+    kind = {"fp4": torch.uint8, "i8": torch.int8, "e4m3": torch.uint8}.get(fmt) or TYPES[fmt]
     codes = torch.empty((units, 2, HKV, rows, width), dtype=kind, device="cuda")
     scales = None
-    if fmt in ("i4", "i8"):
-        scales = torch.empty((units, 2, HKV, rows) + ((D // GROUP,) if fmt == "i4" else ()), dtype=torch.bfloat16,
-                             device="cuda")
+    if fmt == "fp4":
+        scales = torch.empty((units, 2, HKV, rows, D // GROUP), dtype=torch.uint8, device="cuda")
+    elif fmt == "i8":
+        scales = torch.empty((units, 2, HKV, rows), dtype=torch.bfloat16, device="cuda")
     gain = torch.ones((2, HKV, 1, D), device="cuda")
     gain[0] = torch.exp(0.4 * _randn((HKV, 1, D), seed, 3))
     step = max(1, (1 << 27) // (2 * HKV * rows * D))
     for k in range(0, units, step):
         n = min(step, units - k)
         x = _randn((n, 2, HKV, rows, D), seed, 100 + k) * gain
-        c, s = _quantise(x, fmt)
-        codes[k:k + n] = c
-        if scales is not None:
-            scales[k:k + n] = s
+        for plane in (0, 1):
+            c, s = _quantise(x[:, plane], fmt, SCALES.get(fmt, (1, 1))[plane])
+            codes[k:k + n, plane] = c
+            if scales is not None:
+                scales[k:k + n, plane] = s
     table = None
     if page:
         order = torch.randperm(units, generator=_gen(seed, 4), device="cuda")
@@ -223,9 +234,9 @@ def _cache(case, fmt, seed):
 def prepare(case, seed):
     kind, B = case["kind"], case["batch"]
     dtype = TYPES[case["dtype"]]
-    s = {"kind": kind, "case": case, "dtype": dtype}
+    fmt = "fp4" if kind == "decode" else case["fmt"]
+    s = {"kind": kind, "case": case, "dtype": dtype, "scale": SCALES.get(fmt, (1.0, 1.0))}
     if kind in ("decode", "read"):
-        fmt = "i4" if kind == "decode" else case["fmt"]
         s["lens_host"] = _lengths(case, seed)
         s["lens"] = s["lens_host"].to(torch.int32).cuda()
         s["kv"], s["scales"], s["table"] = _cache(case, fmt, seed)
@@ -243,7 +254,7 @@ def prepare(case, seed):
         import gqa_decode_attention_sm_gb300 as gq
         if kind == "decode" and case["q_len"] == 1 and not case["page"]:
             s["plan"] = gq.prepare({"Q": s["q"], "KV": s["kv"], "KV_SCALES": s["scales"], "O": s["out"],
-                                    "sequence_lengths": s["lens"]})
+                                    "sequence_lengths": s["lens"]}, k_scale=s["scale"][0], v_scale=s["scale"][1])
         elif kind == "decode":
             s["splits"] = gq.plan(B, case["capacity"], 4)
             s["workspace"] = torch.zeros(gq.workspace_size(B * case["q_len"], case["capacity"], s["splits"]),
@@ -319,14 +330,15 @@ def _plain_decode(s):
     T, C, B = case["q_len"], case["capacity"], case["batch"]
     q = s["q"].to(torch.float32).view(B, T, HKV, HQ // HKV, D).permute(0, 2, 1, 3, 4).reshape(B, HKV, T * 4, D)
     kv, sc = _rows_of(s["kv"], s["table"]), _rows_of(s["scales"], s["table"])
-    scores = torch.matmul(q, _values(kv[:, 0], sc[:, 0], "i4").transpose(-1, -2)) / math.sqrt(D)  # [B, 8, T*4, C]
+    k = _values(kv[:, 0], sc[:, 0], "fp4", s["scale"][0])
+    scores = torch.matmul(q, k.transpose(-1, -2)) / math.sqrt(D)  # [B, 8, T*4, C]
     last = s["lens"].view(B, 1) - T + 1 + torch.arange(T, device="cuda").view(1, T)  # slots below it are seen
     seen = torch.arange(C, device="cuda") < last.repeat_interleave(4, 1).view(B, 1, T * 4, 1)
     scores = torch.where(seen, scores, torch.full_like(scores, -math.inf))
     top = scores.amax(-1, keepdim=True)
     p = torch.exp(scores - torch.where(torch.isinf(top), torch.zeros_like(top), top))
     total = p.sum(-1, keepdim=True)
-    o = torch.matmul(p, _values(kv[:, 1], sc[:, 1], "i4"))
+    o = torch.matmul(p, _values(kv[:, 1], sc[:, 1], "fp4", s["scale"][1]))
     o = torch.where(total > 0, o / total, torch.zeros_like(o))
     return o.view(B, HKV, T, 4, D).permute(0, 2, 1, 3, 4).reshape(s["q"].shape).to(s["dtype"])
 
@@ -334,7 +346,9 @@ def _plain_decode(s):
 def _plain_read(s):
     case = s["case"]
     C = case["capacity"]
-    x = _values(_rows_of(s["kv"], s["table"]), _rows_of(s["scales"], s["table"]), case["fmt"])
+    kv, sc = _rows_of(s["kv"], s["table"]), _rows_of(s["scales"], s["table"])
+    x = torch.stack([_values(kv[:, p], None if sc is None else sc[:, p], case["fmt"], s["scale"][p])
+                     for p in (0, 1)], 1)
     first = s["starts"] if s["starts"] is not None else torch.zeros_like(s["lens"])
     at = (torch.arange(C, device="cuda") + first.view(-1, 1)).clamp(max=C - 1).long()  # [B, C]
     if s["starts"] is not None:
@@ -378,7 +392,7 @@ def _plain_write(s):
     if s["table"] is not None:
         rows, slots = s["table"][rows, slots // case["page"]].long(), slots % case["page"]
     for plane, x in ((0, k), (1, s["v"].double())):
-        c, sc = _quantise(x, case["fmt"])
+        c, sc = _quantise(x, case["fmt"], s["scale"][plane])
         s["kv"][rows, plane, :, slots] = c
         if sc is not None:
             s["scales"][rows, plane, :, slots] = sc
@@ -391,18 +405,19 @@ def _plain_write(s):
 def _run_own(s):
     import gqa_decode_attention_sm_gb300 as gq
     case = s["case"]
+    scale = dict(k_scale=s["scale"][0], v_scale=s["scale"][1])
     if s["kind"] == "decode":
         if "plan" in s:
             return {"out": gq.launch(s["plan"])}
         if s["table"] is not None:
             return {"out": gq.gqa_decode_paged(s["q"], s["kv"], s["table"], s["lens"], out=s["out"],
                                                num_splits=s["splits"], workspace=s["workspace"],
-                                               kv_scales=s["scales"])}
+                                               kv_scales=s["scales"], **scale)}
         return {"out": gq.gqa_decode_verify(s["q"], s["kv"], s["lens"], kv_scales=s["scales"], out=s["out"],
-                                            num_splits=s["splits"], workspace=s["workspace"])}
+                                            num_splits=s["splits"], workspace=s["workspace"], **scale)}
     if s["kind"] in ("write", "store"):
         how = dict(q_out=s["q_out"], mrope_section=s["section"], mrope_interleaved=case["interleaved"],
-                   kv_scales=s["scales"])
+                   kv_scales=s["scales"], **scale)
         if s["table"] is not None:
             gq.write_kv_paged(s["q"], s["k"], s["v"], s["qw"], s["kw"], s["pos"], s["rows"], s["slots"], s["kv"],
                               s["table"], **how)
@@ -411,9 +426,10 @@ def _run_own(s):
         if s["kind"] == "write":
             return {"q_out": s["q_out"], "kv": s["kv"]}
     if s["table"] is not None:
-        kv = gq.read_kv_paged(s["kv"], s["table"], s["lens"], starts=s["starts"], out=s["out"], kv_scales=s["scales"])
+        kv = gq.read_kv_paged(s["kv"], s["table"], s["lens"], starts=s["starts"], out=s["out"], kv_scales=s["scales"],
+                              **scale)
     else:
-        kv = gq.read_kv(s["kv"], s["lens"], starts=s["starts"], out=s["out"], kv_scales=s["scales"])
+        kv = gq.read_kv(s["kv"], s["lens"], starts=s["starts"], out=s["out"], kv_scales=s["scales"], **scale)
     return {"kv": kv} if s["kind"] == "read" else {"q_out": s["q_out"], "kv": kv}
 
 
@@ -431,17 +447,20 @@ def _row64(s, b, plane, fmt, L):
     else:
         codes = s["kv"][b, plane, :, :L]
         scales = None if s["scales"] is None else s["scales"][b, plane, :, :L]
-    if fmt == "i4":
+    if fmt == "fp4":
+        level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+        level = torch.cat((level, -level))
         x = torch.empty((HKV, L, D), dtype=torch.float64, device="cuda")
-        x[..., 0::2] = ((codes.to(torch.int16) + 8) % 16 - 8).double()
-        x[..., 1::2] = ((codes.to(torch.int16) // 16 + 8) % 16 - 8).double()
+        x[..., 0::2] = level[codes.long() % 16]
+        x[..., 1::2] = level[codes.long() // 16]
+        step = scales.contiguous().view(torch.float8_e4m3fn).double() * s["scale"][plane]
         for g in range(D // GROUP):
-            x[..., GROUP * g:GROUP * (g + 1)] *= scales[..., g:g + 1].double()
+            x[..., GROUP * g:GROUP * (g + 1)] *= step[..., g:g + 1]
         return x
     if fmt == "i8":
         return codes.double() * scales.double()[..., None]
     if fmt == "e4m3":
-        return codes.contiguous().view(torch.float8_e4m3fn).double()
+        return codes.contiguous().view(torch.float8_e4m3fn).double() * s["scale"][plane]
     return codes.double()
 
 
@@ -456,7 +475,7 @@ def exact(case, seed):
             L = int(s["lens_host"][b])
             if not L:
                 continue
-            K, V = (_row64(s, b, plane, "i4", L) for plane in (0, 1))
+            K, V = (_row64(s, b, plane, "fp4", L) for plane in (0, 1))
             for j in range(T):
                 n = L - T + 1 + j
                 if n < 1:
@@ -492,14 +511,25 @@ def exact(case, seed):
         q_out, k = head(s["q"], s["qw"]), head(s["k"], s["kw"])
         fmt = case["fmt"]
         kv = torch.stack((k, s["v"].double()), 1)  # [N, 2, 8, 128]
-        if fmt in ("i4", "i8"):  # rounded to the codes that stand for them
-            top, width = (7, 32) if fmt == "i4" else (127, 128)
-            g = kv.reshape(*kv.shape[:-1], 128 // width, width)
-            step = (g.abs().max(-1, keepdim=True).values / top).to(torch.bfloat16).double()
+        k_scale, v_scale = s["scale"]
+        all_of = torch.tensor([k_scale, v_scale], dtype=torch.float64, device="cuda").view(1, 2, 1, 1)
+        if fmt == "fp4":  # rounded to what the codes stand for: the levels' midpoints go to the even code
+            g = (kv / all_of).reshape(-1, 2, HKV, 8, 16)
+            step = torch.clamp(g.abs().max(-1, keepdim=True).values / 6, max=448).float()
+            step = step.to(torch.float8_e4m3fn).double()
+            t = g / step.clamp(min=1e-30)
+            m = t.abs()
+            near = torch.zeros_like(m)
+            for low, high, even in ((0, 0.5, 0), (0.5, 1, 1), (1, 1.5, 1), (1.5, 2, 2), (2, 3, 2), (3, 4, 4), (4, 6, 4)):
+                mid = (low + high) / 2
+                near = torch.where((m > mid) | ((m == mid) & (even == high)), float(high), near)
+            kv = (torch.sign(t) * near * step).reshape(kv.shape) * all_of
+        elif fmt == "i8":
+            step = (kv.abs().max(-1, keepdim=True).values / 127).to(torch.bfloat16).double()
             step[step == 0] = 1
-            kv = (torch.clamp(torch.round(g / step), -top, top) * step).reshape(kv.shape)
+            kv = torch.clamp(torch.round(kv / step), -127, 127) * step
         elif fmt == "e4m3":
-            kv = kv.clamp(-448, 448).float().to(torch.float8_e4m3fn).double()
+            kv = (kv / all_of).clamp(-448, 448).float().to(torch.float8_e4m3fn).double() * all_of
         rows, slots = s["rows"].tolist(), s["slots"].tolist()
         if kind == "write":
             whole = s["kv"].double()
