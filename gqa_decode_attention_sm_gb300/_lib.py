@@ -21,7 +21,7 @@ EXPORTS = (
     "gqa_decode_combine_stage", "gqa_decode_workspace_init", "gqa_decode_get_status",
     "gqa_decode_noalloc", "gqa_decode_noalloc_get_status", "gqa_decode_debug_skip_tile",
     "gqa_decode_debug_cut_extents", "gqa_decode_int8kv", "gqa_decode_paged",
-    "gqa_decode_verify", "gqa_append_kv", "gqa_append_kv_paged",
+    "gqa_decode_verify", "gqa_append_kv", "gqa_append_kv_paged", "gqa_decode_fp4kv",
 )
 
 
@@ -53,6 +53,7 @@ def _declare(lib):
         "gqa_decode_noalloc": (i, [p, p, p, p, i, i, i, f, i, p]),
         "gqa_decode_noalloc_get_status": (i, [p, ctypes.POINTER(ctypes.c_uint32)]),
         "gqa_decode_int8kv": (i, [p, p, p, p, p, i, i, i, f, i, p, sz, p]),
+        "gqa_decode_fp4kv": (i, [p, p, p, p, p, i, i, i, f, f, f, i, p, sz, p]),
         "gqa_decode_paged": (i, [p, i, p, i, p, p, i, i, i, p, p, i, i, f, f, f, i, p, sz, p]),
         "gqa_decode_verify": (i, [p, i, p, i, p, p, p, i, i, i, f, f, f, i, p, sz, p]),
         "gqa_append_kv": (i, [p, p, p, p, p, i, p, p, i, p, p, i, p, i, f, f, f, f, p, sz, p]),

@@ -22,7 +22,7 @@ from ._lib import GqaError
 
 HQ, HKV, D = 32, 8, 128
 F16, BF16 = 0, 1
-KV_F16, KV_BF16, KV_E4M3, KV_I8 = 0, 1, 2, 3
+KV_F16, KV_BF16, KV_E4M3, KV_I8, KV_E2M1 = 0, 1, 2, 3, 4
 MAX_SPLITS = 256
 FLAG_LENGTH_CLAMPED = 0x1
 FLAG_WAIT_TIMEOUT = 0x2
@@ -33,9 +33,10 @@ FLAG_BOUNDS = 0x10  # range-checked build only: an access fell outside its buffe
 _QDT = {torch.float16: F16, torch.bfloat16: BF16}
 _KVF = {torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.uint8: KV_E4M3,
         torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_I8}
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 __all__ = ["GqaError", "append_kv_paged", "gqa_decode", "gqa_decode_fp8kv", "gqa_decode_int8kv", "gqa_decode_paged",
-           "gqa_decode_verify", "append_kv",
+           "gqa_decode_verify", "gqa_decode_fp4kv", "append_kv",
            "prepare", "launch",
            "Prepared",
            "workspace_size", "plan", "get_status", "split_stage", "combine_stage", "split_geometry",
@@ -65,13 +66,34 @@ def _require(t, name, shape, dtypes, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+def _kv_format(kv, name, lead):
+    """Format of a cache [lead.., 2, 8, rows, 128], or uint8 [.., 64]: e2m1
+    pairs, two to a byte.  ``lead``: its first dimension (None: any)."""
+    if not isinstance(kv, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    e2m1 = kv.dtype == torch.uint8 and kv.dim() == 5 and kv.shape[4] == D // 2
+    first = "num_pages" if lead is None else lead
+    if (kv.dim() != 5 or (lead is not None and kv.shape[0] != lead) or kv.shape[1:3] != (2, HKV)
+            or (kv.shape[4] != D and not e2m1)):
+        raise ValueError(f"{name} must be [{first}, 2, {HKV}, {'page_size' if lead is None else 'capacity'}, {D}] "
+                         f"(uint8 [.., {D // 2}] for e2m1), got {tuple(kv.shape)}")
+    return KV_E2M1 if e2m1 else _KVF.get(kv.dtype, -1)
+
+
+def _require_scales(scales, name, kv, kvf):
+    """Row scales of an int8 (bf16) or e2m1 (e4m3) cache; the others have none."""
+    if kvf == KV_I8:
+        _require(scales, name, kv.shape[:4], (torch.bfloat16,), kv.device)
+    elif kvf == KV_E2M1:
+        _require(scales, name, (*kv.shape[:4], 8), _FP8, kv.device)
+
+
 def _geometry(q, kv, lens):
     _require(q, "q", None, (torch.float16, torch.bfloat16))
     if q.dim() != 3 or q.shape[1:] != (HQ, D):
         raise ValueError(f"q must be [batch, {HQ}, {D}], got {tuple(q.shape)}")
     B = q.shape[0]
-    if kv.dim() != 5 or kv.shape[0] != B or kv.shape[1:3] != (2, HKV) or kv.shape[4] != D:
-        raise ValueError(f"kv must be [{B}, 2, {HKV}, capacity, {D}], got {tuple(kv.shape)}")
+    _kv_format(kv, "kv", B)
     C = kv.shape[3]
     _require(kv, "kv", None, tuple(_KVF), q.device)
     _require(lens, "sequence_lengths", (B,), (torch.int32,), q.device)
@@ -142,7 +164,7 @@ class Prepared:
     k_scale: float
     v_scale: float
     num_splits: int
-    kv_scales: torch.Tensor | None = None  # int8 cache: bf16 [B,2,8,C]
+    kv_scales: torch.Tensor | None = None  # int8 cache: bf16 [B,2,8,C]; e2m1 cache: e4m3 [B,2,8,C,8]
 
     @property
     def workspace_bytes(self) -> int:
@@ -164,22 +186,21 @@ def prepare(tensors: dict, q_scale: float = 1.0, num_splits=None, k_scale=None, 
     """Validate once and allocate the split workspace once (outside any capture).
 
     ``tensors`` holds "Q", "KV", "O", "sequence_lengths", and "KV_SCALES" for an
-    int8 cache.  An e4m3 cache (uint8 or float8_e4m3fn storage) needs k_scale
-    and v_scale.  A ``workspace`` given by the caller (uint8, at least
+    int8 or e2m1 cache.  An e4m3 cache (uint8 or float8_e4m3fn storage) needs
+    k_scale and v_scale.  A ``workspace`` given by the caller (uint8, at least
     workspace_size bytes) should have its 256-byte header (status flags) zeroed
     before first use (``workspace_init``).
     """
     q, kv, out, lens = tensors["Q"], tensors["KV"], tensors["O"], tensors["sequence_lengths"]
     B, C = _geometry(q, kv, lens)
     kv_scales = tensors.get("KV_SCALES")
-    if kv.dtype == torch.int8:
-        _require(kv_scales, "KV_SCALES", (B, 2, HKV, C), (torch.bfloat16,), q.device)
+    kvf = _kv_format(kv, "KV", B)
+    _require_scales(kv_scales, "KV_SCALES", kv, kvf)
     _require(out, "O", q.shape, (q.dtype,), q.device)
     for name, t in (("Q", q), ("KV", kv), ("sequence_lengths", lens), ("KV_SCALES", kv_scales)):
         if t is not None and _storage_overlaps(out, t):
             raise ValueError(f"O must not share storage with {name}")
-    kvf = _KVF[kv.dtype]
-    if kvf not in (KV_E4M3, KV_I8) and kv.dtype != q.dtype:
+    if kvf in (KV_F16, KV_BF16) and kv.dtype != q.dtype:
         raise ValueError("fp16/bf16 KV must have the dtype of Q")
     if kvf == KV_E4M3:
         if k_scale is None or v_scale is None:
@@ -198,7 +219,7 @@ def prepare(tensors: dict, q_scale: float = 1.0, num_splits=None, k_scale=None, 
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace has {workspace.numel()} bytes, needs {nbytes}")
     return Prepared(q, kv, out, lens, workspace, B, C, _QDT[q.dtype], kvf, float(q_scale),
-                    float(k_scale), float(v_scale), S, kv_scales if kvf == KV_I8 else None)
+                    float(k_scale), float(v_scale), S, kv_scales if kvf in (KV_I8, KV_E2M1) else None)
 
 
 def launch(p: Prepared) -> torch.Tensor:
@@ -210,6 +231,10 @@ def launch(p: Prepared) -> torch.Tensor:
             _lib.check(lib.gqa_decode_int8kv(_ptr(p.q), _ptr(p.kv), _ptr(p.kv_scales), _ptr(p.lens),
                                              _ptr(p.out), p.batch, p.capacity, p.q_dtype, p.q_scale,
                                              p.num_splits, _ptr(p.workspace), p.workspace_bytes, st))
+        elif p.kv_format == KV_E2M1:
+            _lib.check(lib.gqa_decode_fp4kv(_ptr(p.q), _ptr(p.kv), _ptr(p.kv_scales), _ptr(p.lens), _ptr(p.out),
+                                            p.batch, p.capacity, p.q_dtype, p.q_scale, p.k_scale, p.v_scale,
+                                            p.num_splits, _ptr(p.workspace), p.workspace_bytes, st))
         elif p.kv_format == KV_E4M3 and p.q_dtype == BF16:
             _lib.check(lib.gqa_decode_fp8kv(_ptr(p.q), _ptr(p.kv), _ptr(p.lens), _ptr(p.out), p.batch,
                                             p.capacity, p.q_scale, p.k_scale, p.v_scale, p.num_splits,
@@ -226,7 +251,7 @@ def launch(p: Prepared) -> torch.Tensor:
 
 def split_stage(p: Prepared) -> None:
     """Stage 1 alone (streams K/V, writes partials or, with one split, out).
-    Not for an int8 cache (its scales go through gqa_decode_int8kv)."""
+    Not for an int8 or e2m1 cache (their scales go through launch)."""
     with torch.cuda.device(p.q.device):
         _lib.check(_lib.load().gqa_decode_split_stage(
             _ptr(p.q), p.q_dtype, _ptr(p.kv), p.kv_format, _ptr(p.lens), _ptr(p.out), p.batch,
@@ -246,7 +271,7 @@ def gqa_decode_fp8kv(q, kv, sequence_lengths, k_scale: float, v_scale: float, q_
                      out=None, num_splits=None, workspace=None):
     """e4m3 KV cache (uint8 or float8_e4m3fn storage), bf16 q and out."""
     B, C = _geometry(q, kv, sequence_lengths)
-    if q.dtype != torch.bfloat16 or _KVF[kv.dtype] != KV_E4M3:
+    if q.dtype != torch.bfloat16 or _kv_format(kv, "kv", B) != KV_E4M3:
         raise ValueError("gqa_decode_fp8kv takes bf16 q and an e4m3 (uint8) KV cache")
     if out is None:
         out = torch.empty_like(q)
@@ -283,11 +308,38 @@ def gqa_decode_int8kv(q, kv, kv_scales, sequence_lengths, q_scale: float = 1.0, 
     return out
 
 
+def gqa_decode_fp4kv(q, kv, kv_scales, sequence_lengths, k_scale: float = 1.0, v_scale: float = 1.0,
+                     q_scale: float = 1.0, out=None, num_splits=None, workspace=None):
+    """4-bit cache: kv uint8 [batch, 2, 8, capacity, 64], byte j of a row holding
+    the e2m1 codes of dims 2j (low nibble) and 2j + 1; kv_scales e4m3 (uint8 or
+    float8_e4m3fn) [batch, 2, 8, capacity, 8], one for each 16 dims; k_scale and
+    v_scale multiply all keys and all values.  fp16/bf16 q and out."""
+    B, C = _geometry(q, kv, sequence_lengths)
+    if _kv_format(kv, "kv", B) != KV_E2M1:
+        raise ValueError("gqa_decode_fp4kv takes a uint8 cache [batch, 2, 8, capacity, 64]")
+    _require_scales(kv_scales, "kv_scales", kv, KV_E2M1)
+    if out is None:
+        out = torch.empty_like(q)
+    _require(out, "out", q.shape, (q.dtype,), q.device)
+    S = plan(B, C, KV_E2M1, q.device) if not num_splits else int(num_splits)
+    nbytes = workspace_size(B, C, S)
+    if workspace is None:
+        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+    _require(workspace, "workspace", None, (torch.uint8,), q.device)
+    with torch.cuda.device(q.device):
+        _lib.check(_lib.load().gqa_decode_fp4kv(
+            _ptr(q), _ptr(kv), _ptr(kv_scales), _ptr(sequence_lengths), _ptr(out), B, C, _QDT[q.dtype],
+            float(q_scale), float(k_scale), float(v_scale), S, _ptr(workspace), workspace.numel(),
+            _stream(q.device)))
+    return out
+
+
 def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float = 1.0,
                      k_scale: float = 1.0, v_scale: float = 1.0, out=None, num_splits=None,
                      workspace=None, kv_scales=None):
     """Paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (fp16/bf16, e4m3 as
-    uint8/float8_e4m3fn, or int8 with kv_scales bf16 [num_pages, 2, 8, page_size]),
+    uint8/float8_e4m3fn, or int8 with kv_scales bf16 [num_pages, 2, 8, page_size];
+    e2m1: uint8 [.., page_size, 64] with kv_scales e4m3 [.., page_size, 8]),
     block_table int32 [batch, max_pages]; q [batch, 32, 128], or [batch, T, 32, 128]
     for a verify window of T = 1..4 tokens; returns out (q's shape)."""
     _require(q, "q", None, (torch.float16, torch.bfloat16))
@@ -298,17 +350,14 @@ def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float 
         T = q.shape[1]
     else:
         raise ValueError(f"q must be [batch, {HQ}, {D}] or [batch, T (1..4), {HQ}, {D}]")
-    if kv_pages.dim() != 5 or kv_pages.shape[1:3] != (2, HKV) or kv_pages.shape[4] != D:
-        raise ValueError("kv_pages must be [num_pages, 2, 8, page_size, 128]")
+    kvf = _kv_format(kv_pages, "kv_pages", None)
     _require(kv_pages, "kv_pages", None, tuple(_KVF), q.device)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [batch, max_pages]")
     _require(block_table, "block_table", None, (torch.int32,), q.device)
     _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), q.device)
-    kvf = _KVF[kv_pages.dtype]
     num_pages, page_size, max_pages = kv_pages.shape[0], kv_pages.shape[3], block_table.shape[1]
-    if kvf == KV_I8:
-        _require(kv_scales, "kv_scales", (num_pages, 2, HKV, page_size), (torch.bfloat16,), q.device)
+    _require_scales(kv_scales, "kv_scales", kv_pages, kvf)
     C = max_pages * page_size
     if out is None:
         out = torch.empty_like(q)
@@ -319,7 +368,7 @@ def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float 
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     with torch.cuda.device(q.device):
         _lib.check(_lib.load().gqa_decode_paged(
-            _ptr(q), _QDT[q.dtype], _ptr(kv_pages), kvf, _ptr(kv_scales) if kvf == KV_I8 else None,
+            _ptr(q), _QDT[q.dtype], _ptr(kv_pages), kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None,
             _ptr(block_table), max_pages, num_pages, page_size, _ptr(sequence_lengths), _ptr(out), B, T,
             float(q_scale), float(k_scale), float(v_scale), S, _ptr(workspace), workspace.numel(),
             _stream(q.device)))
@@ -330,19 +379,16 @@ def gqa_decode_verify(q, kv, sequence_lengths, q_scale: float = 1.0, k_scale: fl
                       v_scale: float = 1.0, kv_scales=None, out=None, num_splits=None, workspace=None):
     """Verify window: q [batch, T, 32, 128] (T = 1..4 draft tokens, the last T slots
     of each cache row); query j attends slots [0, len - T + j].  Any KV format
-    (int8 needs kv_scales).  Returns out [batch, T, 32, 128]."""
+    (int8 and e2m1 need kv_scales).  Returns out [batch, T, 32, 128]."""
     _require(q, "q", None, (torch.float16, torch.bfloat16))
     if q.dim() != 4 or q.shape[2:] != (HQ, D):
         raise ValueError(f"q must be [batch, T, {HQ}, {D}], got {tuple(q.shape)}")
     B, T = q.shape[0], q.shape[1]
-    if kv.dim() != 5 or kv.shape[0] != B or kv.shape[1:3] != (2, HKV) or kv.shape[4] != D:
-        raise ValueError(f"kv must be [{B}, 2, {HKV}, capacity, {D}]")
+    kvf = _kv_format(kv, "kv", B)
     C = kv.shape[3]
     _require(kv, "kv", None, tuple(_KVF), q.device)
     _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), q.device)
-    kvf = _KVF[kv.dtype]
-    if kvf == KV_I8:
-        _require(kv_scales, "kv_scales", (B, 2, HKV, C), (torch.bfloat16,), q.device)
+    _require_scales(kv_scales, "kv_scales", kv, kvf)
     if out is None:
         out = torch.empty_like(q)
     _require(out, "out", q.shape, (q.dtype,), q.device)
@@ -352,7 +398,7 @@ def gqa_decode_verify(q, kv, sequence_lengths, q_scale: float = 1.0, k_scale: fl
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     with torch.cuda.device(q.device):
         _lib.check(_lib.load().gqa_decode_verify(
-            _ptr(q), _QDT[q.dtype], _ptr(kv), kvf, _ptr(kv_scales) if kvf == KV_I8 else None,
+            _ptr(q), _QDT[q.dtype], _ptr(kv), kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None,
             _ptr(sequence_lengths), _ptr(out), B, C, T, float(q_scale), float(k_scale), float(v_scale), S,
             _ptr(workspace), workspace.numel(), _stream(q.device)))
     return out

@@ -9,14 +9,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libgqa_decode.so")
 INCLUDE = os.path.join(ROOT, "include")
-MAIN_SRC = os.path.join(PKG, "csrc", "gqa_decode.cu")
+# translation units, compiled side by side
+SRCS = [os.path.join(PKG, "csrc", name) for name in ("gqa_decode.cu", "fp4_decode.cu")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC", "-shared", "-t", "0"]
 
 
 def _sources():
-    return ([MAIN_SRC] + glob.glob(os.path.join(PKG, "csrc", "**", "*.cuh"), recursive=True)
+    return (glob.glob(os.path.join(PKG, "csrc", "**", "*.cuh"), recursive=True)
             + glob.glob(os.path.join(PKG, "csrc", "**", "*.cu"), recursive=True)
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
@@ -33,7 +34,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if os.path.getmtime(LIB_PATH) >= newest:
             return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-o", tmp, MAIN_SRC]
+    cmd = [nvcc(), *NVCC_FLAGS, "-I" + INCLUDE, "-o", tmp, *SRCS]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
@@ -53,7 +54,7 @@ def build_checked(force: bool = False, verbose: bool = False) -> str:
         if os.path.getmtime(CHECKED_LIB_PATH) >= newest:
             return CHECKED_LIB_PATH
     tmp = CHECKED_LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, "-DGQA_CHECKED", "-I" + INCLUDE, "-o", tmp, MAIN_SRC]
+    cmd = [nvcc(), *NVCC_FLAGS, "-DGQA_CHECKED", "-I" + INCLUDE, "-o", tmp, *SRCS]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)

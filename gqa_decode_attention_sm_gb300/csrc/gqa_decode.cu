@@ -21,7 +21,7 @@
 #include "kernels/append_kv.cuh"
 #include "kernels/combine.cuh"
 #include "kernels/common.cuh"
-#include "kernels/split_kv_mma.cuh"
+#include "kernels/split_launch.cuh"
 
 static_assert(GQA_MAX_SPLITS <= 32 * gqa::kCombineChunks, "the combine's chunks cover every split slot");
 
@@ -48,7 +48,6 @@ gqa_status_t cuda_fail(cudaError_t e, const char* what) {
 // ---------------------------------------------------------------- devices
 
 constexpr int kMaxDevices = 64;
-constexpr int kClusterMaxSplits = 8;  // the on-chip merge: clusters of 2..8 splits (portable sizes)
 
 // Per-device result of the one-time check.  Kept once known for good: the
 // device is ready (sm_count set) or is not a compute capability 10.3 part.  A
@@ -63,61 +62,9 @@ struct DeviceState {
   // resident at once, by [KV format][q format][q_len - 1][s]
   // (cudaOccupancyMaxActiveClusters).  A cluster's CTAs share one GPC, so a
   // grid that nearly fills the SMs can hold fewer clusters than slots / s.
-  int cluster_fit[4][2][kMaxQLen][kClusterMaxSplits + 1] = {};
+  ClusterFit cluster_fit[5][2] = {};
 };
 DeviceState g_devices[kMaxDevices];
-
-template <int KVF, int QF>
-cudaError_t set_split_attributes() {
-  cudaError_t e = cudaSuccess;
-  const auto set = [&](auto kernel, int bytes) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  set(split_kv_mma_kernel<KVF, QF, 1, false, false>, mma_smem_bytes(KVF, 1));
-  set(split_kv_mma_kernel<KVF, QF, 2, false, false>, mma_smem_bytes(KVF, 2));
-  set(split_kv_mma_kernel<KVF, QF, 3, false, false>, mma_smem_bytes(KVF, 3));
-  set(split_kv_mma_kernel<KVF, QF, 4, false, false>, mma_smem_bytes(KVF, 4));
-  set(split_kv_mma_kernel<KVF, QF, 1, true, false>, mma_smem_bytes(KVF, 1, true));
-  set(split_kv_mma_kernel<KVF, QF, 2, true, false>, mma_smem_bytes(KVF, 2, true));
-  set(split_kv_mma_kernel<KVF, QF, 3, true, false>, mma_smem_bytes(KVF, 3, true));
-  set(split_kv_mma_kernel<KVF, QF, 4, true, false>, mma_smem_bytes(KVF, 4, true));
-  set(split_kv_mma_kernel<KVF, QF, 1, false, true>, mma_smem_bytes(KVF, 1));
-  set(split_kv_mma_kernel<KVF, QF, 2, false, true>, mma_smem_bytes(KVF, 2));
-  set(split_kv_mma_kernel<KVF, QF, 3, false, true>, mma_smem_bytes(KVF, 3));
-  set(split_kv_mma_kernel<KVF, QF, 4, false, true>, mma_smem_bytes(KVF, 4));
-  return e;
-}
-
-template <int KVF, int QF, int NQ>
-cudaError_t query_cluster_fit(DeviceState& st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMmaThreads, 1, 1);
-  cfg.dynamicSmemBytes = mma_smem_bytes(KVF, NQ);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  for (int s = 2; s <= kClusterMaxSplits; ++s) {
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = (unsigned)s;
-    cfg.gridDim = dim3(kHkv, 1, (unsigned)s);
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, split_kv_mma_kernel<KVF, QF, NQ, false, true>, &cfg);
-    if (e != cudaSuccess) return e;
-    st.cluster_fit[KVF][QF][NQ - 1][s] = n;
-  }
-  return cudaSuccess;
-}
-
-template <int KVF, int QF>
-cudaError_t query_cluster_fits(DeviceState& st) {
-  cudaError_t e = query_cluster_fit<KVF, QF, 1>(st);
-  if (e == cudaSuccess) e = query_cluster_fit<KVF, QF, 2>(st);
-  if (e == cudaSuccess) e = query_cluster_fit<KVF, QF, 3>(st);
-  if (e == cudaSuccess) e = query_cluster_fit<KVF, QF, 4>(st);
-  return e;
-}
 
 // One-time per-device check (compute capability 10.3), opt-in to the split
 // kernel's dynamic shared memory, and the cluster occupancy table.  Runs
@@ -152,12 +99,16 @@ void init_device(int dev, DeviceState& st) {
   const char* what = "cudaFuncSetAttribute";
   if (a == cudaSuccess) {
     what = "cudaOccupancyMaxActiveClusters";
-    a = query_cluster_fits<kKvF16, kQF16>(st);
-    if (a == cudaSuccess) a = query_cluster_fits<kKvBF16, kQBF16>(st);
-    if (a == cudaSuccess) a = query_cluster_fits<kKvE4M3, kQBF16>(st);
-    if (a == cudaSuccess) a = query_cluster_fits<kKvE4M3, kQF16>(st);
-    if (a == cudaSuccess) a = query_cluster_fits<kKvI8, kQBF16>(st);
-    if (a == cudaSuccess) a = query_cluster_fits<kKvI8, kQF16>(st);
+    a = query_cluster_fits<kKvF16, kQF16>(st.cluster_fit[kKvF16][kQF16]);
+    if (a == cudaSuccess) a = query_cluster_fits<kKvBF16, kQBF16>(st.cluster_fit[kKvBF16][kQBF16]);
+    if (a == cudaSuccess) a = query_cluster_fits<kKvE4M3, kQBF16>(st.cluster_fit[kKvE4M3][kQBF16]);
+    if (a == cudaSuccess) a = query_cluster_fits<kKvE4M3, kQF16>(st.cluster_fit[kKvE4M3][kQF16]);
+    if (a == cudaSuccess) a = query_cluster_fits<kKvI8, kQBF16>(st.cluster_fit[kKvI8][kQBF16]);
+    if (a == cudaSuccess) a = query_cluster_fits<kKvI8, kQF16>(st.cluster_fit[kKvI8][kQF16]);
+  }
+  if (a == cudaSuccess) {
+    what = "setting up the e2m1 kernels";
+    a = e2m1_setup(st.cluster_fit[kKvE2M1]);
   }
   if (prev >= 0 && prev != dev) cudaSetDevice(prev);
   if (a != cudaSuccess) {
@@ -207,7 +158,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-size_t kv_elem_bytes(int fmt) { return is_8bit(fmt) ? 1 : 2; }
+bool known_format(int fmt) { return fmt >= kKvF16 && fmt <= kKvE2M1; }
 
 size_t partial_o_bytes(int batch, int splits) {
   return align_up((size_t)batch * kHq * splits * kD * sizeof(float), 256);
@@ -236,7 +187,7 @@ struct Call {
   cudaStream_t stream;
   uint64_t wait_budget_ns = kWaitBudgetNs;
   int skip_tile = -1;
-  const uint16_t* kv_scales = nullptr;  // int8 cache only
+  const void* kv_scales = nullptr;  // int8 (bf16) and e2m1 (e4m3) caches only
   const int32_t* block_table = nullptr;  // paged cache only
   int page_log2 = 0, max_pages = 0, num_pages = 0;
   int q_len = 1;  // query tokens per request (verify window)
@@ -259,13 +210,16 @@ gqa_status_t validate(const Call& c, bool q_scale_positive, bool need_q) {
   if (st != GQA_OK) return st;
   if (c.q_dtype != GQA_F16 && c.q_dtype != GQA_BF16)
     return fail(GQA_ERR_INVALID_ARGUMENT, "unknown q/out dtype %d", c.q_dtype);
-  if (c.kv_format != kKvF16 && c.kv_format != kKvBF16 && c.kv_format != kKvE4M3 && c.kv_format != kKvI8)
+  if (!known_format(c.kv_format))
     return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", c.kv_format);
-  if (!is_8bit(c.kv_format) && c.kv_format != c.q_dtype)
+  if (!is_narrow(c.kv_format) && c.kv_format != c.q_dtype)
     return fail(GQA_ERR_INVALID_ARGUMENT, "fp16/bf16 KV must have the dtype of q");
   if (c.kv_format == kKvI8 && (!c.kv_scales || !aligned(c.kv_scales, 16) || c.capacity % 8 != 0))
     return fail(GQA_ERR_INVALID_ARGUMENT,
                 "an int8 cache needs a 16-byte aligned bf16 scale array and a capacity that is a multiple of 8");
+  if (c.kv_format == kKvE2M1 && (!c.kv_scales || !aligned(c.kv_scales, 16) || c.capacity % 2 != 0))
+    return fail(GQA_ERR_INVALID_ARGUMENT,
+                "an e2m1 cache needs a 16-byte aligned e4m3 scale array and a capacity that is a multiple of 2");
   if (!std::isfinite(c.q_scale) || c.q_scale < 0.f || (q_scale_positive && c.q_scale == 0.f))
     return fail(GQA_ERR_INVALID_ARGUMENT, "q_scale must be finite and %s 0", q_scale_positive ? ">" : ">=");
   if (!std::isfinite(c.k_scale) || c.k_scale <= 0.f || !std::isfinite(c.v_scale) || c.v_scale <= 0.f)
@@ -279,9 +233,9 @@ gqa_status_t validate(const Call& c, bool q_scale_positive, bool need_q) {
   if (c.workspace_bytes < need)
     return fail(GQA_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", c.workspace_bytes, need);
   const size_t qo_bytes = (size_t)c.batch * c.q_len * kHq * kD * 2;
-  const size_t kv_bytes =
-      c.block_table ? (size_t)c.num_pages * 2 * kHkv * ((size_t)1 << c.page_log2) * kD * kv_elem_bytes(c.kv_format)
-                    : (size_t)c.batch * 2 * kHkv * (size_t)c.capacity * kD * kv_elem_bytes(c.kv_format);
+  const size_t kv_rows = c.block_table ? (size_t)c.num_pages * 2 * kHkv * ((size_t)1 << c.page_log2)
+                                       : (size_t)c.batch * 2 * kHkv * (size_t)c.capacity;
+  const size_t kv_bytes = kv_rows * kv_row_bytes(c.kv_format);
   const size_t lens_bytes = (size_t)c.batch * 4;
   if ((need_q && overlap(c.out, qo_bytes, c.q, qo_bytes)) || overlap(c.out, qo_bytes, c.kv, kv_bytes) ||
       overlap(c.out, qo_bytes, c.lens, lens_bytes) || overlap(c.out, qo_bytes, c.workspace, need))
@@ -294,11 +248,10 @@ gqa_status_t validate(const Call& c, bool q_scale_positive, bool need_q) {
     if (overlap(c.out, qo_bytes, c.block_table, bt_bytes) || overlap(c.workspace, need, c.block_table, bt_bytes))
       return fail(GQA_ERR_ALIASING, "out or the workspace overlaps the block table");
   }
-  if (c.kv_format == kKvI8) {
-    const size_t sc_bytes = c.block_table ? (size_t)c.num_pages * 2 * kHkv * ((size_t)1 << c.page_log2) * 2
-                                          : (size_t)c.batch * 2 * kHkv * (size_t)c.capacity * 2;
+  if (scale_row_bytes(c.kv_format) > 0) {
+    const size_t sc_bytes = kv_rows * scale_row_bytes(c.kv_format);
     if (overlap(c.out, qo_bytes, c.kv_scales, sc_bytes) || overlap(c.workspace, need, c.kv_scales, sc_bytes))
-      return fail(GQA_ERR_ALIASING, "out or the workspace overlaps the int8 scales");
+      return fail(GQA_ERR_ALIASING, "out or the workspace overlaps the cache's scales");
   }
   return GQA_OK;
 }
@@ -396,50 +349,6 @@ int plan_splits(int batch, int capacity, int kv_format, int sm_count) {
 
 // ---------------------------------------------------------------- launches
 
-// `bal_ctas` > 0: the balanced schedule on that many CTAs (single token).
-// `cluster`: the one-piece grid as clusters of its `cluster` splits, merged
-// on chip (no combine kernel).
-template <int KVF, int QF, bool BAL, bool CL>
-cudaError_t launch_nq(cudaLaunchConfig_t& cfg, const SplitParams& sp, int q_len) {
-  switch (q_len) {
-    case 1: return cudaLaunchKernelEx(&cfg, split_kv_mma_kernel<KVF, QF, 1, BAL, CL>, sp);
-    case 2: return cudaLaunchKernelEx(&cfg, split_kv_mma_kernel<KVF, QF, 2, BAL, CL>, sp);
-    case 3: return cudaLaunchKernelEx(&cfg, split_kv_mma_kernel<KVF, QF, 3, BAL, CL>, sp);
-    default: return cudaLaunchKernelEx(&cfg, split_kv_mma_kernel<KVF, QF, 4, BAL, CL>, sp);
-  }
-}
-
-template <int KVF, int QF>
-cudaError_t launch_split_t(const SplitParams& sp, int q_len, int bal_ctas, int cluster, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kMmaThreads, 1, 1);
-  cfg.stream = stream;
-  // programmatic dependent launch: CTAs may become resident while the
-  // previous grid in the stream drains; they wait (griddepcontrol.wait)
-  // before reading any input
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (bal_ctas > 0) {
-    cfg.gridDim = dim3(bal_ctas, 1, 1);
-    cfg.dynamicSmemBytes = mma_smem_bytes(KVF, q_len, true);
-    return launch_nq<KVF, QF, true, false>(cfg, sp, q_len);
-  }
-  cfg.gridDim = dim3(kHkv, sp.batch, sp.splits_eff);
-  cfg.dynamicSmemBytes = mma_smem_bytes(KVF, q_len);
-  if (cluster > 0) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = (unsigned)cluster;
-    cfg.numAttrs = 2;
-    return launch_nq<KVF, QF, false, true>(cfg, sp, q_len);
-  }
-  return launch_nq<KVF, QF, false, false>(cfg, sp, q_len);
-}
-
 template <int QF>
 cudaError_t launch_combine_t(const CombineParams& cp, int batch_rows, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -519,7 +428,7 @@ BalPlan bal_plan(const Call& c) {
   // CTAs per SM its issue-heavier CTAs pay more for the extra prologues and
   // pieces (64 x U[16k, 32k] in 256-token pages: int8 461 us with one wave,
   // 469 with four; e4m3 444 against 451).
-  const bool waves4 = c.block_table != nullptr && !is_8bit(c.kv_format);
+  const bool waves4 = c.block_table != nullptr && !is_narrow(c.kv_format);
   bp.ctas = (int)((waves4 ? 4 : 1) * slots);
   bp.q_min = (int)((nmax + c.num_splits - 2) / (c.num_splits - 1));
   return bp;
@@ -552,8 +461,8 @@ int cluster_fit(const Call& c, int s) {
   if (st.state.load(std::memory_order_acquire) != 1 || st.sm_count != c.sms) return 0;
   const auto& row = st.cluster_fit[c.kv_format];
   const int nq = c.q_len - 1;
-  if (!is_8bit(c.kv_format)) return row[c.kv_format == kKvF16 ? kQF16 : kQBF16][nq][s];
-  // an 8-bit cache with either q format when the call does not say which
+  if (!is_narrow(c.kv_format)) return row[c.kv_format == kKvF16 ? kQF16 : kQBF16][nq][s];
+  // an 8- or 4-bit cache with either q format when the call does not say which
   if (c.q_dtype == GQA_F16 || c.q_dtype == GQA_BF16) return row[c.q_dtype][nq][s];
   return std::min(row[kQF16][nq][s], row[kQBF16][nq][s]);
 }
@@ -598,8 +507,8 @@ gqa_status_t run_split(const Call& c) {
   sp.bal_q_min = bp.q_min;
   const size_t page_rows = c.block_table ? ((size_t)1 << c.page_log2) : (size_t)c.capacity;
   const size_t units = c.block_table ? (size_t)c.num_pages : (size_t)c.batch;
-  sp.kv_bytes = units * 2 * kHkv * page_rows * kD * kv_elem_bytes(c.kv_format);
-  sp.scales_bytes = c.kv_format == kKvI8 ? units * 2 * kHkv * page_rows * 2 : 0;
+  sp.kv_bytes = units * 2 * kHkv * page_rows * kv_row_bytes(c.kv_format);
+  sp.scales_bytes = units * 2 * kHkv * page_rows * scale_row_bytes(c.kv_format);
   if (kChecked) {
     sp.kv_bytes -= std::min<size_t>(sp.kv_bytes, g_cut_kv_bytes.load());
     sp.scales_bytes -= std::min<size_t>(sp.scales_bytes, g_cut_scales_bytes.load());
@@ -611,9 +520,11 @@ gqa_status_t run_split(const Call& c) {
   else if (c.kv_format == kKvE4M3)
     e = c.q_dtype == GQA_BF16 ? launch_split_t<kKvE4M3, kQBF16>(sp, ql, nb, cl, c.stream)
                               : launch_split_t<kKvE4M3, kQF16>(sp, ql, nb, cl, c.stream);
-  else
+  else if (c.kv_format == kKvI8)
     e = c.q_dtype == GQA_BF16 ? launch_split_t<kKvI8, kQBF16>(sp, ql, nb, cl, c.stream)
                               : launch_split_t<kKvI8, kQF16>(sp, ql, nb, cl, c.stream);
+  else
+    e = e2m1_launch_split(sp, c.q_dtype, ql, nb, cl, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "split kernel launch");
   return GQA_OK;
 }
@@ -709,7 +620,7 @@ gqa_status_t append_kv(const void* q_proj, const void* k_proj, const void* v_pro
       (!is_8bit(fmt) && !aligned(kv, 2)) || (kv_scales_bf16 && !aligned(kv_scales_bf16, 2)))
     return fail(GQA_ERR_INVALID_ARGUMENT, "misaligned argument");
   const size_t qb = (size_t)batch * kHq * kD * 2, kvb_in = (size_t)batch * kHkv * kD * 2;
-  const size_t cache = units * 2 * kHkv * unit_rows * kD * kv_elem_bytes(fmt);
+  const size_t cache = units * 2 * kHkv * unit_rows * kv_row_bytes(fmt);
   const void* ins[] = {q_proj, k_proj, v_proj};
   const size_t in_bytes[] = {qb, kvb_in, kvb_in};
   for (int i = 0; i < 3; ++i)
@@ -795,9 +706,7 @@ gqa_status_t gqa_decode_plan(int batch, int capacity, gqa_kv_format_t kv_format,
   if (!num_splits_out) return fail(GQA_ERR_INVALID_ARGUMENT, "num_splits_out is null");
   gqa_status_t st = validate_shape(batch, capacity);
   if (st != GQA_OK) return st;
-  if (kv_format != GQA_KV_F16 && kv_format != GQA_KV_BF16 && kv_format != GQA_KV_E4M3 &&
-      kv_format != GQA_KV_I8)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
+  if (!known_format((int)kv_format)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
   int sms = 0;
   st = device_ready(device, &sms);
   if (st != GQA_OK) return st;
@@ -810,9 +719,7 @@ gqa_status_t gqa_decode_plan_for(int batch, int capacity, gqa_kv_format_t kv_for
   if (!num_splits_out) return fail(GQA_ERR_INVALID_ARGUMENT, "num_splits_out is null");
   gqa_status_t st = validate_shape(batch, capacity);
   if (st != GQA_OK) return st;
-  if (kv_format != GQA_KV_F16 && kv_format != GQA_KV_BF16 && kv_format != GQA_KV_E4M3 &&
-      kv_format != GQA_KV_I8)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
+  if (!known_format((int)kv_format)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
   if (sm_count < 1) return fail(GQA_ERR_INVALID_ARGUMENT, "sm_count %d < 1", sm_count);
   *num_splits_out = plan_splits(batch, capacity, kv_format, sm_count);
   return GQA_OK;
@@ -823,9 +730,7 @@ gqa_status_t gqa_decode_split_geometry(int capacity, int num_splits, gqa_kv_form
   if (!chunk_tokens_out || !splits_effective_out) return fail(GQA_ERR_INVALID_ARGUMENT, "null output pointer");
   gqa_status_t st = validate_shape(1, capacity);
   if (st != GQA_OK) return st;
-  if (kv_format != GQA_KV_F16 && kv_format != GQA_KV_BF16 && kv_format != GQA_KV_E4M3 &&
-      kv_format != GQA_KV_I8)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
+  if (!known_format((int)kv_format)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
   if (num_splits < 1 || num_splits > GQA_MAX_SPLITS)
     return fail(GQA_ERR_INVALID_ARGUMENT, "num_splits %d outside [1, %d]", num_splits, GQA_MAX_SPLITS);
   *chunk_tokens_out = split_chunk(capacity, num_splits, (int)kv_format);
@@ -838,9 +743,7 @@ gqa_status_t gqa_decode_launch_count_for(int batch, int capacity, gqa_kv_format_
   if (!launches_out) return fail(GQA_ERR_INVALID_ARGUMENT, "launches_out is null");
   gqa_status_t st = validate_shape(batch, capacity);
   if (st != GQA_OK) return st;
-  if (kv_format != GQA_KV_F16 && kv_format != GQA_KV_BF16 && kv_format != GQA_KV_E4M3 &&
-      kv_format != GQA_KV_I8)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
+  if (!known_format((int)kv_format)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", (int)kv_format);
   if (q_len < 1 || q_len > kMaxQLen) return fail(GQA_ERR_INVALID_ARGUMENT, "q_len %d outside [1, %d]", q_len, kMaxQLen);
   if (num_splits < 1 || num_splits > GQA_MAX_SPLITS)
     return fail(GQA_ERR_INVALID_ARGUMENT, "num_splits %d outside [1, %d]", num_splits, GQA_MAX_SPLITS);
@@ -897,8 +800,22 @@ gqa_status_t gqa_decode_int8kv(const void* q, const int8_t* kv_i8, const uint16_
   return run_combine(c);
 }
 
+gqa_status_t gqa_decode_fp4kv(const void* q, const uint8_t* kv_e2m1, const uint8_t* kv_scales_e4m3,
+                              const int32_t* lens, void* out, int batch, int capacity, gqa_dtype_t dtype,
+                              float q_scale, float k_scale, float v_scale, int num_splits, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  Call c{q, (int)dtype, kv_e2m1, kKvE2M1, lens, out, batch, capacity, q_scale, k_scale, v_scale, num_splits,
+         workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
+  c.kv_scales = kv_scales_e4m3;
+  gqa_status_t st = prepare_call(c, false, true);
+  if (st != GQA_OK) return st;
+  st = run_split(c);
+  if (st != GQA_OK) return st;
+  return run_combine(c);
+}
+
 gqa_status_t gqa_decode_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages, gqa_kv_format_t kv_format,
-                              const uint16_t* kv_scales_pages, const int32_t* block_table, int max_pages_per_seq,
+                              const void* kv_scales_pages, const int32_t* block_table, int max_pages_per_seq,
                               int num_pages, int page_size, const int32_t* lens, void* out, int batch, int q_len,
                               float q_scale, float k_scale, float v_scale, int num_splits, void* workspace,
                               size_t workspace_bytes, void* stream) {
@@ -917,13 +834,14 @@ gqa_status_t gqa_decode_paged(const void* q, gqa_dtype_t q_dtype, const void* kv
     if (!aligned(kv_scales_pages, 16))
       return fail(GQA_ERR_INVALID_ARGUMENT, "the int8 scale pool must be 16-byte aligned");
   }
+  // (validate checks an e2m1 cache's scales)
   Call c{q, (int)q_dtype, kv_pages, (int)kv_format, lens, out, batch, (int)cap, q_scale, k_scale, v_scale,
          num_splits, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
   c.block_table = block_table;
   c.max_pages = max_pages_per_seq;
   c.num_pages = num_pages;
   c.q_len = q_len;
-  if (kv_format == GQA_KV_I8) c.kv_scales = kv_scales_pages;
+  if (scale_row_bytes((int)kv_format) > 0) c.kv_scales = kv_scales_pages;
   int lg = 0;
   while ((1 << lg) < page_size) ++lg;
   c.page_log2 = lg;
@@ -935,7 +853,7 @@ gqa_status_t gqa_decode_paged(const void* q, gqa_dtype_t q_dtype, const void* kv
 }
 
 gqa_status_t gqa_decode_verify(const void* q, gqa_dtype_t q_dtype, const void* kv, gqa_kv_format_t kv_format,
-                               const uint16_t* kv_scales_bf16, const int32_t* lens, void* out, int batch,
+                               const void* kv_scales, const int32_t* lens, void* out, int batch,
                                int capacity, int q_len, float q_scale, float k_scale, float v_scale,
                                int num_splits, void* workspace, size_t workspace_bytes, void* stream) {
   if (q_len < 1 || q_len > kMaxQLen)
@@ -943,7 +861,7 @@ gqa_status_t gqa_decode_verify(const void* q, gqa_dtype_t q_dtype, const void* k
   Call c{q, (int)q_dtype, kv, (int)kv_format, lens, out, batch, capacity, q_scale, k_scale, v_scale,
          num_splits, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
   c.q_len = q_len;
-  c.kv_scales = kv_scales_bf16;
+  c.kv_scales = kv_scales;
   gqa_status_t st = prepare_call(c, false, true);
   if (st != GQA_OK) return st;
   st = run_split(c);
@@ -992,6 +910,8 @@ gqa_status_t gqa_decode_split_stage(const void* q, gqa_dtype_t q_dtype, const vo
                                     void* workspace, size_t workspace_bytes, void* stream) {
   if (kv_format == GQA_KV_I8)
     return fail(GQA_ERR_INVALID_ARGUMENT, "an int8 cache needs its scales: use gqa_decode_int8kv");
+  if (kv_format == GQA_KV_E2M1)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "an e2m1 cache needs its scales: use gqa_decode_fp4kv");
   Call c{q, (int)q_dtype, kv, (int)kv_format, lens, out, batch, capacity, q_scale, k_scale, v_scale,
          num_splits, workspace, workspace_bytes, static_cast<cudaStream_t>(stream)};
   gqa_status_t st = prepare_call(c, false, true);
@@ -1024,13 +944,12 @@ gqa_status_t gqa_decode_combine_stage(const int32_t* lens, void* out, gqa_dtype_
   // the checks (a null kv would be rejected) and skip the q checks.
   static const uint4 dummy = {0, 0, 0, 0};
   const int fmt = (int)kv_format;
-  Call c{nullptr, (int)out_dtype, &dummy, is_8bit(fmt) ? fmt : (int)out_dtype, lens, out, batch,
+  Call c{nullptr, (int)out_dtype, &dummy, is_narrow(fmt) ? fmt : (int)out_dtype, lens, out, batch,
          capacity, 1.f, 1.f, v_scale, num_splits, const_cast<void*>(workspace), workspace_bytes,
          static_cast<cudaStream_t>(stream)};
-  if (fmt != kKvE4M3 && fmt != kKvI8 && fmt != kKvF16 && fmt != kKvBF16)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", fmt);
+  if (!known_format(fmt)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", fmt);
   c.kv_format = fmt;
-  if (!is_8bit(fmt) && fmt != (int)out_dtype)
+  if (!is_narrow(fmt) && fmt != (int)out_dtype)
     return fail(GQA_ERR_INVALID_ARGUMENT, "fp16/bf16 KV must have the dtype of out");
   // the dummy kv range (batch*capacity*...) would spuriously overlap out; check
   // only what stage 2 touches

@@ -17,16 +17,32 @@ constexpr int kHkv = 8;
 constexpr int kGroup = kHq / kHkv;
 constexpr int kD = 128;
 
-enum KvFormat : int { kKvF16 = 0, kKvBF16 = 1, kKvE4M3 = 2, kKvI8 = 3 };
+enum KvFormat : int { kKvF16 = 0, kKvBF16 = 1, kKvE4M3 = 2, kKvI8 = 3, kKvE2M1 = 4 };
 enum QFormat : int { kQF16 = 0, kQBF16 = 1 };
 
 __host__ __device__ constexpr bool is_8bit(int kv_format) {
   return kv_format == kKvE4M3 || kv_format == kKvI8;
 }
 
-// Tokens per pipeline tile: one tile of one plane is 16 KB for every format.
+// Formats narrower than 16 bits: widened to f16 for the tensor cores.
+__host__ __device__ constexpr bool is_narrow(int kv_format) {
+  return is_8bit(kv_format) || kv_format == kKvE2M1;
+}
+
+// Bytes of one cache row (128 elements of one plane, KV head and slot).
+__host__ __device__ constexpr int kv_row_bytes(int kv_format) {
+  return kv_format == kKvE2M1 ? kD / 2 : (is_8bit(kv_format) ? kD : 2 * kD);
+}
+// Bytes of a row's scales: one bf16 for int8, an e4m3 for each 16 elements
+// for e2m1, none otherwise.
+constexpr int kE2M1Group = 16;
+__host__ __device__ constexpr int scale_row_bytes(int kv_format) {
+  return kv_format == kKvI8 ? 2 : (kv_format == kKvE2M1 ? kD / kE2M1Group : 0);
+}
+
+// Tokens per pipeline tile: one tile of one plane is 16 KB (e2m1: 8 KB).
 __host__ __device__ constexpr int tile_tokens(int kv_format) {
-  return is_8bit(kv_format) ? 128 : 64;
+  return is_narrow(kv_format) ? 128 : 64;
 }
 
 // Balanced schedule of the split kernel: the stream positions a row of n tiles
@@ -50,8 +66,7 @@ __host__ __device__ inline int bal_row_cost(int sum_tiles, int min_tiles, int ct
 
 template <int KVF>
 struct KvTraits {
-  static constexpr int kElemBytes = is_8bit(KVF) ? 1 : 2;
-  static constexpr int kRowBytes = kD * kElemBytes;  // one token of one KV head
+  static constexpr int kRowBytes = kv_row_bytes(KVF);  // one token of one KV head
   static constexpr int kTile = tile_tokens(KVF);
   static constexpr int kTileBytes = kTile * kRowBytes;
 };
@@ -243,6 +258,26 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
   return h2;
+}
+
+// The four bytes of w, each two e2m1 codes (low nibble = first element) ->
+// f16x2 pairs with the hardware conversion (exact).  It issues at the rate of
+// an integer instruction on GB300 (2 clocks per warp and SM sub-partition),
+// whichever byte it takes.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&d)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // Two int8 codes (low byte = first element) -> exact f16x2 of code + 1152.

@@ -58,16 +58,21 @@
 // the dot product, k_scale on scores, v_scale on the output).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace gqa {
 
-constexpr int kStageBytes = 2 * 16384;  // one K tile + one V tile (16 KB each)
+// one K tile + one V tile (16 KB each; e2m1: 8 KB)
+__host__ __device__ constexpr int stage_bytes(int kvf) { return 2 * tile_tokens(kvf) * kv_row_bytes(kvf); }
 
 struct SplitParams {
   const void* q;          // [B,32,128] fp16/bf16
-  const void* kv;         // [B,2,8,C,128] fp16/bf16/e4m3/int8
-  const uint16_t* kv_scales;  // int8 cache: bf16 [B or num_pages, 2, 8, C or page size], one scale per row
+  const void* kv;         // [B,2,8,C,128] fp16/bf16/e4m3/int8, or [B,2,8,C,64] bytes of e2m1 pairs
+  // int8 cache: bf16 [B or num_pages, 2, 8, C or page size], one scale per row;
+  // e2m1 cache: e4m3 bytes, 8 per row
+  const void* kv_scales;
   const int32_t* lens;    // [B]
   void* out;              // [B,32,128], written by pieces that are their row's only one
   float* part_o;          // [B,32,S,128] unnormalised accumulator
@@ -126,10 +131,12 @@ constexpr int kMmaThreads = (kMmaConsumerWarps + 1) * 32;
 // (A warp's registers come from one quarter of the SM's register file: 3
 // CTAs of 5 warps put 4 warps on some quarter, 128 registers each at most;
 // 2 CTAs put 3, 168 at most.)
+// An e2m1 stage is half as large, so it keeps 3 stages at 3 CTAs per SM.
 __host__ __device__ constexpr int mma_stages(int kvf, int nq) { return is_8bit(kvf) && nq <= 2 ? 2 : 3; }
-__host__ __device__ constexpr int mma_ctas_per_sm(int kvf, int nq) { return is_8bit(kvf) && nq <= 2 ? 3 : 2; }
+__host__ __device__ constexpr int mma_ctas_per_sm(int kvf, int nq) { return is_narrow(kvf) && nq <= 2 ? 3 : 2; }
 constexpr int kMaxQLen = 4;  // query tokens per request (a verify window when > 1)
-constexpr int kScaleStageBytes = 2 * 128 * 2;  // int8 cache: K and V row scales of one 128-token tile
+// K and V row scales of one 128-token tile (int8: 2 bytes a row; e2m1: 8)
+__host__ __device__ constexpr int scale_stage_bytes(int kvf) { return 2 * 128 * (kvf == kKvE2M1 ? 8 : 2); }
 // Balanced schedule: batches up to this size (every CTA's prologue scans the
 // lengths).  Its merge area sits outside the ring, which keeps streaming the
 // next piece while the consumers merge the last: [4 warps][4 heads][128 + 2],
@@ -140,15 +147,15 @@ static_assert((kMmaThreads + 3 + kBalMaxBatch) * 4 <= kBalMergeBytes, "the lengt
 // the balanced cursor's slot of 16 ints per warp (its state and the current
 // piece's output coordinates), after the merge area
 constexpr int kBalRunBytes = (kMmaConsumerWarps + 1) * 16 * 4;
-// 3- and 4-token windows over 8-bit caches keep their Q^T fragments in
+// 3- and 4-token windows over 8- and 4-bit caches keep their Q^T fragments in
 // shared memory, one copy per CTA ([k-step][lane][n-tile][2 words]; in the
 // balanced schedule's merge area, idle while a piece streams, else after the
 // ring's barriers): 32 registers fewer, so each warp can take two slabs of a
 // tile together without spills.
-__host__ __device__ constexpr bool mma_q_in_smem(int kvf, int nq) { return is_8bit(kvf) && nq > 2; }
+__host__ __device__ constexpr bool mma_q_in_smem(int kvf, int nq) { return is_narrow(kvf) && nq > 2; }
 constexpr int kQSmemBytes = 8 * 32 * 2 * 2 * 4;
 __host__ __device__ constexpr int mma_smem_bytes(int kvf, int nq, bool bal = false) {
-  return mma_stages(kvf, nq) * (kStageBytes + kScaleStageBytes + 2 * 8) + (bal ? kBalMergeBytes + kBalRunBytes : 0) +
+  return mma_stages(kvf, nq) * (stage_bytes(kvf) + scale_stage_bytes(kvf) + 2 * 8) + (bal ? kBalMergeBytes + kBalRunBytes : 0) +
          (!bal && mma_q_in_smem(kvf, nq) ? kQSmemBytes : 0);
 }
 static_assert(kQSmemBytes <= kBalMergeBytes, "the Q^T fragments fit the merge area");
@@ -157,20 +164,27 @@ static_assert(2 * (mma_smem_bytes(kKvF16, kMaxQLen, true) + 1024) <= 228 * 1024 
                   2 * (mma_smem_bytes(kKvF16, 1, true) + 1024) <= 228 * 1024 &&
                   3 * (mma_smem_bytes(kKvE4M3, 1, true) + 1024) <= 228 * 1024 &&
                   3 * (mma_smem_bytes(kKvE4M3, 2, true) + 1024) <= 228 * 1024 &&
-                  2 * (mma_smem_bytes(kKvE4M3, kMaxQLen, true) + 1024) <= 228 * 1024,
+                  2 * (mma_smem_bytes(kKvE4M3, kMaxQLen, true) + 1024) <= 228 * 1024 &&
+                  3 * (mma_smem_bytes(kKvE2M1, 1, true) + 1024) <= 228 * 1024 &&
+                  3 * (mma_smem_bytes(kKvE2M1, 2, true) + 1024) <= 228 * 1024 &&
+                  2 * (mma_smem_bytes(kKvE2M1, kMaxQLen, true) + 1024) <= 228 * 1024,
               "the balanced schedule keeps its residency");
 // With one piece per CTA the epilogue merges the 4 warps' states in the ring
 // (idle by then): [warp][column][128] accumulators + [warp][column] max and
 // denominator.
-static_assert(kMmaConsumerWarps * kGroup * 2 * (kD + 2) * 4 <= mma_stages(kKvE4M3, 2) * kStageBytes &&
-                  kMmaConsumerWarps * kGroup * kMaxQLen * (kD + 2) * 4 <= mma_stages(kKvF16, kMaxQLen) * kStageBytes,
+static_assert(kMmaConsumerWarps * kGroup * 2 * (kD + 2) * 4 <= mma_stages(kKvE4M3, 2) * stage_bytes(kKvE4M3) &&
+                  kMmaConsumerWarps * kGroup * kMaxQLen * (kD + 2) * 4 <= mma_stages(kKvF16, kMaxQLen) * stage_bytes(kKvF16),
               "merge area must fit in the ring");
 
 // ... and the cluster merge's state [column][128] + max + denominator after it.
 static_assert(kMmaConsumerWarps * kGroup * kMaxQLen * (kD + 2) * 4 + kGroup * kMaxQLen * (kD + 2) * 4 <=
-                      mma_stages(kKvF16, kMaxQLen) * kStageBytes &&
+                      mma_stages(kKvF16, kMaxQLen) * stage_bytes(kKvF16) &&
                   kMmaConsumerWarps * kGroup * 2 * (kD + 2) * 4 + kGroup * 2 * (kD + 2) * 4 <=
-                      mma_stages(kKvE4M3, 2) * kStageBytes,
+                      mma_stages(kKvE4M3, 2) * stage_bytes(kKvE4M3) &&
+                  kMmaConsumerWarps * kGroup * kMaxQLen * (kD + 2) * 4 + kGroup * kMaxQLen * (kD + 2) * 4 <=
+                      mma_stages(kKvE2M1, kMaxQLen) * stage_bytes(kKvE2M1) &&
+                  kMmaConsumerWarps * kGroup * 2 * (kD + 2) * 4 + kGroup * 2 * (kD + 2) * 4 <=
+                      mma_stages(kKvE2M1, 2) * stage_bytes(kKvE2M1),
               "cluster merge state must fit in the ring");
 
 // ---------------------------------------------------------------- mma.sync
@@ -299,11 +313,14 @@ constexpr bool kMmaBF16 = KVF == kKvBF16;
 //              ks = 2i + h covers chunk dims 4h..4h+3 (a0 <- 4h,4h+1; a2 <- 4h+2,4h+3)
 //   e4m3 KV:   lane cq reads 16-byte chunks cq + 4i (i = 0..1, 16 dims each);
 //              ks = 4i + s covers chunk dims 4s..4s+3 (a0 <- 4s,4s+1; a2 <- 4s+2,4s+3)
+//   e2m1 KV:   lane cq reads its 16-byte chunk (dims 32cq..32cq+31, two scale
+//              groups); ks covers its dims 4ks..4ks+3 (a0 <- 4ks,4ks+1; a2 <- +2,+3)
 // The Q^T B-fragment (b0 = Q[head gq][kp 2cq,2cq+1], b1 = [2cq+8, 2cq+9]) uses
 // the same map, so the dot products are unchanged.
 template <int KVF>
 __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2/b1*/) {
-  if constexpr (is_8bit(KVF)) return 16 * (cq + 4 * (ks >> 2)) + 4 * (ks & 3) + 2 * pair;
+  if constexpr (KVF == kKvE2M1) return 32 * cq + 4 * ks + 2 * pair;
+  else if constexpr (is_8bit(KVF)) return 16 * (cq + 4 * (ks >> 2)) + 4 * (ks & 3) + 2 * pair;
   else return 8 * (cq + 4 * (ks >> 1)) + 4 * (ks & 1) + 2 * pair;
 }
 
@@ -519,14 +536,20 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
   // tokens 507.9 / 540.7 -> 503.8 / 507.9, int8 618.5 / 620.5 -> 602.1 /
   // 616.4 (pairs with Q in registers spilled more and made all but the e4m3
   // 4-token window slower).
-  constexpr int kSG = is_8bit(KVF) && NQ > 2 ? 2 : 1;
+  constexpr int kSG = is_narrow(KVF) && NQ > 2 ? 2 : 1;
   constexpr bool kQS = mma_q_in_smem(KVF, NQ);
   static_assert(kSlabs % kSG == 0, "whole slab groups");
   constexpr int kCols = kGroup * NQ;                            // (query token, head) columns
   constexpr int kNT = (kCols + 7) / 8;                          // 8-column mma n-tiles
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
-  uint16_t* scl = reinterpret_cast<uint16_t*>(smem + kMmaStages * kStageBytes);  // [stage][K|V][128]
+  constexpr int kStageBytes = stage_bytes(KVF);
+  constexpr int kScaleStageBytes = scale_stage_bytes(KVF);
+  // a row's scales (int8: one bf16; e2m1: eight e4m3)
+  constexpr bool kScaled = scale_row_bytes(KVF) > 0;
+  using RowScale = std::conditional_t<KVF == kKvE2M1, uint2, uint16_t>;
+  constexpr int kScaleRowsPer16 = 16 / (int)sizeof(RowScale);
+  RowScale* scl = reinterpret_cast<RowScale*>(smem + kMmaStages * kStageBytes);  // [stage][K|V][128]
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scl) + kMmaStages * kScaleStageBytes);
   uint64_t* empty = full + kMmaStages;
   static_assert(!(BAL && CL), "the cluster merge serves the one-piece grid");
@@ -734,7 +757,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
         const int rows = min(T::kTile, t_end - t0);
         uint8_t* dK = ring + st * kStageBytes;
         uint8_t* dV = dK + T::kTileBytes;
-        uint16_t* dsk = scl + st * (kScaleStageBytes / 2);
+        RowScale* dsk = scl + st * (kScaleStageBytes / (int)sizeof(RowScale));
         // The page of slot t (all lanes take part: they fetch block-table
         // entries 32 at a time): its id, the row in it, and the end of the
         // segment [t, seg_end) that stays in it.  A contiguous cache is one
@@ -762,24 +785,27 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
             seg_end = min(t0 + rows, (pg + 1) << p.page_log2);
           }
         };
-        // int8 row scales ([page or b][2][8][rows] bf16): whole 16-byte groups
-        // of 8 rows by bulk copy with their page segment, the ragged tail
-        // (< 8 rows, all in the last page) by plain loads before the arrive
-        const int n8 = rows & ~7;
-        if constexpr (KVF == kKvI8) {
+        // Row scales ([page or b][2][8][rows], int8: a bf16; e2m1: 8 bytes):
+        // whole 16-byte groups (8 or 2 rows) by bulk copy with their page
+        // segment, the ragged tail (all in the last page) by plain loads
+        // before the arrive
+        const RowScale* const scales = static_cast<const RowScale*>(p.kv_scales);
+        const int n8 = rows & ~(kScaleRowsPer16 - 1);
+        if constexpr (kScaled) {
           if (n8 < rows) {
             size_t page;
             int in_page, seg_end;
             seg_of(t0 + n8, page, in_page, seg_end);
             if (lane == 0) {
-              const uint16_t* gs = p.kv_scales + (page * 2 * kHkv + g) * page_rows + in_page;
+              const RowScale* gs = scales + (page * 2 * kHkv + g) * page_rows + in_page;
               for (int r = 0; r < rows - n8; ++r) {
-                const uint16_t* sk = gs + r;
-                const uint16_t* sv = gs + (size_t)kHkv * page_rows + r;
+                const RowScale* sk = gs + r;
+                const RowScale* sv = gs + (size_t)kHkv * page_rows + r;
                 if constexpr (kChecked) {
-                  if (!in_extent(p.kv_scales, p.scales_bytes, sk, 2) || !in_extent(p.kv_scales, p.scales_bytes, sv, 2)) {
+                  if (!in_extent(scales, p.scales_bytes, sk, sizeof(RowScale)) ||
+                      !in_extent(scales, p.scales_bytes, sv, sizeof(RowScale))) {
                     atomicOr(p.flags, GQA_FLAG_BOUNDS);
-                    sk = sv = p.kv_scales;
+                    sk = sv = scales;
                   }
                 }
                 dsk[n8 + r] = *sk;
@@ -788,7 +814,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
             }
           }
         }
-        const uint32_t scale_bytes = KVF == kKvI8 ? 4u * (uint32_t)n8 : 0u;
+        const uint32_t scale_bytes = kScaled ? 2u * (uint32_t)sizeof(RowScale) * (uint32_t)n8 : 0u;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], 2u * (uint32_t)rows * T::kRowBytes + scale_bytes);
         for (int t = t0; t < t0 + rows;) {
           size_t page;
@@ -808,17 +834,17 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
             }
             bulk_load(dK + (t - t0) * T::kRowBytes, src, seg_bytes, &full[st], pol);
             bulk_load(dV + (t - t0) * T::kRowBytes, srcV, seg_bytes, &full[st], pol);
-            if constexpr (KVF == kKvI8) {
+            if constexpr (kScaled) {
               const int s_end = min(seg_end, t0 + n8);
               if (s_end > t) {
-                const uint16_t* gs = p.kv_scales + (page * 2 * kHkv + g) * page_rows + in_page;
-                const uint16_t* gsv = gs + (size_t)kHkv * page_rows;
-                const uint32_t sb = (uint32_t)(s_end - t) * 2u;
+                const RowScale* gs = scales + (page * 2 * kHkv + g) * page_rows + in_page;
+                const RowScale* gsv = gs + (size_t)kHkv * page_rows;
+                const uint32_t sb = (uint32_t)(s_end - t) * (uint32_t)sizeof(RowScale);
                 if constexpr (kChecked) {
-                  if (!in_extent(p.kv_scales, p.scales_bytes, gs, sb) || !in_extent(p.kv_scales, p.scales_bytes, gsv, sb)) {
+                  if (!in_extent(scales, p.scales_bytes, gs, sb) || !in_extent(scales, p.scales_bytes, gsv, sb)) {
                     atomicOr(p.flags, GQA_FLAG_BOUNDS);
-                    gs = p.kv_scales;
-                    gsv = p.kv_scales + (size_t)kHkv * page_rows;
+                    gs = scales;
+                    gsv = scales + (size_t)kHkv * page_rows;
                   }
                 }
                 bulk_load(dsk + (t - t0), gs, sb, &full[st], pol);
@@ -868,14 +894,14 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
     }
 
     // Q^T B-fragments: column gq of each n-tile (zero for padding).  A bf16 q
-    // meeting f16 tensor cores (8-bit KV) is first scaled by a power of two
+    // meeting f16 tensor cores (8- and 4-bit KV) is first scaled by a power of two
     // 2^e per column, chosen so that the column's largest |q| lands in
     // [2^14, 2^15): every element of magnitude >= 2^-31 of that maximum is
     // then exact in f16, the rest round on the f16 subnormal grid (2^-39 of
     // the maximum at most), and nothing saturates.  The column's score scale
     // takes 2^-e (sl2c below); power-of-two scaling commutes with FP32
     // rounding, so a q already in f16 range scores bit for bit as unscaled.
-    constexpr bool kQPow2 = is_8bit(KVF) && QF == kQBF16;
+    constexpr bool kQPow2 = is_narrow(KVF) && QF == kQBF16;
     uint32_t qb[kNT][8][2];
     float sl2c[kNT][2];  // score scale of this lane's columns 2cq, 2cq+1 (scale_log2 * 2^-e)
   #pragma unroll
@@ -984,9 +1010,10 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
       const int rows = min(T::kTile, t_end - tile_t0);
       // int8: the bf16 row scale of tile row r (plane 0: K, 1: V), read where
       // it is used (fewer live registers); 0 past the tile's rows
-      const uint16_t* tsk = scl + st * (kScaleStageBytes / 2);
+      const RowScale* tsk = scl + st * (kScaleStageBytes / (int)sizeof(RowScale));
       const auto row_scale = [&](int r, int plane) {
-        return r < rows ? __uint_as_float((uint32_t)tsk[plane * T::kTile + r] << 16) : 0.f;
+        return r < rows ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(tsk)[plane * T::kTile + r] << 16)
+                        : 0.f;
       };
 
   #pragma unroll
@@ -1013,7 +1040,41 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
         {
           const uint8_t* k0 = sK + (R + gq) * T::kRowBytes;
           const uint8_t* k1 = k0 + 8 * T::kRowBytes;
-          if constexpr (is_8bit(KVF)) {
+          if constexpr (KVF == kKvE2M1) {
+            // The group scales join K here: code * scale is exact in f16 (at
+            // most 2 + 4 significand bits, magnitudes 2^-10 to 2688), so the
+            // scores need no step of their own.  Lane cq's chunk is the whole
+            // of groups 2cq and 2cq + 1.  Past the tile's rows the scales are
+            // whatever the stage held; those scores are masked below.
+            const uint4 x = *reinterpret_cast<const uint4*>(k0 + 16 * cq);
+            const uint4 y = *reinterpret_cast<const uint4*>(k1 + 16 * cq);
+            const uint16_t* skr = reinterpret_cast<const uint16_t*>(tsk + R + gq) + cq;
+            const uint32_t sa = e4m3x2_to_f16x2(skr[0]), sb = e4m3x2_to_f16x2(skr[8 * 4]);
+            const uint32_t sal[2] = {prmt(sa, sa, 0x1010u), prmt(sa, sa, 0x3232u)};
+            const uint32_t sbl[2] = {prmt(sb, sb, 0x1010u), prmt(sb, sb, 0x3232u)};
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  #pragma unroll
+            for (int w = 0; w < 4; ++w) {  // word w: dims 32cq + 8w .. +7, k-steps 2w and 2w + 1
+              uint32_t a[4], c[4];
+              e2m1x8_to_f16(xs[w], a);  // row gq
+              e2m1x8_to_f16(ys[w], c);  // row gq + 8
+  #pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int ks = 2 * w + h;
+                const uint32_t a0 = mul_f16x2(a[2 * h], sal[w >> 1]), a2 = mul_f16x2(a[2 * h + 1], sal[w >> 1]);
+                const uint32_t a1 = mul_f16x2(c[2 * h], sbl[w >> 1]), a3 = mul_f16x2(c[2 * h + 1], sbl[w >> 1]);
+                if constexpr (kQS) {
+                  const uint4 qv = ld_shared_u4(qfr + (ks * 32 + lane) * 4);
+                  mma16816<false>(sc[0], a0, a1, a2, a3, qv.x, qv.y);
+                  mma16816<false>(sc[kNT - 1], a0, a1, a2, a3, qv.z, qv.w);
+                } else {
+  #pragma unroll
+                  for (int nt = 0; nt < kNT; ++nt)
+                    mma16816<false>(sc[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
+                }
+              }
+            }
+          } else if constexpr (is_8bit(KVF)) {
   #pragma unroll
             for (int ci = 0; ci < 2; ++ci) {
               const uint4 x = *reinterpret_cast<const uint4*>(k0 + 16 * (cq + 4 * ci));
@@ -1183,7 +1244,43 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
         const uint8_t* v0 = sV + r0 * T::kRowBytes;
         const bool ok0 = !partial || r0 < rows, ok1 = !partial || r0 + 1 < rows;
         const bool ok2 = !partial || r0 + 8 < rows, ok3 = !partial || r0 + 9 < rows;
-        if constexpr (is_8bit(KVF)) {
+        if constexpr (KVF == kKvE2M1) {
+          // 8 bytes a token: dims 16gq..16gq+15, one scale group.  Nibbles of
+          // the two tokens of a pair are joined into bytes, so that each
+          // conversion yields one dim of both tokens; code * scale is exact.
+          // A token past the tile's rows takes scale 0 (its weight is 0, but
+          // its stale scale could be NaN).
+          const uint2 w0 = *reinterpret_cast<const uint2*>(v0 + 8 * gq);
+          const uint2 w1 = *reinterpret_cast<const uint2*>(v0 + T::kRowBytes + 8 * gq);
+          const uint2 w2 = *reinterpret_cast<const uint2*>(v0 + 8 * T::kRowBytes + 8 * gq);
+          const uint2 w3 = *reinterpret_cast<const uint2*>(v0 + 9 * T::kRowBytes + 8 * gq);
+          const uint8_t* svr = reinterpret_cast<const uint8_t*>(tsk + T::kTile + r0) + gq;
+          uint32_t s0 = svr[0], s1 = svr[8], s2 = svr[64], s3 = svr[72];
+          if (!ok0) s0 = 0u;
+          if (!ok1) s1 = 0u;
+          if (!ok2) s2 = 0u;
+          if (!ok3) s3 = 0u;
+          const uint32_t sA = e4m3x2_to_f16x2((uint16_t)(s0 | (s1 << 8)));  // tokens r0, r0 + 1
+          const uint32_t sB = e4m3x2_to_f16x2((uint16_t)(s2 | (s3 << 8)));  // tokens r0 + 8, r0 + 9
+          const uint32_t a[2] = {w0.x, w0.y}, bq[2] = {w1.x, w1.y}, c[2] = {w2.x, w2.y}, d[2] = {w3.x, w3.y};
+          constexpr uint32_t kLow = 0x0f0f0f0fu;
+  #pragma unroll
+          for (int j = 0; j < 2; ++j) {  // word j: dims 16gq + 8j .. +7 -> m-tiles 4j..4j+3
+            uint32_t e0[4], e1[4], e2[4], e3[4];
+            e2m1x8_to_f16((a[j] & kLow) | ((bq[j] << 4) & ~kLow), e0);  // even dims of tokens r0, r0 + 1
+            e2m1x8_to_f16(((a[j] >> 4) & kLow) | (bq[j] & ~kLow), e1);  // odd dims
+            e2m1x8_to_f16((c[j] & kLow) | ((d[j] << 4) & ~kLow), e2);   // tokens r0 + 8, r0 + 9
+            e2m1x8_to_f16(((c[j] >> 4) & kLow) | (d[j] & ~kLow), e3);
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t A0 = mul_f16x2(e0[i], sA), A1 = mul_f16x2(e1[i], sA);
+              const uint32_t A2 = mul_f16x2(e2[i], sB), A3 = mul_f16x2(e3[i], sB);
+  #pragma unroll
+              for (int nt = 0; nt < kNT; ++nt)
+                mma16816<false>(o[nt][4 * j + i], A0, A1, A2, A3, bh[sj][nt][0], bh[sj][nt][1]);
+            }
+          }
+        } else if constexpr (is_8bit(KVF)) {
           uint4 w0 = *reinterpret_cast<const uint4*>(v0 + 16 * gq);
           uint4 w1 = *reinterpret_cast<const uint4*>(v0 + T::kRowBytes + 16 * gq);
           uint4 w2 = *reinterpret_cast<const uint4*>(v0 + 8 * T::kRowBytes + 16 * gq);

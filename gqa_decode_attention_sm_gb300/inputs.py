@@ -17,6 +17,11 @@ An INT8 cache (kv_dtype "i8") stores int8 codes with one bf16 scale per
 (plane, KV head, position) row: scale = amax(|row|)/127 rounded to bf16,
 code = round(x / scale) clipped to [-127, 127].
 
+A 4-bit cache (kv_dtype "e2m1") stores two e2m1 codes to a byte (dim 2j in the
+low nibble of byte j), one e4m3 scale for every 16 dims of a row (the group's
+amax / 6 / tensor scale) and a tensor scale each for K and V (k_scale,
+v_scale): amax / (6 * 448) over the plane.
+
 Recipe: a torch.Generator on the target device; lengths drawn first from
 ``seed``; q from ``seed + 1``; the KV slice of batch row b from
 ``seed * 7919 + 1000 + b`` so rows can be generated (and regenerated) one at a
@@ -36,7 +41,7 @@ E4M3_MAX = 448.0
 class Workload:
     index: int
     name: str
-    kv_dtype: str          # "f16" | "bf16" | "e4m3" | "i8"
+    kv_dtype: str          # "f16" | "bf16" | "e4m3" | "i8" | "e2m1"
     q_dtype: str           # "f16" | "bf16"
     batch: int
     capacity: int
@@ -68,7 +73,7 @@ def custom(batch: int, capacity: int, len_lo: int, len_hi: int | None = None,
            kv_std: float = 1.0, q_scale: float = 1.0, index: int = 0, q_len: int = 1) -> Workload:
     """A workload of any size with the same recipe (edge cases, small tests)."""
     if q_dtype is None:
-        q_dtype = "bf16" if kv_dtype in ("e4m3", "i8") else kv_dtype
+        q_dtype = "bf16" if kv_dtype in ("e4m3", "i8", "e2m1") else kv_dtype
     return Workload(index, f"custom B{batch} C{capacity}", kv_dtype, q_dtype, batch, capacity,
                     len_lo, len_lo if len_hi is None else len_hi, nan_tail, kv_std, q_scale, q_len)
 
@@ -83,7 +88,7 @@ def _gen(device, seed: int) -> torch.Generator:
 
 
 def kv_storage_dtype(w: Workload) -> torch.dtype:
-    if w.kv_dtype == "e4m3":
+    if w.kv_dtype in ("e4m3", "e2m1"):
         return torch.uint8
     if w.kv_dtype == "i8":
         return torch.int8
@@ -98,12 +103,37 @@ def _kv_row_fp32(w: Workload, b: int, device, seed: int) -> torch.Tensor:
     return x
 
 
+def quantise_e2m1(x: torch.Tensor, scale: float):
+    """Rows x [..., 128] (fp32 or fp64) as e2m1 bytes [..., 64] and e4m3 group
+    scales (as bytes) [..., 8]; to the nearest level, ties to the even code."""
+    g = (x / scale).unflatten(-1, (8, 16))
+    s = (g.abs().amax(-1) / 6).clamp(max=E4M3_MAX).to(torch.float32).to(torch.float8_e4m3fn)
+    wide = s.to(x.dtype).unsqueeze(-1)
+    t = torch.where(wide > 0, g / wide, torch.zeros_like(g))
+    m = t.abs().clamp(max=6)
+    step = torch.where(m < 2, 0.5, torch.where(m < 4, 1.0, 2.0)).to(x.dtype)
+    m = (m / step).round() * step
+    c = torch.where(m < 2, 2 * m, torch.where(m < 4, m + 2, m / 2 + 4)).to(torch.uint8)
+    c = (c | ((t < 0).to(torch.uint8) << 3)).flatten(-2)
+    return c[..., 0::2] | (c[..., 1::2] << 4), s.view(torch.uint8)
+
+
+def dequantise_e2m1(codes: torch.Tensor, scales: torch.Tensor, scale: float) -> torch.Tensor:
+    """The fp64 values [..., 128] of e2m1 bytes [..., 64] and scale bytes [..., 8]."""
+    level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=codes.device)
+    level = torch.cat((level, -level))
+    n = torch.stack((codes & 15, codes >> 4), -1).flatten(-2).long()
+    s = scales.contiguous().view(torch.float8_e4m3fn).to(torch.float64) * scale
+    return (level[n].unflatten(-1, (8, 16)) * s.unsqueeze(-1)).flatten(-2)
+
+
 def make(w: Workload, device="cpu", seed: int | None = None, lens=None) -> dict:
     """Build one batch of inputs on ``device``.
 
     Returns a dict with q [B,32,128] ([B,q_len,32,128] for a verify window),
     kv [B,2,8,C,128] (uint8 bytes for e4m3,
-    int8 codes for i8), kv_scales (bf16 [B,2,8,C] for i8, else None), lens
+    int8 codes for i8; [B,2,8,C,64] bytes for e2m1), kv_scales (bf16 [B,2,8,C]
+    for i8, uint8 [B,2,8,C,8] for e2m1, else None), lens
     int32 [B], q_scale, k_scale, v_scale (python floats; the e4m3 scale is the
     fp32 value actually stored), and the workload.
     ``lens`` overrides the drawn lengths (a list or tensor of B ints).
@@ -123,7 +153,7 @@ def make(w: Workload, device="cpu", seed: int | None = None, lens=None) -> dict:
     q = torch.randn(q_shape, generator=_gen(device, seed + 1), device=device,
                     dtype=torch.float32).to(_TORCH[w.q_dtype])
 
-    kv = torch.empty((B, 2, HKV, C, D), device=device, dtype=kv_storage_dtype(w))
+    kv = torch.empty((B, 2, HKV, C, D // 2 if w.kv_dtype == "e2m1" else D), device=device, dtype=kv_storage_dtype(w))
     k_scale = v_scale = 1.0
     kv_scales = None
     if w.kv_dtype == "i8":
@@ -135,6 +165,16 @@ def make(w: Workload, device="cpu", seed: int | None = None, lens=None) -> dict:
             codes = torch.round(x / sc.float().unsqueeze(-1)).clamp_(-127, 127)
             kv[b].copy_(codes.to(torch.int8))
             kv_scales[b].copy_(sc)
+    elif w.kv_dtype == "e2m1":
+        kv_scales = torch.empty((B, 2, HKV, C, 8), device=device, dtype=torch.uint8)
+        amax = torch.zeros(2, device=device, dtype=torch.float32)
+        for b in range(B):
+            amax = torch.maximum(amax, _kv_row_fp32(w, b, device, seed).abs().amax(dim=(1, 2, 3)))
+        k_scale, v_scale = (float(a) for a in (amax / (6 * E4M3_MAX)).tolist())
+        for b in range(B):
+            x = _kv_row_fp32(w, b, device, seed)
+            for p, sc in ((0, k_scale), (1, v_scale)):
+                kv[b, p], kv_scales[b, p] = quantise_e2m1(x[p], sc)
     elif w.kv_dtype == "e4m3":
         # one amax over every K and V value of the allocated cache
         amax = torch.zeros((), device=device, dtype=torch.float32)
@@ -152,7 +192,7 @@ def make(w: Workload, device="cpu", seed: int | None = None, lens=None) -> dict:
         fill_tail(kv, lens_t, w.kv_dtype)
         if kv_scales is not None:  # codes have no NaN: poison the unused rows' scales instead
             for b, L in enumerate(lens_t.tolist()):
-                kv_scales[b, :, :, L:] = float("nan")
+                kv_scales[b, :, :, L:] = 0x7F if w.kv_dtype == "e2m1" else float("nan")
     return dict(q=q, kv=kv, lens=lens_t.to(device), q_scale=w.q_scale, k_scale=k_scale,
                 v_scale=v_scale, kv_scales=kv_scales, workload=w)
 
@@ -193,7 +233,9 @@ def fill_tail(kv: torch.Tensor, lens, kv_dtype: str, value: float = float("nan")
     for b, L in enumerate(lens_l):
         if L >= kv.shape[3]:
             continue
-        if kv_dtype == "i8":  # codes cannot hold NaN: use the extreme code
+        if kv_dtype == "e2m1":  # codes cannot hold NaN: the largest magnitude
+            kv[b, :, :, L:, :].fill_(0xFF)
+        elif kv_dtype == "i8":  # codes cannot hold NaN: use the extreme code
             kv[b, :, :, L:, :].fill_(-128 if value != value else int(max(-127, min(127, value))))
         elif kv_dtype == "e4m3":
             if value != value:  # NaN
@@ -254,7 +296,8 @@ def paginate(t: dict, page_size: int, extra_pages: int = 3, seed: int = 0) -> di
     scales = t.get("kv_scales")
     spages = None
     if scales is not None:
-        spages = torch.full((num_pages, 2, H, page_size), float("nan"), dtype=scales.dtype, device=kv.device)
+        spages = torch.full((num_pages, 2, H, page_size, *scales.shape[4:]),
+                            0x7F if scales.dtype == torch.uint8 else float("nan"), dtype=scales.dtype, device=kv.device)
     spare = [int(x) for x in ids[len(used):]] or [int(ids[0])]
     table = torch.full((B, per), spare[0], dtype=torch.int32)
     for n, (b, j) in enumerate(used):

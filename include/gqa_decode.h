@@ -12,16 +12,18 @@
  *   that splits the 32 heads into 8 groups of 4 consecutive heads).  For every batch row b and query head h:
  *     s_t   = q_scale * k_scale / sqrt(128) * dot(q[b,h,:], K[b,g,t,:]),  0 <= t < len[b]
  *     out[b,h,:] = v_scale * sum_t softmax(s)_t * V[b,g,t,:]
- *   k_scale = v_scale = 1 except on the e4m3 entry point.  Slots t >= len[b]
+ *   k_scale = v_scale = 1 except for the e4m3 and e2m1 caches.  Slots t >= len[b]
  *   are never read.  Arithmetic is FP32 (exp2-domain online softmax); the
  *   output is rounded once to fp16/bf16, round-to-nearest-even.
  *
  * Layouts (all dense, row-major, contiguous; element offsets):
  *   q    [batch, 32, 128]              fp16 or bf16 (gqa_dtype_t)
  *   kv   [batch, 2, 8, capacity, 128]  plane 0 = K, plane 1 = V; same dtype
- *                                      as q, e4m3 bytes (fp8 entry) or int8
- *                                      codes with bf16 row scales (int8 entry);
- *                                      a paged pool on the paged entries
+ *                                      as q, e4m3 bytes (fp8 entry), int8
+ *                                      codes with bf16 row scales (int8 entry)
+ *                                      or [..., 64] bytes of e2m1 pairs with
+ *                                      e4m3 group scales (fp4 entry); a paged
+ *                                      pool on the paged entries
  *   lens int32 [batch], device memory, read only by the kernels; the contract
  *        is 1 <= lens[b] <= capacity (see "Lengths" below)
  *   out  [batch, 32, 128]              same dtype as q (bf16 on the fp8 entry)
@@ -93,7 +95,13 @@ typedef enum {
 
 typedef enum { GQA_F16 = 0, GQA_BF16 = 1 } gqa_dtype_t;
 
-typedef enum { GQA_KV_F16 = 0, GQA_KV_BF16 = 1, GQA_KV_E4M3 = 2, GQA_KV_I8 = 3 } gqa_kv_format_t;
+typedef enum {
+  GQA_KV_F16 = 0,
+  GQA_KV_BF16 = 1,
+  GQA_KV_E4M3 = 2,
+  GQA_KV_I8 = 3,
+  GQA_KV_E2M1 = 4 /* 4 bits: see gqa_decode_fp4kv */
+} gqa_kv_format_t;
 
 /* Bits of the status word in the workspace header. */
 #define GQA_FLAG_LENGTH_CLAMPED 0x1u  /* some lens[b] was outside [1, capacity] */
@@ -130,7 +138,7 @@ gqa_status_t gqa_decode_plan_for(int batch, int capacity, gqa_kv_format_t kv_for
                                  int* num_splits_out);
 
 /* Split geometry (pure host arithmetic): tokens per split, rounded up to
- * whole 64-token (fp16/bf16) or 128-token (8-bit) tiles, and the number of
+ * whole 64-token (fp16/bf16) or 128-token (8- and 4-bit) tiles, and the number of
  * splits that hold slots, ceil(capacity / chunk) <= num_splits.  With one
  * piece per CTA, split s covers slots [s * chunk, min((s + 1) * chunk, len));
  * the balanced schedule cuts rows elsewhere but never into more pieces.
@@ -198,15 +206,32 @@ gqa_status_t gqa_decode_int8kv(const void* q, const int8_t* kv_i8, const uint16_
                                gqa_dtype_t dtype, float q_scale, int num_splits, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* FP4 KV cache: e2m1 codes in blocks of 16 with an e4m3 scale each, and one
+ * FP32 scale for all keys and one for all values (the two-level scaling of
+ * the FP4 tensor formats).  kv_e2m1 is [batch, 2, 8, capacity, 64] bytes: byte j of a row holds
+ * dims 2j (low nibble) and 2j + 1 (high nibble), each a sign bit and one of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6.  kv_scales_e4m3 is [batch, 2, 8, capacity, 8]
+ * e4m3fn bytes, 16-byte aligned: byte j scales dims 16j .. 16j + 15.  Element
+ * d of a key row is code[d] * scale[d / 16] * k_scale, of a value row the
+ * same with v_scale.  capacity must be a multiple of 2 (the scales are staged
+ * by 16-byte bulk copies).  q and out are fp16 or bf16 (`dtype`).  Codes and
+ * scales of slots >= len[b] are never used.  k_scale and v_scale finite and
+ * > 0, q_scale finite and >= 0.  Other rules as gqa_decode_prepared (no
+ * allocation, no host sync).  The pages have no counterpart to this call. */
+gqa_status_t gqa_decode_fp4kv(const void* q, const uint8_t* kv_e2m1, const uint8_t* kv_scales_e4m3,
+                              const int32_t* lens, void* out, int batch, int capacity,
+                              gqa_dtype_t dtype, float q_scale, float k_scale, float v_scale,
+                              int num_splits, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Paged KV cache.  The pages only say that a paged cache is gathered into
  * one contiguous prefix matrix before attention; this entry reads the pages
  * in place instead, with the same result.  Layout (this library's reading):
  *   kv_pages        [num_pages, 2, 8, page_size, 128] in `kv_format` (fp16,
- *                   bf16, e4m3 or int8), each (page, plane, KV head) block
- *                   contiguous
- *   kv_scales_pages int8 only (NULL otherwise): bf16 [num_pages, 2, 8,
- *                   page_size], the row scales of the same page rows,
- *                   16-byte aligned
+ *                   bf16, e4m3 or int8; e2m1: [..., page_size, 64] bytes),
+ *                   each (page, plane, KV head) block contiguous
+ *   kv_scales_pages int8: bf16 [num_pages, 2, 8, page_size]; e2m1: e4m3 bytes
+ *                   [num_pages, 2, 8, page_size, 8]; the row scales of the
+ *                   same page rows, 16-byte aligned (NULL otherwise)
  *   block_table     int32 [batch, max_pages_per_seq], device memory, read only
  *                   by the kernels: slot t of batch row b is row t % page_size
  *                   of page block_table[b][t / page_size]
@@ -217,12 +242,12 @@ gqa_status_t gqa_decode_int8kv(const void* q, const int8_t* kv_i8, const uint16_
  * GQA_FLAG_PAGE_CLAMPED, never dereferenced out of bounds.  q_len 1..4: q
  * and out are [batch, q_len, 32, 128] and query j attends slots
  * [0, len - q_len + j] (gqa_decode_verify); 1 is plain decode.  q/out dtype
- * `q_dtype` (must equal fp16/bf16 KV; either for 8-bit KV).  k_scale,
- * v_scale as gqa_decode_fp8kv (1 for the other formats).  Both stages, no
+ * `q_dtype` (must equal fp16/bf16 KV; either for 8- and 4-bit KV).  k_scale,
+ * v_scale as gqa_decode_fp8kv (1 for the other formats but e2m1).  Both stages, no
  * allocation, no host sync; the workspace as gqa_decode_prepared for batch
  * * q_len rows and capacity max_pages_per_seq * page_size. */
 gqa_status_t gqa_decode_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages,
-                              gqa_kv_format_t kv_format, const uint16_t* kv_scales_pages,
+                              gqa_kv_format_t kv_format, const void* kv_scales_pages,
                               const int32_t* block_table, int max_pages_per_seq, int num_pages,
                               int page_size, const int32_t* lens, void* out, int batch, int q_len,
                               float q_scale, float k_scale, float v_scale, int num_splits,
@@ -237,11 +262,12 @@ gqa_status_t gqa_decode_paged(const void* q, gqa_dtype_t q_dtype, const void* kv
  * holds gqa_decode_workspace_size(batch * q_len, capacity, num_splits) bytes.
  * Lengths must lie in [q_len, capacity]; a query with no slot (len below
  * q_len) gets a zero row and GQA_FLAG_LENGTH_CLAMPED.  kv_format: fp16 / bf16
- * (= q_dtype), e4m3 or int8 (kv_scales_bf16 as gqa_decode_int8kv, else NULL).
- * k_scale, v_scale as gqa_decode_fp8kv (1 unless e4m3).  q_scale finite and
+ * (= q_dtype), e4m3, int8 (kv_scales as gqa_decode_int8kv) or e2m1 (kv_scales
+ * as gqa_decode_fp4kv; NULL for the others).  k_scale, v_scale as
+ * gqa_decode_fp8kv (1 unless e4m3 or e2m1).  q_scale finite and
  * >= 0.  Both stages, no allocation, no host sync. */
 gqa_status_t gqa_decode_verify(const void* q, gqa_dtype_t q_dtype, const void* kv,
-                               gqa_kv_format_t kv_format, const uint16_t* kv_scales_bf16,
+                               gqa_kv_format_t kv_format, const void* kv_scales,
                                const int32_t* lens, void* out, int batch, int capacity, int q_len,
                                float q_scale, float k_scale, float v_scale, int num_splits,
                                void* workspace, size_t workspace_bytes, void* stream);
@@ -256,8 +282,9 @@ gqa_status_t gqa_decode_verify(const void* q, gqa_dtype_t q_dtype, const void* k
  * output it launches nothing.  Both must be given the same geometry, scales
  * and workspace, in this order, on one stream, with the same device
  * current.  Validation as gqa_decode_prepared, except that
- * q_scale may be 0.  Stage 1 does not take an int8 cache (it has no scale
- * argument: use gqa_decode_int8kv); stage 2 accepts every format. */
+ * q_scale may be 0.  Stage 1 does not take an int8 or e2m1 cache (it has no
+ * scale argument: use gqa_decode_int8kv or gqa_decode_fp4kv); stage 2 accepts
+ * every format. */
 gqa_status_t gqa_decode_split_stage(const void* q, gqa_dtype_t q_dtype, const void* kv,
                                     gqa_kv_format_t kv_format, const int32_t* lens, void* out,
                                     int batch, int capacity, float q_scale, float k_scale,
