@@ -22,6 +22,7 @@ EXPORTS = (
     "gqa_decode_noalloc", "gqa_decode_noalloc_get_status", "gqa_decode_debug_skip_tile",
     "gqa_decode_debug_cut_extents", "gqa_decode_int8kv", "gqa_decode_paged",
     "gqa_decode_verify", "gqa_append_kv", "gqa_append_kv_paged", "gqa_decode_fp4kv",
+    "gqa_write_kv", "gqa_write_kv_paged", "gqa_read_kv", "gqa_read_kv_paged",
 )
 
 
@@ -34,6 +35,7 @@ class GqaError(RuntimeError):
 
 def _declare(lib):
     p, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ll = ctypes.c_longlong
     sig = {
         "gqa_status_string": (ctypes.c_char_p, [i]),
         "gqa_last_error": (ctypes.c_char_p, []),
@@ -58,6 +60,11 @@ def _declare(lib):
         "gqa_decode_verify": (i, [p, i, p, i, p, p, p, i, i, i, f, f, f, i, p, sz, p]),
         "gqa_append_kv": (i, [p, p, p, p, p, i, p, p, i, p, p, i, p, i, f, f, f, f, p, sz, p]),
         "gqa_append_kv_paged": (i, [p, p, p, p, p, i, p, p, i, p, p, i, p, p, i, i, i, f, f, f, f, p, sz, p]),
+        "gqa_write_kv": (i, [p, p, p, ll, ll, ll, p, p, i, p, p, i, p, p, i, p, p, i, p, i, i, f, f, f, f, p, sz, p]),
+        "gqa_write_kv_paged": (i, [p, p, p, ll, ll, ll, p, p, i, p, p, i, p, p, i, p, p, i, p, p, i, i, i, i, f, f, f,
+                                   f, p, sz, p]),
+        "gqa_read_kv": (i, [p, i, p, p, p, p, i, i, i, i, f, f, p, sz, p]),
+        "gqa_read_kv_paged": (i, [p, i, p, p, i, i, i, p, p, p, i, i, i, f, f, p, sz, p]),
         "gqa_decode_debug_skip_tile": (i, [p, i, p, i, p, p, i, i, f, f, f, i, p, sz, i,
                                            ctypes.c_uint64, p]),
         "gqa_decode_debug_cut_extents": (i, [ctypes.c_uint64, ctypes.c_uint64]),

@@ -37,6 +37,7 @@ _FP8 = (torch.uint8, torch.float8_e4m3fn)
 
 __all__ = ["GqaError", "append_kv_paged", "gqa_decode", "gqa_decode_fp8kv", "gqa_decode_int8kv", "gqa_decode_paged",
            "gqa_decode_verify", "gqa_decode_fp4kv", "append_kv",
+           "write_kv", "write_kv_paged", "read_kv", "read_kv_paged",
            "prepare", "launch",
            "Prepared",
            "workspace_size", "plan", "get_status", "split_stage", "combine_stage", "split_geometry",
@@ -419,10 +420,10 @@ def append_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots, kv, 
     _require(k_norm_w, "k_norm_w", (D,), (dt,), q_proj.device)
     _require(positions, "positions", (B,), (torch.int32,), q_proj.device)
     _require(slots, "slots", (B,), (torch.int32,), q_proj.device)
-    if kv.dim() != 5 or kv.shape[0] != B or kv.shape[1:3] != (2, HKV) or kv.shape[4] != D:
-        raise ValueError(f"kv must be [{B}, 2, {HKV}, capacity, {D}]")
+    kvf = _kv_format(kv, "kv", B)
     _require(kv, "kv", None, tuple(_KVF), q_proj.device)
-    kvf = _KVF[kv.dtype]
+    if kvf == KV_E2M1:
+        _require_scales(kv_scales, "kv_scales", kv, kvf)
     if q_out is None:
         q_out = torch.empty_like(q_proj)
     _require(q_out, "q_out", q_proj.shape, (dt,), q_proj.device)
@@ -440,8 +441,8 @@ def append_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots
                     q_out=None, eps: float = 1e-6, rope_theta: float = 1e6, k_scale: float = 1.0,
                     v_scale: float = 1.0, kv_scales=None, workspace=None):
     """append_kv on a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and,
-    for int8, kv_scales [num_pages, 2, 8, page_size] bf16), block_table int32
-    [batch, max_pages]; slot s of row b lands in row s % page_size of page
+    for int8, kv_scales [num_pages, 2, 8, page_size] bf16; e2m1: uint8 [.., 64]
+    and e4m3 scales [.., 8]), block_table int32 [batch, max_pages]; slot s of row b lands in row s % page_size of page
     block_table[b, s // page_size]."""
     _require(q_proj, "q_proj", None, (torch.float16, torch.bfloat16))
     B = q_proj.shape[0]
@@ -453,16 +454,13 @@ def append_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots
     _require(k_norm_w, "k_norm_w", (D,), (dt,), q_proj.device)
     _require(positions, "positions", (B,), (torch.int32,), q_proj.device)
     _require(slots, "slots", (B,), (torch.int32,), q_proj.device)
-    if kv_pages.dim() != 5 or kv_pages.shape[1:3] != (2, HKV) or kv_pages.shape[4] != D:
-        raise ValueError("kv_pages must be [num_pages, 2, 8, page_size, 128]")
+    kvf = _kv_format(kv_pages, "kv_pages", None)
     _require(kv_pages, "kv_pages", None, tuple(_KVF), q_proj.device)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [batch, max_pages]")
     _require(block_table, "block_table", None, (torch.int32,), q_proj.device)
-    kvf = _KVF[kv_pages.dtype]
     num_pages, page_size = kv_pages.shape[0], kv_pages.shape[3]
-    if kvf == KV_I8:
-        _require(kv_scales, "kv_scales", (num_pages, 2, HKV, page_size), (torch.bfloat16,), q_proj.device)
+    _require_scales(kv_scales, "kv_scales", kv_pages, kvf)
     if q_out is None:
         q_out = torch.empty_like(q_proj)
     _require(q_out, "q_out", q_proj.shape, (dt,), q_proj.device)
@@ -475,6 +473,162 @@ def append_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots
             _ptr(workspace) if workspace is not None else None,
             workspace.numel() if workspace is not None else 0, _stream(q_proj.device)))
     return q_out
+
+
+def _tokens(t, name, heads, n, dtype, device):
+    """Projection [tokens, heads, 128] whose tokens may lie apart (a part of a
+    fused projection); returns its token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != (n, heads, D) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} [{n}, {heads}, {D}], got {t.dtype} {tuple(t.shape)}")
+    if n and (t.stride(2) != 1 or t.stride(1) != D):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if n > 1 else heads * D
+
+
+def _require_table(block_table, batch, device):
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    if block_table.dim() != 2 or (batch is not None and block_table.shape[0] != batch):
+        raise ValueError("block_table must be [batch, max_pages]")
+    _require(block_table, "block_table", None, (torch.int32,), device)
+
+
+def _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv, block_table, paged, q_out,
+           mrope_section, mrope_interleaved, eps, rope_theta, k_scale, v_scale, kv_scales, workspace):
+    if not isinstance(q_proj, torch.Tensor):
+        raise TypeError("q_proj must be a torch.Tensor")
+    if not q_proj.is_cuda or q_proj.dim() != 3 or q_proj.dtype not in _QDT:
+        raise ValueError(f"q_proj must be a CUDA fp16/bf16 tensor [tokens, {HQ}, {D}]")
+    n, dt, dev = q_proj.shape[0], q_proj.dtype, q_proj.device
+    strides = [_tokens(t, name, h, n, dt, dev) for t, name, h in
+               ((q_proj, "q_proj", HQ), (k_proj, "k_proj", HKV), (v_proj, "v_proj", HKV))]
+    if (q_norm_w is None) != (k_norm_w is None):
+        raise ValueError("q_norm_w and k_norm_w are given together or not at all")
+    if q_norm_w is not None:
+        _require(q_norm_w, "q_norm_w", (D,), (dt,), dev)
+        _require(k_norm_w, "k_norm_w", (D,), (dt,), dev)
+    section = None
+    if mrope_section is not None:
+        if len(mrope_section) != 3:
+            raise ValueError("mrope_section holds three counts (time, height, width)")
+        section = (ctypes.c_int * 3)(*(int(x) for x in mrope_section))
+    _require(positions, "positions", (n,) if section is None else (3, n), (torch.int32,), dev)
+    _require(rows, "rows", (n,), (torch.int32,), dev)
+    _require(slots, "slots", (n,), (torch.int32,), dev)
+    name = "kv_pages" if paged else "kv"
+    kvf = _kv_format(kv, name, None)
+    _require(kv, name, None, tuple(_KVF), dev)
+    _require_scales(kv_scales, "kv_scales", kv, kvf)
+    if paged:
+        _require_table(block_table, None, dev)
+    if workspace is not None:
+        _require(workspace, "workspace", None, (torch.uint8,), dev)
+    if q_out is None:
+        q_out = torch.empty((n, HQ, D), dtype=dt, device=dev)
+    _require(q_out, "q_out", (n, HQ, D), (dt,), dev)
+    if n == 0:
+        return q_out
+    lib = _lib.load()
+    head = (_ptr(q_proj), _ptr(k_proj), _ptr(v_proj), *strides, None if q_norm_w is None else _ptr(q_norm_w),
+            None if k_norm_w is None else _ptr(k_norm_w), _QDT[dt], _ptr(positions), section,
+            1 if mrope_interleaved else 0, _ptr(rows), _ptr(slots), n, _ptr(q_out), _ptr(kv), kvf,
+            _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None)
+    tail = (float(eps), float(rope_theta), float(k_scale), float(v_scale),
+            None if workspace is None else _ptr(workspace), 0 if workspace is None else workspace.numel())
+    with torch.cuda.device(dev):
+        if paged:
+            _lib.check(lib.gqa_write_kv_paged(*head, _ptr(block_table), block_table.shape[0], block_table.shape[1],
+                                              kv.shape[0], kv.shape[3], *tail, _stream(dev)))
+        else:
+            _lib.check(lib.gqa_write_kv(*head, kv.shape[0], kv.shape[3], *tail, _stream(dev)))
+    return q_out
+
+
+def write_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv, q_out=None, mrope_section=None,
+             mrope_interleaved: bool = False, eps: float = 1e-6, rope_theta: float = 1e6, k_scale: float = 1.0,
+             v_scale: float = 1.0, kv_scales=None, workspace=None):
+    """append_kv for many tokens at once (a prompt, a chunk of one, verify
+    windows): q_proj [tokens, 32, 128], k_proj and v_proj [tokens, 8, 128]
+    (tokens may lie apart: parts of a fused projection); token n goes to slot
+    slots[n] of cache row rows[n], each (row, slot) at most once; a slot outside
+    the cache (a padding token's -1) is not written.  positions int32 [tokens],
+    or [3, tokens] (time, height, width) with mrope_section, the three counts of
+    the 64 rotary angles, in blocks or interleaved.  q_norm_w and k_norm_w None:
+    no norm.  kv of any format (e2m1: uint8 [.., 64] with e4m3 kv_scales
+    [.., 8]).  Returns q_out [tokens, 32, 128]."""
+    return _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv, None, False, q_out,
+                  mrope_section, mrope_interleaved, eps, rope_theta, k_scale, v_scale, kv_scales, workspace)
+
+
+def write_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv_pages, block_table,
+                   q_out=None, mrope_section=None, mrope_interleaved: bool = False, eps: float = 1e-6,
+                   rope_theta: float = 1e6, k_scale: float = 1.0, v_scale: float = 1.0, kv_scales=None,
+                   workspace=None):
+    """write_kv on a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
+    its scale pages), block_table int32 [batch, max_pages]; slot s of row b is
+    row s % page_size of page block_table[b, s // page_size]."""
+    return _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv_pages, block_table, True,
+                  q_out, mrope_section, mrope_interleaved, eps, rope_theta, k_scale, v_scale, kv_scales, workspace)
+
+
+def _read(kv, block_table, paged, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales, workspace):
+    name = "kv_pages" if paged else "kv"
+    kvf = _kv_format(kv, name, None)
+    _require(kv, name, None, tuple(_KVF))
+    dev = kv.device
+    _require_scales(kv_scales, "kv_scales", kv, kvf)
+    if paged:
+        _require_table(block_table, None, dev)
+    B = block_table.shape[0] if paged else kv.shape[0]
+    C = block_table.shape[1] * kv.shape[3] if paged else kv.shape[3]
+    _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
+    if starts is not None:
+        _require(starts, "starts", (B,), (torch.int32,), dev)
+    if workspace is not None:
+        _require(workspace, "workspace", None, (torch.uint8,), dev)
+    if dtype is not None and dtype not in _QDT:
+        raise ValueError(f"dtype must be one of {tuple(_QDT)}, got {dtype}")
+    if out is None:
+        if dtype is None:
+            dtype = kv.dtype if kvf in (KV_F16, KV_BF16) else torch.bfloat16
+        out = torch.empty((B, 2, HKV, C, D), dtype=dtype, device=dev)
+    _require(out, "out", None, tuple(_QDT) if dtype is None else (dtype,), dev)
+    if out.dim() != 5 or tuple(out.shape[:3]) != (B, 2, HKV) or out.shape[4] != D:
+        raise ValueError(f"out must be [{B}, 2, {HKV}, out_capacity, {D}], got {tuple(out.shape)}")
+    lib = _lib.load()
+    sc = _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None
+    ws = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
+    st = None if starts is None else _ptr(starts)
+    with torch.cuda.device(dev):
+        if paged:
+            _lib.check(lib.gqa_read_kv_paged(_ptr(kv), kvf, sc, _ptr(block_table), block_table.shape[1], kv.shape[0],
+                                             kv.shape[3], _ptr(sequence_lengths), st, _ptr(out), _QDT[out.dtype], B,
+                                             out.shape[3], float(k_scale), float(v_scale), *ws, _stream(dev)))
+        else:
+            _lib.check(lib.gqa_read_kv(_ptr(kv), kvf, sc, _ptr(sequence_lengths), st, _ptr(out), _QDT[out.dtype], B, C,
+                                       out.shape[3], float(k_scale), float(v_scale), *ws, _stream(dev)))
+    return out
+
+
+def read_kv(kv, sequence_lengths, starts=None, out=None, dtype=None, k_scale: float = 1.0, v_scale: float = 1.0,
+            kv_scales=None, workspace=None):
+    """Slots [starts, sequence_lengths) of every row of a cache of any format, as
+    fp16 or bf16, into out [batch, 2, 8, out_capacity, 128] from slot 0 on; the
+    rest of out keeps what it holds (a new one, of the cache's capacity and of
+    ``dtype``, is not initialised).  starts None: 0."""
+    return _read(kv, None, False, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales, workspace)
+
+
+def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None, dtype=None, k_scale: float = 1.0,
+                  v_scale: float = 1.0, kv_scales=None, workspace=None):
+    """read_kv from a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
+    its scale pages), block_table int32 [batch, max_pages]."""
+    return _read(kv_pages, block_table, True, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales,
+                 workspace)
 
 
 def workspace_init(workspace: torch.Tensor) -> None:

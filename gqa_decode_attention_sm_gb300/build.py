@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libgqa_decode.so")
 INCLUDE = os.path.join(ROOT, "include")
 # translation units, compiled side by side
-SRCS = [os.path.join(PKG, "csrc", name) for name in ("gqa_decode.cu", "fp4_decode.cu")]
+SRCS = [os.path.join(PKG, "csrc", name) for name in ("gqa_decode.cu", "fp4_decode.cu", "cache_io.cu")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-t", "0"]
@@ -19,6 +19,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 def _sources():
     return (glob.glob(os.path.join(PKG, "csrc", "**", "*.cuh"), recursive=True)
             + glob.glob(os.path.join(PKG, "csrc", "**", "*.cu"), recursive=True)
+            + glob.glob(os.path.join(PKG, "csrc", "**", "*.h"), recursive=True)
             + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 

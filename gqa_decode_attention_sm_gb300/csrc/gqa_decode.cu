@@ -19,6 +19,7 @@
 
 #include "gqa_decode.h"
 #include "kernels/append_kv.cuh"
+#include "kernels/cache_io.h"
 #include "kernels/combine.cuh"
 #include "kernels/common.cuh"
 #include "kernels/split_launch.cuh"
@@ -586,12 +587,234 @@ gqa_status_t prepare_call(Call& c, bool q_scale_positive, bool need_q) {
   return st;
 }
 
+// A cache as the write and read-back calls take it: contiguous (block_table =
+// nullptr; units = batch rows) or paged (units = num_pages).
+struct CacheArgs {
+  void* kv;
+  int format;
+  void* scales;
+  int batch, capacity;  // capacity: slots a row holds (paged: max_pages * page size)
+  const int32_t* block_table;
+  int max_pages, num_pages, page_log2;
+  float k_scale, v_scale;
+  size_t rows() const {
+    return (block_table ? (size_t)num_pages << page_log2 : (size_t)batch * capacity) * 2 * kHkv;
+  }
+  size_t kv_bytes() const { return rows() * kv_row_bytes(format); }
+  size_t scale_bytes() const { return rows() * scale_row_bytes(format); }
+  size_t table_bytes() const { return block_table ? (size_t)batch * max_pages * 4 : 0; }
+};
+
+gqa_status_t paged_args(CacheArgs& c, const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                        int page_size) {
+  if (!block_table) return fail(GQA_ERR_INVALID_ARGUMENT, "block_table is null");
+  if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1)) != 0)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "page_size %d is not a power of two in [16, 65536]", page_size);
+  if (num_pages < 1 || max_pages_per_seq < 1)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "num_pages and max_pages_per_seq must be >= 1");
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap > (1LL << 30)) return fail(GQA_ERR_INVALID_ARGUMENT, "max_pages_per_seq * page_size exceeds 2^30");
+  if (!aligned(block_table, 4)) return fail(GQA_ERR_INVALID_ARGUMENT, "block_table must be 4-byte aligned");
+  c.block_table = block_table;
+  c.max_pages = max_pages_per_seq;
+  c.num_pages = num_pages;
+  c.capacity = (int)cap;
+  c.page_log2 = 0;
+  while ((1 << c.page_log2) < page_size) ++c.page_log2;
+  return GQA_OK;
+}
+
+gqa_status_t validate_cache(const CacheArgs& c, const void* workspace, size_t workspace_bytes) {
+  gqa_status_t st = validate_shape(c.batch, c.capacity);
+  if (st != GQA_OK) return st;
+  if (!known_format(c.format)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", c.format);
+  if (!c.kv || !aligned(c.kv, 16)) return fail(GQA_ERR_INVALID_ARGUMENT, "kv must be non-null and 16-byte aligned");
+  if (scale_row_bytes(c.format) > 0 && (!c.scales || !aligned(c.scales, 2)))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "an int8 or e2m1 cache needs its 2-byte aligned row scales");
+  if (!std::isfinite(c.k_scale) || c.k_scale <= 0.f || !std::isfinite(c.v_scale) || c.v_scale <= 0.f)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "k_scale and v_scale must be finite and > 0");
+  if (workspace && workspace_bytes < GQA_WORKSPACE_HEADER_BYTES)
+    return fail(GQA_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than its %d-byte header", GQA_WORKSPACE_HEADER_BYTES);
+  if (workspace && !aligned(workspace, 4)) return fail(GQA_ERR_INVALID_ARGUMENT, "workspace must be 4-byte aligned");
+  return GQA_OK;
+}
+
+// What a write call takes besides the cache.
+struct WriteArgs {
+  const void *q_proj, *k_proj, *v_proj;
+  long long q_stride, k_stride, v_stride;  // elements from one token to the next
+  const void *q_norm_w, *k_norm_w;
+  int dtype;
+  const int32_t* positions;
+  const int* section;  // host: three counts, or null
+  int interleaved;
+  const int32_t *rows, *slots;
+  int tokens;
+  void* q_out;
+  float eps, rope_theta;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+
+// theta^(-i/64) / (2 pi) modulo 1 as a 64-bit fraction: the FP64 frequency's
+// product with 1 / (2 pi), itself held as two doubles, to about 2^-64.
+uint64_t turn_fraction(double inv_freq) {
+  constexpr double kInvHi = 0x1.45f306dc9c883p-3;    // the double nearest to 1 / (2 pi)
+  constexpr double kInvLo = -0x1.6b01ec5417056p-57;  // the rest
+  const double hi = inv_freq * kInvHi;
+  const double lo = std::fma(inv_freq, kInvHi, -hi) + inv_freq * kInvLo;
+  const double whole = std::floor(hi);
+  return (uint64_t)std::ldexp(hi - whole, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
+}
+
+gqa_status_t write_kv(const CacheArgs& c, const WriteArgs& a) {
+  if (a.tokens == 0) return GQA_OK;
+  if (a.tokens < 0 || a.tokens > (1 << 27)) return fail(GQA_ERR_INVALID_ARGUMENT, "tokens %d outside [0, 2^27]", a.tokens);
+  if (!a.q_proj || !a.k_proj || !a.v_proj || !a.positions || !a.slots || !a.q_out)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if ((a.q_norm_w == nullptr) != (a.k_norm_w == nullptr))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "q_norm_w and k_norm_w are given together or not at all");
+  if (a.dtype != GQA_F16 && a.dtype != GQA_BF16) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown dtype %d", a.dtype);
+  gqa_status_t st = validate_cache(c, a.workspace, a.workspace_bytes);
+  if (st != GQA_OK) return st;
+  if (!is_narrow(c.format) && c.format != a.dtype)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "fp16/bf16 KV must have the dtype of the projections");
+  // (the e2m1 scales' products and reciprocals stay normal FP32 numbers)
+  if (c.format == kKvE2M1 && (c.k_scale < 0x1p-100f || c.k_scale > 0x1p100f || c.v_scale < 0x1p-100f || c.v_scale > 0x1p100f))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "the tensor scales of an e2m1 cache must lie in [2^-100, 2^100]");
+  if (!std::isfinite(a.eps) || a.eps < 0.f) return fail(GQA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  if (!std::isfinite(a.rope_theta) || a.rope_theta < 1.f)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "rope_theta must be finite and >= 1");
+  if (a.section) {
+    const int* s = a.section;
+    if (s[0] < 0 || s[1] < 0 || s[2] < 0 || s[0] > 64 || s[1] > 64 || s[2] > 64 || s[0] + s[1] + s[2] != kD / 2)
+      return fail(GQA_ERR_INVALID_ARGUMENT, "the three rotary sections must be >= 0 and sum to 64");
+    if (a.interleaved && (s[1] > 21 || s[2] > 21))
+      return fail(GQA_ERR_INVALID_ARGUMENT, "interleaved sections hold at most 21 of height and of width");
+  }
+  const void* vec[] = {a.q_proj, a.k_proj, a.v_proj, a.q_out, a.q_norm_w, a.k_norm_w};
+  for (const void* ptr : vec)
+    if (!aligned(ptr, 16)) return fail(GQA_ERR_INVALID_ARGUMENT, "projections, weights and q_out must be 16-byte aligned");
+  const long long stride[] = {a.q_stride, a.k_stride, a.v_stride};
+  const long long width[] = {kHq * kD, kHkv * kD, kHkv * kD};
+  for (int i = 0; i < 3; ++i)
+    if (stride[i] < width[i] || stride[i] % 8 != 0 || stride[i] > (1LL << 32))
+      return fail(GQA_ERR_INVALID_ARGUMENT, "a token stride must be a multiple of 8 elements and hold the token's heads");
+  if (!aligned(a.positions, 4) || !aligned(a.slots, 4) || !aligned(a.rows, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "positions, rows and slots must be 4-byte aligned");
+  // nothing that is written overlaps anything else
+  const size_t n = (size_t)a.tokens;
+  const struct { const void* p; size_t bytes; } ins[] = {
+      {a.q_proj, ((n - 1) * a.q_stride + width[0]) * 2}, {a.k_proj, ((n - 1) * a.k_stride + width[1]) * 2},
+      {a.v_proj, ((n - 1) * a.v_stride + width[2]) * 2}, {a.q_norm_w, a.q_norm_w ? (size_t)kD * 2 : 0},
+      {a.k_norm_w, a.k_norm_w ? (size_t)kD * 2 : 0},     {a.positions, n * 4 * (a.section ? 3 : 1)},
+      {a.rows, a.rows ? n * 4 : 0},                      {a.slots, n * 4},
+      {c.block_table, c.table_bytes()}};
+  const struct { const void* p; size_t bytes; } outs[] = {
+      {a.q_out, n * kHq * kD * 2}, {c.kv, c.kv_bytes()}, {c.scales, c.scale_bytes()},
+      {a.workspace, a.workspace ? (size_t)GQA_WORKSPACE_HEADER_BYTES : 0}};
+  for (size_t i = 0; i < sizeof outs / sizeof outs[0]; ++i) {
+    if (!outs[i].bytes) continue;
+    for (const auto& in : ins)
+      if (in.bytes && overlap(outs[i].p, outs[i].bytes, in.p, in.bytes))
+        return fail(GQA_ERR_ALIASING, "q_out, the cache, its scales or the workspace overlaps an input");
+    for (size_t k = i + 1; k < sizeof outs / sizeof outs[0]; ++k)
+      if (outs[k].bytes && overlap(outs[i].p, outs[i].bytes, outs[k].p, outs[k].bytes))
+        return fail(GQA_ERR_ALIASING, "q_out, the cache, its scales and the workspace overlap one another");
+  }
+  int sms = 0;
+  st = current_device_ready(&sms);
+  if (st != GQA_OK) return st;
+  WriteParams w = {};
+  w.q_proj = static_cast<const uint16_t*>(a.q_proj);
+  w.k_proj = static_cast<const uint16_t*>(a.k_proj);
+  w.v_proj = static_cast<const uint16_t*>(a.v_proj);
+  w.q_stride = a.q_stride;
+  w.k_stride = a.k_stride;
+  w.v_stride = a.v_stride;
+  w.q_norm_w = static_cast<const uint16_t*>(a.q_norm_w);
+  w.k_norm_w = static_cast<const uint16_t*>(a.k_norm_w);
+  w.positions = a.positions;
+  w.rows = a.rows;
+  w.slots = a.slots;
+  w.q_out = static_cast<uint16_t*>(a.q_out);
+  w.kv = c.kv;
+  w.kv_scales = c.scales;
+  w.flags = static_cast<uint32_t*>(a.workspace);
+  w.tokens = a.tokens;
+  w.batch = c.batch;
+  w.capacity = c.capacity;
+  w.block_table = c.block_table;
+  w.max_pages = c.max_pages;
+  w.num_pages = c.num_pages;
+  w.page_log2 = c.page_log2;
+  w.eps = a.eps;
+  w.k_scale = c.k_scale;
+  w.v_scale = c.v_scale;
+  w.k_inv_scale = 1.f / c.k_scale;
+  w.v_inv_scale = 1.f / c.v_scale;
+  for (int i = 0; i < kD / 2; ++i) {
+    w.inv_freq[i] = std::pow((double)a.rope_theta, -(double)i / (kD / 2));
+    w.turns[i] = turn_fraction(w.inv_freq[i]);
+    int axis = 0;
+    if (a.section && a.interleaved) axis = i % 3 == 1 && i < 3 * a.section[1] ? 1 : (i % 3 == 2 && i < 3 * a.section[2] ? 2 : 0);
+    else if (a.section) axis = (i >= a.section[0]) + (i >= a.section[0] + a.section[1]);
+    w.axis[i] = (uint8_t)axis;
+  }
+  w.kv_rows = c.rows();
+  const cudaError_t e = launch_write_kv(w, c.format, a.dtype == GQA_BF16 ? kQBF16 : kQF16, sms, a.stream);
+  if (e != cudaSuccess) return cuda_fail(e, "write kernel launch");
+  return GQA_OK;
+}
+
+gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* starts, void* out, int out_dtype,
+                     int out_capacity, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!lens || !out) return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (out_dtype != GQA_F16 && out_dtype != GQA_BF16) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown out dtype %d", out_dtype);
+  if (out_capacity < 1 || out_capacity > (1 << 30))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "out_capacity %d outside [1, 2^30]", out_capacity);
+  gqa_status_t st = validate_cache(c, workspace, workspace_bytes);
+  if (st != GQA_OK) return st;
+  if (!aligned(out, 16) || !aligned(lens, 4) || !aligned(starts, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned, lens and starts 4-byte");
+  const size_t out_bytes = (size_t)c.batch * 2 * kHkv * out_capacity * kD * 2, b4 = (size_t)c.batch * 4;
+  if (overlap(out, out_bytes, c.kv, c.kv_bytes()) || overlap(out, out_bytes, lens, b4) ||
+      (starts && overlap(out, out_bytes, starts, b4)) ||
+      (c.scale_bytes() && overlap(out, out_bytes, c.scales, c.scale_bytes())) ||
+      (c.block_table && overlap(out, out_bytes, c.block_table, c.table_bytes())) ||
+      (workspace && overlap(out, out_bytes, workspace, GQA_WORKSPACE_HEADER_BYTES)))
+    return fail(GQA_ERR_ALIASING, "out overlaps the cache, its scales, the lengths, the block table or the workspace");
+  st = current_device_ready(nullptr);
+  if (st != GQA_OK) return st;
+  ReadParams r = {};
+  r.kv = c.kv;
+  r.kv_scales = c.scales;
+  r.lens = lens;
+  r.starts = starts;
+  r.out = out;
+  r.flags = static_cast<uint32_t*>(workspace);
+  r.batch = c.batch;
+  r.capacity = c.capacity;
+  r.out_capacity = out_capacity;
+  r.block_table = c.block_table;
+  r.max_pages = c.max_pages;
+  r.num_pages = c.num_pages;
+  r.page_log2 = c.page_log2;
+  r.k_scale = c.k_scale;
+  r.v_scale = c.v_scale;
+  r.kv_rows = c.rows();
+  const cudaError_t e = launch_read_kv(r, c.format, out_dtype == GQA_BF16 ? kQBF16 : kQF16, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "read kernel launch");
+  return GQA_OK;
+}
+
 // The append step on a contiguous cache (block_table = nullptr; `units` =
 // batch, `unit_rows` = capacity) or a paged one (units = num_pages, unit_rows
 // = page size, capacity = max_pages * page size).
 gqa_status_t append_kv(const void* q_proj, const void* k_proj, const void* v_proj, const void* q_norm_w,
                        const void* k_norm_w, gqa_dtype_t dtype, const int32_t* positions, const int32_t* slots,
-                       int batch, void* q_out, void* kv, gqa_kv_format_t kv_format, uint16_t* kv_scales_bf16,
+                       int batch, void* q_out, void* kv, gqa_kv_format_t kv_format, void* kv_scales,
                        int capacity, const int32_t* block_table, int max_pages, int num_pages, int page_log2,
                        size_t units, size_t unit_rows, float eps, float rope_theta, float k_scale, float v_scale,
                        void* workspace, size_t workspace_bytes, void* stream) {
@@ -601,11 +824,17 @@ gqa_status_t append_kv(const void* q_proj, const void* k_proj, const void* v_pro
   if (st != GQA_OK) return st;
   if (dtype != GQA_F16 && dtype != GQA_BF16) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown dtype %d", (int)dtype);
   const int fmt = (int)kv_format;
-  if (fmt != kKvF16 && fmt != kKvBF16 && fmt != kKvE4M3 && fmt != kKvI8)
-    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", fmt);
+  if (!known_format(fmt)) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown KV format %d", fmt);
+  if (fmt == kKvE2M1) {  // one token a row of the many-token write
+    const CacheArgs c{kv, fmt, kv_scales, batch, capacity, block_table, max_pages, num_pages, page_log2, k_scale, v_scale};
+    const WriteArgs a{q_proj, k_proj, v_proj, kHq * kD, kHkv * kD, kHkv * kD, q_norm_w, k_norm_w, (int)dtype, positions,
+                      nullptr, 0, nullptr, slots, batch, q_out, eps, rope_theta, workspace, workspace_bytes,
+                      static_cast<cudaStream_t>(stream)};
+    return write_kv(c, a);
+  }
   if (!is_8bit(fmt) && fmt != (int)dtype)
     return fail(GQA_ERR_INVALID_ARGUMENT, "fp16/bf16 KV must have the dtype of the projections");
-  if (fmt == kKvI8 && !kv_scales_bf16) return fail(GQA_ERR_INVALID_ARGUMENT, "an int8 cache needs kv_scales_bf16");
+  if (fmt == kKvI8 && !kv_scales) return fail(GQA_ERR_INVALID_ARGUMENT, "an int8 cache needs its bf16 row scales");
   if (!std::isfinite(eps) || eps < 0.f) return fail(GQA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
   if (!std::isfinite(rope_theta) || rope_theta <= 0.f)
     return fail(GQA_ERR_INVALID_ARGUMENT, "rope_theta must be finite and > 0");
@@ -617,7 +846,7 @@ gqa_status_t append_kv(const void* q_proj, const void* k_proj, const void* v_pro
   for (const void* ptr : h16)
     if (!aligned(ptr, 2)) return fail(GQA_ERR_INVALID_ARGUMENT, "16-bit arrays must be 2-byte aligned");
   if (!aligned(positions, 4) || !aligned(slots, 4) || (workspace && !aligned(workspace, 4)) ||
-      (!is_8bit(fmt) && !aligned(kv, 2)) || (kv_scales_bf16 && !aligned(kv_scales_bf16, 2)))
+      (!is_8bit(fmt) && !aligned(kv, 2)) || (kv_scales && !aligned(kv_scales, 2)))
     return fail(GQA_ERR_INVALID_ARGUMENT, "misaligned argument");
   const size_t qb = (size_t)batch * kHq * kD * 2, kvb_in = (size_t)batch * kHkv * kD * 2;
   const size_t cache = units * 2 * kHkv * unit_rows * kv_row_bytes(fmt);
@@ -640,7 +869,7 @@ gqa_status_t append_kv(const void* q_proj, const void* k_proj, const void* v_pro
   ap.slots = slots;
   ap.q_out = q_out;
   ap.kv = kv;
-  ap.kv_scales = kv_scales_bf16;
+  ap.kv_scales = static_cast<uint16_t*>(kv_scales);
   ap.flags = static_cast<uint32_t*>(workspace);
   ap.batch = batch;
   ap.capacity = capacity;
@@ -872,19 +1101,19 @@ gqa_status_t gqa_decode_verify(const void* q, gqa_dtype_t q_dtype, const void* k
 
 gqa_status_t gqa_append_kv(const void* q_proj, const void* k_proj, const void* v_proj, const void* q_norm_w,
                            const void* k_norm_w, gqa_dtype_t dtype, const int32_t* positions, const int32_t* slots,
-                           int batch, void* q_out, void* kv, gqa_kv_format_t kv_format, uint16_t* kv_scales_bf16,
+                           int batch, void* q_out, void* kv, gqa_kv_format_t kv_format, void* kv_scales,
                            int capacity, float eps, float rope_theta, float k_scale, float v_scale, void* workspace,
                            size_t workspace_bytes, void* stream) {
   if (capacity < 1) return fail(GQA_ERR_INVALID_ARGUMENT, "capacity %d < 1", capacity);
   return append_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, dtype, positions, slots, batch, q_out, kv, kv_format,
-                   kv_scales_bf16, capacity, nullptr, 0, 0, 0, batch > 0 ? (size_t)batch : 0, (size_t)capacity,
+                   kv_scales, capacity, nullptr, 0, 0, 0, batch > 0 ? (size_t)batch : 0, (size_t)capacity,
                    eps, rope_theta, k_scale, v_scale, workspace, workspace_bytes, stream);
 }
 
 gqa_status_t gqa_append_kv_paged(const void* q_proj, const void* k_proj, const void* v_proj,
                                  const void* q_norm_w, const void* k_norm_w, gqa_dtype_t dtype,
                                  const int32_t* positions, const int32_t* slots, int batch, void* q_out,
-                                 void* kv_pages, gqa_kv_format_t kv_format, uint16_t* kv_scales_pages,
+                                 void* kv_pages, gqa_kv_format_t kv_format, void* kv_scales_pages,
                                  const int32_t* block_table, int max_pages_per_seq, int num_pages, int page_size,
                                  float eps, float rope_theta, float k_scale, float v_scale, void* workspace,
                                  size_t workspace_bytes, void* stream) {
@@ -902,6 +1131,60 @@ gqa_status_t gqa_append_kv_paged(const void* q_proj, const void* k_proj, const v
                    kv_format, kv_scales_pages, (int)cap, block_table, max_pages_per_seq, num_pages, lg,
                    (size_t)num_pages, (size_t)page_size, eps, rope_theta, k_scale, v_scale, workspace,
                    workspace_bytes, stream);
+}
+
+gqa_status_t gqa_write_kv(const void* q_proj, const void* k_proj, const void* v_proj, long long q_stride,
+                          long long k_stride, long long v_stride, const void* q_norm_w, const void* k_norm_w,
+                          gqa_dtype_t dtype, const int32_t* positions, const int* mrope_section,
+                          int mrope_interleaved, const int32_t* rows, const int32_t* slots, int tokens, void* q_out,
+                          void* kv, gqa_kv_format_t kv_format, void* kv_scales, int batch, int capacity, float eps,
+                          float rope_theta, float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  const CacheArgs c{kv, (int)kv_format, kv_scales, batch, capacity, nullptr, 0, 0, 0, k_scale, v_scale};
+  if (!rows) return fail(GQA_ERR_INVALID_ARGUMENT, "rows is null");
+  return write_kv(c, {q_proj, k_proj, v_proj, q_stride, k_stride, v_stride, q_norm_w, k_norm_w, (int)dtype, positions,
+                      mrope_section, mrope_interleaved, rows, slots, tokens, q_out, eps, rope_theta, workspace,
+                      workspace_bytes, static_cast<cudaStream_t>(stream)});
+}
+
+gqa_status_t gqa_write_kv_paged(const void* q_proj, const void* k_proj, const void* v_proj, long long q_stride,
+                                long long k_stride, long long v_stride, const void* q_norm_w, const void* k_norm_w,
+                                gqa_dtype_t dtype, const int32_t* positions, const int* mrope_section,
+                                int mrope_interleaved, const int32_t* rows, const int32_t* slots, int tokens,
+                                void* q_out, void* kv_pages, gqa_kv_format_t kv_format, void* kv_scales_pages,
+                                const int32_t* block_table, int batch, int max_pages_per_seq, int num_pages,
+                                int page_size, float eps, float rope_theta, float k_scale, float v_scale,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  CacheArgs c{kv_pages, (int)kv_format, kv_scales_pages, batch, 0, nullptr, 0, 0, 0, k_scale, v_scale};
+  gqa_status_t st = paged_args(c, block_table, max_pages_per_seq, num_pages, page_size);
+  if (st != GQA_OK) return st;
+  if (!rows) return fail(GQA_ERR_INVALID_ARGUMENT, "rows is null");
+  return write_kv(c, {q_proj, k_proj, v_proj, q_stride, k_stride, v_stride, q_norm_w, k_norm_w, (int)dtype, positions,
+                      mrope_section, mrope_interleaved, rows, slots, tokens, q_out, eps, rope_theta, workspace,
+                      workspace_bytes, static_cast<cudaStream_t>(stream)});
+}
+
+gqa_status_t gqa_read_kv(const void* kv, gqa_kv_format_t kv_format, const void* kv_scales, const int32_t* lens,
+                         const int32_t* starts, void* out, gqa_dtype_t out_dtype, int batch, int capacity,
+                         int out_capacity, float k_scale, float v_scale, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  const CacheArgs c{const_cast<void*>(kv), (int)kv_format, const_cast<void*>(kv_scales), batch, capacity, nullptr,
+                    0, 0, 0, k_scale, v_scale};
+  return read_kv(c, lens, starts, out, (int)out_dtype, out_capacity, workspace, workspace_bytes,
+                 static_cast<cudaStream_t>(stream));
+}
+
+gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, const void* kv_scales_pages,
+                               const int32_t* block_table, int max_pages_per_seq, int num_pages, int page_size,
+                               const int32_t* lens, const int32_t* starts, void* out, gqa_dtype_t out_dtype,
+                               int batch, int out_capacity, float k_scale, float v_scale, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  CacheArgs c{const_cast<void*>(kv_pages), (int)kv_format, const_cast<void*>(kv_scales_pages), batch, 0, nullptr,
+              0, 0, 0, k_scale, v_scale};
+  gqa_status_t st = paged_args(c, block_table, max_pages_per_seq, num_pages, page_size);
+  if (st != GQA_OK) return st;
+  return read_kv(c, lens, starts, out, (int)out_dtype, out_capacity, workspace, workspace_bytes,
+                 static_cast<cudaStream_t>(stream));
 }
 
 gqa_status_t gqa_decode_split_stage(const void* q, gqa_dtype_t q_dtype, const void* kv,

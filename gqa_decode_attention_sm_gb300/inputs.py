@@ -103,11 +103,22 @@ def _kv_row_fp32(w: Workload, b: int, device, seed: int) -> torch.Tensor:
     return x
 
 
+def _to_e4m3(t: torch.Tensor) -> torch.Tensor:
+    """fp64 or fp32 t >= 0 to the nearest e4m3: by way of an fp32 that is rounded
+    to odd, so that no fp64 just off a tie is rounded twice."""
+    f = t.to(torch.float32)
+    if t.dtype == torch.float64:
+        b = f.view(torch.int32)
+        b = torch.where(f.double() > t, b - 1, b)  # towards zero
+        f = torch.where(f.double() != t, b | 1, b).view(torch.float32)
+    return f.clamp(max=E4M3_MAX).to(torch.float8_e4m3fn)
+
+
 def quantise_e2m1(x: torch.Tensor, scale: float):
     """Rows x [..., 128] (fp32 or fp64) as e2m1 bytes [..., 64] and e4m3 group
     scales (as bytes) [..., 8]; to the nearest level, ties to the even code."""
     g = (x / scale).unflatten(-1, (8, 16))
-    s = (g.abs().amax(-1) / 6).clamp(max=E4M3_MAX).to(torch.float32).to(torch.float8_e4m3fn)
+    s = _to_e4m3(g.abs().amax(-1) / 6)
     wide = s.to(x.dtype).unsqueeze(-1)
     t = torch.where(wide > 0, g / wide, torch.zeros_like(g))
     m = t.abs().clamp(max=6)

@@ -384,7 +384,8 @@ gqa_status_t gqa_decode_debug_cut_extents(uint64_t kv_cut_bytes, uint64_t scales
  * weights are `dtype`.  The cache format decides the write: fp16/bf16 (must
  * equal dtype; RNE), e4m3 (value / k_scale or / v_scale, RNE, saturating) or
  * int8 (codes round-to-nearest-even of value / scale with a fresh bf16 row
- * scale amax/127 written to kv_scales_bf16, clipped to +-127).  positions and
+ * scale amax/127 written to kv_scales, clipped to +-127) or e2m1 (as
+ * gqa_write_kv, whose rules for alignment and rope_theta then hold too).  positions and
  * slots are int32 [batch] in device memory, read only by the kernel; a slot
  * outside [0, capacity) is not written and, when a workspace is given, sets
  * GQA_FLAG_SLOT_CLAMPED in its header (workspace may be NULL).  eps finite >= 0,
@@ -393,7 +394,7 @@ gqa_status_t gqa_decode_debug_cut_extents(uint64_t kv_cut_bytes, uint64_t scales
 gqa_status_t gqa_append_kv(const void* q_proj, const void* k_proj, const void* v_proj,
                            const void* q_norm_w, const void* k_norm_w, gqa_dtype_t dtype,
                            const int32_t* positions, const int32_t* slots, int batch, void* q_out,
-                           void* kv, gqa_kv_format_t kv_format, uint16_t* kv_scales_bf16, int capacity,
+                           void* kv, gqa_kv_format_t kv_format, void* kv_scales, int capacity,
                            float eps, float rope_theta, float k_scale, float v_scale, void* workspace,
                            size_t workspace_bytes, void* stream);
 
@@ -409,10 +410,96 @@ gqa_status_t gqa_append_kv_paged(const void* q_proj, const void* k_proj, const v
                                  const void* q_norm_w, const void* k_norm_w, gqa_dtype_t dtype,
                                  const int32_t* positions, const int32_t* slots, int batch,
                                  void* q_out, void* kv_pages, gqa_kv_format_t kv_format,
-                                 uint16_t* kv_scales_pages, const int32_t* block_table,
+                                 void* kv_scales_pages, const int32_t* block_table,
                                  int max_pages_per_seq, int num_pages, int page_size, float eps,
                                  float rope_theta, float k_scale, float v_scale, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/* Many tokens at once: the append step for the tokens of prompts, of chunks of
+ * them or of verify windows (the "Qwen3-VL official BF16 on Jetson Thor
+ * (SM110)" docs, "Runtime architecture": a batched norm + RoPE + cache write
+ * for prefill), with rotary positions of one axis, or of the three axes of
+ * image and video tokens.  Token n belongs to batch row rows[n] and goes to
+ * its slot slots[n]; the tokens of a call come in any order, each (row, slot)
+ * at most once.
+ *   q_proj [tokens, 32, 128], k_proj and v_proj [tokens, 8, 128] of `dtype`:
+ *     token n starts q_stride (k_stride, v_stride) elements after token n - 1
+ *     (parts of a fused projection); strides are multiples of 8 and hold at
+ *     least the token's heads
+ *   q_norm_w, k_norm_w [128], or both NULL: no norm (y = x, eps unused)
+ *   positions int32 [tokens], or [3, tokens] (time, height, width) with
+ *     mrope_section, three counts in HOST memory that sum to 64: angle i turns
+ *     with axis 0, 1 or 2.  In blocks (mrope_interleaved 0): the first
+ *     section[0] angles are time, then section[1] height, then width.
+ *     Interleaved: i is height if i % 3 == 1 and i < 3 section[1], width if
+ *     i % 3 == 2 and i < 3 section[2], else time (at most 21 of each).
+ *     mrope_section NULL: one axis.
+ *   rows, slots int32 [tokens]
+ *   q_out [tokens, 32, 128], dense
+ * The arithmetic of y and z is gqa_append_kv's, in FP32 with angles exact to
+ * 2^-33 of a turn: q_out and a 16-bit cache hold z within half a step plus
+ * 2^-19 of the head's largest |z|.  Cache formats as gqa_append_kv, and e2m1
+ * (kv_scales: e4m3 bytes, 8 a row): each 16 dims x of a row get the scale
+ * s = e4m3(amax(|x|) / (6 k_scale)) (v_scale for values; to the nearest,
+ * saturating at 448) and the codes nearest to x / (s k_scale), ties to the
+ * even code, saturating at 6; s = 0 gives codes 0.  Scales and codes are those
+ * of the exact z and v.  kv as gqa_decode's, [batch, 2, 8, capacity, 128]
+ * (e2m1: 64 bytes a row).  A row outside [0, batch) or a slot outside
+ * [0, capacity) writes nothing to the cache (q_out is still written) and sets
+ * GQA_FLAG_SLOT_CLAMPED in the workspace's header, if there is one: a padded
+ * batch gives its padding slot -1.  tokens = 0 does nothing.  Pointers are
+ * 16-byte aligned (int32 arrays and the workspace 4, scales 2).  eps finite
+ * >= 0, rope_theta finite >= 1, k_scale and v_scale finite > 0 (e2m1: within
+ * [2^-100, 2^100]).  Nothing written may overlap anything else
+ * (GQA_ERR_ALIASING).  One launch, no allocation, no host sync. */
+gqa_status_t gqa_write_kv(const void* q_proj, const void* k_proj, const void* v_proj,
+                          long long q_stride, long long k_stride, long long v_stride,
+                          const void* q_norm_w, const void* k_norm_w, gqa_dtype_t dtype,
+                          const int32_t* positions, const int* mrope_section, int mrope_interleaved,
+                          const int32_t* rows, const int32_t* slots, int tokens, void* q_out, void* kv,
+                          gqa_kv_format_t kv_format, void* kv_scales, int batch, int capacity, float eps,
+                          float rope_theta, float k_scale, float v_scale, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The same on a paged cache (the layout of gqa_decode_paged; block_table
+ * [batch, max_pages_per_seq]): slot s of row b is row s % page_size of page
+ * block_table[b][s / page_size].  A block-table entry outside [0, num_pages)
+ * sets GQA_FLAG_PAGE_CLAMPED and nothing of that token is written to the
+ * cache. */
+gqa_status_t gqa_write_kv_paged(const void* q_proj, const void* k_proj, const void* v_proj,
+                                long long q_stride, long long k_stride, long long v_stride,
+                                const void* q_norm_w, const void* k_norm_w, gqa_dtype_t dtype,
+                                const int32_t* positions, const int* mrope_section, int mrope_interleaved,
+                                const int32_t* rows, const int32_t* slots, int tokens, void* q_out,
+                                void* kv_pages, gqa_kv_format_t kv_format, void* kv_scales_pages,
+                                const int32_t* block_table, int batch, int max_pages_per_seq, int num_pages,
+                                int page_size, float eps, float rope_theta, float k_scale, float v_scale,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Reading a cache back (the "FreeToken-Kai: Running on Turing (sm_75)" docs,
+ * change 7: a paged prefix gathered into a contiguous matrix, quantised rows
+ * decoded once): slots [starts[b], lens[b]) of every batch row, of a cache of
+ * any format, into out [batch, 2, 8, out_capacity, 128] (`out_dtype`) from slot
+ * 0 on, out_capacity slots at most; the rest of out keeps what it holds.  Each
+ * element is code * scale * k_scale (v_scale for values) in FP32, rounded once;
+ * a 16-bit cache's is the value itself (the scales are not used).  lens and starts int32 [batch], device memory;
+ * starts may be NULL (0).  A length outside [0, capacity] or a start outside
+ * [0, length] is clamped and sets GQA_FLAG_LENGTH_CLAMPED in the header of the
+ * workspace, if one is given.  kv and out 16-byte aligned; out overlaps
+ * nothing else.  One launch, no allocation, no host sync. */
+gqa_status_t gqa_read_kv(const void* kv, gqa_kv_format_t kv_format, const void* kv_scales,
+                         const int32_t* lens, const int32_t* starts, void* out, gqa_dtype_t out_dtype,
+                         int batch, int capacity, int out_capacity, float k_scale, float v_scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same from a paged cache (the layout of gqa_decode_paged).  A block-table
+ * entry in use outside [0, num_pages) is clamped and sets
+ * GQA_FLAG_PAGE_CLAMPED. */
+gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, const void* kv_scales_pages,
+                               const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                               int page_size, const int32_t* lens, const int32_t* starts, void* out,
+                               gqa_dtype_t out_dtype, int batch, int out_capacity, float k_scale,
+                               float v_scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Zero the workspace header (status flags) on `stream`.  Asynchronous. */
 gqa_status_t gqa_decode_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
