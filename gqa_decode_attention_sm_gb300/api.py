@@ -12,6 +12,7 @@ provides device memory and the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -48,11 +49,30 @@ def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
 
+# The current stream's handle without building a Stream object (a few us a call
+# less on the serving path).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _current(device: torch.device):
+    """torch.cuda.device(device), which costs nothing where it is current."""
+    return _SAME_DEVICE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
 def _require(t, name, shape, dtypes, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (t.is_cuda if device is None else t.device == device)
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        return
+    # say what is wrong
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -72,13 +92,15 @@ def _kv_format(kv, name, lead):
     pairs, two to a byte.  ``lead``: its first dimension (None: any)."""
     if not isinstance(kv, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    e2m1 = kv.dtype == torch.uint8 and kv.dim() == 5 and kv.shape[4] == D // 2
-    first = "num_pages" if lead is None else lead
-    if (kv.dim() != 5 or (lead is not None and kv.shape[0] != lead) or kv.shape[1:3] != (2, HKV)
-            or (kv.shape[4] != D and not e2m1)):
-        raise ValueError(f"{name} must be [{first}, 2, {HKV}, {'page_size' if lead is None else 'capacity'}, {D}] "
-                         f"(uint8 [.., {D // 2}] for e2m1), got {tuple(kv.shape)}")
-    return KV_E2M1 if e2m1 else _KVF.get(kv.dtype, -1)
+    shape = kv.shape
+    if len(shape) == 5 and shape[1] == 2 and shape[2] == HKV and (lead is None or shape[0] == lead):
+        if shape[4] == D:
+            return _KVF.get(kv.dtype, -1)
+        if shape[4] == D // 2 and kv.dtype == torch.uint8:
+            return KV_E2M1
+    raise ValueError(f"{name} must be [{'num_pages' if lead is None else lead}, 2, {HKV}, "
+                     f"{'page_size' if lead is None else 'capacity'}, {D}] (uint8 [.., {D // 2}] for e2m1), "
+                     f"got {tuple(shape)}")
 
 
 def _require_scales(scales, name, kv, kvf):
@@ -86,7 +108,7 @@ def _require_scales(scales, name, kv, kvf):
     if kvf == KV_I8:
         _require(scales, name, kv.shape[:4], (torch.bfloat16,), kv.device)
     elif kvf == KV_E2M1:
-        _require(scales, name, (*kv.shape[:4], 8), _FP8, kv.device)
+        _require(scales, name, kv.shape[:4] + (8,), _FP8, kv.device)
 
 
 def _geometry(q, kv, lens):
@@ -141,7 +163,7 @@ def gqa_decode(q, kv, sequence_lengths, q_scale: float = 1.0, out=None):
     if out is None:
         out = torch.empty_like(q)
     _require(out, "out", q.shape, (q.dtype,), q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode(_ptr(q), _ptr(kv), _ptr(sequence_lengths), _ptr(out), B, C,
                                           _QDT[q.dtype], float(q_scale), _stream(q.device)))
     return out
@@ -226,7 +248,7 @@ def prepare(tensors: dict, q_scale: float = 1.0, num_splits=None, k_scale=None, 
 def launch(p: Prepared) -> torch.Tensor:
     """Run both stages on the current stream: no allocation, no host read."""
     lib = _lib.load()
-    with torch.cuda.device(p.q.device):
+    with _current(p.q.device):
         st = _stream(p.q.device)
         if p.kv_format == KV_I8:
             _lib.check(lib.gqa_decode_int8kv(_ptr(p.q), _ptr(p.kv), _ptr(p.kv_scales), _ptr(p.lens),
@@ -253,7 +275,7 @@ def launch(p: Prepared) -> torch.Tensor:
 def split_stage(p: Prepared) -> None:
     """Stage 1 alone (streams K/V, writes partials or, with one split, out).
     Not for an int8 or e2m1 cache (their scales go through launch)."""
-    with torch.cuda.device(p.q.device):
+    with _current(p.q.device):
         _lib.check(_lib.load().gqa_decode_split_stage(
             _ptr(p.q), p.q_dtype, _ptr(p.kv), p.kv_format, _ptr(p.lens), _ptr(p.out), p.batch,
             p.capacity, p.q_scale, p.k_scale, p.v_scale, p.num_splits, _ptr(p.workspace),
@@ -262,7 +284,7 @@ def split_stage(p: Prepared) -> None:
 
 def combine_stage(p: Prepared) -> None:
     """Stage 2 alone (log-sum-exp merge of the partials; nothing with one split)."""
-    with torch.cuda.device(p.q.device):
+    with _current(p.q.device):
         _lib.check(_lib.load().gqa_decode_combine_stage(
             _ptr(p.lens), _ptr(p.out), p.q_dtype, p.kv_format, p.batch, p.capacity, p.v_scale,
             p.num_splits, _ptr(p.workspace), p.workspace_bytes, _stream(p.q.device)))
@@ -281,7 +303,7 @@ def gqa_decode_fp8kv(q, kv, sequence_lengths, k_scale: float, v_scale: float, q_
     nbytes = workspace_size(B, C, S)
     if workspace is None:
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode_fp8kv(
             _ptr(q), _ptr(kv), _ptr(sequence_lengths), _ptr(out), B, C, float(q_scale), float(k_scale),
             float(v_scale), S, _ptr(workspace), workspace.numel(), _stream(q.device)))
@@ -302,7 +324,7 @@ def gqa_decode_int8kv(q, kv, kv_scales, sequence_lengths, q_scale: float = 1.0, 
     nbytes = workspace_size(B, C, S)
     if workspace is None:
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode_int8kv(
             _ptr(q), _ptr(kv), _ptr(kv_scales), _ptr(sequence_lengths), _ptr(out), B, C, _QDT[q.dtype],
             float(q_scale), S, _ptr(workspace), workspace.numel(), _stream(q.device)))
@@ -327,7 +349,7 @@ def gqa_decode_fp4kv(q, kv, kv_scales, sequence_lengths, k_scale: float = 1.0, v
     if workspace is None:
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
     _require(workspace, "workspace", None, (torch.uint8,), q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode_fp4kv(
             _ptr(q), _ptr(kv), _ptr(kv_scales), _ptr(sequence_lengths), _ptr(out), B, C, _QDT[q.dtype],
             float(q_scale), float(k_scale), float(v_scale), S, _ptr(workspace), workspace.numel(),
@@ -367,7 +389,7 @@ def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float 
     nbytes = workspace_size(B * T, C, S)
     if workspace is None:
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode_paged(
             _ptr(q), _QDT[q.dtype], _ptr(kv_pages), kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None,
             _ptr(block_table), max_pages, num_pages, page_size, _ptr(sequence_lengths), _ptr(out), B, T,
@@ -397,7 +419,7 @@ def gqa_decode_verify(q, kv, sequence_lengths, q_scale: float = 1.0, k_scale: fl
     nbytes = workspace_size(B * T, C, S)
     if workspace is None:
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
-    with torch.cuda.device(q.device):
+    with _current(q.device):
         _lib.check(_lib.load().gqa_decode_verify(
             _ptr(q), _QDT[q.dtype], _ptr(kv), kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None,
             _ptr(sequence_lengths), _ptr(out), B, C, T, float(q_scale), float(k_scale), float(v_scale), S,
@@ -427,7 +449,7 @@ def append_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots, kv, 
     if q_out is None:
         q_out = torch.empty_like(q_proj)
     _require(q_out, "q_out", q_proj.shape, (dt,), q_proj.device)
-    with torch.cuda.device(q_proj.device):
+    with _current(q_proj.device):
         _lib.check(_lib.load().gqa_append_kv(
             _ptr(q_proj), _ptr(k_proj), _ptr(v_proj), _ptr(q_norm_w), _ptr(k_norm_w), _QDT[dt],
             _ptr(positions), _ptr(slots), B, _ptr(q_out), _ptr(kv), kvf,
@@ -464,7 +486,7 @@ def append_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, slots
     if q_out is None:
         q_out = torch.empty_like(q_proj)
     _require(q_out, "q_out", q_proj.shape, (dt,), q_proj.device)
-    with torch.cuda.device(q_proj.device):
+    with _current(q_proj.device):
         _lib.check(_lib.load().gqa_append_kv_paged(
             _ptr(q_proj), _ptr(k_proj), _ptr(v_proj), _ptr(q_norm_w), _ptr(k_norm_w), _QDT[dt],
             _ptr(positions), _ptr(slots), B, _ptr(q_out), _ptr(kv_pages), kvf,
@@ -482,11 +504,13 @@ def _tokens(t, name, heads, n, dtype, device):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != (n, heads, D) or t.dtype != dtype:
+    if t.shape != (n, heads, D) or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} [{n}, {heads}, {D}], got {t.dtype} {tuple(t.shape)}")
-    if n and (t.stride(2) != 1 or t.stride(1) != D):
+    if t.is_contiguous():
+        return heads * D
+    if t.stride(2) != 1 or t.stride(1) != D:
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if n > 1 else heads * D
+    return t.stride(0)
 
 
 def _require_table(block_table, batch, device):
@@ -539,7 +563,7 @@ def _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, k
             _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None)
     tail = (float(eps), float(rope_theta), float(k_scale), float(v_scale),
             None if workspace is None else _ptr(workspace), 0 if workspace is None else workspace.numel())
-    with torch.cuda.device(dev):
+    with _current(dev):
         if paged:
             _lib.check(lib.gqa_write_kv_paged(*head, _ptr(block_table), block_table.shape[0], block_table.shape[1],
                                               kv.shape[0], kv.shape[3], *tail, _stream(dev)))
@@ -603,7 +627,7 @@ def _read(kv, block_table, paged, sequence_lengths, starts, out, dtype, k_scale,
     sc = _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None
     ws = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel())
     st = None if starts is None else _ptr(starts)
-    with torch.cuda.device(dev):
+    with _current(dev):
         if paged:
             _lib.check(lib.gqa_read_kv_paged(_ptr(kv), kvf, sc, _ptr(block_table), block_table.shape[1], kv.shape[0],
                                              kv.shape[3], _ptr(sequence_lengths), st, _ptr(out), _QDT[out.dtype], B,
@@ -633,7 +657,7 @@ def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None
 
 def workspace_init(workspace: torch.Tensor) -> None:
     """Zero a workspace's header (status flags) on the current stream."""
-    with torch.cuda.device(workspace.device):
+    with _current(workspace.device):
         _lib.check(_lib.load().gqa_decode_workspace_init(_ptr(workspace), workspace.numel(),
                                                          _stream(workspace.device)))
 
@@ -642,7 +666,7 @@ def get_status(p_or_workspace) -> int:
     """Debug only (synchronises): read and clear the workspace status flags."""
     ws = p_or_workspace.workspace if isinstance(p_or_workspace, Prepared) else p_or_workspace
     flags = ctypes.c_uint32(0)
-    with torch.cuda.device(ws.device):
+    with _current(ws.device):
         _lib.check(_lib.load().gqa_decode_get_status(_ptr(ws), ws.numel(), _stream(ws.device),
                                                      ctypes.byref(flags)))
     return flags.value

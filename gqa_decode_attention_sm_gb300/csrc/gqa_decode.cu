@@ -14,6 +14,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 #include <string>
 
@@ -668,6 +669,18 @@ uint64_t turn_fraction(double inv_freq) {
   return (uint64_t)std::ldexp(hi - whole, 64) + (uint64_t)(int64_t)std::llrint(std::ldexp(lo, 64));
 }
 
+// The fractions of the 64 rotary frequencies of `theta`, kept by the calling
+// thread for its next call with the same theta (64 pow cost a few us).
+const uint64_t* turn_fractions(float theta) {
+  thread_local float known = -1.f;
+  thread_local uint64_t turns[kD / 2];
+  if (known != theta) {
+    for (int i = 0; i < kD / 2; ++i) turns[i] = turn_fraction(std::pow((double)theta, -(double)i / (kD / 2)));
+    known = theta;
+  }
+  return turns;
+}
+
 gqa_status_t write_kv(const CacheArgs& c, const WriteArgs& a) {
   if (a.tokens == 0) return GQA_OK;
   if (a.tokens < 0 || a.tokens > (1 << 27)) return fail(GQA_ERR_INVALID_ARGUMENT, "tokens %d outside [0, 2^27]", a.tokens);
@@ -754,9 +767,8 @@ gqa_status_t write_kv(const CacheArgs& c, const WriteArgs& a) {
   w.v_scale = c.v_scale;
   w.k_inv_scale = 1.f / c.k_scale;
   w.v_inv_scale = 1.f / c.v_scale;
+  std::memcpy(w.turns, turn_fractions(a.rope_theta), sizeof w.turns);
   for (int i = 0; i < kD / 2; ++i) {
-    w.inv_freq[i] = std::pow((double)a.rope_theta, -(double)i / (kD / 2));
-    w.turns[i] = turn_fraction(w.inv_freq[i]);
     int axis = 0;
     if (a.section && a.interleaved) axis = i % 3 == 1 && i < 3 * a.section[1] ? 1 : (i % 3 == 2 && i < 3 * a.section[2] ? 2 : 0);
     else if (a.section) axis = (i >= a.section[0]) + (i >= a.section[0] + a.section[1]);

@@ -61,7 +61,6 @@ struct WriteParams {
   int max_pages, num_pages, page_log2;
   float eps, k_scale, v_scale, k_inv_scale, v_inv_scale;
   uint64_t turns[kD / 2];    // theta^(-i/64) / (2 pi) modulo 1, in units of 2^-64
-  double inv_freq[kD / 2];   // theta^(-i/64)
   uint8_t axis[kD / 2];      // which row of positions
   size_t kv_rows;            // rows of 128 in the cache, for checked builds
 };
@@ -201,8 +200,9 @@ __device__ __noinline__ void key_codes_f64(const WriteParams& p, int n, const ui
   double zl[8], zh[8], al = 0.0, ah = 0.0;
   for (int i = 0; i < 8; ++i) {
     const int a = 8 * idx + i;
-    Float2 sv, cv;
-    sincos_series((double)__ldg(p.positions + (size_t)p.axis[a] * p.tokens + n) * p.inv_freq[a], sv, cv);
+    const int64_t pos = __ldg(p.positions + (size_t)p.axis[a] * p.tokens + n);
+    Float2 sv, cv;  // the angle's part of a turn, in [-pi, pi)
+    sincos_series((double)(int64_t)((uint64_t)pos * p.turns[a]) * 3.4061215800865545e-19, sv, cv);  // 2 pi / 2^64
     const double s = (double)sv.hi + (double)sv.lo, c = (double)cv.hi + (double)cv.lo;
     const double yl = (double)xl[i] * (double)wl[i] * r, yh = (double)xh[i] * (double)wh[i] * r;
     zl[i] = yl * c - yh * s;
