@@ -324,6 +324,187 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
   else return 8 * (cq + 4 * (ks >> 1)) + 4 * (ks & 1) + 2 * pair;
 }
 
+// ---------------------------------------------------------------- e2m1 tile
+//
+// One warp's 32 tokens of an e2m1 tile (rows R .. R + 31): scores, softmax and
+// output for kNT n-tiles of columns.
+//
+// The group scales join K and V before the products: code * scale is exact in
+// f16 (at most 2 + 4 significand bits, magnitudes 2^-10 to 2688), so neither
+// scores nor weights need a step of their own.  Per 16 tokens that is 64
+// conversions on the integer pipe and 64 multiplications on the FP16 one,
+// which run side by side.
+//
+// FULL: no slot is masked.  The weights are then 2^(score * scale - m) by one
+// FMA and ex2, and the maximum m of a column is only looked for (shuffles) when
+// some lane's score exceeds it (a vote), which after a piece's first tiles is
+// rare.  Masked tokens take weight 0 by selection; a token past the tile's rows
+// also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
+// that are masked).
+constexpr int kFp4Tokens = 32;
+template <int kNT, bool FULL>
+__device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV, const uint2* ks, const uint2* vs, int R,
+                                           int rows, int tile_t0, const uint32_t (&qb)[kNT][8][2], const uint32_t* qfr,
+                                           const float (&sl2c)[kNT][2], const int (&lim)[kNT], float (&m)[kNT][2],
+                                           float (&l)[kNT][2], float (&o)[kNT][8][4]) {
+  constexpr int kSG = kFp4Tokens / 16, kRow = kv_row_bytes(kKvE2M1);
+  const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3;
+  float x[kSG][kNT][4];
+#pragma unroll
+  for (int sj = 0; sj < kSG; ++sj) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) x[sj][nt][0] = x[sj][nt][1] = x[sj][nt][2] = x[sj][nt][3] = 0.f;
+    // lane cq's 16 bytes of rows gq and gq + 8: groups 2cq and 2cq + 1
+    const int r = R + 16 * sj + gq;
+    const uint4 a4 = *reinterpret_cast<const uint4*>(sK + r * kRow + 16 * cq);
+    const uint4 b4 = *reinterpret_cast<const uint4*>(sK + (r + 8) * kRow + 16 * cq);
+    const uint16_t* skr = reinterpret_cast<const uint16_t*>(ks + r) + cq;
+    const uint32_t sa = e4m3x2_to_f16x2(skr[0]), sb = e4m3x2_to_f16x2(skr[8 * 4]);
+    const uint32_t sal[2] = {prmt(sa, sa, 0x1010u), prmt(sa, sa, 0x3232u)};
+    const uint32_t sbl[2] = {prmt(sb, sb, 0x1010u), prmt(sb, sb, 0x3232u)};
+    const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w}, bw[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {  // word w: dims 32cq + 8w .. +7, k-steps 2w and 2w + 1
+      uint32_t a[4], c[4];
+      e2m1x8_to_f16(aw[w], a);
+      e2m1x8_to_f16(bw[w], c);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = 2 * w + h;
+        const uint32_t a0 = mul_f16x2(a[2 * h], sal[w >> 1]), a2 = mul_f16x2(a[2 * h + 1], sal[w >> 1]);
+        const uint32_t a1 = mul_f16x2(c[2 * h], sbl[w >> 1]), a3 = mul_f16x2(c[2 * h + 1], sbl[w >> 1]);
+        if constexpr (kNT == 2) {  // Q^T in shared memory
+          const uint4 qv = ld_shared_u4(qfr + (k * 32 + lane) * 4);
+          mma16816<false>(x[sj][0], a0, a1, a2, a3, qv.x, qv.y);
+          mma16816<false>(x[sj][1], a0, a1, a2, a3, qv.z, qv.w);
+        } else {
+          mma16816<false>(x[sj][0], a0, a1, a2, a3, qb[0][k][0], qb[0][k][1]);
+        }
+      }
+    }
+    // x[sj][nt]: [0] token gq column 2cq, [1] column 2cq + 1, [2], [3] token gq + 8
+    if constexpr (!FULL) {
+      const int ta = tile_t0 + r, tb = ta + 8;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) {
+        x[sj][nt][0] = ta < lim[nt] ? x[sj][nt][0] * sl2c[nt][0] : -INFINITY;
+        x[sj][nt][1] = ta < lim[nt] ? x[sj][nt][1] * sl2c[nt][1] : -INFINITY;
+        x[sj][nt][2] = tb < lim[nt] ? x[sj][nt][2] * sl2c[nt][0] : -INFINITY;
+        x[sj][nt][3] = tb < lim[nt] ? x[sj][nt][3] * sl2c[nt][1] : -INFINITY;
+      }
+    }
+  }
+
+  // ---- online softmax per column
+  bool grow = false;
+#pragma unroll
+  for (int sj = 0; sj < kSG; ++sj)
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      if constexpr (FULL) {
+        grow |= fmaxf(fmaf(x[sj][nt][0], sl2c[nt][0], -m[nt][0]), fmaf(x[sj][nt][2], sl2c[nt][0], -m[nt][0])) > 0.f ||
+                fmaxf(fmaf(x[sj][nt][1], sl2c[nt][1], -m[nt][1]), fmaf(x[sj][nt][3], sl2c[nt][1], -m[nt][1])) > 0.f;
+      } else {
+        grow |= fmaxf(x[sj][nt][0], x[sj][nt][2]) > m[nt][0] || fmaxf(x[sj][nt][1], x[sj][nt][3]) > m[nt][1];
+      }
+    }
+  if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      float h0 = -INFINITY, h1 = -INFINITY;
+#pragma unroll
+      for (int sj = 0; sj < kSG; ++sj) {
+        h0 = fmaxf(h0, fmaxf(x[sj][nt][0], x[sj][nt][2]));
+        h1 = fmaxf(h1, fmaxf(x[sj][nt][1], x[sj][nt][3]));
+      }
+      if constexpr (FULL) {  // (scales are >= 0)
+        h0 *= sl2c[nt][0];
+        h1 *= sl2c[nt][1];
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, off));
+        h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, off));
+      }
+      h0 = fmaxf(h0, m[nt][0]);
+      h1 = fmaxf(h1, m[nt][1]);
+      // 0 when the old max was -inf; 1 when unchanged (also covers -inf == -inf)
+      const float a0 = h0 == m[nt][0] ? 1.f : ex2(m[nt][0] - h0);
+      const float a1 = h1 == m[nt][1] ? 1.f : ex2(m[nt][1] - h1);
+      l[nt][0] *= a0;
+      l[nt][1] *= a1;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        o[nt][mt][0] *= a0;
+        o[nt][mt][2] *= a0;
+        o[nt][mt][1] *= a1;
+        o[nt][mt][3] *= a1;
+      }
+      m[nt][0] = h0;
+      m[nt][1] = h1;
+    }
+  }
+
+  // ---- weights as P^T B-fragments (see the transposes of the other formats);
+  // the denominator sums them before their rounding to f16
+  uint32_t pb[kSG][kNT][2];
+#pragma unroll
+  for (int sj = 0; sj < kSG; ++sj)
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      float p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (FULL) p[e] = ex2(fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]));
+        else p[e] = x[sj][nt][e] == -INFINITY ? 0.f : ex2(x[sj][nt][e] - m[nt][e & 1]);
+      }
+      l[nt][0] += p[0] + p[2];
+      l[nt][1] += p[1] + p[3];
+      pb[sj][nt][0] = transpose8x8_b16(pack_f16(p[0], p[1]));
+      pb[sj][nt][1] = transpose8x8_b16(pack_f16(p[2], p[3]));
+    }
+
+  // ---- O^T += V^T . P^T: lane (gq, cq) takes 8 bytes, dims 16gq .. 16gq + 15 (one
+  // scale group), of tokens 2cq, 2cq + 1, 2cq + 8, 2cq + 9.  The nibbles of a
+  // pair's two tokens are joined into bytes, so that each conversion yields one
+  // dim of both.
+#pragma unroll
+  for (int sj = 0; sj < kSG; ++sj) {
+    const int r = R + 16 * sj + 2 * cq;
+    const uint8_t* v = sV + r * kRow + 8 * gq;
+    const uint2 w0 = *reinterpret_cast<const uint2*>(v), w1 = *reinterpret_cast<const uint2*>(v + kRow);
+    const uint2 w2 = *reinterpret_cast<const uint2*>(v + 8 * kRow), w3 = *reinterpret_cast<const uint2*>(v + 9 * kRow);
+    const uint8_t* svr = reinterpret_cast<const uint8_t*>(vs + r) + gq;
+    uint32_t s0 = svr[0], s1 = svr[8], s2 = svr[64], s3 = svr[72];
+    if constexpr (!FULL) {
+      if (r >= rows) s0 = 0u;
+      if (r + 1 >= rows) s1 = 0u;
+      if (r + 8 >= rows) s2 = 0u;
+      if (r + 9 >= rows) s3 = 0u;
+    }
+    const uint32_t sA = e4m3x2_to_f16x2((uint16_t)(s0 | (s1 << 8)));  // tokens r, r + 1
+    const uint32_t sB = e4m3x2_to_f16x2((uint16_t)(s2 | (s3 << 8)));  // tokens r + 8, r + 9
+    const uint32_t a[2] = {w0.x, w0.y}, b[2] = {w1.x, w1.y}, c[2] = {w2.x, w2.y}, d[2] = {w3.x, w3.y};
+    constexpr uint32_t kLow = 0x0f0f0f0fu;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // word j: dims 16gq + 8j .. +7 -> m-tiles 4j .. 4j + 3
+      uint32_t e0[4], e1[4], e2[4], e3[4];
+      e2m1x8_to_f16((a[j] & kLow) | ((b[j] << 4) & ~kLow), e0);  // even dims of tokens r, r + 1
+      e2m1x8_to_f16(((a[j] >> 4) & kLow) | (b[j] & ~kLow), e1);  // odd dims
+      e2m1x8_to_f16((c[j] & kLow) | ((d[j] << 4) & ~kLow), e2);  // tokens r + 8, r + 9
+      e2m1x8_to_f16(((c[j] >> 4) & kLow) | (d[j] & ~kLow), e3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t A0 = mul_f16x2(e0[i], sA), A1 = mul_f16x2(e1[i], sA);
+        const uint32_t A2 = mul_f16x2(e2[i], sB), A3 = mul_f16x2(e3[i], sB);
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          mma16816<false>(o[nt][4 * j + i], A0, A1, A2, A3, pb[sj][nt][0], pb[sj][nt][1]);
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ work pieces
 
 // Tokens [t_begin, t_end) of row (b, KV head g) (L = the row's length).  Its
@@ -536,7 +717,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
   // tokens 507.9 / 540.7 -> 503.8 / 507.9, int8 618.5 / 620.5 -> 602.1 /
   // 616.4 (pairs with Q in registers spilled more and made all but the e4m3
   // 4-token window slower).
-  constexpr int kSG = is_narrow(KVF) && NQ > 2 ? 2 : 1;
+  constexpr int kSG = is_8bit(KVF) && NQ > 2 ? 2 : 1;
   constexpr bool kQS = mma_q_in_smem(KVF, NQ);
   static_assert(kSlabs % kSG == 0, "whole slab groups");
   constexpr int kCols = kGroup * NQ;                            // (query token, head) columns
@@ -1008,6 +1189,16 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
       const uint8_t* sV = sK + T::kTileBytes;
       const int tile_t0 = t_begin + i * T::kTile;
       const int rows = min(T::kTile, t_end - tile_t0);
+      if constexpr (KVF == kKvE2M1) {
+        const uint2* const ts = scl + st * (kScaleStageBytes / (int)sizeof(RowScale));
+        const int R = warp * 16 * kSlabs;
+        static_assert(T::kTile / kMmaConsumerWarps == kFp4Tokens, "a warp's share of a tile");
+        // the earliest query's last slot is past the tile: nothing is masked
+        if (rows == T::kTile && tile_t0 + T::kTile <= L - NQ + 1)
+          fp4_tokens<kNT, true>(sK, sV, ts, ts + T::kTile, R, rows, tile_t0, qb, kQS ? qfr : nullptr, sl2c, lim, m, l, o);
+        else if (R < rows)  // warp-uniform
+          fp4_tokens<kNT, false>(sK, sV, ts, ts + T::kTile, R, rows, tile_t0, qb, kQS ? qfr : nullptr, sl2c, lim, m, l, o);
+      } else {
       // int8: the bf16 row scale of tile row r (plane 0: K, 1: V), read where
       // it is used (fewer live registers); 0 past the tile's rows
       const RowScale* tsk = scl + st * (kScaleStageBytes / (int)sizeof(RowScale));
@@ -1040,41 +1231,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
         {
           const uint8_t* k0 = sK + (R + gq) * T::kRowBytes;
           const uint8_t* k1 = k0 + 8 * T::kRowBytes;
-          if constexpr (KVF == kKvE2M1) {
-            // The group scales join K here: code * scale is exact in f16 (at
-            // most 2 + 4 significand bits, magnitudes 2^-10 to 2688), so the
-            // scores need no step of their own.  Lane cq's chunk is the whole
-            // of groups 2cq and 2cq + 1.  Past the tile's rows the scales are
-            // whatever the stage held; those scores are masked below.
-            const uint4 x = *reinterpret_cast<const uint4*>(k0 + 16 * cq);
-            const uint4 y = *reinterpret_cast<const uint4*>(k1 + 16 * cq);
-            const uint16_t* skr = reinterpret_cast<const uint16_t*>(tsk + R + gq) + cq;
-            const uint32_t sa = e4m3x2_to_f16x2(skr[0]), sb = e4m3x2_to_f16x2(skr[8 * 4]);
-            const uint32_t sal[2] = {prmt(sa, sa, 0x1010u), prmt(sa, sa, 0x3232u)};
-            const uint32_t sbl[2] = {prmt(sb, sb, 0x1010u), prmt(sb, sb, 0x3232u)};
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-  #pragma unroll
-            for (int w = 0; w < 4; ++w) {  // word w: dims 32cq + 8w .. +7, k-steps 2w and 2w + 1
-              uint32_t a[4], c[4];
-              e2m1x8_to_f16(xs[w], a);  // row gq
-              e2m1x8_to_f16(ys[w], c);  // row gq + 8
-  #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int ks = 2 * w + h;
-                const uint32_t a0 = mul_f16x2(a[2 * h], sal[w >> 1]), a2 = mul_f16x2(a[2 * h + 1], sal[w >> 1]);
-                const uint32_t a1 = mul_f16x2(c[2 * h], sbl[w >> 1]), a3 = mul_f16x2(c[2 * h + 1], sbl[w >> 1]);
-                if constexpr (kQS) {
-                  const uint4 qv = ld_shared_u4(qfr + (ks * 32 + lane) * 4);
-                  mma16816<false>(sc[0], a0, a1, a2, a3, qv.x, qv.y);
-                  mma16816<false>(sc[kNT - 1], a0, a1, a2, a3, qv.z, qv.w);
-                } else {
-  #pragma unroll
-                  for (int nt = 0; nt < kNT; ++nt)
-                    mma16816<false>(sc[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
-                }
-              }
-            }
-          } else if constexpr (is_8bit(KVF)) {
+          if constexpr (is_8bit(KVF)) {
   #pragma unroll
             for (int ci = 0; ci < 2; ++ci) {
               const uint4 x = *reinterpret_cast<const uint4*>(k0 + 16 * (cq + 4 * ci));
@@ -1244,43 +1401,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
         const uint8_t* v0 = sV + r0 * T::kRowBytes;
         const bool ok0 = !partial || r0 < rows, ok1 = !partial || r0 + 1 < rows;
         const bool ok2 = !partial || r0 + 8 < rows, ok3 = !partial || r0 + 9 < rows;
-        if constexpr (KVF == kKvE2M1) {
-          // 8 bytes a token: dims 16gq..16gq+15, one scale group.  Nibbles of
-          // the two tokens of a pair are joined into bytes, so that each
-          // conversion yields one dim of both tokens; code * scale is exact.
-          // A token past the tile's rows takes scale 0 (its weight is 0, but
-          // its stale scale could be NaN).
-          const uint2 w0 = *reinterpret_cast<const uint2*>(v0 + 8 * gq);
-          const uint2 w1 = *reinterpret_cast<const uint2*>(v0 + T::kRowBytes + 8 * gq);
-          const uint2 w2 = *reinterpret_cast<const uint2*>(v0 + 8 * T::kRowBytes + 8 * gq);
-          const uint2 w3 = *reinterpret_cast<const uint2*>(v0 + 9 * T::kRowBytes + 8 * gq);
-          const uint8_t* svr = reinterpret_cast<const uint8_t*>(tsk + T::kTile + r0) + gq;
-          uint32_t s0 = svr[0], s1 = svr[8], s2 = svr[64], s3 = svr[72];
-          if (!ok0) s0 = 0u;
-          if (!ok1) s1 = 0u;
-          if (!ok2) s2 = 0u;
-          if (!ok3) s3 = 0u;
-          const uint32_t sA = e4m3x2_to_f16x2((uint16_t)(s0 | (s1 << 8)));  // tokens r0, r0 + 1
-          const uint32_t sB = e4m3x2_to_f16x2((uint16_t)(s2 | (s3 << 8)));  // tokens r0 + 8, r0 + 9
-          const uint32_t a[2] = {w0.x, w0.y}, bq[2] = {w1.x, w1.y}, c[2] = {w2.x, w2.y}, d[2] = {w3.x, w3.y};
-          constexpr uint32_t kLow = 0x0f0f0f0fu;
-  #pragma unroll
-          for (int j = 0; j < 2; ++j) {  // word j: dims 16gq + 8j .. +7 -> m-tiles 4j..4j+3
-            uint32_t e0[4], e1[4], e2[4], e3[4];
-            e2m1x8_to_f16((a[j] & kLow) | ((bq[j] << 4) & ~kLow), e0);  // even dims of tokens r0, r0 + 1
-            e2m1x8_to_f16(((a[j] >> 4) & kLow) | (bq[j] & ~kLow), e1);  // odd dims
-            e2m1x8_to_f16((c[j] & kLow) | ((d[j] << 4) & ~kLow), e2);   // tokens r0 + 8, r0 + 9
-            e2m1x8_to_f16(((c[j] >> 4) & kLow) | (d[j] & ~kLow), e3);
-  #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t A0 = mul_f16x2(e0[i], sA), A1 = mul_f16x2(e1[i], sA);
-              const uint32_t A2 = mul_f16x2(e2[i], sB), A3 = mul_f16x2(e3[i], sB);
-  #pragma unroll
-              for (int nt = 0; nt < kNT; ++nt)
-                mma16816<false>(o[nt][4 * j + i], A0, A1, A2, A3, bh[sj][nt][0], bh[sj][nt][1]);
-            }
-          }
-        } else if constexpr (is_8bit(KVF)) {
+        if constexpr (is_8bit(KVF)) {
           uint4 w0 = *reinterpret_cast<const uint4*>(v0 + 16 * gq);
           uint4 w1 = *reinterpret_cast<const uint4*>(v0 + T::kRowBytes + 16 * gq);
           uint4 w2 = *reinterpret_cast<const uint4*>(v0 + 8 * T::kRowBytes + 16 * gq);
@@ -1341,6 +1462,7 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
       // carries more than 16 tiles' worth of it
       if constexpr (KVF == kKvI8) {
         if ((i & 15) == 15) take_v_bias(o, vw);
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
