@@ -274,12 +274,6 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&d)[4]) {
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
       : "r"(w));
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // Two int8 codes (low byte = first element) -> exact f16x2 of code + 1152.
 // With b = code + 128 (flip the sign bit), the f16 pattern 0x6400 | b is
 // 1024 + b, an integer in [1024, 1279], exact in f16.  Four codes of a word

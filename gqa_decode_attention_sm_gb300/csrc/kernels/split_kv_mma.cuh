@@ -131,7 +131,8 @@ constexpr int kMmaThreads = (kMmaConsumerWarps + 1) * 32;
 // (A warp's registers come from one quarter of the SM's register file: 3
 // CTAs of 5 warps put 4 warps on some quarter, 128 registers each at most;
 // 2 CTAs put 3, 168 at most.)
-// An e2m1 stage is half as large, so it keeps 3 stages at 3 CTAs per SM.
+// An e2m1 stage is half as large, so it keeps 3 stages at 3 CTAs per SM (8 x
+// 32768 tokens, us per call: 60 so, 64 with 2 stages, 63 at 4 CTAs of 2 stages).
 __host__ __device__ constexpr int mma_stages(int kvf, int nq) { return is_8bit(kvf) && nq <= 2 ? 2 : 3; }
 __host__ __device__ constexpr int mma_ctas_per_sm(int kvf, int nq) { return is_narrow(kvf) && nq <= 2 ? 3 : 2; }
 constexpr int kMaxQLen = 4;  // query tokens per request (a verify window when > 1)
@@ -331,9 +332,17 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 //
 // The group scales join K and V before the products: code * scale is exact in
 // f16 (at most 2 + 4 significand bits, magnitudes 2^-10 to 2688), so neither
-// scores nor weights need a step of their own.  Per 16 tokens that is 64
-// conversions on the integer pipe and 64 multiplications on the FP16 one,
-// which run side by side.
+// scores nor weights need a step of their own.
+//
+// What bounds it: the arithmetic.  Per 16 tokens a warp issues 64 conversions
+// (integer pipe, 2 clocks each on an SM quarter), 64 f16 multiplications (2
+// clocks, and they hold up the mma: 16 mma alone take 129 clocks, with 64
+// multiplications 229) and 16 mma (8 clocks).  At 8 x 131072 a call takes 194
+// us; with its copies left out 188, with its arithmetic left out 175.  Taking
+// 32 tokens a step instead of 16 was worth 6 %; a second accumulator chain for
+// the scores, more CTAs per SM or larger tiles nothing.  Scaling the weights
+// instead of V would need an m-tile's 16 dims in one scale group, which rows in
+// their natural order do not give a lane without byte loads.
 //
 // FULL: no slot is masked.  The weights are then 2^(score * scale - m) by one
 // FMA and ex2, and the maximum m of a column is only looked for (shuffles) when
@@ -342,6 +351,11 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 // also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
 // that are masked).
 constexpr int kFp4Tokens = 32;
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, __half2 b) {
+  const __half2 d = __hmul2(as_half2(a), b);
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
 template <int kNT, bool FULL>
 __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV, const uint2* ks, const uint2* vs, int R,
                                            int rows, int tile_t0, const uint32_t (&qb)[kNT][8][2], const uint32_t* qfr,
@@ -359,9 +373,9 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
     const uint4 a4 = *reinterpret_cast<const uint4*>(sK + r * kRow + 16 * cq);
     const uint4 b4 = *reinterpret_cast<const uint4*>(sK + (r + 8) * kRow + 16 * cq);
     const uint16_t* skr = reinterpret_cast<const uint16_t*>(ks + r) + cq;
-    const uint32_t sa = e4m3x2_to_f16x2(skr[0]), sb = e4m3x2_to_f16x2(skr[8 * 4]);
-    const uint32_t sal[2] = {prmt(sa, sa, 0x1010u), prmt(sa, sa, 0x3232u)};
-    const uint32_t sbl[2] = {prmt(sb, sb, 0x1010u), prmt(sb, sb, 0x3232u)};
+    const __half2 sa = as_half2(e4m3x2_to_f16x2(skr[0])), sb = as_half2(e4m3x2_to_f16x2(skr[8 * 4]));
+    const __half2 sal[2] = {__low2half2(sa), __high2half2(sa)};
+    const __half2 sbl[2] = {__low2half2(sb), __high2half2(sb)};
     const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w}, bw[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
     for (int w = 0; w < 4; ++w) {  // word w: dims 32cq + 8w .. +7, k-steps 2w and 2w + 1
@@ -371,8 +385,8 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = 2 * w + h;
-        const uint32_t a0 = mul_f16x2(a[2 * h], sal[w >> 1]), a2 = mul_f16x2(a[2 * h + 1], sal[w >> 1]);
-        const uint32_t a1 = mul_f16x2(c[2 * h], sbl[w >> 1]), a3 = mul_f16x2(c[2 * h + 1], sbl[w >> 1]);
+        const uint32_t a0 = mul_half2(a[2 * h], sal[w >> 1]), a2 = mul_half2(a[2 * h + 1], sal[w >> 1]);
+        const uint32_t a1 = mul_half2(c[2 * h], sbl[w >> 1]), a3 = mul_half2(c[2 * h + 1], sbl[w >> 1]);
         if constexpr (kNT == 2) {  // Q^T in shared memory
           const uint4 qv = ld_shared_u4(qfr + (k * 32 + lane) * 4);
           mma16816<false>(x[sj][0], a0, a1, a2, a3, qv.x, qv.y);
@@ -396,18 +410,27 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
   }
 
   // ---- online softmax per column
+  float y[kSG][kNT][4];  // FULL: log2 of the weights
   bool grow = false;
+  if constexpr (FULL) {
+    float top = -INFINITY;
 #pragma unroll
-  for (int sj = 0; sj < kSG; ++sj)
+    for (int sj = 0; sj < kSG; ++sj)
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      if constexpr (FULL) {
-        grow |= fmaxf(fmaf(x[sj][nt][0], sl2c[nt][0], -m[nt][0]), fmaf(x[sj][nt][2], sl2c[nt][0], -m[nt][0])) > 0.f ||
-                fmaxf(fmaf(x[sj][nt][1], sl2c[nt][1], -m[nt][1]), fmaf(x[sj][nt][3], sl2c[nt][1], -m[nt][1])) > 0.f;
-      } else {
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[sj][nt][e] = fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]);
+          top = fmaxf(top, y[sj][nt][e]);
+        }
+    grow = top > 0.f;
+  } else {
+#pragma unroll
+    for (int sj = 0; sj < kSG; ++sj)
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
         grow |= fmaxf(x[sj][nt][0], x[sj][nt][2]) > m[nt][0] || fmaxf(x[sj][nt][1], x[sj][nt][3]) > m[nt][1];
-      }
-    }
+  }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
@@ -442,6 +465,12 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       }
       m[nt][0] = h0;
       m[nt][1] = h1;
+      if constexpr (FULL) {
+#pragma unroll
+        for (int sj = 0; sj < kSG; ++sj)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[sj][nt][e] = fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]);
+      }
     }
   }
 
@@ -455,7 +484,7 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if constexpr (FULL) p[e] = ex2(fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]));
+        if constexpr (FULL) p[e] = ex2(y[sj][nt][e]);
         else p[e] = x[sj][nt][e] == -INFINITY ? 0.f : ex2(x[sj][nt][e] - m[nt][e & 1]);
       }
       l[nt][0] += p[0] + p[2];
@@ -482,8 +511,8 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       if (r + 8 >= rows) s2 = 0u;
       if (r + 9 >= rows) s3 = 0u;
     }
-    const uint32_t sA = e4m3x2_to_f16x2((uint16_t)(s0 | (s1 << 8)));  // tokens r, r + 1
-    const uint32_t sB = e4m3x2_to_f16x2((uint16_t)(s2 | (s3 << 8)));  // tokens r + 8, r + 9
+    const __half2 sA = as_half2(e4m3x2_to_f16x2((uint16_t)prmt(s0, s1, 0x0040u)));  // tokens r, r + 1
+    const __half2 sB = as_half2(e4m3x2_to_f16x2((uint16_t)prmt(s2, s3, 0x0040u)));  // tokens r + 8, r + 9
     const uint32_t a[2] = {w0.x, w0.y}, b[2] = {w1.x, w1.y}, c[2] = {w2.x, w2.y}, d[2] = {w3.x, w3.y};
     constexpr uint32_t kLow = 0x0f0f0f0fu;
 #pragma unroll
@@ -495,8 +524,8 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       e2m1x8_to_f16(((c[j] >> 4) & kLow) | (d[j] & ~kLow), e3);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t A0 = mul_f16x2(e0[i], sA), A1 = mul_f16x2(e1[i], sA);
-        const uint32_t A2 = mul_f16x2(e2[i], sB), A3 = mul_f16x2(e3[i], sB);
+        const uint32_t A0 = mul_half2(e0[i], sA), A1 = mul_half2(e1[i], sA);
+        const uint32_t A2 = mul_half2(e2[i], sB), A3 = mul_half2(e3[i], sB);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt)
           mma16816<false>(o[nt][4 * j + i], A0, A1, A2, A3, pb[sj][nt][0], pb[sj][nt][1]);
@@ -1191,8 +1220,8 @@ __global__ void __launch_bounds__(kMmaThreads, mma_ctas_per_sm(KVF, NQ))
       const int rows = min(T::kTile, t_end - tile_t0);
       if constexpr (KVF == kKvE2M1) {
         const uint2* const ts = scl + st * (kScaleStageBytes / (int)sizeof(RowScale));
-        const int R = warp * 16 * kSlabs;
         static_assert(T::kTile / kMmaConsumerWarps == kFp4Tokens, "a warp's share of a tile");
+        const int R = warp * kFp4Tokens;
         // the earliest query's last slot is past the tile: nothing is masked
         if (rows == T::kTile && tile_t0 + T::kTile <= L - NQ + 1)
           fp4_tokens<kNT, true>(sK, sV, ts, ts + T::kTile, R, rows, tile_t0, qb, kQS ? qfr : nullptr, sl2c, lim, m, l, o);
