@@ -29,38 +29,47 @@ cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, int threads, cudaSt
 
 }  // namespace
 
-cudaError_t launch_write_kv(WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream) {
-  // Few tokens: a warp for each unit of four heads, so that the call's latency
-  // is one unit's; many: a warp for each token, so that its angles are formed
-  // once.
-  p.parts = p.tokens <= 8 * sms ? kWriteUnits : 1;
-  const long long items = (long long)p.tokens * p.parts;
+template <int U>
+cudaError_t launch_write_u(const WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream) {
+  const long long items = (long long)p.tokens * (kWriteUnits / U);
   const dim3 grid((unsigned)std::min<long long>((items + kWriteWarps - 1) / kWriteWarps, 2LL * sms));
   const bool bf = qf == kQBF16;
+  const auto go = [&](auto kernel) { return launch(kernel, p, grid, kWriteThreads, stream); };
   switch (kvf) {
-    case kKvF16: return launch(write_kv_kernel<kKvF16, kQF16>, p, grid, kWriteThreads, stream);
-    case kKvBF16: return launch(write_kv_kernel<kKvBF16, kQBF16>, p, grid, kWriteThreads, stream);
-    case kKvE4M3:
-      return launch(bf ? write_kv_kernel<kKvE4M3, kQBF16> : write_kv_kernel<kKvE4M3, kQF16>, p, grid, kWriteThreads,
-                    stream);
-    case kKvI8:
-      return launch(bf ? write_kv_kernel<kKvI8, kQBF16> : write_kv_kernel<kKvI8, kQF16>, p, grid, kWriteThreads,
-                    stream);
-    default:
-      return launch(bf ? write_kv_kernel<kKvE2M1, kQBF16> : write_kv_kernel<kKvE2M1, kQF16>, p, grid, kWriteThreads,
-                    stream);
+    case kKvF16: return go(write_kv_kernel<kKvF16, kQF16, U>);
+    case kKvBF16: return go(write_kv_kernel<kKvBF16, kQBF16, U>);
+    case kKvE4M3: return bf ? go(write_kv_kernel<kKvE4M3, kQBF16, U>) : go(write_kv_kernel<kKvE4M3, kQF16, U>);
+    case kKvI8: return bf ? go(write_kv_kernel<kKvI8, kQBF16, U>) : go(write_kv_kernel<kKvI8, kQF16, U>);
+    default: return bf ? go(write_kv_kernel<kKvE2M1, kQBF16, U>) : go(write_kv_kernel<kKvE2M1, kQF16, U>);
   }
 }
 
-cudaError_t launch_read_kv(const ReadParams& p, int kvf, int of, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.out_capacity + kReadChunk - 1) / kReadChunk), 2 * kHkv, (unsigned)p.batch);
-  const bool bf = of == kQBF16;
+cudaError_t launch_write_kv(const WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream) {
+  // Few tokens (all their units resident at once): a warp for each unit, so that
+  // the call's latency is one unit's.
+  return (long long)p.tokens * kWriteUnits <= 2LL * kWriteWarps * sms ? launch_write_u<1>(p, kvf, qf, sms, stream)
+                                                                      : launch_write_u<4>(p, kvf, qf, sms, stream);
+}
+
+// About 64 CTAs an SM (8 waves) over the rows: lengths are on the device, so the
+// grid covers the capacity and short rows leave early; with fewer CTAs the long
+// rows finish late (8 x U[16k, 32k] e2m1 tokens: 148 us; 155 with 32).
+template <int KVF>
+cudaError_t launch_read_t(const ReadParams& p, int of, int sms, cudaStream_t stream) {
+  const long long rows = 2LL * kHkv * p.batch;
+  const long long chunks = ((long long)p.out_capacity + kReadChunk - 1) / kReadChunk;
+  const long long want = (64LL * sms + rows - 1) / rows;
+  const dim3 grid((unsigned)std::min(chunks, want), 2 * kHkv, (unsigned)p.batch);
+  return launch(of == kQBF16 ? read_kv_kernel<KVF, kQBF16> : read_kv_kernel<KVF, kQF16>, p, grid, kReadThreads, stream);
+}
+
+cudaError_t launch_read_kv(const ReadParams& p, int kvf, int of, int sms, cudaStream_t stream) {
   switch (kvf) {
-    case kKvF16: return launch(bf ? read_kv_kernel<kKvF16, kQBF16> : read_kv_kernel<kKvF16, kQF16>, p, grid, kReadThreads, stream);
-    case kKvBF16: return launch(bf ? read_kv_kernel<kKvBF16, kQBF16> : read_kv_kernel<kKvBF16, kQF16>, p, grid, kReadThreads, stream);
-    case kKvE4M3: return launch(bf ? read_kv_kernel<kKvE4M3, kQBF16> : read_kv_kernel<kKvE4M3, kQF16>, p, grid, kReadThreads, stream);
-    case kKvI8: return launch(bf ? read_kv_kernel<kKvI8, kQBF16> : read_kv_kernel<kKvI8, kQF16>, p, grid, kReadThreads, stream);
-    default: return launch(bf ? read_kv_kernel<kKvE2M1, kQBF16> : read_kv_kernel<kKvE2M1, kQF16>, p, grid, kReadThreads, stream);
+    case kKvF16: return launch_read_t<kKvF16>(p, of, sms, stream);
+    case kKvBF16: return launch_read_t<kKvBF16>(p, of, sms, stream);
+    case kKvE4M3: return launch_read_t<kKvE4M3>(p, of, sms, stream);
+    case kKvI8: return launch_read_t<kKvI8>(p, of, sms, stream);
+    default: return launch_read_t<kKvE2M1>(p, of, sms, stream);
   }
 }
 

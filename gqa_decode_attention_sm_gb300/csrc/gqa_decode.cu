@@ -797,7 +797,8 @@ gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* sta
       (c.block_table && overlap(out, out_bytes, c.block_table, c.table_bytes())) ||
       (workspace && overlap(out, out_bytes, workspace, GQA_WORKSPACE_HEADER_BYTES)))
     return fail(GQA_ERR_ALIASING, "out overlaps the cache, its scales, the lengths, the block table or the workspace");
-  st = current_device_ready(nullptr);
+  int sms = 0;
+  st = current_device_ready(&sms);
   if (st != GQA_OK) return st;
   ReadParams r = {};
   r.kv = c.kv;
@@ -816,7 +817,7 @@ gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* sta
   r.k_scale = c.k_scale;
   r.v_scale = c.v_scale;
   r.kv_rows = c.rows();
-  const cudaError_t e = launch_read_kv(r, c.format, out_dtype == GQA_BF16 ? kQBF16 : kQF16, stream);
+  const cudaError_t e = launch_read_kv(r, c.format, out_dtype == GQA_BF16 ? kQBF16 : kQF16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "read kernel launch");
   return GQA_OK;
 }

@@ -9,7 +9,7 @@
 namespace gqa {
 
 // kvf: KvFormat, qf and of: QFormat; sms: the current device's SM count.
-cudaError_t launch_write_kv(WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream);
-cudaError_t launch_read_kv(const ReadParams& p, int kvf, int of, cudaStream_t stream);
+cudaError_t launch_write_kv(const WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream);
+cudaError_t launch_read_kv(const ReadParams& p, int kvf, int of, int sms, cudaStream_t stream);
 
 }  // namespace gqa

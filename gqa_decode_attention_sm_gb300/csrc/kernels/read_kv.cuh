@@ -3,9 +3,14 @@
 // slot 0 on ([B, 2, 8, out_capacity, 128]).
 //
 // Each value is code * scale (* the tensor scale) in FP32, exact but for the
-// tensor scale's product, and rounded once.  Eight threads hold a row, sixteen
-// elements each (one e2m1 scale group), and a thread has kReadRows rows in
-// flight; a CTA reads kReadChunk slots of one (row, plane, KV head).
+// tensor scale's product, and rounded once.  Eight threads hold a row, 16
+// elements each (an e2m1 scale group); a CTA takes every gridDim.x-th chunk of 32
+// slots of one (row, plane, KV head).
+//
+// Bound by HBM, most of it the output's writes.  One row in flight a thread and
+// many CTAs keep the writes of a CTA close together: 8 x U[16k, 32k] e2m1 tokens
+// (328 bytes a row moved) take 148 us, 1.03 of the copy peak, with 4 rows in
+// flight 197; 16 threads a row 175.
 #pragma once
 
 #include "common.cuh"
@@ -13,8 +18,10 @@
 namespace gqa {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 4;                                // rows a thread has in flight
-constexpr int kReadChunk = kReadRows * kReadThreads / 8;    // slots a CTA reads
+constexpr int kReadRowThreads = 8;                           // threads a row
+constexpr int kReadElems = kD / kReadRowThreads;             // elements of a thread
+constexpr int kReadChunk = kReadThreads / kReadRowThreads;   // slots a CTA takes at once
+static_assert(kReadElems == kE2M1Group, "a thread's elements have one e2m1 scale");
 
 struct ReadParams {
   const void* kv;
@@ -51,14 +58,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
   if ((len != len_raw || start != start_raw) && p.flags && pg == 0 && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(p.flags, GQA_FLAG_LENGTH_CLAMPED);
   const int n = min(len - start, p.out_capacity);
-  const int j0 = blockIdx.x * kReadChunk + (threadIdx.x >> 3), e = threadIdx.x & 7;
-  constexpr int kWords = kv_row_bytes(KVF) / 32;  // 32-bit words of a thread's 16 elements
-  uint32_t w[kReadRows][kWords];
-  float sc[kReadRows];
-#pragma unroll
-  for (int k = 0; k < kReadRows; ++k) {
-    const int j = j0 + k * (kReadThreads / 8);
-    if (j >= n) continue;
+  constexpr int kWords = kv_row_bytes(KVF) / (4 * kReadRowThreads);  // 32-bit words of a thread's elements
+  const int e = threadIdx.x % kReadRowThreads;
+  const float all = pg < kHkv ? p.k_scale : p.v_scale;
+  for (int j = blockIdx.x * kReadChunk + threadIdx.x / kReadRowThreads; j < n; j += gridDim.x * kReadChunk) {
     const int t = start + j;
     size_t unit = (size_t)b, rows = (size_t)p.capacity, in = (size_t)t;
     if (p.block_table != nullptr) {
@@ -79,52 +82,40 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
       }
     }
     const uint32_t* src = static_cast<const uint32_t*>(p.kv) + row * (kv_row_bytes(KVF) / 4) + e * kWords;
+    uint32_t w[kWords], o[kReadElems / 2];
     if constexpr (kWords == 2) {
       const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
-      w[k][0] = v.x;
-      w[k][1] = v.y;
+      w[0] = v.x;
+      w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
         const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        w[k][4 * i] = v.x;
-        w[k][4 * i + 1] = v.y;
-        w[k][4 * i + 2] = v.z;
-        w[k][4 * i + 3] = v.w;
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
       }
     }
-    if constexpr (KVF == kKvE2M1) {
-      const uint32_t s = __ldg(static_cast<const uint8_t*>(p.kv_scales) + row * 8 + e);
-      sc[k] = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)s)).x;
-    } else if constexpr (KVF == kKvI8) {
-      sc[k] = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.kv_scales) + row) << 16);
-    } else {
-      sc[k] = 1.f;
-    }
-  }
-  const float all = pg < kHkv ? p.k_scale : p.v_scale;
-#pragma unroll
-  for (int k = 0; k < kReadRows; ++k) {
-    const int j = j0 + k * (kReadThreads / 8);
-    if (j >= n) continue;
-    uint32_t o[8];
     if constexpr (KVF == kKvF16 || KVF == kKvBF16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kReadElems / 2; ++i) {
         if constexpr ((KVF == kKvF16) == (OF == kQF16)) {
-          o[i] = w[k][i];
+          o[i] = w[i];
         } else {
-          const float2 f = KVF == kKvF16 ? f16x2_to_f32x2(w[k][i]) : bf16x2_to_f32x2(w[k][i]);
+          const float2 f = KVF == kKvF16 ? f16x2_to_f32x2(w[i]) : bf16x2_to_f32x2(w[i]);
           o[i] = read_round2<OF>(f.x, f.y);
         }
       }
     } else {
-      float x[16];
+      float x[kReadElems], sc = 1.f;
       if constexpr (KVF == kKvE2M1) {
+        const uint32_t s = __ldg(static_cast<const uint8_t*>(p.kv_scales) + row * (kD / kE2M1Group) + e);
+        sc = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)s)).x;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kWords; ++i) {
           uint32_t d[4];
-          e2m1x8_to_f16(w[k][i], d);
+          e2m1x8_to_f16(w[i], d);
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const float2 f = f16x2_to_f32x2(d[m]);
@@ -134,23 +125,24 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
         }
       } else if constexpr (KVF == kKvE4M3) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[k][i >> 1] >> (16 * (i & 1)))));
+        for (int i = 0; i < kReadElems / 2; ++i) {
+          const float2 f = f16x2_to_f32x2(e4m3x2_to_f16x2((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
           x[2 * i] = f.x;
           x[2 * i + 1] = f.y;
         }
       } else {
+        sc = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p.kv_scales) + row) << 16);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = (float)(int8_t)(w[k][i >> 2] >> (8 * (i & 3)));
+        for (int i = 0; i < kReadElems; ++i) x[i] = (float)(int8_t)(w[i >> 2] >> (8 * (i & 3)));
       }
-      // code * scale is exact; then the tensor scale (1 for int8), rounded once in FP32
+      // code * scale is exact; then the tensor scale, rounded once in FP32
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = read_round2<OF>(x[2 * i] * sc[k] * all, x[2 * i + 1] * sc[k] * all);
+      for (int i = 0; i < kReadElems / 2; ++i) o[i] = read_round2<OF>(x[2 * i] * sc * all, x[2 * i + 1] * sc * all);
     }
     uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                          (((size_t)b * 2 * kHkv + pg) * p.out_capacity + j) * kD) + 2 * e;
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                                          (((size_t)b * 2 * kHkv + pg) * p.out_capacity + j) * kD + e * kReadElems);
+#pragma unroll
+    for (int i = 0; i < kReadElems / 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
   }
 }
 

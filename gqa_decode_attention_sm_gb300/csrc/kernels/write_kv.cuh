@@ -13,24 +13,27 @@
 //   e2m1       e4m3 scale amax / (6 * tensor scale) of each 16 dims, code = the
 //              e2m1 level nearest to x / (scale * tensor scale)
 //
-// A warp takes a whole token (or, for few tokens, one of its 12 units of 4
-// heads: 8 of q, 2 of k, 2 of v).  A quarter of the warp holds one head, a lane
-// dims 8i..8i+7 and 64+8i..: every rotary pair stays in a lane, a load or a
-// store is 16 bytes and the norm takes three shuffles for four heads.  The 64
-// angles of a token are spread over the lanes, two each, and handed round by
-// shuffles.
+// A token is 12 units of 4 heads (8 of q, 2 of k, 2 of v).  A warp takes 4 units
+// at a time (16 q heads, or k and v), or for few tokens one, and issues all their
+// loads before anything else.  A quarter of the warp holds one head, a lane dims
+// 8i..8i+7 and 64+8i..: every rotary pair stays in a lane, a load or a store is
+// 16 bytes and the norm takes three shuffles for four heads.  The 64 angles of a
+// token are spread over the lanes, two each (the same two for every token), and
+// handed round by shuffles.
 //
 // Angles without FP64 (slow on sm_103a): the host holds theta^(-i/64) / (2 pi)
 // as a 64-bit binary fraction of a turn, so that position * fraction modulo
 // 2^64 is the angle in turns with the whole turns gone, for any 32-bit position
 // within 2^-33 of a turn.  The top two bits (after adding an eighth of a turn)
 // are the quadrant; sin and cos of the rest, |x| <= pi/4, are the Taylor series
-// to x^9 and x^10 (first terms left out below 2^-28), within about 2^-23.
+// to x^9 and x^10 (first terms left out below 2^-28) at the FP32 next to x, and
+// one step along the derivative to x itself: within about 2^-24.
 //
 // e2m1 keys are rounded as the exact z would be.  The FP32 z is off by at most
 // kKeyError of the head's largest magnitude; where that could turn a group's
-// scale or a code (the two ends of the interval round apart), the warp computes
-// those heads again in FP64 (about one unit in a hundred).  Values are exact
+// scale or a code (the two ends of the interval round apart), the warp forms the
+// elements in doubt again, exactly enough (about one unit of four heads in a
+// hundred has one).  Values are exact
 // inputs: their quotients are brought to the tie or off it by the sign of the
 // exact remainder.
 #pragma once
@@ -56,7 +59,6 @@ struct WriteParams {
   void* kv_scales;                      // int8: bf16 a row; e2m1: 8 e4m3 a row
   uint32_t* flags;                      // optional status word
   int tokens, batch, capacity;
-  int parts;                            // warps per token: 1, or kWriteUnits
   const int32_t* block_table;           // paged cache, else null
   int max_pages, num_pages, page_log2;
   float eps, k_scale, v_scale, k_inv_scale, v_inv_scale;
@@ -69,17 +71,25 @@ struct WriteParams {
 __device__ __forceinline__ void sincos_turn(uint64_t turn, float& s, float& c) {
   const uint32_t h = (uint32_t)(turn >> 32);
   const uint32_t quad = (h + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(h - (quad << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const int32_t r = (int32_t)(h - (quad << 30));
+  constexpr float kUnit = 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float rf = (float)r;
+  const float x = rf * kUnit;
+  // what the two roundings of x left out (and 2 pi / 2^32 itself, to a second term)
+  const float rest = fmaf((float)(r - (int32_t)rf), kUnit, fmaf(rf, kUnit, -x) + rf * -4.0709404e-17f);
   const float x2 = x * x;
   float sp = fmaf(x2, 2.75573192e-6f, -1.98412698e-4f);  // 1/9!, -1/7!
   sp = fmaf(x2, sp, 8.33333333e-3f);
   sp = fmaf(x2, sp, -1.66666667e-1f);
-  const float sx = fmaf(x * x2, sp, x);
+  float sx = fmaf(x * x2, sp, x);
   float cp = fmaf(x2, -2.75573192e-7f, 2.48015873e-5f);  // -1/10!, 1/8!
   cp = fmaf(x2, cp, -1.38888889e-3f);
   cp = fmaf(x2, cp, 4.16666667e-2f);
   cp = fmaf(x2, cp, -0.5f);
-  const float cx = fmaf(x2, cp, 1.f);
+  float cx = fmaf(x2, cp, 1.f);
+  const float s0 = sx;
+  sx = fmaf(cx, rest, sx);
+  cx = fmaf(-s0, rest, cx);
   s = quad & 1u ? cx : sx;
   c = quad & 1u ? sx : cx;
   if (quad & 2u) s = -s;
@@ -165,73 +175,31 @@ __device__ __forceinline__ float amax8(const float (&x)[8]) {
   return m;
 }
 
-// The bound of |FP32 z - z| as a share of the head's largest |z|: sums of 16
-// squares in a lane and 8 lanes (19 roundings of the sum, half of that in its
-// root), rsqrt, a coefficient w * cos with cos within 2^-23, and the products:
-// below 2^-20.2 of |y_i| + |y_{i+64}|, itself at most twice the largest |z|.
-constexpr float kKeyError = 0x1p-19f;
+// The bound of |FP32 z - z| as a share of the head's largest |z|, A:
+//   cos and sin within 2^-24, their products with a weight and the one rounded
+//   product of the rotation: 3 * 2^-24 (|y_i cos| + |y_j sin|), at most 3 * 2^-24
+//   of the pair's length, itself at most sqrt(2) A; two more roundings of z
+//   r: the sum of squares (4 levels in a lane, 3 over the lanes, 8 roundings, half
+//   of them in the root), 1 / 128 and eps, rsqrt and its Newton step: 6.5 * 2^-24
+// together 12.8 * 2^-24; 3 * 2^-24 more where a quotient is formed from z, and a
+// little to spare.
+constexpr float kKeyError = 0x1.2p-20f;
 
 struct KeyCodes {
   uint32_t lo, hi;  // codes of dims 8i..8i+7 and 64+8i..
   uint32_t slo, shi;  // the scale bytes of their groups
 };
 
-// One unit of four key heads in FP64: this lane's 16 dims of its quarter's head.
-template <int QF>
-__device__ __noinline__ void key_codes_f64(const WriteParams& p, int n, const uint4& wlo, const uint4& whi,
-                                           KeyCodes& out) {
-  const int idx = threadIdx.x & 7;
-  float xl[8], xh[8], wl[8], wh[8];
-  unpack8<QF>(wlo, xl);
-  unpack8<QF>(whi, xh);
-  double r = 1.0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) wl[i] = wh[i] = 1.f;
-  if (p.k_norm_w) {
-    double ss = 0.0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fma((double)xl[i], (double)xl[i], fma((double)xh[i], (double)xh[i], ss));
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    r = 1.0 / sqrt(ss / kD + (double)p.eps);
-    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 8 * idx), wl);
-    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 64 + 8 * idx), wh);
-  }
-  double zl[8], zh[8], al = 0.0, ah = 0.0;
-  for (int i = 0; i < 8; ++i) {
-    const int a = 8 * idx + i;
-    const int64_t pos = __ldg(p.positions + (size_t)p.axis[a] * p.tokens + n);
-    Float2 sv, cv;  // the angle's part of a turn, in [-pi, pi)
-    sincos_series((double)(int64_t)((uint64_t)pos * p.turns[a]) * 3.4061215800865545e-19, sv, cv);  // 2 pi / 2^64
-    const double s = (double)sv.hi + (double)sv.lo, c = (double)cv.hi + (double)cv.lo;
-    const double yl = (double)xl[i] * (double)wl[i] * r, yh = (double)xh[i] * (double)wh[i] * r;
-    zl[i] = yl * c - yh * s;
-    zh[i] = yh * c + yl * s;
-    al = fmax(al, fabs(zl[i]));
-    ah = fmax(ah, fabs(zh[i]));
-  }
-  al = fmax(al, __shfl_xor_sync(0xffffffffu, al, 1));
-  ah = fmax(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
-  const double ks = (double)p.k_scale;
-  out.slo = to_e4m3x2(double_to_round(al / (6.0 * ks)), 0.f) & 0xffu;
-  out.shi = to_e4m3x2(double_to_round(ah / (6.0 * ks)), 0.f) & 0xffu;
-  const double sl = (double)e4m3_value(out.slo) * ks, sh = (double)e4m3_value(out.shi) * ks;
-  float ql[8], qh[8];
-  for (int i = 0; i < 8; ++i) {
-    ql[i] = sl > 0.0 ? double_to_round(zl[i] / sl) : 0.f;
-    qh[i] = sh > 0.0 ? double_to_round(zh[i] / sh) : 0.f;
-  }
-  out.lo = to_e2m1x8(ql);
-  out.hi = to_e2m1x8(qh);
-}
-
-// Scale byte and codes of one group half from FP32 z within `e` of the exact
-// ones (amax: the group's); false if the exact ones could differ.
-__device__ __forceinline__ bool key_group(const float (&z)[8], float amax, float e, float k_scale, float inv6,
-                                          uint32_t& codes, uint32_t& scale) {
-  // (e covers the roundings of inv6, inv and the products too: 2^-22 of amax)
+// Scale byte of a group whose largest FP32 |z| is `amax`, within `e` of the exact
+// one; false if the exact one could round to another.
+__device__ __forceinline__ bool key_scale(float amax, float e, float inv6, uint32_t& scale) {
   const uint32_t two = to_e4m3x2((amax + e) * inv6, fmaxf(amax - e, 0.f) * inv6);
   scale = two & 0xffu;
+  return scale == (two >> 8);
+}
+// Codes of eight of its z; the nibbles of `unsure` that are not 0 could be others.
+__device__ __forceinline__ void key_codes(const float (&z)[8], float e, uint32_t scale, float k_scale, uint32_t& codes,
+                                          uint32_t& unsure) {
   const float s = e4m3_value(scale) * k_scale;
   const float inv = s > 0.f ? 1.f / s : 0.f;
   const float ei = e * inv;
@@ -242,8 +210,86 @@ __device__ __forceinline__ bool key_group(const float (&z)[8], float amax, float
     down[i] = fmaf(z[i], inv, -ei);
   }
   codes = to_e2m1x8(up);
-  // (a zero of either sign is the same value)
-  return scale == (two >> 8) && ((codes ^ to_e2m1x8(down)) & 0x77777777u) == 0u;
+  unsure = (codes ^ to_e2m1x8(down)) & 0x77777777u;  // (a zero of either sign is the same value)
+}
+
+// One unit of four key heads whose rounding FP32 could not decide: the elements
+// in doubt, and nothing else, are formed again to about 2^-45 (the norm in
+// double-float, the angle's series in double-float, the rest in FP64).
+template <int QF>
+__device__ __noinline__ void key_codes_exact(const WriteParams& p, int n, const uint4& wlo, const uint4& whi,
+                                             const float (&zl)[8], const float (&zh)[8], float gl, float gh, float e,
+                                             KeyCodes& out) {
+  const int idx = threadIdx.x & 7;
+  float yl[8], yh[8];
+  unpack8<QF>(wlo, yl);
+  unpack8<QF>(whi, yh);
+  double r = 1.0;
+  if (p.k_norm_w) {
+    Float2 acc = {0.f, 0.f};  // (squares of 16-bit elements are exact)
+    for (int i = 0; i < 8; ++i) {
+      acc = df_add(acc, Float2{yl[i] * yl[i], 0.f});
+      acc = df_add(acc, Float2{yh[i] * yh[i], 0.f});
+    }
+    for (int off = 4; off > 0; off >>= 1)
+      acc = df_add(acc, Float2{__shfl_xor_sync(0xffffffffu, acc.hi, off), __shfl_xor_sync(0xffffffffu, acc.lo, off)});
+    const double ss = ((double)acc.hi + (double)acc.lo) * (1.0 / kD) + (double)p.eps;
+    r = (double)rsqrtf((float)ss);  // and two Newton steps: 2^-22, 2^-43, below 2^-50
+    r = fma(r * 0.5, fma(-ss * r, r, 1.0), r);
+    r = fma(r * 0.5, fma(-ss * r, r, 1.0), r);
+    float wl[8], wh[8];
+    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 8 * idx), wl);
+    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 64 + 8 * idx), wh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // (exact)
+      yl[i] *= wl[i];
+      yh[i] *= wh[i];
+    }
+  }
+  const auto exact = [&](int i, double& lo, double& hi) {
+    const int a = 8 * idx + i;
+    const int64_t pos = __ldg(p.positions + (size_t)p.axis[a] * p.tokens + n);
+    Float2 sv, cv;  // the angle's part of a turn, in [-pi, pi)
+    sincos_series((double)(int64_t)((uint64_t)pos * p.turns[a]) * 3.4061215800865545e-19, sv, cv);  // 2 pi / 2^64
+    const double s = (double)sv.hi + (double)sv.lo, c = (double)cv.hi + (double)cv.lo;
+    const double u = (double)yl[i] * r, v = (double)yh[i] * r;
+    lo = u * c - v * s;
+    hi = v * c + u * s;
+  };
+  const double ks = (double)p.k_scale;
+  const float inv6 = 1.f / (6.f * p.k_scale);
+  // scales in doubt: from the exact values of the elements that could be the largest
+  const bool sure_l = key_scale(gl, e, inv6, out.slo), sure_h = key_scale(gh, e, inv6, out.shi);
+  if (!__all_sync(0xffffffffu, sure_l && sure_h)) {
+    double al = 0.0, ah = 0.0;
+    for (int i = 0; i < 8; ++i) {
+      const bool nl = !sure_l && fabsf(zl[i]) >= gl - 2.f * e, nh = !sure_h && fabsf(zh[i]) >= gh - 2.f * e;
+      if (!__any_sync(0xffffffffu, nl || nh)) continue;
+      double lo, hi;
+      exact(i, lo, hi);
+      if (nl) al = fmax(al, fabs(lo));
+      if (nh) ah = fmax(ah, fabs(hi));
+    }
+    al = fmax(al, __shfl_xor_sync(0xffffffffu, al, 1));
+    ah = fmax(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
+    if (!sure_l) out.slo = to_e4m3x2(double_to_round(al / (6.0 * ks)), 0.f) & 0xffu;
+    if (!sure_h) out.shi = to_e4m3x2(double_to_round(ah / (6.0 * ks)), 0.f) & 0xffu;
+  }
+  uint32_t ul, uh;
+  key_codes(zl, e, out.slo, p.k_scale, out.lo, ul);
+  key_codes(zh, e, out.shi, p.k_scale, out.hi, uh);
+  const double sl = (double)e4m3_value(out.slo) * ks, sh = (double)e4m3_value(out.shi) * ks;
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t mask = 0xfu << (4 * i);
+    if (!__any_sync(0xffffffffu, ((ul | uh) & mask) != 0u)) continue;
+    double lo, hi;
+    exact(i, lo, hi);
+    // (an exact tie's quotient is exact)
+    float q[8] = {sl > 0.0 ? double_to_round(lo / sl) : 0.f, sh > 0.0 ? double_to_round(hi / sh) : 0.f};
+    const uint32_t c = to_e2m1x8(q);
+    out.lo = (out.lo & ~mask) | ((c & 0xfu) << (4 * i));
+    out.hi = (out.hi & ~mask) | (((c >> 4) & 0xfu) << (4 * i));
+  }
 }
 
 // Where the cache rows of a token go: row index of (plane 0, head 0), and how
@@ -313,12 +359,16 @@ __device__ __forceinline__ void rotate_unit(const uint4& wlo, const uint4& whi, 
   unpack8<QF>(whi, xh);
   float r = 1.f;
   if (norm) {
-    float ss = 0.f;
+    float t[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(xl[i], xl[i], fmaf(xh[i], xh[i], ss));
+    for (int i = 0; i < 4; ++i)
+      t[i] = fmaf(xl[i], xl[i], xh[i] * xh[i]) + fmaf(xl[i + 4], xl[i + 4], xh[i + 4] * xh[i + 4]);
+    float ss = (t[0] + t[1]) + (t[2] + t[3]);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    r = rsqrtf(fmaf(ss, 1.f / kD, eps));
+    ss = fmaf(ss, 1.f / kD, eps);
+    r = rsqrtf(ss);
+    if (ss > 0x1p-60f && ss < 0x1p60f) r = fmaf(0.5f * r, fmaf(-ss * r, r, 1.f), r);  // (a Newton step)
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -365,11 +415,15 @@ __device__ __forceinline__ void store_unit(const WriteParams& p, int n, int plan
       const float gh = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
       float e = fmaxf(gl, gh);
       e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
-      e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4)) * (1.25f * kKeyError);
+      e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4)) * kKeyError;
       const float inv6 = 1.f / (6.f * p.k_scale);
-      bool sure = key_group(xl, gl, e, p.k_scale, inv6, k.lo, k.slo);
-      sure &= key_group(xh, gh, e, p.k_scale, inv6, k.hi, k.shi);
-      if (!__all_sync(0xffffffffu, sure)) key_codes_f64<QF>(p, n, wlo, whi, k);
+      bool sure = key_scale(gl, e, inv6, k.slo);
+      sure &= key_scale(gh, e, inv6, k.shi);
+      uint32_t ul, uh;
+      key_codes(xl, e, k.slo, p.k_scale, k.lo, ul);
+      key_codes(xh, e, k.shi, p.k_scale, k.hi, uh);
+      if (!__all_sync(0xffffffffu, sure && (ul | uh) == 0u))
+        key_codes_exact<QF>(p, n, wlo, whi, xl, xh, gl, gh, e, k);
     } else {
       // values are the inputs themselves: exact
       const float al = amax8(xl), ah = amax8(xh);
@@ -417,27 +471,41 @@ __device__ __forceinline__ void store_unit(const WriteParams& p, int n, int plan
   }
 }
 
-template <int KVF, int QF>
+// U: units a warp takes at a time, 4 (parts of a token: q 0..3, q 4..7, k and v)
+// or 1.
+template <int KVF, int QF, int U>
 __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid_constant__ WriteParams p) {
-  __shared__ uint64_t turns[kD / 2];
-  __shared__ uint8_t axis[kD / 2];
+  constexpr int kParts = kWriteUnits / U;
+  static_assert(kWriteQUnits % U == 0 && (U == 1 || U == kWriteUnits - kWriteQUnits), "whole parts");
   pdl_launch_dependents();
-  if (threadIdx.x < kD / 2) {
-    turns[threadIdx.x] = p.turns[threadIdx.x];
-    axis[threadIdx.x] = p.axis[threadIdx.x];
-  }
-  __syncthreads();
-  pdl_wait_prior_grid();
   const int lane = threadIdx.x & 31, quarter = lane >> 3, idx = lane & 7;
-  const long long items = (long long)p.tokens * p.parts;
+  // this lane's two angles
+  uint64_t turn[2];
+  int axis[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    turn[j] = p.turns[8 * idx + 2 * quarter + j];
+    axis[j] = p.axis[8 * idx + 2 * quarter + j];
+  }
+  pdl_wait_prior_grid();
+  const long long items = (long long)p.tokens * kParts;
   const int step = gridDim.x * kWriteWarps;
   for (long long it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5); it < items; it += step) {
-    const int n = p.parts == 1 ? (int)it : (int)(it / kWriteUnits);
-    const int u0 = p.parts == 1 ? 0 : (int)(it - (long long)n * kWriteUnits);
-    const int u1 = p.parts == 1 ? kWriteUnits : u0 + 1;
-    const bool does_kv = u1 > kWriteQUnits;
+    const int n = (int)(it / kParts), u0 = (int)(it - (long long)n * kParts) * U;
+    uint4 wlo[U], whi[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = u0 + i;
+      const uint16_t* src = u < kWriteQUnits ? p.q_proj + n * p.q_stride + u * 4 * kD
+                            : u < kWriteQUnits + kWriteKUnits
+                                ? p.k_proj + n * p.k_stride + (u - kWriteQUnits) * 4 * kD
+                                : p.v_proj + n * p.v_stride + (u - kWriteQUnits - kWriteKUnits) * 4 * kD;
+      const uint4* s4 = reinterpret_cast<const uint4*>(src + quarter * kD + 8 * idx);
+      wlo[i] = __ldg(s4);
+      whi[i] = __ldg(s4 + 8);
+    }
     RowAt at{0, 0, false};
-    if (does_kv) at = locate(p, n);
+    if (u0 + U > kWriteQUnits) at = locate(p, n);
 
     // the token's angles (not needed by its values)
     float cs[8], sn[8];
@@ -445,9 +513,8 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
       float c2[2], s2[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int a = 8 * idx + 2 * quarter + j;
-        const int pos = __ldg(p.positions + (size_t)axis[a] * p.tokens + n);
-        sincos_turn((uint64_t)(int64_t)pos * turns[a], s2[j], c2[j]);
+        const int pos = __ldg(p.positions + (size_t)axis[j] * p.tokens + n);
+        sincos_turn((uint64_t)(int64_t)pos * turn[j], s2[j], c2[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -455,46 +522,39 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         sn[j] = __shfl_sync(0xffffffffu, s2[j & 1], (j >> 1) * 8 + idx);
       }
     }
-
-    // keys
-    const int k0 = max(u0, kWriteQUnits), k1 = min(u1, kWriteQUnits + kWriteKUnits);
-    if (k0 < k1) {
-      Coefs kc;
-      make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
-      for (int u = k0; u < k1; ++u) {
-        const int g = 4 * (u - kWriteQUnits) + quarter;
-        const uint4* src = reinterpret_cast<const uint4*>(p.k_proj + n * p.k_stride + g * kD + 8 * idx);
-        const uint4 wlo = __ldg(src), whi = __ldg(src + 8);
-        float zl[8], zh[8];
-        rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
-        store_unit<KVF, QF>(p, n, 0, at.base + g * at.head, idx, at.ok, wlo, whi, zl, zh);
-      }
-    }
-    // values
-    const int v0 = max(u0, kWriteQUnits + kWriteKUnits);
-    for (int u = v0; u < u1; ++u) {
-      const int g = 4 * (u - kWriteQUnits - kWriteKUnits) + quarter;
-      const uint4* src = reinterpret_cast<const uint4*>(p.v_proj + n * p.v_stride + g * kD + 8 * idx);
-      const uint4 wlo = __ldg(src), whi = __ldg(src + 8);
-      float xl[8], xh[8];
-      unpack8<QF>(wlo, xl);
-      unpack8<QF>(whi, xh);
-      store_unit<KVF, QF>(p, n, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo, whi, xl, xh);
-    }
-    // queries
     if (u0 < kWriteQUnits) {
       Coefs qc;
       make_coefs<QF>(p.q_norm_w, idx, cs, sn, qc);
-      const uint16_t* src = p.q_proj + n * p.q_stride + quarter * kD + 8 * idx;
-      uint16_t* dst = p.q_out + (size_t)n * kHq * kD + quarter * kD + 8 * idx;
-      for (int u = u0; u < min(u1, kWriteQUnits); ++u) {
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + u * 4 * kD);
-        const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+      uint16_t* dst = p.q_out + ((size_t)n * kHq + 4 * u0 + quarter) * kD + 8 * idx;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
         float zl[8], zh[8];
-        rotate_unit<QF>(wlo, whi, qc, p.q_norm_w != nullptr, p.eps, zl, zh);
-        uint4* d4 = reinterpret_cast<uint4*>(dst + u * 4 * kD);
+        rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
+        uint4* d4 = reinterpret_cast<uint4*>(dst + i * 4 * kD);
         d4[0] = round8<QF>(zl);
         d4[8] = round8<QF>(zh);
+      }
+      continue;
+    }
+    if (u0 < kWriteQUnits + kWriteKUnits) {
+      Coefs kc;
+      make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+#pragma unroll
+      for (int i = 0; i < (U == 1 ? 1 : kWriteKUnits); ++i) {
+        const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
+        float zl[8], zh[8];
+        rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
+        store_unit<KVF, QF>(p, n, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh);
+      }
+    }
+    if (u0 + U > kWriteQUnits + kWriteKUnits) {
+#pragma unroll
+      for (int i = U == 1 ? 0 : kWriteKUnits; i < U; ++i) {
+        const int g = 4 * (u0 + i - kWriteQUnits - kWriteKUnits) + quarter;
+        float xl[8], xh[8];
+        unpack8<QF>(wlo[i], xl);
+        unpack8<QF>(whi[i], xh);
+        store_unit<KVF, QF>(p, n, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo[i], whi[i], xl, xh);
       }
     }
   }
