@@ -110,6 +110,32 @@ __device__ __forceinline__ Float2 df_add(Float2 a, Float2 c) {
 }
 __device__ __forceinline__ constexpr Float2 df_const(double d) { return {(float)d, (float)(d - (double)(float)d)}; }
 
+// sin x and cos x for |x| <= pi/4, x a double-float pair: the series of
+// sincos_series below.
+__device__ __forceinline__ void sincos_reduced(Float2 x, Float2& sx, Float2& cx) {
+  constexpr Float2 kSin[9] = {df_const(0x1p+0), df_const(-0x1.5555555555555p-3), df_const(0x1.1111111111111p-7),
+                              df_const(-0x1.a01a01a01a01ap-13), df_const(0x1.71de3a556c734p-19),
+                              df_const(-0x1.ae64567f544e4p-26), df_const(0x1.6124613a86d09p-33),
+                              df_const(-0x1.ae7f3e733b81fp-41), df_const(0x1.952c77030ad4ap-49)};
+  constexpr Float2 kCos[9] = {df_const(0x1p+0), df_const(-0x1p-1), df_const(0x1.5555555555555p-5),
+                              df_const(-0x1.6c16c16c16c17p-10), df_const(0x1.a01a01a01a01ap-16),
+                              df_const(-0x1.27e4fb7789f5cp-22), df_const(0x1.1eed8eff8d898p-29),
+                              df_const(-0x1.93974a8c07c9dp-37), df_const(0x1.ae7f3e733b81fp-45)};
+  const float xh = x.hi;
+  const float p = __fmul_rn(xh, xh);
+  float e = fmaf(xh, xh, -p);
+  e = fmaf(__fadd_rn(xh, xh), x.lo, e);  // + 2 xh xl (xl^2 is below 2^-48 x^2)
+  const Float2 x2 = fast_two_sum(p, e);
+  Float2 ps = kSin[8], pc = kCos[8];
+#pragma unroll
+  for (int k = 7; k >= 0; --k) {
+    ps = df_add(df_mul(ps, x2), kSin[k]);
+    pc = df_add(df_mul(pc, x2), kCos[k]);
+  }
+  sx = df_mul(ps, x);
+  cx = pc;
+}
+
 // sin a and cos a for an angle below 2^31 radians as double-float pairs,
 // from the mathematics rather than the library routine.  FP64 issues at a
 // small fraction of the FP32 rate on sm_103a, and the same series in FP64
@@ -127,30 +153,13 @@ __device__ __forceinline__ constexpr Float2 df_const(double d) { return {(float)
 // the given a (checked against libm on the CPU by an emulation of the same
 // float operations over |x| <= pi/4).
 __device__ __forceinline__ void sincos_series(double a, Float2& s, Float2& c) {
-  constexpr Float2 kSin[9] = {df_const(0x1p+0), df_const(-0x1.5555555555555p-3), df_const(0x1.1111111111111p-7),
-                              df_const(-0x1.a01a01a01a01ap-13), df_const(0x1.71de3a556c734p-19),
-                              df_const(-0x1.ae64567f544e4p-26), df_const(0x1.6124613a86d09p-33),
-                              df_const(-0x1.ae7f3e733b81fp-41), df_const(0x1.952c77030ad4ap-49)};
-  constexpr Float2 kCos[9] = {df_const(0x1p+0), df_const(-0x1p-1), df_const(0x1.5555555555555p-5),
-                              df_const(-0x1.6c16c16c16c17p-10), df_const(0x1.a01a01a01a01ap-16),
-                              df_const(-0x1.27e4fb7789f5cp-22), df_const(0x1.1eed8eff8d898p-29),
-                              df_const(-0x1.93974a8c07c9dp-37), df_const(0x1.ae7f3e733b81fp-45)};
   const double q = rint(a * kTwoOverPi);
   double xd = fma(-q, kHalfPiHi, a);
   xd = fma(-q, kHalfPiLo, xd);
   const float xh = (float)xd;
   const Float2 x = {xh, (float)(xd - (double)xh)};
-  const float p = __fmul_rn(xh, xh);
-  float e = fmaf(xh, xh, -p);
-  e = fmaf(__fadd_rn(xh, xh), x.lo, e);  // + 2 xh xl (xl^2 is below 2^-48 x^2)
-  const Float2 x2 = fast_two_sum(p, e);
-  Float2 ps = kSin[8], pc = kCos[8];
-#pragma unroll
-  for (int k = 7; k >= 0; --k) {
-    ps = df_add(df_mul(ps, x2), kSin[k]);
-    pc = df_add(df_mul(pc, x2), kCos[k]);
-  }
-  const Float2 sx = df_mul(ps, x), cx = pc;
+  Float2 sx, cx;
+  sincos_reduced(x, sx, cx);
   const Float2 nsx = {-sx.hi, -sx.lo}, ncx = {-cx.hi, -cx.lo};
   switch ((int)((long long)q & 3)) {
     case 0: s = sx; c = cx; break;

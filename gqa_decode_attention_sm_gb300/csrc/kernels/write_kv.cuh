@@ -31,9 +31,11 @@
 //
 // e2m1 keys are rounded as the exact z would be.  The FP32 z is off by at most
 // kKeyError of the head's largest magnitude; where that could turn a group's
-// scale or a code (the two ends of the interval round apart), the warp forms the
-// elements in doubt again, exactly enough (about one unit of four heads in a
-// hundred has one).  Values are exact
+// scale or a code (the two ends of the interval round apart), the unit goes on the
+// warp's list (about one unit of four heads in fifty), and the warp forms its
+// elements in doubt again, exactly enough, when its tokens are done.  (Called
+// where the doubt arises, that code cost every unit its registers: 4096 tokens
+// into an fp4 cache and back 55 us, without any of it 39.)  Values are exact
 // inputs: their quotients are brought to the tie or off it by the sign of the
 // exact remainder.
 #pragma once
@@ -45,6 +47,7 @@ namespace gqa {
 constexpr int kWriteThreads = 256;
 constexpr int kWriteWarps = kWriteThreads / 32;
 constexpr int kWriteUnits = 12;  // units of 4 heads in a token: q 0..7, k 8..9, v 10..11
+constexpr int kWriteDoubts = 32;  // units a warp's list holds
 constexpr int kWriteQUnits = kHq / 4, kWriteKUnits = kHkv / 4;
 
 struct WriteParams {
@@ -160,12 +163,15 @@ __device__ __forceinline__ float quotient_to_round(float x, float inv, float sh,
   return m + fminf(fmaxf(d, -t), t);
 }
 
-// A double as the FP32 number that rounds to any narrower format as the double
-// does: cut off, with the last bit set where something was lost (rounding to
-// odd; a narrow format's ties end in zeros).
-__device__ __forceinline__ float double_to_round(double t) {
-  const float f = __double2float_rz(t);
-  return (double)f != t ? __uint_as_float(__float_as_uint(f) | 1u) : f;
+// The same for x and S known as double-float pairs (x to about 2^-44 of itself):
+// at a midpoint the sign of the remainder decides.
+__device__ __forceinline__ float quotient_to_round(Float2 x, float inv, Float2 S) {
+  const float q = x.hi * inv;
+  const float m = __uint_as_float((__float_as_uint(q) + 0x40u) & ~0x7fu);
+  const Float2 ms = df_mul(Float2{m, 0.f}, S);
+  const float d = df_add(x, Float2{-ms.hi, -ms.lo}).hi;
+  const float t = fabsf(m) * 0x1p-20f;
+  return d > 0.f ? m + t : (d < 0.f ? m - t : m);
 }
 
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
@@ -213,30 +219,52 @@ __device__ __forceinline__ void key_codes(const float (&z)[8], float e, uint32_t
   unsure = (codes ^ to_e2m1x8(down)) & 0x77777777u;  // (a zero of either sign is the same value)
 }
 
+// sin and cos of `turn` * 2 pi / 2^64 as double-float pairs, within about 2^-46.
+__device__ __forceinline__ void sincos_turn_exact(uint64_t turn, Float2& s, Float2& c) {
+  const uint32_t quad = (uint32_t)((turn + (1ull << 61)) >> 62);
+  const int64_t r = (int64_t)(turn - ((uint64_t)quad << 62));
+  const float hi = (float)(int32_t)(r >> 32);
+  const float lo = (float)(r - ((int64_t)(int32_t)hi << 32)) * 0x1p-32f;
+  constexpr Float2 kUnit = df_const(1.4629180792671596e-09);  // 2 pi / 2^32
+  Float2 sx, cx;
+  sincos_reduced(df_mul(fast_two_sum(hi, lo), kUnit), sx, cx);
+  s = quad & 1u ? cx : sx;
+  c = quad & 1u ? sx : cx;
+  if (quad & 2u) s = Float2{-s.hi, -s.lo};
+  if ((quad + 1u) & 2u) c = Float2{-c.hi, -c.lo};
+}
+__device__ __forceinline__ Float2 df_scale(float a, Float2 b) { return df_mul(Float2{a, 0.f}, b); }
+
 // One unit of four key heads whose rounding FP32 could not decide: the elements
-// in doubt, and nothing else, are formed again to about 2^-45 (the norm in
-// double-float, the angle's series in double-float, the rest in FP64).
+// in doubt, and nothing else, are formed again in double-float arithmetic, to
+// about 2^-43 of the head's largest.  (FP64 would do, at many times the latency.)
 template <int QF>
-__device__ __noinline__ void key_codes_exact(const WriteParams& p, int n, const uint4& wlo, const uint4& whi,
+__device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, const uint4& wlo, const uint4& whi,
                                              const float (&zl)[8], const float (&zh)[8], float gl, float gh, float e,
                                              KeyCodes& out) {
   const int idx = threadIdx.x & 7;
   float yl[8], yh[8];
   unpack8<QF>(wlo, yl);
   unpack8<QF>(whi, yh);
-  double r = 1.0;
+  Float2 r = {1.f, 0.f};
   if (p.k_norm_w) {
-    Float2 acc = {0.f, 0.f};  // (squares of 16-bit elements are exact)
+    Float2 acc[4] = {};  // (squares of 16-bit elements are exact)
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      acc = df_add(acc, Float2{yl[i] * yl[i], 0.f});
-      acc = df_add(acc, Float2{yh[i] * yh[i], 0.f});
+      acc[i & 3] = df_add(acc[i & 3], Float2{yl[i] * yl[i], 0.f});
+      acc[i & 3] = df_add(acc[i & 3], Float2{yh[i] * yh[i], 0.f});
     }
+    Float2 ss = df_add(df_add(acc[0], acc[1]), df_add(acc[2], acc[3]));
+#pragma unroll
     for (int off = 4; off > 0; off >>= 1)
-      acc = df_add(acc, Float2{__shfl_xor_sync(0xffffffffu, acc.hi, off), __shfl_xor_sync(0xffffffffu, acc.lo, off)});
-    const double ss = ((double)acc.hi + (double)acc.lo) * (1.0 / kD) + (double)p.eps;
-    r = (double)rsqrtf((float)ss);  // and two Newton steps: 2^-22, 2^-43, below 2^-50
-    r = fma(r * 0.5, fma(-ss * r, r, 1.0), r);
-    r = fma(r * 0.5, fma(-ss * r, r, 1.0), r);
+      ss = df_add(ss, Float2{__shfl_xor_sync(0xffffffffu, ss.hi, off), __shfl_xor_sync(0xffffffffu, ss.lo, off)});
+    ss = df_add(Float2{ss.hi * (1.f / kD), ss.lo * (1.f / kD)}, Float2{p.eps, 0.f});
+    // 1 / sqrt(ss) = r0 (1 - h)^(-1/2), h = 1 - ss r0^2 about 2^-21: to h^2
+    const float r0 = rsqrtf(ss.hi);
+    const float rr = r0 * r0;
+    const Float2 t = df_mul(ss, Float2{rr, fmaf(r0, r0, -rr)});
+    const float h = (1.f - t.hi) - t.lo;
+    r = fast_two_sum(r0, r0 * fmaf(0.375f * h, h, 0.5f * h));
     float wl[8], wh[8];
     unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 8 * idx), wl);
     unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 64 + 8 * idx), wh);
@@ -246,46 +274,56 @@ __device__ __noinline__ void key_codes_exact(const WriteParams& p, int n, const 
       yh[i] *= wh[i];
     }
   }
-  const auto exact = [&](int i, double& lo, double& hi) {
+  const auto exact = [&](int i, Float2& lo, Float2& hi) {
     const int a = 8 * idx + i;
     const int64_t pos = __ldg(p.positions + (size_t)p.axis[a] * p.tokens + n);
-    Float2 sv, cv;  // the angle's part of a turn, in [-pi, pi)
-    sincos_series((double)(int64_t)((uint64_t)pos * p.turns[a]) * 3.4061215800865545e-19, sv, cv);  // 2 pi / 2^64
-    const double s = (double)sv.hi + (double)sv.lo, c = (double)cv.hi + (double)cv.lo;
-    const double u = (double)yl[i] * r, v = (double)yh[i] * r;
-    lo = u * c - v * s;
-    hi = v * c + u * s;
+    Float2 s, c;
+    sincos_turn_exact((uint64_t)pos * p.turns[a], s, c);
+    const Float2 us = df_scale(yl[i], s), vs = df_scale(yh[i], s);
+    lo = df_mul(r, df_add(df_scale(yl[i], c), Float2{-vs.hi, -vs.lo}));
+    hi = df_mul(r, df_add(df_scale(yh[i], c), us));
   };
-  const double ks = (double)p.k_scale;
-  const float inv6 = 1.f / (6.f * p.k_scale);
+  const auto larger = [](Float2 a, Float2 b) {  // the larger magnitude, as a pair >= 0
+    if (b.hi < 0.f) b = Float2{-b.hi, -b.lo};
+    return b.hi > a.hi || (b.hi == a.hi && b.lo > a.lo) ? b : a;
+  };
+  const auto of_pair = [&](Float2 a) {  // the larger of the two lanes that share a group
+    return larger(a, Float2{__shfl_xor_sync(0xffffffffu, a.hi, 1), __shfl_xor_sync(0xffffffffu, a.lo, 1)});
+  };
+  const float ks = p.k_scale, k6 = 6.f * ks, inv6 = 1.f / k6;
   // scales in doubt: from the exact values of the elements that could be the largest
   const bool sure_l = key_scale(gl, e, inv6, out.slo), sure_h = key_scale(gh, e, inv6, out.shi);
   if (!__all_sync(0xffffffffu, sure_l && sure_h)) {
-    double al = 0.0, ah = 0.0;
+    Float2 al = {0.f, 0.f}, ah = {0.f, 0.f};
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       const bool nl = !sure_l && fabsf(zl[i]) >= gl - 2.f * e, nh = !sure_h && fabsf(zh[i]) >= gh - 2.f * e;
       if (!__any_sync(0xffffffffu, nl || nh)) continue;
-      double lo, hi;
+      Float2 lo, hi;
       exact(i, lo, hi);
-      if (nl) al = fmax(al, fabs(lo));
-      if (nh) ah = fmax(ah, fabs(hi));
+      if (nl) al = larger(al, lo);
+      if (nh) ah = larger(ah, hi);
     }
-    al = fmax(al, __shfl_xor_sync(0xffffffffu, al, 1));
-    ah = fmax(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
-    if (!sure_l) out.slo = to_e4m3x2(double_to_round(al / (6.0 * ks)), 0.f) & 0xffu;
-    if (!sure_h) out.shi = to_e4m3x2(double_to_round(ah / (6.0 * ks)), 0.f) & 0xffu;
+    al = of_pair(al);
+    ah = of_pair(ah);
+    const Float2 S = {k6, fmaf(6.f, ks, -k6)};
+    const uint32_t two = to_e4m3x2(quotient_to_round(al, inv6, S), quotient_to_round(ah, inv6, S));
+    if (!sure_l) out.slo = two & 0xffu;
+    if (!sure_h) out.shi = two >> 8;
   }
   uint32_t ul, uh;
-  key_codes(zl, e, out.slo, p.k_scale, out.lo, ul);
-  key_codes(zh, e, out.shi, p.k_scale, out.hi, uh);
-  const double sl = (double)e4m3_value(out.slo) * ks, sh = (double)e4m3_value(out.shi) * ks;
+  key_codes(zl, e, out.slo, ks, out.lo, ul);
+  key_codes(zh, e, out.shi, ks, out.hi, uh);
+  const float vl = e4m3_value(out.slo), vh = e4m3_value(out.shi), sl = vl * ks, sh = vh * ks;
+#pragma unroll 1
   for (int i = 0; i < 8; ++i) {
     const uint32_t mask = 0xfu << (4 * i);
     if (!__any_sync(0xffffffffu, ((ul | uh) & mask) != 0u)) continue;
-    double lo, hi;
+    Float2 lo, hi;
     exact(i, lo, hi);
-    // (an exact tie's quotient is exact)
-    float q[8] = {sl > 0.0 ? double_to_round(lo / sl) : 0.f, sh > 0.0 ? double_to_round(hi / sh) : 0.f};
+    float q[8] = {};
+    if (sl > 0.f) q[0] = quotient_to_round(lo, 1.f / sl, Float2{sl, fmaf(vl, ks, -sl)});
+    if (sh > 0.f) q[1] = quotient_to_round(hi, 1.f / sh, Float2{sh, fmaf(vh, ks, -sh)});
     const uint32_t c = to_e2m1x8(q);
     out.lo = (out.lo & ~mask) | ((c & 0xfu) << (4 * i));
     out.hi = (out.hi & ~mask) | (((c >> 4) & 0xfu) << (4 * i));
@@ -401,29 +439,49 @@ __device__ __forceinline__ uint2 e4m3_8(const float (&x)[8], float inv) {
                     to_e4m3x2(x[4] * inv, x[5] * inv) | (to_e4m3x2(x[6] * inv, x[7] * inv) << 16));
 }
 
-// One unit of four cache rows (KV heads 4u .. 4u + 3 of `plane`) to row `row`.
+// The largest |z| of a lane's two groups, and the bound of the error of its
+// head's z.
+__device__ __forceinline__ void key_bounds(const float (&zl)[8], const float (&zh)[8], float& gl, float& gh, float& e) {
+  gl = amax8(zl);
+  gh = amax8(zh);
+  gl = fmaxf(gl, __shfl_xor_sync(0xffffffffu, gl, 1));
+  gh = fmaxf(gh, __shfl_xor_sync(0xffffffffu, gh, 1));
+  e = fmaxf(gl, gh);
+  e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
+  e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4)) * kKeyError;
+}
+
+__device__ __forceinline__ void store_e2m1(const WriteParams& p, size_t row, int idx, const KeyCodes& k) {
+  uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kv_row_bytes(kKvE2M1);
+  *reinterpret_cast<uint32_t*>(dst + 4 * idx) = k.lo;
+  *reinterpret_cast<uint32_t*>(dst + 32 + 4 * idx) = k.hi;
+  if ((idx & 1) == 0) {
+    uint8_t* sc = static_cast<uint8_t*>(p.kv_scales) + row * scale_row_bytes(kKvE2M1) + (idx >> 1);
+    sc[0] = (uint8_t)k.slo;
+    sc[4] = (uint8_t)k.shi;
+  }
+}
+
+// One unit of four cache rows (KV heads 4u .. 4u + 3 of `plane`) to row `row`;
+// true if it holds an e2m1 key in doubt.
 template <int KVF, int QF>
-__device__ __forceinline__ void store_unit(const WriteParams& p, int n, int plane, size_t row, int idx, bool ok,
+__device__ __forceinline__ bool store_unit(const WriteParams& p, int plane, size_t row, int idx, bool ok,
                                            const uint4& wlo, const uint4& whi, const float (&xl)[8],
                                            const float (&xh)[8]) {
+  bool doubt = false;  // (warp-uniform)
   uint8_t* dst = static_cast<uint8_t*>(p.kv) + row * kv_row_bytes(KVF);
   if constexpr (KVF == kKvE2M1) {
     KeyCodes k;
     if (plane == 0) {
-      const float al = amax8(xl), ah = amax8(xh);
-      const float gl = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, 1));
-      const float gh = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
-      float e = fmaxf(gl, gh);
-      e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
-      e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4)) * kKeyError;
+      float gl, gh, e;
+      key_bounds(xl, xh, gl, gh, e);
       const float inv6 = 1.f / (6.f * p.k_scale);
       bool sure = key_scale(gl, e, inv6, k.slo);
       sure &= key_scale(gh, e, inv6, k.shi);
       uint32_t ul, uh;
       key_codes(xl, e, k.slo, p.k_scale, k.lo, ul);
       key_codes(xh, e, k.shi, p.k_scale, k.hi, uh);
-      if (!__all_sync(0xffffffffu, sure && (ul | uh) == 0u))
-        key_codes_exact<QF>(p, n, wlo, whi, xl, xh, gl, gh, e, k);
+      doubt = !__all_sync(0xffffffffu, sure && (ul | uh) == 0u);
     } else {
       // values are the inputs themselves: exact
       const float al = amax8(xl), ah = amax8(xh);
@@ -443,54 +501,84 @@ __device__ __forceinline__ void store_unit(const WriteParams& p, int n, int plan
         (half ? k.hi : k.lo) = to_e2m1x8(q);
       }
     }
-    if (!ok) return;
-    *reinterpret_cast<uint32_t*>(dst + 4 * idx) = k.lo;
-    *reinterpret_cast<uint32_t*>(dst + 32 + 4 * idx) = k.hi;
-    if ((idx & 1) == 0) {
-      uint8_t* sc = static_cast<uint8_t*>(p.kv_scales) + row * scale_row_bytes(KVF) + (idx >> 1);
-      sc[0] = (uint8_t)k.slo;
-      sc[4] = (uint8_t)k.shi;
-    }
+    if (ok) store_e2m1(p, row, idx, k);
   } else if constexpr (KVF == kKvI8) {
     uint2 lo, hi;
     uint16_t scale;
     int8_row(xl, xh, lo, hi, scale);
-    if (!ok) return;
+    if (!ok) return false;
     *reinterpret_cast<uint2*>(dst + 8 * idx) = lo;
     *reinterpret_cast<uint2*>(dst + 64 + 8 * idx) = hi;
     if (idx == 0) static_cast<uint16_t*>(p.kv_scales)[row] = scale;
   } else if constexpr (KVF == kKvE4M3) {
-    if (!ok) return;
+    if (!ok) return false;
     const float inv = plane == 0 ? p.k_inv_scale : p.v_inv_scale;
     *reinterpret_cast<uint2*>(dst + 8 * idx) = e4m3_8(xl, inv);
     *reinterpret_cast<uint2*>(dst + 64 + 8 * idx) = e4m3_8(xh, inv);
   } else {
-    if (!ok) return;
+    if (!ok) return false;
     *reinterpret_cast<uint4*>(dst + 16 * idx) = plane == 0 ? round8<QF>(xl) : wlo;
     *reinterpret_cast<uint4*>(dst + 128 + 16 * idx) = plane == 0 ? round8<QF>(xh) : whi;
+  }
+  return doubt;
+}
+
+// This lane's eight cosines and sines of token n; turn and axis: its own two
+// angles'.
+__device__ __forceinline__ void token_angles(const WriteParams& p, int n, const uint64_t (&turn)[2], const int (&axis)[2],
+                                             float (&cs)[8], float (&sn)[8]) {
+  float c2[2], s2[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int pos = __ldg(p.positions + (size_t)axis[j] * p.tokens + n);
+    sincos_turn((uint64_t)(int64_t)pos * turn[j], s2[j], c2[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int from = (j >> 1) * 8 + (threadIdx.x & 7);
+    cs[j] = __shfl_sync(0xffffffffu, c2[j & 1], from);
+    sn[j] = __shfl_sync(0xffffffffu, s2[j & 1], from);
   }
 }
 
 // U: units a warp takes at a time, 4 (parts of a token: q 0..3, q 4..7, k and v)
-// or 1.
+// or 1.  The grid is the CTAs resident at once (2 an SM).
+//
+// Bound by HBM for the 16-bit cache (24 KB a token moved): 8192 tokens take 33.3
+// us, 0.89 of the copy peak; one warp a token with a load at a time took 50, two
+// units at a time 38.6, a CTA for every 8 parts 35-38.  An e2m1 cache adds the
+// rounding of keys and values, about as much arithmetic as the rest.
 template <int KVF, int QF, int U>
 __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kParts = kWriteUnits / U;
+  __shared__ int2 lists[KVF == kKvE2M1 ? kWriteWarps : 1][KVF == kKvE2M1 ? kWriteDoubts : 1];
+  [[maybe_unused]] int2* list = lists[KVF == kKvE2M1 ? threadIdx.x >> 5 : 0];
   static_assert(kWriteQUnits % U == 0 && (U == 1 || U == kWriteUnits - kWriteQUnits), "whole parts");
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, quarter = lane >> 3, idx = lane & 7;
-  // this lane's two angles
+  // this lane's two angles, by way of shared memory (lanes that read different
+  // words of the parameters are served one by one)
+  __shared__ uint64_t turns[kD / 2];
+  __shared__ uint8_t axes[kD / 2];
+  if (threadIdx.x < kD / 2) {
+    turns[threadIdx.x] = p.turns[threadIdx.x];
+    axes[threadIdx.x] = p.axis[threadIdx.x];
+  }
+  __syncthreads();
   uint64_t turn[2];
   int axis[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    turn[j] = p.turns[8 * idx + 2 * quarter + j];
-    axis[j] = p.axis[8 * idx + 2 * quarter + j];
+    turn[j] = turns[8 * idx + 2 * quarter + j];
+    axis[j] = axes[8 * idx + 2 * quarter + j];
   }
   pdl_wait_prior_grid();
   const long long items = (long long)p.tokens * kParts;
   const int step = gridDim.x * kWriteWarps;
-  for (long long it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5); it < items; it += step) {
+  long long it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
+  [[maybe_unused]] int doubts = 0;  // units on this warp's list
+  do {
+  for (; it < items && (KVF != kKvE2M1 || doubts <= kWriteDoubts - kWriteKUnits); it += step) {
     const int n = (int)(it / kParts), u0 = (int)(it - (long long)n * kParts) * U;
     uint4 wlo[U], whi[U];
 #pragma unroll
@@ -509,19 +597,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
 
     // the token's angles (not needed by its values)
     float cs[8], sn[8];
-    if (u0 < kWriteQUnits + kWriteKUnits) {
-      float c2[2], s2[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int pos = __ldg(p.positions + (size_t)axis[j] * p.tokens + n);
-        sincos_turn((uint64_t)(int64_t)pos * turn[j], s2[j], c2[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        cs[j] = __shfl_sync(0xffffffffu, c2[j & 1], (j >> 1) * 8 + idx);
-        sn[j] = __shfl_sync(0xffffffffu, s2[j & 1], (j >> 1) * 8 + idx);
-      }
-    }
+    if (u0 < kWriteQUnits + kWriteKUnits) token_angles(p, n, turn, axis, cs, sn);
     if (u0 < kWriteQUnits) {
       Coefs qc;
       make_coefs<QF>(p.q_norm_w, idx, cs, sn, qc);
@@ -544,7 +620,10 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
         float zl[8], zh[8];
         rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
-        store_unit<KVF, QF>(p, n, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh);
+        if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh)) {
+          if (lane == 0) list[doubts] = make_int2(n, u0 + i - kWriteQUnits);
+          ++doubts;
+        }
       }
     }
     if (u0 + U > kWriteQUnits + kWriteKUnits) {
@@ -554,10 +633,32 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         float xl[8], xh[8];
         unpack8<QF>(wlo[i], xl);
         unpack8<QF>(whi[i], xh);
-        store_unit<KVF, QF>(p, n, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo[i], whi[i], xl, xh);
+        store_unit<KVF, QF>(p, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo[i], whi[i], xl, xh);
       }
     }
   }
+  if constexpr (KVF == kKvE2M1) {
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < doubts; ++i) {  // the same lanes write the same bytes again
+      const int n = list[i].x, g = 4 * list[i].y + quarter;
+      const RowAt at = locate(p, n);
+      const uint4* s4 = reinterpret_cast<const uint4*>(p.k_proj + n * p.k_stride + g * kD + 8 * idx);
+      const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+      float cs[8], sn[8], zl[8], zh[8], gl, gh, e;
+      token_angles(p, n, turn, axis, cs, sn);
+      Coefs kc;
+      make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+      rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
+      key_bounds(zl, zh, gl, gh, e);
+      KeyCodes k;
+      key_codes_exact<QF>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
+      if (at.ok) store_e2m1(p, at.base + g * at.head, idx, k);
+    }
+    doubts = 0;
+    __syncwarp();
+  }
+  } while (it < items);
 }
 
 }  // namespace gqa

@@ -286,6 +286,20 @@ def test_many_keys_are_rounded_as_the_exact_ones():
     check_write(t, torch.bfloat16, "e2m1", 1, 6000, section=(24, 20, 20), interleaved=True, ks=10 / 1024, vs=9 / 1024)
 
 
+def test_every_key_in_doubt():
+    # position 0 without a norm: z = x, and every code is a tie.  More tokens than a
+    # warp's list of units in doubt holds (32, for about 33 units a warp here)
+    n = 40000
+    t = tokens(n, 1, n, torch.bfloat16, seed=26)
+    t["pos"] = torch.zeros(n, dtype=torch.int32, device=DEV)
+    level = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], device=DEV)
+    x = level[torch.randint(0, 8, (n, HKV, D), generator=gen(3), device=DEV)]
+    x = x * torch.where(torch.rand((n, HKV, D), generator=gen(4), device=DEV) < 0.5, -1.0, 1.0)
+    x[..., ::16] = 6.0
+    t["k"] = x.to(torch.bfloat16)
+    check_write(t, torch.bfloat16, "e2m1", 1, n, norm=False)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
 @pytest.mark.parametrize("page", [0, 16])
 @pytest.mark.parametrize("n", [20, 2500])
