@@ -73,6 +73,7 @@ def _declare(lib):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    lib.addresses = {name: ctypes.cast(getattr(lib, name), p).value for name in sig}  # for the native binding
     return lib
 
 
@@ -91,6 +92,11 @@ def load(path: str | None = None):
                 return lib
             _lib = lib
         return _lib
+
+
+def address(name: str) -> int:
+    """Address of a function of the loaded library."""
+    return (_lib or load()).addresses[name]
 
 
 def check(status: int) -> None:

@@ -21,6 +21,13 @@ import torch
 from . import _lib
 from ._lib import GqaError
 
+try:  # the native binding (built by build.build_native); without it every call takes the paths below
+    from . import _native
+    if _native.torch_version != torch.__version__:
+        _native = None
+except ImportError:
+    _native = None
+
 HQ, HKV, D = 32, 8, 128
 F16, BF16 = 0, 1
 KV_F16, KV_BF16, KV_E4M3, KV_I8, KV_E2M1 = 0, 1, 2, 3, 4
@@ -245,8 +252,20 @@ def prepare(tensors: dict, q_scale: float = 1.0, num_splits=None, k_scale=None, 
                     float(k_scale), float(v_scale), S, kv_scales if kvf in (KV_I8, KV_E2M1) else None)
 
 
+def _result(done):
+    """A native call's answer: its output, or a status that is not GQA_OK."""
+    if isinstance(done, int):
+        _lib.check(done)
+    return done
+
+
 def launch(p: Prepared) -> torch.Tensor:
     """Run both stages on the current stream: no allocation, no host read."""
+    if _native is not None and p.kv_format == KV_E2M1:
+        done = _native.attend(_lib.address("gqa_decode_fp4kv"), 0, p.q, p.kv, None, p.lens, p.out, p.kv_scales,
+                              p.workspace, p.num_splits, p.q_scale, p.k_scale, p.v_scale)
+        if done is not None:
+            return _result(done)
     lib = _lib.load()
     with _current(p.q.device):
         st = _stream(p.q.device)
@@ -337,6 +356,11 @@ def gqa_decode_fp4kv(q, kv, kv_scales, sequence_lengths, k_scale: float = 1.0, v
     the e2m1 codes of dims 2j (low nibble) and 2j + 1; kv_scales e4m3 (uint8 or
     float8_e4m3fn) [batch, 2, 8, capacity, 8], one for each 16 dims; k_scale and
     v_scale multiply all keys and all values.  fp16/bf16 q and out."""
+    if _native is not None:
+        done = _native.attend(_lib.address("gqa_decode_fp4kv"), 0, q, kv, None, sequence_lengths, out, kv_scales,
+                              workspace, num_splits, q_scale, k_scale, v_scale)
+        if done is not None:
+            return _result(done)
     B, C = _geometry(q, kv, sequence_lengths)
     if _kv_format(kv, "kv", B) != KV_E2M1:
         raise ValueError("gqa_decode_fp4kv takes a uint8 cache [batch, 2, 8, capacity, 64]")
@@ -365,6 +389,11 @@ def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float 
     e2m1: uint8 [.., page_size, 64] with kv_scales e4m3 [.., page_size, 8]),
     block_table int32 [batch, max_pages]; q [batch, 32, 128], or [batch, T, 32, 128]
     for a verify window of T = 1..4 tokens; returns out (q's shape)."""
+    if _native is not None:
+        done = _native.attend(_lib.address("gqa_decode_paged"), 2, q, kv_pages, block_table, sequence_lengths, out,
+                              kv_scales, workspace, num_splits, q_scale, k_scale, v_scale)
+        if done is not None:
+            return _result(done)
     _require(q, "q", None, (torch.float16, torch.bfloat16))
     B = q.shape[0]
     if q.dim() == 3 and q.shape[1:] == (HQ, D):
@@ -403,6 +432,11 @@ def gqa_decode_verify(q, kv, sequence_lengths, q_scale: float = 1.0, k_scale: fl
     """Verify window: q [batch, T, 32, 128] (T = 1..4 draft tokens, the last T slots
     of each cache row); query j attends slots [0, len - T + j].  Any KV format
     (int8 and e2m1 need kv_scales).  Returns out [batch, T, 32, 128]."""
+    if _native is not None:
+        done = _native.attend(_lib.address("gqa_decode_verify"), 1, q, kv, None, sequence_lengths, out, kv_scales,
+                              workspace, num_splits, q_scale, k_scale, v_scale)
+        if done is not None:
+            return _result(done)
     _require(q, "q", None, (torch.float16, torch.bfloat16))
     if q.dim() != 4 or q.shape[2:] != (HQ, D):
         raise ValueError(f"q must be [batch, T, {HQ}, {D}], got {tuple(q.shape)}")
@@ -584,6 +618,12 @@ def write_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots,
     the 64 rotary angles, in blocks or interleaved.  q_norm_w and k_norm_w None:
     no norm.  kv of any format (e2m1: uint8 [.., 64] with e4m3 kv_scales
     [.., 8]).  Returns q_out [tokens, 32, 128]."""
+    if _native is not None:
+        done = _native.write(_lib.address("gqa_write_kv"), False, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
+                             rows, slots, kv, None, q_out, mrope_section, mrope_interleaved, eps, rope_theta,
+                             k_scale, v_scale, kv_scales, workspace)
+        if done is not None:
+            return _result(done)
     return _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv, None, False, q_out,
                   mrope_section, mrope_interleaved, eps, rope_theta, k_scale, v_scale, kv_scales, workspace)
 
@@ -595,6 +635,12 @@ def write_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, 
     """write_kv on a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
     its scale pages), block_table int32 [batch, max_pages]; slot s of row b is
     row s % page_size of page block_table[b, s // page_size]."""
+    if _native is not None:
+        done = _native.write(_lib.address("gqa_write_kv_paged"), True, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
+                             rows, slots, kv_pages, block_table, q_out, mrope_section, mrope_interleaved, eps, rope_theta,
+                             k_scale, v_scale, kv_scales, workspace)
+        if done is not None:
+            return _result(done)
     return _write(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots, kv_pages, block_table, True,
                   q_out, mrope_section, mrope_interleaved, eps, rope_theta, k_scale, v_scale, kv_scales, workspace)
 
@@ -644,6 +690,11 @@ def read_kv(kv, sequence_lengths, starts=None, out=None, dtype=None, k_scale: fl
     fp16 or bf16, into out [batch, 2, 8, out_capacity, 128] from slot 0 on; the
     rest of out keeps what it holds (a new one, of the cache's capacity and of
     ``dtype``, is not initialised).  starts None: 0."""
+    if _native is not None:
+        done = _native.read(_lib.address("gqa_read_kv"), False, kv, None, sequence_lengths, starts, out, dtype, k_scale,
+                            v_scale, kv_scales, workspace)
+        if done is not None:
+            return _result(done)
     return _read(kv, None, False, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales, workspace)
 
 
@@ -651,6 +702,11 @@ def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None
                   v_scale: float = 1.0, kv_scales=None, workspace=None):
     """read_kv from a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
     its scale pages), block_table int32 [batch, max_pages]."""
+    if _native is not None:
+        done = _native.read(_lib.address("gqa_read_kv_paged"), True, kv_pages, block_table, sequence_lengths, starts, out, dtype, k_scale,
+                            v_scale, kv_scales, workspace)
+        if done is not None:
+            return _result(done)
     return _read(kv_pages, block_table, True, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales,
                  workspace)
 

@@ -61,3 +61,33 @@ def build_checked(force: bool = False, verbose: bool = False) -> str:
     subprocess.run(cmd, check=True)
     os.replace(tmp, CHECKED_LIB_PATH)
     return CHECKED_LIB_PATH
+
+
+NATIVE_SRC = os.path.join(PKG, "csrc", "binding.cpp")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
+
+
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """The native binding of the cache write and read-back calls (a CPython
+    extension against the installed torch's headers, compiled with g++)."""
+    import sysconfig
+
+    import torch
+
+    if not force and os.path.exists(NATIVE_PATH):
+        newest = max(os.path.getmtime(s) for s in (NATIVE_SRC, os.path.join(INCLUDE, "gqa_decode.h")))
+        if os.path.getmtime(NATIVE_PATH) >= newest:
+            return NATIVE_PATH
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    includes = [INCLUDE, os.path.join(home, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DGQA_TORCH_VERSION="{torch.__version__}"', *("-I" + i for i in includes), NATIVE_SRC, "-o", tmp, "-L" + lib,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, NATIVE_PATH)
+    return NATIVE_PATH

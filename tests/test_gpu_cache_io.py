@@ -611,3 +611,59 @@ def test_no_tokens_and_refusals():
         gq.read_kv(kv, lens, out=kv)
     with pytest.raises(TypeError):
         gq.read_kv_paged(kv, None, lens)
+
+
+def test_the_native_binding_and_the_interpreted_one_are_alike(monkeypatch):
+    assert api._native is not None, "the native binding is not built"
+    t = tokens(37, 2, 64, torch.bfloat16, seed=30, fused=True, axes=3)
+    table, units = page_table(2, 64, 16)
+    lens = torch.tensor([64, 33], dtype=torch.int32, device=DEV)
+    calls = []
+    real = api._native
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*a):
+                r = getattr(real, name)(*a)
+                calls.append((name, r is not None))
+                return r
+            return call
+
+    got = []
+    for native in (Spy(), None):
+        monkeypatch.setattr(api, "_native", native)
+        for paged in (False, True):
+            kv, sc = new_cache("e2m1", units if paged else 2, 16 if paged else 64)
+            how = dict(mrope_section=(24, 20, 20), mrope_interleaved=True, k_scale=0.01, v_scale=0.02, kv_scales=sc)
+            a = (t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"])
+            out = torch.zeros((2, 2, HKV, 64, D), dtype=torch.float16, device=DEV)
+            rd = dict(out=out, k_scale=0.01, v_scale=0.02, kv_scales=sc)
+            if paged:
+                q_out = gq.write_kv_paged(*a, kv, table, **how)
+                gq.read_kv_paged(kv, table, lens, **rd)
+            else:
+                q_out = gq.write_kv(*a, kv, **how)
+                gq.read_kv(kv, lens, **rd)
+            got.append((q_out, kv, sc, out))
+        # a refused call gives the same error either way
+        with pytest.raises(gq.GqaError, match="sum to 64"):
+            gq.write_kv(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"],
+                        new_cache("bf16", 2, 64)[0], mrope_section=(1, 2, 3))
+    assert calls == [("write", True), ("read", True)] * 2 + [("write", True)]
+    for x, y in zip(got[:2], got[2:]):
+        assert all(torch.equal(u, v) for u, v in zip(x, y))
+
+
+def test_a_stream_of_its_own_and_tensors_made_elsewhere():
+    # the call runs on the current stream, whichever stream made its tensors
+    t = tokens(500, 1, 500, torch.bfloat16, seed=31)
+    ref = run_write(t, "bf16", 1, 500)
+    kv = new_cache("bf16", 1, 500)[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms: a call on another stream would pass it
+        q = t["q"] * 1
+        q_out = gq.write_kv(q, t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"], kv)
+    side.synchronize()
+    assert torch.equal(q_out, ref[0]) and torch.equal(kv, ref[1])

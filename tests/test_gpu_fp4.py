@@ -277,3 +277,18 @@ def test_refusals():
         gq.split_stage(p)
     with pytest.raises((ValueError, gq.GqaError)):
         gq.gqa_decode_fp8kv(t["q"], t["kv"], t["lens"], 1.0, 1.0)
+
+
+@pytest.mark.parametrize("T,page", [(1, 0), (3, 0), (1, 32), (2, 32)])
+def test_the_native_binding_and_the_interpreted_one_are_alike(T, page, monkeypatch):
+    assert api._native is not None, "the native binding is not built"
+    t = make(3, 256, [256, 100, T], "bf16", T)
+    native = decode(t, 4, page)[0]
+    calls = []
+    real = api._native
+    monkeypatch.setattr(api, "_native", type("Spy", (), {"attend": lambda self, *a: calls.append(real.attend(*a)) or calls[-1]})())
+    out = torch.empty_like(t["q"])
+    assert torch.equal(decode(t, 4, page, out=out)[0], native)
+    assert len(calls) == 1 and calls[0] is out  # with everything given, the native call is the one that runs
+    monkeypatch.setattr(api, "_native", None)
+    assert torch.equal(decode(t, 4, page)[0], native)
