@@ -328,6 +328,12 @@ int plan_splits(int batch, int capacity, int kv_format, int sm_count) {
     // 10.4 -> 12.6 and 11.1 -> 14.3; bf16 4 x 8192 22.2 -> 20.2 but 24.1 ->
     // 26.1).
     long long s = (long long)std::llround(std::sqrt(6.0 * (double)nmax));
+    // An e2m1 tile brings half the bytes and takes as long to compute, so more
+    // splits pay: about sqrt(16 nmax), 32 at most (one request in a CUDA graph,
+    // us per call, the rule above -> this: 512 tokens 4.4 -> 3.8, 2048 5.0 -> 4.4,
+    // 4096 5.7 -> 5.0, 16384 9.4 -> 8.6, 32768 14.3 -> 12.5, there with 64
+    // splits 14.4).
+    if (kv_format == kKvE2M1) s = std::min(32LL, (long long)std::llround(std::sqrt(16.0 * (double)nmax)));
     const long long wave = slots / units;
     if (s > wave && !(batch >= 8 && capacity >= 4096)) s = wave;
     if (s < 1) s = 1;
@@ -342,7 +348,10 @@ int plan_splits(int batch, int capacity, int kv_format, int sm_count) {
   per = (per + tile - 1) / tile * tile;
   // at least two tiles per split: a one-tile split costs more in fixed
   // prologue/epilogue than it streams (measured on the 1 x 1024 fp16 case)
-  if (per < 2 * tile) per = 2 * tile;
+  // (e2m1: from 4 tiles on a row a one-tile split pays; 256 tokens take 3.4 us in
+  // one split, 3.7 in two)
+  const long long least = kv_format == kKvE2M1 && nmax >= 4 ? tile : 2 * tile;
+  if (per < least) per = least;
   long long s = (capacity + per - 1) / per;
   if (s < 1) s = 1;
   if (s > GQA_MAX_SPLITS) s = GQA_MAX_SPLITS;
