@@ -160,7 +160,7 @@ __device__ __forceinline__ float quotient_to_round(float x, float inv, float sh,
   const float m = __uint_as_float((__float_as_uint(q) + 0x40u) & ~0x7fu);
   const float d = fmaf(-m, sl, fmaf(-m, sh, x)) * (inv * 4096.f);
   const float t = fabsf(m) * 0x1p-20f;
-  return m + fminf(fmaxf(d, -t), t);
+  return fabsf(q) < INFINITY ? m + fminf(fmaxf(d, -t), t) : q;  // (an infinity saturates)
 }
 
 // The same for x and S known as double-float pairs (x to about 2^-44 of itself):

@@ -280,6 +280,20 @@ def test_magnitudes(mag, fmt):
     check_write(t, torch.bfloat16, fmt, 1, 64, norm=True, ks=0.01, vs=0.01)
 
 
+def test_infinite_values_saturate():
+    t = tokens(8, 1, 8, torch.bfloat16, seed=32)
+    t["v"][0, 0, 5], t["v"][1, 3, 100], t["v"][2, 7, 0] = math.inf, -math.inf, 3e38
+    t["v"][2, 7, 1] = 1e4
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, 8, ks=1.0, vs=1.0)
+    got, gsc, _ = rows_at(kv, sc, table, 0, t["rows"], t["slots"])
+    v = inputs.dequantise_e2m1(got[:, 1], gsc[:, 1], 1.0)
+    assert v[0, 0, 5] == 2688 and v[1, 3, 100] == -2688 and v[2, 7, 0] == 2688 and v[2, 7, 1] == 2688
+    finite = torch.isfinite(t["v"].double()).unflatten(-1, (8, 16)).all(-1) & (t["v"].abs().amax(-1) < 1e3)[..., None]
+    want, wsc = inputs.quantise_e2m1(torch.nan_to_num(t["v"].double(), posinf=0, neginf=0), 1.0)
+    assert torch.equal(gsc[:, 1][finite], wsc[finite])
+    assert same_codes(got[:, 1].unflatten(-1, (8, 8))[finite], want.unflatten(-1, (8, 8))[finite])
+
+
 def test_many_keys_are_rounded_as_the_exact_ones():
     # about a hundredth of the units meet a rounding that FP32 cannot decide
     t = tokens(6000, 1, 6000, torch.bfloat16, seed=10, axes=3)
