@@ -45,10 +45,16 @@ cudaError_t launch_write_u(const WriteParams& p, int kvf, int qf, int sms, cudaS
 }
 
 cudaError_t launch_write_kv(const WriteParams& p, int kvf, int qf, int sms, cudaStream_t stream) {
-  // Few tokens (all their units resident at once): a warp for each unit, so that
-  // the call's latency is one unit's.
-  return (long long)p.tokens * kWriteUnits <= 2LL * kWriteWarps * sms ? launch_write_u<1>(p, kvf, qf, sms, stream)
-                                                                      : launch_write_u<4>(p, kvf, qf, sms, stream);
+  // Few tokens: a warp for each unit, so that the call's latency is one unit's, as
+  // long as all are resident at once (202 tokens on 152 SMs), or three times that
+  // where the cache's rounding makes a part of four units long.  In a CUDA graph,
+  // us, units / parts: bf16 64 tokens 2.4 / 2.6, 200 2.5 / 3.1, 256 3.4 / 3.1, 768
+  // 5.6 / 3.5; int8 64 3.0 / 5.0, 512 5.1 / 6.1, 768 6.9 / 5.9; e2m1 64 4.2 / 7.2,
+  // 512 7.1 / 8.5, 768 8.9 / 8.2.
+  const long long waves = kvf == kKvI8 || kvf == kKvE2M1 ? 3 : 1;
+  return (long long)p.tokens * kWriteUnits <= waves * 2 * kWriteWarps * sms
+             ? launch_write_u<1>(p, kvf, qf, sms, stream)
+             : launch_write_u<4>(p, kvf, qf, sms, stream);
 }
 
 // About 64 CTAs an SM (8 waves) over the rows: lengths are on the device, so the

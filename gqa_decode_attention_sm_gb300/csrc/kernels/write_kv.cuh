@@ -546,13 +546,14 @@ __device__ __forceinline__ void token_angles(const WriteParams& p, int n, const 
 //
 // Bound by HBM for the 16-bit cache (24 KB a token moved): 8192 tokens take 33.3
 // us, 0.89 of the copy peak; one warp a token with a load at a time took 50, two
-// units at a time 38.6, a CTA for every 8 parts 35-38.  An e2m1 cache adds the
-// rounding of keys and values, about as much arithmetic as the rest.
+// units at a time 38.6.  An e2m1 cache adds the rounding of keys and values, half
+// as much arithmetic again.
 template <int KVF, int QF, int U>
 __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kParts = kWriteUnits / U;
-  __shared__ int2 lists[KVF == kKvE2M1 ? kWriteWarps : 1][KVF == kKvE2M1 ? kWriteDoubts : 1];
-  [[maybe_unused]] int2* list = lists[KVF == kKvE2M1 ? threadIdx.x >> 5 : 0];
+  constexpr bool kList = KVF == kKvE2M1 && U > 1;
+  __shared__ int2 lists[kList ? kWriteWarps : 1][kList ? kWriteDoubts : 1];
+  [[maybe_unused]] int2* list = lists[kList ? threadIdx.x >> 5 : 0];
   static_assert(kWriteQUnits % U == 0 && (U == 1 || U == kWriteUnits - kWriteQUnits), "whole parts");
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, quarter = lane >> 3, idx = lane & 7;
@@ -577,87 +578,97 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
   const int step = gridDim.x * kWriteWarps;
   long long it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   [[maybe_unused]] int doubts = 0;  // units on this warp's list
+  // the same lanes write the bytes of a unit in doubt again
+  [[maybe_unused]] const auto settle = [&](int n, const RowAt& at, int g, const uint4& wlo, const uint4& whi,
+                                           const float(&zl)[8], const float(&zh)[8]) {
+    float gl, gh, e;
+    key_bounds(zl, zh, gl, gh, e);
+    KeyCodes k;
+    key_codes_exact<QF>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
+    if (at.ok) store_e2m1(p, at.base + g * at.head, idx, k);
+  };
   do {
-  for (; it < items && (KVF != kKvE2M1 || doubts <= kWriteDoubts - kWriteKUnits); it += step) {
-    const int n = (int)(it / kParts), u0 = (int)(it - (long long)n * kParts) * U;
-    uint4 wlo[U], whi[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int u = u0 + i;
-      const uint16_t* src = u < kWriteQUnits ? p.q_proj + n * p.q_stride + u * 4 * kD
-                            : u < kWriteQUnits + kWriteKUnits
-                                ? p.k_proj + n * p.k_stride + (u - kWriteQUnits) * 4 * kD
-                                : p.v_proj + n * p.v_stride + (u - kWriteQUnits - kWriteKUnits) * 4 * kD;
-      const uint4* s4 = reinterpret_cast<const uint4*>(src + quarter * kD + 8 * idx);
-      wlo[i] = __ldg(s4);
-      whi[i] = __ldg(s4 + 8);
-    }
-    RowAt at{0, 0, false};
-    if (u0 + U > kWriteQUnits) at = locate(p, n);
-
-    // the token's angles (not needed by its values)
-    float cs[8], sn[8];
-    if (u0 < kWriteQUnits + kWriteKUnits) token_angles(p, n, turn, axis, cs, sn);
-    if (u0 < kWriteQUnits) {
-      Coefs qc;
-      make_coefs<QF>(p.q_norm_w, idx, cs, sn, qc);
-      uint16_t* dst = p.q_out + ((size_t)n * kHq + 4 * u0 + quarter) * kD + 8 * idx;
+    for (; it < items && (!kList || doubts <= kWriteDoubts - kWriteKUnits); it += step) {
+      const int n = (int)(it / kParts), u0 = (int)(it - (long long)n * kParts) * U;
+      uint4 wlo[U], whi[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        float zl[8], zh[8];
-        rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
-        uint4* d4 = reinterpret_cast<uint4*>(dst + i * 4 * kD);
-        d4[0] = round8<QF>(zl);
-        d4[8] = round8<QF>(zh);
+        const int u = u0 + i;
+        const uint16_t* src = u < kWriteQUnits ? p.q_proj + n * p.q_stride + u * 4 * kD
+                              : u < kWriteQUnits + kWriteKUnits
+                                  ? p.k_proj + n * p.k_stride + (u - kWriteQUnits) * 4 * kD
+                                  : p.v_proj + n * p.v_stride + (u - kWriteQUnits - kWriteKUnits) * 4 * kD;
+        const uint4* s4 = reinterpret_cast<const uint4*>(src + quarter * kD + 8 * idx);
+        wlo[i] = __ldg(s4);
+        whi[i] = __ldg(s4 + 8);
       }
-      continue;
-    }
-    if (u0 < kWriteQUnits + kWriteKUnits) {
-      Coefs kc;
-      make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+      RowAt at{0, 0, false};
+      if (u0 + U > kWriteQUnits) at = locate(p, n);
+
+      // the token's angles (not needed by its values)
+      float cs[8], sn[8];
+      if (u0 < kWriteQUnits + kWriteKUnits) token_angles(p, n, turn, axis, cs, sn);
+      if (u0 < kWriteQUnits) {
+        Coefs qc;
+        make_coefs<QF>(p.q_norm_w, idx, cs, sn, qc);
+        uint16_t* dst = p.q_out + ((size_t)n * kHq + 4 * u0 + quarter) * kD + 8 * idx;
 #pragma unroll
-      for (int i = 0; i < (U == 1 ? 1 : kWriteKUnits); ++i) {
-        const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
-        float zl[8], zh[8];
-        rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
-        if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh)) {
-          if (lane == 0) list[doubts] = make_int2(n, u0 + i - kWriteQUnits);
-          ++doubts;
+        for (int i = 0; i < U; ++i) {
+          float zl[8], zh[8];
+          rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
+          uint4* d4 = reinterpret_cast<uint4*>(dst + i * 4 * kD);
+          d4[0] = round8<QF>(zl);
+          d4[8] = round8<QF>(zh);
+        }
+        continue;
+      }
+      if (u0 < kWriteQUnits + kWriteKUnits) {
+        Coefs kc;
+        make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+#pragma unroll
+        for (int i = 0; i < (U == 1 ? 1 : kWriteKUnits); ++i) {
+          const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
+          float zl[8], zh[8];
+          rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
+          if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh)) {
+            if constexpr (U == 1) {  // (a call of few tokens is as long as its longest unit)
+              settle(n, at, g, wlo[i], whi[i], zl, zh);
+            } else {
+              if (lane == 0) list[doubts] = make_int2(n, u0 + i - kWriteQUnits);
+              ++doubts;
+            }
+          }
+        }
+      }
+      if (u0 + U > kWriteQUnits + kWriteKUnits) {
+#pragma unroll
+        for (int i = U == 1 ? 0 : kWriteKUnits; i < U; ++i) {
+          const int g = 4 * (u0 + i - kWriteQUnits - kWriteKUnits) + quarter;
+          float xl[8], xh[8];
+          unpack8<QF>(wlo[i], xl);
+          unpack8<QF>(whi[i], xh);
+          store_unit<KVF, QF>(p, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo[i], whi[i], xl, xh);
         }
       }
     }
-    if (u0 + U > kWriteQUnits + kWriteKUnits) {
-#pragma unroll
-      for (int i = U == 1 ? 0 : kWriteKUnits; i < U; ++i) {
-        const int g = 4 * (u0 + i - kWriteQUnits - kWriteKUnits) + quarter;
-        float xl[8], xh[8];
-        unpack8<QF>(wlo[i], xl);
-        unpack8<QF>(whi[i], xh);
-        store_unit<KVF, QF>(p, 1, at.base + (kHkv + g) * at.head, idx, at.ok, wlo[i], whi[i], xl, xh);
-      }
-    }
-  }
-  if constexpr (KVF == kKvE2M1) {
-    __syncwarp();
+    if constexpr (kList) {
+      __syncwarp();
 #pragma unroll 1
-    for (int i = 0; i < doubts; ++i) {  // the same lanes write the same bytes again
-      const int n = list[i].x, g = 4 * list[i].y + quarter;
-      const RowAt at = locate(p, n);
-      const uint4* s4 = reinterpret_cast<const uint4*>(p.k_proj + n * p.k_stride + g * kD + 8 * idx);
-      const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
-      float cs[8], sn[8], zl[8], zh[8], gl, gh, e;
-      token_angles(p, n, turn, axis, cs, sn);
-      Coefs kc;
-      make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
-      rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
-      key_bounds(zl, zh, gl, gh, e);
-      KeyCodes k;
-      key_codes_exact<QF>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
-      if (at.ok) store_e2m1(p, at.base + g * at.head, idx, k);
+      for (int i = 0; i < doubts; ++i) {
+        const int n = list[i].x, g = 4 * list[i].y + quarter;
+        const RowAt at = locate(p, n);
+        const uint4* s4 = reinterpret_cast<const uint4*>(p.k_proj + n * p.k_stride + g * kD + 8 * idx);
+        const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+        float cs[8], sn[8], zl[8], zh[8];
+        token_angles(p, n, turn, axis, cs, sn);
+        Coefs kc;
+        make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+        rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
+        settle(n, at, g, wlo, whi, zl, zh);
+      }
+      doubts = 0;
+      __syncwarp();
     }
-    doubts = 0;
-    __syncwarp();
-  }
   } while (it < items);
 }
 

@@ -127,7 +127,7 @@ size_t gqa_decode_workspace_size(int batch, int capacity, int num_splits);
  * KV splits from batch x capacity, the KV format and the SM count of `device`:
  * about 8 waves of (batch, KV head, split) work items over the worst case, or,
  * for latency-bound sizes (at most 16 tiles per resident CTA in all), about
- * sqrt(6 x tiles per row) capped at one wave.  Writes the chosen count
+ * sqrt(6 x tiles per row) (e2m1: sqrt(16 x tiles), 32 at most) capped at one wave.  Writes the chosen count
  * (1..GQA_MAX_SPLITS) to *num_splits_out. */
 gqa_status_t gqa_decode_plan(int batch, int capacity, gqa_kv_format_t kv_format, int device,
                              int* num_splits_out);
