@@ -681,3 +681,69 @@ def test_a_stream_of_its_own_and_tensors_made_elsewhere():
         q_out = gq.write_kv(q, t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"], kv)
     side.synchronize()
     assert torch.equal(q_out, ref[0]) and torch.equal(kv, ref[1])
+
+
+def random_call(seed):
+    """One random write, read back and (e2m1) decoded, each against its definition."""
+    rng = np.random.default_rng(seed)
+    fmt, dtype = FORMATS[rng.integers(len(FORMATS))] if rng.random() < 0.5 else ("e2m1", "bf16")
+    page = int(rng.choice([0, 16, 32, 128]))
+    B = int(rng.integers(1, 6))
+    C = int(np.exp(rng.uniform(np.log(16), np.log(1500))))
+    C = -(-C // (page or 8)) * (page or 8)
+    n = int(min(B * C, np.exp(rng.uniform(0, np.log(4000)))))
+    axes = int(rng.choice([1, 3]))
+    interleaved = bool(rng.random() < 0.5)
+    section = None
+    if axes == 3:
+        h, w = (int(x) for x in rng.integers(0, 22 if interleaved else 33, 2))
+        section = (64 - h - w, h, w)
+    ks, vs = (float(np.float32(x)) for x in np.exp(rng.uniform(-6, -2, 2))) if fmt in SCALES else (1.0, 1.0)
+    t = tokens(n, B, C, TD[dtype], seed=seed, fused=bool(rng.random() < 0.5), axes=axes, mag=float(np.exp(rng.uniform(-3, 3))))
+    t["pos"] = torch.randint(0, 1 << int(rng.integers(1, 23)), t["pos"].shape, generator=gen(seed + 1), device=DEV,
+                             dtype=torch.int64).to(torch.int32)
+    q_out, kv, sc, table = check_write(t, TD[dtype], fmt, B, C, page, section, interleaved, norm=bool(rng.random() < 0.8),
+                                       ks=ks, vs=vs, seed=seed)
+    if fmt == "e2m1":
+        sc.clamp_(max=0x7E)
+    lens = torch.tensor(rng.integers(0, C + 1, B), dtype=torch.int32, device=DEV)
+    starts = torch.tensor([int(rng.integers(0, int(x) + 1)) for x in lens], dtype=torch.int32, device=DEV)
+    want = contiguous(values32(kv, sc, fmt, ks, vs), table)
+    out = torch.full((B, 2, HKV, int(rng.integers(1, C + 9)), D), 3.0, dtype=TD[dtype], device=DEV)
+    ref = out.clone()
+    for b in range(B):
+        s, m = int(starts[b]), min(int(lens[b]) - int(starts[b]), out.shape[3])
+        ref[b, :, :, :m] = want[b, :, :, s:s + m].to(TD[dtype])
+    how = dict(starts=starts, out=out, k_scale=ks, v_scale=vs, kv_scales=sc)
+    got = gq.read_kv_paged(kv, table, lens, **how) if page else gq.read_kv(kv, lens, **how)
+    assert torch.equal(got, ref)
+    if fmt != "e2m1":
+        return
+    T = int(rng.integers(1, 5))
+    q = torch.randn((B, T, HQ, D) if T > 1 else (B, HQ, D), generator=gen(seed + 2), device=DEV).to(TD[dtype])
+    S = int(rng.integers(1, 20))
+    q_scale = float(np.float32(1.0 / max(1.0, float(want[:, 0].square().mean().sqrt()))))  # scores of the order of one
+    sc_kw = dict(k_scale=ks, v_scale=vs, kv_scales=sc, q_scale=q_scale, num_splits=S)
+    if page:
+        o = gq.gqa_decode_paged(q, kv, table, lens, **sc_kw)
+    else:
+        o = gq.gqa_decode_verify(q if T > 1 else q[:, None].contiguous(), kv, lens, **sc_kw).view(q.shape)
+    x = want.double()
+    ref = torch.zeros((B, T, HQ, D), dtype=torch.float64, device=DEV)
+    for b in range(B):
+        for j in range(T):
+            m = int(lens[b]) - T + 1 + j
+            if m > 0:
+                s = torch.einsum("ghd,gtd->ght", q.view(B, T, HQ, D)[b, j].double().view(8, 4, D), x[b, 0, :, :m])
+                ref[b, j] = torch.einsum("ght,gtd->ghd", torch.softmax(s * q_scale / math.sqrt(D), -1),
+                                         x[b, 1, :, :m]).reshape(HQ, D)
+    # half a step of the output; the weights' rounding to fp16 (2^-11 and 2^-25 a
+    # token) and the scores' (2^-13), each of the largest value
+    top = float(x[:, 1].abs().max())
+    bound = ref.abs() * (torch.finfo(o.dtype).eps / 2) + top * (2 ** -11 + C * 2 ** -25 + 2 ** -13) + 2 ** -25
+    assert ((o.view(ref.shape).double() - ref).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_calls(seed):
+    random_call(seed)
