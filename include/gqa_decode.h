@@ -464,7 +464,8 @@ gqa_status_t gqa_write_kv(const void* q_proj, const void* k_proj, const void* v_
 
 /* The same on a paged cache (the layout of gqa_decode_paged; block_table
  * [batch, max_pages_per_seq]): slot s of row b is row s % page_size of page
- * block_table[b][s / page_size].  A block-table entry outside [0, num_pages)
+ * block_table[b][s / page_size] (two tokens of a call must not meet there
+ * either, where rows share a page).  A block-table entry outside [0, num_pages)
  * sets GQA_FLAG_PAGE_CLAMPED and nothing of that token is written to the
  * cache. */
 gqa_status_t gqa_write_kv_paged(const void* q_proj, const void* k_proj, const void* v_proj,
