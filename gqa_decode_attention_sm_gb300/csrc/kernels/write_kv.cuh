@@ -216,7 +216,11 @@ __device__ __forceinline__ void key_codes(const float (&z)[8], float e, uint32_t
     down[i] = fmaf(z[i], inv, -ei);
   }
   codes = to_e2m1x8(up);
-  unsure = (codes ^ to_e2m1x8(down)) & 0x77777777u;  // (a zero of either sign is the same value)
+  const uint32_t low = to_e2m1x8(down);
+  // a zero of either sign is the same value; every other magnitude counts with its
+  // sign (an interval about zero may reach the same code on both sides)
+  const uint32_t nonzero = ((codes | low) & 0x77777777u) + 0x77777777u;  // bit 3 of each nibble
+  unsure = (codes ^ low) & (nonzero | 0x77777777u);
 }
 
 // sin and cos of `turn` * 2 pi / 2^64 as double-float pairs, within about 2^-46.

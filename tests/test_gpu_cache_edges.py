@@ -1,0 +1,50 @@
+"""Cache writes at the edges of their number formats, against their definitions in 64 bits (GPU)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gqa_decode_attention_sm_gb300 as gq
+from gqa_decode_attention_sm_gb300 import inputs
+from test_gpu_cache_io import (D, DEV, HKV, HQ, TD, check_heads, gen, library, new_cache, rotated, rows_at, run_write,
+                               same_codes, tokens)
+
+pytestmark = pytest.mark.gpu
+
+
+def check_e2m1(got, gsc, plane, x, scale):
+    """Codes and scales of one plane against exact x [N, 8, 128]; a group with a NaN has the NaN scale, whatever
+    its codes."""
+    codes, scales = inputs.quantise_e2m1(x, scale)
+    nan = torch.isnan(x).unflatten(-1, (8, 16)).any(-1)
+    assert ((gsc[:, plane] & 0x7F) == 0x7F)[nan].all(), "a NaN is kept as the group's NaN scale"
+    assert torch.equal(gsc[:, plane][~nan], scales[~nan]), f"{int((gsc[:, plane] != scales)[~nan].sum())} scales"
+    a, b = (c.unflatten(-1, (8, 8))[~nan] for c in (got[:, plane], codes))
+    assert same_codes(a, b), f"{int((a != b).sum())} bytes of {a.numel()}"
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [40, 1000])  # keys in doubt settled at once, and from the list
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("sparse", [False, True])
+def test_small_groups_in_large_heads(dtype, n, norm, sparse):
+    """Groups 1 to 2e-6 of their head's largest, with exact zeros and both signs: the FP32 error of the head is then
+    up to several steps of a group's codes.  Sparse: a group holds zeros and both signs of one size alone, whose
+    codes are far from every border but the one between the two signs of a zero.  Positions 0 to 3 (the definition's
+    own angles are then good to 2^-51)."""
+    t = tokens(n, 1, n, TD[dtype], seed=40)
+    t["pos"] = (torch.arange(n, device=DEV) % 4).to(torch.int32)
+    size = torch.tensor([1, 1e-4, 2e-5, 1e-5, 1e-6, 1e-6, 1e-6, 1e-6], device=DEV).repeat_interleave(16)
+    big = 1000.0
+    x = torch.randn((n, HKV, D), generator=gen(41), device=DEV)
+    if sparse:
+        x = torch.sign(x)
+    x = torch.where(torch.rand((n, HKV, D), generator=gen(42), device=DEV) < 0.6, torch.zeros_like(x), x) * size * big
+    x[..., 64:] = 0  # (pairs (i, i + 64) turn into one another)
+    t["k"] = x.to(TD[dtype])
+    t["kw"] = torch.ones_like(t["kw"])
+    ks = float(np.float32((big if not norm else 8.0) / (6 * 448)))
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, n, norm=norm, ks=ks, vs=1.0)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_e2m1(got, gsc, 0, rotated(t["k"], t["kw"] if norm else None, t["pos"]), ks)
