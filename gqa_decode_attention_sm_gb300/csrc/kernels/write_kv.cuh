@@ -180,6 +180,18 @@ __device__ __forceinline__ float amax8(const float (&x)[8]) {
   for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
   return m;
 }
+// The larger of two, NaN if either is (fmaxf drops a NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+__device__ __forceinline__ float amax8_nan(const float (&x)[8]) {
+  float m = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+  return m;
+}
 
 // The bound of |FP32 z - z| as a share of the head's largest |z|, A:
 //   cos and sin within 2^-24, their products with a weight and the one rounded
@@ -197,9 +209,10 @@ struct KeyCodes {
 };
 
 // Scale byte of a group whose largest FP32 |z| is `amax`, within `e` of the exact
-// one; false if the exact one could round to another.
+// one; false if the exact one could round to another.  (An infinite amax gives 448,
+// a NaN the NaN.)
 __device__ __forceinline__ bool key_scale(float amax, float e, float inv6, uint32_t& scale) {
-  const uint32_t two = to_e4m3x2((amax + e) * inv6, fmaxf(amax - e, 0.f) * inv6);
+  const uint32_t two = to_e4m3x2((amax + e) * inv6, max_nan(amax - e, 0.f) * inv6);
   scale = two & 0xffu;
   return scale == (two >> 8);
 }
@@ -329,8 +342,9 @@ __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, con
     if (sl > 0.f) q[0] = quotient_to_round(lo, 1.f / sl, Float2{sl, fmaf(vl, ks, -sl)});
     if (sh > 0.f) q[1] = quotient_to_round(hi, 1.f / sh, Float2{sh, fmaf(vh, ks, -sh)});
     const uint32_t c = to_e2m1x8(q);
-    out.lo = (out.lo & ~mask) | ((c & 0xfu) << (4 * i));
-    out.hi = (out.hi & ~mask) | (((c >> 4) & 0xfu) << (4 * i));
+    // (only what is in doubt: an infinite element has no exact pair)
+    if (ul & mask) out.lo = (out.lo & ~mask) | ((c & 0xfu) << (4 * i));
+    if (uh & mask) out.hi = (out.hi & ~mask) | (((c >> 4) & 0xfu) << (4 * i));
   }
 }
 
@@ -443,16 +457,29 @@ __device__ __forceinline__ uint2 e4m3_8(const float (&x)[8], float inv) {
                     to_e4m3x2(x[4] * inv, x[5] * inv) | (to_e4m3x2(x[6] * inv, x[7] * inv) << 16));
 }
 
-// The largest |z| of a lane's two groups, and the bound of the error of its
-// head's z.
+// The largest |z| of a lane's two groups (NaN with one in them), and the bound of
+// the error of its head's z (not finite where some z is not: see finite_bound).
 __device__ __forceinline__ void key_bounds(const float (&zl)[8], const float (&zh)[8], float& gl, float& gh, float& e) {
-  gl = amax8(zl);
-  gh = amax8(zh);
-  gl = fmaxf(gl, __shfl_xor_sync(0xffffffffu, gl, 1));
-  gh = fmaxf(gh, __shfl_xor_sync(0xffffffffu, gh, 1));
-  e = fmaxf(gl, gh);
-  e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 2));
-  e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, 4)) * kKeyError;
+  gl = amax8_nan(zl);
+  gh = amax8_nan(zh);
+  gl = max_nan(gl, __shfl_xor_sync(0xffffffffu, gl, 1));
+  gh = max_nan(gh, __shfl_xor_sync(0xffffffffu, gh, 1));
+  e = max_nan(gl, gh);
+  e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, 2));
+  e = max_nan(e, __shfl_xor_sync(0xffffffffu, e, 4)) * kKeyError;
+}
+// The bound of the finite z of a head, from the largest of them: a pair is finite
+// only where both its elements are, and its error comes from them alone.
+__device__ __forceinline__ float finite_bound(const float (&zl)[8], const float (&zh)[8]) {
+  float e = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(zl[i]), b = fabsf(zh[i]);
+    e = fmaxf(e, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+  }
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, off));
+  return e * kKeyError;
 }
 
 __device__ __forceinline__ void store_e2m1(const WriteParams& p, size_t row, int idx, const KeyCodes& k) {
@@ -482,15 +509,16 @@ __device__ __forceinline__ bool store_unit(const WriteParams& p, int plane, size
       const float inv6 = 1.f / (6.f * p.k_scale);
       bool sure = key_scale(gl, e, inv6, k.slo);
       sure &= key_scale(gh, e, inv6, k.shi);
+      sure &= e < INFINITY;  // (infinite and NaN keys are settled as those in doubt)
       uint32_t ul, uh;
       key_codes(xl, e, k.slo, p.k_scale, k.lo, ul);
       key_codes(xh, e, k.shi, p.k_scale, k.hi, uh);
       doubt = !__all_sync(0xffffffffu, sure && (ul | uh) == 0u);
     } else {
       // values are the inputs themselves: exact
-      const float al = amax8(xl), ah = amax8(xh);
-      const float gl = fmaxf(al, __shfl_xor_sync(0xffffffffu, al, 1));
-      const float gh = fmaxf(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
+      const float al = amax8_nan(xl), ah = amax8_nan(xh);
+      const float gl = max_nan(al, __shfl_xor_sync(0xffffffffu, al, 1));
+      const float gh = max_nan(ah, __shfl_xor_sync(0xffffffffu, ah, 1));
       const float vs = p.v_scale, d6 = 6.f * vs, d6l = fmaf(6.f, vs, -d6), inv6 = 1.f / d6;
       const uint32_t two = to_e4m3x2(quotient_to_round(gl, inv6, d6, d6l), quotient_to_round(gh, inv6, d6, d6l));
       k.slo = two & 0xffu;
@@ -587,6 +615,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
                                            const float(&zl)[8], const float(&zh)[8]) {
     float gl, gh, e;
     key_bounds(zl, zh, gl, gh, e);
+    if (!__all_sync(0xffffffffu, e < INFINITY)) e = finite_bound(zl, zh);  // (the same where all are finite)
     KeyCodes k;
     key_codes_exact<QF>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
     if (at.ok) store_e2m1(p, at.base + g * at.head, idx, k);

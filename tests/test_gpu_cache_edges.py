@@ -48,3 +48,37 @@ def test_small_groups_in_large_heads(dtype, n, norm, sparse):
     q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, n, norm=norm, ks=ks, vs=1.0)
     got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
     check_e2m1(got, gsc, 0, rotated(t["k"], t["kw"] if norm else None, t["pos"]), ks)
+
+
+@pytest.mark.parametrize("n", [12, 1200])
+@pytest.mark.parametrize("norm", [False, True])
+def test_infinite_keys_saturate_and_nan_is_kept(n, norm):
+    t = tokens(n, 1, n, torch.bfloat16, seed=43)
+    t["pos"] = (1 + torch.arange(n, device=DEV) % 7).to(torch.int32)
+    for k in range(0, n, 12):
+        t["k"][k, 0, 5] = math.inf
+        t["k"][k + 1, 3, 100] = -math.inf
+        t["k"][k + 2, 7, 40] = math.nan
+        t["k"][k + 3, 1, 2], t["k"][k + 3, 1, 66] = math.inf, math.inf  # a pair: inf - inf among them
+        t["k"][k + 4, 2, 1], t["k"][k + 4, 2, 90] = math.nan, math.inf
+        t["k"][k + 5] = math.nan
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, n, norm=norm, ks=10 / 1024, vs=9 / 1024)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_e2m1(got, gsc, 0, rotated(t["k"], t["kw"] if norm else None, t["pos"]), 10 / 1024)
+    check_e2m1(got, gsc, 1, t["v"].double(), 9 / 1024)
+
+
+@pytest.mark.parametrize("n", [12, 1200])
+def test_nan_values_are_kept(n):
+    t = tokens(n, 1, n, torch.bfloat16, seed=44)
+    for k in range(0, n, 12):
+        t["v"][k, 0, 5] = math.nan
+        t["v"][k + 1, 3, 100], t["v"][k + 1, 3, 101] = -math.inf, math.nan
+        t["v"][k + 2, 4] = math.nan
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, n, ks=10 / 1024, vs=9 / 1024)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_e2m1(got, gsc, 0, rotated(t["k"], t["kw"], t["pos"]), 10 / 1024)
+    check_e2m1(got, gsc, 1, t["v"].double(), 9 / 1024)
+    back = gq.read_kv(kv, torch.tensor([n], dtype=torch.int32, device=DEV), k_scale=10 / 1024, v_scale=9 / 1024,
+                      kv_scales=sc)[0, 1].transpose(0, 1)[t["slots"].long()]
+    assert torch.isnan(back[0, 0, :16]).all() and not torch.isnan(back[0, 0, 16:]).any()
