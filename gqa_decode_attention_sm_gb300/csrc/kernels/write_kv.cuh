@@ -160,7 +160,8 @@ __device__ __forceinline__ float quotient_to_round(float x, float inv, float sh,
   const float m = __uint_as_float((__float_as_uint(q) + 0x40u) & ~0x7fu);
   const float d = fmaf(-m, sl, fmaf(-m, sh, x)) * (inv * 4096.f);
   const float t = fabsf(m) * 0x1p-20f;
-  return fabsf(q) < INFINITY ? m + fminf(fmaxf(d, -t), t) : q;  // (an infinity saturates)
+  // (past 2^127, where m may be infinite, every format saturates; a NaN stays one)
+  return fabsf(q) < 0x1p127f ? m + fminf(fmaxf(d, -t), t) : q;
 }
 
 // The same for x and S known as double-float pairs (x to about 2^-44 of itself):

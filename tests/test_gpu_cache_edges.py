@@ -82,3 +82,23 @@ def test_nan_values_are_kept(n):
     back = gq.read_kv(kv, torch.tensor([n], dtype=torch.int32, device=DEV), k_scale=10 / 1024, v_scale=9 / 1024,
                       kv_scales=sc)[0, 1].transpose(0, 1)[t["slots"].long()]
     assert torch.isnan(back[0, 0, :16]).all() and not torch.isnan(back[0, 0, 16:]).any()
+
+
+def test_values_whose_quotient_is_next_to_the_largest_float():
+    # 2^118 / (6 v_scale) just below 2^128: rounded up to a short number it would be infinite
+    f = np.float32
+    found = None
+    for k in range(1, 2000):
+        vs = f(f(2.0 ** -10) / f(6)) + f(k - 1000) * f(2.0 ** -36)
+        d6 = f(6) * f(vs)
+        inv = f(1) / d6
+        q = f(2.0 ** 118) * inv
+        if np.isfinite(q) and q.view(np.uint32) >= 0x7F7FFFC0:
+            found = float(f(vs))
+            break
+    assert found is not None
+    t = tokens(4, 1, 4, torch.bfloat16, seed=45)
+    t["v"][0, 0, 0], t["v"][1, 1, 17] = 2.0 ** 118, -2.0 ** 118
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, 4, ks=1.0, vs=found)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_e2m1(got, gsc, 1, t["v"].double(), found)
