@@ -347,7 +347,9 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 // FULL: no slot is masked.  The weights are then 2^(score * scale - m) by one
 // FMA and ex2, and the maximum m of a column is only looked for (shuffles) when
 // some lane's score exceeds it (a vote), which after a piece's first tiles is
-// rare.  Masked tokens take weight 0 by selection; a token past the tile's rows
+// rare.  The scores that it is looked for in are then rounded before m is taken
+// off: above 2^24 an FMA would leave the product's rounding, many powers of two,
+// in the largest one's weight.  Masked tokens take weight 0 by selection; a token past the tile's rows
 // also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
 // that are masked).
 constexpr int kFp4Tokens = 32;
@@ -465,11 +467,12 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       }
       m[nt][0] = h0;
       m[nt][1] = h1;
-      if constexpr (FULL) {
+      if constexpr (FULL) {  // (from the rounded scores, as the maximum is)
 #pragma unroll
         for (int sj = 0; sj < kSG; ++sj)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[sj][nt][e] = fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]);
+          for (int e = 0; e < 4; ++e)
+            y[sj][nt][e] = __fsub_rn(__fmul_rn(x[sj][nt][e], sl2c[nt][e & 1]), m[nt][e & 1]);
       }
     }
   }
