@@ -344,15 +344,25 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 // instead of V would need an m-tile's 16 dims in one scale group, which rows in
 // their natural order do not give a lane without byte loads.
 //
+// The weights meet V in fp16, so they are 2^(score - m) with m the maximum less 15
+// (kFp4Shift): the largest is about 2^15, and one is a normal fp16 number, rounded
+// by 2^-12 of itself at most, down to 2^-29 of the largest (with weights up to 1 it
+// was 2^-14: beside a key 17 nats above the others, what the others bring was 2 %
+// off, and lost at 20).  The denominator sums them as they are in FP32.  The states
+// that merge (warps, pieces) hold this m, so the shift drops out.  m is not moved
+// while scores stay below m + 15.5 (2^15.5 < 65504).  From 2^20 on a shift by 15
+// would come out rounded; m is then the maximum itself.
+//
 // FULL: no slot is masked.  The weights are then 2^(score * scale - m) by one
-// FMA and ex2, and the maximum m of a column is only looked for (shuffles) when
-// some lane's score exceeds it (a vote), which after a piece's first tiles is
-// rare.  The scores that it is looked for in are then rounded before m is taken
+// FMA and ex2, and the maximum of a column is only looked for (shuffles) when
+// some lane's score exceeds that limit (a vote), which after a piece's first tiles
+// is rare.  The scores that it is looked for in are then rounded before m is taken
 // off: above 2^24 an FMA would leave the product's rounding, many powers of two,
 // in the largest one's weight.  Masked tokens take weight 0 by selection; a token past the tile's rows
 // also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
 // that are masked).
 constexpr int kFp4Tokens = 32;
+constexpr float kFp4Shift = 15.f, kFp4Limit = 15.5f;
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, __half2 b) {
   const __half2 d = __hmul2(as_half2(a), b);
@@ -425,13 +435,14 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
           y[sj][nt][e] = fmaf(x[sj][nt][e], sl2c[nt][e & 1], -m[nt][e & 1]);
           top = fmaxf(top, y[sj][nt][e]);
         }
-    grow = top > 0.f;
+    grow = top > kFp4Limit;
   } else {
 #pragma unroll
     for (int sj = 0; sj < kSG; ++sj)
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
-        grow |= fmaxf(x[sj][nt][0], x[sj][nt][2]) > m[nt][0] || fmaxf(x[sj][nt][1], x[sj][nt][3]) > m[nt][1];
+        grow |= fmaxf(x[sj][nt][0], x[sj][nt][2]) > m[nt][0] + kFp4Limit ||
+                fmaxf(x[sj][nt][1], x[sj][nt][3]) > m[nt][1] + kFp4Limit;
   }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -451,9 +462,9 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
         h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, off));
         h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, off));
       }
-      h0 = fmaxf(h0, m[nt][0]);
-      h1 = fmaxf(h1, m[nt][1]);
-      // 0 when the old max was -inf; 1 when unchanged (also covers -inf == -inf)
+      h0 = fmaxf(fabsf(h0) < 0x1p20f ? h0 - kFp4Shift : h0, m[nt][0]);
+      h1 = fmaxf(fabsf(h1) < 0x1p20f ? h1 - kFp4Shift : h1, m[nt][1]);
+      // 0 when the old m was -inf; 1 when unchanged (also covers -inf == -inf)
       const float a0 = h0 == m[nt][0] ? 1.f : ex2(m[nt][0] - h0);
       const float a1 = h1 == m[nt][1] ? 1.f : ex2(m[nt][1] - h1);
       l[nt][0] *= a0;

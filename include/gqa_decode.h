@@ -214,7 +214,9 @@ gqa_status_t gqa_decode_int8kv(const void* q, const int8_t* kv_i8, const uint16_
  * e4m3fn bytes, 16-byte aligned: byte j scales dims 16j .. 16j + 15.  Element
  * d of a key row is code[d] * scale[d / 16] * k_scale, of a value row the
  * same with v_scale.  capacity must be a multiple of 2 (the scales are staged
- * by 16-byte bulk copies).  q and out are fp16 or bf16 (`dtype`).  Codes and
+ * by 16-byte bulk copies).  q and out are fp16 or bf16 (`dtype`).  Each
+ * softmax weight is rounded to fp16 where it meets V (by 2^-12 of itself down to
+ * 2^-29 of the largest); everything else is FP32 or exact.  Codes and
  * scales of slots >= len[b] are never used.  k_scale and v_scale finite and
  * > 0, q_scale finite and >= 0.  Other rules as gqa_decode_prepared (no
  * allocation, no host sync).  The pages have no counterpart to this call. */
