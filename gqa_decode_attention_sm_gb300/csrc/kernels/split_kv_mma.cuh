@@ -524,6 +524,25 @@ __device__ __forceinline__ void fp4_tokens(const uint8_t* sK, const uint8_t* sV,
       if (r + 1 >= rows) s1 = 0u;
       if (r + 8 >= rows) s2 = 0u;
       if (r + 9 >= rows) s3 = 0u;
+      // A NaN scale is for the queries that see its token alone (0 * NaN would reach
+      // those it is masked for): taken out of the product, and put into the outputs
+      // (this lane's are dims of its own group) of the columns that see the first one.
+      const auto is_nan = [](uint32_t e4m3) { return (e4m3 & 0x7fu) == 0x7fu; };
+      const bool n0 = is_nan(s0), n1 = is_nan(s1), n2 = is_nan(s2), n3 = is_nan(s3);
+      if (__any_sync(0xffffffffu, n0 | n1 | n2 | n3)) {
+        int first = n0 ? r : (n1 ? r + 1 : (n2 ? r + 8 : (n3 ? r + 9 : rows)));
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
+        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
+        if (n0) s0 = 0u;
+        if (n1) s1 = 0u;
+        if (n2) s2 = 0u;
+        if (n3) s3 = 0u;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+          if (first < rows && tile_t0 + first < lim[nt])
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = NAN;
+      }
     }
     const __half2 sA = as_half2(e4m3x2_to_f16x2((uint16_t)prmt(s0, s1, 0x0040u)));  // tokens r, r + 1
     const __half2 sB = as_half2(e4m3x2_to_f16x2((uint16_t)prmt(s2, s3, 0x0040u)));  // tokens r + 8, r + 9

@@ -43,3 +43,25 @@ def test_scores_past_the_range_of_float_differences(q_scale, T, lens, S):
     t["q_scale"] = q_scale
     ref = reference(t)
     assert_close(decode(t, S)[0], t, ref)
+
+
+def test_a_draft_of_nan_reaches_only_the_queries_that_see_it():
+    for T, page in ((2, 0), (3, 0), (4, 0), (3, 16)):
+        t = make(2, 512, [300, 257], "bf16", T, seed=52)
+        clean = decode(t, 2, page)[0].clone()
+        for b, L in enumerate((300, 257)):
+            t["kv_scales"][b, 1, 2, L - 1, 3] = 0x7F  # the last draft's value, dims 48 .. 63 of KV head 2
+        out = decode(t, 2, page)[0]
+        assert torch.equal(out[:, :-1], clean[:, :-1])
+        last = torch.isnan(out[:, -1]).view(2, 8, 4, 8, 16)
+        assert last[:, 2, :, 3].all()
+        last[:, 2, :, 3] = False
+        assert not last.any()
+        # and in a key: the whole head of the queries that see it
+        t = make(2, 512, [300, 257], "bf16", T, seed=52)
+        for b, L in enumerate((300, 257)):
+            t["kv_scales"][b, 0, 5, L - 2, 0] = 0x7F
+        out = decode(t, 2, page)[0]
+        assert torch.equal(out[:, :T - 2], clean[:, :T - 2])
+        seen = torch.isnan(out[:, T - 2:]).view(2, -1, 8, 4, 128)
+        assert seen[:, :, 5].all() and not seen[:, :, [0, 1, 2, 3, 4, 6, 7]].any()
