@@ -40,6 +40,8 @@
 // exact remainder.
 #pragma once
 
+#include <type_traits>
+
 #include "append_kv.cuh"
 
 namespace gqa {
@@ -194,6 +196,41 @@ __device__ __forceinline__ float amax8_nan(const float (&x)[8]) {
   return m;
 }
 
+// mean(x^2) + eps of a head whose lane holds xl and xh (the same in its 8 lanes).
+__device__ __forceinline__ float mean_square(const float (&xl)[8], const float (&xh)[8], float eps) {
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    t[i] = fmaf(xl[i], xl[i], xh[i] * xh[i]) + fmaf(xl[i + 4], xl[i + 4], xh[i + 4] * xh[i + 4]);
+  float ss = (t[0] + t[1]) + (t[2] + t[3]);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+  return fmaf(ss, 1.f / kD, eps);
+}
+// FP32 holds the squares of such a head, and a sum of them, well inside its range:
+// so it is for fp16 at any size, for bf16 from about 2^-30 (with a smaller eps) to
+// 2^30.
+__device__ __forceinline__ bool squares_fit(float ss) { return ss > 0x1p-60f && ss < 0x1p60f; }
+// A head whose squares do not fit is scaled by the power of two k that brings its
+// largest element, or the root of eps, to [1, 2), and eps by k^2: the normalised
+// head is the same.  A head of zeros without eps, and one with an infinite element,
+// stay as they are.
+__device__ __forceinline__ void scale_head(float (&xl)[8], float (&xh)[8], float& eps) {
+  float m = fmaxf(amax8(xl), amax8(xh));
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  m = fmaxf(m, sqrtf(eps));
+  if (squares_fit(mean_square(xl, xh, eps)) || m == 0.f || !(m < INFINITY)) return;
+  const int exponent = (int)(__float_as_uint(m) >> 23);  // 0 for a subnormal m: k = 2^127 will do
+  const float k = __uint_as_float((uint32_t)max(254 - exponent, 1) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    xl[i] *= k;
+    xh[i] *= k;
+  }
+  eps = eps * k * k;
+}
+
 // The bound of |FP32 z - z| as a share of the head's largest |z|, A:
 //   cos and sin within 2^-24, their products with a weight and the one rounded
 //   product of the rotation: 3 * 2^-24 (|y_i cos| + |y_j sin|), at most 3 * 2^-24
@@ -256,7 +293,7 @@ __device__ __forceinline__ Float2 df_scale(float a, Float2 b) { return df_mul(Fl
 // One unit of four key heads whose rounding FP32 could not decide: the elements
 // in doubt, and nothing else, are formed again in double-float arithmetic, to
 // about 2^-43 of the head's largest.  (FP64 would do, at many times the latency.)
-template <int QF>
+template <int QF, bool ANY>
 __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, const uint4& wlo, const uint4& whi,
                                              const float (&zl)[8], const float (&zh)[8], float gl, float gh, float e,
                                              KeyCodes& out) {
@@ -266,6 +303,8 @@ __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, con
   unpack8<QF>(whi, yh);
   Float2 r = {1.f, 0.f};
   if (p.k_norm_w) {
+    float eps = p.eps;
+    if constexpr (ANY) scale_head(yl, yh, eps);
     Float2 acc[4] = {};  // (squares of 16-bit elements are exact)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -276,7 +315,7 @@ __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, con
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1)
       ss = df_add(ss, Float2{__shfl_xor_sync(0xffffffffu, ss.hi, off), __shfl_xor_sync(0xffffffffu, ss.lo, off)});
-    ss = df_add(Float2{ss.hi * (1.f / kD), ss.lo * (1.f / kD)}, Float2{p.eps, 0.f});
+    ss = df_add(Float2{ss.hi * (1.f / kD), ss.lo * (1.f / kD)}, Float2{eps, 0.f});
     // 1 / sqrt(ss) = r0 (1 - h)^(-1/2), h = 1 - ss r0^2 about 2^-21: to h^2
     const float r0 = rsqrtf(ss.hi);
     const float rr = r0 * r0;
@@ -408,30 +447,29 @@ __device__ __forceinline__ void make_coefs(const uint16_t* w, int idx, const flo
     k.d[i] = wl[i] * sn[i];
   }
 }
-template <int QF>
-__device__ __forceinline__ void rotate_unit(const uint4& wlo, const uint4& whi, const Coefs& k, bool norm, float eps,
+// The result says whether the squares fit; ANY (elsewhere too) takes heads whose
+// squares do not.
+template <int QF, bool ANY = false>
+__device__ __forceinline__ bool rotate_unit(const uint4& wlo, const uint4& whi, const Coefs& k, bool norm, float eps,
                                             float (&zl)[8], float (&zh)[8]) {
   float xl[8], xh[8];
   unpack8<QF>(wlo, xl);
   unpack8<QF>(whi, xh);
   float r = 1.f;
+  bool fit = true;
   if (norm) {
-    float t[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      t[i] = fmaf(xl[i], xl[i], xh[i] * xh[i]) + fmaf(xl[i + 4], xl[i + 4], xh[i + 4] * xh[i + 4]);
-    float ss = (t[0] + t[1]) + (t[2] + t[3]);
-#pragma unroll
-    for (int off = 4; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    ss = fmaf(ss, 1.f / kD, eps);
+    if constexpr (ANY) scale_head(xl, xh, eps);
+    const float ss = mean_square(xl, xh, eps);
+    fit = squares_fit(ss);
     r = rsqrtf(ss);
-    if (ss > 0x1p-60f && ss < 0x1p60f) r = fmaf(0.5f * r, fmaf(-ss * r, r, 1.f), r);  // (a Newton step)
+    if (fit) r = fmaf(0.5f * r, fmaf(-ss * r, r, 1.f), r);  // (a Newton step)
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     zl[i] = r * fmaf(xl[i], k.a[i], -(xh[i] * k.b[i]));
     zh[i] = r * fmaf(xh[i], k.c[i], xl[i] * k.d[i]);
   }
+  return fit;
 }
 
 // int8: the row's bf16 scale and codes (as an append step writes them).
@@ -611,14 +649,20 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
   const int step = gridDim.x * kWriteWarps;
   long long it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   [[maybe_unused]] int doubts = 0;  // units on this warp's list
+  // Heads whose squares do not fit FP32 are looked for on the way, and a warp that
+  // met one writes its units again after its tokens.  (4096 bf16 tokens into an
+  // e2m1 cache 24.8 us, 24.1 without any of it; a branch in each unit, which keeps
+  // the loads and shuffles of four from overlapping, 25.5.)
+  constexpr bool kWide = QF == kQBF16;
+  bool fit = true;
   // the same lanes write the bytes of a unit in doubt again
-  [[maybe_unused]] const auto settle = [&](int n, const RowAt& at, int g, const uint4& wlo, const uint4& whi,
+  [[maybe_unused]] const auto settle = [&](auto any, int n, const RowAt& at, int g, const uint4& wlo, const uint4& whi,
                                            const float(&zl)[8], const float(&zh)[8]) {
     float gl, gh, e;
     key_bounds(zl, zh, gl, gh, e);
     if (!__all_sync(0xffffffffu, e < INFINITY)) e = finite_bound(zl, zh);  // (the same where all are finite)
     KeyCodes k;
-    key_codes_exact<QF>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
+    key_codes_exact<QF, any.value>(p, n, wlo, whi, zl, zh, gl, gh, e, k);
     if (at.ok) store_e2m1(p, at.base + g * at.head, idx, k);
   };
   do {
@@ -649,7 +693,7 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           float zl[8], zh[8];
-          rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
+          fit &= rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
           uint4* d4 = reinterpret_cast<uint4*>(dst + i * 4 * kD);
           d4[0] = round8<QF>(zl);
           d4[8] = round8<QF>(zh);
@@ -663,10 +707,10 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         for (int i = 0; i < (U == 1 ? 1 : kWriteKUnits); ++i) {
           const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
           float zl[8], zh[8];
-          rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
+          fit &= rotate_unit<QF>(wlo[i], whi[i], kc, p.k_norm_w != nullptr, p.eps, zl, zh);
           if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo[i], whi[i], zl, zh)) {
             if constexpr (U == 1) {  // (a call of few tokens is as long as its longest unit)
-              settle(n, at, g, wlo[i], whi[i], zl, zh);
+              settle(std::false_type(), n, at, g, wlo[i], whi[i], zl, zh);
             } else {
               if (lane == 0) list[doubts] = make_int2(n, u0 + i - kWriteQUnits);
               ++doubts;
@@ -698,12 +742,43 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         Coefs kc;
         make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
         rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
-        settle(n, at, g, wlo, whi, zl, zh);
+        settle(std::false_type(), n, at, g, wlo, whi, zl, zh);
       }
       doubts = 0;
       __syncwarp();
     }
   } while (it < items);
+  if constexpr (kWide) {
+    if (__all_sync(0xffffffffu, fit)) return;
+#pragma unroll 1
+    for (it = (long long)blockIdx.x * kWriteWarps + (threadIdx.x >> 5); it < items; it += step) {
+#pragma unroll 1
+      for (int i = 0; i < U; ++i) {
+        const int n = (int)(it / kParts), u = (int)(it - (long long)n * kParts) * U + i;
+        if (u >= kWriteQUnits + kWriteKUnits) break;  // (values have no norm)
+        const bool q = u < kWriteQUnits;
+        const int g = 4 * (q ? u : u - kWriteQUnits) + quarter;
+        const uint16_t* w = q ? p.q_norm_w : p.k_norm_w;
+        const uint4* s4 =
+            reinterpret_cast<const uint4*>((q ? p.q_proj + n * p.q_stride : p.k_proj + n * p.k_stride) + g * kD + 8 * idx);
+        const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+        float cs[8], sn[8], zl[8], zh[8];
+        token_angles(p, n, turn, axis, cs, sn);
+        Coefs kc;
+        make_coefs<QF>(w, idx, cs, sn, kc);
+        rotate_unit<QF, true>(wlo, whi, kc, true, p.eps, zl, zh);
+        if (q) {
+          uint4* d4 = reinterpret_cast<uint4*>(p.q_out + ((size_t)n * kHq + g) * kD + 8 * idx);
+          d4[0] = round8<QF>(zl);
+          d4[8] = round8<QF>(zh);
+        } else {
+          const RowAt at = locate(p, n);
+          if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo, whi, zl, zh))
+            settle(std::true_type(), n, at, g, wlo, whi, zl, zh);
+        }
+      }
+    }
+  }
 }
 
 }  // namespace gqa

@@ -102,3 +102,20 @@ def test_values_whose_quotient_is_next_to_the_largest_float():
     q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, 4, ks=1.0, vs=found)
     got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
     check_e2m1(got, gsc, 1, t["v"].double(), found)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("mag,eps", [(1e30, 1e-6), (3e36, 1e-6), (1e-25, 0.0), (1e-36, 0.0), (1e-12, 1e-24),
+                                     (1e-30, 1e-30), (1e-12, 1e-38)])
+@pytest.mark.parametrize("n", [40, 1000])
+def test_norms_whose_squares_leave_fp32(fmt, mag, eps, n):
+    t = tokens(n, 1, n, torch.bfloat16, seed=46, mag=mag / 20)
+    t["pos"] = (torch.arange(n, device=DEV) % 1000).to(torch.int32)
+    q_out, kv, sc, before, table, flags = run_write(t, fmt, 1, n, ks=10 / 1024, vs=1.0, eps=eps)
+    check_heads(q_out, rotated(t["q"], t["qw"], t["pos"], eps=eps))
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    z = rotated(t["k"], t["kw"], t["pos"], eps=eps)
+    if fmt == "bf16":
+        check_heads(got[:, 0], z)
+    else:
+        check_e2m1(got, gsc, 0, z, 10 / 1024)
