@@ -705,6 +705,9 @@ gqa_status_t write_kv(const CacheArgs& c, const WriteArgs& a) {
   // (the e2m1 scales' products and reciprocals stay normal FP32 numbers)
   if (c.format == kKvE2M1 && (c.k_scale < 0x1p-100f || c.k_scale > 0x1p100f || c.v_scale < 0x1p-100f || c.v_scale > 0x1p100f))
     return fail(GQA_ERR_INVALID_ARGUMENT, "the tensor scales of an e2m1 cache must lie in [2^-100, 2^100]");
+  // (an e4m3 write multiplies with the reciprocals: infinite ones would make zeros NaN)
+  if (c.format == kKvE4M3 && (c.k_scale < 0x1p-126f || c.k_scale > 0x1p126f || c.v_scale < 0x1p-126f || c.v_scale > 0x1p126f))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "the scales of an e4m3 cache must lie in [2^-126, 2^126]");
   if (!std::isfinite(a.eps) || a.eps < 0.f) return fail(GQA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
   if (!std::isfinite(a.rope_theta) || a.rope_theta < 1.f)
     return fail(GQA_ERR_INVALID_ARGUMENT, "rope_theta must be finite and >= 1");

@@ -12,7 +12,7 @@
 //   a_i = pos * theta^(-i/64)                    (rotate-half RoPE)
 // q -> q_out (q's dtype, RNE); k -> K plane at `slot`; v is written unchanged
 // to the V plane.  The cache format decides the write: fp16/bf16 (RNE),
-// e4m3 (value / scale, RNE, saturating), int8 (one bf16 scale amax/127 per
+// e4m3 (value * (1 / scale) in FP32, RNE, saturating), int8 (one bf16 scale amax/127 per
 // row, codes round-to-nearest-even, clipped to +-127).
 //
 // One CTA per batch row, 8 warps; each warp takes six whole head vectors (all

@@ -8,7 +8,8 @@
 //   a_i = positions[axis(i)][n] * theta^(-i/64)
 // q -> q_out (one rounding); k and v -> row rows[n], slot slots[n] of the cache:
 //   fp16/bf16  one rounding
-//   e4m3       x / scale, to the nearest, saturating
+//   e4m3       x * (1 / scale) in FP32, to the nearest, saturating: the append step's
+//              codes, next to a tie (2^-23) the other neighbour of x / scale's
 //   int8       bf16 scale amax / 127 of the row, code = round(x / scale)
 //   e2m1       e4m3 scale amax / (6 * tensor scale) of each 16 dims, code = the
 //              e2m1 level nearest to x / (scale * tensor scale)

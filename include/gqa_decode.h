@@ -384,7 +384,9 @@ gqa_status_t gqa_decode_debug_cut_extents(uint64_t kv_cut_bytes, uint64_t scales
  * slot slots[b] <- z of the 8 key heads; the V plane at that slot <- v_proj
  * unchanged.  q_proj [batch,32,128], k_proj and v_proj [batch,8,128] and the
  * weights are `dtype`.  The cache format decides the write: fp16/bf16 (must
- * equal dtype; RNE), e4m3 (value / k_scale or / v_scale, RNE, saturating) or
+ * equal dtype; RNE), e4m3 (value * (1 / k_scale) or * (1 / v_scale), quotient
+ * and product in FP32, RNE, saturating: the code of value / scale but where that
+ * lies within 2^-23 of itself of a tie, and either neighbour there) or
  * int8 (codes round-to-nearest-even of value / scale with a fresh bf16 row
  * scale amax/127 written to kv_scales, clipped to +-127) or e2m1 (as
  * gqa_write_kv, whose rules for alignment and rope_theta then hold too).  positions and
@@ -454,7 +456,8 @@ gqa_status_t gqa_append_kv_paged(const void* q_proj, const void* k_proj, const v
  * batch gives its padding slot -1.  tokens = 0 does nothing.  Pointers are
  * 16-byte aligned (int32 arrays and the workspace 4, scales 2).  eps finite
  * >= 0, rope_theta finite >= 1, k_scale and v_scale finite > 0 (e2m1: within
- * [2^-100, 2^100]).  Nothing written may overlap anything else
+ * [2^-100, 2^100]; e4m3: [2^-126, 2^126], so that their reciprocals are normal
+ * numbers; the other formats' writes do not use them).  Nothing written may overlap anything else
  * (GQA_ERR_ALIASING).  One launch, no allocation, no host sync. */
 gqa_status_t gqa_write_kv(const void* q_proj, const void* k_proj, const void* v_proj,
                           long long q_stride, long long k_stride, long long v_stride,

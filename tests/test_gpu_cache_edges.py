@@ -119,3 +119,28 @@ def test_norms_whose_squares_leave_fp32(fmt, mag, eps, n):
         check_heads(got[:, 0], z)
     else:
         check_e2m1(got, gsc, 0, z, 10 / 1024)
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.02, 0.7, 1.3, 41.0, 2.0 ** -5])
+def test_e4m3_values_are_products_with_the_reciprocal(scale):
+    """Every finite fp16 value, written by both entries: the FP32 product with the FP32 reciprocal, rounded to e4m3
+    (no value further from value / scale than half a step and the two FP32 roundings)."""
+    bits = torch.arange(65536, device=DEV).to(torch.int32).to(torch.int16).view(torch.float16)
+    v = bits[torch.isfinite(bits)]
+    n = -(-v.numel() // (HKV * D))
+    v = torch.cat((v, torch.zeros(n * HKV * D - v.numel(), dtype=v.dtype, device=DEV))).view(n, HKV, D)
+    t = tokens(n, 1, n, torch.float16, seed=47)
+    t["v"] = v
+    q_out, kv, sc, before, table, flags = run_write(t, "e4m3", 1, n, ks=1.0, vs=scale)
+    got, _, _ = rows_at(kv, None, None, 0, t["rows"], t["slots"])
+    inv = np.float32(1) / np.float32(scale)
+    want = (v.float() * float(inv)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(got[:, 1], want.view(torch.uint8))
+    x = torch.clamp(v.double() / float(np.float32(scale)), -448, 448)
+    back = got[:, 1].contiguous().view(torch.float8_e4m3fn).double()
+    assert ((back - x).abs() <= torch.clamp(x.abs() * (2 ** -4 + 2 ** -22), min=2 ** -10 * (1 + 2 ** -18))).all()
+    # the append step takes one token a row
+    kv2, _ = new_cache("e4m3", n, 8)
+    slots = torch.zeros(n, dtype=torch.int32, device=DEV)
+    gq.append_kv(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], slots, kv2, k_scale=1.0, v_scale=scale)
+    assert torch.equal(kv2[:, 1, :, 0], got[:, 1])
