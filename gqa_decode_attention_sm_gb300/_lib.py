@@ -11,11 +11,12 @@ import threading
 from .build import LIB_PATH
 
 _lib = None
+binding_interface = None  # the C interface that the native binding was built for, once it is loaded
 _lock = threading.Lock()
 
 # Every extern "C" function declared in include/gqa_decode.h.
 EXPORTS = (
-    "gqa_status_string", "gqa_last_error", "gqa_decode_workspace_size", "gqa_decode_plan",
+    "gqa_status_string", "gqa_last_error", "gqa_interface", "gqa_decode_workspace_size", "gqa_decode_plan",
     "gqa_decode_plan_for", "gqa_decode_split_geometry", "gqa_decode_launch_count_for",
     "gqa_decode", "gqa_decode_prepared", "gqa_decode_fp8kv", "gqa_decode_split_stage",
     "gqa_decode_combine_stage", "gqa_decode_workspace_init", "gqa_decode_get_status",
@@ -39,6 +40,7 @@ def _declare(lib):
     sig = {
         "gqa_status_string": (ctypes.c_char_p, [i]),
         "gqa_last_error": (ctypes.c_char_p, []),
+        "gqa_interface": (ctypes.c_char_p, []),
         "gqa_decode_workspace_size": (sz, [i, i, i]),
         "gqa_decode_plan": (i, [i, i, i, i, ctypes.POINTER(ctypes.c_int)]),
         "gqa_decode_plan_for": (i, [i, i, i, i, ctypes.POINTER(ctypes.c_int)]),
@@ -74,6 +76,7 @@ def _declare(lib):
         fn.restype = res
         fn.argtypes = args
     lib.addresses = {name: ctypes.cast(getattr(lib, name), p).value for name in sig}  # for the native binding
+    lib.interface = lib.gqa_interface().decode()
     return lib
 
 
@@ -95,8 +98,10 @@ def load(path: str | None = None):
 
 
 def address(name: str) -> int:
-    """Address of a function of the loaded library."""
-    return (_lib or load()).addresses[name]
+    """Address of a function of the loaded library for the native binding; 0, which it
+    does not call, if the two were built for different interfaces."""
+    lib = _lib or load()
+    return lib.addresses[name] if lib.interface == binding_interface else 0
 
 
 def check(status: int) -> None:

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 from dataclasses import dataclass
 
 import torch
@@ -21,12 +22,34 @@ import torch
 from . import _lib
 from ._lib import GqaError
 
-try:  # the native binding (built by build.build_native); without it every call takes the paths below
-    from . import _native
-    if _native.torch_version != torch.__version__:
-        _native = None
-except ImportError:
-    _native = None
+
+def _load_native():
+    """The native binding (built by build.build_native) if it is there and for this
+    torch, else None: every call then takes its path below."""
+    importlib.invalidate_caches()  # (this process may have built it)
+    try:
+        from . import _native as module
+    except ImportError:
+        return None
+    if getattr(module, "interface", None) is None or module.torch_version != torch.__version__:
+        return None
+    _lib.binding_interface = module.interface
+    return module
+
+
+def __getattr__(name):  # _native is loaded when it is first asked for
+    if name == "_native":
+        globals()[name] = _load_native()
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def _binding():
+    try:
+        return _native
+    except NameError:
+        return __getattr__("_native")
+
 
 HQ, HKV, D = 32, 8, 128
 F16, BF16 = 0, 1
@@ -261,8 +284,9 @@ def _result(done):
 
 def launch(p: Prepared) -> torch.Tensor:
     """Run both stages on the current stream: no allocation, no host read."""
-    if _native is not None and p.kv_format == KV_E2M1:
-        done = _native.attend(_lib.address("gqa_decode_fp4kv"), 0, p.q, p.kv, None, p.lens, p.out, p.kv_scales,
+    native = _binding() if p.kv_format == KV_E2M1 else None
+    if native is not None:
+        done = native.attend(_lib.address("gqa_decode_fp4kv"), 0, p.q, p.kv, None, p.lens, p.out, p.kv_scales,
                               p.workspace, p.num_splits, p.q_scale, p.k_scale, p.v_scale)
         if done is not None:
             return _result(done)
@@ -356,8 +380,9 @@ def gqa_decode_fp4kv(q, kv, kv_scales, sequence_lengths, k_scale: float = 1.0, v
     the e2m1 codes of dims 2j (low nibble) and 2j + 1; kv_scales e4m3 (uint8 or
     float8_e4m3fn) [batch, 2, 8, capacity, 8], one for each 16 dims; k_scale and
     v_scale multiply all keys and all values.  fp16/bf16 q and out."""
-    if _native is not None:
-        done = _native.attend(_lib.address("gqa_decode_fp4kv"), 0, q, kv, None, sequence_lengths, out, kv_scales,
+    native = _binding()
+    if native is not None:
+        done = native.attend(_lib.address("gqa_decode_fp4kv"), 0, q, kv, None, sequence_lengths, out, kv_scales,
                               workspace, num_splits, q_scale, k_scale, v_scale)
         if done is not None:
             return _result(done)
@@ -389,8 +414,9 @@ def gqa_decode_paged(q, kv_pages, block_table, sequence_lengths, q_scale: float 
     e2m1: uint8 [.., page_size, 64] with kv_scales e4m3 [.., page_size, 8]),
     block_table int32 [batch, max_pages]; q [batch, 32, 128], or [batch, T, 32, 128]
     for a verify window of T = 1..4 tokens; returns out (q's shape)."""
-    if _native is not None:
-        done = _native.attend(_lib.address("gqa_decode_paged"), 2, q, kv_pages, block_table, sequence_lengths, out,
+    native = _binding()
+    if native is not None:
+        done = native.attend(_lib.address("gqa_decode_paged"), 2, q, kv_pages, block_table, sequence_lengths, out,
                               kv_scales, workspace, num_splits, q_scale, k_scale, v_scale)
         if done is not None:
             return _result(done)
@@ -432,8 +458,9 @@ def gqa_decode_verify(q, kv, sequence_lengths, q_scale: float = 1.0, k_scale: fl
     """Verify window: q [batch, T, 32, 128] (T = 1..4 draft tokens, the last T slots
     of each cache row); query j attends slots [0, len - T + j].  Any KV format
     (int8 and e2m1 need kv_scales).  Returns out [batch, T, 32, 128]."""
-    if _native is not None:
-        done = _native.attend(_lib.address("gqa_decode_verify"), 1, q, kv, None, sequence_lengths, out, kv_scales,
+    native = _binding()
+    if native is not None:
+        done = native.attend(_lib.address("gqa_decode_verify"), 1, q, kv, None, sequence_lengths, out, kv_scales,
                               workspace, num_splits, q_scale, k_scale, v_scale)
         if done is not None:
             return _result(done)
@@ -618,8 +645,9 @@ def write_kv(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, slots,
     the 64 rotary angles, in blocks or interleaved.  q_norm_w and k_norm_w None:
     no norm.  kv of any format (e2m1: uint8 [.., 64] with e4m3 kv_scales
     [.., 8]).  Returns q_out [tokens, 32, 128]."""
-    if _native is not None:
-        done = _native.write(_lib.address("gqa_write_kv"), False, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
+    native = _binding()
+    if native is not None:
+        done = native.write(_lib.address("gqa_write_kv"), False, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
                              rows, slots, kv, None, q_out, mrope_section, mrope_interleaved, eps, rope_theta,
                              k_scale, v_scale, kv_scales, workspace)
         if done is not None:
@@ -635,8 +663,9 @@ def write_kv_paged(q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions, rows, 
     """write_kv on a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
     its scale pages), block_table int32 [batch, max_pages]; slot s of row b is
     row s % page_size of page block_table[b, s // page_size]."""
-    if _native is not None:
-        done = _native.write(_lib.address("gqa_write_kv_paged"), True, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
+    native = _binding()
+    if native is not None:
+        done = native.write(_lib.address("gqa_write_kv_paged"), True, q_proj, k_proj, v_proj, q_norm_w, k_norm_w, positions,
                              rows, slots, kv_pages, block_table, q_out, mrope_section, mrope_interleaved, eps, rope_theta,
                              k_scale, v_scale, kv_scales, workspace)
         if done is not None:
@@ -690,8 +719,9 @@ def read_kv(kv, sequence_lengths, starts=None, out=None, dtype=None, k_scale: fl
     fp16 or bf16, into out [batch, 2, 8, out_capacity, 128] from slot 0 on; the
     rest of out keeps what it holds (a new one, of the cache's capacity and of
     ``dtype``, is not initialised).  starts None: 0."""
-    if _native is not None:
-        done = _native.read(_lib.address("gqa_read_kv"), False, kv, None, sequence_lengths, starts, out, dtype, k_scale,
+    native = _binding()
+    if native is not None:
+        done = native.read(_lib.address("gqa_read_kv"), False, kv, None, sequence_lengths, starts, out, dtype, k_scale,
                             v_scale, kv_scales, workspace)
         if done is not None:
             return _result(done)
@@ -702,8 +732,9 @@ def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None
                   v_scale: float = 1.0, kv_scales=None, workspace=None):
     """read_kv from a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
     its scale pages), block_table int32 [batch, max_pages]."""
-    if _native is not None:
-        done = _native.read(_lib.address("gqa_read_kv_paged"), True, kv_pages, block_table, sequence_lengths, starts, out, dtype, k_scale,
+    native = _binding()
+    if native is not None:
+        done = native.read(_lib.address("gqa_read_kv_paged"), True, kv_pages, block_table, sequence_lengths, starts, out, dtype, k_scale,
                             v_scale, kv_scales, workspace)
         if done is not None:
             return _result(done)

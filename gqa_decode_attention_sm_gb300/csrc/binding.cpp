@@ -1,7 +1,8 @@
-// Native binding of the cache write and read-back calls and of decode calls with
-// everything given (output, split count, workspace): the argument checks and the
-// call of the C ABI without the interpreter between them (writing 256 tokens
-// costs the host 4 us a call so, 16 us through ctypes).
+// Native binding of the cache write and read-back calls, and of gqa_decode_fp4kv,
+// gqa_decode_verify and gqa_decode_paged (caches of every format) and a prepared
+// 4-bit launch with everything given (output, split count, workspace): the argument
+// checks and the call of the C ABI without the interpreter between them (writing 256
+// tokens costs the host 4 us a call so, 16 us through ctypes).
 //
 // Each function checks exactly what api.py checks.  Arguments in any other form
 // than the plain one (wrong types, shapes or devices, tensor subclasses, another
@@ -329,8 +330,11 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, 
 
 PyMODINIT_FUNC PyInit__native(void) {
   PyObject* m = PyModule_Create(&kModule);
-  // the torch it was compiled against: api.py takes it only with the same one
-  if (m && PyModule_AddStringConstant(m, "torch_version", GQA_TORCH_VERSION) < 0) {
+  // the torch and the C interface it was compiled against: api.py takes it only
+  // with the same ones (and the build looks for built_for in the file)
+  if (m && (PyModule_AddStringConstant(m, "torch_version", GQA_TORCH_VERSION) < 0 ||
+            PyModule_AddStringConstant(m, "interface", GQA_INTERFACE) < 0 ||
+            PyModule_AddStringConstant(m, "built_for", GQA_BUILT_FOR) < 0)) {
     Py_DECREF(m);
     return nullptr;
   }

@@ -950,6 +950,14 @@ const char* gqa_status_string(gqa_status_t status) {
 
 const char* gqa_last_error(void) { return g_last_error.c_str(); }
 
+// GQA_INTERFACE: a token that the build forms from the header's digest
+#define GQA_TEXT_OF(x) #x
+#define GQA_TEXT(x) GQA_TEXT_OF(x)
+#ifndef GQA_INTERFACE
+#define GQA_INTERFACE
+#endif
+const char* gqa_interface(void) { return GQA_TEXT(GQA_INTERFACE); }
+
 size_t gqa_decode_workspace_size(int batch, int capacity, int num_splits) {
   if (batch < 1 || capacity < 1 || num_splits < 1 || num_splits > GQA_MAX_SPLITS) return 0;
   return workspace_bytes_for(batch, num_splits);

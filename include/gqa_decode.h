@@ -117,6 +117,11 @@ const char* gqa_status_string(gqa_status_t status);
 /* Details of the last failure on the calling thread ("" if none). */
 const char* gqa_last_error(void);
 
+/* Which interface the library was built with: a digest of this header (static
+ * string, "" if the build gave none).  A binding that calls functions by address
+ * compares it with that of the header it was compiled against. */
+const char* gqa_interface(void);
+
 /* Bytes of workspace needed for (batch, capacity, num_splits); 0 if the
  * arguments are invalid (batch, capacity < 1; num_splits outside
  * [1, GQA_MAX_SPLITS]).  num_splits = 1 needs only the 256-byte header. */
