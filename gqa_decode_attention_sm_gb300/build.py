@@ -56,7 +56,7 @@ CHECKED_LIB_PATH = os.path.join(PKG, "libgqa_decode_checked.so")
 
 
 def build_checked(force: bool = False, verbose: bool = False) -> str:
-    """The same library with every kernel access range-checked (-DGQA_CHECKED):
+    """The same library with the kernels' accesses range-checked (-DGQA_CHECKED):
     an access outside its buffer sets GQA_FLAG_BOUNDS and is redirected inside
     it.  For tests only; the product library is built without the checks."""
     if not force and os.path.exists(CHECKED_LIB_PATH):

@@ -615,6 +615,18 @@ struct CacheArgs {
   size_t table_bytes() const { return block_table ? (size_t)batch * max_pages * 4 : 0; }
 };
 
+// Rows of 128 that the checked build's write and read-back kernels may touch (cut
+// short by gqa_decode_debug_cut_extents).
+size_t checked_rows(const CacheArgs& c) {
+  size_t cut = 0;
+  if (kChecked) {
+    const auto whole = [](uint64_t bytes, int row) -> size_t { return row ? bytes / row + (bytes % row != 0) : 0; };
+    cut = std::max(whole(g_cut_kv_bytes.load(), kv_row_bytes(c.format)),
+                   whole(g_cut_scales_bytes.load(), scale_row_bytes(c.format)));
+  }
+  return c.rows() - std::min(c.rows(), cut);
+}
+
 gqa_status_t paged_args(CacheArgs& c, const int32_t* block_table, int max_pages_per_seq, int num_pages,
                         int page_size) {
   if (!block_table) return fail(GQA_ERR_INVALID_ARGUMENT, "block_table is null");
@@ -786,7 +798,11 @@ gqa_status_t write_kv(const CacheArgs& c, const WriteArgs& a) {
     else if (a.section) axis = (i >= a.section[0]) + (i >= a.section[0] + a.section[1]);
     w.axis[i] = (uint8_t)axis;
   }
-  w.kv_rows = c.rows();
+  w.kv_rows = checked_rows(c);
+  w.q_bytes = ins[0].bytes;
+  w.k_bytes = ins[1].bytes;
+  w.v_bytes = ins[2].bytes;
+  w.pos_bytes = n * 4 * (a.section ? 3 : 1);
   const cudaError_t e = launch_write_kv(w, c.format, a.dtype == GQA_BF16 ? kQBF16 : kQF16, sms, a.stream);
   if (e != cudaSuccess) return cuda_fail(e, "write kernel launch");
   return GQA_OK;
@@ -828,7 +844,7 @@ gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* sta
   r.page_log2 = c.page_log2;
   r.k_scale = c.k_scale;
   r.v_scale = c.v_scale;
-  r.kv_rows = c.rows();
+  r.kv_rows = checked_rows(c);
   const cudaError_t e = launch_read_kv(r, c.format, out_dtype == GQA_BF16 ? kQBF16 : kQF16, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "read kernel launch");
   return GQA_OK;

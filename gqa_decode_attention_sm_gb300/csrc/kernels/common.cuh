@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "gqa_decode.h"
+
 namespace gqa {
 
 // 32 query heads share 8 KV heads (4 per KV head), head_dim 128, one query
@@ -84,8 +86,9 @@ __host__ __device__ inline int split_count(int capacity, int num_splits, int kv_
 }
 
 // Checked builds (compiled with -DGQA_CHECKED; the product library is not):
-// every global-memory access of the kernels is tested against the extent of
-// its buffer first.  One outside it sets GQA_FLAG_BOUNDS in the status word
+// every global-memory access whose place is computed (cache rows and scales,
+// partial results, outputs, and in the write and read-back kernels every load and
+// store) is tested against the extent of its buffer first.  One outside it sets GQA_FLAG_BOUNDS in the status word
 // and is redirected to an address inside the buffer, so a bad index is
 // reported and nothing faults.  The tests run their cases through such a
 // build and require the flag never to be set.
@@ -98,6 +101,18 @@ constexpr bool kChecked = false;
 __device__ __forceinline__ bool in_extent(const void* base, size_t extent, const void* p, size_t bytes) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(base), a = reinterpret_cast<uintptr_t>(p);
   return a >= b && bytes <= extent && a - b <= extent - bytes;
+}
+// `p`, to an object of `bytes` in a buffer; checked builds: the buffer's start, and
+// the flag, where it is not in it.  (The buffers hold such an object at their start.)
+template <class T>
+__device__ __forceinline__ T* in_buffer(T* p, size_t bytes, const void* base, size_t extent, uint32_t* flags) {
+  if constexpr (kChecked) {
+    if (!in_extent(base, extent, p, bytes)) {
+      if (flags) atomicOr(flags, GQA_FLAG_BOUNDS);
+      return (T*)base;
+    }
+  }
+  return p;
 }
 
 // Default bound of a pipeline wait (a healthy wait lasts microseconds).

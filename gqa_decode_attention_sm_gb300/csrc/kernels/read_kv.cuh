@@ -53,7 +53,9 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int b = blockIdx.z, pg = blockIdx.y;  // pg = plane * 8 + KV head
-  const int len_raw = __ldg(p.lens + b), start_raw = p.starts ? __ldg(p.starts + b) : 0;
+  const size_t list = (size_t)p.batch * 4;
+  const int len_raw = __ldg(in_buffer(p.lens + b, 4, p.lens, list, p.flags));
+  const int start_raw = p.starts ? __ldg(in_buffer(p.starts + b, 4, p.starts, list, p.flags)) : 0;
   const int len = min(max(len_raw, 0), p.capacity), start = min(max(start_raw, 0), len);
   if ((len != len_raw || start != start_raw) && p.flags && pg == 0 && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(p.flags, GQA_FLAG_LENGTH_CLAMPED);
@@ -65,7 +67,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
     const int t = start + j;
     size_t unit = (size_t)b, rows = (size_t)p.capacity, in = (size_t)t;
     if (p.block_table != nullptr) {
-      int id = __ldg(p.block_table + (size_t)b * p.max_pages + (t >> p.page_log2));
+      int id = __ldg(in_buffer(p.block_table + (size_t)b * p.max_pages + (t >> p.page_log2), 4, p.block_table,
+                               (size_t)p.batch * p.max_pages * 4, p.flags));
       if (id < 0 || id >= p.num_pages) {  // out-of-contract page id: clamp, flag, never fault
         if (p.flags) atomicOr(p.flags, GQA_FLAG_PAGE_CLAMPED);
         id = min(max(id, 0), p.num_pages - 1);
@@ -139,8 +142,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < kReadElems / 2; ++i) o[i] = read_round2<OF>(x[2 * i] * sc * all, x[2 * i + 1] * sc * all);
     }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                          (((size_t)b * 2 * kHkv + pg) * p.out_capacity + j) * kD + e * kReadElems);
+    uint16_t* out = static_cast<uint16_t*>(p.out);
+    const size_t at = (((size_t)b * 2 * kHkv + pg) * p.out_capacity + j) * kD + e * kReadElems;
+    uint4* dst = reinterpret_cast<uint4*>(in_buffer(out + at, kReadElems * 2, out,
+                                                    (size_t)p.batch * 2 * kHkv * p.out_capacity * kD * 2, p.flags));
 #pragma unroll
     for (int i = 0; i < kReadElems / 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
   }

@@ -70,8 +70,21 @@ struct WriteParams {
   float eps, k_scale, v_scale, k_inv_scale, v_inv_scale;
   uint64_t turns[kD / 2];    // theta^(-i/64) / (2 pi) modulo 1, in units of 2^-64
   uint8_t axis[kD / 2];      // which row of positions
-  size_t kv_rows;            // rows of 128 in the cache, for checked builds
+  // for checked builds: rows of 128 in the cache, bytes of the projections and positions
+  size_t kv_rows, q_bytes, k_bytes, v_bytes, pos_bytes;
 };
+
+__device__ __forceinline__ int position(const WriteParams& p, int axis, int n) {
+  return __ldg(in_buffer(p.positions + (size_t)axis * p.tokens + n, 4, p.positions, p.pos_bytes, p.flags));
+}
+// 8 elements at `at`, in a projection or a norm weight `base` of `bytes`.
+__device__ __forceinline__ uint4 load8(const WriteParams& p, const uint16_t* at, const uint16_t* base, size_t bytes) {
+  return __ldg(reinterpret_cast<const uint4*>(in_buffer(at, 16, base, bytes, p.flags)));
+}
+// ... of q_out
+__device__ __forceinline__ void store8(const WriteParams& p, uint16_t* at, const uint4& v) {
+  *reinterpret_cast<uint4*>(in_buffer(at, 16, p.q_out, (size_t)p.tokens * kHq * kD * 2, p.flags)) = v;
+}
 
 // sin and cos of `turn` * 2 pi / 2^64
 __device__ __forceinline__ void sincos_turn(uint64_t turn, float& s, float& c) {
@@ -324,8 +337,8 @@ __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, con
     const float h = (1.f - t.hi) - t.lo;
     r = fast_two_sum(r0, r0 * fmaf(0.375f * h, h, 0.5f * h));
     float wl[8], wh[8];
-    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 8 * idx), wl);
-    unpack8<QF>(*reinterpret_cast<const uint4*>(p.k_norm_w + 64 + 8 * idx), wh);
+    unpack8<QF>(load8(p, p.k_norm_w + 8 * idx, p.k_norm_w, 2 * kD), wl);
+    unpack8<QF>(load8(p, p.k_norm_w + 64 + 8 * idx, p.k_norm_w, 2 * kD), wh);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // (exact)
       yl[i] *= wl[i];
@@ -334,7 +347,7 @@ __device__ __forceinline__ void key_codes_exact(const WriteParams& p, int n, con
   }
   const auto exact = [&](int i, Float2& lo, Float2& hi) {
     const int a = 8 * idx + i;
-    const int64_t pos = __ldg(p.positions + (size_t)p.axis[a] * p.tokens + n);
+    const int64_t pos = position(p, p.axis[a], n);
     Float2 s, c;
     sincos_turn_exact((uint64_t)pos * p.turns[a], s, c);
     const Float2 us = df_scale(yl[i], s), vs = df_scale(yh[i], s);
@@ -396,14 +409,16 @@ struct RowAt {
   bool ok;
 };
 __device__ __forceinline__ RowAt locate(const WriteParams& p, int n) {
-  const int b = p.rows ? __ldg(p.rows + n) : n;
-  const int slot = __ldg(p.slots + n);
+  const size_t list = (size_t)p.tokens * 4;
+  const int b = p.rows ? __ldg(in_buffer(p.rows + n, 4, p.rows, list, p.flags)) : n;
+  const int slot = __ldg(in_buffer(p.slots + n, 4, p.slots, list, p.flags));
   RowAt at;
   at.ok = b >= 0 && b < p.batch && slot >= 0 && slot < p.capacity;
   uint32_t flag = at.ok ? 0u : GQA_FLAG_SLOT_CLAMPED;
   size_t unit = at.ok ? (size_t)b : 0, rows = (size_t)p.capacity, in = at.ok ? (size_t)slot : 0;
   if (p.block_table != nullptr && at.ok) {
-    const int id = __ldg(p.block_table + (size_t)b * p.max_pages + (slot >> p.page_log2));
+    const int id = __ldg(in_buffer(p.block_table + (size_t)b * p.max_pages + (slot >> p.page_log2), 4, p.block_table,
+                                   (size_t)p.batch * p.max_pages * 4, p.flags));
     if (id < 0 || id >= p.num_pages) {  // never write through an out-of-range entry
       at.ok = false;
       flag = GQA_FLAG_PAGE_CLAMPED;
@@ -430,12 +445,12 @@ struct Coefs {
   float a[8], b[8], c[8], d[8];
 };
 template <int QF>
-__device__ __forceinline__ void make_coefs(const uint16_t* w, int idx, const float (&cs)[8], const float (&sn)[8],
+__device__ __forceinline__ void make_coefs(const WriteParams& p, const uint16_t* w, int idx, const float (&cs)[8], const float (&sn)[8],
                                            Coefs& k) {
   float wl[8], wh[8];
   if (w) {
-    unpack8<QF>(__ldg(reinterpret_cast<const uint4*>(w + 8 * idx)), wl);
-    unpack8<QF>(__ldg(reinterpret_cast<const uint4*>(w + 64 + 8 * idx)), wh);
+    unpack8<QF>(load8(p, w + 8 * idx, w, 2 * kD), wl);
+    unpack8<QF>(load8(p, w + 64 + 8 * idx, w, 2 * kD), wh);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) wl[i] = wh[i] = 1.f;
@@ -602,7 +617,7 @@ __device__ __forceinline__ void token_angles(const WriteParams& p, int n, const 
   float c2[2], s2[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int pos = __ldg(p.positions + (size_t)axis[j] * p.tokens + n);
+    const int pos = position(p, axis[j], n);
     sincos_turn((uint64_t)(int64_t)pos * turn[j], s2[j], c2[j]);
   }
 #pragma unroll
@@ -673,13 +688,15 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int u = u0 + i;
-        const uint16_t* src = u < kWriteQUnits ? p.q_proj + n * p.q_stride + u * 4 * kD
-                              : u < kWriteQUnits + kWriteKUnits
-                                  ? p.k_proj + n * p.k_stride + (u - kWriteQUnits) * 4 * kD
+        const bool q = u < kWriteQUnits, k = u < kWriteQUnits + kWriteKUnits;
+        const uint16_t* src = q   ? p.q_proj + n * p.q_stride + u * 4 * kD
+                              : k ? p.k_proj + n * p.k_stride + (u - kWriteQUnits) * 4 * kD
                                   : p.v_proj + n * p.v_stride + (u - kWriteQUnits - kWriteKUnits) * 4 * kD;
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + quarter * kD + 8 * idx);
-        wlo[i] = __ldg(s4);
-        whi[i] = __ldg(s4 + 8);
+        src += quarter * kD + 8 * idx;
+        const uint16_t* base = q ? p.q_proj : (k ? p.k_proj : p.v_proj);
+        const size_t bytes = q ? p.q_bytes : (k ? p.k_bytes : p.v_bytes);
+        wlo[i] = load8(p, src, base, bytes);
+        whi[i] = load8(p, src + 64, base, bytes);
       }
       RowAt at{0, 0, false};
       if (u0 + U > kWriteQUnits) at = locate(p, n);
@@ -689,21 +706,20 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
       if (u0 < kWriteQUnits + kWriteKUnits) token_angles(p, n, turn, axis, cs, sn);
       if (u0 < kWriteQUnits) {
         Coefs qc;
-        make_coefs<QF>(p.q_norm_w, idx, cs, sn, qc);
+        make_coefs<QF>(p, p.q_norm_w, idx, cs, sn, qc);
         uint16_t* dst = p.q_out + ((size_t)n * kHq + 4 * u0 + quarter) * kD + 8 * idx;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
           float zl[8], zh[8];
           fit &= rotate_unit<QF>(wlo[i], whi[i], qc, p.q_norm_w != nullptr, p.eps, zl, zh);
-          uint4* d4 = reinterpret_cast<uint4*>(dst + i * 4 * kD);
-          d4[0] = round8<QF>(zl);
-          d4[8] = round8<QF>(zh);
+          store8(p, dst + i * 4 * kD, round8<QF>(zl));
+          store8(p, dst + i * 4 * kD + 64, round8<QF>(zh));
         }
         continue;
       }
       if (u0 < kWriteQUnits + kWriteKUnits) {
         Coefs kc;
-        make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+        make_coefs<QF>(p, p.k_norm_w, idx, cs, sn, kc);
 #pragma unroll
         for (int i = 0; i < (U == 1 ? 1 : kWriteKUnits); ++i) {
           const int g = 4 * (u0 + i - kWriteQUnits) + quarter;
@@ -736,12 +752,12 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
       for (int i = 0; i < doubts; ++i) {
         const int n = list[i].x, g = 4 * list[i].y + quarter;
         const RowAt at = locate(p, n);
-        const uint4* s4 = reinterpret_cast<const uint4*>(p.k_proj + n * p.k_stride + g * kD + 8 * idx);
-        const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+        const uint16_t* src = p.k_proj + n * p.k_stride + g * kD + 8 * idx;
+        const uint4 wlo = load8(p, src, p.k_proj, p.k_bytes), whi = load8(p, src + 64, p.k_proj, p.k_bytes);
         float cs[8], sn[8], zl[8], zh[8];
         token_angles(p, n, turn, axis, cs, sn);
         Coefs kc;
-        make_coefs<QF>(p.k_norm_w, idx, cs, sn, kc);
+        make_coefs<QF>(p, p.k_norm_w, idx, cs, sn, kc);
         rotate_unit<QF>(wlo, whi, kc, p.k_norm_w != nullptr, p.eps, zl, zh);
         settle(std::false_type(), n, at, g, wlo, whi, zl, zh);
       }
@@ -759,19 +775,19 @@ __global__ void __launch_bounds__(kWriteThreads, 2) write_kv_kernel(const __grid
         if (u >= kWriteQUnits + kWriteKUnits) break;  // (values have no norm)
         const bool q = u < kWriteQUnits;
         const int g = 4 * (q ? u : u - kWriteQUnits) + quarter;
-        const uint16_t* w = q ? p.q_norm_w : p.k_norm_w;
-        const uint4* s4 =
-            reinterpret_cast<const uint4*>((q ? p.q_proj + n * p.q_stride : p.k_proj + n * p.k_stride) + g * kD + 8 * idx);
-        const uint4 wlo = __ldg(s4), whi = __ldg(s4 + 8);
+        const uint16_t *base = q ? p.q_proj : p.k_proj, *w = q ? p.q_norm_w : p.k_norm_w;
+        const size_t bytes = q ? p.q_bytes : p.k_bytes;
+        const uint16_t* src = base + n * (q ? p.q_stride : p.k_stride) + g * kD + 8 * idx;
+        const uint4 wlo = load8(p, src, base, bytes), whi = load8(p, src + 64, base, bytes);
         float cs[8], sn[8], zl[8], zh[8];
         token_angles(p, n, turn, axis, cs, sn);
         Coefs kc;
-        make_coefs<QF>(w, idx, cs, sn, kc);
+        make_coefs<QF>(p, w, idx, cs, sn, kc);
         rotate_unit<QF, true>(wlo, whi, kc, true, p.eps, zl, zh);
         if (q) {
-          uint4* d4 = reinterpret_cast<uint4*>(p.q_out + ((size_t)n * kHq + g) * kD + 8 * idx);
-          d4[0] = round8<QF>(zl);
-          d4[8] = round8<QF>(zh);
+          uint16_t* dst = p.q_out + ((size_t)n * kHq + g) * kD + 8 * idx;
+          store8(p, dst, round8<QF>(zl));
+          store8(p, dst + 64, round8<QF>(zh));
         } else {
           const RowAt at = locate(p, n);
           if (store_unit<KVF, QF>(p, 0, at.base + g * at.head, idx, at.ok, wlo, whi, zl, zh))

@@ -366,11 +366,12 @@ gqa_status_t gqa_decode_debug_skip_tile(const void* q, gqa_dtype_t q_dtype, cons
 
 /* Test hook of the range-checked build (compiled with GQA_CHECKED; not for
  * production use).  From the next launch of this process on, the extents
- * that the split kernel's range checks compare against are cut short: the
- * KV cache (or page pool) by `kv_cut_bytes` and the int8 row scales by
+ * that the range checks of the split, the many-token write and the read-back
+ * kernels compare against are cut short: the
+ * KV cache (or page pool) by `kv_cut_bytes` and the int8 or e2m1 row scales by
  * `scales_cut_bytes` (each to 0 at most).  A cache access past the cut extent
  * then sets GQA_FLAG_BOUNDS and is redirected to an address inside the
- * buffer, as a real out-of-range access would be, so a test can see the
+ * buffer (a write is left out), as a real out-of-range access would be, so a test can see the
  * checks fire without any access leaving the real buffers; outputs of such
  * launches are invalid.  0, 0 restores the true extents.  The product build
  * has no range checks: there it accepts 0, 0 and rejects anything else with

@@ -6,9 +6,9 @@ import pytest
 import torch
 
 import gqa_decode_attention_sm_gb300 as gq
-from gqa_decode_attention_sm_gb300 import inputs
-from test_gpu_cache_io import (D, DEV, HKV, HQ, TD, check_heads, gen, library, new_cache, rotated, rows_at, run_write,
-                               same_codes, tokens)
+from gqa_decode_attention_sm_gb300 import _lib, api, inputs
+from test_gpu_cache_io import (D, DEV, HKV, TD, check_heads, gen, library, new_cache, page_table,  # noqa: F401
+                               rotated, rows_at, run_write, same_codes, tokens)
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +144,53 @@ def test_e4m3_values_are_products_with_the_reciprocal(scale):
     slots = torch.zeros(n, dtype=torch.int32, device=DEV)
     gq.append_kv(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], slots, kv2, k_scale=1.0, v_scale=scale)
     assert torch.equal(kv2[:, 1, :, 0], got[:, 1])
+
+
+@pytest.mark.parametrize("what", ["write", "write scales", "read", "decode", "decode scales"])
+def test_cut_extents_make_the_checks_fire(library, what):  # noqa: F811
+    """The checked library's range checks see an access past extents that are cut short (and keep it inside the
+    real buffers); with the true extents the same call is clean.  The product library has no checks to cut."""
+    lib = _lib.load()
+    n = 512
+    t = tokens(n, 2, 256, torch.bfloat16, seed=48)
+    kv, sc = new_cache("e2m1", 2, 256)
+    table, units = page_table(2, 256, 16)
+    pages, page_sc = new_cache("e2m1", units, 16)
+    lens = torch.tensor([256, 255], dtype=torch.int32, device=DEV)
+    how = dict(k_scale=0.01, v_scale=0.01)
+
+    def run(paged):
+        ws = torch.zeros(gq.workspace_size(2, 256, 2), dtype=torch.uint8, device=DEV)
+        a = (t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"])
+        if what.startswith("write"):
+            if paged:
+                gq.write_kv_paged(*a, pages, table, kv_scales=page_sc, workspace=ws, **how)
+            else:
+                gq.write_kv(*a, kv, kv_scales=sc, workspace=ws, **how)
+        elif what == "read":
+            if paged:
+                gq.read_kv_paged(pages, table, lens, kv_scales=page_sc, workspace=ws, **how)
+            else:
+                gq.read_kv(kv, lens, kv_scales=sc, workspace=ws, **how)
+        elif paged:
+            gq.gqa_decode_paged(t["q"][:2], pages, table, lens, num_splits=2, workspace=ws, kv_scales=page_sc, **how)
+        else:
+            gq.gqa_decode_fp4kv(t["q"][:2], kv, sc, lens, num_splits=2, workspace=ws, **how)
+        return gq.get_status(ws)
+
+    for paged, codes, scales in ((False, kv, sc), (True, pages, page_sc)):
+        cut = (0, scales.numel() // 2) if what.endswith("scales") else (codes.numel() // 2, 0)
+        if library == "product":
+            assert lib.gqa_decode_debug_cut_extents(*cut) == 1
+            continue
+        before = codes.clone()
+        try:
+            assert lib.gqa_decode_debug_cut_extents(*cut) == 0
+            flags = run(paged)
+        finally:
+            assert lib.gqa_decode_debug_cut_extents(0, 0) == 0
+        assert flags & api.FLAG_BOUNDS and not flags & api.FLAG_WAIT_TIMEOUT, hex(flags)
+        if what.startswith("write"):  # nothing behind the cut is written
+            assert torch.equal(codes[codes.shape[0] // 2 + 1:], before[codes.shape[0] // 2 + 1:])
+            assert torch.equal(codes[-1], before[-1])
+        assert not run(paged) & api.FLAG_BOUNDS
