@@ -28,7 +28,8 @@
 // within 2^-33 of a turn.  The top two bits (after adding an eighth of a turn)
 // are the quadrant; sin and cos of the rest, |x| <= pi/4, are the Taylor series
 // to x^9 and x^10 (first terms left out below 2^-28) at the FP32 next to x, and
-// one step along the derivative to x itself: within about 2^-24.
+// one step along the derivative to x itself: within 1.5 * 2^-24 (a CPU test goes
+// through the same operations).
 //
 // e2m1 keys are rounded as the exact z would be.  The FP32 z is off by at most
 // kKeyError of the head's largest magnitude; where that could turn a group's
@@ -245,15 +246,19 @@ __device__ __forceinline__ void scale_head(float (&xl)[8], float (&xh)[8], float
   eps = eps * k * k;
 }
 
-// The bound of |FP32 z - z| as a share of the head's largest |z|, A:
-//   cos and sin within 2^-24, their products with a weight and the one rounded
-//   product of the rotation: 3 * 2^-24 (|y_i cos| + |y_j sin|), at most 3 * 2^-24
-//   of the pair's length, itself at most sqrt(2) A; two more roundings of z
-//   r: the sum of squares (4 levels in a lane, 3 over the lanes, 8 roundings, half
-//   of them in the root), 1 / 128 and eps, rsqrt and its Newton step: 6.5 * 2^-24
-// together 12.8 * 2^-24; 3 * 2^-24 more where a quotient is formed from z, and a
-// little to spare.
-constexpr float kKeyError = 0x1.2p-20f;
+// The bound of |FP32 z - z| as a share of the head's largest |z|, A, in units of
+// 2^-24 (a rounding is one of what it rounds, at most; P is the pair's length, at
+// most sqrt(2) A; |y_i| + |y_j| <= sqrt(2) P and |y_i cos| + |y_j sin| <= P):
+//   cos and sin off by 1.5, whatever their size: 1.5 (|y_i| + |y_j|)     2.2 P
+//   their products with a weight: |y_i cos| + |y_j sin|                    1 P
+//   the rotation's one rounded product: |y_j sin|                          1 P
+//   (4.2 P: 5.9 A) the rotation's sum and the product with r               2 A
+//   r: 9 roundings of mean(x^2) + eps (5 in a lane, 3 over the lanes, eps), half of
+//   them in the root, and 1.5 of the Newton step                           6 A
+// together 13.9; 4 more where a quotient is formed from z (amax +- e, 6 k_scale, its
+// reciprocal, the product).  The constant is 22, which also covers an eps past 2^60
+// (no Newton step: 4 instead of 1.5).
+constexpr float kKeyError = 0x1.6p-20f;
 
 struct KeyCodes {
   uint32_t lo, hi;  // codes of dims 8i..8i+7 and 64+8i..
