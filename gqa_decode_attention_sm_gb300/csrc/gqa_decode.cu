@@ -818,13 +818,17 @@ gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* sta
   if (st != GQA_OK) return st;
   if (!aligned(out, 16) || !aligned(lens, 4) || !aligned(starts, 4))
     return fail(GQA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned, lens and starts 4-byte");
+  // nothing that is written (out, the status word) overlaps anything else
   const size_t out_bytes = (size_t)c.batch * 2 * kHkv * out_capacity * kD * 2, b4 = (size_t)c.batch * 4;
-  if (overlap(out, out_bytes, c.kv, c.kv_bytes()) || overlap(out, out_bytes, lens, b4) ||
-      (starts && overlap(out, out_bytes, starts, b4)) ||
-      (c.scale_bytes() && overlap(out, out_bytes, c.scales, c.scale_bytes())) ||
-      (c.block_table && overlap(out, out_bytes, c.block_table, c.table_bytes())) ||
-      (workspace && overlap(out, out_bytes, workspace, GQA_WORKSPACE_HEADER_BYTES)))
-    return fail(GQA_ERR_ALIASING, "out overlaps the cache, its scales, the lengths, the block table or the workspace");
+  const size_t ws_bytes = workspace ? (size_t)GQA_WORKSPACE_HEADER_BYTES : 0;
+  const struct { const void* p; size_t bytes; } ins[] = {
+      {c.kv, c.kv_bytes()}, {c.scales, c.scale_bytes()}, {lens, b4}, {starts, starts ? b4 : 0},
+      {c.block_table, c.table_bytes()}};
+  for (const auto& in : ins)
+    if (in.bytes && (overlap(out, out_bytes, in.p, in.bytes) || (ws_bytes && overlap(workspace, ws_bytes, in.p, in.bytes))))
+      return fail(GQA_ERR_ALIASING, "out or the workspace overlaps the cache, its scales, the lengths or the block table");
+  if (ws_bytes && overlap(out, out_bytes, workspace, ws_bytes))
+    return fail(GQA_ERR_ALIASING, "out overlaps the workspace");
   int sms = 0;
   st = current_device_ready(&sms);
   if (st != GQA_OK) return st;

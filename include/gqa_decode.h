@@ -499,8 +499,8 @@ gqa_status_t gqa_write_kv_paged(const void* q_proj, const void* k_proj, const vo
  * a 16-bit cache's is the value itself (the scales are not used).  lens and starts int32 [batch], device memory;
  * starts may be NULL (0).  A length outside [0, capacity] or a start outside
  * [0, length] is clamped and sets GQA_FLAG_LENGTH_CLAMPED in the header of the
- * workspace, if one is given.  kv and out 16-byte aligned; out overlaps
- * nothing else.  One launch, no allocation, no host sync. */
+ * workspace, if one is given.  kv and out 16-byte aligned; neither out nor the
+ * workspace overlaps anything else.  One launch, no allocation, no host sync. */
 gqa_status_t gqa_read_kv(const void* kv, gqa_kv_format_t kv_format, const void* kv_scales,
                          const int32_t* lens, const int32_t* starts, void* out, gqa_dtype_t out_dtype,
                          int batch, int capacity, int out_capacity, float k_scale, float v_scale,

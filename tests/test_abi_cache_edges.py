@@ -5,7 +5,7 @@ import sys
 import torch
 
 from gqa_decode_attention_sm_gb300 import _lib, api, build
-from test_abi_fp4 import EINVAL, P, _write, lib  # noqa: F401
+from test_abi_fp4 import EALIAS, EINVAL, P, _write, lib  # noqa: F401
 
 E4M3 = 2
 
@@ -49,3 +49,16 @@ def test_importing_the_package_loads_no_binary():
             "assert api._binding() is not None and any(x.endswith('_native.so') for x in maps())\n")
     build.build_native()
     subprocess.run([sys.executable, "-c", code], check=True, cwd=build.ROOT)
+
+
+def test_a_read_backs_workspace_overlaps_no_input(lib):  # noqa: F811
+    # (a flag set in it would change the cache or the lengths)
+    def call(ws, paged=False):
+        kv, sc, lens, starts, out, table = P[:6]
+        if paged:
+            return lib.gqa_read_kv_paged(kv, 4, sc, table, 4, 16, 64, lens, starts, out, 1, 2, 64, 1.0, 1.0, ws, 256, None)
+        return lib.gqa_read_kv(kv, 4, sc, lens, starts, out, 1, 2, 64, 64, 1.0, 1.0, ws, 256, None)
+
+    for ws in (P[0] + 64, P[1], P[2] - 252, P[3], P[4] - 128):
+        assert call(ws) == EALIAS and call(ws, True) == EALIAS
+    assert call(P[5], True) == EALIAS
