@@ -2,6 +2,7 @@
 import subprocess
 import sys
 
+import pytest
 import torch
 
 from gqa_decode_attention_sm_gb300 import _lib, api, build
@@ -62,3 +63,16 @@ def test_a_read_backs_workspace_overlaps_no_input(lib):  # noqa: F811
     for ws in (P[0] + 64, P[1], P[2] - 252, P[3], P[4] - 128):
         assert call(ws) == EALIAS and call(ws, True) == EALIAS
     assert call(P[5], True) == EALIAS
+
+
+@pytest.mark.parametrize("which", ["build", "build_checked", "build_native"])
+def test_a_build_that_fails_is_told_even_beside_an_older_binary(which, monkeypatch):
+    import __graft_entry__ as entry
+
+    def broken(**kw):
+        raise subprocess.CalledProcessError(1, "nvcc")
+
+    for name in ("build", "build_checked", "build_native"):
+        monkeypatch.setattr(build, name, broken if name == which else lambda **kw: None)
+    with pytest.raises(subprocess.CalledProcessError):
+        entry.build()
