@@ -7,8 +7,8 @@ import torch
 
 import gqa_decode_attention_sm_gb300 as gq
 from gqa_decode_attention_sm_gb300 import _lib, api, inputs
-from test_gpu_cache_io import (D, DEV, HKV, TD, check_heads, gen, library, new_cache, page_table,  # noqa: F401
-                               rotated, rows_at, run_write, same_codes, tokens)
+from test_gpu_cache_io import (D, DEV, HKV, TD, check_heads, check_written, gen, library, new_cache,  # noqa: F401
+                               page_table, rotated, rows_at, run_write, same_codes, tokens)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,21 +104,22 @@ def test_values_whose_quotient_is_next_to_the_largest_float():
     check_e2m1(got, gsc, 1, t["v"].double(), found)
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1", "e4m3", "i8"])
 @pytest.mark.parametrize("mag,eps", [(1e30, 1e-6), (3e36, 1e-6), (1e-25, 0.0), (1e-36, 0.0), (1e-12, 1e-24),
                                      (1e-30, 1e-30), (1e-12, 1e-38)])
 @pytest.mark.parametrize("n", [40, 1000])
 def test_norms_whose_squares_leave_fp32(fmt, mag, eps, n):
     t = tokens(n, 1, n, torch.bfloat16, seed=46, mag=mag / 20)
     t["pos"] = (torch.arange(n, device=DEV) % 1000).to(torch.int32)
+    t["v"] = torch.randn(t["v"].shape, generator=gen(49), device=DEV).to(torch.bfloat16)  # (values have no norm)
     q_out, kv, sc, before, table, flags = run_write(t, fmt, 1, n, ks=10 / 1024, vs=1.0, eps=eps)
     check_heads(q_out, rotated(t["q"], t["qw"], t["pos"], eps=eps))
     got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
     z = rotated(t["k"], t["kw"], t["pos"], eps=eps)
-    if fmt == "bf16":
-        check_heads(got[:, 0], z)
-    else:
+    if fmt == "e2m1":
         check_e2m1(got, gsc, 0, z, 10 / 1024)
+    else:
+        check_written(fmt, torch.bfloat16, got, gsc, z, t["v"], 10 / 1024, 1.0)
 
 
 @pytest.mark.parametrize("scale", [0.01, 0.02, 0.7, 1.3, 41.0, 2.0 ** -5])
