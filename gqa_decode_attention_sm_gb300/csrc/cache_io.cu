@@ -50,7 +50,8 @@ cudaError_t launch_write_kv(const WriteParams& p, int kvf, int qf, int sms, cuda
   // where the cache's rounding makes a part of four units long.  In a CUDA graph,
   // us, units / parts: bf16 64 tokens 2.4 / 2.6, 200 2.5 / 3.1, 256 3.4 / 3.1, 768
   // 5.6 / 3.5; int8 64 3.0 / 5.0, 512 5.1 / 6.1, 768 6.9 / 5.9; e2m1 64 4.2 / 7.2,
-  // 512 7.1 / 8.5, 768 8.9 / 8.2.
+  // 512 7.1 / 8.5, 768 8.9 / 8.2; e4m3, which rounds by one instruction, as the
+  // 16-bit caches: 256 3.4 / 3.1, 512 4.6 / 3.6.
   const long long waves = kvf == kKvI8 || kvf == kKvE2M1 ? 3 : 1;
   return (long long)p.tokens * kWriteUnits <= waves * 2 * kWriteWarps * sms
              ? launch_write_u<1>(p, kvf, qf, sms, stream)

@@ -267,6 +267,18 @@ __device__ __forceinline__ float2 bf16x2_to_f32x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
+// Two FP32 values -> fp16 or bf16 (QFormat), to the nearest, lo in the low half.
+template <int QF>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  if constexpr (QF == kQF16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
 // Two e4m3 bytes (low byte = first element) -> f16x2 with the hardware
 // conversion; every e4m3 value is exact in fp16.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t two) {

@@ -37,17 +37,6 @@ struct ReadParams {
   size_t kv_rows;  // rows of 128 in the cache, for checked builds
 };
 
-template <int OF>
-__device__ __forceinline__ uint32_t read_round2(float lo, float hi) {
-  if constexpr (OF == kQF16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
 template <int KVF, int OF>
 __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_constant__ ReadParams p) {
   pdl_launch_dependents();
@@ -107,7 +96,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
           o[i] = w[i];
         } else {
           const float2 f = KVF == kKvF16 ? f16x2_to_f32x2(w[i]) : bf16x2_to_f32x2(w[i]);
-          o[i] = read_round2<OF>(f.x, f.y);
+          o[i] = round2<OF>(f.x, f.y);
         }
       }
     } else {
@@ -140,7 +129,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_cons
       }
       // code * scale is exact; then the tensor scale, rounded once in FP32
 #pragma unroll
-      for (int i = 0; i < kReadElems / 2; ++i) o[i] = read_round2<OF>(x[2 * i] * sc * all, x[2 * i + 1] * sc * all);
+      for (int i = 0; i < kReadElems / 2; ++i) o[i] = round2<OF>(x[2 * i] * sc * all, x[2 * i + 1] * sc * all);
     }
     uint16_t* out = static_cast<uint16_t*>(p.out);
     const size_t at = (((size_t)b * 2 * kHkv + pg) * p.out_capacity + j) * kD + e * kReadElems;

@@ -127,16 +127,6 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 template <int QF>
-__device__ __forceinline__ uint32_t round2(float lo, float hi) {
-  if constexpr (QF == kQF16) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <int QF>
 __device__ __forceinline__ uint4 round8(const float (&z)[8]) {
   return make_uint4(round2<QF>(z[0], z[1]), round2<QF>(z[2], z[3]), round2<QF>(z[4], z[5]), round2<QF>(z[6], z[7]));
 }
