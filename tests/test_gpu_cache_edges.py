@@ -92,7 +92,8 @@ def test_values_whose_quotient_is_next_to_the_largest_float():
         vs = f(f(2.0 ** -10) / f(6)) + f(k - 1000) * f(2.0 ** -36)
         d6 = f(6) * f(vs)
         inv = f(1) / d6
-        q = f(2.0 ** 118) * inv
+        with np.errstate(over="ignore"):
+            q = f(2.0 ** 118) * inv
         if np.isfinite(q) and q.view(np.uint32) >= 0x7F7FFFC0:
             found = float(f(vs))
             break
@@ -195,3 +196,38 @@ def test_cut_extents_make_the_checks_fire(library, what):  # noqa: F811
             assert torch.equal(codes[codes.shape[0] // 2 + 1:], before[codes.shape[0] // 2 + 1:])
             assert torch.equal(codes[-1], before[-1])
         assert not run(paged) & api.FLAG_BOUNDS
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_random_sizes_zeros_and_specials(seed):
+    # groups of a head up to 2^60 apart (fp16: 2^14), zeros, powers of two (ties), infinities and NaN; positions below
+    # 64, where the definition's angles are good to 2^-47
+    rng, g = np.random.default_rng(seed), gen(seed + 60)
+    dtype = [torch.float16, torch.bfloat16][rng.integers(2)]
+    n = int(np.exp(rng.uniform(0, np.log(2500))))
+    t = tokens(n, 1, n, dtype, seed=seed)
+    t["pos"] = torch.randint(0, int(rng.integers(1, 64)), (n,), generator=g, device=DEV).to(torch.int32)
+    wide, middle = (14, 0.0) if dtype == torch.float16 else (60, float(rng.uniform(-60, 60)))
+    for name, heads in (("q", 32), ("k", 8), ("v", 8)):
+        e = middle - torch.rand((n, heads, 8, 1), generator=g, device=DEV) * (wide * float(rng.random()))
+        x = torch.randn((n, heads, 8, 16), generator=g, device=DEV) * torch.exp2(e)
+        x[torch.rand(x.shape, generator=g, device=DEV) < float(rng.choice([0, 0.3, 0.9]))] = 0
+        if rng.random() < 0.3:
+            x = torch.exp2(torch.round(torch.log2(x.abs().clamp(min=1e-38)))) * torch.sign(x)
+        if rng.random() < 0.4:
+            x[torch.rand(x.shape, generator=g, device=DEV) < 1e-3] = float(rng.choice([math.inf, -math.inf, math.nan]))
+        t[name] = x.flatten(2).to(dtype).contiguous()
+    norm, eps = bool(rng.random() < 0.6), float(rng.choice([1e-6, 0.0, 1e-20, 1.0]))
+    z = rotated(t["k"], t["kw"] if norm else None, t["pos"], eps=eps)
+    scale = []
+    for x in (z, t["v"].double()):
+        top = torch.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0).abs().max() * 2.0 ** float(rng.uniform(-3, 3)) / 2688
+        scale.append(float(np.float32(min(2.0 ** 99, max(2.0 ** -99, float(top))))))
+    q_out, kv, sc, before, table, flags = run_write(t, "e2m1", 1, n, norm=norm, ks=scale[0], vs=scale[1], eps=eps)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_e2m1(got, gsc, 0, z, scale[0])
+    check_e2m1(got, gsc, 1, t["v"].double(), scale[1])
+    zq = rotated(t["q"], t["qw"] if norm else None, t["pos"], eps=eps)
+    heads = torch.isfinite(zq).all(-1) & (zq.abs().amax(-1) < torch.finfo(dtype).max / 2)
+    check_heads(q_out[heads], zq[heads])
+    assert torch.isnan(q_out[torch.isnan(zq)]).all()
