@@ -337,8 +337,9 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 // What bounds it: the arithmetic.  Per 16 tokens a warp issues 64 conversions
 // (integer pipe, 2 clocks each on an SM quarter), 64 f16 multiplications (2
 // clocks, and they hold up the mma: 16 mma alone take 129 clocks, with 64
-// multiplications 229) and 16 mma (8 clocks).  At 8 x 131072 a call takes 194
-// us; with its copies left out 188, with its arithmetic left out 175.  Taking
+// multiplications 229) and 16 mma (8 clocks).  At 8 x 131072 a call takes 191
+// us; it took 194 when, with its copies left out, it took 188, and with its
+// arithmetic left out 175.  Taking
 // 32 tokens a step instead of 16 was worth 6 %; a second accumulator chain for
 // the scores, more CTAs per SM or larger tiles nothing.  Scaling the weights
 // instead of V would need an m-tile's 16 dims in one scale group, which rows in

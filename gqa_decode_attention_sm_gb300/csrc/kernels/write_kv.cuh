@@ -34,7 +34,7 @@
 // e2m1 keys are rounded as the exact z would be.  The FP32 z is off by at most
 // kKeyError of the head's largest magnitude; where that could turn a group's
 // scale or a code (the two ends of the interval round apart), the unit goes on the
-// warp's list (about one unit of four heads in fifty), and the warp forms its
+// warp's list (about one unit of four heads in 45), and the warp forms its
 // elements in doubt again, exactly enough, when its tokens are done.  (Called
 // where the doubt arises, that code cost every unit its registers: 4096 tokens
 // into an fp4 cache and back 55 us, without any of it 39.)  Values are exact

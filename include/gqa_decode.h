@@ -453,10 +453,11 @@ gqa_status_t gqa_append_kv_paged(const void* q_proj, const void* k_proj, const v
  * s = e4m3(amax(|x|) / (6 k_scale)) (v_scale for values; to the nearest,
  * saturating at 448) and the codes nearest to x / (s k_scale), ties to the
  * even code, saturating at 6; s = 0 gives codes 0.  Scales and codes are those
- * of the exact z and v; an infinite element saturates, and 16 dims with a NaN
- * among them get the NaN scale 0x7f (their codes are any): they read back as
- * NaN.  kv as gqa_decode's, [batch, 2, 8, capacity, 128]
- * (e2m1: 64 bytes a row).  A row outside [0, batch) or a slot outside
+ * of the exact v, and of the exact z (known to 2^-43 of the head's largest |z|
+ * and an angle of 2^-64 of a turn a position: nearer to a tie than that, either
+ * neighbour).  An infinite element saturates, and 16 dims with a NaN among them
+ * get the NaN scale 0x7f (their codes are any): they read back as NaN.  kv as
+ * gqa_decode's, [batch, 2, 8, capacity, 128] (e2m1: 64 bytes a row).  A row outside [0, batch) or a slot outside
  * [0, capacity) writes nothing to the cache (q_out is still written) and sets
  * GQA_FLAG_SLOT_CLAMPED in the workspace's header, if there is one: a padded
  * batch gives its padding slot -1.  tokens = 0 does nothing.  Pointers are
