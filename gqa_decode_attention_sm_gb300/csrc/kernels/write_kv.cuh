@@ -214,8 +214,8 @@ __device__ __forceinline__ float mean_square(const float (&xl)[8], const float (
 }
 // FP32 holds the squares of such a head, and a sum of them, well inside its range:
 // so it is for fp16 at any size, for bf16 from about 2^-30 (with a smaller eps) to
-// 2^30.
-__device__ __forceinline__ bool squares_fit(float ss) { return ss > 0x1p-60f && ss < 0x1p60f; }
+// 2^30.  (A NaN stays one either way: padding often holds some.)
+__device__ __forceinline__ bool squares_fit(float ss) { return !(ss <= 0x1p-60f || ss >= 0x1p60f); }
 // A head whose squares do not fit is scaled by the power of two k that brings its
 // largest element, or the root of eps, to [1, 2), and eps by k^2: the normalised
 // head is the same.  A head of zeros without eps, and one with an infinite element,
@@ -563,7 +563,7 @@ __device__ __forceinline__ bool store_unit(const WriteParams& p, int plane, size
       uint32_t ul, uh;
       key_codes(xl, e, k.slo, p.k_scale, k.lo, ul);
       key_codes(xh, e, k.shi, p.k_scale, k.hi, uh);
-      doubt = !__all_sync(0xffffffffu, sure && (ul | uh) == 0u);
+      doubt = ok && !__all_sync(0xffffffffu, sure && (ul | uh) == 0u);  // (ok is the token's, the warp's)
     } else {
       // values are the inputs themselves: exact
       const float al = amax8_nan(xl), ah = amax8_nan(xh);

@@ -231,3 +231,24 @@ def test_random_sizes_zeros_and_specials(seed):
     heads = torch.isfinite(zq).all(-1) & (zq.abs().amax(-1) < torch.finfo(dtype).max / 2)
     check_heads(q_out[heads], zq[heads])
     assert torch.isnan(q_out[torch.isnan(zq)]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1", "i8"])
+@pytest.mark.parametrize("n", [60, 2000])
+def test_padding_may_hold_anything(fmt, n):
+    # the tokens of slot -1 are NaN, infinite and huge: the others are what they are without them
+    t = tokens(n, 1, n, torch.bfloat16, seed=55)
+    pad = torch.rand(n, generator=gen(56), device=DEV) < 0.5
+    t["pos"] = (torch.arange(n, device=DEV) % 5000).to(torch.int32)
+    for name in "qkv":
+        junk = torch.randint(-32768, 32768, t[name].shape, generator=gen(57), device=DEV).to(torch.int16)
+        t[name][pad] = junk.view(torch.bfloat16)[pad]
+    t["slots"][pad] = -1
+    t["pos"][pad] = torch.randint(-2 ** 31, 2 ** 31 - 1, (int(pad.sum()),), generator=gen(58), device=DEV).to(torch.int32)
+    q_out, kv, sc, before, table, flags = run_write(t, fmt, 1, n, ks=10 / 1024, vs=9 / 1024)
+    assert flags == api.FLAG_SLOT_CLAMPED
+    check_heads(q_out[~pad], rotated(t["q"], t["qw"], t["pos"])[~pad])
+    got, gsc, (r, s) = rows_at(kv, sc, None, 0, t["rows"][~pad], t["slots"][~pad])
+    check_written(fmt, torch.bfloat16, got, gsc, rotated(t["k"], t["kw"], t["pos"])[~pad], t["v"][~pad], 10 / 1024, 9 / 1024)
+    before[0][r, :, :, s] = got
+    assert torch.equal(before[0].view(torch.uint8), kv.view(torch.uint8))
