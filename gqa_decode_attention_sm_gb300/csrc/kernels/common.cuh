@@ -88,9 +88,9 @@ __host__ __device__ inline int split_count(int capacity, int num_splits, int kv_
 // Checked builds (compiled with -DGQA_CHECKED; the product library is not):
 // every global-memory access whose place is computed (cache rows and scales,
 // partial results, outputs, and in the write and read-back kernels every load and
-// store) is tested against the extent of its buffer first.  One outside it sets GQA_FLAG_BOUNDS in the status word
-// and is redirected to an address inside the buffer, so a bad index is
-// reported and nothing faults.  The tests run their cases through such a
+// store) is tested against the extent of its buffer first.  One outside it sets
+// GQA_FLAG_BOUNDS in the status word and is redirected to an address inside the
+// buffer (or left out), so a bad index is reported and nothing faults.  The tests run their cases through such a
 // build and require the flag never to be set.
 #ifdef GQA_CHECKED
 constexpr bool kChecked = true;

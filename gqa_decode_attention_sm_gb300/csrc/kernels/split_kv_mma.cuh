@@ -359,8 +359,8 @@ __device__ __forceinline__ int qk_dim(int cq, int ks, int pair /*0: a0/b0, 1: a2
 // some lane's score exceeds that limit (a vote), which after a piece's first tiles
 // is rare.  The scores that it is looked for in are then rounded before m is taken
 // off: above 2^24 an FMA would leave the product's rounding, many powers of two,
-// in the largest one's weight.  Masked tokens take weight 0 by selection; a token past the tile's rows
-// also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
+// in the largest one's weight.  Masked tokens take weight 0 by selection; a token
+// past the tile's rows also takes V scale 0 (its stale scale could be NaN; K's reaches only scores
 // that are masked).
 constexpr int kFp4Tokens = 32;
 constexpr float kFp4Shift = 15.f, kFp4Limit = 15.5f;

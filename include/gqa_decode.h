@@ -394,7 +394,8 @@ gqa_status_t gqa_decode_debug_cut_extents(uint64_t kv_cut_bytes, uint64_t scales
  * and product in FP32, RNE, saturating: the code of value / scale but where that
  * lies within 2^-23 of itself of a tie, and either neighbour there) or
  * int8 (codes round-to-nearest-even of value / scale with a fresh bf16 row
- * scale amax/127 written to kv_scales, clipped to +-127) or e2m1 (as
+ * scale amax/127 written to kv_scales, clipped to +-127; a NaN among other
+ * numbers gets code 0) or e2m1 (as
  * gqa_write_kv, whose rules for alignment and rope_theta then hold too).  positions and
  * slots are int32 [batch] in device memory, read only by the kernel; a slot
  * outside [0, capacity) is not written and, when a workspace is given, sets

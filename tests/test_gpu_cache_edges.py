@@ -252,3 +252,91 @@ def test_padding_may_hold_anything(fmt, n):
     check_written(fmt, torch.bfloat16, got, gsc, rotated(t["k"], t["kw"], t["pos"])[~pad], t["v"][~pad], 10 / 1024, 9 / 1024)
     before[0][r, :, :, s] = got
     assert torch.equal(before[0].view(torch.uint8), kv.view(torch.uint8))
+
+
+def test_threads_on_their_own_streams():
+    # calls release the interpreter: four threads at once, each with its own cache, theta and stream
+    import threading
+    n, C = 96, 128
+    jobs, errors = [], []
+    for k in range(4):
+        t = tokens(n, 1, C, torch.bfloat16, seed=70 + k)
+        kv, sc = new_cache("e2m1", 1, C, seed=k)
+        jobs.append((t, kv, sc, 1e4 * (k + 1)))
+
+    def chain(t, kv, sc, theta):
+        how = dict(k_scale=0.01, v_scale=0.01, kv_scales=sc)
+        lens = torch.tensor([C], dtype=torch.int32, device=DEV)
+        q = gq.write_kv(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"], kv, rope_theta=theta, **how)
+        ws = torch.zeros(gq.workspace_size(1, C, 2), dtype=torch.uint8, device=DEV)
+        out = gq.gqa_decode_fp4kv(q[:1], kv, sc, lens, 0.01, 0.01, out=torch.empty_like(q[:1]), num_splits=2, workspace=ws)
+        back = gq.read_kv(kv, lens, out=torch.zeros((1, 2, HKV, C, D), dtype=torch.float16, device=DEV), **how)
+        return q, kv.clone(), sc.clone(), out, back
+
+    want = [chain(*j) for j in jobs]
+    torch.cuda.synchronize()
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = chain(*jobs[k])
+                    stream.synchronize()
+                    assert all(torch.equal(a, b) for a, b in zip(got, want[k]))
+                    with pytest.raises(gq.GqaError, match="rope_theta"):  # the message is the thread's own
+                        chain(*jobs[k][:3], 0.25 * (k + 1) if k < 3 else -1.0)
+        except BaseException as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not errors, errors
+
+
+def test_the_largest_batch_and_page(library):  # noqa: F811
+    # 65535 rows of 16 slots: the last rows' grid coordinates
+    B, C, n = 65535, 16, 64
+    kv = torch.zeros((B, 2, HKV, C, 64), dtype=torch.uint8, device=DEV)
+    sc = torch.zeros((B, 2, HKV, C, 8), dtype=torch.uint8, device=DEV)
+    t = tokens(n, 1, n, torch.bfloat16, seed=80)
+    t["rows"] = (B - 1 - torch.arange(n, device=DEV) // C).to(torch.int32)
+    t["slots"] = (torch.arange(n, device=DEV) % C).to(torch.int32)
+    ws = torch.zeros(gq.workspace_size(B, C, 1), dtype=torch.uint8, device=DEV)
+    how = dict(k_scale=0.01, v_scale=0.01, kv_scales=sc)
+    gq.write_kv(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"], kv, workspace=ws, **how)
+    got, gsc, _ = rows_at(kv, sc, None, 0, t["rows"], t["slots"])
+    check_written("e2m1", torch.bfloat16, got, gsc, rotated(t["k"], t["kw"], t["pos"]), t["v"], 0.01, 0.01)
+    lens = torch.full((B,), C, dtype=torch.int32, device=DEV)
+    back = gq.read_kv(kv, lens, out=torch.ones((B, 2, HKV, C, D), dtype=torch.bfloat16, device=DEV), workspace=ws, **how)
+    assert not back[:B - n // C].any()
+    tail = torch.stack([inputs.dequantise_e2m1(kv[B - n // C:, p], sc[B - n // C:, p], 1.0) for p in (0, 1)], 1)
+    assert torch.equal(back[B - n // C:], (tail.float() * float(np.float32(0.01))).bfloat16())
+    q = torch.randn((B, 32, D), generator=gen(81), device=DEV).to(torch.bfloat16)
+    out = gq.gqa_decode_fp4kv(q, kv, sc, lens, 0.01, 0.01, num_splits=1, workspace=ws)
+    assert not out[:B - n // C].any()
+    assert gq.get_status(ws) == 0
+    x = back[-1].double()
+    s = torch.einsum("ghd,gtd->ght", q[-1].double().view(8, 4, D), tail[-1, 0] * 0.01) / math.sqrt(D)
+    ref = torch.einsum("ght,gtd->ghd", torch.softmax(s, -1), tail[-1, 1] * 0.01).reshape(32, D)
+    assert ((out[-1].double() - ref).abs() <= ref.abs() * 2 ** -8 + x[1].abs().max() * 2 ** -10).all()
+    del kv, sc, back, q, out
+    # pages of 65536 slots, the last slots of the second page of a row
+    P = 65536
+    kv, sc = new_cache("e2m1", 3, P, seed=82)
+    table = torch.tensor([[2, 0]], dtype=torch.int32, device=DEV)
+    t["rows"].zero_()
+    t["slots"] = (2 * P - n + torch.arange(n, device=DEV)).to(torch.int32)
+    gq.write_kv_paged(t["q"], t["k"], t["v"], t["qw"], t["kw"], t["pos"], t["rows"], t["slots"], kv, table, k_scale=0.01,
+                      v_scale=0.01, kv_scales=sc, workspace=ws)
+    got, gsc, _ = rows_at(kv, sc, table, P, t["rows"], t["slots"])
+    check_written("e2m1", torch.bfloat16, got, gsc, rotated(t["k"], t["kw"], t["pos"]), t["v"], 0.01, 0.01)
+    lens = torch.tensor([2 * P], dtype=torch.int32, device=DEV)
+    out = gq.read_kv_paged(kv, table, lens, starts=lens - 2 * n, out=torch.zeros((1, 2, HKV, 2 * n, D), dtype=torch.float16,
+                           device=DEV), k_scale=0.01, v_scale=0.01, kv_scales=sc, workspace=ws)
+    x = torch.stack([inputs.dequantise_e2m1(kv[0, p, :, -2 * n:], sc[0, p, :, -2 * n:], 1.0) for p in (0, 1)])
+    assert torch.equal(out[0], (x.float() * float(np.float32(0.01))).half())
+    assert gq.get_status(ws) == 0
