@@ -24,6 +24,9 @@ EXPORTS = (
     "gqa_decode_debug_cut_extents", "gqa_decode_int8kv", "gqa_decode_paged",
     "gqa_decode_verify", "gqa_append_kv", "gqa_append_kv_paged", "gqa_decode_fp4kv",
     "gqa_write_kv", "gqa_write_kv_paged", "gqa_read_kv", "gqa_read_kv_paged",
+    "gqa_prefill_workspace_size", "gqa_prefill", "gqa_prefill_paged", "gqa_verify_drafts",
+    "gqa_weights_workspace_size", "gqa_accumulate_weights", "gqa_accumulate_weights_paged",
+    "gqa_evict_workspace_size", "gqa_evict_kv", "gqa_evict_kv_paged",
 )
 
 
@@ -67,6 +70,16 @@ def _declare(lib):
                                    f, p, sz, p]),
         "gqa_read_kv": (i, [p, i, p, p, p, p, i, i, i, i, f, f, p, sz, p]),
         "gqa_read_kv_paged": (i, [p, i, p, p, i, i, i, p, p, p, i, i, i, f, f, p, sz, p]),
+        "gqa_prefill_workspace_size": (sz, []),
+        "gqa_prefill": (i, [p, i, p, i, p, p, p, p, i, i, i, f, f, f, p, sz, p]),
+        "gqa_prefill_paged": (i, [p, i, p, i, p, p, i, i, i, p, p, p, i, i, f, f, f, p, sz, p]),
+        "gqa_verify_drafts": (i, [p, ll, ll, p, ll, ll, i, p, p, p, p, p, p, i, i, i, p, sz, p]),
+        "gqa_weights_workspace_size": (sz, [i, i, i]),
+        "gqa_accumulate_weights": (i, [p, i, p, i, p, p, p, i, i, i, f, f, i, p, sz, p]),
+        "gqa_accumulate_weights_paged": (i, [p, i, p, i, p, p, i, i, i, p, p, i, i, f, f, i, p, sz, p]),
+        "gqa_evict_workspace_size": (sz, [i, i]),
+        "gqa_evict_kv": (i, [p, i, p, p, p, p, p, p, p, p, i, i, i, i, i, i, i, p, sz, p]),
+        "gqa_evict_kv_paged": (i, [p, i, p, p, i, i, i, p, p, p, i, p, p, p, i, i, i, i, i, p, sz, p]),
         "gqa_decode_debug_skip_tile": (i, [p, i, p, i, p, p, i, i, f, f, f, i, p, sz, i,
                                            ctypes.c_uint64, p]),
         "gqa_decode_debug_cut_extents": (i, [ctypes.c_uint64, ctypes.c_uint64]),

@@ -69,6 +69,8 @@ _FP8 = (torch.uint8, torch.float8_e4m3fn)
 __all__ = ["GqaError", "append_kv_paged", "gqa_decode", "gqa_decode_fp8kv", "gqa_decode_int8kv", "gqa_decode_paged",
            "gqa_decode_verify", "gqa_decode_fp4kv", "append_kv",
            "write_kv", "write_kv_paged", "read_kv", "read_kv_paged",
+           "gqa_prefill", "gqa_prefill_paged", "verify_drafts", "accumulate_weights", "accumulate_weights_paged",
+           "evict_kv", "evict_kv_paged", "prefill_workspace_size", "weights_workspace_size", "evict_workspace_size",
            "prepare", "launch",
            "Prepared",
            "workspace_size", "plan", "get_status", "split_stage", "combine_stage", "split_geometry",
@@ -740,6 +742,280 @@ def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None
             return _result(done)
     return _read(kv_pages, block_table, True, sequence_lengths, starts, out, dtype, k_scale, v_scale, kv_scales,
                  workspace)
+
+
+def prefill_workspace_size() -> int:
+    return int(_lib.load().gqa_prefill_workspace_size())
+
+
+def weights_workspace_size(batch: int, capacity: int, q_len: int = 1) -> int:
+    n = _lib.load().gqa_weights_workspace_size(batch, capacity, q_len)
+    if n == 0:
+        raise ValueError("invalid batch/capacity/q_len")
+    return int(n)
+
+
+def evict_workspace_size(batch: int, keep: int) -> int:
+    n = _lib.load().gqa_evict_workspace_size(batch, keep)
+    if n == 0:
+        raise ValueError("invalid batch/keep")
+    return int(n)
+
+
+def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    _require(workspace, "workspace", None, (torch.uint8,), device)
+    return workspace
+
+
+def _cache_args(kv, block_table, paged, kv_scales, device):
+    """Checks of a cache that a call reads: (format, scales' pointer, batch, capacity)."""
+    name = "kv_pages" if paged else "kv"
+    kvf = _kv_format(kv, name, None)
+    _require(kv, name, None, tuple(_KVF), device)
+    _require_scales(kv_scales, "kv_scales", kv, kvf)
+    if paged:
+        _require_table(block_table, None, kv.device)
+    batch = block_table.shape[0] if paged else kv.shape[0]
+    capacity = block_table.shape[1] * kv.shape[3] if paged else kv.shape[3]
+    return kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None, batch, capacity
+
+
+def _prefill(q, kv, block_table, paged, chunk_starts, sequence_lengths, q_scale, k_scale, v_scale, kv_scales, out,
+             workspace):
+    _require(q, "q", None, tuple(_QDT))
+    if q.dim() != 3 or q.shape[1:] != (HQ, D):
+        raise ValueError(f"q must be [tokens, {HQ}, {D}], got {tuple(q.shape)}")
+    dev, dt = q.device, _QDT[q.dtype]
+    kvf, sc, B, C = _cache_args(kv, block_table, paged, kv_scales, dev)
+    _require(chunk_starts, "chunk_starts", (B + 1,), (torch.int32,), dev)
+    _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
+    if out is None:
+        out = torch.zeros_like(q)
+    _require(out, "out", q.shape, (q.dtype,), dev)
+    workspace = _workspace(workspace, prefill_workspace_size(), dev)
+    lib = _lib.load()
+    tail = (float(q_scale), float(k_scale), float(v_scale), _ptr(workspace), workspace.numel())
+    with _current(dev):
+        if paged:
+            _lib.check(lib.gqa_prefill_paged(_ptr(q), dt, _ptr(kv), kvf, sc, _ptr(block_table), block_table.shape[1],
+                                             kv.shape[0], kv.shape[3], _ptr(chunk_starts), _ptr(sequence_lengths),
+                                             _ptr(out), q.shape[0], B, *tail, _stream(dev)))
+        else:
+            _lib.check(lib.gqa_prefill(_ptr(q), dt, _ptr(kv), kvf, sc, _ptr(chunk_starts), _ptr(sequence_lengths),
+                                       _ptr(out), q.shape[0], B, C, *tail, _stream(dev)))
+    return out
+
+
+def gqa_prefill(q, kv, chunk_starts, sequence_lengths, q_scale: float = 1.0, k_scale: float = 1.0,
+                v_scale: float = 1.0, kv_scales=None, out=None, workspace=None):
+    """Attention of chunks of new tokens over the cache they are already written to
+    (write_kv): row b's tokens are q[chunk_starts[b]:chunk_starts[b + 1]], the last n of
+    its sequence_lengths[b] slots, and query j of them attends slots [0, len - n + j].
+    q [tokens, 32, 128]; chunk_starts int32 [batch + 1], never decreasing; kv of any
+    format (int8 and e2m1 with kv_scales).  Returns out (q's shape); tokens outside
+    every chunk keep what out holds (a new out: zeros).  workspace: uint8,
+    prefill_workspace_size() bytes."""
+    return _prefill(q, kv, None, False, chunk_starts, sequence_lengths, q_scale, k_scale, v_scale, kv_scales, out,
+                    workspace)
+
+
+def gqa_prefill_paged(q, kv_pages, block_table, chunk_starts, sequence_lengths, q_scale: float = 1.0,
+                      k_scale: float = 1.0, v_scale: float = 1.0, kv_scales=None, out=None, workspace=None):
+    """gqa_prefill over a paged cache: kv_pages [num_pages, 2, 8, page_size, 128] (and
+    its scale pages), block_table int32 [batch, max_pages]."""
+    return _prefill(q, kv_pages, block_table, True, chunk_starts, sequence_lengths, q_scale, k_scale, v_scale,
+                    kv_scales, out, workspace)
+
+
+_PROB = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _prob_strides(t, name, shape, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {dtype} {shape} on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.numel() and t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"the vocabulary of {name} must be contiguous")
+    # (a dimension of one row has no stride of its own)
+    token = t.stride(1) if shape[1] > 1 else shape[2]
+    batch = t.stride(0) if shape[0] > 1 else shape[1] * token
+    return batch, token
+
+
+def verify_drafts(probs, drafts, uniforms, draft_probs=None, sequence_lengths=None, out_lengths=None, tokens=None,
+                  accepted=None, workspace=None):
+    """After a verify window of T tokens (the last accepted one and T - 1 drafts): the
+    drafts that stay, and the token behind them.  probs [batch, T, vocab] (fp32, fp16 or
+    bf16; rows may lie apart), the target's; drafts int32 [batch, T - 1], a row with
+    fewer ending in -1; uniforms fp32 [batch, T], random numbers in [0, 1); draft_probs
+    [batch, T - 1, vocab] of the same dtype, what the drafts were drawn from (None: each
+    had probability one).  Draft j stays while uniforms[j] * q_j(d_j) < p_j(d_j); after
+    n of them one token is drawn from max(p_n - q_n, 0), or from p_n if no draft was
+    left, by uniforms[T - 1].  Returns (tokens int32 [batch, T], the n drafts, the drawn
+    token, then -1; accepted int32 [batch], n).  sequence_lengths int32 [batch] (of a
+    cache that holds all T) are shortened by the refused drafts, into out_lengths, or in
+    place if that is None."""
+    if not isinstance(probs, torch.Tensor):
+        raise TypeError("probs must be a torch.Tensor")
+    if not probs.is_cuda or probs.dim() != 3 or probs.dtype not in _PROB:
+        raise ValueError("probs must be a CUDA fp32/fp16/bf16 tensor [batch, T, vocab]")
+    B, T, V = probs.shape
+    dev = probs.device
+    ps = _prob_strides(probs, "probs", (B, T, V), probs.dtype, dev)
+    _require(drafts, "drafts", (B, T - 1), (torch.int32,), dev)
+    _require(uniforms, "uniforms", (B, T), (torch.float32,), dev)
+    ds = (0, 0)
+    if draft_probs is not None:
+        ds = _prob_strides(draft_probs, "draft_probs", (B, T - 1, V), probs.dtype, dev)
+    if sequence_lengths is not None:
+        _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
+        if out_lengths is None:
+            out_lengths = sequence_lengths
+    elif out_lengths is not None:
+        raise ValueError("out_lengths needs sequence_lengths")
+    if out_lengths is not None:
+        _require(out_lengths, "out_lengths", (B,), (torch.int32,), dev)
+    if tokens is None:
+        tokens = torch.empty((B, T), dtype=torch.int32, device=dev)
+    _require(tokens, "tokens", (B, T), (torch.int32,), dev)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=torch.int32, device=dev)
+    _require(accepted, "accepted", (B,), (torch.int32,), dev)
+    if workspace is not None:
+        _require(workspace, "workspace", None, (torch.uint8,), dev)
+    with _current(dev):
+        _lib.check(_lib.load().gqa_verify_drafts(
+            _ptr(probs), *ps, None if draft_probs is None or T == 1 else _ptr(draft_probs), *ds, _PROB[probs.dtype],
+            _ptr(drafts) if T > 1 else None, _ptr(uniforms),
+            None if sequence_lengths is None else _ptr(sequence_lengths),
+            None if out_lengths is None else _ptr(out_lengths), _ptr(tokens), _ptr(accepted), B, T, V,
+            None if workspace is None else _ptr(workspace), 0 if workspace is None else workspace.numel(),
+            _stream(dev)))
+    return tokens, accepted
+
+
+def _accumulate(q, kv, block_table, paged, sequence_lengths, weights, q_scale, k_scale, kv_scales, add, workspace):
+    _require(q, "q", None, tuple(_QDT))
+    if q.dim() == 3 and q.shape[1:] == (HQ, D):
+        T = 1
+    elif q.dim() == 4 and q.shape[2:] == (HQ, D) and 1 <= q.shape[1] <= 4:
+        T = q.shape[1]
+    else:
+        raise ValueError(f"q must be [batch, {HQ}, {D}] or [batch, T (1..4), {HQ}, {D}]")
+    dev = q.device
+    kvf, sc, B, C = _cache_args(kv, block_table, paged, kv_scales, dev)
+    if q.shape[0] != B:
+        raise ValueError(f"q has {q.shape[0]} rows, the cache {B}")
+    _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
+    _require(weights, "weights", (B, HKV, C), (torch.float32,), dev)
+    workspace = _workspace(workspace, weights_workspace_size(B, C, T), dev)
+    lib = _lib.load()
+    tail = (T, float(q_scale), float(k_scale), 1 if add else 0, _ptr(workspace), workspace.numel())
+    with _current(dev):
+        if paged:
+            _lib.check(lib.gqa_accumulate_weights_paged(
+                _ptr(q), _QDT[q.dtype], _ptr(kv), kvf, sc, _ptr(block_table), block_table.shape[1], kv.shape[0],
+                kv.shape[3], _ptr(sequence_lengths), _ptr(weights), B, *tail, _stream(dev)))
+        else:
+            _lib.check(lib.gqa_accumulate_weights(_ptr(q), _QDT[q.dtype], _ptr(kv), kvf, sc, _ptr(sequence_lengths),
+                                                  _ptr(weights), B, C, *tail, _stream(dev)))
+    return weights
+
+
+def accumulate_weights(q, kv, sequence_lengths, weights, q_scale: float = 1.0, k_scale: float = 1.0, kv_scales=None,
+                       add: bool = True, workspace=None):
+    """The softmax weights that a step's queries give the slots of a cache, summed over
+    the 4 heads of each KV head and the step's tokens, added to weights fp32 [batch, 8,
+    capacity] (add=False: written).  q [batch, 32, 128], or [batch, T, 32, 128] for the
+    T = 1..4 tokens of a verify window; kv of any format.  Slots at and past the length
+    keep what they hold.  Returns weights."""
+    return _accumulate(q, kv, None, False, sequence_lengths, weights, q_scale, k_scale, kv_scales, add, workspace)
+
+
+def accumulate_weights_paged(q, kv_pages, block_table, sequence_lengths, weights, q_scale: float = 1.0,
+                             k_scale: float = 1.0, kv_scales=None, add: bool = True, workspace=None):
+    """accumulate_weights over a paged cache; weights fp32 [batch, 8, max_pages * page_size]."""
+    return _accumulate(q, kv_pages, block_table, True, sequence_lengths, weights, q_scale, k_scale, kv_scales, add,
+                       workspace)
+
+
+def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, first, out, out_scales, out_table,
+           out_lengths, out_weights, kept, kv_scales, workspace):
+    _require(kv, "kv_pages" if paged else "kv", None, tuple(_KVF))
+    dev = kv.device
+    kvf, sc, B, C = _cache_args(kv, block_table, paged, kv_scales, dev)
+    keep = int(keep)
+    _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
+    _require(weights, "weights", (B, HKV, C), (torch.float32,), dev)
+    in_place = out is None and out_table is None
+    osc, out_capacity = None, 0
+    if out is not None:
+        if _kv_format(out, "out", B) != kvf:
+            raise ValueError("out must have the format of kv")
+        _require(out, "out", None, (kv.dtype,), dev)
+        _require_scales(out_scales, "out_scales", out, kvf)
+        osc, out_capacity = _ptr(out_scales) if kvf in (KV_I8, KV_E2M1) else None, out.shape[3]
+    if out_table is not None:
+        _require_table(out_table, B, dev)
+    if in_place:
+        if out_lengths is not None or out_weights is not None or out_scales is not None:
+            raise ValueError("an eviction in place has no out_lengths, out_weights or out_scales")
+    else:
+        if out_lengths is None:
+            raise ValueError("out_lengths is needed unless the eviction is in place")
+        _require(out_lengths, "out_lengths", (B,), (torch.int32,), dev)
+    wcap = 0
+    if out_weights is not None:
+        _require(out_weights, "out_weights", None, (torch.float32,), dev)
+        if out_weights.dim() != 3 or out_weights.shape[:2] != (B, HKV):
+            raise ValueError(f"out_weights must be [{B}, {HKV}, slots], got {tuple(out_weights.shape)}")
+        wcap = out_weights.shape[2]
+    nbytes = evict_workspace_size(B, keep)
+    if kept is None:
+        kept = torch.empty((B, HKV, keep), dtype=torch.int32, device=dev)
+    _require(kept, "kept", (B, HKV, keep), (torch.int32,), dev)
+    workspace = _workspace(workspace, nbytes, dev)
+    lib = _lib.load()
+    ol = None if in_place else _ptr(out_lengths)
+    ow = None if out_weights is None else _ptr(out_weights)
+    tail = (wcap, keep, int(recent), int(first), _ptr(workspace), workspace.numel())
+    with _current(dev):
+        if paged:
+            _lib.check(lib.gqa_evict_kv_paged(
+                _ptr(kv), kvf, sc, _ptr(block_table), block_table.shape[1], kv.shape[0], kv.shape[3],
+                _ptr(sequence_lengths), _ptr(weights), None if out_table is None else _ptr(out_table),
+                0 if out_table is None else out_table.shape[1], ol, ow, _ptr(kept), B, *tail, _stream(dev)))
+        else:
+            _lib.check(lib.gqa_evict_kv(_ptr(kv), kvf, sc, _ptr(sequence_lengths), _ptr(weights),
+                                        None if out is None else _ptr(out), osc, ol, ow, _ptr(kept), B, C, out_capacity,
+                                        *tail, _stream(dev)))
+    return kept
+
+
+def evict_kv(kv, sequence_lengths, weights, keep: int, recent: int = 0, first: int = 0, out=None, out_scales=None,
+             out_lengths=None, out_weights=None, kept=None, kv_scales=None, workspace=None):
+    """Makes a cache smaller: of each row's slots ``keep`` stay (all, if there are no
+    more), the ``first`` first, the ``recent`` last and of the others those with the
+    largest weights (fp32 [batch, 8, capacity], of accumulate_weights; equal ones: the
+    lowest slots), each KV head choosing for itself.  They move, in order, to slots 0, 1,
+    ... of ``out`` (a cache of the same format, with out_scales, out_lengths int32 [batch]
+    and, optionally, out_weights fp32 [batch, 8, slots], 0 behind the kept ones); without
+    ``out`` in place, where sequence_lengths and weights are updated too.  Returns kept
+    int32 [batch, 8, keep], the slots they came from (-1 behind the last)."""
+    return _evict(kv, None, False, sequence_lengths, weights, keep, recent, first, out, out_scales, None, out_lengths,
+                  out_weights, kept, kv_scales, workspace)
+
+
+def evict_kv_paged(kv_pages, block_table, sequence_lengths, weights, keep: int, recent: int = 0, first: int = 0,
+                   out_table=None, out_lengths=None, out_weights=None, kept=None, kv_scales=None, workspace=None):
+    """evict_kv on a paged cache: the kept rows move to the pages of the same pool that
+    out_table int32 [batch, pages] names (none of them in use by a row), or in place
+    (then no page may belong to two rows)."""
+    return _evict(kv_pages, block_table, True, sequence_lengths, weights, keep, recent, first, None, None, out_table,
+                  out_lengths, out_weights, kept, kv_scales, workspace)
 
 
 def workspace_init(workspace: torch.Tensor) -> None:

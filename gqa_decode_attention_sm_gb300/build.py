@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libgqa_decode.so")
 INCLUDE = os.path.join(ROOT, "include")
 # translation units, compiled side by side
-SRCS = [os.path.join(PKG, "csrc", name) for name in ("gqa_decode.cu", "fp4_decode.cu", "cache_io.cu")]
+SRCS = [os.path.join(PKG, "csrc", name) for name in ("gqa_decode.cu", "fp4_decode.cu", "cache_io.cu", "prefill.cu",
+                                                   "serving.cu")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-t", "0"]

@@ -23,6 +23,7 @@
 #include "kernels/cache_io.h"
 #include "kernels/combine.cuh"
 #include "kernels/common.cuh"
+#include "kernels/serving.h"
 #include "kernels/split_launch.cuh"
 
 static_assert(GQA_MAX_SPLITS <= 32 * gqa::kCombineChunks, "the combine's chunks cover every split slot");
@@ -111,6 +112,10 @@ void init_device(int dev, DeviceState& st) {
   if (a == cudaSuccess) {
     what = "setting up the e2m1 kernels";
     a = e2m1_setup(st.cluster_fit[kKvE2M1]);
+  }
+  if (a == cudaSuccess) {
+    what = "setting up the serving kernels";
+    a = serving_setup();
   }
   if (prev >= 0 && prev != dev) cudaSetDevice(prev);
   if (a != cudaSuccess) {
@@ -854,6 +859,249 @@ gqa_status_t read_kv(const CacheArgs& c, const int32_t* lens, const int32_t* sta
   return GQA_OK;
 }
 
+// A range of memory that a call reads or writes.
+struct Range { const void* p; size_t bytes; };
+
+bool meet(const Range& a, const Range& b) { return a.p && b.p && a.bytes && b.bytes && overlap(a.p, a.bytes, b.p, b.bytes); }
+
+// Nothing that is written overlaps anything else.
+template <size_t I, size_t O>
+gqa_status_t no_aliasing(const Range (&ins)[I], const Range (&outs)[O]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (const Range& in : ins)
+      if (meet(outs[i], in)) return fail(GQA_ERR_ALIASING, "an output or the workspace overlaps an input");
+    for (size_t k = i + 1; k < O; ++k)
+      if (meet(outs[i], outs[k])) return fail(GQA_ERR_ALIASING, "two of the outputs and the workspace overlap");
+  }
+  return GQA_OK;
+}
+
+// The cache, and a workspace that a call needs, of the serving calls.
+gqa_status_t validate_serving(const CacheArgs& c, const void* workspace, size_t workspace_bytes, size_t need) {
+  gqa_status_t st = validate_cache(c, nullptr, 0);
+  if (st != GQA_OK) return st;
+  if (c.format == kKvE2M1 && !aligned(c.scales, 8))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "an e2m1 cache's scales must be 8-byte aligned");
+  if (!workspace || !aligned(workspace, 16))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "workspace must be non-null and 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(GQA_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  return GQA_OK;
+}
+
+gqa_status_t validate_query(const CacheArgs& c, const void* q, int q_dtype, float q_scale) {
+  if (!q || !aligned(q, 16)) return fail(GQA_ERR_INVALID_ARGUMENT, "q must be non-null and 16-byte aligned");
+  if (q_dtype != GQA_F16 && q_dtype != GQA_BF16) return fail(GQA_ERR_INVALID_ARGUMENT, "unknown dtype %d", q_dtype);
+  if (!is_narrow(c.format) && c.format != q_dtype)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "fp16/bf16 KV must have the dtype of q");
+  if (!std::isfinite(q_scale) || q_scale < 0.f) return fail(GQA_ERR_INVALID_ARGUMENT, "q_scale must be finite and >= 0");
+  return GQA_OK;
+}
+
+CacheView view_of(const CacheArgs& c, void* workspace) {
+  CacheView v = {};
+  v.kv = c.kv;
+  v.scales = c.scales;
+  v.block_table = c.block_table;
+  v.flags = static_cast<uint32_t*>(workspace);
+  v.batch = c.batch;
+  v.capacity = c.capacity;
+  v.max_pages = c.max_pages;
+  v.num_pages = c.num_pages;
+  v.page_log2 = c.page_log2;
+  v.rows = checked_rows(c);
+  return v;
+}
+
+// log2(e) / sqrt(128): the softmax runs in the exp2 domain
+float softmax_scale_log2(float q_scale, float k_scale) {
+  return (float)((double)q_scale * (double)k_scale * 1.4426950408889634 / std::sqrt(128.0));
+}
+
+gqa_status_t prefill(const CacheArgs& c, const void* q, int q_dtype, const int32_t* chunk_starts, const int32_t* lens,
+                     void* out, int tokens, float q_scale, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream) {
+  if (tokens == 0) return GQA_OK;
+  if (tokens < 0 || tokens > (1 << 27)) return fail(GQA_ERR_INVALID_ARGUMENT, "tokens %d outside [0, 2^27]", tokens);
+  if (!chunk_starts || !lens || !out) return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  const size_t need = gqa_prefill_workspace_size();
+  gqa_status_t st = validate_serving(c, workspace, workspace_bytes, need);
+  if (st != GQA_OK) return st;
+  st = validate_query(c, q, q_dtype, q_scale);
+  if (st != GQA_OK) return st;
+  if (!aligned(out, 16) || !aligned(chunk_starts, 4) || !aligned(lens, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned, chunk_starts and lens 4-byte");
+  const size_t qb = (size_t)tokens * kHq * kD * 2;
+  const Range ins[] = {{q, qb}, {c.kv, c.kv_bytes()}, {c.scales, c.scale_bytes()},
+                       {chunk_starts, ((size_t)c.batch + 1) * 4}, {lens, (size_t)c.batch * 4},
+                       {c.block_table, c.table_bytes()}};
+  const Range outs[] = {{out, qb}, {workspace, need}};
+  st = no_aliasing(ins, outs);
+  if (st != GQA_OK) return st;
+  int sms = 0;
+  st = current_device_ready(&sms);
+  if (st != GQA_OK) return st;
+  PrefillParams p = {};
+  p.c = view_of(c, workspace);
+  p.q = q;
+  p.out = out;
+  p.chunk_starts = chunk_starts;
+  p.lens = lens;
+  p.tokens = tokens;
+  p.scale_log2 = softmax_scale_log2(q_scale, c.k_scale);
+  p.v_scale = c.v_scale;
+  const cudaError_t e = launch_prefill(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, sms, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
+  return GQA_OK;
+}
+
+// How the score kernel cuts a row: chunks of whole slab rounds, about 8 CTAs an SM in
+// all where the capacity gives as many, 1024 chunks a row at most.
+constexpr int kScoreRound = kScoreWarps * kSlab;
+int max_score_chunks(int capacity) { return (int)std::min(1024LL, ((long long)capacity + kScoreRound - 1) / kScoreRound); }
+
+size_t score_bytes(int batch, int capacity, int q_len) {
+  return align_up((size_t)batch * kHkv * capacity * 4 * q_len * sizeof(float), 256);
+}
+
+gqa_status_t accumulate(const CacheArgs& c, const void* q, int q_dtype, const int32_t* lens, float* weights, int q_len,
+                        float q_scale, int add, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (q_len < 1 || q_len > 4) return fail(GQA_ERR_INVALID_ARGUMENT, "q_len %d outside [1, 4]", q_len);
+  if (!lens || !weights) return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  const size_t need = gqa_weights_workspace_size(c.batch, c.capacity, q_len);
+  gqa_status_t st = validate_serving(c, workspace, workspace_bytes, need);
+  if (st != GQA_OK) return st;
+  st = validate_query(c, q, q_dtype, q_scale);
+  if (st != GQA_OK) return st;
+  if (!aligned(weights, 16) || !aligned(lens, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "weights must be 16-byte aligned, lens 4-byte");
+  const Range ins[] = {{q, (size_t)c.batch * q_len * kHq * kD * 2}, {c.kv, c.kv_bytes()}, {c.scales, c.scale_bytes()},
+                       {lens, (size_t)c.batch * 4}, {c.block_table, c.table_bytes()}};
+  const Range outs[] = {{weights, (size_t)c.batch * kHkv * c.capacity * 4}, {workspace, need}};
+  st = no_aliasing(ins, outs);
+  if (st != GQA_OK) return st;
+  int sms = 0;
+  st = current_device_ready(&sms);
+  if (st != GQA_OK) return st;
+  WeightParams p = {};
+  p.c = view_of(c, workspace);
+  p.q = q;
+  p.lens = lens;
+  p.weights = weights;
+  char* ws = static_cast<char*>(workspace) + GQA_WORKSPACE_HEADER_BYTES;
+  p.scores = reinterpret_cast<float*>(ws);
+  p.stats = reinterpret_cast<float2*>(ws + score_bytes(c.batch, c.capacity, q_len));
+  p.scale_log2 = softmax_scale_log2(q_scale, c.k_scale);
+  const long long want = std::max(1LL, std::min<long long>(max_score_chunks(c.capacity), (8LL * sms + kHkv * c.batch - 1) / (kHkv * (long long)c.batch)));
+  p.chunk = (int)(((c.capacity + want - 1) / want + kScoreRound - 1) / kScoreRound * kScoreRound);
+  p.chunks = (c.capacity + p.chunk - 1) / p.chunk;
+  p.add = add != 0;
+  const cudaError_t e = launch_sum_weights(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, q_len, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "weight sum kernel launch");
+  return GQA_OK;
+}
+
+size_t evict_chunks(int keep) {  // of the narrowest rows' moves the fewest, of 16-bit rows the most
+  return ((size_t)keep + move_rows(kKvF16) - 1) / move_rows(kKvF16);
+}
+
+// What an eviction takes besides the cache; out and out_table null: in place.
+struct EvictArgs {
+  int32_t* lens;
+  float* weights;
+  void *out, *out_scales;
+  const int32_t* out_table;
+  int out_capacity, out_max_pages;
+  int32_t* out_lens;
+  float* out_weights;
+  int32_t* kept;
+  int weights_capacity, keep, recent, first;
+  void* workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+
+gqa_status_t evict(const CacheArgs& c, const EvictArgs& a) {
+  if (a.keep < 1 || a.keep > (1 << 30)) return fail(GQA_ERR_INVALID_ARGUMENT, "keep %d outside [1, 2^30]", a.keep);
+  if (a.first < 0 || a.recent < 0 || (long long)a.first + a.recent > a.keep)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "first and recent must be >= 0 and no more than keep together");
+  if (!a.lens || !a.weights || !a.kept) return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  const size_t need = gqa_evict_workspace_size(c.batch, a.keep);
+  gqa_status_t st = validate_serving(c, a.workspace, a.workspace_bytes, need);
+  if (st != GQA_OK) return st;
+  const bool in_place = !a.out && !a.out_table;
+  if (in_place && (a.out_scales || a.out_lens || a.out_weights))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "an eviction in place has no out_scales, out_lens or out_weights");
+  if (!in_place) {
+    if (!a.out_lens) return fail(GQA_ERR_INVALID_ARGUMENT, "out_lens is null");
+    if (!c.block_table && scale_row_bytes(c.format) && !a.out_scales) return fail(GQA_ERR_INVALID_ARGUMENT, "out_scales is null");
+    const long long room = c.block_table ? (long long)a.out_max_pages << c.page_log2 : a.out_capacity;
+    if (a.out_max_pages < 0 || room < a.keep || room > (1LL << 30))
+      return fail(GQA_ERR_INVALID_ARGUMENT, "the output holds %lld slots a row, fewer than keep or more than 2^30", room);
+    if (a.out_weights && (a.weights_capacity < a.keep || a.weights_capacity > (1 << 30)))
+      return fail(GQA_ERR_INVALID_ARGUMENT, "weights_capacity %d below keep or above 2^30", a.weights_capacity);
+  }
+  if (!aligned(a.weights, 16) || !aligned(a.out, 16) || !aligned(a.out_scales, c.format == kKvE2M1 ? 8 : 2) ||
+      !aligned(a.lens, 4) || !aligned(a.out_lens, 4) || !aligned(a.out_weights, 4) || !aligned(a.kept, 4) ||
+      !aligned(a.out_table, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "misaligned argument");
+  if ((long long)c.batch * kHkv * 2 * (long long)evict_chunks(a.keep) > 0x7fffffffLL)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "batch * keep is too large");
+  CacheArgs to = c;
+  if (!in_place && c.block_table) {
+    to.block_table = a.out_table;
+    to.max_pages = a.out_max_pages;
+    to.capacity = a.out_max_pages << c.page_log2;
+  } else if (!in_place) {
+    to.kv = a.out;
+    to.scales = a.out_scales;
+    to.capacity = a.out_capacity;
+  }
+  const size_t b4 = (size_t)c.batch * 4;
+  const Range lens{a.lens, b4}, weights{a.weights, (size_t)c.batch * kHkv * c.capacity * 4};
+  const Range cache{c.kv, c.kv_bytes()}, scales{c.scales, c.scale_bytes()}, table{c.block_table, c.table_bytes()};
+  const Range kept{a.kept, (size_t)c.batch * kHkv * a.keep * 4}, ws{a.workspace, need}, none{nullptr, 0};
+  if (in_place || c.block_table) {
+    const Range ins[] = {table, {a.out_table, to.table_bytes()}, in_place ? none : lens, in_place ? none : weights};
+    const Range outs[] = {cache, scales, in_place ? lens : Range{a.out_lens, b4},
+                          in_place ? weights : Range{a.out_weights, (size_t)c.batch * kHkv * a.weights_capacity * 4}, kept, ws};
+    st = no_aliasing(ins, outs);
+  } else {
+    const Range ins[] = {cache, scales, lens, weights};
+    const Range outs[] = {{to.kv, to.kv_bytes()}, {to.scales, to.scale_bytes()}, {a.out_lens, b4},
+                          {a.out_weights, (size_t)c.batch * kHkv * a.weights_capacity * 4}, kept, ws};
+    st = no_aliasing(ins, outs);
+  }
+  if (st != GQA_OK) return st;
+  int sms = 0;
+  st = current_device_ready(&sms);
+  if (st != GQA_OK) return st;
+  EvictParams p = {};
+  p.src = view_of(c, a.workspace);
+  p.dst = view_of(to, a.workspace);
+  p.lens = a.lens;
+  p.out_lens = in_place ? a.lens : a.out_lens;
+  p.weights = a.weights;
+  p.out_weights = in_place ? a.weights : a.out_weights;
+  p.kept = a.kept;
+  char* at = static_cast<char*>(a.workspace) + GQA_WORKSPACE_HEADER_BYTES;
+  p.old_lens = reinterpret_cast<int32_t*>(at);
+  at += align_up(b4, 256);
+  p.ticket = reinterpret_cast<uint32_t*>(at);
+  p.read_flags = reinterpret_cast<uint32_t*>(at + 256);
+  p.flags = static_cast<uint32_t*>(a.workspace);
+  p.batch = c.batch;
+  p.keep = a.keep;
+  p.recent = a.recent;
+  p.first = a.first;
+  p.weights_capacity = in_place ? c.capacity : a.weights_capacity;
+  p.chunks = (int)(((size_t)a.keep + move_rows(c.format) - 1) / move_rows(c.format));
+  p.in_place = in_place;
+  const cudaError_t e = launch_evict(p, c.format, a.stream);
+  if (e != cudaSuccess) return cuda_fail(e, "eviction kernel launch");
+  return GQA_OK;
+}
+
 // The append step on a contiguous cache (block_table = nullptr; `units` =
 // batch, `unit_rows` = capacity) or a paged one (units = num_pages, unit_rows
 // = page size, capacity = max_pages * page size).
@@ -1238,6 +1486,159 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
   if (st != GQA_OK) return st;
   return read_kv(c, lens, starts, out, (int)out_dtype, out_capacity, workspace, workspace_bytes,
                  static_cast<cudaStream_t>(stream));
+}
+
+size_t gqa_prefill_workspace_size(void) { return GQA_WORKSPACE_HEADER_BYTES; }
+
+gqa_status_t gqa_prefill(const void* q, gqa_dtype_t q_dtype, const void* kv, gqa_kv_format_t kv_format,
+                         const void* kv_scales, const int32_t* chunk_starts, const int32_t* lens, void* out,
+                         int tokens, int batch, int capacity, float q_scale, float k_scale, float v_scale,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const CacheArgs c{const_cast<void*>(kv), (int)kv_format, const_cast<void*>(kv_scales), batch, capacity, nullptr,
+                    0, 0, 0, k_scale, v_scale};
+  return prefill(c, q, (int)q_dtype, chunk_starts, lens, out, tokens, q_scale, workspace, workspace_bytes,
+                 static_cast<cudaStream_t>(stream));
+}
+
+gqa_status_t gqa_prefill_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages, gqa_kv_format_t kv_format,
+                               const void* kv_scales_pages, const int32_t* block_table, int max_pages_per_seq,
+                               int num_pages, int page_size, const int32_t* chunk_starts, const int32_t* lens,
+                               void* out, int tokens, int batch, float q_scale, float k_scale, float v_scale,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  CacheArgs c{const_cast<void*>(kv_pages), (int)kv_format, const_cast<void*>(kv_scales_pages), batch, 0, nullptr,
+              0, 0, 0, k_scale, v_scale};
+  gqa_status_t st = paged_args(c, block_table, max_pages_per_seq, num_pages, page_size);
+  if (st != GQA_OK) return st;
+  return prefill(c, q, (int)q_dtype, chunk_starts, lens, out, tokens, q_scale, workspace, workspace_bytes,
+                 static_cast<cudaStream_t>(stream));
+}
+
+gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride, long long probs_token_stride,
+                               const void* draft_probs, long long draft_batch_stride, long long draft_token_stride,
+                               gqa_prob_t prob_type, const int32_t* drafts, const float* uniforms,
+                               const int32_t* lens, int32_t* out_lens, int32_t* tokens, int32_t* accepted,
+                               int batch, int window, int vocab, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (batch < 1 || batch > 65535) return fail(GQA_ERR_INVALID_ARGUMENT, "batch %d outside [1, 65535]", batch);
+  if (window < 1 || window > kMaxWindow) return fail(GQA_ERR_INVALID_ARGUMENT, "window %d outside [1, %d]", window, kMaxWindow);
+  // (2^24 terms of up to 2^38 units: the sum stays below 2^63)
+  if (vocab < 1 || vocab > (1 << 24)) return fail(GQA_ERR_INVALID_ARGUMENT, "vocab %d outside [1, 2^24]", vocab);
+  if (!probs || !uniforms || !tokens || !accepted || (window > 1 && !drafts))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if ((lens == nullptr) != (out_lens == nullptr))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "lens and out_lens are given together or not at all");
+  if (prob_type != GQA_PROB_F16 && prob_type != GQA_PROB_BF16 && prob_type != GQA_PROB_F32)
+    return fail(GQA_ERR_INVALID_ARGUMENT, "unknown prob_type %d", (int)prob_type);
+  const size_t width = prob_type == GQA_PROB_F32 ? 4 : 2;
+  const bool with_q = draft_probs != nullptr && window > 1;
+  const auto strides_fit = [&](long long bs, long long ts, long long rows) {
+    return ts >= vocab && ts <= (1LL << 40) / rows && bs >= rows * ts - (ts - vocab) && bs <= (1LL << 40);
+  };
+  if (!strides_fit(probs_batch_stride, probs_token_stride, window) ||
+      (with_q && !strides_fit(draft_batch_stride, draft_token_stride, window - 1)))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "strides must hold the rows without overlap and be at most 2^40 elements");
+  if (!aligned(probs, width) || !aligned(draft_probs, width) || !aligned(drafts, 4) || !aligned(uniforms, 4) ||
+      !aligned(lens, 4) || !aligned(out_lens, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) || !aligned(workspace, 4))
+    return fail(GQA_ERR_INVALID_ARGUMENT, "misaligned argument");
+  if (workspace && workspace_bytes < GQA_WORKSPACE_HEADER_BYTES)
+    return fail(GQA_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than its %d-byte header", GQA_WORKSPACE_HEADER_BYTES);
+  const size_t B = (size_t)batch;
+  const size_t p_bytes = ((B - 1) * probs_batch_stride + (window - 1) * probs_token_stride + vocab) * width;
+  const size_t q_bytes = with_q ? ((B - 1) * draft_batch_stride + (window - 2) * draft_token_stride + vocab) * width : 0;
+  const Range ins[] = {{probs, p_bytes}, {draft_probs, q_bytes}, {drafts, B * (window - 1) * 4}, {uniforms, B * window * 4},
+                       {lens == out_lens ? nullptr : lens, B * 4}};
+  const Range outs[] = {{out_lens, B * 4}, {tokens, B * window * 4}, {accepted, B * 4},
+                        {workspace, (size_t)GQA_WORKSPACE_HEADER_BYTES}};
+  gqa_status_t st = no_aliasing(ins, outs);
+  if (st != GQA_OK) return st;
+  int sms = 0;
+  st = current_device_ready(&sms);
+  if (st != GQA_OK) return st;
+  DraftParams p = {};
+  p.probs = probs;
+  p.draft_probs = with_q ? draft_probs : nullptr;
+  p.p_batch = probs_batch_stride;
+  p.p_token = probs_token_stride;
+  p.q_batch = draft_batch_stride;
+  p.q_token = draft_token_stride;
+  p.drafts = drafts;
+  p.uniforms = uniforms;
+  p.lens = lens;
+  p.out_lens = out_lens;
+  p.tokens = tokens;
+  p.accepted = accepted;
+  p.flags = static_cast<uint32_t*>(workspace);
+  p.batch = batch;
+  p.window = window;
+  p.vocab = vocab;
+  p.p_bytes = p_bytes;
+  p.q_bytes = q_bytes;
+  const int pf = prob_type == GQA_PROB_F32 ? kPF32 : (prob_type == GQA_PROB_BF16 ? kPBF16 : kPF16);
+  const cudaError_t e = launch_verify_drafts(p, pf, sms, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "draft verification kernel launch");
+  return GQA_OK;
+}
+
+size_t gqa_weights_workspace_size(int batch, int capacity, int q_len) {
+  if (batch < 1 || batch > 65535 || capacity < 1 || capacity > (1 << 30) || q_len < 1 || q_len > 4) return 0;
+  return GQA_WORKSPACE_HEADER_BYTES + score_bytes(batch, capacity, q_len) +
+         align_up((size_t)batch * kHkv * max_score_chunks(capacity) * 4 * q_len * sizeof(float2), 256);
+}
+
+gqa_status_t gqa_accumulate_weights(const void* q, gqa_dtype_t q_dtype, const void* kv, gqa_kv_format_t kv_format,
+                                    const void* kv_scales, const int32_t* lens, float* weights, int batch,
+                                    int capacity, int q_len, float q_scale, float k_scale, int add, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  const CacheArgs c{const_cast<void*>(kv), (int)kv_format, const_cast<void*>(kv_scales), batch, capacity, nullptr,
+                    0, 0, 0, k_scale, 1.f};
+  return accumulate(c, q, (int)q_dtype, lens, weights, q_len, q_scale, add, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+gqa_status_t gqa_accumulate_weights_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages,
+                                          gqa_kv_format_t kv_format, const void* kv_scales_pages,
+                                          const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                          int page_size, const int32_t* lens, float* weights, int batch, int q_len,
+                                          float q_scale, float k_scale, int add, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  CacheArgs c{const_cast<void*>(kv_pages), (int)kv_format, const_cast<void*>(kv_scales_pages), batch, 0, nullptr,
+              0, 0, 0, k_scale, 1.f};
+  gqa_status_t st = paged_args(c, block_table, max_pages_per_seq, num_pages, page_size);
+  if (st != GQA_OK) return st;
+  return accumulate(c, q, (int)q_dtype, lens, weights, q_len, q_scale, add, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream));
+}
+
+size_t gqa_evict_workspace_size(int batch, int keep) {
+  if (batch < 1 || batch > 65535 || keep < 1 || keep > (1 << 30)) return 0;
+  return GQA_WORKSPACE_HEADER_BYTES + align_up((size_t)batch * 4, 256) + 256 +
+         align_up((size_t)batch * kHkv * 2 * evict_chunks(keep) * 4, 256);
+}
+
+gqa_status_t gqa_evict_kv(void* kv, gqa_kv_format_t kv_format, void* kv_scales, int32_t* lens, float* weights,
+                          void* out, void* out_scales, int32_t* out_lens, float* out_weights, int32_t* kept,
+                          int batch, int capacity, int out_capacity, int weights_capacity, int keep, int recent,
+                          int first, void* workspace, size_t workspace_bytes, void* stream) {
+  const CacheArgs c{kv, (int)kv_format, kv_scales, batch, capacity, nullptr, 0, 0, 0, 1.f, 1.f};
+  const EvictArgs a{lens, weights, out, out_scales, nullptr, out_capacity, 0, out_lens, out_weights, kept,
+                    weights_capacity, keep, recent, first, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream)};
+  return evict(c, a);
+}
+
+gqa_status_t gqa_evict_kv_paged(void* kv_pages, gqa_kv_format_t kv_format, void* kv_scales_pages,
+                                const int32_t* block_table, int max_pages_per_seq, int num_pages, int page_size,
+                                int32_t* lens, float* weights, const int32_t* out_table, int out_max_pages,
+                                int32_t* out_lens, float* out_weights, int32_t* kept, int batch,
+                                int weights_capacity, int keep, int recent, int first, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  CacheArgs c{kv_pages, (int)kv_format, kv_scales_pages, batch, 0, nullptr, 0, 0, 0, 1.f, 1.f};
+  gqa_status_t st = paged_args(c, block_table, max_pages_per_seq, num_pages, page_size);
+  if (st != GQA_OK) return st;
+  const EvictArgs a{lens, weights, nullptr, nullptr, out_table, 0, out_max_pages, out_lens, out_weights, kept,
+                    weights_capacity, keep, recent, first, workspace, workspace_bytes,
+                    static_cast<cudaStream_t>(stream)};
+  return evict(c, a);
 }
 
 gqa_status_t gqa_decode_split_stage(const void* q, gqa_dtype_t q_dtype, const void* kv,

@@ -1,0 +1,299 @@
+// Making a cache smaller: of the slots [0, L) of a row the first `first`, the last
+// `recent` and, of those between, the ones of the largest weights stay, `keep` in
+// all, each KV head choosing for itself; they move in their order to slots 0, 1, ...
+//
+// select_kv_kernel finds a head's threshold, the k-th largest weight, digit by digit
+// (11, 11 and 10 bits of the weights' order-preserving integers, a histogram each),
+// and then writes the kept slots in ascending order by a prefix sum of "above the
+// threshold, or equal to it and among the first such".  A cluster of CTAs shares a
+// head: each holds its part of the weights in shared memory, so that they are read
+// once, and the histograms and counts meet in distributed shared memory.  Everything
+// counted is whole numbers, so the result does not depend on any order.
+//
+// move_kv_kernel gathers the rows (and their scales and weights), 16 KB a CTA.  Bound
+// by HBM.  In place a CTA may overwrite rows that another has yet to read: the CTAs
+// take their chunks by ticket in ascending order, say when theirs is read and write
+// once all chunks before it have been read.  Reading waits for nothing and a later
+// chunk's rows lie behind every row that an earlier one writes, so no wait can last
+// longer than the loads of CTAs that run already.
+#pragma once
+
+#include "cache_rows.cuh"
+
+namespace gqa {
+
+constexpr int kSelectBins = 2048;
+constexpr int kSelectKeys = 48 * 1024;  // weights that a CTA holds in shared memory (192 KB)
+constexpr int kMoveThreads = 256;
+constexpr int kMoveBytes = 16384;  // of rows that a CTA moves
+
+__host__ __device__ constexpr int move_rows(int kv_format) { return kMoveBytes / kv_row_bytes(kv_format); }
+
+struct EvictParams {
+  CacheView src, dst;  // dst: the same cache in place
+  const int32_t* lens;
+  int32_t* out_lens;
+  const float* weights;  // [B, 8, capacity]
+  float* out_weights;    // [B, 8, weights_capacity] or null; in place: weights
+  int32_t* kept;         // [B, 8, keep]
+  int32_t* old_lens;     // [B], workspace: the clamped lengths
+  uint32_t* ticket;      // workspace, in place
+  uint32_t* read_flags;  // [B, 8, 2, chunks], workspace, in place
+  uint32_t* flags;
+  int batch, keep, recent, first, weights_capacity, chunks;
+  int in_place;
+  int cluster;  // CTAs that share a head
+  int held;  // weights a CTA of the select kernel holds in shared memory (0: reads them each time)
+};
+
+// Integers in the order of the weights; NaN below everything, both zeros one.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// A head's CTAs: the cluster's, or one CTA launched without a cluster, which has no
+// use for the cluster's barrier and shared memory.
+__device__ __forceinline__ void head_sync(int S) {
+  if (S > 1) cluster_sync_all();
+  else __syncthreads();
+}
+__device__ __forceinline__ uint32_t head_ld(const uint32_t* p, int S, int rank) {
+  if (S == 1) return *p;
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_map(smem_addr(p), (uint32_t)rank)) : "memory");
+  return v;
+}
+
+template <int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kSelectWarps = kSelectThreads / 32;
+  static_assert(2 * kSelectThreads == kSelectBins, "a thread counts two bins");
+  extern __shared__ uint32_t s_keys[];
+  __shared__ uint32_t s_hist[2][kSelectBins];
+  __shared__ uint32_t s_part[kSelectWarps], s_part2[kSelectWarps];
+  __shared__ uint32_t s_bin, s_above, s_count[2];
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int S = p.cluster, rank = (int)blockIdx.x % S;
+  const int unit = blockIdx.x / S, b = unit / kHkv;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const int C = p.src.capacity;
+  const int L = clamp_length(__ldg(p.lens + b), C, p.flags, unit % kHkv == 0 && rank == 0 && tid == 0);
+  const int n = min(L, p.keep);
+  int32_t* kept = p.kept + (size_t)unit * p.keep;
+  if (rank == 0 && tid == 0 && unit % kHkv == 0) p.old_lens[b] = L;
+  if (p.in_place) {
+    for (int i = rank * kSelectThreads + tid; i < 2 * p.chunks; i += S * kSelectThreads)
+      p.read_flags[(size_t)unit * 2 * p.chunks + i] = 0u;
+    if (unit == 0 && rank == 0 && tid == 0) *p.ticket = 0u;
+  }
+  if (L <= p.keep) {  // (the same in every CTA of the cluster)
+    for (int i = rank * kSelectThreads + tid; i < p.keep; i += S * kSelectThreads) kept[i] = i < n ? i : -1;
+    return;
+  }
+  // first + recent <= keep < L
+  const int lo = p.first, hi = L - p.recent;
+  for (int i = rank * kSelectThreads + tid; i < p.first + p.recent; i += S * kSelectThreads)
+    kept[i < p.first ? i : p.keep - p.recent + (i - p.first)] = i < p.first ? i : hi + (i - p.first);
+  const float* w = p.weights + (size_t)unit * C;
+  const size_t w_extent = (size_t)p.batch * kHkv * C * 4;
+  const auto load_key = [&](int t) { return weight_key(__ldg(in_buffer(w + t, 4, p.weights, w_extent, p.flags))); };
+  // the CTA's candidates, and the warps': consecutive slots
+  const int all = hi - lo;
+  const int seg = ((all + S - 1) / S + 31) / 32 * 32;
+  const int c0 = (int)min((long long)all, (long long)rank * seg), c1 = min(all - c0, seg) + c0;
+  const bool held = c1 - c0 <= p.held;
+  if (held)
+    for (int i = c0 + tid; i < c1; i += kSelectThreads) s_keys[i - c0] = load_key(lo + i);
+  const auto key = [&](int i) { return held ? s_keys[i - c0] : load_key(lo + i); };
+  uint32_t need = (uint32_t)(p.keep - p.first - p.recent);  // to be found, of those equal so far
+  uint32_t threshold = 0xffffffffu;                         // (no weight's key)
+  if (need > 0) {
+    threshold = 0;
+    constexpr int kShift[3] = {21, 10, 0};
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      const int shift = kShift[d], bits = d == 2 ? 10 : 11;
+      const uint32_t mask = (1u << bits) - 1;
+      uint32_t* hist = s_hist[d & 1];
+      for (int i = tid; i < kSelectBins; i += kSelectThreads) hist[i] = 0u;
+      __syncthreads();
+      for (int i = c0 + tid; i < c1; i += kSelectThreads) {
+        const uint32_t x = key(i);
+        if (d == 0 || (x >> (shift + bits)) == (threshold >> (shift + bits))) atomicAdd(&hist[x >> shift & mask], 1u);
+      }
+      // (a histogram is cleared again two digits later, after the other's cluster
+      // barrier, when every CTA has read it)
+      head_sync(S);
+      uint32_t mine[2] = {0, 0};  // bins 2 tid, 2 tid + 1 counted from the top
+      const int top = kSelectBins - 1 - 2 * tid;
+      for (int k = 0; k < S; ++k) {
+        mine[0] += head_ld(hist + top, S, k);
+        mine[1] += head_ld(hist + top - 1, S, k);
+      }
+      uint32_t upto = mine[0] + mine[1];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      if (lane == 31) s_part[warp] = upto;
+      __syncthreads();
+      uint32_t above = upto - mine[0] - mine[1];
+      for (int k = 0; k < warp; ++k) above += s_part[k];
+      if (above < need && need <= above + mine[0]) {
+        s_bin = (uint32_t)top;
+        s_above = above;
+      } else if (above + mine[0] < need && need <= above + mine[0] + mine[1]) {
+        s_bin = (uint32_t)(top - 1);
+        s_above = above + mine[0];
+      }
+      __syncthreads();
+      threshold |= s_bin << shift;
+      need -= s_above;
+    }
+  }
+  // how many lie above and on the threshold before each warp's slots
+  const int per = ((c1 - c0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+  const int w0 = min(c1, c0 + warp * per), w1 = min(c1, w0 + per);
+  uint32_t above = 0, equal = 0;
+  for (int i = w0; i < w1; i += 32) {
+    const uint32_t x = i + lane < w1 ? key(i + lane) : 0u;
+    above += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && x > threshold));
+    equal += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && x == threshold));
+  }
+  __syncthreads();  // (s_part is done with)
+  if (lane == 0) {
+    s_part[warp] = above;
+    s_part2[warp] = equal;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t x = 0, y = 0;
+    for (int k = 0; k < kSelectWarps; ++k) {
+      x += s_part[k];
+      y += s_part2[k];
+    }
+    s_count[0] = x;
+    s_count[1] = y;
+  }
+  head_sync(S);
+  above = equal = 0;
+  for (int k = 0; k < rank; ++k) {
+    above += head_ld(s_count, S, k);
+    equal += head_ld(s_count + 1, S, k);
+  }
+  head_sync(S);  // (nobody's shared memory is left while it is read)
+  for (int k = 0; k < warp; ++k) {
+    above += s_part[k];
+    equal += s_part2[k];
+  }
+  for (int i = w0; i < w1; i += 32) {
+    const bool in = i + lane < w1;
+    const uint32_t x = in ? key(i + lane) : 0u;
+    const uint32_t gt = __ballot_sync(0xffffffffu, in && x > threshold);
+    const uint32_t eq = __ballot_sync(0xffffffffu, in && x == threshold);
+    const uint32_t before = (1u << lane) - 1;
+    const uint32_t rank_eq = equal + __popc(eq & before);
+    if (in && (x > threshold || (x == threshold && rank_eq < need))) {
+      const uint32_t at = (uint32_t)p.first + above + __popc(gt & before) + min(rank_eq, need);
+      if (at < (uint32_t)p.keep) kept[at] = lo + i + lane;  // (always; every address here is held in bounds)
+    }
+    above += __popc(gt);
+    equal += __popc(eq);
+  }
+}
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+template <int KVF>
+__global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kRow = kv_row_bytes(KVF), kPer = kRow / 16;     // threads a row
+  constexpr int kRows = move_rows(KVF), kStep = kMoveThreads / kPer;  // rows a CTA has, and takes at once
+  constexpr int kIter = kRows / kStep;
+  __shared__ uint32_t s_ticket;
+  __shared__ int s_late;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  uint32_t job = blockIdx.x;
+  if (p.in_place) {
+    if (threadIdx.x == 0) {
+      s_ticket = atomicAdd(p.ticket, 1u);
+      s_late = 0;
+    }
+    __syncthreads();
+    job = s_ticket;
+  }
+  const int chunk = (int)(job % (uint32_t)p.chunks);
+  const int up = (int)(job / (uint32_t)p.chunks), plane = up & 1, unit = up >> 1, b = unit / kHkv;
+  const int L = min(max(p.old_lens[b], 0), p.src.capacity), n = min(L, p.keep);
+  const int pg = plane * kHkv + unit % kHkv;
+  if (unit % kHkv == 0 && plane == 0 && chunk == 0 && threadIdx.x == 0) p.out_lens[b] = n;
+  if (p.in_place && L <= p.keep) return;  // nothing moves
+  const int lane = threadIdx.x % kPer, first = chunk * kRows;
+  const int32_t* kept = p.kept + (size_t)unit * p.keep;
+  const float* w = p.weights + (size_t)unit * p.src.capacity;
+  uint4 x[kIter];
+  uint2 sc[kIter];
+  float wt[kIter];
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) {
+    const int at = first + k * kStep + threadIdx.x / kPer;
+    if (at >= n) continue;
+    const int t = min(max(kept[at], 0), p.src.capacity - 1);  // (a slot, whatever the caller's kept was written with since)
+    const size_t row = cache_row(p.src, b, pg, t);
+    x[k] = *(reinterpret_cast<const uint4*>(p.src.kv) + row * kPer + lane);
+    if (lane == 0) {
+      if constexpr (KVF == kKvI8) sc[k].x = static_cast<const uint16_t*>(p.src.scales)[row];
+      if constexpr (KVF == kKvE2M1) sc[k] = static_cast<const uint2*>(p.src.scales)[row];
+      if (plane == 0 && p.out_weights) wt[k] = w[t];
+    }
+  }
+  if (p.in_place) {
+    uint32_t* read = p.read_flags + (size_t)up * p.chunks;
+    __threadfence();  // this thread's reads come before the flag
+    __syncthreads();
+    if (threadIdx.x == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(read + chunk), "r"(1u) : "memory");
+    const uint64_t deadline = global_timer_ns() + kWaitBudgetNs;
+    for (int c = threadIdx.x; c < chunk; c += kMoveThreads)
+      while (load_acquire(read + c) == 0u)
+        if (global_timer_ns() > deadline) {
+          s_late = 1;
+          break;
+        }
+    __syncthreads();
+    if (s_late) {
+      if (threadIdx.x == 0 && p.flags) atomicOr(p.flags, GQA_FLAG_WAIT_TIMEOUT);
+      return;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kIter; ++k) {
+    const int at = first + k * kStep + threadIdx.x / kPer;
+    if (at >= n) continue;
+    bool known = true;
+    const size_t row = cache_row(p.dst, b, pg, at, &known);
+    if (!known) continue;
+    *(reinterpret_cast<uint4*>(const_cast<void*>(p.dst.kv)) + row * kPer + lane) = x[k];
+    if (lane == 0) {
+      if constexpr (KVF == kKvI8) static_cast<uint16_t*>(const_cast<void*>(p.dst.scales))[row] = (uint16_t)sc[k].x;
+      if constexpr (KVF == kKvE2M1) static_cast<uint2*>(const_cast<void*>(p.dst.scales))[row] = sc[k];
+      if (plane == 0 && p.out_weights) p.out_weights[(size_t)unit * p.weights_capacity + at] = wt[k];
+    }
+  }
+  // slots behind the kept ones start their sums at zero (in place: those that held tokens)
+  if (plane == 0 && p.out_weights) {
+    const int end = chunk < p.chunks - 1 ? first + kRows : (p.in_place ? L : p.weights_capacity);
+    for (int at = max(first, n) + threadIdx.x; at < end; at += kMoveThreads)
+      p.out_weights[(size_t)unit * p.weights_capacity + at] = 0.f;
+  }
+  // (kept[] of a row shorter than `keep` ends in -1, written by the select kernel)
+}
+
+}  // namespace gqa

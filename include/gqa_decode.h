@@ -517,6 +517,139 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
                                gqa_dtype_t out_dtype, int batch, int out_capacity, float k_scale,
                                float v_scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of chunks of new tokens over the cache that they are already written
+ * to (the "FreeToken-Kai: Running on Turing (sm_75)" docs, change 7: prefill
+ * attention over the paged prefix; here the pages are read in place).  The chunks
+ * of the rows lie one behind another: row b has tokens chunk_starts[b] ..
+ * chunk_starts[b + 1] - 1 of q and out [tokens, 32, 128], n of them, and they are
+ * the last n of the lens[b] slots of its cache: query j (from 0) attends slots
+ * [0, lens[b] - n + j].  n may be 0 or the whole row.  chunk_starts int32
+ * [batch + 1], never decreasing, within [0, tokens], and lens int32 [batch], are
+ * device memory, read only by the kernels; tokens of q outside every chunk
+ * (padding behind the last one) are not read, and out keeps what it holds there.
+ * A length outside [0, capacity] or a start out of order is clamped and sets
+ * GQA_FLAG_LENGTH_CLAMPED; a query with no slot (n above the length) gets a zero
+ * row and sets it too.  Formats, scales and q_scale as gqa_decode_verify, but no
+ * rule on the capacity of an int8 or e2m1 cache.  Scores, maximum and sum are
+ * FP32; each softmax weight is rounded to q's type where it meets V.  A value (or
+ * key) that a query does not see never reaches its output, whatever it holds.
+ * q, kv, out and the workspace 16-byte aligned (int8 scales 2, e2m1 scales 8);
+ * nothing written overlaps anything else.  The workspace holds
+ * gqa_prefill_workspace_size() bytes whatever the sizes; its header as
+ * gqa_decode_prepared's.  tokens = 0 does nothing.  No allocation, no host sync. */
+size_t gqa_prefill_workspace_size(void);
+gqa_status_t gqa_prefill(const void* q, gqa_dtype_t q_dtype, const void* kv, gqa_kv_format_t kv_format,
+                         const void* kv_scales, const int32_t* chunk_starts, const int32_t* lens,
+                         void* out, int tokens, int batch, int capacity, float q_scale, float k_scale,
+                         float v_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over a paged cache (the layout and page rules of gqa_decode_paged). */
+gqa_status_t gqa_prefill_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages,
+                               gqa_kv_format_t kv_format, const void* kv_scales_pages,
+                               const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                               int page_size, const int32_t* chunk_starts, const int32_t* lens,
+                               void* out, int tokens, int batch, float q_scale, float k_scale,
+                               float v_scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* After a verify window: which of its drafted tokens stay, and the token that
+ * follows them.  A window has T tokens, the last accepted one and T - 1 drafts.
+ *   probs [batch, T, vocab] of `prob_type`: row j is the target's distribution
+ *     behind token j of the window
+ *   drafts int32 [batch, T - 1]: token j + 1 of the window; a row with fewer
+ *     drafts ends in -1 (an id of vocab or above ends them too, and sets
+ *     GQA_FLAG_SLOT_CLAMPED)
+ *   draft_probs [batch, T - 1, vocab], the distributions that the drafts were drawn
+ *     from, or NULL: each draft had probability one
+ *   uniforms float [batch, T], random numbers in [0, 1)
+ * Draft j is taken if all before it are and uniforms[j] * q_j(d_j) < p_j(d_j)
+ * (exactly; p, q = probs, draft_probs; a NaN refuses).  With n taken, tokens[b]
+ * holds those n, then one drawn from max(p_n - q_n, 0) if a draft was refused,
+ * from p_n if none was left, then -1; accepted[b] = n.  The draw: each term,
+ * rounded once to FP32, clipped to [0, 1] (NaN: 0), is taken to whole units of
+ * 2^-38, and the token is the first whose running sum is above
+ * floor(sum * floor(uniforms[T - 1] * 2^24) / 2^24).  If nothing is left of p
+ * beside q, the draw is from p_n; if that has no weight either, the token is -1.
+ * out_lens[b] = max(lens[b] - (T - 1) + n, 0), the length without the refused
+ * drafts' slots (lens counts all T of the window); lens and out_lens may both be
+ * NULL, or be the same array.  Strides are in elements; the vocab's are 1.  T
+ * 1..32 (drafts may be NULL with T = 1).  Arrays aligned to their elements; the
+ * workspace (optional) has the status flags; nothing written overlaps anything
+ * else.  One launch, no allocation, no host sync. */
+typedef enum { GQA_PROB_F16 = 0, GQA_PROB_BF16 = 1, GQA_PROB_F32 = 2 } gqa_prob_t;
+gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride,
+                               long long probs_token_stride, const void* draft_probs,
+                               long long draft_batch_stride, long long draft_token_stride,
+                               gqa_prob_t prob_type, const int32_t* drafts, const float* uniforms,
+                               const int32_t* lens, int32_t* out_lens, int32_t* tokens,
+                               int32_t* accepted, int batch, int window, int vocab, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* The softmax weights that a step gives the slots of a cache, summed over the 4
+ * query heads of each KV head and the q_len tokens of the step (1..4, the last
+ * slots as in gqa_decode_verify):
+ *   w[b, g, t] = sum over j, h of softmax over [0, len - q_len + j] of
+ *                q_scale * k_scale / sqrt(128) * dot(q[b, j, h], K[b, g, .]) at t
+ * weights float [batch, 8, capacity]: for t < lens[b], w is added to it (add != 0)
+ * or written (add = 0); slots at and past the length keep what they hold.  FP32
+ * throughout.  Formats as gqa_decode_verify (no rule on the capacity), lengths too;
+ * a query that sees no slot gives no weight.  Pointers 16-byte aligned (int8
+ * scales 2, e2m1 scales 8, lens 4).  The workspace holds
+ * gqa_weights_workspace_size(batch, capacity, q_len) bytes (0: invalid sizes).
+ * Two launches, no allocation, no host sync. */
+size_t gqa_weights_workspace_size(int batch, int capacity, int q_len);
+gqa_status_t gqa_accumulate_weights(const void* q, gqa_dtype_t q_dtype, const void* kv,
+                                    gqa_kv_format_t kv_format, const void* kv_scales, const int32_t* lens,
+                                    float* weights, int batch, int capacity, int q_len, float q_scale,
+                                    float k_scale, int add, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+gqa_status_t gqa_accumulate_weights_paged(const void* q, gqa_dtype_t q_dtype, const void* kv_pages,
+                                          gqa_kv_format_t kv_format, const void* kv_scales_pages,
+                                          const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                          int page_size, const int32_t* lens, float* weights, int batch,
+                                          int q_len, float q_scale, float k_scale, int add, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Making a cache smaller by such weights.  Of the lens[b] slots of a row, `keep`
+ * stay (all, if there are no more): the first `first`, the last `recent`, and of
+ * those between the ones with the largest weights, of equal ones the lowest slots
+ * (both zeros are equal; NaN is below everything).  Each KV head chooses for itself.
+ * The kept rows of K and V (and their scales) move, in their order, to slots 0, 1,
+ * ... of `out`; kept int32 [batch, 8, keep] gets the slots they come from, -1
+ * behind the last; out_lens[b] = min(lens[b], keep).  The keys keep the rotation of
+ * their first positions.
+ *   out NULL: in place.  lens and weights [batch, 8, capacity] are updated, the
+ *     weights of slots that no longer hold a token set to 0; rows of no more than
+ *     `keep` slots do not change.  out_scales, out_lens and out_weights are NULL.
+ *   else out [batch, 2, 8, out_capacity, 128] of the cache's format, out_scales,
+ *     out_lens [batch], out_weights [batch, 8, weights_capacity] (or NULL), whose
+ *     slots behind the kept ones are set to 0; both capacities at least `keep`.
+ * Slots of `out` past the new length keep what they hold.  keep in [1, 2^30],
+ * first, recent >= 0, first + recent <= keep.  kv, out and weights 16-byte aligned
+ * (int8 scales 2, e2m1 scales 8, int32 arrays 4); nothing written overlaps anything
+ * else (but in place).  The workspace holds gqa_evict_workspace_size(batch, keep)
+ * bytes (0: invalid sizes).  Two launches, no allocation, no host sync.  Should a
+ * wait of an eviction in place run out (GQA_FLAG_WAIT_TIMEOUT), the cache is
+ * invalid. */
+size_t gqa_evict_workspace_size(int batch, int keep);
+gqa_status_t gqa_evict_kv(void* kv, gqa_kv_format_t kv_format, void* kv_scales, int32_t* lens,
+                          float* weights, void* out, void* out_scales, int32_t* out_lens,
+                          float* out_weights, int32_t* kept, int batch, int capacity, int out_capacity,
+                          int weights_capacity, int keep, int recent, int first, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The same on a paged cache: out_table int32 [batch, out_max_pages] names the pages
+ * of the same pool that the kept rows move to (out_max_pages * page_size at least
+ * `keep`), none of them a page of a block table's row in use; NULL: in place, where
+ * no page may belong to two rows.  A block-table entry in use outside [0, num_pages)
+ * is clamped and sets GQA_FLAG_PAGE_CLAMPED; where rows are written to, they are
+ * left out instead. */
+gqa_status_t gqa_evict_kv_paged(void* kv_pages, gqa_kv_format_t kv_format, void* kv_scales_pages,
+                                const int32_t* block_table, int max_pages_per_seq, int num_pages,
+                                int page_size, int32_t* lens, float* weights, const int32_t* out_table,
+                                int out_max_pages, int32_t* out_lens, float* out_weights, int32_t* kept,
+                                int batch, int weights_capacity, int keep, int recent, int first,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Zero the workspace header (status flags) on `stream`.  Asynchronous. */
 gqa_status_t gqa_decode_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
 

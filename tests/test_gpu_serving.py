@@ -1,0 +1,493 @@
+"""Prompt attention, draft verification, weight sums and eviction against their
+definitions in 64 bits (GPU), on the product and on the range-checked library.
+
+Bounds, each derived from the arithmetic and not from a run:
+  scores    the products of 16-bit values are exact in FP32; 128 of them are added,
+            each addition off by 2^-23 of the sum of their magnitudes m at most (the
+            tensor cores cut where FP32 rounds), so |ds| <= 2^-16 m, and the scaling
+            adds 2^-22 |s|
+  weights   exp(s - max) / sum is off by 2 |ds| (its own score and the sum's) and
+            2^-19 (exp2, the sum, the division)
+  outputs   those, half a step of q's type for the weight where it meets V, all times
+            sum of weight * |V|, and half a step of the output's type
+  tokens, lengths, kept slots and moved rows: equal
+"""
+import math
+
+import pytest
+import torch
+
+import gqa_decode_attention_sm_gb300 as gq
+from gqa_decode_attention_sm_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+TD = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+HQ, HKV, D = 32, 8, 128
+SCALE = {"e4m3": (0.03125, 0.046875), "e2m1": (0.4, 0.7)}
+
+
+@pytest.fixture(scope="module", params=["product", "checked"], autouse=True)
+def library(request):
+    from gqa_decode_attention_sm_gb300 import build as gbuild
+    saved = _lib._lib
+    _lib._lib = None
+    if request.param == "checked":
+        _lib._lib = _lib.load(gbuild.build_checked())
+    else:
+        gbuild.build()
+        _lib.load()
+    torch.cuda.init()
+    yield request.param
+    _lib._lib = saved
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def new_cache(fmt, units, rows, seed=0):
+    g = gen(seed + 17)
+    shape = (units, 2, HKV, rows, 64 if fmt == "e2m1" else D)
+    if fmt in TD:
+        return torch.randn(shape, generator=g, device=DEV).to(TD[fmt]), None
+    if fmt == "e4m3":
+        return (4 * torch.randn(shape, generator=g, device=DEV)).to(torch.float8_e4m3fn).view(torch.uint8), None
+    if fmt == "i8":
+        kv = torch.randint(-127, 128, shape, generator=g, device=DEV).to(torch.int8)
+        return kv, (0.002 + 0.02 * torch.rand(shape[:4], generator=g, device=DEV)).to(torch.bfloat16)
+    kv = torch.randint(0, 256, shape, generator=g, device=DEV).to(torch.uint8)
+    sc = (0.5 * torch.rand((*shape[:4], 8), generator=g, device=DEV)).to(torch.float8_e4m3fn).view(torch.uint8)
+    return kv, sc
+
+
+def values(kv, sc, fmt, scale):
+    """Rows in 64 bits."""
+    if fmt in TD:
+        return kv.double()
+    if fmt == "e4m3":
+        return kv.view(torch.float8_e4m3fn).double() * scale
+    if fmt == "i8":
+        return kv.double() * sc.double()[..., None]
+    level = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=DEV)
+    level = torch.cat((level, -level))
+    x = torch.stack((level[(kv & 15).long()], level[(kv >> 4).long()]), -1).flatten(-2)
+    return x * sc.view(torch.float8_e4m3fn).double().repeat_interleave(16, -1) * scale
+
+
+def paged(kv, sc, page, batch, capacity, seed=0):
+    """The cache in shuffled pages with spare ones: (pages, scale pages, block table)."""
+    per = capacity // page
+    n = batch * per
+    order = torch.randperm(n + 3, generator=gen(seed + 5), device=DEV)[:n]
+
+    def scatter(x):
+        if x is None:
+            return None
+        x = x.unflatten(3, (per, page)).movedim(3, 1).flatten(0, 1)  # [B * per, 2, 8, page, ...]
+        out = torch.zeros((n + 3, *x.shape[1:]), dtype=x.dtype, device=DEV)
+        out[order] = x
+        return out
+    return scatter(kv), scatter(sc), order.to(torch.int32).view(batch, per).contiguous()
+
+
+def scale_of(fmt):
+    return SCALE.get(fmt, (1.0, 1.0))
+
+
+def check_flags(ws, library, want=0):
+    assert gq.get_status(ws) == want
+
+
+# ------------------------------------------------------------------ prefill
+
+
+def attend64(q, K, V, end):
+    """One query token's heads over slots [0, end): output, sum of weight * |V|, score error bound."""
+    o, a, e = (torch.zeros((HQ, D), dtype=torch.float64, device=DEV) for _ in range(3))
+    if end > 0:
+        k, v = (x[:, :end].repeat_interleave(4, 0) for x in (K, V))
+        s = torch.einsum("hd,htd->ht", q.double(), k) / math.sqrt(128.0)
+        m = torch.einsum("hd,htd->ht", q.double().abs(), k.abs()).amax(-1) / math.sqrt(128.0)
+        w = torch.softmax(s, -1)
+        o, a = torch.einsum("ht,htd->hd", w, v), torch.einsum("ht,htd->hd", w, v.abs())
+        e = (2 ** -16 * m + 2 ** -22 * s.abs().amax(-1))[:, None].expand(HQ, D)
+    return o, a, e
+
+
+def prefill_case(fmt, dtype, rows, capacity, page=0, seed=0, pad=3, q_scale=1.0, mag=1.0, sample=None, edit=None):
+    """rows: (n, length) of each batch row."""
+    B = len(rows)
+    kv, sc = new_cache(fmt, B, capacity, seed)
+    ks, vs = scale_of(fmt)
+    if edit:
+        edit(kv, sc)
+    K, V = (values(kv[:, p], None if sc is None else sc[:, p], fmt, s) for p, s in ((0, ks), (1, vs)))
+    n = [r[0] for r in rows]
+    starts = torch.tensor([0] + list(torch.tensor(n).cumsum(0)), dtype=torch.int32, device=DEV)
+    lens = torch.tensor([r[1] for r in rows], dtype=torch.int32, device=DEV)
+    N = sum(n)
+    q = (mag * torch.randn((N + pad, HQ, D), generator=gen(seed + 1), device=DEV)).to(TD[dtype])
+    out = torch.full_like(q, 7.0)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    how = dict(q_scale=q_scale, k_scale=ks, v_scale=vs, out=out, workspace=ws)
+    if page:
+        pool, pool_sc, table = paged(kv, sc, page, B, capacity, seed)
+        gq.gqa_prefill_paged(q, pool, table, starts, lens, kv_scales=pool_sc, **how)
+    else:
+        gq.gqa_prefill(q, kv, starts, lens, kv_scales=sc, **how)
+    torch.cuda.synchronize()
+    assert (out[N:] == 7.0).all(), "rows behind the last chunk changed"
+    half = torch.finfo(TD[dtype]).eps / 2
+    tiny = torch.finfo(TD[dtype]).tiny
+    at = 0
+    for b, (nb, L) in enumerate(rows):
+        picks = range(nb) if sample is None or nb <= sample else sorted({0, nb - 1, *torch.randint(
+            0, nb, (sample,), generator=torch.Generator().manual_seed(seed + b)).tolist()})
+        for j in picks:
+            ref, a, e = attend64(q[at + j] * q_scale, K[b], V[b], L - nb + j + 1)
+            bound = half * ref.abs() + (half + 2 * e + 2 ** -18) * a + tiny * half
+            err = (out[at + j].double() - ref).abs()
+            assert (err <= bound).all(), \
+                f"row {b} query {j}: worst {float((err / bound).max()):.3f} of the bound, {float(err.max()):.3e}"
+        at += nb
+    return ws
+
+
+FORMATS = [("f16", "f16"), ("bf16", "bf16"), ("e4m3", "bf16"), ("e4m3", "f16"), ("i8", "bf16"), ("i8", "f16"),
+           ("e2m1", "bf16"), ("e2m1", "f16")]
+
+
+@pytest.mark.parametrize("page", [0, 16, 128])
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+def test_prefill_formats(library, fmt, dtype, page):
+    rows = [(1, 1), (5, 5), (0, 17), (33, 100), (64, 64), (70, 384), (3, 384), (129, 257)]
+    ws = prefill_case(fmt, dtype, rows, 384, page)
+    check_flags(ws, library)
+
+
+@pytest.mark.parametrize("rows", [
+    [(1, 1)], [(1, 2000)], [(2, 130)], [(31, 31)], [(32, 128)], [(33, 129)], [(63, 640)], [(64, 1000)], [(65, 1001)],
+    [(127, 127)], [(128, 255)], [(300, 300)], [(0, 0), (0, 5), (7, 9)], [(1, 1)] * 40, [(17, 1024)],
+    [(513, 2049), (0, 2049), (1, 1), (700, 700), (256, 1999)]])
+@pytest.mark.parametrize("fmt", ["f16", "bf16", "i8"])
+def test_prefill_sizes(library, fmt, rows):
+    prefill_case(fmt, "bf16" if fmt == "bf16" else "f16", rows, 2049, sample=40)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("bf16", "bf16"), ("f16", "f16"), ("e2m1", "bf16")])
+def test_prefill_long(library, fmt, dtype):
+    # few tokens over a long row, many over a medium one: rows cut into pieces and merged
+    prefill_case(fmt, dtype, [(40, 40000), (1500, 6000), (2, 30001)], 40000, sample=10, seed=3)
+    prefill_case(fmt, dtype, [(100, 32768)], 32768, page=256, sample=10, seed=4)
+
+
+# ------------------------------------------------------------------- drafts
+
+
+def drafts64(p, d, u, q, lens):
+    """The definition with whole numbers of the interpreter."""
+    B, T, V = p.shape
+    tokens, accepted, out = [], [], []
+    for b in range(B):
+        taken, row = [], None
+        for j in range(T - 1):
+            t = int(d[b, j])
+            if not 0 <= t < V:
+                break
+            qd = 1.0 if q is None else float(q[b, j, t])
+            if float(u[b, j]) * qd < float(p[b, j, t]):
+                taken.append(t)
+                row = None
+            else:
+                row = torch.zeros(V, device=p.device) if q is None else q[b, j].float()
+                if q is None:
+                    row[t] = math.inf
+                break
+        pn = p[b, len(taken)].float()
+
+        def whole(x):
+            x = torch.nan_to_num(x, nan=0.0).clamp(0, 1)
+            return (x.double() * 2.0 ** 38).round().long().tolist()
+        w = whole(pn) if row is None else whole(pn - row)
+        if not any(w):
+            w = whole(pn)
+        total, k = sum(w), int(min(max(math.floor(float(u[b, -1]) * 2 ** 24), 0), 2 ** 24 - 1))
+        target, acc, pick = (total * k) >> 24, 0, -1
+        for i, x in enumerate(w):
+            acc += x
+            if acc > target:
+                pick = i
+                break
+        n = len(taken)
+        tokens.append(taken + [pick] + [-1] * (T - 1 - n))
+        accepted.append(n)
+        out.append(max(int(lens[b]) - (T - 1) + n, 0))
+    return tokens, accepted, out
+
+
+def draft_inputs(B, T, V, dtype, seed=0, sharp=2.5):
+    g = gen(seed)
+    p = torch.softmax(sharp * torch.randn((B, T, V), generator=g, device=DEV), -1)
+    q = torch.softmax(torch.log(p[:, :T - 1].clamp(min=1e-30)) + 0.8 * torch.randn((B, T - 1, V), generator=g, device=DEV), -1)
+    e = -torch.log1p(-torch.rand((B, T - 1, V), generator=g, device=DEV))
+    d = (q / e.clamp(min=1e-30)).argmax(-1).to(torch.int32) if T > 1 else torch.zeros((B, 0), dtype=torch.int32, device=DEV)
+    u = torch.rand((B, T), generator=g, device=DEV)
+    return p.to(TD[dtype]), d.contiguous(), u, q.to(TD[dtype]), torch.randint(T, 999, (B,), generator=g, device=DEV, dtype=torch.int32)
+
+
+def check_drafts(p, d, u, q, lens):
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    new = torch.zeros_like(lens)
+    tokens, accepted = gq.verify_drafts(p, d, u, draft_probs=q, sequence_lengths=lens, out_lengths=new, workspace=ws)
+    want = drafts64(p, d, u, q, lens)
+    assert accepted.tolist() == want[1]
+    assert tokens.tolist() == want[0]
+    assert new.tolist() == want[2]
+    return gq.get_status(ws)
+
+
+@pytest.mark.parametrize("greedy", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("B,T,V", [(1, 4, 32000), (3, 2, 1), (5, 3, 2), (9, 4, 37), (4, 1, 1000), (2, 8, 4097), (7, 5, 50001),
+                                   (3, 32, 300), (2, 3, 200003)])
+def test_drafts(library, B, T, V, dtype, greedy):
+    p, d, u, q, lens = draft_inputs(B, T, V, dtype, seed=V + T)
+    if T > 2:
+        d[0, 1] = -1
+    assert check_drafts(p, d, u, None if greedy else q, lens) == 0
+
+
+def test_drafts_strided_and_in_place(library):
+    p, d, u, q, lens = draft_inputs(6, 4, 1003, "f32", seed=5)
+    wide = torch.full((6, 4, 1024), 9.0, device=DEV)
+    wide[..., :1003] = p
+    wide_q = torch.full((6, 5, 1029), 9.0, device=DEV)
+    wide_q[:, 1:4, 2:1005] = q
+    want = drafts64(p, d, u, q, lens)
+    tokens, accepted = gq.verify_drafts(wide[..., :1003], d, u, draft_probs=wide_q[:, 1:4, 2:1005], sequence_lengths=lens)
+    assert tokens.tolist() == want[0] and accepted.tolist() == want[1] and lens.tolist() == want[2]
+
+
+def test_drafts_edges(library):
+    V = 5000
+    p, d, u, q, lens = draft_inputs(12, 4, V, "f32", seed=6)
+    p[0, :, :] = 0
+    p[0, :, 4999] = 1.0      # a target that is sure of the last token
+    p[1] = float("nan")      # nothing to draw from
+    p[2, 0] = q[2, 0]        # p = q: a refusal leaves nothing beside q
+    u[2, 0] = 0.99999994
+    q[2, 0, d[2, 0]] *= 1.5
+    p[3, :, 7] = float("nan")
+    q[4] = 0                 # a draft that its model never draws
+    u[5] = 0
+    u[6] = 1 - 2 ** -24
+    d[7, 0] = -1             # no draft at all
+    d[8, 2] = -5
+    p[9] = 0
+    p[9, :, 3] = 2 ** -39    # below half a unit (ties to even: 0)
+    p[10] = 1e-12
+    lens[11] = 2             # shorter than what is taken back
+    assert check_drafts(p, d, u, q, lens) == 0
+    d[0, 0] = V
+    assert check_drafts(p, d, u, q, lens) == gq.api.FLAG_SLOT_CLAMPED
+
+
+# ------------------------------------------------------------------ weights
+
+
+def weights64(q, K, L, T):
+    """[8, L] sums and their score error bounds."""
+    w, e = torch.zeros((HKV, L), dtype=torch.float64, device=DEV), torch.zeros((HKV, L), dtype=torch.float64, device=DEV)
+    for j in range(T):
+        n = L - T + 1 + j
+        if n < 1:
+            continue
+        k = K[:, :n].repeat_interleave(4, 0)
+        s = torch.einsum("hd,htd->ht", q[j].double(), k) / math.sqrt(128.0)
+        m = torch.einsum("hd,htd->ht", q[j].double().abs(), k.abs()).amax(-1, keepdim=True) / math.sqrt(128.0)
+        x = torch.softmax(s, -1)
+        ds = 2 ** -16 * m + 2 ** -22 * s.abs().amax(-1, keepdim=True)
+        w[:, :n] += x.view(HKV, 4, n).sum(1)
+        e[:, :n] += (x * (2 * ds + 2 ** -19)).view(HKV, 4, n).sum(1)
+    return w, e
+
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+def test_weights(library, fmt, dtype, T, page):
+    B, C = 5, 640
+    kv, sc = new_cache(fmt, B, C, 2)
+    ks, _ = scale_of(fmt)
+    lens = torch.tensor([640, 1, 0, 129, 333], dtype=torch.int32, device=DEV)
+    q = torch.randn((B, T, HQ, D), generator=gen(3), device=DEV).to(TD[dtype])
+    K = values(kv[:, 0], None if sc is None else sc[:, 0], fmt, ks)
+    old = torch.rand((B, HKV, C), generator=gen(4), device=DEV)
+    ws = torch.zeros(gq.weights_workspace_size(B, C, T), dtype=torch.uint8, device=DEV)
+    how = dict(k_scale=ks, workspace=ws)
+    for add in (True, False):
+        acc = old.clone()
+        if page:
+            pool, psc, table = paged(kv, sc, page, B, C)
+            gq.accumulate_weights_paged(q, pool, table, lens, acc, kv_scales=psc, add=add, **how)
+        else:
+            gq.accumulate_weights(q[:, 0].contiguous() if T == 1 else q, kv, lens, acc, kv_scales=sc, add=add, **how)
+        for b, L in enumerate(lens.tolist()):
+            assert torch.equal(acc[b, :, L:], old[b, :, L:])
+            w, e = weights64(q[b], K[b], L, T)
+            if add:
+                w = w + old[b, :, :L].double()
+                e = e + 2 ** -24 * w
+            assert ((acc[b, :, :L].double() - w).abs() <= e + 2 ** -126).all()
+    want = gq.api.FLAG_LENGTH_CLAMPED  # a row without a slot for each query
+    assert gq.get_status(ws) == want
+
+
+@pytest.mark.parametrize("fmt,dtype,B,C", [("bf16", "bf16", 1, 70001), ("e4m3", "bf16", 3, 9000), ("e2m1", "f16", 40, 258)])
+def test_weights_sizes(library, fmt, dtype, B, C):
+    kv, sc = new_cache(fmt, B, C, 5)
+    ks, _ = scale_of(fmt)
+    lens = torch.randint(4, C + 1, (B,), generator=gen(6), device=DEV, dtype=torch.int32)
+    q = torch.randn((B, 2, HQ, D), generator=gen(7), device=DEV).to(TD[dtype])
+    acc = torch.zeros((B, HKV, C), device=DEV)
+    gq.accumulate_weights(q, kv, lens, acc, k_scale=ks, kv_scales=sc)
+    for b in range(0, B, max(1, B // 5)):
+        L = int(lens[b])
+        K = values(kv[b, 0], None if sc is None else sc[b, 0], fmt, ks)
+        w, e = weights64(q[b], K, L, 2)
+        assert ((acc[b, :, :L].double() - w).abs() <= e + 2 ** -126).all()
+        assert not acc[b, :, L:].any()
+
+
+# ----------------------------------------------------------------- eviction
+
+
+def kept64(w, L, keep, recent, first):
+    """The kept slots of one head, by sorting."""
+    if L <= keep:
+        return list(range(L))
+    vals = [-math.inf if x != x else x for x in w]
+    isnan = [x != x for x in w]
+    rest = sorted(range(first, L - recent), key=lambda t: (isnan[t], -vals[t], t))[:keep - first - recent]
+    return sorted(list(range(first)) + rest + list(range(L - recent, L)))
+
+
+def evict_inputs(fmt, B, C, seed=0, ties=True):
+    kv, sc = new_cache(fmt, B, C, seed)
+    w = torch.exp(2 * torch.randn((B, HKV, C), generator=gen(seed + 1), device=DEV)) / C
+    if ties:  # sums of few values, zeros among them
+        w = torch.where(torch.rand(w.shape, generator=gen(seed + 2), device=DEV) < 0.3, (w * C).floor() / C, w)
+    return kv, sc, w
+
+
+def check_evicted(fmt, kv, sc, w, lens, keep, recent, first, got_kv, got_sc, got_w, got_lens, kept, clean_w=True):
+    for b, L in enumerate(lens.tolist()):
+        n = min(L, keep)
+        assert int(got_lens[b]) == n
+        for h in range(HKV):
+            at = kept64(w[b, h, :L].tolist(), L, keep, recent, first)
+            assert kept[b, h].tolist() == at + [-1] * (keep - n)
+            at = torch.tensor(at, dtype=torch.long, device=DEV)
+            assert torch.equal(got_kv[b, :, h, :n].view(torch.uint8), kv[b, :, h][:, at].view(torch.uint8))
+            if sc is not None:
+                assert torch.equal(got_sc[b, :, h, :n], sc[b, :, h][:, at])
+            if got_w is not None:
+                assert torch.equal(got_w[b, h, :n], w[b, h, at])
+                assert not got_w[b, h, n:L if not clean_w else None].any()
+
+
+EVICTIONS = [  # batch, capacity, lengths, keep, recent, first
+    (1, 1024, [1024], 512, 32, 4),
+    (3, 300, [300, 0, 77], 77, 0, 0),
+    (2, 200, [200, 133], 1, 0, 0),
+    (2, 200, [199, 2], 1, 1, 0),
+    (2, 640, [640, 500], 100, 60, 40),
+    (1, 640, [639], 638, 5, 2),
+    (2, 9000, [9000, 4097], 2050, 100, 1),
+    (1, 40000, [39999], 10000, 7, 3),
+]
+
+
+@pytest.mark.parametrize("B,C,lens,keep,recent,first", EVICTIONS)
+@pytest.mark.parametrize("fmt", ["f16", "e4m3", "i8", "e2m1"])
+def test_evict_into_another(library, fmt, B, C, lens, keep, recent, first):
+    if fmt != "f16" and C > 10000:
+        pytest.skip("one format is enough for the long row")
+    kv, sc, w = evict_inputs(fmt, B, C, seed=keep)
+    before = [x.clone() for x in (kv, w)]
+    lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out, out_sc = new_cache(fmt, B, keep + 3, seed=99)
+    fill = out.clone()
+    out_w, out_lens = torch.full((B, HKV, keep + 5), 3.0, device=DEV), torch.full_like(lens, -1)
+    ws = torch.zeros(gq.evict_workspace_size(B, keep), dtype=torch.uint8, device=DEV)
+    kept = gq.evict_kv(kv, lens, w, keep, recent=recent, first=first, out=out, out_scales=out_sc, out_lengths=out_lens,
+                       out_weights=out_w, kv_scales=sc, workspace=ws)
+    assert gq.get_status(ws) == 0
+    assert torch.equal(kv.view(torch.uint8), before[0].view(torch.uint8)) and torch.equal(w, before[1])
+    check_evicted(fmt, kv, sc, w, lens, keep, recent, first, out, out_sc, out_w, out_lens, kept)
+    for b, n in enumerate(out_lens.tolist()):
+        assert torch.equal(out[b, :, :, n:].view(torch.uint8), fill[b, :, :, n:].view(torch.uint8))
+
+
+@pytest.mark.parametrize("B,C,lens,keep,recent,first", EVICTIONS)
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_evict_in_place(library, fmt, B, C, lens, keep, recent, first):
+    kv, sc, w = evict_inputs(fmt, B, C, seed=keep + 1)
+    lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    new_kv, new_sc, new_w, new_lens = (None if x is None else x.clone() for x in (kv, sc, w, lens))
+    ws = torch.zeros(gq.evict_workspace_size(B, keep), dtype=torch.uint8, device=DEV)
+    kept = gq.evict_kv(new_kv, new_lens, new_w, keep, recent=recent, first=first, kv_scales=new_sc, workspace=ws)
+    assert gq.get_status(ws) == 0
+    check_evicted(fmt, kv, sc, w, lens, keep, recent, first, new_kv, new_sc, new_w, new_lens, kept, clean_w=False)
+    for b, L in enumerate(lens.tolist()):  # slots past the old length, and past the new one in the cache, as they were
+        n = min(L, keep)
+        assert torch.equal(new_w[b, :, L:], w[b, :, L:])
+        assert torch.equal(new_kv[b, :, :, n:].view(torch.uint8), kv[b, :, :, n:].view(torch.uint8))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("fmt,page", [("bf16", 16), ("i8", 64), ("e2m1", 32)])
+def test_evict_paged(library, fmt, page, in_place):
+    B, C, keep, recent, first = 3, 64 * 20, 333, 40, 2
+    kv, sc, w = evict_inputs(fmt, B, C, seed=7)
+    lens = torch.tensor([C, 300, 1001], dtype=torch.int32, device=DEV)
+    per = -(-keep // page)
+    room = new_cache(fmt, B, C + per * page, seed=8)
+    room[0][:, :, :, :C] = kv
+    if sc is not None:
+        room[1][:, :, :, :C] = sc
+    pool, psc, table = paged(*room, page, B, C + per * page, seed=9)
+    src, dst = table[:, :C // page].contiguous(), table[:, C // page:].contiguous()
+    kept = torch.zeros((B, HKV, keep), dtype=torch.int32, device=DEV)
+    if in_place:
+        new_lens, new_w = lens.clone(), w.clone()
+        gq.evict_kv_paged(pool, src, new_lens, new_w, keep, recent, first, kept=kept, kv_scales=psc)
+        dst = src
+    else:
+        new_lens, new_w = torch.zeros_like(lens), torch.full((B, HKV, keep), 2.0, device=DEV)
+        gq.evict_kv_paged(pool, src, lens, w, keep, recent, first, out_table=dst, out_lengths=new_lens,
+                          out_weights=new_w, kept=kept, kv_scales=psc)
+
+    def flat(x):
+        return None if x is None else x[dst.long()].movedim(1, 3).flatten(3, 4)
+    check_evicted(fmt, kv, sc, w, lens, keep, recent, first, flat(pool), flat(psc), new_w, new_lens, kept,
+                  clean_w=not in_place)
+
+
+def test_evict_special_weights(library):
+    kv, sc, w = evict_inputs("f16", 1, 500, seed=3)
+    w[0, 0, ::3] = float("nan")
+    w[0, 1] = 0.0
+    w[0, 1, ::2] = -0.0
+    w[0, 2, 10:400] = float("inf")
+    w[0, 3] = -w[0, 3]
+    w[0, 4, ::5] = -float("inf")
+    w[0, 5] = float("nan")
+    w[0, 6] = torch.arange(500, device=DEV) * 1e-45
+    lens = torch.tensor([500], dtype=torch.int32, device=DEV)
+    out, ol = torch.zeros((1, 2, HKV, 250, D), dtype=torch.float16, device=DEV), torch.zeros_like(lens)
+    kept = gq.evict_kv(kv, lens, w, 250, 10, 5, out=out, out_lengths=ol)
+    for h in range(HKV):
+        assert kept[0, h].tolist() == kept64(w[0, h].tolist(), 500, 250, 10, 5)
