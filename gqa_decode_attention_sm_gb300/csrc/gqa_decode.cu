@@ -116,6 +116,7 @@ void init_device(int dev, DeviceState& st) {
   if (a == cudaSuccess) {
     what = "setting up the serving kernels";
     a = serving_setup();
+    if (a == cudaSuccess) a = prefill_setup();
   }
   if (prev >= 0 && prev != dev) cudaSetDevice(prev);
   if (a != cudaSuccess) {
@@ -918,6 +919,10 @@ float softmax_scale_log2(float q_scale, float k_scale) {
   return (float)((double)q_scale * (double)k_scale * 1.4426950408889634 / std::sqrt(128.0));
 }
 
+// Partials of the prompt attention: two pieces a CTA.
+constexpr size_t kPrefillMlBytes = (size_t)2 * kPfMaxCtas * 2 * kPfRows * sizeof(float2);
+constexpr size_t kPrefillOBytes = (size_t)2 * kPfMaxCtas * 2 * kPfRows * kD * sizeof(float);
+
 gqa_status_t prefill(const CacheArgs& c, const void* q, int q_dtype, const int32_t* chunk_starts, const int32_t* lens,
                      void* out, int tokens, float q_scale, void* workspace, size_t workspace_bytes,
                      cudaStream_t stream) {
@@ -929,6 +934,7 @@ gqa_status_t prefill(const CacheArgs& c, const void* q, int q_dtype, const int32
   if (st != GQA_OK) return st;
   st = validate_query(c, q, q_dtype, q_scale);
   if (st != GQA_OK) return st;
+  if (c.rows() > 0x7fffffff) return fail(GQA_ERR_INVALID_ARGUMENT, "the cache has more than 2^31 - 1 rows");
   if (!aligned(out, 16) || !aligned(chunk_starts, 4) || !aligned(lens, 4))
     return fail(GQA_ERR_INVALID_ARGUMENT, "out must be 16-byte aligned, chunk_starts and lens 4-byte");
   const size_t qb = (size_t)tokens * kHq * kD * 2;
@@ -948,9 +954,14 @@ gqa_status_t prefill(const CacheArgs& c, const void* q, int q_dtype, const int32
   p.chunk_starts = chunk_starts;
   p.lens = lens;
   p.tokens = tokens;
+  char* ws = static_cast<char*>(workspace) + GQA_WORKSPACE_HEADER_BYTES;
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws + kPrefillMlBytes);
+  p.ctas = std::min(sms, kPfMaxCtas);
   p.scale_log2 = softmax_scale_log2(q_scale, c.k_scale);
   p.v_scale = c.v_scale;
-  const cudaError_t e = launch_prefill(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, sms, stream);
+  p.wait_budget_ns = kWaitBudgetNs;
+  const cudaError_t e = launch_prefill(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
   return GQA_OK;
 }
@@ -1488,7 +1499,7 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
                  static_cast<cudaStream_t>(stream));
 }
 
-size_t gqa_prefill_workspace_size(void) { return GQA_WORKSPACE_HEADER_BYTES; }
+size_t gqa_prefill_workspace_size(void) { return GQA_WORKSPACE_HEADER_BYTES + kPrefillMlBytes + kPrefillOBytes; }
 
 gqa_status_t gqa_prefill(const void* q, gqa_dtype_t q_dtype, const void* kv, gqa_kv_format_t kv_format,
                          const void* kv_scales, const int32_t* chunk_starts, const int32_t* lens, void* out,

@@ -1,22 +1,296 @@
-// Attention of chunks of new tokens over a cache: the simplest form, a warp for a
-// token and a KV head.
+// Attention of chunks of new tokens over a cache, on the tcgen05 tensor cores.
+//
+// A unit is 64 tokens of a row with the 4 query heads of one KV head: two tiles of 128
+// rows (row = token * 4 + head) that share every K and V tile.  For each 128 slots
+//   S = Q K^T      tcgen05.mma 128x128x128, both operands in shared memory, S in TMEM
+//   P = 2^(S - m)  a warpgroup a tile, a thread a row: no exchange between threads for
+//                  the maximum and the sum; P goes back over S in TMEM, in 16 bits
+//   O += P V       tcgen05.mma, P from TMEM, V as it lies in the cache (MN-major)
+// One thread issues the products in the order S0 S1 | O0 S0' O1 S1' | ...: while one
+// tile's softmax runs the tensor cores work on the other.  The products of one thread
+// run in order, so "S0' is there" says that O0 is complete, and a row's O may be
+// rescaled then without another barrier.  It is rescaled only when its maximum grows
+// by more than 8 (weights up to 2^15: with a maximum at 2^7, small weights of an fp16
+// P stay normal numbers down to 2^-21 of the largest).
+//
+// K and V tiles go through a ring of five 32 KB slots in the 128-byte swizzled layout.
+// 16-bit caches come by TMA (a box of 128 rows, or of a page's), and two warps look at
+// the V tiles that hold slots which some query of the unit does not see: a zero weight
+// times an infinity or NaN there would be NaN, so rows past the length become zeros and
+// other values that are not finite zeros too, to be put into the rows that do see
+// them in the epilogue (rarely: then straight from the cache).  Narrow caches are
+// widened to fp16 (exact) by three warps; a bf16 q is then scaled by a power of two a
+// row into fp16's range, so these calls have fp16 products whatever q's type is.
+// int8 scales multiply the columns of S and of P.
+//
+// All rows' tiles form one stream that the resident CTAs (one an SM) cut into equal
+// runs, whatever the lengths are; a unit cut by a run's end leaves FP32 partials (two a
+// CTA at most) that a second kernel merges.
 #pragma once
+
+#include <cuda.h>
 
 #include "cache_rows.cuh"
 
 namespace gqa {
 
+constexpr int kPfThreads = 384;      // two softmax warpgroups, one of issue and load warps
+constexpr int kPfTokens = 64;        // tokens of a unit
+constexpr int kPfRows = 128;         // rows of a tile
+constexpr int kPfTile = 128;         // slots of a K or V tile
+constexpr int kPfTileBytes = kPfTile * kD * 2;
+constexpr int kPfSlots = 5;
+constexpr int kPfMaxCtas = 160;
+constexpr int kPfMinRun = 2;         // K/V tiles a CTA takes at least
+constexpr float kPfLift = 7.f;       // log2 of the weight of a row's maximum
+constexpr float kPfGrow = 8.f;       // growth of the maximum that a row is rescaled for
+
 struct PrefillParams {
   CacheView c;
-  const void* q;               // [tokens, 32, 128]
-  void* out;                   // [tokens, 32, 128]
+  const void* q;                // [tokens, 32, 128]
+  void* out;                    // [tokens, 32, 128]
   const int32_t* chunk_starts;  // [B + 1]
-  const int32_t* lens;         // [B]
-  int tokens;
+  const int32_t* lens;          // [B]
+  float* part_o;                // [2 * ctas][128 dims][256 rows]
+  float2* part_ml;              // [2 * ctas][256 rows]: maximum, sum
+  int tokens, ctas;
+  int box;                      // rows of a TMA box (16-bit caches)
   float scale_log2, v_scale;
+  uint64_t wait_budget_ns;
 };
 
-// Eight consecutive elements of a row as floats, scales included.
+// ---- the schedule ----------------------------------------------------------
+
+// A batch row's chunk.
+struct PfRow {
+  int at, n, len, base;  // first token, tokens, length, length - tokens
+  __device__ __forceinline__ int units() const { return (n + kPfTokens - 1) / kPfTokens; }
+  // K/V tiles of unit m: up to what its last token sees (a row shorter than its chunk
+  // counts as if it were as long, so that every unit has a tile)
+  __device__ __forceinline__ int tiles(int m) const {
+    return (max(base, 0) + min(n, (m + 1) * kPfTokens) + kPfTile - 1) / kPfTile;
+  }
+  // Sum of tiles(k) for k < m, m < units() or all of them.  tiles(k) = floor((q + k) / 2)
+  // for full units, q = floor((base + 64 + 127) / 64), and sums of floor(j / 2) are squares.
+  __device__ __forceinline__ long long tiles_before(int m) const {
+    const int u = units();
+    const long long q = (max(base, 0) + kPfTokens + kPfTile - 1) / kPfTokens;
+    const auto f = [](long long x) { return (x - 1) * (x - 1) / 4; };
+    const long long full = min(m, u - 1);
+    return m <= 0 ? 0 : f(q + full) - f(q) + (m == u ? tiles(u - 1) : 0);
+  }
+  __device__ __forceinline__ long long all_tiles() const { return n > 0 ? kHkv * tiles_before(units()) : 0; }
+};
+
+__device__ __forceinline__ PfRow pf_row(const PrefillParams& p, int b) {
+  PfRow r;
+  r.at = min(max(__ldg(p.chunk_starts + b), 0), p.tokens);
+  r.n = min(max(__ldg(p.chunk_starts + b + 1), r.at), p.tokens) - r.at;
+  r.len = min(max(__ldg(p.lens + b), 0), p.c.capacity);
+  r.base = r.len - r.n;
+  return r;
+}
+
+// A part of a unit: K/V tiles [j0, j1) of `all`.
+struct PfSegment {
+  int b, g, m, j0, j1, all;
+  PfRow row;
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == all; }
+  __device__ __forceinline__ int tiles() const { return j1 - j0; }
+  __device__ __forceinline__ int rows_of_q() const { return row.n - m * kPfTokens > kPfTokens / 2 ? 2 : 1; }
+  __device__ __forceinline__ int first_seen() const { return row.base + m * kPfTokens; }  // the unit's first token sees slots up to it
+};
+
+// Where a position of the stream lies: position `rem` of row b's.
+__device__ __forceinline__ void pf_locate(const PfRow& r, long long rem, int& g, int& m, int& j) {
+  const int u = r.units();
+  const long long head = r.tiles_before(u);
+  g = (int)(rem / head);
+  rem -= g * head;
+  int lo = 0, hi = u - 1;  // the last unit whose tiles begin at or before rem
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (r.tiles_before(mid) <= rem) lo = mid;
+    else hi = mid - 1;
+  }
+  m = lo;
+  j = (int)(rem - r.tiles_before(lo));
+}
+
+// A CTA's run: each role walks it by itself.
+struct PfCursor {
+  int b, g, m, j;
+  long long left;
+  PfRow row;
+  __device__ __forceinline__ bool next(const PrefillParams& p, PfSegment& s) {
+    if (left <= 0) return false;
+    s.b = b;
+    s.g = g;
+    s.m = m;
+    s.row = row;
+    s.all = row.tiles(m);
+    s.j0 = j;
+    s.j1 = (int)min((long long)s.all, j + left);
+    left -= s.j1 - s.j0;
+    j = 0;
+    if (++m == row.units()) {
+      m = 0;
+      if (++g == kHkv) {
+        g = 0;
+        while (left > 0 && ++b < p.c.batch) {
+          row = pf_row(p, b);
+          if (row.n > 0) break;
+        }
+        if (b >= p.c.batch) left = 0;
+      }
+    }
+    return true;
+  }
+};
+
+struct PfPlan {
+  long long total, run;
+};
+
+// The stream's length and a CTA's run.  Every thread of the block calls it.
+__device__ __forceinline__ PfPlan pf_plan(const PrefillParams& p, long long* s_sum) {
+  long long sum = 0;
+  for (int b = threadIdx.x; b < p.c.batch; b += blockDim.x) sum += pf_row(p, b).all_tiles();
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x / 32] = sum;
+  __syncthreads();
+  PfPlan plan;
+  plan.total = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) plan.total += s_sum[w];
+  plan.run = max((plan.total + p.ctas - 1) / p.ctas, (long long)kPfMinRun);
+  __syncthreads();
+  return plan;
+}
+
+// The row that holds position `at` < total, and the position within it: warp-wide.
+__device__ __forceinline__ int pf_find_row(const PrefillParams& p, long long at, long long& rem) {
+  const int lane = threadIdx.x & 31;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.c.batch; b0 += 32) {
+    const long long mine = b0 + lane < p.c.batch ? pf_row(p, b0 + lane).all_tiles() : 0;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > at);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      rem = at - before - __shfl_sync(0xffffffffu, upto - mine, k);
+      return b0 + k;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  rem = 0;
+  return p.c.batch;
+}
+
+// ---- tcgen05 ---------------------------------------------------------------
+
+// Shared-memory descriptor of a 128-byte swizzled operand: K-major (lead unused) or
+// MN-major (lead: bytes from 64 elements of M or N to the next); 1024 bytes from eight
+// rows to the next.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t address, uint32_t lead) {
+  return (uint64_t)((address & 0x3ffffu) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// FP32 accumulators, 128 x 128, fp16 or bf16 operands; B MN-major for P V.
+__host__ __device__ constexpr uint32_t tc_idesc(bool bf16, bool b_mn) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"((uint32_t)add)
+      : "memory");
+}
+// The barrier is arrived at when every product issued so far by this thread is done.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+#define GQA_R8(a, i) "=r"((a)[i]), "=r"((a)[(i) + 1]), "=r"((a)[(i) + 2]), "=r"((a)[(i) + 3]), "=r"((a)[(i) + 4]), \
+                     "=r"((a)[(i) + 5]), "=r"((a)[(i) + 6]), "=r"((a)[(i) + 7])
+#define GQA_W8(a, i) "r"((a)[i]), "r"((a)[(i) + 1]), "r"((a)[(i) + 2]), "r"((a)[(i) + 3]), "r"((a)[(i) + 4]), \
+                     "r"((a)[(i) + 5]), "r"((a)[(i) + 6]), "r"((a)[(i) + 7])
+// 32 columns of the warp's 32 TMEM lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t* x, uint32_t address) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : GQA_R8(x, 0), GQA_R8(x, 8), GQA_R8(x, 16), GQA_R8(x, 24)
+      : "r"(address)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t address, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(address),
+      GQA_W8(x, 0), GQA_W8(x, 8), GQA_W8(x, 16), GQA_W8(x, 24)
+      : "memory");
+}
+#undef GQA_R8
+#undef GQA_W8
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// A box of the cache, 64 elements wide, to shared memory.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int row, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(row), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// ---- shared memory ---------------------------------------------------------
+
+struct PfShared {
+  uint8_t q[2][kPfTileBytes];         // [tile][64-dim half][row][128 bytes]
+  uint8_t kv[kPfSlots][kPfTileBytes];  // [64-dim half][slot][128 bytes]
+  // int8: a tile's K and V row scales and the V scales' exponents (bf16 bits).  Three
+  // tiles' are enough: a slot of K or V of tile j is free once the softmax of tile
+  // j - 3 is done, five slots being two and a half tiles.
+  uint16_t scales[3][3][kPfTile];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t kv_full[kPfSlots], kv_empty[kPfSlots], v_fixed[4];
+  long long sum[kPfThreads / 32];
+  PfCursor cursor;
+  uint32_t tmem;
+  int odd[8];  // a segment's number + 1 where a value was taken out of V
+};
+
+// Position of a 16-byte piece of a row in a swizzled tile.
+__device__ __forceinline__ uint32_t pf_piece(int row, int piece) {
+  return (uint32_t)((piece >> 3) * (kPfTileBytes / 2) + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void st_shared16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+// Neither infinite nor NaN, of two 16-bit numbers.
+template <int QF>
+__device__ __forceinline__ bool pair_finite(uint32_t w) {
+  constexpr uint32_t kExp = QF == kQF16 ? 0x7c00u : 0x7f80u;
+  return (w & kExp) != kExp && (w >> 16 & kExp) != kExp;
+}
+
+// Eight elements of a row as floats, the tensor scale left out.
 template <int KVF>
 __device__ __forceinline__ void row8(const CacheView& c, size_t row, int i, float (&x)[8]) {
   if constexpr (!is_narrow(KVF)) {
@@ -30,7 +304,6 @@ __device__ __forceinline__ void row8(const CacheView& c, size_t row, int i, floa
     }
   } else {
     uint32_t w[4] = {}, d[8];
-    float s = 1.f;
     uint32_t group = 0;
     if constexpr (KVF == kKvE2M1) {
       w[0] = __ldg(reinterpret_cast<const uint32_t*>(c.kv) + row * 16 + i);
@@ -39,84 +312,573 @@ __device__ __forceinline__ void row8(const CacheView& c, size_t row, int i, floa
       const uint2 v = __ldg(reinterpret_cast<const uint2*>(c.kv) + row * 16 + i);
       w[0] = v.x;
       w[1] = v.y;
-      if constexpr (KVF == kKvI8) s = bf16_bits_to_f32(__ldg(static_cast<const uint16_t*>(c.scales) + row));
     }
     widen16<KVF, kQF16>(w, group, d);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = f16x2_to_f32x2(d[k]);
-      x[2 * k] = f.x * s;
-      x[2 * k + 1] = f.y * s;
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
     }
   }
 }
 
+// ---- the kernel ------------------------------------------------------------
+
+// KVF: cache format, QF: q's and out's type.  The products' type is a 16-bit cache's,
+// else fp16.
 template <int KVF, int QF>
-__global__ void __launch_bounds__(128) prefill_kernel(const __grid_constant__ PrefillParams p) {
-  __shared__ float s_q[4][4][kD];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = blockIdx.y;
-  const int i = blockIdx.x * 4 + warp;
-  if (i >= p.tokens) return;
-  int b = 0, at = 0, n = 0;
-  for (; b < p.c.batch; ++b) {
-    at = min(max(__ldg(p.chunk_starts + b), 0), p.tokens);
-    n = min(max(__ldg(p.chunk_starts + b + 1), at), p.tokens) - at;
-    if (i >= at && i < at + n) break;
+__global__ void __launch_bounds__(kPfThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap map) {
+  constexpr bool kNarrow = is_narrow(KVF), kI8 = KVF == kKvI8;
+  constexpr int MF = kNarrow ? (int)kQF16 : QF;  // type of the products' operands
+  extern __shared__ __align__(1024) uint8_t s_raw[];
+  PfShared& sm = *reinterpret_cast<PfShared*>(s_raw);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  pdl_launch_dependents();
+  if (smem_addr(s_raw) % 1024 != 0) {  // (the swizzled tiles need it; it is so)
+    if (tid == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_BOUNDS);
+    return;
   }
-  if (b == p.c.batch) return;
-  const int len = clamp_length(__ldg(p.lens + b), p.c.capacity, p.c.flags, lane == 0);
-  const int end = len - n + (i - at) + 1;  // slots seen
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + ((size_t)i * kHq + 4 * g) * kD;
-  for (int k = lane; k < 2 * kD; k += 32) {
-    const float2 f = pair_to_f32x2<QF>(reinterpret_cast<const uint32_t*>(q)[k]);
-    s_q[warp][k / 64][2 * (k % 64)] = f.x;
-    s_q[warp][k / 64][2 * (k % 64) + 1] = f.y;
-  }
-  __syncwarp();
-  float m[4], l[4], o[4][4];
-  for (int h = 0; h < 4; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    for (int k = 0; k < 4; ++k) o[h][k] = 0.f;
-  }
-  for (int t0 = 0; t0 < end; t0 += 32) {
-    const int t = min(t0 + lane, end - 1);
-    const size_t krow = cache_row(p.c, b, g, t);
-    float s[4] = {};
-    for (int k = 0; k < 16; ++k) {
-      float x[8];
-      row8<KVF>(p.c, krow, k, x);
-      for (int h = 0; h < 4; ++h)
-        for (int e = 0; e < 8; ++e) s[h] += x[e] * s_q[warp][h][8 * k + e];
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], kPfRows);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], kPfRows);
+      mbar_init(&sm.o_full[i], 1);
     }
-    for (int h = 0; h < 4; ++h) {
-      const bool in = t0 + lane < end;
-      s[h] = in ? s[h] * p.scale_log2 : -INFINITY;
-      float top = fmaxf(m[h], s[h]);
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - top);
-      m[h] = top;
-      s[h] = in ? ex2(s[h] - (top == -INFINITY ? 0.f : top)) : 0.f;
-      float sum = s[h];
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-      l[h] = l[h] * f + sum;
-      for (int k = 0; k < 4; ++k) o[h][k] *= f;
+    for (int i = 0; i < kPfSlots; ++i) {
+      mbar_init(&sm.kv_full[i], kNarrow ? 3 : 1);
+      mbar_init(&sm.kv_empty[i], 1);
     }
-    for (int j = 0; j < min(32, end - t0); ++j) {
-      const size_t vrow = cache_row(p.c, b, kHkv + g, t0 + j);
-      float x[8];
-      row8<KVF>(p.c, vrow, lane / 2, x);
-      for (int h = 0; h < 4; ++h) {
-        const float w = __shfl_sync(0xffffffffu, s[h], j);
-        for (int k = 0; k < 4; ++k) o[h][k] += w * (lane & 1 ? x[4 + k] : x[k]);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.v_fixed[i], 2);
+    mbar_init(&sm.done, 1);
+    for (int i = 0; i < 8; ++i) sm.odd[i] = 0;
+    fence_barrier_init();
+  }
+  pdl_wait_prior_grid();
+  const PfPlan plan = pf_plan(p, sm.sum);
+  const long long begin = (long long)blockIdx.x * plan.run;
+  if (begin >= plan.total) return;  // (all of the block)
+  if (warp == 0) {
+    long long rem;
+    const int b = pf_find_row(p, begin, rem);
+    if (lane == 0) {
+      PfCursor c;
+      c.b = b;
+      c.row = pf_row(p, b);
+      c.left = min(plan.run, plan.total - begin);
+      pf_locate(c.row, rem, c.g, c.m, c.j);
+      sm.cursor = c;
+    }
+  } else if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_fence_before();
+  }
+  // lengths and starts that are out of order are told once
+  if (blockIdx.x == 0 && p.c.flags) {
+    for (int b = tid; b < p.c.batch; b += kPfThreads) {
+      const int at = __ldg(p.chunk_starts + b), end = __ldg(p.chunk_starts + b + 1), len = __ldg(p.lens + b);
+      if (at < 0 || end < at || end > p.tokens || len < 0 || len > p.c.capacity || len < end - at)
+        atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  PfCursor cur = sm.cursor;
+  PfSegment sg;
+  const uint64_t budget = p.wait_budget_ns;
+  bool ok = true;
+  // bounded waits: of one thread, and of a warp, whose lanes go on or give up together
+  const auto wait_one = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, global_timer_ns() + budget);
+    return ok;
+  };
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    wait_one(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+
+  // Registers: 168 a thread at launch, 504 over the three warpgroups' like threads;
+  // 208 for each softmax thread (a row of S is 128) and 88 for the others use as many.
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int t = warp / 4, r = tid & (kPfRows - 1);
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 TMEM lanes
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * 128;
+    uint32_t s_phase = 0;
+    uint32_t seg = 0, o_phase = 0;
+    int tile_no = 0;  // of the CTA's K/V tiles, for the scales' ring
+    for (; ok && cur.next(p, sg); ++seg) {
+      if (t >= sg.rows_of_q()) {
+        tile_no += sg.tiles();
+        continue;
+      }
+      const int token = sg.m * kPfTokens + t * 32 + r / 4;
+      const bool live = token < sg.row.n;
+      const size_t row_at = ((size_t)(sg.row.at + token) * kHq + 4 * sg.g + (r & 3)) * kD;
+      float scale = p.scale_log2;
+      {
+        uint4 x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          x[i] = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_at) + i)
+                      : make_uint4(0, 0, 0, 0);
+        if constexpr (kNarrow && QF == kQBF16) {
+          // by a power of two into fp16's range: the largest |q| into [2^14, 2^15)
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+          }
+          // (its exponent -100 at least, so that the scale's stays a normal number)
+          const int e = min(max((int)(top >> 7) - 127, -100), 127);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23), down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+          scale *= down;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = bf16x2_to_f32x2(w[k]);
+              w[k] = round2<kQF16>(f.x * up, f.y * up);
+            }
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(sm.q[t] + pf_piece(r, i)) = x[i];
+      }
+      proxy_fence();
+      mbar_arrive(&sm.q_full[t]);
+      // slots that the row sees: up to `seen` (none: a row without a token, or without a slot)
+      const int seen = live ? sg.row.base + token : -1;
+      float m = -INFINITY, l = 0.f;
+      for (int j = sg.j0; ok && j < sg.j1; ++j, ++tile_no) {
+        if (!wait(&sm.s_full[t], s_phase)) break;
+        s_phase ^= 1;
+        tc_fence_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_ld32(x + 32 * k, s_at + 32 * k);
+        tc_wait_ld();
+        float* s = reinterpret_cast<float*>(x);
+        const uint16_t(*scales)[kPfTile] = sm.scales[tile_no % 3];
+        if constexpr (kI8) {
+          // (the scales of V are there with V, which is the ring's next item)
+          const uint32_t v_item = 2 * (uint32_t)tile_no + 1;
+          if (!wait(&sm.kv_full[v_item % kPfSlots], v_item / kPfSlots & 1)) break;
+#pragma unroll
+          for (int k = 0; k < 128; k += 2) {
+            const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[0] + k));
+            s[k] *= f.x;
+            s[k + 1] *= f.y;
+          }
+        }
+        const int visible = seen - j * kPfTile + 1;  // columns of this tile that the row sees
+        const bool masked = __any_sync(0xffffffffu, visible < kPfTile);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = k < visible ? s[k] : -INFINITY;
+        }
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < 128; k += 4) {
+          if constexpr (kI8) {
+            // int8: of the weight times its V scale, which is what P holds
+            const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[2] + k));
+            const float2 g = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[2] + k + 2));
+            top4[0] = fmaxf(top4[0], fmaf(s[k], scale, f.x));
+            top4[1] = fmaxf(top4[1], fmaf(s[k + 1], scale, f.y));
+            top4[2] = fmaxf(top4[2], fmaf(s[k + 2], scale, g.x));
+            top4[3] = fmaxf(top4[3], fmaf(s[k + 3], scale, g.y));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top4[i] = fmaxf(top4[i], s[k + i]);
+          }
+        }
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * (kI8 ? 1.f : scale);
+        if (__any_sync(0xffffffffu, top > m + kPfGrow)) {
+          const float grown = fmaxf(m, top);
+          const float f = m == grown ? 1.f : ex2(m - grown);  // (0 from -inf)
+          m = grown;
+          l *= f;
+          if (j > sg.j0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[32];
+              tc_ld32(o, o_at + 32 * k);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc_st32(o_at + 32 * k, o);
+            }
+          }
+        }
+        const float minus = kPfLift - (m == -INFINITY ? 0.f : m);
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 128; k += 4) {
+          float w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = ex2(fmaf(s[k + i], scale, minus));
+            sum4[i] += w[i];
+          }
+          if constexpr (kI8) {
+            const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[1] + k));
+            const float2 g = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[1] + k + 2));
+            // (a hidden slot's weight stays zero whatever its scale is)
+            w[0] = masked && k >= visible ? 0.f : w[0] * f.x;
+            w[1] = masked && k + 1 >= visible ? 0.f : w[1] * f.y;
+            w[2] = masked && k + 2 >= visible ? 0.f : w[2] * g.x;
+            w[3] = masked && k + 3 >= visible ? 0.f : w[3] * g.y;
+          }
+          x[k / 2] = round2<MF>(w[0], w[1]);
+          x[k / 2 + 1] = round2<MF>(w[2], w[3]);
+        }
+        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+        tc_st32(s_at, x);
+        tc_st32(s_at + 32, x + 32);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[t]);
+      }
+      if (!wait(&sm.o_full[t], o_phase)) break;
+      o_phase ^= 1;
+      tc_fence_after();
+      const bool odd = sm.odd[seg & 7] == (int)seg + 1;
+      const bool whole = sg.whole();
+      const int slot = 2 * (int)blockIdx.x + (sg.j0 > 0 ? 0 : 1);
+      const float f = l == 0.f ? 0.f : p.v_scale / l;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        uint32_t o[32];
+        __syncwarp();
+        tc_ld32(o, o_at + 32 * k);
+        tc_wait_ld();
+        if (odd) {
+          // values taken out of V: into the rows that see their slots
+          for (int u = max(sg.first_seen() + 1, sg.j0 * kPfTile); u <= min(seen, sg.j1 * kPfTile - 1); ++u) {
+            const size_t vrow = cache_row(p.c, sg.b, kHkv + sg.g, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y[8];
+              row8<KVF>(p.c, vrow, 4 * k + i, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (!(fabsf(y[e]) <= 3.4e38f)) o[8 * i + e] = __float_as_uint(__uint_as_float(o[8 * i + e]) + y[e]);
+            }
+          }
+        }
+        if (whole) {
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_at) + 4 * k;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = round2<QF>(__uint_as_float(o[8 * i + 2 * e]) * f, __uint_as_float(o[8 * i + 2 * e + 1]) * f);
+              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+          float* dst = p.part_o + ((size_t)slot * kD + 32 * k) * (2 * kPfRows) + t * kPfRows + r;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dst[i * (2 * kPfRows)] = __uint_as_float(o[i]);
+        }
+      }
+      if (!whole) p.part_ml[(size_t)slot * (2 * kPfRows) + t * kPfRows + r] = make_float2(m, l);
+    }
+  } else if (warp == 8) {
+    // ----------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t kQk = tc_idesc(MF == kQBF16, false), kPv = tc_idesc(MF == kQBF16, true);
+      const uint32_t q0 = smem_addr(sm.q[0]), kv0 = smem_addr(sm.kv[0]);
+      const auto qk = [&](int t, int slot) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * (kPfTileBytes / 2) + (k & 3) * 32;
+          tc_mma_ss(tmem + t * 128, tc_desc(q0 + t * kPfTileBytes + off, 16), tc_desc(kv0 + slot * kPfTileBytes + off, 16), kQk,
+                    k > 0);
+        }
+      };
+      const auto pv = [&](int t, int slot, bool add) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, tc_desc(kv0 + slot * kPfTileBytes + k * 2048, kPfTileBytes / 2),
+                    kPv, add || k > 0);
+      };
+      uint32_t item = 0, v_no = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      while (ok && cur.next(p, sg)) {
+        const int nq = sg.rows_of_q(), n = sg.tiles();
+        for (int j = -1; ok && j < n; ++j) {
+          const uint32_t v_item = item - 1;  // (of tile j; K of tile j + 1 is item)
+          const int k_slot = (int)(item % kPfSlots);
+          const uint32_t k_parity = item / kPfSlots & 1;
+          if (j >= 0) {
+            const int v_slot = (int)(v_item % kPfSlots);
+            const bool there = kNarrow ? wait_one(&sm.kv_full[v_slot], v_item / kPfSlots & 1)
+                                       : wait_one(&sm.v_fixed[v_no & 3], v_no >> 2 & 1);
+            if (!there) break;
+            ++v_no;
+          }
+          for (int t = 0; t < nq; ++t) {
+            if (j >= 0) {
+              if (!wait_one(&sm.p_full[t], p_phase[t])) break;
+              p_phase[t] ^= 1;
+              tc_fence_after();
+              pv(t, (int)(v_item % kPfSlots), j > 0);
+              if (j == n - 1) tc_commit(&sm.o_full[t]);
+              if (t == nq - 1) tc_commit(&sm.kv_empty[v_item % kPfSlots]);
+            } else {
+              if (!wait_one(&sm.q_full[t], q_phase[t])) break;
+              q_phase[t] ^= 1;
+              tc_fence_after();
+            }
+            if (j + 1 < n) {
+              if (t == 0 && !wait_one(&sm.kv_full[k_slot], k_parity)) break;
+              qk(t, k_slot);
+              tc_commit(&sm.s_full[t]);
+              if (t == nq - 1) tc_commit(&sm.kv_empty[k_slot]);
+            }
+          }
+          if (j + 1 < n) item += 2;
+        }
+      }
+      if (!ok) {  // products in flight end before the block's memory is given up
+        tc_commit(&sm.done);
+        mbar_wait(&sm.done, 0, global_timer_ns() + 1000000000ull);
       }
     }
+  } else {
+    // -------------------------------------------------------- K and V tiles
+    uint32_t item = 0;
+    uint32_t seg = 0, v_no = 0;
+    int tile_no = 0;
+    for (; ok && cur.next(p, sg); ++seg) {
+      const int len = sg.row.len;
+      for (int j = sg.j0; ok && j < sg.j1; ++j, ++tile_no) {
+        const int t0 = j * kPfTile;
+        const bool hidden = t0 + kPfTile - 1 > sg.first_seen();  // slots that some query does not see
+        for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+          const int slot = (int)(item % kPfSlots);
+          const uint32_t round = item / kPfSlots;
+          const int pg = plane * kHkv + sg.g;
+          uint8_t* dst = sm.kv[slot];
+          if constexpr (kNarrow) {
+            if (!wait(&sm.kv_empty[slot], (round & 1) ^ 1)) break;
+            const int worker = tid - 288;  // 96 of them
+            bool odd = false;
+            // pieces of 16 elements, eight to a row
+            constexpr int kBatch = 4;
+            for (int i0 = worker; i0 < kPfTile * 8; i0 += 96 * kBatch) {
+              uint4 x[kBatch];
+              uint32_t sc[kBatch];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + 96 * k, row = i >> 3, piece = i & 7;
+                x[k] = make_uint4(0, 0, 0, 0);
+                sc[k] = 0;
+                if (i < kPfTile * 8 && t0 + row < len) {
+                  const size_t at = cache_row(p.c, sg.b, pg, t0 + row);
+                  if constexpr (KVF == kKvE2M1) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.c.kv) + at * 8 + piece);
+                    x[k].x = v.x;
+                    x[k].y = v.y;
+                    sc[k] = __ldg(static_cast<const uint8_t*>(p.c.scales) + at * 8 + piece);
+                  } else {
+                    x[k] = __ldg(reinterpret_cast<const uint4*>(p.c.kv) + at * 8 + piece);
+                    if constexpr (kI8)
+                      if (piece == 0) sc[k] = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
+                  }
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + 96 * k, row = i >> 3, piece = i & 7;
+                if (i >= kPfTile * 8) continue;
+                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                uint32_t d[8];
+                widen16<KVF, kQF16>(w, sc[k], d);
+                if constexpr (!kI8) {
+                  if (plane == 1 && hidden && t0 + row > sg.first_seen()) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                      if (!pair_finite<kQF16>(d[e])) {
+                        odd = true;
+                        if (!pair_finite<kQF16>(d[e] & 0xffffu)) d[e] &= 0xffff0000u;
+                        if (!pair_finite<kQF16>(d[e] & 0xffff0000u)) d[e] &= 0xffffu;
+                      }
+                    }
+                  }
+                }
+                st_shared16(dst + pf_piece(row, 2 * piece), d[0], d[1], d[2], d[3]);
+                st_shared16(dst + pf_piece(row, 2 * piece + 1), d[4], d[5], d[6], d[7]);
+                if constexpr (kI8)
+                  if (piece == 0) {
+                    uint16_t(*scales)[kPfTile] = sm.scales[tile_no % 3];
+                    scales[plane][row] = (uint16_t)sc[k];
+                    // |scale| <= 2^lg (-60 at least, so that the weights' sum stays in range)
+                    const int lg = max((int)(sc[k] >> 7 & 0xff) - 126, -60);
+                    if (plane == 1) scales[2][row] = (uint16_t)(__float_as_uint((float)lg) >> 16);
+                  }
+              }
+            }
+            if (odd) sm.odd[seg & 7] = (int)seg + 1;
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.kv_full[slot]);
+          } else if (warp == 9) {
+            if (!wait(&sm.kv_empty[slot], (round & 1) ^ 1)) break;
+            // boxes of `box` rows: one, or a page's each; pages past the length are left out
+            const int boxes = kPfTile / p.box;
+            int row = -1;
+            if (p.c.block_table == nullptr) {
+              if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
+            } else if (lane < boxes && t0 + lane * p.box < len) {
+              row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
+            }
+            const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) {
+              if (some) mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(__popc(some) * p.box * kD * 2));
+              else mbar_arrive(&sm.kv_full[slot]);
+            }
+            __syncwarp();
+            if (row >= 0) {
+              const uint32_t at = smem_addr(dst) + lane * p.box * 128;
+              tma_box(at, &map, 0, row, &sm.kv_full[slot]);
+              tma_box(at + kPfTileBytes / 2, &map, 64, row, &sm.kv_full[slot]);
+            }
+          } else if (plane == 1) {
+            // the V tiles that hold hidden slots
+            if (!wait(&sm.kv_full[slot], round & 1)) break;
+            if (hidden) {
+              bool odd = false;
+              for (int i = tid - 320; i < kPfTile * 16; i += 64) {
+                const int row = i >> 4, u = t0 + row;
+                if (u <= sg.first_seen()) continue;
+                uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
+                if (u >= len) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                uint4 v = *at;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
+                  if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
+                }
+                if (bad) {
+                  odd = true;
+                  *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              if (odd) sm.odd[seg & 7] = (int)seg + 1;
+              proxy_fence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_fixed[v_no & 3]);
+            ++v_no;
+          }
+        }
+      }
+    }
+    // copies in flight land before the block's shared memory is given up
+    if (!kNarrow && warp == 9 && !ok) {
+      ok = true;
+      for (uint32_t k = item > kPfSlots ? item - kPfSlots : 0; k < item; ++k)
+        mbar_wait(&sm.kv_full[k % kPfSlots], k / kPfSlots & 1, global_timer_ns() + 1000000ull);
+      ok = false;
+    }
   }
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + ((size_t)i * kHq + 4 * g) * kD) + 2 * lane;
-  for (int h = 0; h < 4; ++h) {
-    const float f = l[h] == 0.f ? 0.f : p.v_scale / l[h];
-    out[64 * h] = round2<QF>(o[h][0] * f, o[h][1] * f);
-    out[64 * h + 1] = round2<QF>(o[h][2] * f, o[h][3] * f);
+  if (!ok && lane == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_WAIT_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ---- merging a unit's pieces -----------------------------------------------
+
+constexpr int kMergeThreads = 128;
+
+// CTA (c, k): rows [32 k, 32 k + 32) of the unit that run c begins inside of, if c is
+// the first run that does.
+template <int QF>
+__global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  __shared__ long long s_sum[kMergeThreads / 32];
+  __shared__ PfSegment s_unit;
+  __shared__ int s_pieces;  // 0: nothing to do
+  __shared__ long long s_begin;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const PfPlan plan = pf_plan(p, s_sum);
+  const int c = (int)blockIdx.x + 1;
+  const long long at = c * plan.run;
+  if (at >= plan.total) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    long long rem;
+    const int b = pf_find_row(p, at, rem);
+    if (lane == 0) {
+      PfSegment u;
+      u.b = b;
+      u.row = pf_row(p, b);
+      int j;
+      pf_locate(u.row, rem, u.g, u.m, j);
+      u.all = u.row.tiles(u.m);
+      const long long begin = at - j;  // the unit's first position
+      s_begin = begin;
+      // inside the unit, and no earlier run's begin is
+      s_pieces = j > 0 && at - plan.run <= begin ? (int)((begin + u.all - 1) / plan.run - begin / plan.run) + 1 : 0;
+      s_unit = u;
+    }
+  }
+  __syncthreads();
+  if (s_pieces == 0) return;
+  const PfSegment u = s_unit;
+  const int row = 32 * (int)blockIdx.y + lane, token = u.m * kPfTokens + row / 4;
+  if (u.m * kPfTokens + 8 * (int)blockIdx.y >= u.row.n) return;
+  const bool live = token < u.row.n;
+  const int first = (int)(s_begin / plan.run);
+  float m = -INFINITY;
+  const auto slot_of = [&](int k) { return 2 * (first + k) + ((long long)(first + k) * plan.run > s_begin ? 0 : 1); };
+  for (int k = 0; k < s_pieces; ++k) m = fmaxf(m, p.part_ml[(size_t)slot_of(k) * (2 * kPfRows) + row].x);
+  float l = 0.f, o[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) o[i] = 0.f;
+  for (int k = 0; k < s_pieces; ++k) {
+    const int slot = slot_of(k);
+    const float2 x = p.part_ml[(size_t)slot * (2 * kPfRows) + row];
+    const float f = x.x == -INFINITY ? 0.f : ex2(x.x - m);
+    if (x.y != 0.f) l += x.y * f;
+    const float* src = p.part_o + ((size_t)slot * kD + 32 * warp) * (2 * kPfRows) + row;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = fmaf(src[i * (2 * kPfRows)], f, o[i]);
+  }
+  if (!live) return;
+  const float f = l == 0.f ? 0.f : p.v_scale / l;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                        ((size_t)(u.row.at + token) * kHq + 4 * u.g + (row & 3)) * kD + 32 * warp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = round2<QF>(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
+    dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
