@@ -960,7 +960,6 @@ gqa_status_t prefill(const CacheArgs& c, const void* q, int q_dtype, const int32
   p.ctas = std::min(sms, kPfMaxCtas);
   p.scale_log2 = softmax_scale_log2(q_scale, c.k_scale);
   p.v_scale = c.v_scale;
-  p.wait_budget_ns = kWaitBudgetNs;
   const cudaError_t e = launch_prefill(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, stream);
   if (e != cudaSuccess) return cuda_fail(e, "prefill kernel launch");
   return GQA_OK;

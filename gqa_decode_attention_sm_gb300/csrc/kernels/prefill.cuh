@@ -56,7 +56,6 @@ struct PrefillParams {
   int tokens, ctas;
   int box;                      // rows of a TMA box (16-bit caches)
   float scale_log2, v_scale;
-  uint64_t wait_budget_ns;
 };
 
 // ---- the schedule ----------------------------------------------------------
@@ -91,16 +90,6 @@ __device__ __forceinline__ PfRow pf_row(const PrefillParams& p, int b) {
   return r;
 }
 
-// A part of a unit: K/V tiles [j0, j1) of `all`.
-struct PfSegment {
-  int b, g, m, j0, j1, all;
-  PfRow row;
-  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == all; }
-  __device__ __forceinline__ int tiles() const { return j1 - j0; }
-  __device__ __forceinline__ int rows_of_q() const { return row.n - m * kPfTokens > kPfTokens / 2 ? 2 : 1; }
-  __device__ __forceinline__ int first_seen() const { return row.base + m * kPfTokens; }  // the unit's first token sees slots up to it
-};
-
 // Where a position of the stream lies: position `rem` of row b's.
 __device__ __forceinline__ void pf_locate(const PfRow& r, long long rem, int& g, int& m, int& j) {
   const int u = r.units();
@@ -117,35 +106,47 @@ __device__ __forceinline__ void pf_locate(const PfRow& r, long long rem, int& g,
   j = (int)(rem - r.tiles_before(lo));
 }
 
-// A CTA's run: each role walks it by itself.
+// A CTA's run, walked by each warp by itself: the part of a unit that it is at, K/V
+// tiles [j0, j1) of `all`.  Kept in shared memory, one for each warp: a row of S leaves
+// a softmax thread no registers for it, and it is looked at once a unit.
 struct PfCursor {
-  int b, g, m, j;
-  long long left;
+  long long left;  // tiles of the run from j0 on
   PfRow row;
-  __device__ __forceinline__ bool next(const PrefillParams& p, PfSegment& s) {
-    if (left <= 0) return false;
-    s.b = b;
-    s.g = g;
-    s.m = m;
-    s.row = row;
-    s.all = row.tiles(m);
-    s.j0 = j;
-    s.j1 = (int)min((long long)s.all, j + left);
-    left -= s.j1 - s.j0;
-    j = 0;
-    if (++m == row.units()) {
-      m = 0;
-      if (++g == kHkv) {
-        g = 0;
-        while (left > 0 && ++b < p.c.batch) {
-          row = pf_row(p, b);
-          if (row.n > 0) break;
+  int b, g, m, j0, j1, all, begun;
+  // The next part, by one lane.
+  __device__ __forceinline__ void step(const PrefillParams& p) {
+    if (begun) {
+      left -= j1 - j0;
+      j0 = 0;
+      if (++m == row.units()) {
+        m = 0;
+        if (++g == kHkv) {
+          g = 0;
+          while (left > 0 && ++b < p.c.batch) {
+            row = pf_row(p, b);
+            if (row.n > 0) break;
+          }
+          if (b >= p.c.batch) left = 0;
         }
-        if (b >= p.c.batch) left = 0;
       }
     }
-    return true;
+    begun = 1;
+    if (left > 0) {
+      all = row.tiles(m);
+      j1 = (int)min((long long)all, j0 + left);
+    }
   }
+  // The same by a warp; false at the run's end.
+  __device__ __forceinline__ bool next(const PrefillParams& p) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) step(p);
+    __syncwarp();
+    return left > 0;
+  }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == all; }
+  __device__ __forceinline__ int rows_of_q() const { return row.n - m * kPfTokens > kPfTokens / 2 ? 2 : 1; }
+  // the last slot that every token of the unit sees
+  __device__ __forceinline__ int first_seen() const { return row.base + m * kPfTokens; }
 };
 
 struct PfPlan {
@@ -205,24 +206,36 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t address, uint32_t lead) {
 __host__ __device__ constexpr uint32_t tc_idesc(bool bf16, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One lane of a converged warp, always the same.  The whole warp runs the code around
+// a product, so that its operands stay in uniform registers; the lane issues it.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t one;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if (elect_lane())
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)add)
-      : "memory");
+  if (elect_lane())
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"((uint32_t)add)
+        : "memory");
 }
-// The barrier is arrived at when every product issued so far by this thread is done.
+// The barrier is arrived at when every product issued so far by the elected lane is done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+  if (elect_lane())
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -264,17 +277,54 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 struct PfShared {
   uint8_t q[2][kPfTileBytes];         // [tile][64-dim half][row][128 bytes]
   uint8_t kv[kPfSlots][kPfTileBytes];  // [64-dim half][slot][128 bytes]
-  // int8: a tile's K and V row scales and the V scales' exponents (bf16 bits).  Three
-  // tiles' are enough: a slot of K or V of tile j is free once the softmax of tile
-  // j - 3 is done, five slots being two and a half tiles.
-  uint16_t scales[3][3][kPfTile];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
-  uint64_t kv_full[kPfSlots], kv_empty[kPfSlots], v_fixed[4];
-  long long sum[kPfThreads / 32];
-  PfCursor cursor;
+  // int8: a tile's K and V row scales (bf16 bits).  Three tiles' are enough: a slot of K
+  // or V of tile j is free once the softmax of tile j - 3 is done, five slots being two
+  // and a half tiles.
+  uint16_t scales[3][2][kPfTile];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;  // (P in halves of 64 slots)
+  // Of a tile: K there, V there, V looked through (tile & 3 each; at most three tiles
+  // are between a load and its product).  A barrier is waited on in every one of its
+  // phases by whoever waits on it: a parity says nothing about a phase further on.
+  uint64_t k_full[4], v_full[4], v_fixed[4];
+  uint64_t kv_empty[kPfSlots];
+  PfCursor cursor[kPfThreads / 32 + 3];  // (three of the loads ahead of a narrow cache)
   uint32_t tmem;
   int odd[8];  // a segment's number + 1 where a value was taken out of V
 };
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Waits for a phase, two seconds at most (32 bits of the nanosecond timer keep the
+// registers of the waiting roles free).
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const auto now = [] {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+  };
+  const uint32_t begun = now();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (now() - begun > 2000000000u) return false;
+  }
+}
 
 // Position of a 16-byte piece of a row in a swizzled tile.
 __device__ __forceinline__ uint32_t pf_piece(int row, int piece) {
@@ -344,32 +394,34 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], kPfRows);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kPfRows);
+      mbar_init(&sm.p_full[i][0], kPfRows);
+      mbar_init(&sm.p_full[i][1], kPfRows);
       mbar_init(&sm.o_full[i], 1);
     }
-    for (int i = 0; i < kPfSlots; ++i) {
-      mbar_init(&sm.kv_full[i], kNarrow ? 3 : 1);
-      mbar_init(&sm.kv_empty[i], 1);
+    for (int i = 0; i < kPfSlots; ++i) mbar_init(&sm.kv_empty[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&sm.k_full[i], kNarrow ? 3 : 1);
+      mbar_init(&sm.v_full[i], kNarrow ? 3 : 1);
+      mbar_init(&sm.v_fixed[i], 2);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sm.v_fixed[i], 2);
     mbar_init(&sm.done, 1);
     for (int i = 0; i < 8; ++i) sm.odd[i] = 0;
     fence_barrier_init();
   }
   pdl_wait_prior_grid();
-  const PfPlan plan = pf_plan(p, sm.sum);
+  const PfPlan plan = pf_plan(p, reinterpret_cast<long long*>(sm.q[0]));
   const long long begin = (long long)blockIdx.x * plan.run;
   if (begin >= plan.total) return;  // (all of the block)
   if (warp == 0) {
     long long rem;
     const int b = pf_find_row(p, begin, rem);
-    if (lane == 0) {
-      PfCursor c;
+    if (lane < kPfThreads / 32 + 3) {
+      PfCursor& c = sm.cursor[lane];
       c.b = b;
       c.row = pf_row(p, b);
       c.left = min(plan.run, plan.total - begin);
-      pf_locate(c.row, rem, c.g, c.m, c.j);
-      sm.cursor = c;
+      c.begun = 0;
+      pf_locate(c.row, rem, c.g, c.m, c.j0);
     }
   } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
@@ -387,17 +439,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  PfCursor cur = sm.cursor;
-  PfSegment sg;
-  const uint64_t budget = p.wait_budget_ns;
+  PfCursor& sg = sm.cursor[warp];
   bool ok = true;
-  // bounded waits: of one thread, and of a warp, whose lanes go on or give up together
-  const auto wait_one = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait(bar, parity, global_timer_ns() + budget);
-    return ok;
-  };
+  // a bounded wait of a warp, whose lanes go on or give up together
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    wait_one(bar, parity);
+    if (!pf_wait(bar, parity)) ok = false;
     ok = __all_sync(0xffffffffu, ok);
     return ok;
   };
@@ -414,37 +460,41 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint32_t s_phase = 0;
     uint32_t seg = 0, o_phase = 0;
     int tile_no = 0;  // of the CTA's K/V tiles, for the scales' ring
-    for (; ok && cur.next(p, sg); ++seg) {
+    for (; ok && sg.next(p); ++seg) {
       if (t >= sg.rows_of_q()) {
-        tile_no += sg.tiles();
+        tile_no += sg.j1 - sg.j0;
         continue;
       }
       const int token = sg.m * kPfTokens + t * 32 + r / 4;
       const bool live = token < sg.row.n;
-      const size_t row_at = ((size_t)(sg.row.at + token) * kHq + 4 * sg.g + (r & 3)) * kD;
       float scale = p.scale_log2;
       {
+        // the warp's 32 rows, two at a time: 16 lanes hold a row's 256 bytes
+        const int piece = lane & 15;
         uint4 x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          x[i] = live ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row_at) + i)
-                      : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 16; ++i) {
+          const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (tok < sg.row.n)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + piece);
+        }
         if constexpr (kNarrow && QF == kQBF16) {
-          // by a power of two into fp16's range: the largest |q| into [2^14, 2^15)
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
-          }
-          // (its exponent -100 at least, so that the scale's stays a normal number)
-          const int e = min(max((int)(top >> 7) - 127, -100), 127);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23), down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
-          scale *= down;
+          // by a power of two into fp16's range: a row's largest |q| into [2^14, 2^15)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // (its exponent -100 at least, so that the scale's stays a normal number)
+            const int e = min(max((int)(top >> 7) - 127, -100), 127);
+            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+            const int mine = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);  // (row 2 i + (lane & 1)'s)
+            if (lane >> 1 == i) scale *= __uint_as_float((uint32_t)(127 - 14 + mine) << 23);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float2 f = bf16x2_to_f32x2(w[k]);
@@ -454,14 +504,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) *reinterpret_cast<uint4*>(sm.q[t] + pf_piece(r, i)) = x[i];
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<uint4*>(sm.q[t] + pf_piece((warp & 3) * 32 + 2 * i + (lane >> 4), piece)) = x[i];
       }
       proxy_fence();
       mbar_arrive(&sm.q_full[t]);
       // slots that the row sees: up to `seen` (none: a row without a token, or without a slot)
       const int seen = live ? sg.row.base + token : -1;
       float m = -INFINITY, l = 0.f;
-      for (int j = sg.j0; ok && j < sg.j1; ++j, ++tile_no) {
+      const int j0 = sg.j0, j1 = sg.j1;
+      for (int j = j0; ok && j < j1; ++j, ++tile_no) {
         if (!wait(&sm.s_full[t], s_phase)) break;
         s_phase ^= 1;
         tc_fence_after();
@@ -472,9 +524,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         float* s = reinterpret_cast<float*>(x);
         const uint16_t(*scales)[kPfTile] = sm.scales[tile_no % 3];
         if constexpr (kI8) {
-          // (the scales of V are there with V, which is the ring's next item)
-          const uint32_t v_item = 2 * (uint32_t)tile_no + 1;
-          if (!wait(&sm.kv_full[v_item % kPfSlots], v_item / kPfSlots & 1)) break;
+          // (the scales of V are there with V)
+          if (!wait(&sm.v_full[tile_no & 3], tile_no >> 2 & 1)) break;
 #pragma unroll
           for (int k = 0; k < 128; k += 2) {
             const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[0] + k));
@@ -490,27 +541,26 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 128; k += 4) {
-          if constexpr (kI8) {
-            // int8: of the weight times its V scale, which is what P holds
-            const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[2] + k));
-            const float2 g = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[2] + k + 2));
-            top4[0] = fmaxf(top4[0], fmaf(s[k], scale, f.x));
-            top4[1] = fmaxf(top4[1], fmaf(s[k + 1], scale, f.y));
-            top4[2] = fmaxf(top4[2], fmaf(s[k + 2], scale, g.x));
-            top4[3] = fmaxf(top4[3], fmaf(s[k + 3], scale, g.y));
-          } else {
+        for (int k = 0; k < 128; k += 8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top4[i] = fmaxf(top4[i], s[k + i]);
-          }
+          for (int i = 0; i < 4; ++i) top4[i] = fmaxf(top4[i], fmaxf(s[k + i], s[k + i + 4]));
         }
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * (kI8 ? 1.f : scale);
+        float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * scale;
+        if constexpr (kI8) {
+          // int8: P holds weights times V scales, so the largest of these counts too, by
+          // its exponent (-60 at least: the weights' sum stays in range)
+          uint32_t big = 0;
+#pragma unroll
+          for (int k = 0; k < 128; k += 2) big = __vmaxu2(big, *reinterpret_cast<const uint32_t*>(scales[1] + k) & 0x7fff7fffu);
+          const int lg = (int)(max(big & 0xffffu, big >> 16) >> 7) - 126;
+          top += (float)max(lg, -60);
+        }
         if (__any_sync(0xffffffffu, top > m + kPfGrow)) {
           const float grown = fmaxf(m, top);
           const float f = m == grown ? 1.f : ex2(m - grown);  // (0 from -inf)
           m = grown;
           l *= f;
-          if (j > sg.j0) {
+          if (j > j0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t o[32];
@@ -523,33 +573,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
         const float minus = kPfLift - (m == -INFINITY ? 0.f : m);
-        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 scale2 = make_float2(scale, scale), minus2 = make_float2(minus, minus);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
         for (int k = 0; k < 128; k += 4) {
-          float w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            w[i] = ex2(fmaf(s[k + i], scale, minus));
-            sum4[i] += w[i];
-          }
+          float2 a = fma2(make_float2(s[k], s[k + 1]), scale2, minus2), b = fma2(make_float2(s[k + 2], s[k + 3]), scale2, minus2);
+          a = make_float2(ex2(a.x), ex2(a.y));
+          b = make_float2(ex2(b.x), ex2(b.y));
+          sum0 = add2(sum0, a);
+          sum1 = add2(sum1, b);
           if constexpr (kI8) {
             const float2 f = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[1] + k));
             const float2 g = bf16x2_to_f32x2(*reinterpret_cast<const uint32_t*>(scales[1] + k + 2));
             // (a hidden slot's weight stays zero whatever its scale is)
-            w[0] = masked && k >= visible ? 0.f : w[0] * f.x;
-            w[1] = masked && k + 1 >= visible ? 0.f : w[1] * f.y;
-            w[2] = masked && k + 2 >= visible ? 0.f : w[2] * g.x;
-            w[3] = masked && k + 3 >= visible ? 0.f : w[3] * g.y;
+            a.x = masked && k >= visible ? 0.f : a.x * f.x;
+            a.y = masked && k + 1 >= visible ? 0.f : a.y * f.y;
+            b.x = masked && k + 2 >= visible ? 0.f : b.x * g.x;
+            b.y = masked && k + 3 >= visible ? 0.f : b.y * g.y;
           }
-          x[k / 2] = round2<MF>(w[0], w[1]);
-          x[k / 2 + 1] = round2<MF>(w[2], w[3]);
+          x[k / 2] = round2<MF>(a.x, a.y);
+          x[k / 2 + 1] = round2<MF>(b.x, b.y);
+          if (k == 60) {  // the first half of P: its product starts
+            tc_st32(s_at, x);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sm.p_full[t][0]);
+          }
         }
-        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
-        tc_st32(s_at, x);
+        sum0 = add2(sum0, sum1);
+        l += sum0.x + sum0.y;
         tc_st32(s_at + 32, x + 32);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&sm.p_full[t]);
+        mbar_arrive(&sm.p_full[t][1]);
       }
       if (!wait(&sm.o_full[t], o_phase)) break;
       o_phase ^= 1;
@@ -579,16 +635,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           }
         }
         if (whole) {
-          if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row_at) + 4 * k;
+          // through the tile's place in shared memory (its products with K are done)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = round2<QF>(__uint_as_float(o[8 * i + 2 * e]) * f, __uint_as_float(o[8 * i + 2 * e + 1]) * f);
-              dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int e = 0; e < 4; ++e)
+              w[e] = round2<QF>(__uint_as_float(o[8 * i + 2 * e]) * f, __uint_as_float(o[8 * i + 2 * e + 1]) * f);
+            *reinterpret_cast<uint4*>(sm.q[t] + pf_piece(r, 4 * k + i)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
           float* dst = p.part_o + ((size_t)slot * kD + 32 * k) * (2 * kPfRows) + t * kPfRows + r;
@@ -596,210 +650,247 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int i = 0; i < 32; ++i) dst[i * (2 * kPfRows)] = __uint_as_float(o[i]);
         }
       }
+      if (whole) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
+          if (tok < sg.row.n)
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                       ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + (lane & 15)) =
+                *reinterpret_cast<const uint4*>(sm.q[t] + pf_piece(row, lane & 15));
+        }
+        __syncwarp();
+      }
       if (!whole) p.part_ml[(size_t)slot * (2 * kPfRows) + t * kPfRows + r] = make_float2(m, l);
     }
   } else if (warp == 8) {
     // ----------------------------------------------------------- products
-    if (lane == 0) {
+    {
       constexpr uint32_t kQk = tc_idesc(MF == kQBF16, false), kPv = tc_idesc(MF == kQBF16, true);
-      const uint32_t q0 = smem_addr(sm.q[0]), kv0 = smem_addr(sm.kv[0]);
+      const uint64_t q0 = tc_desc(smem_addr(sm.q[0]), 16), k0 = tc_desc(smem_addr(sm.kv[0]), 16),
+                     v0 = tc_desc(smem_addr(sm.kv[0]), kPfTileBytes / 2);
+      // (a descriptor's address counts 16 bytes in its lowest 14 bits; all of shared memory fits)
       const auto qk = [&](int t, int slot) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * (kPfTileBytes / 2) + (k & 3) * 32;
-          tc_mma_ss(tmem + t * 128, tc_desc(q0 + t * kPfTileBytes + off, 16), tc_desc(kv0 + slot * kPfTileBytes + off, 16), kQk,
-                    k > 0);
+          const uint32_t off = ((k >> 2) * (kPfTileBytes / 2) + (k & 3) * 32) >> 4;
+          tc_mma_ss(tmem + t * 128, q0 + (uint32_t)(t * (kPfTileBytes >> 4)) + off,
+                    k0 + (uint32_t)(slot * (kPfTileBytes >> 4)) + off, kQk, k > 0);
         }
       };
-      const auto pv = [&](int t, int slot, bool add) {
+      const auto pv = [&](int t, int slot, int half, bool add) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, tc_desc(kv0 + slot * kPfTileBytes + k * 2048, kPfTileBytes / 2),
-                    kPv, add || k > 0);
+        for (int i = 0; i < 4; ++i) {
+          const int k = 4 * half + i;
+          tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, v0 + (uint32_t)(slot * (kPfTileBytes >> 4) + k * 128), kPv,
+                    add || k > 0);
+        }
       };
-      uint32_t item = 0, v_no = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      while (ok && cur.next(p, sg)) {
-        const int nq = sg.rows_of_q(), n = sg.tiles();
+      int k_no = 0, v_no = 0;  // tiles whose K, V came to be used
+      uint32_t q_phase = 0, p_phase = 0;
+      while (ok && sg.next(p)) {
+        const int nq = sg.rows_of_q(), n = sg.j1 - sg.j0;
         for (int j = -1; ok && j < n; ++j) {
-          const uint32_t v_item = item - 1;  // (of tile j; K of tile j + 1 is item)
-          const int k_slot = (int)(item % kPfSlots);
-          const uint32_t k_parity = item / kPfSlots & 1;
+          const int k_slot = 2 * k_no % kPfSlots, v_slot = (2 * v_no + 1) % kPfSlots;
           if (j >= 0) {
-            const int v_slot = (int)(v_item % kPfSlots);
-            const bool there = kNarrow ? wait_one(&sm.kv_full[v_slot], v_item / kPfSlots & 1)
-                                       : wait_one(&sm.v_fixed[v_no & 3], v_no >> 2 & 1);
-            if (!there) break;
-            ++v_no;
+            uint64_t* there = kNarrow ? &sm.v_full[v_no & 3] : &sm.v_fixed[v_no & 3];
+            if (!wait(there, v_no >> 2 & 1)) break;
           }
           for (int t = 0; t < nq; ++t) {
             if (j >= 0) {
-              if (!wait_one(&sm.p_full[t], p_phase[t])) break;
-              p_phase[t] ^= 1;
+              if (!wait(&sm.p_full[t][0], p_phase >> t & 1)) break;
               tc_fence_after();
-              pv(t, (int)(v_item % kPfSlots), j > 0);
+              pv(t, v_slot, 0, j > 0);
+              if (!wait(&sm.p_full[t][1], p_phase >> t & 1)) break;
+              p_phase ^= 1u << t;
+              tc_fence_after();
+              pv(t, v_slot, 1, true);
               if (j == n - 1) tc_commit(&sm.o_full[t]);
-              if (t == nq - 1) tc_commit(&sm.kv_empty[v_item % kPfSlots]);
+              if (t == nq - 1) tc_commit(&sm.kv_empty[v_slot]);
             } else {
-              if (!wait_one(&sm.q_full[t], q_phase[t])) break;
-              q_phase[t] ^= 1;
+              if (!wait(&sm.q_full[t], q_phase >> t & 1)) break;
+              q_phase ^= 1u << t;
               tc_fence_after();
             }
             if (j + 1 < n) {
-              if (t == 0 && !wait_one(&sm.kv_full[k_slot], k_parity)) break;
+              if (t == 0 && !wait(&sm.k_full[k_no & 3], k_no >> 2 & 1)) break;
               qk(t, k_slot);
               tc_commit(&sm.s_full[t]);
               if (t == nq - 1) tc_commit(&sm.kv_empty[k_slot]);
             }
           }
-          if (j + 1 < n) item += 2;
+          if (j >= 0) ++v_no;
+          if (j + 1 < n) ++k_no;
         }
       }
       if (!ok) {  // products in flight end before the block's memory is given up
         tc_commit(&sm.done);
-        mbar_wait(&sm.done, 0, global_timer_ns() + 1000000000ull);
+        pf_wait(&sm.done, 0);
+        __syncwarp();
       }
     }
   } else {
     // -------------------------------------------------------- K and V tiles
-    uint32_t item = 0;
-    uint32_t seg = 0, v_no = 0;
-    int tile_no = 0;
-    for (; ok && cur.next(p, sg); ++seg) {
-      const int len = sg.row.len;
-      for (int j = sg.j0; ok && j < sg.j1; ++j, ++tile_no) {
-        const int t0 = j * kPfTile;
-        const bool hidden = t0 + kPfTile - 1 > sg.first_seen();  // slots that some query does not see
-        for (int plane = 0; ok && plane < 2; ++plane, ++item) {
-          const int slot = (int)(item % kPfSlots);
-          const uint32_t round = item / kPfSlots;
-          const int pg = plane * kHkv + sg.g;
-          uint8_t* dst = sm.kv[slot];
-          if constexpr (kNarrow) {
-            if (!wait(&sm.kv_empty[slot], (round & 1) ^ 1)) break;
-            const int worker = tid - 288;  // 96 of them
+    if constexpr (kNarrow) {
+      // Three warps widen; a thread has pieces of 16 elements, 96 apart, eight to a row.
+      // The next tile's bytes are loaded into registers before this one's are widened.
+      constexpr int kPieces = (kPfTile * 8 + 95) / 96;
+      const int worker = tid - 288;
+      uint4 x[kPieces];
+      uint32_t sc[kPieces];
+      PfCursor& as = sm.cursor[warp + 3];
+      int aj = 0, ajend = 0, aplane = 1;  // the item to load: its tile and plane
+      const auto fetch = [&]() {
+        if (aplane == 0) {
+          aplane = 1;
+        } else {
+          aplane = 0;
+          if (++aj >= ajend) {
+            if (!as.next(p)) return;
+            aj = as.j0;
+            ajend = as.j1;
+          }
+        }
+        const int t0 = aj * kPfTile, pg = aplane * kHkv + as.g;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const int i = worker + 96 * k, row = i >> 3, piece = i & 7;
+          x[k] = make_uint4(0, 0, 0, 0);
+          sc[k] = 0;
+          if (i < kPfTile * 8 && t0 + row < as.row.len) {
+            const size_t at = cache_row(p.c, as.b, pg, t0 + row);
+            if constexpr (KVF == kKvE2M1) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.c.kv) + at * 8 + piece);
+              x[k].x = v.x;
+              x[k].y = v.y;
+              sc[k] = __ldg(static_cast<const uint8_t*>(p.c.scales) + at * 8 + piece);
+            } else {
+              x[k] = __ldg(reinterpret_cast<const uint4*>(p.c.kv) + at * 8 + piece);
+              if constexpr (kI8)
+                if (piece == 0) sc[k] = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
+            }
+          }
+        }
+      };
+      uint32_t item = 0, seg = 0;
+      int tile_no = 0;
+      fetch();
+      for (; ok && sg.next(p); ++seg) {
+        const int first_seen = sg.first_seen(), j1 = sg.j1;
+        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+          const int t0 = j * kPfTile;
+          const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
+          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+            const int slot = (int)(item % kPfSlots);
+            uint8_t* dst = sm.kv[slot];
+            if (!wait(&sm.kv_empty[slot], (item / kPfSlots & 1) ^ 1)) break;
             bool odd = false;
-            // pieces of 16 elements, eight to a row
-            constexpr int kBatch = 4;
-            for (int i0 = worker; i0 < kPfTile * 8; i0 += 96 * kBatch) {
-              uint4 x[kBatch];
-              uint32_t sc[kBatch];
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + 96 * k, row = i >> 3, piece = i & 7;
-                x[k] = make_uint4(0, 0, 0, 0);
-                sc[k] = 0;
-                if (i < kPfTile * 8 && t0 + row < len) {
-                  const size_t at = cache_row(p.c, sg.b, pg, t0 + row);
-                  if constexpr (KVF == kKvE2M1) {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.c.kv) + at * 8 + piece);
-                    x[k].x = v.x;
-                    x[k].y = v.y;
-                    sc[k] = __ldg(static_cast<const uint8_t*>(p.c.scales) + at * 8 + piece);
-                  } else {
-                    x[k] = __ldg(reinterpret_cast<const uint4*>(p.c.kv) + at * 8 + piece);
-                    if constexpr (kI8)
-                      if (piece == 0) sc[k] = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
-                  }
-                }
-              }
+            for (int k = 0; k < kPieces; ++k) {
+              const int i = worker + 96 * k, row = i >> 3, piece = i & 7;
+              if (i >= kPfTile * 8) continue;
+              const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              uint32_t d[8];
+              widen16<KVF, kQF16>(w, sc[k], d);
+              if constexpr (!kI8) {
+                if (plane == 1 && hidden && t0 + row > first_seen) {
 #pragma unroll
-              for (int k = 0; k < kBatch; ++k) {
-                const int i = i0 + 96 * k, row = i >> 3, piece = i & 7;
-                if (i >= kPfTile * 8) continue;
-                const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                uint32_t d[8];
-                widen16<KVF, kQF16>(w, sc[k], d);
-                if constexpr (!kI8) {
-                  if (plane == 1 && hidden && t0 + row > sg.first_seen()) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                      if (!pair_finite<kQF16>(d[e])) {
-                        odd = true;
-                        if (!pair_finite<kQF16>(d[e] & 0xffffu)) d[e] &= 0xffff0000u;
-                        if (!pair_finite<kQF16>(d[e] & 0xffff0000u)) d[e] &= 0xffffu;
-                      }
+                  for (int e = 0; e < 8; ++e) {
+                    if (!pair_finite<kQF16>(d[e])) {
+                      odd = true;
+                      if (!pair_finite<kQF16>(d[e] & 0xffffu)) d[e] &= 0xffff0000u;
+                      if (!pair_finite<kQF16>(d[e] & 0xffff0000u)) d[e] &= 0xffffu;
                     }
                   }
                 }
-                st_shared16(dst + pf_piece(row, 2 * piece), d[0], d[1], d[2], d[3]);
-                st_shared16(dst + pf_piece(row, 2 * piece + 1), d[4], d[5], d[6], d[7]);
-                if constexpr (kI8)
-                  if (piece == 0) {
-                    uint16_t(*scales)[kPfTile] = sm.scales[tile_no % 3];
-                    scales[plane][row] = (uint16_t)sc[k];
-                    // |scale| <= 2^lg (-60 at least, so that the weights' sum stays in range)
-                    const int lg = max((int)(sc[k] >> 7 & 0xff) - 126, -60);
-                    if (plane == 1) scales[2][row] = (uint16_t)(__float_as_uint((float)lg) >> 16);
-                  }
               }
+              st_shared16(dst + pf_piece(row, 2 * piece), d[0], d[1], d[2], d[3]);
+              st_shared16(dst + pf_piece(row, 2 * piece + 1), d[4], d[5], d[6], d[7]);
+              if constexpr (kI8)
+                if (piece == 0) sm.scales[tile_no % 3][plane][row] = (uint16_t)sc[k];
             }
             if (odd) sm.odd[seg & 7] = (int)seg + 1;
             proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.kv_full[slot]);
-          } else if (warp == 9) {
-            if (!wait(&sm.kv_empty[slot], (round & 1) ^ 1)) break;
-            // boxes of `box` rows: one, or a page's each; pages past the length are left out
-            const int boxes = kPfTile / p.box;
-            int row = -1;
-            if (p.c.block_table == nullptr) {
-              if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
-            } else if (lane < boxes && t0 + lane * p.box < len) {
-              row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
-            }
-            const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
-            if (lane == 0) {
-              if (some) mbar_arrive_expect_tx(&sm.kv_full[slot], (uint32_t)(__popc(some) * p.box * kD * 2));
-              else mbar_arrive(&sm.kv_full[slot]);
-            }
-            __syncwarp();
-            if (row >= 0) {
-              const uint32_t at = smem_addr(dst) + lane * p.box * 128;
-              tma_box(at, &map, 0, row, &sm.kv_full[slot]);
-              tma_box(at + kPfTileBytes / 2, &map, 64, row, &sm.kv_full[slot]);
-            }
-          } else if (plane == 1) {
-            // the V tiles that hold hidden slots
-            if (!wait(&sm.kv_full[slot], round & 1)) break;
-            if (hidden) {
-              bool odd = false;
-              for (int i = tid - 320; i < kPfTile * 16; i += 64) {
-                const int row = i >> 4, u = t0 + row;
-                if (u <= sg.first_seen()) continue;
-                uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
-                if (u >= len) {
-                  *at = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
-                uint4 v = *at;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool bad = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
-                  if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
-                }
-                if (bad) {
-                  odd = true;
-                  *at = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              }
-              if (odd) sm.odd[seg & 7] = (int)seg + 1;
-              proxy_fence();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_fixed[v_no & 3]);
-            ++v_no;
+            if (lane == 0) mbar_arrive(plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3]);
+            fetch();
           }
         }
       }
-    }
-    // copies in flight land before the block's shared memory is given up
-    if (!kNarrow && warp == 9 && !ok) {
-      ok = true;
-      for (uint32_t k = item > kPfSlots ? item - kPfSlots : 0; k < item; ++k)
-        mbar_wait(&sm.kv_full[k % kPfSlots], k / kPfSlots & 1, global_timer_ns() + 1000000ull);
-      ok = false;
+    } else {
+      uint32_t item = 0, seg = 0;
+      int tile_no = 0;
+      for (; ok && sg.next(p); ++seg) {
+        const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
+        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+          const int t0 = j * kPfTile;
+          const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
+          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+            const int slot = (int)(item % kPfSlots);
+            uint64_t* full = plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3];
+            const int pg = plane * kHkv + sg.g;
+            uint8_t* dst = sm.kv[slot];
+            if (warp == 9) {
+              if (!wait(&sm.kv_empty[slot], (item / kPfSlots & 1) ^ 1)) break;
+              // boxes of `box` rows: one, or a page's each; pages past the length are left out
+              const int boxes = kPfTile / p.box;
+              int row = -1;
+              if (p.c.block_table == nullptr) {
+                if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
+              } else if (lane < boxes && t0 + lane * p.box < len) {
+                row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
+              }
+              const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
+              if (lane == 0) {
+                if (some) mbar_arrive_expect_tx(full, (uint32_t)(__popc(some) * p.box * kD * 2));
+                else mbar_arrive(full);
+              }
+              __syncwarp();
+              if (row >= 0) {
+                const uint32_t at = smem_addr(dst) + lane * p.box * 128;
+                tma_box(at, &map, 0, row, full);
+                tma_box(at + kPfTileBytes / 2, &map, 64, row, full);
+              }
+            } else if (plane == 1) {
+              // the V tiles that hold hidden slots
+              if (!wait(full, tile_no >> 2 & 1)) break;
+              if (hidden) {
+                bool odd = false;
+                for (int i = tid - 320; i < kPfTile * 16; i += 64) {
+                  const int row = i >> 4, u = t0 + row;
+                  if (u <= first_seen) continue;
+                  uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
+                  if (u >= len) {
+                    *at = make_uint4(0, 0, 0, 0);
+                    continue;
+                  }
+                  uint4 v = *at;
+                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                  bool bad = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
+                    if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
+                  }
+                  if (bad) {
+                    odd = true;
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                  }
+                }
+                if (odd) sm.odd[seg & 7] = (int)seg + 1;
+                proxy_fence();
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.v_fixed[tile_no & 3]);
+            }
+          }
+        }
+      }
+      // copies in flight land before the block's shared memory is given up
+      if (warp == 9 && !ok)
+        for (uint32_t k = item > kPfSlots ? item - kPfSlots : 0; k < item; ++k)
+          pf_wait(k & 1 ? &sm.v_full[k / 2 & 3] : &sm.k_full[k / 2 & 3], k / 8 & 1);
     }
   }
   if (!ok && lane == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_WAIT_TIMEOUT);
@@ -820,7 +911,7 @@ constexpr int kMergeThreads = 128;
 template <int QF>
 __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
   __shared__ long long s_sum[kMergeThreads / 32];
-  __shared__ PfSegment s_unit;
+  __shared__ PfCursor s_unit;
   __shared__ int s_pieces;  // 0: nothing to do
   __shared__ long long s_begin;
   pdl_launch_dependents();
@@ -834,7 +925,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
     long long rem;
     const int b = pf_find_row(p, at, rem);
     if (lane == 0) {
-      PfSegment u;
+      PfCursor u;
       u.b = b;
       u.row = pf_row(p, b);
       int j;
@@ -849,7 +940,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
   }
   __syncthreads();
   if (s_pieces == 0) return;
-  const PfSegment u = s_unit;
+  const PfCursor& u = s_unit;
   const int row = 32 * (int)blockIdx.y + lane, token = u.m * kPfTokens + row / 4;
   if (u.m * kPfTokens + 8 * (int)blockIdx.y >= u.row.n) return;
   const bool live = token < u.row.n;
