@@ -18,8 +18,8 @@
 // the V tiles that hold slots which some query of the unit does not see: a zero weight
 // times an infinity or NaN there would be NaN, so rows past the length become zeros and
 // other values that are not finite zeros too, to be put into the rows that do see
-// them in the epilogue (rarely: then straight from the cache).  Narrow caches are
-// widened to fp16 (exact) by three warps; a bf16 q is then scaled by a power of two a
+// them in the epilogue (rarely: then straight from the cache).  Narrow caches come by
+// TMA as they are and those two warps widen them to fp16 (exact); a bf16 q is then scaled by a power of two a
 // row into fp16's range, so these calls have fp16 products whatever q's type is.
 // int8 scales multiply the columns of S and of P.
 //
@@ -54,7 +54,7 @@ struct PrefillParams {
   float* part_o;                // [2 * ctas][128 dims][256 rows]
   float2* part_ml;              // [2 * ctas][256 rows]: maximum, sum
   int tokens, ctas;
-  int box;                      // rows of a TMA box (16-bit caches)
+  int box;                      // rows loaded together: a tile's, or a page's if it is smaller
   float scale_log2, v_scale;
 };
 
@@ -277,17 +277,17 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 struct PfShared {
   uint8_t q[2][kPfTileBytes];         // [tile][64-dim half][row][128 bytes]
   uint8_t kv[kPfSlots][kPfTileBytes];  // [64-dim half][slot][128 bytes]
-  // int8: a tile's K and V row scales (bf16 bits).  Three tiles' are enough: a slot of K
-  // or V of tile j is free once the softmax of tile j - 3 is done, five slots being two
-  // and a half tiles.
-  uint16_t scales[3][2][kPfTile];
+  // int8: a tile's K and V row scales (bf16 bits).  Four tiles' are enough: they are
+  // loaded once item i - 2 (two to a tile) has been widened, which had to wait until
+  // item i - 6 was used, and so for the softmax of four tiles before.
+  uint16_t scales[4][2][kPfTile];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;  // (P in halves of 64 slots)
   // Of a tile: K there, V there, V looked through (tile & 3 each; at most three tiles
   // are between a load and its product).  A barrier is waited on in every one of its
   // phases by whoever waits on it: a parity says nothing about a phase further on.
   uint64_t k_full[4], v_full[4], v_fixed[4];
-  uint64_t kv_empty[kPfSlots];
-  PfCursor cursor[kPfThreads / 32 + 3];  // (three of the loads ahead of a narrow cache)
+  uint64_t kv_empty[kPfSlots], raw_full[3], raw_empty[3];
+  PfCursor cursor[kPfThreads / 32];
   uint32_t tmem;
   int odd[8];  // a segment's number + 1 where a value was taken out of V
 };
@@ -382,6 +382,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap map) {
   constexpr bool kNarrow = is_narrow(KVF), kI8 = KVF == kKvI8;
   constexpr int MF = kNarrow ? (int)kQF16 : QF;  // type of the products' operands
+  // Slots of K and V tiles.  A narrow cache gives the fifth to tiles as they lie in
+  // memory, with an e2m1 cache's scales behind the codes.
+  constexpr int kSlots = kNarrow ? kPfSlots - 1 : kPfSlots;
+  constexpr int kRawBytes = kPfTile * (kv_row_bytes(KVF) + (KVF == kKvE2M1 ? 8 : 0));
+  constexpr int kRaws = kNarrow ? kPfTileBytes / kRawBytes : 1;
+  static_assert(kRaws <= 3, "barriers of raw tiles");
   extern __shared__ __align__(1024) uint8_t s_raw[];
   PfShared& sm = *reinterpret_cast<PfShared*>(s_raw);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -400,9 +406,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     for (int i = 0; i < kPfSlots; ++i) mbar_init(&sm.kv_empty[i], 1);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.k_full[i], kNarrow ? 3 : 1);
-      mbar_init(&sm.v_full[i], kNarrow ? 3 : 1);
+      mbar_init(&sm.k_full[i], kNarrow ? 2 : 1);
+      mbar_init(&sm.v_full[i], kNarrow ? 2 : 1);
       mbar_init(&sm.v_fixed[i], 2);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sm.raw_full[i], scale_row_bytes(KVF) > 0 ? 2 : 1);
+      mbar_init(&sm.raw_empty[i], 2);
     }
     mbar_init(&sm.done, 1);
     for (int i = 0; i < 8; ++i) sm.odd[i] = 0;
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (warp == 0) {
     long long rem;
     const int b = pf_find_row(p, begin, rem);
-    if (lane < kPfThreads / 32 + 3) {
+    if (lane < kPfThreads / 32) {
       PfCursor& c = sm.cursor[lane];
       c.b = b;
       c.row = pf_row(p, b);
@@ -522,7 +532,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int k = 0; k < 4; ++k) tc_ld32(x + 32 * k, s_at + 32 * k);
         tc_wait_ld();
         float* s = reinterpret_cast<float*>(x);
-        const uint16_t(*scales)[kPfTile] = sm.scales[tile_no % 3];
+        const uint16_t(*scales)[kPfTile] = sm.scales[tile_no & 3];
         if constexpr (kI8) {
           // (the scales of V are there with V)
           if (!wait(&sm.v_full[tile_no & 3], tile_no >> 2 & 1)) break;
@@ -692,7 +702,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       while (ok && sg.next(p)) {
         const int nq = sg.rows_of_q(), n = sg.j1 - sg.j0;
         for (int j = -1; ok && j < n; ++j) {
-          const int k_slot = 2 * k_no % kPfSlots, v_slot = (2 * v_no + 1) % kPfSlots;
+          const int k_slot = 2 * k_no % kSlots, v_slot = (2 * v_no + 1) % kSlots;
           if (j >= 0) {
             uint64_t* there = kNarrow ? &sm.v_full[v_no & 3] : &sm.v_fixed[v_no & 3];
             if (!wait(there, v_no >> 2 & 1)) break;
@@ -732,165 +742,166 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
   } else {
     // -------------------------------------------------------- K and V tiles
-    if constexpr (kNarrow) {
-      // Three warps widen; a thread has pieces of 16 elements, 96 apart, eight to a row.
-      // The next tile's bytes are loaded into registers before this one's are widened.
-      constexpr int kPieces = (kPfTile * 8 + 95) / 96;
-      const int worker = tid - 288;
-      uint4 x[kPieces];
-      uint32_t sc[kPieces];
-      PfCursor& as = sm.cursor[warp + 3];
-      int aj = 0, ajend = 0, aplane = 1;  // the item to load: its tile and plane
-      const auto fetch = [&]() {
-        if (aplane == 0) {
-          aplane = 1;
-        } else {
-          aplane = 0;
-          if (++aj >= ajend) {
-            if (!as.next(p)) return;
-            aj = as.j0;
-            ajend = as.j1;
-          }
-        }
-        const int t0 = aj * kPfTile, pg = aplane * kHkv + as.g;
-#pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-          const int i = worker + 96 * k, row = i >> 3, piece = i & 7;
-          x[k] = make_uint4(0, 0, 0, 0);
-          sc[k] = 0;
-          if (i < kPfTile * 8 && t0 + row < as.row.len) {
-            const size_t at = cache_row(p.c, as.b, pg, t0 + row);
-            if constexpr (KVF == kKvE2M1) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.c.kv) + at * 8 + piece);
-              x[k].x = v.x;
-              x[k].y = v.y;
-              sc[k] = __ldg(static_cast<const uint8_t*>(p.c.scales) + at * 8 + piece);
-            } else {
-              x[k] = __ldg(reinterpret_cast<const uint4*>(p.c.kv) + at * 8 + piece);
-              if constexpr (kI8)
-                if (piece == 0) sc[k] = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
+    uint32_t item = 0, seg = 0;
+    int tile_no = 0;
+    for (; ok && sg.next(p); ++seg) {
+      const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
+      for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+        const int t0 = j * kPfTile;
+        const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
+        for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+          const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
+          uint64_t* there = plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3];
+          uint8_t *dst = sm.kv[slot], *bytes = sm.kv[kSlots] + raw * kRawBytes;
+          if (warp == 9) {
+            // by TMA, in boxes of `box` rows: one, or a page's each; pages past the length
+            // are left out
+            if (!(kNarrow ? wait(&sm.raw_empty[raw], (item / kRaws & 1) ^ 1) : wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)))
+              break;
+            const int pg = plane * kHkv + sg.g, boxes = kPfTile / p.box;
+            uint64_t* full = kNarrow ? &sm.raw_full[raw] : there;
+            int row = -1;
+            if (p.c.block_table == nullptr) {
+              if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
+            } else if (lane < boxes && t0 + lane * p.box < len) {
+              row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
             }
-          }
-        }
-      };
-      uint32_t item = 0, seg = 0;
-      int tile_no = 0;
-      fetch();
-      for (; ok && sg.next(p); ++seg) {
-        const int first_seen = sg.first_seen(), j1 = sg.j1;
-        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
-          const int t0 = j * kPfTile;
-          const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
-          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
-            const int slot = (int)(item % kPfSlots);
-            uint8_t* dst = sm.kv[slot];
-            if (!wait(&sm.kv_empty[slot], (item / kPfSlots & 1) ^ 1)) break;
-            bool odd = false;
-#pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-              const int i = worker + 96 * k, row = i >> 3, piece = i & 7;
-              if (i >= kPfTile * 8) continue;
-              const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-              uint32_t d[8];
-              widen16<KVF, kQF16>(w, sc[k], d);
-              if constexpr (!kI8) {
-                if (plane == 1 && hidden && t0 + row > first_seen) {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    if (!pair_finite<kQF16>(d[e])) {
-                      odd = true;
-                      if (!pair_finite<kQF16>(d[e] & 0xffffu)) d[e] &= 0xffff0000u;
-                      if (!pair_finite<kQF16>(d[e] & 0xffff0000u)) d[e] &= 0xffffu;
-                    }
-                  }
-                }
-              }
-              st_shared16(dst + pf_piece(row, 2 * piece), d[0], d[1], d[2], d[3]);
-              st_shared16(dst + pf_piece(row, 2 * piece + 1), d[4], d[5], d[6], d[7]);
-              if constexpr (kI8)
-                if (piece == 0) sm.scales[tile_no % 3][plane][row] = (uint16_t)sc[k];
+            const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) {
+              if (some) mbar_arrive_expect_tx(full, (uint32_t)(__popc(some) * p.box * kv_row_bytes(KVF)));
+              else mbar_arrive(full);
             }
-            if (odd) sm.odd[seg & 7] = (int)seg + 1;
-            proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3]);
-            fetch();
-          }
-        }
-      }
-    } else {
-      uint32_t item = 0, seg = 0;
-      int tile_no = 0;
-      for (; ok && sg.next(p); ++seg) {
-        const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
-        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
-          const int t0 = j * kPfTile;
-          const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
-          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
-            const int slot = (int)(item % kPfSlots);
-            uint64_t* full = plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3];
-            const int pg = plane * kHkv + sg.g;
-            uint8_t* dst = sm.kv[slot];
-            if (warp == 9) {
-              if (!wait(&sm.kv_empty[slot], (item / kPfSlots & 1) ^ 1)) break;
-              // boxes of `box` rows: one, or a page's each; pages past the length are left out
-              const int boxes = kPfTile / p.box;
-              int row = -1;
-              if (p.c.block_table == nullptr) {
-                if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
-              } else if (lane < boxes && t0 + lane * p.box < len) {
-                row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
-              }
-              const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
-              if (lane == 0) {
-                if (some) mbar_arrive_expect_tx(full, (uint32_t)(__popc(some) * p.box * kD * 2));
-                else mbar_arrive(full);
-              }
-              __syncwarp();
-              if (row >= 0) {
+            if (row >= 0) {
+              if constexpr (kNarrow) {
+                tma_box(smem_addr(bytes) + lane * p.box * kv_row_bytes(KVF), &map, 0, row, full);
+              } else {
                 const uint32_t at = smem_addr(dst) + lane * p.box * 128;
                 tma_box(at, &map, 0, row, full);
                 tma_box(at + kPfTileBytes / 2, &map, 64, row, full);
               }
-            } else if (plane == 1) {
-              // the V tiles that hold hidden slots
-              if (!wait(full, tile_no >> 2 & 1)) break;
-              if (hidden) {
-                bool odd = false;
-                for (int i = tid - 320; i < kPfTile * 16; i += 64) {
-                  const int row = i >> 4, u = t0 + row;
-                  if (u <= first_seen) continue;
-                  uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
-                  if (u >= len) {
-                    *at = make_uint4(0, 0, 0, 0);
-                    continue;
-                  }
-                  uint4 v = *at;
-                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                  bool bad = false;
+            }
+            if constexpr (scale_row_bytes(KVF) > 0) {
+              // the rows' scales: by plain loads (a row's need no more than their own size's alignment)
+              uint2 v[4];
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
-                    if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
+              for (int k = 0; k < 4; ++k) {
+                const int r = 32 * k + lane, first = __shfl_sync(0xffffffffu, row, r / p.box);
+                v[k] = make_uint2(0, 0);
+                if (first >= 0 && t0 + r < len) {
+                  size_t at = (size_t)first + (r & (p.box - 1));
+                  if constexpr (kChecked) {
+                    if (at >= p.c.rows) {
+                      if (p.c.flags) atomicOr(p.c.flags, GQA_FLAG_BOUNDS);
+                      at = 0;
+                    }
                   }
-                  if (bad) {
-                    odd = true;
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                  }
+                  if constexpr (kI8) v[k].x = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
+                  else v[k] = __ldg(static_cast<const uint2*>(p.c.scales) + at);
                 }
-                if (odd) sm.odd[seg & 7] = (int)seg + 1;
-                proxy_fence();
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = 32 * k + lane;
+                if constexpr (kI8) sm.scales[tile_no & 3][plane][r] = (uint16_t)v[k].x;
+                else reinterpret_cast<uint2*>(bytes + kPfTile * kv_row_bytes(KVF))[r] = v[k];
               }
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.v_fixed[tile_no & 3]);
+              if (lane == 0) mbar_arrive(full);
             }
+          } else if constexpr (kNarrow) {
+            // widened: a warp takes four rows at a time, a lane 16 elements, eight lanes a row
+            if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
+            const int piece = lane & 7;
+            const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && hidden;
+            bool odd = false;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += 4) {
+              uint32_t d[4][8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+                if constexpr (KVF == kKvE2M1) {
+                  const uint2 v = *reinterpret_cast<const uint2*>(bytes + row * 64 + piece * 8);
+                  const uint32_t w[2] = {v.x, v.y};
+                  widen16<KVF, kQF16>(w, bytes[kPfTile * 64 + row * 8 + piece], d[i]);
+                } else {
+                  const uint4 v = *reinterpret_cast<const uint4*>(bytes + row * 128 + piece * 16);
+                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                  widen16<KVF, kQF16>(w, 0, d[i]);
+                }
+              }
+              if (tail || check) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int u = t0 + 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    if (u >= len) d[i][e] = 0;
+                    if (check && u > first_seen && !pair_finite<kQF16>(d[i][e])) {
+                      odd = true;
+                      if (!pair_finite<kQF16>(d[i][e] & 0xffffu)) d[i][e] &= 0xffff0000u;
+                      if (!pair_finite<kQF16>(d[i][e] & 0xffff0000u)) d[i][e] &= 0xffffu;
+                    }
+                  }
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+                st_shared16(dst + pf_piece(row, 2 * piece), d[i][0], d[i][1], d[i][2], d[i][3]);
+                st_shared16(dst + pf_piece(row, 2 * piece + 1), d[i][4], d[i][5], d[i][6], d[i][7]);
+              }
+            }
+            if (odd) sm.odd[seg & 7] = (int)seg + 1;
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sm.raw_empty[raw]);
+              mbar_arrive(there);
+            }
+          } else if (plane == 1) {
+            // the V tiles that hold hidden slots
+            if (!wait(there, tile_no >> 2 & 1)) break;
+            if (hidden) {
+              bool odd = false;
+              for (int i = tid - 320; i < kPfTile * 16; i += 64) {
+                const int row = i >> 4, u = t0 + row;
+                if (u <= first_seen) continue;
+                uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
+                if (u >= len) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                const uint4 v = *at;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
+                  if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
+                }
+                if (bad) {
+                  odd = true;
+                  *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+              if (odd) sm.odd[seg & 7] = (int)seg + 1;
+              proxy_fence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.v_fixed[tile_no & 3]);
           }
         }
       }
-      // copies in flight land before the block's shared memory is given up
-      if (warp == 9 && !ok)
-        for (uint32_t k = item > kPfSlots ? item - kPfSlots : 0; k < item; ++k)
-          pf_wait(k & 1 ? &sm.v_full[k / 2 & 3] : &sm.k_full[k / 2 & 3], k / 8 & 1);
+    }
+    // copies in flight land before the block's shared memory is given up
+    if (warp == 9 && !ok) {
+      const uint32_t depth = kNarrow ? kRaws : kSlots;
+      for (uint32_t k = item > depth ? item - depth : 0; k < item; ++k) {
+        if (kNarrow) pf_wait(&sm.raw_full[k % kRaws], k / kRaws & 1);
+        else pf_wait(k & 1 ? &sm.v_full[k / 2 & 3] : &sm.k_full[k / 2 & 3], k / 8 & 1);
+      }
     }
   }
   if (!ok && lane == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_WAIT_TIMEOUT);

@@ -14,14 +14,24 @@ using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*
                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 Encode g_encode = nullptr;
 
-// A 16-bit cache's rows of 128, in boxes of 64 elements and `box` rows.
-cudaError_t encode_rows(CUtensorMap* map, const CacheView& c, int box, int qf) {
-  const cuuint64_t dims[2] = {kD, c.rows}, strides[1] = {2 * kD};
-  const cuuint32_t tile[2] = {kD / 2, (cuuint32_t)box}, steps[2] = {1, 1};
-  const CUresult r = g_encode(map, qf == kQBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                              const_cast<void*>(c.kv), dims, strides, tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+// A cache's rows in boxes of `box`: of a 16-bit cache 64 elements wide and swizzled, of
+// a narrow one whole rows as they are.
+cudaError_t encode_rows(CUtensorMap* map, const CacheView& c, int kvf, int box) {
+  const cuuint32_t steps[2] = {1, 1};
+  CUresult r;
+  if (is_narrow(kvf)) {
+    const cuuint64_t width = (cuuint64_t)kv_row_bytes(kvf), dims[2] = {width, c.rows}, strides[1] = {width};
+    const cuuint32_t tile[2] = {(cuuint32_t)width, (cuuint32_t)box};
+    r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.kv), dims, strides, tile, steps,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t dims[2] = {kD, c.rows}, strides[1] = {2 * kD};
+    const cuuint32_t tile[2] = {kD / 2, (cuuint32_t)box};
+    r = g_encode(map, kvf == kKvBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                 const_cast<void*>(c.kv), dims, strides, tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -79,11 +89,9 @@ cudaError_t prefill_setup() {
 cudaError_t launch_prefill(const PrefillParams& params, int kvf, int qf, cudaStream_t stream) {
   PrefillParams p = params;
   CUtensorMap map = {};
-  if (!is_narrow(kvf)) {
-    p.box = p.c.block_table && p.c.page_log2 < 7 ? 1 << p.c.page_log2 : kPfTile;
-    const cudaError_t e = encode_rows(&map, p.c, p.box, qf);
-    if (e != cudaSuccess) return e;
-  }
+  p.box = p.c.block_table && p.c.page_log2 < 7 ? 1 << p.c.page_log2 : kPfTile;
+  const cudaError_t e = encode_rows(&map, p.c, kvf, p.box);
+  if (e != cudaSuccess) return e;
   const bool bf = qf == kQBF16;
   switch (kvf) {
     case kKvF16: return launch_t<kKvF16, kQF16>(p, map, stream);
