@@ -41,7 +41,15 @@ constexpr int kPfTile = 128;         // slots of a K or V tile
 constexpr int kPfTileBytes = kPfTile * kD * 2;
 constexpr int kPfSlots = 5;
 constexpr int kPfMaxCtas = 160;
-constexpr int kPfMinRun = 2;         // K/V tiles a CTA takes at least
+#ifndef PF_U
+#define PF_U 2
+#endif
+#ifndef PF_MR
+#define PF_MR 2
+#endif
+constexpr int kPfMinRun = PF_MR;         // K/V tiles a CTA takes at least
+constexpr int kPfUnitCost = PF_U;    // what a unit costs besides its tiles (q, the first product, the output), in tiles
+constexpr int kPfFewTiles = 4;       // tiles a CTA up to which that is not counted (every CTA then has about one piece)
 constexpr float kPfLift = 7.f;       // log2 of the weight of a row's maximum
 constexpr float kPfGrow = 8.f;       // growth of the maximum that a row is rescaled for
 
@@ -69,16 +77,17 @@ struct PfRow {
   __device__ __forceinline__ int tiles(int m) const {
     return (max(base, 0) + min(n, (m + 1) * kPfTokens) + kPfTile - 1) / kPfTile;
   }
-  // Sum of tiles(k) for k < m, m < units() or all of them.  tiles(k) = floor((q + k) / 2)
+  // Positions of the stream before unit m: `cost` and its tiles for each unit k < m, m <=
+  // units().  tiles(k) = floor((q + k) / 2)
   // for full units, q = floor((base + 64 + 127) / 64), and sums of floor(j / 2) are squares.
-  __device__ __forceinline__ long long tiles_before(int m) const {
+  __device__ __forceinline__ long long before(int m, int cost) const {
     const int u = units();
     const long long q = (max(base, 0) + kPfTokens + kPfTile - 1) / kPfTokens;
     const auto f = [](long long x) { return (x - 1) * (x - 1) / 4; };
     const long long full = min(m, u - 1);
-    return m <= 0 ? 0 : f(q + full) - f(q) + (m == u ? tiles(u - 1) : 0);
+    return m <= 0 ? 0 : f(q + full) - f(q) + (m == u ? tiles(u - 1) : 0) + (long long)m * cost;
   }
-  __device__ __forceinline__ long long all_tiles() const { return n > 0 ? kHkv * tiles_before(units()) : 0; }
+  __device__ __forceinline__ long long positions(int cost) const { return n > 0 ? kHkv * before(units(), cost) : 0; }
 };
 
 __device__ __forceinline__ PfRow pf_row(const PrefillParams& p, int b) {
@@ -90,29 +99,30 @@ __device__ __forceinline__ PfRow pf_row(const PrefillParams& p, int b) {
   return r;
 }
 
-// Where a position of the stream lies: position `rem` of row b's.
-__device__ __forceinline__ void pf_locate(const PfRow& r, long long rem, int& g, int& m, int& j) {
+// Where a position of the stream lies, position `rem` of row r's: tile j of unit m, or
+// (j < 0) in the unit's cost, -j positions before its first tile.
+__device__ __forceinline__ void pf_locate(const PfRow& r, long long rem, int cost, int& g, int& m, int& j) {
   const int u = r.units();
-  const long long head = r.tiles_before(u);
+  const long long head = r.before(u, cost);
   g = (int)(rem / head);
   rem -= g * head;
-  int lo = 0, hi = u - 1;  // the last unit whose tiles begin at or before rem
+  int lo = 0, hi = u - 1;  // the last unit that begins at or before rem
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (r.tiles_before(mid) <= rem) lo = mid;
+    if (r.before(mid, cost) <= rem) lo = mid;
     else hi = mid - 1;
   }
   m = lo;
-  j = (int)(rem - r.tiles_before(lo));
+  j = (int)(rem - r.before(lo, cost)) - cost;
 }
 
 // A CTA's run, walked by each warp by itself: the part of a unit that it is at, K/V
 // tiles [j0, j1) of `all`.  Kept in shared memory, one for each warp: a row of S leaves
 // a softmax thread no registers for it, and it is looked at once a unit.
 struct PfCursor {
-  long long left;  // tiles of the run from j0 on
+  long long left;  // positions of the run from tile j0 on
   PfRow row;
-  int b, g, m, j0, j1, all, begun;
+  int b, g, m, j0, j1, all, begun, cost;
   // The next part, by one lane.
   __device__ __forceinline__ void step(const PrefillParams& p) {
     if (begun) {
@@ -129,6 +139,10 @@ struct PfCursor {
           if (b >= p.c.batch) left = 0;
         }
       }
+      left -= cost;
+    } else if (j0 < 0) {
+      left += j0;
+      j0 = 0;
     }
     begun = 1;
     if (left > 0) {
@@ -150,31 +164,47 @@ struct PfCursor {
 };
 
 struct PfPlan {
-  long long total, run;
+  long long total, run;  // positions in all and a CTA's
+  int cost;              // a unit's besides its tiles
 };
 
-// The stream's length and a CTA's run.  Every thread of the block calls it.
+// Every thread of the block calls it.
 __device__ __forceinline__ PfPlan pf_plan(const PrefillParams& p, long long* s_sum) {
-  long long sum = 0;
-  for (int b = threadIdx.x; b < p.c.batch; b += blockDim.x) sum += pf_row(p, b).all_tiles();
+  long long tiles = 0, units = 0;
+  for (int b = threadIdx.x; b < p.c.batch; b += blockDim.x) {
+    const PfRow r = pf_row(p, b);
+    tiles += r.positions(0);
+    units += kHkv * r.units();
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x / 32] = sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    s_sum[threadIdx.x / 32 * 2] = tiles;
+    s_sum[threadIdx.x / 32 * 2 + 1] = units;
+  }
   __syncthreads();
+  tiles = units = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+    tiles += s_sum[2 * w];
+    units += s_sum[2 * w + 1];
+  }
   PfPlan plan;
-  plan.total = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) plan.total += s_sum[w];
+  plan.cost = tiles > (long long)kPfFewTiles * p.ctas ? kPfUnitCost : 0;
+  plan.total = tiles + plan.cost * units;
   plan.run = max((plan.total + p.ctas - 1) / p.ctas, (long long)kPfMinRun);
   __syncthreads();
   return plan;
 }
 
 // The row that holds position `at` < total, and the position within it: warp-wide.
-__device__ __forceinline__ int pf_find_row(const PrefillParams& p, long long at, long long& rem) {
+__device__ __forceinline__ int pf_find_row(const PrefillParams& p, long long at, int cost, long long& rem) {
   const int lane = threadIdx.x & 31;
   long long before = 0;
   for (int b0 = 0; b0 < p.c.batch; b0 += 32) {
-    const long long mine = b0 + lane < p.c.batch ? pf_row(p, b0 + lane).all_tiles() : 0;
+    const long long mine = b0 + lane < p.c.batch ? pf_row(p, b0 + lane).positions(cost) : 0;
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -424,14 +454,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   if (begin >= plan.total) return;  // (all of the block)
   if (warp == 0) {
     long long rem;
-    const int b = pf_find_row(p, begin, rem);
+    const int b = pf_find_row(p, begin, plan.cost, rem);
     if (lane < kPfThreads / 32) {
       PfCursor& c = sm.cursor[lane];
       c.b = b;
       c.row = pf_row(p, b);
       c.left = min(plan.run, plan.total - begin);
       c.begun = 0;
-      pf_locate(c.row, rem, c.g, c.m, c.j0);
+      c.cost = plan.cost;
+      pf_locate(c.row, rem, c.cost, c.g, c.m, c.j0);
     }
   } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
@@ -470,55 +501,60 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     uint32_t s_phase = 0;
     uint32_t seg = 0, o_phase = 0;
     int tile_no = 0;  // of the CTA's K/V tiles, for the scales' ring
-    for (; ok && sg.next(p); ++seg) {
-      if (t >= sg.rows_of_q()) {
-        tile_no += sg.j1 - sg.j0;
-        continue;
+    float scale = 0.f;
+    // the run's next part that has rows for this warpgroup, and its q into shared memory
+    const auto find = [&]() {
+      bool there = sg.next(p);
+      for (; there && t >= sg.rows_of_q(); there = sg.next(p), ++seg) tile_no += sg.j1 - sg.j0;
+      return there;
+    };
+    const auto load_q = [&]() {
+      scale = p.scale_log2;
+      // the warp's 32 rows, two at a time: 16 lanes hold a row's 256 bytes
+      const int piece = lane & 15;
+      uint4 x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (tok < sg.row.n)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                      ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + piece);
       }
-      const int token = sg.m * kPfTokens + t * 32 + r / 4;
-      const bool live = token < sg.row.n;
-      float scale = p.scale_log2;
-      {
-        // the warp's 32 rows, two at a time: 16 lanes hold a row's 256 bytes
-        const int piece = lane & 15;
-        uint4 x[16];
+      if constexpr (kNarrow && QF == kQBF16) {
+        // by a power of two into fp16's range: a row's largest |q| into [2^14, 2^15)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (tok < sg.row.n)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                        ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + piece);
-        }
-        if constexpr (kNarrow && QF == kQBF16) {
-          // by a power of two into fp16's range: a row's largest |q| into [2^14, 2^15)
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t top = 0;
+          for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
+          for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // (its exponent -100 at least, so that the scale's stays a normal number)
+          const int e = min(max((int)(top >> 7) - 127, -100), 127);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          const int mine = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);  // (row 2 i + (lane & 1)'s)
+          if (lane >> 1 == i) scale *= __uint_as_float((uint32_t)(127 - 14 + mine) << 23);
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // (its exponent -100 at least, so that the scale's stays a normal number)
-            const int e = min(max((int)(top >> 7) - 127, -100), 127);
-            const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-            const int mine = __shfl_sync(0xffffffffu, e, (lane & 1) << 4);  // (row 2 i + (lane & 1)'s)
-            if (lane >> 1 == i) scale *= __uint_as_float((uint32_t)(127 - 14 + mine) << 23);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = bf16x2_to_f32x2(w[k]);
-              w[k] = round2<kQF16>(f.x * up, f.y * up);
-            }
-            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = bf16x2_to_f32x2(w[k]);
+            w[k] = round2<kQF16>(f.x * up, f.y * up);
           }
+          x[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<uint4*>(sm.q[t] + pf_piece((warp & 3) * 32 + 2 * i + (lane >> 4), piece)) = x[i];
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<uint4*>(sm.q[t] + pf_piece((warp & 3) * 32 + 2 * i + (lane >> 4), piece)) = x[i];
       proxy_fence();
       mbar_arrive(&sm.q_full[t]);
+    };
+    bool more = find();
+    if (more) load_q();
+    while (ok && more) {
+      const int token = sg.m * kPfTokens + t * 32 + r / 4;
+      const bool live = token < sg.row.n;
       // slots that the row sees: up to `seen` (none: a row without a token, or without a slot)
       const int seen = live ? sg.row.base + token : -1;
       float m = -INFINITY, l = 0.f;
@@ -617,12 +653,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc_fence_before();
         mbar_arrive(&sm.p_full[t][1]);
       }
+      if (!ok) break;
+      // Q is free once its last product is there, so the next part's goes there now, and
+      // its first S is formed while this part's output is written
+      const bool whole = sg.whole();
+      const int g = sg.g, b = sg.b, hidden = max(sg.first_seen() + 1, j0 * kPfTile), part = (int)seg;
+      const int tokens = sg.row.n - sg.m * kPfTokens - t * 32;  // of the tile
+      const size_t out_at = ((size_t)(sg.row.at + sg.m * kPfTokens + t * 32) * kHq + 4 * g) * kD;
+      ++seg;
+      more = find();
+      if (more) load_q();
       if (!wait(&sm.o_full[t], o_phase)) break;
       o_phase ^= 1;
       tc_fence_after();
-      const bool odd = sm.odd[seg & 7] == (int)seg + 1;
-      const bool whole = sg.whole();
-      const int slot = 2 * (int)blockIdx.x + (sg.j0 > 0 ? 0 : 1);
+      const bool odd = sm.odd[part & 7] == part + 1;
+      const int slot = 2 * (int)blockIdx.x + (j0 > 0 ? 0 : 1);
       const float f = l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
@@ -632,8 +677,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         tc_wait_ld();
         if (odd) {
           // values taken out of V: into the rows that see their slots
-          for (int u = max(sg.first_seen() + 1, sg.j0 * kPfTile); u <= min(seen, sg.j1 * kPfTile - 1); ++u) {
-            const size_t vrow = cache_row(p.c, sg.b, kHkv + sg.g, u);
+          for (int u = hidden; u <= min(seen, j1 * kPfTile - 1); ++u) {
+            const size_t vrow = cache_row(p.c, b, kHkv + g, u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float y[8];
@@ -643,34 +688,42 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (!(fabsf(y[e]) <= 3.4e38f)) o[8 * i + e] = __float_as_uint(__uint_as_float(o[8 * i + e]) + y[e]);
             }
           }
+          __syncwarp();
         }
         if (whole) {
-          // through the tile's place in shared memory (its products with K are done)
+          // four lanes hold a token's four heads: turned about, so that they store 64
+          // bytes of one head after another
+          uint4 c[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               w[e] = round2<QF>(__uint_as_float(o[8 * i + 2 * e]) * f, __uint_as_float(o[8 * i + 2 * e + 1]) * f);
-            *reinterpret_cast<uint4*>(sm.q[t] + pf_piece(r, 4 * k + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+            c[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+#pragma unroll
+          for (int step = 1; step < 4; step *= 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((i & step) == 0) {
+                const bool up = (lane & step) != 0;
+                const uint4 give = up ? c[i] : c[i + step];
+                const uint4 got = make_uint4(__shfl_xor_sync(0xffffffffu, give.x, step), __shfl_xor_sync(0xffffffffu, give.y, step),
+                                             __shfl_xor_sync(0xffffffffu, give.z, step), __shfl_xor_sync(0xffffffffu, give.w, step));
+                c[i] = up ? got : c[i];
+                c[i + step] = up ? c[i + step] : got;
+              }
+          if (r / 4 < tokens) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_at + (size_t)(r / 4) * kHq * kD) + 4 * k + (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i * (kD / 8)] = c[i];
           }
         } else {
           float* dst = p.part_o + ((size_t)slot * kD + 32 * k) * (2 * kPfRows) + t * kPfRows + r;
 #pragma unroll
           for (int i = 0; i < 32; ++i) dst[i * (2 * kPfRows)] = __uint_as_float(o[i]);
         }
-      }
-      if (whole) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
-          if (tok < sg.row.n)
-            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                       ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + (lane & 15)) =
-                *reinterpret_cast<const uint4*>(sm.q[t] + pf_piece(row, lane & 15));
-        }
-        __syncwarp();
       }
       if (!whole) p.part_ml[(size_t)slot * (2 * kPfRows) + t * kPfRows + r] = make_float2(m, l);
     }
@@ -921,7 +974,7 @@ constexpr int kMergeThreads = 128;
 // the first run that does.
 template <int QF>
 __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  __shared__ long long s_sum[kMergeThreads / 32];
+  __shared__ long long s_sum[2 * kMergeThreads / 32];
   __shared__ PfCursor s_unit;
   __shared__ int s_pieces;  // 0: nothing to do
   __shared__ long long s_begin;
@@ -934,15 +987,15 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   if (warp == 0) {
     long long rem;
-    const int b = pf_find_row(p, at, rem);
+    const int b = pf_find_row(p, at, plan.cost, rem);
     if (lane == 0) {
       PfCursor u;
       u.b = b;
       u.row = pf_row(p, b);
       int j;
-      pf_locate(u.row, rem, u.g, u.m, j);
+      pf_locate(u.row, rem, plan.cost, u.g, u.m, j);
       u.all = u.row.tiles(u.m);
-      const long long begin = at - j;  // the unit's first position
+      const long long begin = at - j;  // the position of the unit's first tile
       s_begin = begin;
       // inside the unit, and no earlier run's begin is
       s_pieces = j > 0 && at - plan.run <= begin ? (int)((begin + u.all - 1) / plan.run - begin / plan.run) + 1 : 0;

@@ -75,7 +75,12 @@ cudaError_t prefill_setup() {
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     g_encode = reinterpret_cast<Encode>(fn);
   }
-  cudaError_t e = set_attributes<kKvF16, kQF16>();
+  // (the merge kernel keeps the split of shared memory and L1 that the other needs:
+  // changing it between the two would wait until an SM is empty)
+  cudaError_t e = cudaFuncSetAttribute(prefill_merge_kernel<kQF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(prefill_merge_kernel<kQBF16>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  if (e == cudaSuccess) e = set_attributes<kKvF16, kQF16>();
   if (e == cudaSuccess) e = set_attributes<kKvBF16, kQBF16>();
   if (e == cudaSuccess) e = set_attributes<kKvE4M3, kQF16>();
   if (e == cudaSuccess) e = set_attributes<kKvE4M3, kQBF16>();
