@@ -319,7 +319,7 @@ struct PfShared {
   uint64_t kv_empty[kPfSlots], raw_full[3], raw_empty[3];
   PfCursor cursor[kPfThreads / 32];
   uint32_t tmem;
-  int odd[8];  // a segment's number + 1 where a value was taken out of V
+  uint16_t odd[8];  // a part's number + 1 where a value was taken out of V (a stale one only costs time)
 };
 
 // Two FP32 operations in one instruction.
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (!wait(&sm.o_full[t], o_phase)) break;
       o_phase ^= 1;
       tc_fence_after();
-      const bool odd = sm.odd[part & 7] == part + 1;
+      const bool odd = sm.odd[part & 7] == (uint16_t)(part + 1);
       const int slot = 2 * (int)blockIdx.x + (j0 > 0 ? 0 : 1);
       const float f = l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll 1
@@ -797,83 +797,122 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // -------------------------------------------------------- K and V tiles
     uint32_t item = 0, seg = 0;
     int tile_no = 0;
-    for (; ok && sg.next(p); ++seg) {
-      const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
-      for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
-        const int t0 = j * kPfTile;
-        const bool hidden = t0 + kPfTile - 1 > first_seen;  // slots that some query does not see
-        for (int plane = 0; ok && plane < 2; ++plane, ++item) {
-          const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
-          uint64_t* there = plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3];
-          uint8_t *dst = sm.kv[slot], *bytes = sm.kv[kSlots] + raw * kRawBytes;
-          if (warp == 9) {
-            // by TMA, in boxes of `box` rows: one, or a page's each; pages past the length
-            // are left out
-            if (!(kNarrow ? wait(&sm.raw_empty[raw], (item / kRaws & 1) ^ 1) : wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)))
-              break;
-            const int pg = plane * kHkv + sg.g, boxes = kPfTile / p.box;
-            uint64_t* full = kNarrow ? &sm.raw_full[raw] : there;
-            int row = -1;
-            if (p.c.block_table == nullptr) {
-              if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
-            } else if (lane < boxes && t0 + lane * p.box < len) {
-              row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
-            }
-            const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
-            if (lane == 0) {
-              if (some) mbar_arrive_expect_tx(full, (uint32_t)(__popc(some) * p.box * kv_row_bytes(KVF)));
-              else mbar_arrive(full);
-            }
-            __syncwarp();
-            if (row >= 0) {
-              if constexpr (kNarrow) {
-                tma_box(smem_addr(bytes) + lane * p.box * kv_row_bytes(KVF), &map, 0, row, full);
-              } else {
-                const uint32_t at = smem_addr(dst) + lane * p.box * 128;
-                tma_box(at, &map, 0, row, full);
-                tma_box(at + kPfTileBytes / 2, &map, 64, row, full);
-              }
-            }
-            if constexpr (scale_row_bytes(KVF) > 0) {
-              // the rows' scales: by plain loads (a row's need no more than their own size's alignment)
-              uint2 v[4];
+    if constexpr (kNarrow) {
+      // One warp has the tiles loaded as they lie; two widen them, four rows at a time, a
+      // lane 16 elements, eight lanes a row.  (The first widening a quarter too was
+      // slower: 1108 us against 730, fp4 4 x 1024 of 16384.  It then waits for the others
+      // where it should run ahead of them.)
+      PfCursor& la = sg;
+      uint32_t l_item = 0;
+      int lj = 0, l_end = 0, l_plane = 1, l_len = 0, l_row = -1, ids = 0, ids_next = 0;
+      uint2 sc[4], sc_next[4];  // row scales of the item before the one being loaded, and of that
+      const auto page_of = [&](int j) {  // of the lane's box
+        const int t = j * kPfTile + lane * p.box;
+        return lane < kPfTile / p.box && t < l_len
+                   ? __ldg(p.c.block_table + (size_t)la.b * p.c.max_pages + (t >> p.c.page_log2))
+                   : 0;
+      };
+      const auto load = [&]() {  // false: the run's end
+        if (l_plane == 1 && ++lj >= l_end) {
+          if (!la.next(p)) return false;
+          lj = la.j0;
+          l_end = la.j1;
+          l_len = la.row.len;
+          if (p.c.block_table) ids_next = page_of(lj);
+        }
+        l_plane ^= 1;
+        const int raw = (int)(l_item % kRaws), t0 = lj * kPfTile, pg = l_plane * kHkv + la.g;
+        uint8_t* bytes = sm.kv[kSlots] + raw * kRawBytes;
+        if (l_plane == 0 && p.c.block_table) {
+          ids = ids_next;
+          if (lj + 1 < l_end) ids_next = page_of(lj + 1);
+          if (ids < 0 || ids >= p.c.num_pages) {
+            if (p.c.flags) atomicOr(p.c.flags, GQA_FLAG_PAGE_CLAMPED);
+            ids = min(max(ids, 0), p.c.num_pages - 1);
+          }
+        }
+        l_row = -1;
+        if (p.c.block_table == nullptr) {
+          if (lane == 0) l_row = (int)(((size_t)la.b * 2 * kHkv + pg) * p.c.capacity + t0);
+        } else if (lane < kPfTile / p.box && t0 + lane * p.box < l_len) {
+          l_row = (int)((((size_t)ids * 2 * kHkv + pg) << p.c.page_log2) + ((t0 + lane * p.box) & ((1 << p.c.page_log2) - 1)));
+        }
+        if (!wait(&sm.raw_empty[raw], (l_item / kRaws & 1) ^ 1)) return false;
+        const uint32_t some = __ballot_sync(0xffffffffu, l_row >= 0);
+        if (lane == 0) {
+          if (some) mbar_arrive_expect_tx(&sm.raw_full[raw], (uint32_t)(__popc(some) * p.box * kv_row_bytes(KVF)));
+          else mbar_arrive(&sm.raw_full[raw]);
+        }
+        __syncwarp();
+        if (l_row >= 0) tma_box(smem_addr(bytes) + lane * p.box * kv_row_bytes(KVF), &map, 0, l_row, &sm.raw_full[raw]);
+        if constexpr (scale_row_bytes(KVF) > 0) {
+          // the rows' scales, by plain loads; store_scales puts them behind the codes
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int r = 32 * k + lane, first = __shfl_sync(0xffffffffu, row, r / p.box);
-                v[k] = make_uint2(0, 0);
-                if (first >= 0 && t0 + r < len) {
-                  size_t at = (size_t)first + (r & (p.box - 1));
-                  if constexpr (kChecked) {
-                    if (at >= p.c.rows) {
-                      if (p.c.flags) atomicOr(p.c.flags, GQA_FLAG_BOUNDS);
-                      at = 0;
-                    }
-                  }
-                  if constexpr (kI8) v[k].x = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
-                  else v[k] = __ldg(static_cast<const uint2*>(p.c.scales) + at);
+          for (int k = 0; k < 4; ++k) {
+            const int r = 32 * k + lane, first = __shfl_sync(0xffffffffu, l_row, r / p.box);
+            sc_next[k] = make_uint2(0, 0);
+            if (first >= 0 && t0 + r < l_len) {
+              size_t at = (size_t)first + (r & (p.box - 1));
+              if constexpr (kChecked) {
+                if (at >= p.c.rows) {
+                  if (p.c.flags) atomicOr(p.c.flags, GQA_FLAG_BOUNDS);
+                  at = 0;
                 }
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int r = 32 * k + lane;
-                if constexpr (kI8) sm.scales[tile_no & 3][plane][r] = (uint16_t)v[k].x;
-                else reinterpret_cast<uint2*>(bytes + kPfTile * kv_row_bytes(KVF))[r] = v[k];
-              }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(full);
+              if constexpr (kI8) sc_next[k].x = __ldg(static_cast<const uint16_t*>(p.c.scales) + at);
+              else sc_next[k] = __ldg(static_cast<const uint2*>(p.c.scales) + at);
             }
-          } else if constexpr (kNarrow) {
-            // widened: a warp takes four rows at a time, a lane 16 elements, eight lanes a row
+          }
+        }
+        ++l_item;
+        return true;
+      };
+      const auto store_scales = [&](uint32_t n) {
+        const int raw = (int)(n % kRaws), tile = (int)(n >> 1);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 32 * k + lane;
+          if constexpr (kI8) sm.scales[tile & 3][n & 1][r] = (uint16_t)sc[k].x;
+          else reinterpret_cast<uint2*>(sm.kv[kSlots] + raw * kRawBytes + kPfTile * kv_row_bytes(KVF))[r] = sc[k];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.raw_full[raw]);
+      };
+      if (warp == 9) {
+        // an item's scales are stored when the next one's are on their way
+        for (bool more = true; ok && more;) {
+          const uint32_t n = l_item;
+          more = load();
+          if constexpr (scale_row_bytes(KVF) > 0) {
+            if (n > 0 && ok) store_scales(n - 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[k] = sc_next[k];
+          }
+        }
+        // copies in flight land before the block's shared memory is given up
+        if (!ok)
+          for (uint32_t k = l_item > kRaws ? l_item - kRaws : 0; k < l_item; ++k) pf_wait(&sm.raw_full[k % kRaws], k / kRaws & 1);
+      } else {
+      const int piece = lane & 7;
+      for (; ok && sg.next(p); ++seg) {
+        const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
+        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+          const int t0 = j * kPfTile;
+          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+            const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
+            const uint8_t* bytes = sm.kv[kSlots] + raw * kRawBytes;
+            uint8_t* dst = sm.kv[slot];
             if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
-            const int piece = lane & 7;
-            const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && hidden;
+            // slots past the length, and values that some query does not see
+            const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && t0 + kPfTile - 1 > first_seen;
             bool odd = false;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 16; i0 += 4) {
+            for (int step = 0; step < 4; ++step) {
+              const int row0 = 64 * (warp - 10) + 16 * step + (lane >> 3);
               uint32_t d[4][8];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int row = 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+                const int row = row0 + 4 * i;
                 if constexpr (KVF == kKvE2M1) {
                   const uint2 v = *reinterpret_cast<const uint2*>(bytes + row * 64 + piece * 8);
                   const uint32_t w[2] = {v.x, v.y};
@@ -887,7 +926,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               if (tail || check) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int u = t0 + 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+                  const int u = t0 + row0 + 4 * i;
 #pragma unroll
                   for (int e = 0; e < 8; ++e) {
                     if (u >= len) d[i][e] = 0;
@@ -901,60 +940,92 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int row = 8 * (i0 + i) + 4 * (warp - 10) + (lane >> 3);
+                const int row = row0 + 4 * i;
                 st_shared16(dst + pf_piece(row, 2 * piece), d[i][0], d[i][1], d[i][2], d[i][3]);
                 st_shared16(dst + pf_piece(row, 2 * piece + 1), d[i][4], d[i][5], d[i][6], d[i][7]);
               }
             }
-            if (odd) sm.odd[seg & 7] = (int)seg + 1;
+            if (odd) sm.odd[seg & 7] = (uint16_t)(seg + 1);
             proxy_fence();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&sm.raw_empty[raw]);
-              mbar_arrive(there);
+              mbar_arrive(plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3]);
             }
-          } else if (plane == 1) {
-            // the V tiles that hold hidden slots
-            if (!wait(there, tile_no >> 2 & 1)) break;
-            if (hidden) {
-              bool odd = false;
-              for (int i = tid - 320; i < kPfTile * 16; i += 64) {
-                const int row = i >> 4, u = t0 + row;
-                if (u <= first_seen) continue;
-                uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
-                if (u >= len) {
-                  *at = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
-                const uint4 v = *at;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool bad = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
-                  if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
-                }
-                if (bad) {
-                  odd = true;
-                  *at = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              }
-              if (odd) sm.odd[seg & 7] = (int)seg + 1;
-              proxy_fence();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.v_fixed[tile_no & 3]);
           }
         }
       }
-    }
-    // copies in flight land before the block's shared memory is given up
-    if (warp == 9 && !ok) {
-      const uint32_t depth = kNarrow ? kRaws : kSlots;
-      for (uint32_t k = item > depth ? item - depth : 0; k < item; ++k) {
-        if (kNarrow) pf_wait(&sm.raw_full[k % kRaws], k / kRaws & 1);
-        else pf_wait(k & 1 ? &sm.v_full[k / 2 & 3] : &sm.k_full[k / 2 & 3], k / 8 & 1);
       }
+    } else {
+      for (; ok && sg.next(p); ++seg) {
+        const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
+        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+          const int t0 = j * kPfTile;
+          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+            const int slot = (int)(item % kSlots);
+            uint64_t* full = plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3];
+            uint8_t* dst = sm.kv[slot];
+            if (warp == 9) {
+              // by TMA, in boxes of `box` rows: one, or a page's each; pages past the
+              // length are left out
+              if (!wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
+              const int pg = plane * kHkv + sg.g;
+              int row = -1;
+              if (p.c.block_table == nullptr) {
+                if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
+              } else if (lane < kPfTile / p.box && t0 + lane * p.box < len) {
+                row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
+              }
+              const uint32_t some = __ballot_sync(0xffffffffu, row >= 0);
+              if (lane == 0) {
+                if (some) mbar_arrive_expect_tx(full, (uint32_t)(__popc(some) * p.box * kD * 2));
+                else mbar_arrive(full);
+              }
+              __syncwarp();
+              if (row >= 0) {
+                const uint32_t at = smem_addr(dst) + lane * p.box * 128;
+                tma_box(at, &map, 0, row, full);
+                tma_box(at + kPfTileBytes / 2, &map, 64, row, full);
+              }
+            } else if (plane == 1) {
+              // the V tiles that hold slots which some query does not see
+              if (!wait(full, tile_no >> 2 & 1)) break;
+              if (t0 + kPfTile - 1 > first_seen) {
+                bool odd = false;
+                for (int i = tid - 320; i < kPfTile * 16; i += 64) {
+                  const int row = i >> 4, u = t0 + row;
+                  if (u <= first_seen) continue;
+                  uint4* at = reinterpret_cast<uint4*>(dst + pf_piece(row, i & 15));
+                  if (u >= len) {
+                    *at = make_uint4(0, 0, 0, 0);
+                    continue;
+                  }
+                  const uint4 v = *at;
+                  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                  bool bad = false;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (!pair_finite<MF>(w[e] & 0xffffu)) w[e] &= 0xffff0000u, bad = true;
+                    if (!pair_finite<MF>(w[e] & 0xffff0000u)) w[e] &= 0xffffu, bad = true;
+                  }
+                  if (bad) {
+                    odd = true;
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                  }
+                }
+                if (odd) sm.odd[seg & 7] = (uint16_t)(seg + 1);
+                proxy_fence();
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.v_fixed[tile_no & 3]);
+            }
+          }
+        }
+      }
+      // copies in flight land before the block's shared memory is given up
+      if (warp == 9 && !ok)
+        for (uint32_t k = item > kSlots ? item - kSlots : 0; k < item; ++k)
+          pf_wait(k & 1 ? &sm.v_full[k / 2 & 3] : &sm.k_full[k / 2 & 3], k / 8 & 1);
     }
   }
   if (!ok && lane == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_WAIT_TIMEOUT);
@@ -968,7 +1039,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
 // ---- merging a unit's pieces -----------------------------------------------
 
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeDims = kD / (kMergeThreads / 32);  // of a row that a thread merges
 
 // CTA (c, k): rows [32 k, 32 k + 32) of the unit that run c begins inside of, if c is
 // the first run that does.
@@ -1009,27 +1081,49 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
   if (u.m * kPfTokens + 8 * (int)blockIdx.y >= u.row.n) return;
   const bool live = token < u.row.n;
   const int first = (int)(s_begin / plan.run);
-  float m = -INFINITY;
   const auto slot_of = [&](int k) { return 2 * (first + k) + ((long long)(first + k) * plan.run > s_begin ? 0 : 1); };
-  for (int k = 0; k < s_pieces; ++k) m = fmaxf(m, p.part_ml[(size_t)slot_of(k) * (2 * kPfRows) + row].x);
-  float l = 0.f, o[32];
+  constexpr int kSide = 4;  // pieces whose loads are in flight together
+  float m = -INFINITY;
+  for (int k0 = 0; k0 < s_pieces; k0 += 2 * kSide) {
+    float x[2 * kSide];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) o[i] = 0.f;
-  for (int k = 0; k < s_pieces; ++k) {
-    const int slot = slot_of(k);
-    const float2 x = p.part_ml[(size_t)slot * (2 * kPfRows) + row];
-    const float f = x.x == -INFINITY ? 0.f : ex2(x.x - m);
-    if (x.y != 0.f) l += x.y * f;
-    const float* src = p.part_o + ((size_t)slot * kD + 32 * warp) * (2 * kPfRows) + row;
+    for (int k = 0; k < 2 * kSide; ++k)
+      x[k] = k0 + k < s_pieces ? p.part_ml[(size_t)slot_of(k0 + k) * (2 * kPfRows) + row].x : -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] = fmaf(src[i * (2 * kPfRows)], f, o[i]);
+    for (int k = 0; k < 2 * kSide; ++k) m = fmaxf(m, x[k]);
+  }
+  float l = 0.f, o[kMergeDims];
+#pragma unroll
+  for (int i = 0; i < kMergeDims; ++i) o[i] = 0.f;
+  for (int k0 = 0; k0 < s_pieces; k0 += kSide) {
+    float2 ml[kSide];
+    float y[kSide][kMergeDims];
+#pragma unroll
+    for (int k = 0; k < kSide; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (k0 + k < s_pieces) {
+        const int slot = slot_of(k0 + k);
+        ml[k] = p.part_ml[(size_t)slot * (2 * kPfRows) + row];
+        const float* src = p.part_o + ((size_t)slot * kD + kMergeDims * warp) * (2 * kPfRows) + row;
+#pragma unroll
+        for (int i = 0; i < kMergeDims; ++i) y[k][i] = src[i * (2 * kPfRows)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSide; ++k) {
+      if (k0 + k >= s_pieces) break;
+      const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - m);
+      if (ml[k].y != 0.f) l += ml[k].y * f;
+#pragma unroll
+      for (int i = 0; i < kMergeDims; ++i) o[i] = fmaf(y[k][i], f, o[i]);
+    }
   }
   if (!live) return;
   const float f = l == 0.f ? 0.f : p.v_scale / l;
   uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                        ((size_t)(u.row.at + token) * kHq + 4 * u.g + (row & 3)) * kD + 32 * warp);
+                                        ((size_t)(u.row.at + token) * kHq + 4 * u.g + (row & 3)) * kD + kMergeDims * warp);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kMergeDims / 8; ++i) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = round2<QF>(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
