@@ -1006,7 +1006,7 @@ gqa_status_t accumulate(const CacheArgs& c, const void* q, int q_dtype, const in
   p.chunk = (int)(((c.capacity + want - 1) / want + kScoreRound - 1) / kScoreRound * kScoreRound);
   p.chunks = (c.capacity + p.chunk - 1) / p.chunk;
   p.add = add != 0;
-  const cudaError_t e = launch_sum_weights(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, q_len, stream);
+  const cudaError_t e = launch_sum_weights(p, c.format, q_dtype == GQA_BF16 ? kQBF16 : kQF16, q_len, sms, stream);
   if (e != cudaSuccess) return cuda_fail(e, "weight sum kernel launch");
   return GQA_OK;
 }
@@ -1107,7 +1107,7 @@ gqa_status_t evict(const CacheArgs& c, const EvictArgs& a) {
   p.weights_capacity = in_place ? c.capacity : a.weights_capacity;
   p.chunks = (int)(((size_t)a.keep + move_rows(c.format) - 1) / move_rows(c.format));
   p.in_place = in_place;
-  const cudaError_t e = launch_evict(p, c.format, a.stream);
+  const cudaError_t e = launch_evict(p, c.format, sms, a.stream);
   if (e != cudaSuccess) return cuda_fail(e, "eviction kernel launch");
   return GQA_OK;
 }

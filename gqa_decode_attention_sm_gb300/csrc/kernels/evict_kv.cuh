@@ -2,13 +2,16 @@
 // `recent` and, of those between, the ones of the largest weights stay, `keep` in
 // all, each KV head choosing for itself; they move in their order to slots 0, 1, ...
 //
-// select_kv_kernel finds a head's threshold, the k-th largest weight, digit by digit
-// (11, 11 and 10 bits of the weights' order-preserving integers, a histogram each),
-// and then writes the kept slots in ascending order by a prefix sum of "above the
-// threshold, or equal to it and among the first such".  A cluster of CTAs shares a
-// head: each holds its part of the weights in shared memory, so that they are read
-// once, and the histograms and counts meet in distributed shared memory.  Everything
-// counted is whole numbers, so the result does not depend on any order.
+// A head's threshold is its k-th largest weight, of the weights' order-preserving
+// integers.  select_few_kernel (up to 32768 slots) holds a head's weights in one CTA's
+// registers and finds the threshold bit by bit, counting the weights that are no
+// smaller: about 80 cycles a bit besides a compare a weight, where a histogram's atomics
+// meet in the few bins that softmax weights lie in (32 x 8192: 25 us with histograms).
+// select_kv_kernel takes more: 11, 11 and 10 bits at a time, a histogram each, by a
+// cluster of CTAs that hold their parts of the weights in shared memory; histograms and
+// counts meet in distributed shared memory.  Both then write the kept slots in ascending
+// order by a prefix sum of "above the threshold, or equal to it and among the first
+// such".  Everything counted is whole numbers, so the result does not depend on any order.
 //
 // move_kv_kernel gathers the rows (and their scales and weights), 16 KB a CTA.  Bound
 // by HBM.  In place a CTA may overwrite rows that another has yet to read: the CTAs
@@ -22,6 +25,8 @@
 
 namespace gqa {
 
+constexpr int kFewThreads = 1024;
+constexpr int kFewSlots = 32 * kFewThreads;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectKeys = 48 * 1024;  // weights that a CTA holds in shared memory (192 KB)
 constexpr int kMoveThreads = 256;
@@ -66,6 +71,114 @@ __device__ __forceinline__ uint32_t head_ld(const uint32_t* p, int S, int rank) 
   return v;
 }
 
+// What both kernels do besides choosing: the row's saved length, the in-place move's
+// flags cleared, the slots that are kept anyway.  Returns the slots held; `keep` or
+// fewer need no choice.
+__device__ __forceinline__ int select_begin(const EvictParams& p, int unit, int first, int step) {
+  const int b = unit / kHkv, L = clamp_length(__ldg(p.lens + b), p.src.capacity, p.flags, unit % kHkv == 0 && first == 0);
+  int32_t* kept = p.kept + (size_t)unit * p.keep;
+  if (first == 0 && unit % kHkv == 0) p.old_lens[b] = L;
+  if (p.in_place) {
+    for (int i = first; i < 2 * p.chunks; i += step) p.read_flags[(size_t)unit * 2 * p.chunks + i] = 0u;
+    if (unit == 0 && first == 0) *p.ticket = 0u;
+  }
+  if (L <= p.keep) {
+    for (int i = first; i < p.keep; i += step) kept[i] = i < L ? i : -1;
+  } else {  // first + recent <= keep < L
+    for (int i = first; i < p.first + p.recent; i += step)
+      kept[i < p.first ? i : p.keep - p.recent + (i - p.first)] = i < p.first ? i : L - p.recent + (i - p.first);
+  }
+  return L;
+}
+
+// K weights a thread: warp w has K * 32 consecutive slots, 32 at a time.
+template <int K>
+__global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kWarps = kFewThreads / 32;
+  __shared__ uint32_t s_count[3], s_above[kWarps], s_equal[kWarps];
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int unit = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
+  const int L = select_begin(p, unit, tid, kFewThreads);
+  if (L <= p.keep) return;
+  const int lo = p.first, hi = L - p.recent;
+  const float* w = p.weights + (size_t)unit * p.src.capacity;
+  const size_t extent = (size_t)p.batch * kHkv * p.src.capacity * 4;
+  uint32_t x[K];  // 0 (no weight but NaN) where there is no slot: never counted, its index is looked at
+  const int at = lo + warp * 32 * K + lane;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    x[i] = 0u;
+    if (at + 32 * i < hi) x[i] = weight_key(__ldg(in_buffer(w + at + 32 * i, 4, p.weights, extent, p.flags)));
+  }
+  if (tid < 3) s_count[tid] = 0u;
+  __syncthreads();
+  // The number of weights at or above `least`, which is not 0.  Three counters by turns:
+  // the next call's, read two calls ago, is cleared while this one's is added to.
+  int turn = 0;
+  const auto count = [&](uint32_t least) {
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) n += x[i] >= least;
+    n = __reduce_add_sync(0xffffffffu, n);
+    const int next = turn == 2 ? 0 : turn + 1;
+    if (lane == 0 && n) atomicAdd(&s_count[turn], n);
+    if (tid == 0) s_count[next] = 0u;
+    __syncthreads();
+    n = s_count[turn];
+    turn = next;
+    return n;
+  };
+  // kept: above `threshold`, and the first `equal_needed` equal to it
+  uint32_t need = (uint32_t)(p.keep - p.first - p.recent), threshold = 0u;
+  if (need == 0) {
+    threshold = 0xffffffffu;  // (no weight's key)
+  } else {
+    bool exact = false;
+    for (int bit = 31; bit >= 0 && !exact; --bit) {
+      const uint32_t least = threshold | 1u << bit;
+      const uint32_t n = count(least);
+      if (n >= need) threshold = least;
+      exact = n == need;
+    }
+    if (exact) {
+      threshold -= 1u;  // all at or above it, as many as needed
+      need = 0u;
+    } else {
+      need -= count(threshold + 1u);
+    }
+  }
+  uint32_t above = 0, equal = 0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const bool in = at + 32 * i < hi;
+    above += __popc(__ballot_sync(0xffffffffu, in && x[i] > threshold));
+    equal += __popc(__ballot_sync(0xffffffffu, in && x[i] == threshold));
+  }
+  if (lane == 0) {
+    s_above[warp] = above;
+    s_equal[warp] = equal;
+  }
+  __syncthreads();
+  // before this warp: lane k has warp k's
+  above = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane % kWarps] : 0u);
+  equal = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane % kWarps] : 0u);
+  int32_t* kept = p.kept + (size_t)unit * p.keep;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const bool in = at + 32 * i < hi;
+    const uint32_t gt = __ballot_sync(0xffffffffu, in && x[i] > threshold);
+    const uint32_t eq = __ballot_sync(0xffffffffu, in && x[i] == threshold);
+    const uint32_t before = (1u << lane) - 1, rank = equal + __popc(eq & before);
+    if (in && (x[i] > threshold || (x[i] == threshold && rank < need))) {
+      const uint32_t to = (uint32_t)p.first + above + __popc(gt & before) + min(rank, need);
+      if (to < (uint32_t)p.keep) kept[to] = at + 32 * i;  // (always; every address here is held in bounds)
+    }
+    above += __popc(gt);
+    equal += __popc(eq);
+  }
+}
+
 template <int kSelectThreads>
 __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kSelectWarps = kSelectThreads / 32;
@@ -77,26 +190,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int S = p.cluster, rank = (int)blockIdx.x % S;
-  const int unit = blockIdx.x / S, b = unit / kHkv;
+  const int unit = blockIdx.x / S;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
   const int C = p.src.capacity;
-  const int L = clamp_length(__ldg(p.lens + b), C, p.flags, unit % kHkv == 0 && rank == 0 && tid == 0);
-  const int n = min(L, p.keep);
+  const int L = select_begin(p, unit, rank * kSelectThreads + tid, S * kSelectThreads);
+  if (L <= p.keep) return;  // (the same in every CTA of the cluster)
   int32_t* kept = p.kept + (size_t)unit * p.keep;
-  if (rank == 0 && tid == 0 && unit % kHkv == 0) p.old_lens[b] = L;
-  if (p.in_place) {
-    for (int i = rank * kSelectThreads + tid; i < 2 * p.chunks; i += S * kSelectThreads)
-      p.read_flags[(size_t)unit * 2 * p.chunks + i] = 0u;
-    if (unit == 0 && rank == 0 && tid == 0) *p.ticket = 0u;
-  }
-  if (L <= p.keep) {  // (the same in every CTA of the cluster)
-    for (int i = rank * kSelectThreads + tid; i < p.keep; i += S * kSelectThreads) kept[i] = i < n ? i : -1;
-    return;
-  }
-  // first + recent <= keep < L
   const int lo = p.first, hi = L - p.recent;
-  for (int i = rank * kSelectThreads + tid; i < p.first + p.recent; i += S * kSelectThreads)
-    kept[i < p.first ? i : p.keep - p.recent + (i - p.first)] = i < p.first ? i : hi + (i - p.first);
   const float* w = p.weights + (size_t)unit * C;
   const size_t w_extent = (size_t)p.batch * kHkv * C * 4;
   const auto load_key = [&](int t) { return weight_key(__ldg(in_buffer(w + t, 4, p.weights, w_extent, p.flags))); };
@@ -129,9 +229,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_
       head_sync(S);
       uint32_t mine[2] = {0, 0};  // bins 2 tid, 2 tid + 1 counted from the top
       const int top = kSelectBins - 1 - 2 * tid;
-      for (int k = 0; k < S; ++k) {
-        mine[0] += head_ld(hist + top, S, k);
-        mine[1] += head_ld(hist + top - 1, S, k);
+      uint32_t theirs[8][2];  // (all on their way before the first is added)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        theirs[k][0] = k < S ? head_ld(hist + top, S, k) : 0u;
+        theirs[k][1] = k < S ? head_ld(hist + top - 1, S, k) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        mine[0] += theirs[k][0];
+        mine[1] += theirs[k][1];
       }
       uint32_t upto = mine[0] + mine[1];
 #pragma unroll
@@ -181,9 +288,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_
   }
   head_sync(S);
   above = equal = 0;
-  for (int k = 0; k < rank; ++k) {
-    above += head_ld(s_count, S, k);
-    equal += head_ld(s_count + 1, S, k);
+  uint32_t theirs[8][2];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    theirs[k][0] = k < rank ? head_ld(s_count, S, k) : 0u;
+    theirs[k][1] = k < rank ? head_ld(s_count + 1, S, k) : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    above += theirs[k][0];
+    equal += theirs[k][1];
   }
   head_sync(S);  // (nobody's shared memory is left while it is read)
   for (int k = 0; k < warp; ++k) {

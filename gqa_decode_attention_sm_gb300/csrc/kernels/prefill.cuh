@@ -893,68 +893,68 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!ok)
           for (uint32_t k = l_item > kRaws ? l_item - kRaws : 0; k < l_item; ++k) pf_wait(&sm.raw_full[k % kRaws], k / kRaws & 1);
       } else {
-      const int piece = lane & 7;
-      for (; ok && sg.next(p); ++seg) {
-        const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
-        for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
-          const int t0 = j * kPfTile;
-          for (int plane = 0; ok && plane < 2; ++plane, ++item) {
-            const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
-            const uint8_t* bytes = sm.kv[kSlots] + raw * kRawBytes;
-            uint8_t* dst = sm.kv[slot];
-            if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
-            // slots past the length, and values that some query does not see
-            const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && t0 + kPfTile - 1 > first_seen;
-            bool odd = false;
+        const int piece = lane & 7;
+        for (; ok && sg.next(p); ++seg) {
+          const int len = sg.row.len, first_seen = sg.first_seen(), j1 = sg.j1;
+          for (int j = sg.j0; ok && j < j1; ++j, ++tile_no) {
+            const int t0 = j * kPfTile;
+            for (int plane = 0; ok && plane < 2; ++plane, ++item) {
+              const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
+              const uint8_t* bytes = sm.kv[kSlots] + raw * kRawBytes;
+              uint8_t* dst = sm.kv[slot];
+              if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
+              // slots past the length, and values that some query does not see
+              const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && t0 + kPfTile - 1 > first_seen;
+              bool odd = false;
 #pragma unroll 1
-            for (int step = 0; step < 4; ++step) {
-              const int row0 = 64 * (warp - 10) + 16 * step + (lane >> 3);
-              uint32_t d[4][8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 4 * i;
-                if constexpr (KVF == kKvE2M1) {
-                  const uint2 v = *reinterpret_cast<const uint2*>(bytes + row * 64 + piece * 8);
-                  const uint32_t w[2] = {v.x, v.y};
-                  widen16<KVF, kQF16>(w, bytes[kPfTile * 64 + row * 8 + piece], d[i]);
-                } else {
-                  const uint4 v = *reinterpret_cast<const uint4*>(bytes + row * 128 + piece * 16);
-                  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                  widen16<KVF, kQF16>(w, 0, d[i]);
-                }
-              }
-              if (tail || check) {
+              for (int step = 0; step < 4; ++step) {
+                const int row0 = 64 * (warp - 10) + 16 * step + (lane >> 3);
+                uint32_t d[4][8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int u = t0 + row0 + 4 * i;
+                  const int row = row0 + 4 * i;
+                  if constexpr (KVF == kKvE2M1) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(bytes + row * 64 + piece * 8);
+                    const uint32_t w[2] = {v.x, v.y};
+                    widen16<KVF, kQF16>(w, bytes[kPfTile * 64 + row * 8 + piece], d[i]);
+                  } else {
+                    const uint4 v = *reinterpret_cast<const uint4*>(bytes + row * 128 + piece * 16);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    widen16<KVF, kQF16>(w, 0, d[i]);
+                  }
+                }
+                if (tail || check) {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) {
-                    if (u >= len) d[i][e] = 0;
-                    if (check && u > first_seen && !pair_finite<kQF16>(d[i][e])) {
-                      odd = true;
-                      if (!pair_finite<kQF16>(d[i][e] & 0xffffu)) d[i][e] &= 0xffff0000u;
-                      if (!pair_finite<kQF16>(d[i][e] & 0xffff0000u)) d[i][e] &= 0xffffu;
+                  for (int i = 0; i < 4; ++i) {
+                    const int u = t0 + row0 + 4 * i;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                      if (u >= len) d[i][e] = 0;
+                      if (check && u > first_seen && !pair_finite<kQF16>(d[i][e])) {
+                        odd = true;
+                        if (!pair_finite<kQF16>(d[i][e] & 0xffffu)) d[i][e] &= 0xffff0000u;
+                        if (!pair_finite<kQF16>(d[i][e] & 0xffff0000u)) d[i][e] &= 0xffffu;
+                      }
                     }
                   }
                 }
-              }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 4 * i;
-                st_shared16(dst + pf_piece(row, 2 * piece), d[i][0], d[i][1], d[i][2], d[i][3]);
-                st_shared16(dst + pf_piece(row, 2 * piece + 1), d[i][4], d[i][5], d[i][6], d[i][7]);
+                for (int i = 0; i < 4; ++i) {
+                  const int row = row0 + 4 * i;
+                  st_shared16(dst + pf_piece(row, 2 * piece), d[i][0], d[i][1], d[i][2], d[i][3]);
+                  st_shared16(dst + pf_piece(row, 2 * piece + 1), d[i][4], d[i][5], d[i][6], d[i][7]);
+                }
               }
-            }
-            if (odd) sm.odd[seg & 7] = (uint16_t)(seg + 1);
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sm.raw_empty[raw]);
-              mbar_arrive(plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3]);
+              if (odd) sm.odd[seg & 7] = (uint16_t)(seg + 1);
+              proxy_fence();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&sm.raw_empty[raw]);
+                mbar_arrive(plane == 0 ? &sm.k_full[tile_no & 3] : &sm.v_full[tile_no & 3]);
+              }
             }
           }
         }
-      }
       }
     } else {
       for (; ok && sg.next(p); ++seg) {

@@ -2,17 +2,24 @@
 // the four heads of each KV head and the window's tokens:
 //   weights[b, g, t] (+)= sum over j < T, h in g of exp(s_t - m) / sum_u exp(s_u - m)
 //
-// The weight of a slot needs the sum over all of them.  Two launches: the first
-// reads the keys once and writes every score (FP32, log2 domain) and each chunk's
-// maximum and sum; the second merges those of a row and turns scores into weights.
-// A score costs 4 bytes to write and 4 to read for each head and token, where the key
-// costs 256 bytes (4 bits: 72) for all of them, so keeping the scores beats reading the
-// keys twice except for 3- and 4-token windows over 4- and 8-bit caches.
+// The weight of a slot needs the sum over all of them, so a score is formed, kept, and
+// turned into a weight when the row's maximum and sum are known.
+//
+// fused_weights_kernel keeps them on chip: the CTAs of a cluster share a row of one KV
+// head and hold its scores in shared memory; their maxima and sums meet in distributed
+// shared memory.  For rows whose scores fit and batches that fill the GPU so.
+// Otherwise two launches: score_kv_kernel writes the scores (FP32, log2 domain) and
+// each chunk's maximum and sum, sum_weights_kernel merges those of a row and turns
+// scores into weights.  A score costs 4 bytes to write and 4 to read for each head and
+// token, where the key costs 256 bytes (4 bits: 72) for all of them; reading the keys
+// twice instead would cost less only for 3- and 4-token windows over 4- and 8-bit caches.
 //
 // Scores come from mma.sync m16n8k16 with 16 slots as rows and the (token, head)
 // pairs as columns.  The order of the dims in a dot product is free: each lane loads
 // 16-byte pieces of its two rows and multiplies them as they come, with q arranged
-// alike, so no shared memory and no transposition is needed.  Bound by HBM.
+// alike, so no shared memory and no transposition is needed.  Narrow keys are widened
+// to fp16 (exact), which takes a third of the instructions that bf16 takes; a bf16 q is
+// then scaled by a power of two a column into fp16's range.  Bound by HBM.
 #pragma once
 
 #include "cache_rows.cuh"
@@ -24,7 +31,8 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kSlab = 16;  // slots a warp takes at once
 constexpr int kSumThreads = 256;
 constexpr int kSumSlots = 1024;  // slots a CTA of the second launch takes
-constexpr int kMaxScoreCols = 16;
+constexpr int kRowCluster = 8;           // CTAs of the fused kernel a row
+constexpr int kScoreBytes = 96 * 1024;  // of scores that a CTA of the fused kernel holds (two CTAs an SM)
 
 struct WeightParams {
   CacheView c;
@@ -35,6 +43,7 @@ struct WeightParams {
   float2* stats;        // [B, 8, chunks, 4 T]: maximum, sum
   float scale_log2;
   int chunk, chunks, add;  // slots a CTA of the first launch takes, and how many such
+  int held;                // slots whose scores a CTA of the fused kernel holds
 };
 
 __device__ __forceinline__ void mma_16816_f32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -91,21 +100,23 @@ struct RowPart {
   }
 };
 
-template <int KVF, int QF, int NT>
-__global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_constant__ WeightParams p, int q_len) {
-  __shared__ float2 s_stats[kScoreWarps][8 * NT];
-  pdl_launch_dependents();
-  pdl_wait_prior_grid();
-  const int b = blockIdx.z, g = blockIdx.y;
+__device__ __forceinline__ void merge_stats(float& m0, float& l0, float m1, float l1) {
+  const float top = fmaxf(m0, m1);
+  l0 = (l0 == 0.f ? 0.f : l0 * ex2(m0 - top)) + (l1 == 0.f ? 0.f : l1 * ex2(m1 - top));  // (a NaN sum is not 0)
+  m0 = top;
+}
+
+// Scores of slots [begin, end) of batch row b and KV head g, each pair of columns given
+// to `store`(slot, first column, scores); their maxima and sums in s_stats[0][column].
+template <int KVF, int QF, int NT, class Store>
+__device__ __forceinline__ void score_rows(const WeightParams& p, int q_len, int b, int g, int len, int begin, int end,
+                                           float2 (*s_stats)[8 * NT], const Store& store) {
+  constexpr int MF = is_narrow(KVF) ? (int)kQF16 : QF;  // type of the products' operands
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const int C = p.c.capacity, cols = 4 * q_len;
-  const int raw = __ldg(p.lens + b);
-  const int len = clamp_length(raw, C, p.c.flags, blockIdx.x == 0 && g == 0 && threadIdx.x == 0);
-  if (len < q_len && blockIdx.x == 0 && g == 0 && threadIdx.x == 0 && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
-  const int begin = blockIdx.x * p.chunk, end = min(len, begin + p.chunk);
-  if (begin >= len) return;
+  const int cols = 4 * q_len;
   // q of column 8 nt + r, its dims in the order of a row's pieces
   uint32_t q[NT][16];
+  float scale[NT][2];  // of columns 8 nt + 2 c, + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int col = 8 * nt + r;
@@ -121,6 +132,26 @@ __global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_co
       q[nt][4 * i + 2] = x.z;
       q[nt][4 * i + 3] = x.w;
     }
+    float down = 1.f;
+    if constexpr (MF != QF) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = max(top, max(q[nt][i] & 0x7fffu, q[nt][i] >> 16 & 0x7fffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // the largest |q| into [2^14, 2^15) (its exponent -100 at least, so that the
+      // scale's stays a normal number)
+      const int e = min(max((int)(top >> 7) - 127, -100), 127);
+      const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+      down = __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float2 f = bf16x2_to_f32x2(q[nt][i]);
+        q[nt][i] = round2<kQF16>(f.x * up, f.y * up);
+      }
+    }
+    scale[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * c);
+    scale[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, down, 8 * c + 4);
   }
   float m[NT][2], l[NT][2];
 #pragma unroll
@@ -130,64 +161,73 @@ __global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_co
       m[nt][k] = -INFINITY;
       l[nt][k] = 0.f;
     }
-  const size_t unit = (size_t)b * kHkv + g;
-  float* out = p.scores + unit * C * cols;
-  const size_t out_extent = (size_t)p.c.batch * kHkv * C * cols * 4;
-  RowPart<KVF> next[2];
-  const auto fetch = [&](int t0) {
+  // A narrow row has few bytes: two slabs in flight a warp.  Their rows (a paged cache's
+  // block table) are looked up a step earlier.
+  constexpr int kSub = is_narrow(KVF) ? 2 : 1, kStep = kScoreWarps * kSlab * kSub;
+  RowPart<KVF> next[kSub][2];
+  size_t rows[kSub][2];
+  const auto look = [&](int t0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {  // (a slot at or past the end: the chunk's last one, whose scores are not used)
-      const int t = min(t0 + r + 8 * k, end - 1);
-      next[k].load(p.c, cache_row(p.c, b, g, t), c);
-    }
+    for (int u = 0; u < kSub; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)  // (a slot at or past the end: the last one, whose scores are not used)
+        rows[u][k] = cache_row(p.c, b, g, min(t0 + kSlab * u + r + 8 * k, end - 1));
   };
-  int t0 = begin + warp * kSlab;
-  if (t0 < end) fetch(t0);
-  for (; t0 < end; t0 += kScoreWarps * kSlab) {
-    uint32_t a[2][16];
-    float row_scale[2] = {p.scale_log2, p.scale_log2};
+  int t0 = begin + warp * kSlab * kSub;
+  if (t0 < end) {
+    look(t0);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      next[k].template pairs<QF>(a[k]);
-      if constexpr (KVF == kKvI8) row_scale[k] *= bf16_bits_to_f32((uint16_t)next[k].scale);
-    }
-    if (t0 + kScoreWarps * kSlab < end) fetch(t0 + kScoreWarps * kSlab);
+    for (int u = 0; u < kSub; ++u)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < 2; ++k) next[u][k].load(p.c, rows[u][k], c);
+    if (t0 + kStep < end) look(t0 + kStep);
+  }
+  for (; t0 < end; t0 += kStep) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        mma_16816_f32(d, a[0][2 * s], a[1][2 * s], a[0][2 * s + 1], a[1][2 * s + 1], q[nt][2 * s], q[nt][2 * s + 1],
-                      QF == kQBF16);
-      const int col = 8 * nt + 2 * c;
-      // query j sees slots up to len - T + j
-      const int seen = len - q_len + col / 4;
+    for (int u = 0; u < kSub; ++u) {
+      uint32_t a[2][16];
+      float row_scale[2] = {1.f, 1.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int t = t0 + r + 8 * k;
-        float2 s = make_float2(d[2 * k] * row_scale[k], d[2 * k + 1] * row_scale[k]);
-        if (t > seen || t >= end) s = make_float2(-INFINITY, -INFINITY);
-        if (col < cols && t < end)
-          *reinterpret_cast<float2*>(in_buffer(out + (size_t)t * cols + col, 8, p.scores, out_extent, p.c.flags)) = s;
-        const float sv[2] = {s.x, s.y};
+        next[u][k].template pairs<MF>(a[k]);
+        if constexpr (KVF == kKvI8) row_scale[k] = bf16_bits_to_f32((uint16_t)next[u][k].scale);
+      }
+      if (t0 + kStep < end) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float top = fmaxf(m[nt][e], sv[e]);
-          if (top > m[nt][e]) {
-            l[nt][e] *= ex2(m[nt][e] - top);
-            m[nt][e] = top;
+        for (int k = 0; k < 2; ++k) next[u][k].load(p.c, rows[u][k], c);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          mma_16816_f32(d, a[0][2 * s], a[1][2 * s], a[0][2 * s + 1], a[1][2 * s + 1], q[nt][2 * s], q[nt][2 * s + 1],
+                        MF == kQBF16);
+        const int col = 8 * nt + 2 * c;
+        // query j sees slots up to len - T + j
+        const int seen = len - q_len + col / 4;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = t0 + kSlab * u + r + 8 * k;
+          float2 s = make_float2(d[2 * k] * row_scale[k] * scale[nt][0], d[2 * k + 1] * row_scale[k] * scale[nt][1]);
+          if (t > seen || t >= end) s = make_float2(-INFINITY, -INFINITY);
+          if (col < cols && t < end) store(t, col, s);
+          const float sv[2] = {s.x, s.y};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = fmaxf(m[nt][e], sv[e]);
+            if (top > m[nt][e]) {
+              l[nt][e] *= ex2(m[nt][e] - top);
+              m[nt][e] = top;
+            }
+            if (t <= seen && t < end) l[nt][e] += ex2(sv[e] - m[nt][e]);  // (a NaN score makes a NaN sum)
           }
-          if (t <= seen && t < end) l[nt][e] += ex2(sv[e] - m[nt][e]);  // (a NaN score makes a NaN sum)
         }
       }
     }
+    if (t0 + 2 * kStep < end) look(t0 + 2 * kStep);
   }
-  // the chunk's maximum and sum of each column: over the lanes of a column, then the warps
-  const auto merge = [](float& m0, float& l0, float m1, float l1) {
-    const float top = fmaxf(m0, m1);
-    l0 = (l0 == 0.f ? 0.f : l0 * ex2(m0 - top)) + (l1 == 0.f ? 0.f : l1 * ex2(m1 - top));
-    m0 = top;
-  };
+  // over the lanes of a column, then the warps
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -195,15 +235,92 @@ __global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_co
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         const float mo = __shfl_xor_sync(0xffffffffu, m[nt][e], o), lo = __shfl_xor_sync(0xffffffffu, l[nt][e], o);
-        merge(m[nt][e], l[nt][e], mo, lo);
+        merge_stats(m[nt][e], l[nt][e], mo, lo);
       }
       if (r == 0) s_stats[warp][8 * nt + 2 * c + e] = make_float2(m[nt][e], l[nt][e]);
     }
   __syncthreads();
-  if (threadIdx.x < cols) {
+  if (threadIdx.x < 8 * NT) {
     float2 x = s_stats[0][threadIdx.x];
-    for (int w = 1; w < kScoreWarps; ++w) merge(x.x, x.y, s_stats[w][threadIdx.x].x, s_stats[w][threadIdx.x].y);
-    p.stats[(unit * p.chunks + blockIdx.x) * cols + threadIdx.x] = x;
+    for (int w = 1; w < kScoreWarps; ++w) merge_stats(x.x, x.y, s_stats[w][threadIdx.x].x, s_stats[w][threadIdx.x].y);
+    s_stats[0][threadIdx.x] = x;
+  }
+  __syncthreads();
+}
+
+template <int KVF, int QF, int NT>
+__global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_constant__ WeightParams p, int q_len) {
+  __shared__ float2 s_stats[kScoreWarps][8 * NT];
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int b = blockIdx.z, g = blockIdx.y, C = p.c.capacity, cols = 4 * q_len;
+  const bool tell = blockIdx.x == 0 && g == 0 && threadIdx.x == 0;
+  const int len = clamp_length(__ldg(p.lens + b), C, p.c.flags, tell);
+  if (len < q_len && tell && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
+  const int begin = blockIdx.x * p.chunk, end = min(len, begin + p.chunk);
+  if (begin >= len) return;
+  const size_t unit = (size_t)b * kHkv + g;
+  float* out = p.scores + unit * C * cols;
+  const size_t extent = (size_t)p.c.batch * kHkv * C * cols * 4;
+  score_rows<KVF, QF, NT>(p, q_len, b, g, len, begin, end, s_stats, [&](int t, int col, float2 s) {
+    *reinterpret_cast<float2*>(in_buffer(out + (size_t)t * cols + col, 8, p.scores, extent, p.c.flags)) = s;
+  });
+  if (threadIdx.x < cols) p.stats[(unit * p.chunks + blockIdx.x) * cols + threadIdx.x] = s_stats[0][threadIdx.x];
+}
+
+// A cluster of CTAs a (row, KV head); a CTA's slots are an equal part of the
+// row's, p.held at most.
+template <int KVF, int QF, int NT>
+__global__ void __launch_bounds__(kScoreThreads) fused_weights_kernel(const __grid_constant__ WeightParams p, int q_len) {
+  extern __shared__ float s_scores[];  // [slot][column]
+  __shared__ float2 s_stats[kScoreWarps][8 * NT];
+  __shared__ float s_m[8 * NT], s_r[8 * NT];
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  constexpr int S = kRowCluster;
+  const int rank = (int)blockIdx.x % S;
+  const size_t unit = blockIdx.x / S;
+  const int b = (int)(unit / kHkv), g = (int)(unit % kHkv), C = p.c.capacity, cols = 4 * q_len;
+  const bool tell = rank == 0 && g == 0 && threadIdx.x == 0;
+  const int len = clamp_length(__ldg(p.lens + b), C, p.c.flags, tell);
+  if (len < q_len && tell && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
+  if (len == 0) return;  // (all of the cluster)
+  const int part = ((len + S - 1) / S + kSlab - 1) / kSlab * kSlab;
+  const int begin = min(len, rank * part), end = min(len, begin + part);
+  score_rows<KVF, QF, NT>(p, q_len, b, g, len, begin, end, s_stats, [&](int t, int col, float2 s) {
+    *reinterpret_cast<float2*>(s_scores + (size_t)min(t - begin, p.held - 1) * cols + col) = s;
+  });
+  cluster_sync_all();
+  if (threadIdx.x < 8 * NT) {
+    const uint32_t at = smem_addr(&s_stats[0][threadIdx.x]);
+    float2 y[S];  // (all on their way before the first is merged)
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const uint32_t theirs = cluster_map(at, (uint32_t)k);
+      y[k] = make_float2(cluster_ld(theirs), cluster_ld(theirs + 4));
+    }
+    float2 x = y[0];
+#pragma unroll
+    for (int k = 1; k < S; ++k) merge_stats(x.x, x.y, y[k].x, y[k].y);
+    s_m[threadIdx.x] = x.x;
+    s_r[threadIdx.x] = x.y == 0.f ? 0.f : 1.f / x.y;  // (a query that sees no slot gives no weight)
+  }
+  cluster_sync_all();  // (nobody's shared memory is left while it is read)
+  const size_t extent = (size_t)p.c.batch * kHkv * C * 4;
+  for (int t = begin + threadIdx.x; t < end; t += kScoreThreads) {
+    const float4* src = reinterpret_cast<const float4*>(s_scores + (size_t)(t - begin) * cols);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {
+      if (j >= q_len) break;
+      const float4 x = src[j];
+      const float s[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        if (s[h] != -INFINITY) sum += ex2(s[h] - s_m[4 * j + h]) * s_r[4 * j + h];
+    }
+    float* dst = in_buffer(p.weights + unit * C + t, 4, p.weights, extent, p.c.flags);
+    *dst = p.add ? *dst + sum : sum;
   }
 }
 

@@ -22,6 +22,7 @@
 namespace gqa {
 
 constexpr int kDraftThreads = 512;
+constexpr int kDraftCluster = 8;  // CTAs a request
 constexpr int kDraftWarps = kDraftThreads / 32;
 constexpr int kMaxWindow = 32;  // a warp's lanes judge a window's drafts at once
 
@@ -75,10 +76,24 @@ __device__ __forceinline__ void prob_vec(uint4 v, float (&x)[ProbTraits<PF>::kVe
   }
 }
 
-// The weight of a token with probability p where the draft's was q, in units of
-// 2^-38 (NaN and negative values none; p - q is rounded once, in FP32).
-__device__ __forceinline__ unsigned long long draft_weight(float p, float q) {
-  return (unsigned long long)__float2ll_rn(__saturatef(p - q) * 0x1p38f);
+// The weight of a token with probability p where the draft's was q, in units of 2^-38
+// (NaN and negative values none; p - q is rounded once, in FP32), as 2^22 hi + lo.
+// Whole numbers come from adding 2^23, which costs an FP32 operation where the 64-bit
+// conversion has a sixteenth of its rate (64 x 131072 tokens: 38 us with that, 17
+// so): hi the 2^16 x rounded down, lo the exact rest in units of 2^-22, to the nearest
+// (ties to even: 2^22 hi is even).
+struct DraftWeight {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ DraftWeight draft_weight(float p, float q) {
+  const float x = __saturatef(p - q);
+  const float whole = __fmaf_rz(x, 0x1p16f, 0x1p23f);
+  const float rest = fmaf(x, 0x1p16f, -(whole - 0x1p23f));
+  const float part = __fmaf_rn(rest, 0x1p22f, 0x1p23f);
+  return {__float_as_uint(whole) - 0x4b000000u, __float_as_uint(part) - 0x4b000000u};
+}
+__device__ __forceinline__ unsigned long long units_of(uint32_t hi, uint32_t lo) {
+  return ((unsigned long long)hi << 22) + lo;
 }
 
 // How a request's row is weighed: the row of p, the row of q or none, and the token
@@ -93,7 +108,8 @@ template <int PF>
 __device__ __forceinline__ unsigned long long token_weight(const DraftParams& p, const DraftRow& r, int i) {
   const float a = prob_at<PF>(p.probs, r.p0 + i, p, p.p_bytes);
   const float b = r.q ? prob_at<PF>(p.draft_probs, r.q0 + i, p, p.q_bytes) : 0.f;
-  return i == r.without ? 0ull : draft_weight(a, b);
+  const DraftWeight w = draft_weight(a, b);
+  return i == r.without ? 0ull : units_of(w.hi, w.lo);
 }
 
 // The sum of tokens [lo, hi) over the warp, in every lane.
@@ -128,6 +144,7 @@ __device__ __forceinline__ unsigned long long run_sum(const DraftParams& p, cons
             y[k] = __ldg(in_buffer(vb + g + 32 * k, 16, reinterpret_cast<const uint4*>(p.draft_probs), p.q_bytes, p.flags));
         }
       }
+      uint32_t hi = 0, lo = 0;  // (kDeep * kVec <= 32 terms: below 2^22 and 2^28)
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
         float s[kVec], t[kVec];
@@ -135,8 +152,13 @@ __device__ __forceinline__ unsigned long long run_sum(const DraftParams& p, cons
         prob_vec<PF>(y[k], t);
         const int at = (g + 32 * k) * kVec;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) sum += at + e == skip ? 0ull : draft_weight(s[e], t[e]);
+        for (int e = 0; e < kVec; ++e) {
+          const DraftWeight w = draft_weight(at + e == skip ? 0.f : s[e], t[e]);
+          hi += w.hi;
+          lo += w.lo;
+        }
       }
+      sum += units_of(hi, lo);
     }
     i += groups * kVec;
   }
@@ -179,7 +201,8 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(const __gr
   __shared__ int s_n, s_refused;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int S = (int)cluster_size(), rank = (int)cluster_rank();
+  constexpr int S = kDraftCluster;
+  const int rank = (int)cluster_rank();
   const int b = blockIdx.x / S, T = p.window, V = p.vocab;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const long long pb = (long long)b * p.p_batch, qb = (long long)b * p.q_batch;
@@ -211,6 +234,7 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(const __gr
   }
   __syncthreads();
   const int n = s_n;
+  const float u = __ldg(p.uniforms + (long long)b * T + T - 1);
   DraftRow r;
   r.p0 = pb + n * p.p_token;
   r.q0 = qb + n * p.q_token;
@@ -234,13 +258,15 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(const __gr
     }
     if (threadIdx.x == 0) s_total = here;
     cluster_sync_all();
-    unsigned long long total = 0;
+    unsigned long long total = 0, theirs[kDraftCluster];  // (all on their way before the first is added)
     const uint32_t at = smem_addr(&s_total);
-    for (int k = 0; k < S; ++k) {
-      unsigned long long x;
-      asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(cluster_map(at, (uint32_t)k)) : "memory");
-      before += k < rank ? x : 0ull;
-      total += x;
+#pragma unroll
+    for (int k = 0; k < kDraftCluster; ++k)
+      asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(theirs[k]) : "r"(cluster_map(at, (uint32_t)k)) : "memory");
+#pragma unroll
+    for (int k = 0; k < kDraftCluster; ++k) {
+      before += k < rank ? theirs[k] : 0ull;
+      total += theirs[k];
     }
     cluster_sync_all();  // (nobody's shared memory is left or written while it is read)
     if (total == 0 && attempt == 0 && (r.q || r.without >= 0)) {
@@ -254,7 +280,6 @@ __global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(const __gr
       return;
     }
     // floor(total * u), u in units of 2^-24; 128-bit product
-    const float u = __ldg(p.uniforms + (long long)b * T + T - 1);
     const unsigned long long k = (unsigned long long)fminf(fmaxf(floorf(u * 0x1p24f), 0.f), 0x1p24f - 1.f);
     const unsigned long long target = (total * k) >> 24 | __umul64hi(total, k) << 40;
     if (target >= before && target - before < mine) {

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gqa_decode.h"
 #include "kernels/serving.h"
@@ -36,12 +37,8 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, in
 
 }  // namespace
 
-cudaError_t serving_setup() {
-  return cudaFuncSetAttribute(select_kv_kernel<kSelectThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectKeys * 4);
-}
-
 cudaError_t launch_verify_drafts(const DraftParams& p, int pf, int sms, cudaStream_t stream) {
-  const int S = 8;
+  constexpr int S = kDraftCluster;
   const dim3 grid((unsigned)(p.batch * S));
   switch (pf) {
     case kPF16: return launch(verify_drafts_kernel<kPF16>, grid, kDraftThreads, 0, S, stream, p);
@@ -50,23 +47,53 @@ cudaError_t launch_verify_drafts(const DraftParams& p, int pf, int sms, cudaStre
   }
 }
 
-template <int KVF, int QF>
-cudaError_t launch_score(const WeightParams& p, int q_len, cudaStream_t stream) {
-  const dim3 grid((unsigned)p.chunks, kHkv, (unsigned)p.c.batch);
-  return q_len <= 2 ? launch(score_kv_kernel<KVF, QF, 1>, grid, kScoreThreads, 0, 1, stream, p, q_len)
-                    : launch(score_kv_kernel<KVF, QF, 2>, grid, kScoreThreads, 0, 1, stream, p, q_len);
+// f(KVF, QF) as integral constants
+template <class F>
+cudaError_t with_formats(int kvf, int qf, const F& f) {
+  const auto of = [&](auto k) {
+    return qf == kQBF16 ? f(k, std::integral_constant<int, kQBF16>()) : f(k, std::integral_constant<int, kQF16>());
+  };
+  switch (kvf) {
+    case kKvF16: return f(std::integral_constant<int, kKvF16>(), std::integral_constant<int, kQF16>());
+    case kKvBF16: return f(std::integral_constant<int, kKvBF16>(), std::integral_constant<int, kQBF16>());
+    case kKvE4M3: return of(std::integral_constant<int, kKvE4M3>());
+    case kKvI8: return of(std::integral_constant<int, kKvI8>());
+    default: return of(std::integral_constant<int, kKvE2M1>());
+  }
 }
 
-cudaError_t launch_sum_weights(const WeightParams& p, int kvf, int qf, int q_len, cudaStream_t stream) {
-  const bool bf = qf == kQBF16;
-  cudaError_t e;
-  switch (kvf) {
-    case kKvF16: e = launch_score<kKvF16, kQF16>(p, q_len, stream); break;
-    case kKvBF16: e = launch_score<kKvBF16, kQBF16>(p, q_len, stream); break;
-    case kKvE4M3: e = bf ? launch_score<kKvE4M3, kQBF16>(p, q_len, stream) : launch_score<kKvE4M3, kQF16>(p, q_len, stream); break;
-    case kKvI8: e = bf ? launch_score<kKvI8, kQBF16>(p, q_len, stream) : launch_score<kKvI8, kQF16>(p, q_len, stream); break;
-    default: e = bf ? launch_score<kKvE2M1, kQBF16>(p, q_len, stream) : launch_score<kKvE2M1, kQF16>(p, q_len, stream);
+cudaError_t serving_setup() {
+  cudaError_t e = cudaFuncSetAttribute(select_kv_kernel<kSelectThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelectKeys * 4);
+  for (int kvf = kKvF16; kvf <= kKvE2M1 && e == cudaSuccess; ++kvf)
+    for (int qf = kQF16; qf <= kQBF16 && e == cudaSuccess; ++qf)
+      e = with_formats(kvf, qf, [](auto k, auto q) {
+        const cudaError_t x = cudaFuncSetAttribute(fused_weights_kernel<k(), q(), 1>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreBytes);
+        return x != cudaSuccess ? x : cudaFuncSetAttribute(fused_weights_kernel<k(), q(), 2>,
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreBytes);
+      });
+  return e;
+}
+
+cudaError_t launch_sum_weights(const WeightParams& params, int kvf, int qf, int q_len, int sms, cudaStream_t stream) {
+  WeightParams p = params;
+  // One launch where a cluster of 8 CTAs holds a row's scores and such clusters fill
+  // the GPU, or the rows are short (every CTA of a row then has a few slabs of slots).
+  const long long part = ((p.c.capacity + kRowCluster - 1LL) / kRowCluster + kSlab - 1) / kSlab * kSlab, bytes = part * 16 * q_len;
+  if (bytes <= kScoreBytes && ((long long)kRowCluster * kHkv * p.c.batch >= sms || p.c.capacity <= 8192)) {
+    p.held = (int)part;
+    return with_formats(kvf, qf, [&](auto k, auto q) {
+      return q_len <= 2 ? launch(fused_weights_kernel<k(), q(), 1>, dim3((unsigned)(kRowCluster * kHkv * p.c.batch)), kScoreThreads,
+                                 (size_t)bytes, kRowCluster, stream, p, q_len)
+                        : launch(fused_weights_kernel<k(), q(), 2>, dim3((unsigned)(kRowCluster * kHkv * p.c.batch)), kScoreThreads,
+                                 (size_t)bytes, kRowCluster, stream, p, q_len);
+    });
   }
+  const dim3 scores((unsigned)p.chunks, kHkv, (unsigned)p.c.batch);
+  const cudaError_t e = with_formats(kvf, qf, [&](auto k, auto q) {
+    return q_len <= 2 ? launch(score_kv_kernel<k(), q(), 1>, scores, kScoreThreads, 0, 1, stream, p, q_len)
+                      : launch(score_kv_kernel<k(), q(), 2>, scores, kScoreThreads, 0, 1, stream, p, q_len);
+  });
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)((p.c.capacity + kSumSlots - 1) / kSumSlots), kHkv, (unsigned)p.c.batch);
   switch (q_len) {
@@ -77,17 +104,25 @@ cudaError_t launch_sum_weights(const WeightParams& p, int kvf, int qf, int q_len
   }
 }
 
-cudaError_t launch_evict(const EvictParams& p, int kvf, cudaStream_t stream) {
-  // as many CTAs a head as hold its weights, 4096 each at least (each adds to the
-  // cluster barriers' time), 8 at most
-  int S = 1;
-  while (S < 8 && (p.src.capacity + S - 1) / S > 4096) S *= 2;
+cudaError_t launch_evict(const EvictParams& p, int kvf, int sms, cudaStream_t stream) {
   EvictParams e = p;
-  const long long seg = ((p.src.capacity + S - 1) / S + 31) / 32 * 32;
-  e.cluster = S;
-  e.held = seg <= kSelectKeys ? (int)seg : 0;
-  cudaError_t err = launch(select_kv_kernel<kSelectThreads>, dim3((unsigned)(p.batch * kHkv * S)), kSelectThreads, (size_t)e.held * 4, S,
-                           stream, e);
+  e.cluster = 1;
+  const int C = p.src.capacity;
+  cudaError_t err;
+  if (C <= kFewSlots) {
+    const auto few = [&](auto kernel) { return launch(kernel, dim3((unsigned)(p.batch * kHkv)), kFewThreads, 0, 1, stream, e); };
+    err = C <= kFewThreads ? few(select_few_kernel<1>) : C <= 4 * kFewThreads ? few(select_few_kernel<4>)
+          : C <= 8 * kFewThreads ? few(select_few_kernel<8>) : C <= 16 * kFewThreads ? few(select_few_kernel<16>)
+                                                             : few(select_few_kernel<32>);
+  } else {
+    // CTAs a head: one wave of them, 8 at most (each adds to the cluster's barriers and
+    // to the histograms that every one reads), as many as hold the weights if need be
+    while (e.cluster < 8 && (2LL * e.cluster * p.batch * kHkv <= sms || C > (long long)kSelectKeys * e.cluster)) e.cluster *= 2;
+    const long long seg = ((C + e.cluster - 1LL) / e.cluster + 31) / 32 * 32;
+    e.held = seg <= kSelectKeys ? (int)seg : 0;
+    err = launch(select_kv_kernel<kSelectThreads>, dim3((unsigned)(p.batch * kHkv * e.cluster)), kSelectThreads,
+                 (size_t)e.held * 4, e.cluster, stream, e);
+  }
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)((long long)p.batch * kHkv * 2 * p.chunks));
   switch (kvf) {
