@@ -784,6 +784,12 @@ def _cache_args(kv, block_table, paged, kv_scales, device):
 
 def _prefill(q, kv, block_table, paged, chunk_starts, sequence_lengths, q_scale, k_scale, v_scale, kv_scales, out,
              workspace):
+    native = _binding()
+    if native is not None:
+        done = native.prefill(_lib.address("gqa_prefill_paged" if paged else "gqa_prefill"), paged, q, kv, block_table,
+                              chunk_starts, sequence_lengths, out, kv_scales, workspace, q_scale, k_scale, v_scale)
+        if done is not None:
+            return _result(done)
     _require(q, "q", None, tuple(_QDT))
     if q.dim() != 3 or q.shape[1:] != (HQ, D):
         raise ValueError(f"q must be [tokens, {HQ}, {D}], got {tuple(q.shape)}")
@@ -858,6 +864,13 @@ def verify_drafts(probs, drafts, uniforms, draft_probs=None, sequence_lengths=No
     token, then -1; accepted int32 [batch], n).  sequence_lengths int32 [batch] (of a
     cache that holds all T) are shortened by the refused drafts, into out_lengths, or in
     place if that is None."""
+    native = _binding()
+    if native is not None:
+        done = native.drafts(_lib.address("gqa_verify_drafts"), probs, drafts, uniforms, draft_probs, sequence_lengths,
+                             out_lengths, tokens, accepted, workspace)
+        if done is not None:
+            _lib.check(done)
+            return tokens, accepted
     if not isinstance(probs, torch.Tensor):
         raise TypeError("probs must be a torch.Tensor")
     if not probs.is_cuda or probs.dim() != 3 or probs.dtype not in _PROB:
@@ -898,6 +911,12 @@ def verify_drafts(probs, drafts, uniforms, draft_probs=None, sequence_lengths=No
 
 
 def _accumulate(q, kv, block_table, paged, sequence_lengths, weights, q_scale, k_scale, kv_scales, add, workspace):
+    native = _binding()
+    if native is not None:
+        done = native.weights(_lib.address("gqa_accumulate_weights_paged" if paged else "gqa_accumulate_weights"), paged, q,
+                              kv, block_table, sequence_lengths, weights, kv_scales, workspace, q_scale, k_scale, add)
+        if done is not None:
+            return _result(done)
     _require(q, "q", None, tuple(_QDT))
     if q.dim() == 3 and q.shape[1:] == (HQ, D):
         T = 1
@@ -944,6 +963,13 @@ def accumulate_weights_paged(q, kv_pages, block_table, sequence_lengths, weights
 
 def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, first, out, out_scales, out_table,
            out_lengths, out_weights, kept, kv_scales, workspace):
+    native = _binding()
+    if native is not None:
+        done = native.evict(_lib.address("gqa_evict_kv_paged" if paged else "gqa_evict_kv"), paged, kv, block_table,
+                            sequence_lengths, weights, keep, recent, first, out, out_scales, out_table, out_lengths,
+                            out_weights, kept, kv_scales, workspace)
+        if done is not None:
+            return _result(done)
     _require(kv, "kv_pages" if paged else "kv", None, tuple(_KVF))
     dev = kv.device
     kvf, sc, B, C = _cache_args(kv, block_table, paged, kv_scales, dev)

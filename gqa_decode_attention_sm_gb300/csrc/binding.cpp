@@ -1,6 +1,7 @@
 // Native binding of the cache write and read-back calls, and of gqa_decode_fp4kv,
 // gqa_decode_verify and gqa_decode_paged (caches of every format) and a prepared
-// 4-bit launch with everything given (output, split count, workspace): the argument
+// 4-bit launch with everything given (output, split count, workspace), and of the prompt
+// attention, the draft verification, the weight sums and the eviction: the argument
 // checks and the call of the C ABI without the interpreter between them (writing 256
 // tokens costs the host 4 us a call so, 16 us through ctypes).
 //
@@ -11,6 +12,7 @@
 // tensor, or the C call's status if that is not GQA_OK.  No C++ exception leaves
 // a function.
 #include <Python.h>
+#include <climits>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -306,6 +308,230 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n_args) {
   return st == GQA_OK ? Py_NewRef(a[6]) : PyLong_FromLong(st);
 }
 
+// The block table of a paged call: int32 [batch, pages], or [any, pages] for batch < 0.
+const at::Tensor* table_of(PyObject* o, c10::Device dev, int64_t batch) {
+  const at::Tensor* t = dense(o, dev, at::kInt);
+  return t && t->dim() == 2 && (batch < 0 || t->size(0) == batch) && fits(t->size(0)) && fits(t->size(1)) ? t : nullptr;
+}
+int32_t* i32(const at::Tensor* t) { return t ? static_cast<int32_t*>(t->data_ptr()) : nullptr; }
+float* f32(const at::Tensor* t) { return t ? static_cast<float*>(t->data_ptr()) : nullptr; }
+
+// prefill(address, paged, q, kv, block_table, chunk_starts, sequence_lengths, out,
+//         kv_scales, workspace, q_scale, k_scale, v_scale)
+PyObject* prefill(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 13 || a[7] == Py_None || a[9] == Py_None) return nullptr;
+  void* fn = PyLong_AsVoidPtr(a[0]);
+  const bool paged = a[1] == Py_True;
+  const at::Tensor* q = plain(a[2]);
+  int dtype;
+  Cache c;
+  if (!fn || !q || q->dim() != 3 || q->size(1) != kHq || q->size(2) != kD || !half_type(q->scalar_type(), &dtype) ||
+      !q->is_contiguous() || !fits(q->size(0)))
+    return nullptr;
+  const c10::Device dev = q->device();
+  if (!cache_of(a[3], a[8], c) || c.dev != dev || !fits(c.units) || !fits(c.rows) ||
+      c10::cuda::current_device() != dev.index())
+    return nullptr;
+  const at::Tensor* table = paged ? table_of(a[4], dev, -1) : nullptr;
+  if (paged && !table) return nullptr;
+  const int64_t batch = paged ? table->size(0) : c.units;
+  const at::Tensor *starts = dense(a[5], dev, at::kInt, {batch + 1}), *lens = dense(a[6], dev, at::kInt, {batch}),
+                   *out = dense(a[7], dev, q->scalar_type(), q->sizes());
+  float q_scale, k_scale, v_scale;
+  void* ws;
+  size_t ws_bytes;
+  if (!starts || !lens || !out || !workspace_of(a[9], dev, &ws, &ws_bytes) || !as_float(a[10], &q_scale) ||
+      !as_float(a[11], &k_scale) || !as_float(a[12], &v_scale))
+    return nullptr;
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  const auto dt = static_cast<gqa_dtype_t>(dtype);
+  const auto fmt = static_cast<gqa_kv_format_t>(c.format);
+  const void* const qp = q->data_ptr();
+  void* const to = out->data_ptr();
+  const int tokens = (int)q->size(0);
+  gqa_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  if (paged)
+    st = reinterpret_cast<decltype(&gqa_prefill_paged)>(fn)(
+        qp, dt, c.kv, fmt, c.scales, i32(table), (int)table->size(1), (int)c.units, (int)c.rows, i32(starts), i32(lens), to,
+        tokens, (int)batch, q_scale, k_scale, v_scale, ws, ws_bytes, stream);
+  else
+    st = reinterpret_cast<decltype(&gqa_prefill)>(fn)(qp, dt, c.kv, fmt, c.scales, i32(starts), i32(lens), to, tokens,
+                                                      (int)batch, (int)c.rows, q_scale, k_scale, v_scale, ws, ws_bytes,
+                                                      stream);
+  Py_END_ALLOW_THREADS;
+  return st == GQA_OK ? Py_NewRef(a[7]) : PyLong_FromLong(st);
+}
+
+// Probabilities [batch, rows, vocab] whose rows may lie apart.
+bool probs_of(PyObject* o, c10::Device dev, at::ScalarType type, int64_t batch, int64_t rows, int64_t vocab,
+              const void** ptr, int64_t* batch_stride, int64_t* row_stride) {
+  const at::Tensor* t = plain(o);
+  if (!t || t->device() != dev || t->scalar_type() != type || t->dim() != 3 || t->size(0) != batch ||
+      t->size(1) != rows || t->size(2) != vocab || (vocab > 1 && t->stride(2) != 1))
+    return false;
+  *ptr = t->data_ptr();
+  *row_stride = rows > 1 ? t->stride(1) : vocab;  // (a dimension of one row has no stride of its own)
+  *batch_stride = batch > 1 ? t->stride(0) : rows * *row_stride;
+  return true;
+}
+
+// drafts(address, probs, drafts, uniforms, draft_probs, sequence_lengths, out_lengths,
+//        tokens, accepted, workspace)
+PyObject* drafts(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 10 || a[7] == Py_None || a[8] == Py_None) return nullptr;
+  void* fn = PyLong_AsVoidPtr(a[0]);
+  const at::Tensor* p = plain(a[1]);
+  if (!fn || !p || p->dim() != 3) return nullptr;
+  const at::ScalarType type = p->scalar_type();
+  if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16) return nullptr;
+  const int64_t batch = p->size(0), window = p->size(1), vocab = p->size(2);
+  const c10::Device dev = p->device();
+  if (batch < 1 || window < 1 || vocab < 1 || !fits(batch) || !fits(window) || !fits(vocab) ||
+      c10::cuda::current_device() != dev.index())
+    return nullptr;
+  const void *pp, *qp = nullptr;
+  int64_t ps[2], qs[2] = {0, 0};
+  if (!probs_of(a[1], dev, type, batch, window, vocab, &pp, &ps[0], &ps[1])) return nullptr;
+  if (a[4] != Py_None && !probs_of(a[4], dev, type, batch, window - 1, vocab, &qp, &qs[0], &qs[1])) return nullptr;
+  const at::Tensor *d = dense(a[2], dev, at::kInt, {batch, window - 1}), *u = dense(a[3], dev, at::kFloat, {batch, window}),
+                   *tokens = dense(a[7], dev, at::kInt, {batch, window}), *accepted = dense(a[8], dev, at::kInt, {batch});
+  const at::Tensor *lens = nullptr, *new_lens = nullptr;
+  if (a[5] != Py_None) {
+    lens = dense(a[5], dev, at::kInt, {batch});
+    new_lens = a[6] == Py_None ? lens : dense(a[6], dev, at::kInt, {batch});
+    if (!lens || !new_lens) return nullptr;
+  } else if (a[6] != Py_None) {
+    return nullptr;
+  }
+  void* ws;
+  size_t ws_bytes;
+  if (!d || !u || !tokens || !accepted || !workspace_of(a[9], dev, &ws, &ws_bytes)) return nullptr;
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  const gqa_prob_t pt = type == at::kFloat ? GQA_PROB_F32 : type == at::kHalf ? GQA_PROB_F16 : GQA_PROB_BF16;
+  gqa_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  st = reinterpret_cast<decltype(&gqa_verify_drafts)>(fn)(
+      pp, ps[0], ps[1], window > 1 ? qp : nullptr, qs[0], qs[1], pt, window > 1 ? i32(d) : nullptr, f32(u), i32(lens),
+      i32(new_lens), i32(tokens), i32(accepted), (int)batch, (int)window, (int)vocab, ws, ws_bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return PyLong_FromLong(st);
+}
+
+// weights(address, paged, q, kv, block_table, sequence_lengths, weights, kv_scales,
+//         workspace, q_scale, k_scale, add)
+PyObject* weights(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 12 || a[8] == Py_None) return nullptr;
+  void* fn = PyLong_AsVoidPtr(a[0]);
+  const bool paged = a[1] == Py_True;
+  const at::Tensor* q = plain(a[2]);
+  int dtype;
+  if (!fn || !q || (q->dim() != 3 && q->dim() != 4) || q->size(-2) != kHq || q->size(-1) != kD ||
+      !half_type(q->scalar_type(), &dtype) || !q->is_contiguous())
+    return nullptr;
+  const int64_t batch = q->size(0), q_len = q->dim() == 4 ? q->size(1) : 1;
+  const c10::Device dev = q->device();
+  Cache c;
+  if (!fits(batch) || q_len < 1 || q_len > 4 || !cache_of(a[3], a[7], c) || c.dev != dev || !fits(c.units) ||
+      !fits(c.rows) || c10::cuda::current_device() != dev.index())
+    return nullptr;
+  const at::Tensor* table = paged ? table_of(a[4], dev, batch) : nullptr;
+  if (paged ? !table : c.units != batch) return nullptr;
+  const int64_t capacity = paged ? table->size(1) * c.rows : c.rows;
+  const at::Tensor *lens = dense(a[5], dev, at::kInt, {batch}), *w = dense(a[6], dev, at::kFloat, {batch, kHkv, capacity});
+  float q_scale, k_scale;
+  void* ws;
+  size_t ws_bytes;
+  const int add = PyObject_IsTrue(a[11]);
+  if (!lens || !w || add < 0 || !workspace_of(a[8], dev, &ws, &ws_bytes) || !as_float(a[9], &q_scale) ||
+      !as_float(a[10], &k_scale))
+    return nullptr;
+  void* const stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  const auto dt = static_cast<gqa_dtype_t>(dtype);
+  const auto fmt = static_cast<gqa_kv_format_t>(c.format);
+  const void* const qp = q->data_ptr();
+  gqa_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  if (paged)
+    st = reinterpret_cast<decltype(&gqa_accumulate_weights_paged)>(fn)(
+        qp, dt, c.kv, fmt, c.scales, i32(table), (int)table->size(1), (int)c.units, (int)c.rows, i32(lens), f32(w),
+        (int)batch, (int)q_len, q_scale, k_scale, add, ws, ws_bytes, stream);
+  else
+    st = reinterpret_cast<decltype(&gqa_accumulate_weights)>(fn)(qp, dt, c.kv, fmt, c.scales, i32(lens), f32(w), (int)batch,
+                                                                 (int)c.rows, (int)q_len, q_scale, k_scale, add, ws,
+                                                                 ws_bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return st == GQA_OK ? Py_NewRef(a[6]) : PyLong_FromLong(st);
+}
+
+bool as_int(PyObject* o, int* x) {
+  const long v = PyLong_Check(o) ? PyLong_AsLong(o) : LONG_MIN;
+  if (v < INT32_MIN || v > INT32_MAX) {
+    PyErr_Clear();
+    return false;
+  }
+  *x = (int)v;
+  return true;
+}
+
+// evict(address, paged, kv, block_table, sequence_lengths, weights, keep, recent, first,
+//       out, out_scales, out_table, out_lengths, out_weights, kept, kv_scales, workspace)
+PyObject* evict(PyObject* const* a, Py_ssize_t n_args) {
+  if (n_args != 17 || a[14] == Py_None || a[16] == Py_None) return nullptr;
+  void* fn = PyLong_AsVoidPtr(a[0]);
+  const bool paged = a[1] == Py_True;
+  Cache c, o;
+  int keep, recent, first;
+  if (!fn || !cache_of(a[2], a[15], c) || !fits(c.units) || !fits(c.rows) ||
+      c10::cuda::current_device() != c.dev.index() || !as_int(a[6], &keep) || !as_int(a[7], &recent) ||
+      !as_int(a[8], &first) || keep < 1)
+    return nullptr;
+  const at::Tensor* table = paged ? table_of(a[3], c.dev, -1) : nullptr;
+  if (paged && !table) return nullptr;
+  const int64_t batch = paged ? table->size(0) : c.units, capacity = paged ? table->size(1) * c.rows : c.rows;
+  const bool moved = paged ? a[11] != Py_None : a[9] != Py_None;  // else in place
+  const at::Tensor *lens = dense(a[4], c.dev, at::kInt, {batch}), *w = dense(a[5], c.dev, at::kFloat, {batch, kHkv, capacity}),
+                   *kept = dense(a[14], c.dev, at::kInt, {batch, kHkv, keep}), *out_table = nullptr, *out_lens = nullptr,
+                   *out_w = nullptr;
+  if (!lens || !w || !kept) return nullptr;
+  if (moved) {
+    if (paged) {
+      if (!(out_table = table_of(a[11], c.dev, batch))) return nullptr;
+    } else if (!cache_of(a[9], a[10], o) || o.dev != c.dev || o.format != c.format || o.units != batch || !fits(o.rows) ||
+               THPVariable_Unpack(a[9]).scalar_type() != THPVariable_Unpack(a[2]).scalar_type()) {
+      return nullptr;
+    }
+    if (!(out_lens = dense(a[12], c.dev, at::kInt, {batch}))) return nullptr;
+    if (a[13] != Py_None) {
+      out_w = dense(a[13], c.dev, at::kFloat);
+      if (!out_w || out_w->dim() != 3 || out_w->size(0) != batch || out_w->size(1) != kHkv || !fits(out_w->size(2)))
+        return nullptr;
+    }
+  } else if (a[10] != Py_None || a[12] != Py_None || a[13] != Py_None) {
+    return nullptr;
+  }
+  void* ws;
+  size_t ws_bytes;
+  if (!workspace_of(a[16], c.dev, &ws, &ws_bytes)) return nullptr;
+  void* const stream = c10::cuda::getCurrentCUDAStream(c.dev.index()).stream();
+  const auto fmt = static_cast<gqa_kv_format_t>(c.format);
+  const int wcap = out_w ? (int)out_w->size(2) : 0;
+  gqa_status_t st;
+  Py_BEGIN_ALLOW_THREADS;
+  if (paged)
+    st = reinterpret_cast<decltype(&gqa_evict_kv_paged)>(fn)(
+        c.kv, fmt, const_cast<void*>(c.scales), i32(table), (int)table->size(1), (int)c.units, (int)c.rows, i32(lens), f32(w),
+        i32(out_table), out_table ? (int)out_table->size(1) : 0, i32(out_lens), f32(out_w), i32(kept), (int)batch, wcap, keep,
+        recent, first, ws, ws_bytes, stream);
+  else
+    st = reinterpret_cast<decltype(&gqa_evict_kv)>(fn)(c.kv, fmt, const_cast<void*>(c.scales), i32(lens), f32(w), o.kv,
+                                                       const_cast<void*>(o.scales), i32(out_lens), f32(out_w), i32(kept),
+                                                       (int)batch, (int)c.rows, (int)o.rows, wcap, keep, recent, first, ws,
+                                                       ws_bytes, stream);
+  Py_END_ALLOW_THREADS;
+  return st == GQA_OK ? Py_NewRef(a[14]) : PyLong_FromLong(st);
+}
+
 // Runs f; None where it does not judge its arguments or something threw.
 template <PyObject* (*f)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -323,6 +549,10 @@ PyMethodDef kMethods[] = {
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<attend>)), METH_FASTCALL, nullptr},
     {"write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<write>)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<read>)), METH_FASTCALL, nullptr},
+    {"prefill", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<prefill>)), METH_FASTCALL, nullptr},
+    {"drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<drafts>)), METH_FASTCALL, nullptr},
+    {"weights", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<weights>)), METH_FASTCALL, nullptr},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<evict>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -5,8 +5,9 @@
 // A head's threshold is its k-th largest weight, of the weights' order-preserving
 // integers.  select_few_kernel (up to 32768 slots) holds a head's weights in one CTA's
 // registers and finds the threshold bit by bit, counting the weights that are no
-// smaller: about 80 cycles a bit besides a compare a weight, where a histogram's atomics
-// meet in the few bins that softmax weights lie in (32 x 8192: 25 us with histograms).
+// smaller, from the first bit in which the least and the largest differ, of all of them
+// until 2048 are left and then of those.  (A bit of K weights a thread takes about 200 +
+// 70 K cycles.  Histograms' atomics meet in the few bins that softmax weights lie in.)
 // select_kv_kernel takes more: 11, 11 and 10 bits at a time, a histogram each, by a
 // cluster of CTAs that hold their parts of the weights in shared memory; histograms and
 // counts meet in distributed shared memory.  Both then write the kept slots in ascending
@@ -27,6 +28,7 @@ namespace gqa {
 
 constexpr int kFewThreads = 1024;
 constexpr int kFewSlots = 32 * kFewThreads;
+constexpr int kFewList = 2 * kFewThreads;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectKeys = 48 * 1024;  // weights that a CTA holds in shared memory (192 KB)
 constexpr int kMoveThreads = 256;
@@ -95,7 +97,7 @@ __device__ __forceinline__ int select_begin(const EvictParams& p, int unit, int 
 template <int K>
 __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kFewThreads / 32;
-  __shared__ uint32_t s_count[3], s_above[kWarps], s_equal[kWarps];
+  __shared__ uint32_t s_count[3], s_above[kWarps], s_equal[kWarps], s_list[kFewList], s_listed;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int unit = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -112,14 +114,12 @@ __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_co
     if (at + 32 * i < hi) x[i] = weight_key(__ldg(in_buffer(w + at + 32 * i, 4, p.weights, extent, p.flags)));
   }
   if (tid < 3) s_count[tid] = 0u;
+  if (tid == 0) s_listed = 0u;
   __syncthreads();
-  // The number of weights at or above `least`, which is not 0.  Three counters by turns:
+  // The number of the thread's weights, summed over the block.  Three counters by turns:
   // the next call's, read two calls ago, is cleared while this one's is added to.
   int turn = 0;
-  const auto count = [&](uint32_t least) {
-    uint32_t n = 0;
-#pragma unroll
-    for (int i = 0; i < K; ++i) n += x[i] >= least;
+  const auto total = [&](uint32_t n) {
     n = __reduce_add_sync(0xffffffffu, n);
     const int next = turn == 2 ? 0 : turn + 1;
     if (lane == 0 && n) atomicAdd(&s_count[turn], n);
@@ -129,23 +129,82 @@ __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_co
     turn = next;
     return n;
   };
-  // kept: above `threshold`, and the first `equal_needed` equal to it
-  uint32_t need = (uint32_t)(p.keep - p.first - p.recent), threshold = 0u;
-  if (need == 0) {
-    threshold = 0xffffffffu;  // (no weight's key)
-  } else {
-    bool exact = false;
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
-      const uint32_t least = threshold | 1u << bit;
-      const uint32_t n = count(least);
-      if (n >= need) threshold = least;
-      exact = n == need;
+  const auto count = [&](uint32_t least) {  // weights at or above it, which is not 0
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) n += x[i] >= least;
+    return total(n);
+  };
+  // kept: above `threshold`, and the first `need` equal to it
+  uint32_t need = (uint32_t)(p.keep - p.first - p.recent), threshold = 0xffffffffu;  // (no weight's key)
+  if (need > 0) {
+    // the least and the largest weight: the bits before they differ are known
+    uint32_t most = 0u, least = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      most = max(most, x[i]);
+      least = min(least, x[i] == 0u ? 0xffffffffu : x[i]);
     }
-    if (exact) {
-      threshold -= 1u;  // all at or above it, as many as needed
-      need = 0u;
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+      s_above[warp] = most;
+      s_equal[warp] = least;
+    }
+    __syncthreads();
+    most = __reduce_max_sync(0xffffffffu, s_above[lane % kWarps]);
+    least = __reduce_min_sync(0xffffffffu, s_equal[lane % kWarps]);
+    __syncthreads();
+    uint32_t upto = most == 0u ? 0u : count(least);  // weights at or above t
+    if (upto < need) {                               // NaN among the kept
+      threshold = 0u;
+      need -= upto;
     } else {
-      need -= count(threshold + 1u);
+      int bit = least == most ? -1 : 31 - __clz(least ^ most);
+      // weights of the interval [t, t + 2^(bit + 1)), which holds the threshold, lie below
+      // `upto` and above `over` in order
+      uint32_t t = bit < 0 ? least : least & ~((2u << bit) - 1u), over = 0u;
+      bool exact = upto == need;
+      while (bit >= 0 && !exact && upto - over > kFewList) {
+        const uint32_t middle = t | 1u << bit;
+        const uint32_t n = count(middle);
+        if (n >= need) {
+          t = middle;
+          upto = n;
+        } else {
+          over = n;
+        }
+        exact = n == need;
+        --bit;
+      }
+      if (bit >= 0 && !exact) {
+        // few are left in it: listed, two a thread
+        const uint32_t width = (2u << bit) - 1u;
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (x[i] != 0u && x[i] - t <= width) {
+            const uint32_t to = atomicAdd(&s_listed, 1u);
+            if (to < kFewList) s_list[to] = x[i];
+          }
+        __syncthreads();
+        const uint32_t listed = min(s_listed, (uint32_t)kFewList);
+        const uint32_t y0 = tid < listed ? s_list[tid] : 0u, y1 = tid + kFewThreads < listed ? s_list[tid + kFewThreads] : 0u;
+        const uint32_t outside = over;
+        for (; bit >= 0 && !exact; --bit) {
+          const uint32_t middle = t | 1u << bit;
+          const uint32_t n = outside + total((y0 >= middle) + (y1 >= middle));
+          if (n >= need) {
+            t = middle;
+            upto = n;
+          } else {
+            over = n;
+          }
+          exact = n == need;
+        }
+      }
+      // exact: as many as needed at or above t
+      threshold = exact ? t - 1u : t;
+      need = exact ? 0u : need - over;
     }
   }
   uint32_t above = 0, equal = 0;

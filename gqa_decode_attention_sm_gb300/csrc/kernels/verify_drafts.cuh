@@ -21,7 +21,7 @@
 
 namespace gqa {
 
-constexpr int kDraftThreads = 512;
+constexpr int kDraftThreads = 256;  // (four CTAs an SM at 64 registers: 64 requests are one wave)
 constexpr int kDraftCluster = 8;  // CTAs a request
 constexpr int kDraftWarps = kDraftThreads / 32;
 constexpr int kMaxWindow = 32;  // a warp's lanes judge a window's drafts at once
@@ -196,7 +196,7 @@ __device__ __forceinline__ int find_token(const DraftParams& p, const DraftRow& 
 }
 
 template <int PF>
-__global__ void __launch_bounds__(kDraftThreads) verify_drafts_kernel(const __grid_constant__ DraftParams p) {
+__global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const __grid_constant__ DraftParams p) {
   __shared__ unsigned long long s_warp[kDraftWarps], s_total;
   __shared__ int s_n, s_refused;
   pdl_launch_dependents();
