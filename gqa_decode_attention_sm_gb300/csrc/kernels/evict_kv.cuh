@@ -3,19 +3,21 @@
 // all, each KV head choosing for itself; they move in their order to slots 0, 1, ...
 //
 // A head's threshold is its k-th largest weight, of the weights' order-preserving
-// integers.  select_few_kernel (up to 32768 slots) holds a head's weights in one CTA's
+// integers.  select_few_kernel (up to 8192 slots) holds a head's weights in one CTA's
 // registers and finds the threshold bit by bit, counting the weights that are no
 // smaller, from the first bit in which the least and the largest differ, of all of them
-// until 2048 are left and then of those.  (A bit of K weights a thread takes about 200 +
-// 70 K cycles.  Histograms' atomics meet in the few bins that softmax weights lie in.)
+// until 2048 are left and then of those.  (Histograms' atomics meet in the few bins that
+// softmax weights lie in: 32 x 8192 took 25 us with them; 8 x 32768, a head in one CTA's
+// registers, 36 us against 22 by a cluster of two.)
 // select_kv_kernel takes more: 11, 11 and 10 bits at a time, a histogram each, by a
 // cluster of CTAs that hold their parts of the weights in shared memory; histograms and
 // counts meet in distributed shared memory.  Both then write the kept slots in ascending
 // order by a prefix sum of "above the threshold, or equal to it and among the first
 // such".  Everything counted is whole numbers, so the result does not depend on any order.
 //
-// move_kv_kernel gathers the rows (and their scales and weights), 16 KB a CTA.  Bound
-// by HBM.  In place a CTA may overwrite rows that another has yet to read: the CTAs
+// move_kv_kernel gathers the rows (and their scales and weights), 8 KB a CTA (both
+// kernels, 8 x U[16k, 32k] to 8192 bf16 tokens: 112 us; 16 KB 119, 128 threads 116).
+// Bound by HBM: 537 MB moved, 0.80 of the copy rate.  In place a CTA may overwrite rows that another has yet to read: the CTAs
 // take their chunks by ticket in ascending order, say when theirs is read and write
 // once all chunks before it have been read.  Reading waits for nothing and a later
 // chunk's rows lie behind every row that an earlier one writes, so no wait can last
@@ -26,13 +28,13 @@
 
 namespace gqa {
 
-constexpr int kFewThreads = 1024;
-constexpr int kFewSlots = 32 * kFewThreads;
-constexpr int kFewList = 2 * kFewThreads;
+constexpr int kFewThreads = 512;
+constexpr int kFewSlots = 16 * kFewThreads;
+constexpr int kFewList = 2048;
 constexpr int kSelectBins = 2048;
 constexpr int kSelectKeys = 48 * 1024;  // weights that a CTA holds in shared memory (192 KB)
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 16384;  // of rows that a CTA moves
+constexpr int kMoveBytes = 8192;  // of rows that a CTA moves
 
 __host__ __device__ constexpr int move_rows(int kv_format) { return kMoveBytes / kv_row_bytes(kv_format); }
 
@@ -95,9 +97,10 @@ __device__ __forceinline__ int select_begin(const EvictParams& p, int unit, int 
 
 // K weights a thread: warp w has K * 32 consecutive slots, 32 at a time.
 template <int K>
-__global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const __grid_constant__ EvictParams p) {
   constexpr int kWarps = kFewThreads / 32;
-  __shared__ uint32_t s_count[3], s_above[kWarps], s_equal[kWarps], s_list[kFewList], s_listed;
+  static_assert(kWarps <= 32, "a lane adds a warp's count");
+  __shared__ uint32_t s_count[2][kWarps], s_above[kWarps], s_equal[kWarps], s_list[kFewList], s_listed;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int unit = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid & 31;
@@ -108,25 +111,27 @@ __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_co
   const size_t extent = (size_t)p.batch * kHkv * p.src.capacity * 4;
   uint32_t x[K];  // 0 (no weight but NaN) where there is no slot: never counted, its index is looked at
   const int at = lo + warp * 32 * K + lane;
+  if (!kChecked && lo + (warp + 1) * 32 * K <= hi) {  // the warp's slots are all there: one address, loads side by side
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    x[i] = 0u;
-    if (at + 32 * i < hi) x[i] = weight_key(__ldg(in_buffer(w + at + 32 * i, 4, p.weights, extent, p.flags)));
+    for (int i = 0; i < K; ++i) x[i] = __float_as_uint(__ldg(w + at + 32 * i));
+#pragma unroll
+    for (int i = 0; i < K; ++i) x[i] = weight_key(__uint_as_float(x[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      x[i] = at + 32 * i < hi ? weight_key(__ldg(in_buffer(w + at + 32 * i, 4, p.weights, extent, p.flags))) : 0u;
   }
-  if (tid < 3) s_count[tid] = 0u;
   if (tid == 0) s_listed = 0u;
   __syncthreads();
-  // The number of the thread's weights, summed over the block.  Three counters by turns:
-  // the next call's, read two calls ago, is cleared while this one's is added to.
+  // The sum of the threads' numbers, by two buffers in turn (one is read before the
+  // barrier after which it is written again).
   int turn = 0;
   const auto total = [&](uint32_t n) {
     n = __reduce_add_sync(0xffffffffu, n);
-    const int next = turn == 2 ? 0 : turn + 1;
-    if (lane == 0 && n) atomicAdd(&s_count[turn], n);
-    if (tid == 0) s_count[next] = 0u;
+    if (lane == 0) s_count[turn][warp] = n;
     __syncthreads();
-    n = s_count[turn];
-    turn = next;
+    n = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_count[turn][lane] : 0u);
+    turn ^= 1;
     return n;
   };
   const auto count = [&](uint32_t least) {  // weights at or above it, which is not 0
@@ -187,32 +192,54 @@ __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_co
             if (to < kFewList) s_list[to] = x[i];
           }
         __syncthreads();
-        const uint32_t listed = min(s_listed, (uint32_t)kFewList);
-        const uint32_t y0 = tid < listed ? s_list[tid] : 0u, y1 = tid + kFewThreads < listed ? s_list[tid + kFewThreads] : 0u;
-        const uint32_t outside = over;
-        for (; bit >= 0 && !exact; --bit) {
-          const uint32_t middle = t | 1u << bit;
-          const uint32_t n = outside + total((y0 >= middle) + (y1 >= middle));
-          if (n >= need) {
-            t = middle;
-            upto = n;
-          } else {
-            over = n;
+        // by the first eight warps, whose barrier is shorter
+        constexpr int kListThreads = 256, kEach = kFewList / kListThreads;
+        if (tid < kListThreads) {
+          const uint32_t listed = min(s_listed, (uint32_t)kFewList), outside = over;
+          uint32_t y[kEach];
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) y[i] = tid + kListThreads * i < listed ? s_list[tid + kListThreads * i] : 0u;
+          for (; bit >= 0 && !exact; --bit) {
+            const uint32_t middle = t | 1u << bit;
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) n += y[i] >= middle;
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) s_count[turn][warp] = n;
+            named_barrier_sync(1, kListThreads);
+            n = outside + __reduce_add_sync(0xffffffffu, lane < kListThreads / 32 ? s_count[turn][lane] : 0u);
+            turn ^= 1;
+            if (n >= need) t = middle;
+            else over = n;
+            exact = n == need;
           }
-          exact = n == need;
+          if (tid == 0) {
+            s_above[0] = t;
+            s_above[1] = over;
+            s_above[2] = exact;
+          }
         }
+        __syncthreads();
+        t = s_above[0];
+        over = s_above[1];
+        exact = s_above[2] != 0u;
+        __syncthreads();
       }
       // exact: as many as needed at or above t
       threshold = exact ? t - 1u : t;
       need = exact ? 0u : need - over;
     }
   }
+  // how many lie above and on the threshold before each warp's slots (where there is no
+  // slot x is 0, which is on a threshold of 0 only)
   uint32_t above = 0, equal = 0;
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const bool in = at + 32 * i < hi;
-    above += __popc(__ballot_sync(0xffffffffu, in && x[i] > threshold));
-    equal += __popc(__ballot_sync(0xffffffffu, in && x[i] == threshold));
+  for (int i = 0; i < K; ++i) above += x[i] > threshold;
+  above = __reduce_add_sync(0xffffffffu, above);
+  if (need > 0) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) equal += x[i] == threshold && at + 32 * i < hi;
+    equal = __reduce_add_sync(0xffffffffu, equal);
   }
   if (lane == 0) {
     s_above[warp] = above;
@@ -222,19 +249,22 @@ __global__ void __launch_bounds__(kFewThreads) select_few_kernel(const __grid_co
   // before this warp: lane k has warp k's
   above = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane % kWarps] : 0u);
   equal = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane % kWarps] : 0u);
+  above += min(equal, need);  // those on the threshold that the warps before keep
   int32_t* kept = p.kept + (size_t)unit * p.keep;
+  const uint32_t before = (1u << lane) - 1;
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const bool in = at + 32 * i < hi;
-    const uint32_t gt = __ballot_sync(0xffffffffu, in && x[i] > threshold);
-    const uint32_t eq = __ballot_sync(0xffffffffu, in && x[i] == threshold);
-    const uint32_t before = (1u << lane) - 1, rank = equal + __popc(eq & before);
-    if (in && (x[i] > threshold || (x[i] == threshold && rank < need))) {
-      const uint32_t to = (uint32_t)p.first + above + __popc(gt & before) + min(rank, need);
+    uint32_t chosen = __ballot_sync(0xffffffffu, x[i] > threshold);
+    if (need > 0) {  // and of those on the threshold the first ones
+      const uint32_t eq = __ballot_sync(0xffffffffu, x[i] == threshold && at + 32 * i < hi);
+      chosen |= __ballot_sync(0xffffffffu, (eq >> lane & 1) && equal + __popc(eq & before) < need);
+      equal += __popc(eq);
+    }
+    if (chosen >> lane & 1) {
+      const uint32_t to = (uint32_t)p.first + above + __popc(chosen & before);
       if (to < (uint32_t)p.keep) kept[to] = at + 32 * i;  // (always; every address here is held in bounds)
     }
-    above += __popc(gt);
-    equal += __popc(eq);
+    above += __popc(chosen);
   }
 }
 

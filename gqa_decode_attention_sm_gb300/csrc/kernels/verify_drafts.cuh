@@ -168,7 +168,8 @@ __device__ __forceinline__ unsigned long long run_sum(const DraftParams& p, cons
   return sum;
 }
 
-// The first token of [lo, hi) whose running sum passes `target` (the warp's; one is there).
+// The first token of [lo, hi) whose running sum passes `target` (the warp's; one is
+// there): the 32 tokens that hold it by their sums, then the token among them.
 template <int PF>
 __device__ __forceinline__ int find_token(const DraftParams& p, const DraftRow& r, int lo, int hi,
                                           unsigned long long target) {
@@ -176,20 +177,27 @@ __device__ __forceinline__ int find_token(const DraftParams& p, const DraftRow& 
   unsigned long long before = 0;
   constexpr int kDeep = 8;
   for (int i = lo; i < hi; i += 32 * kDeep) {
-    unsigned long long w[kDeep];
-#pragma unroll
-    for (int k = 0; k < kDeep; ++k) w[k] = i + 32 * k + lane < hi ? token_weight<PF>(p, r, i + 32 * k + lane) : 0ull;
+    DraftWeight w[kDeep];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-      unsigned long long upto = w[k];
+      const int at = min(i + 32 * k + lane, hi - 1);
+      const float a = prob_at<PF>(p.probs, r.p0 + at, p, p.p_bytes);
+      const float b = r.q ? prob_at<PF>(p.draft_probs, r.q0 + at, p, p.q_bytes) : 0.f;
+      w[k] = draft_weight(at == r.without || i + 32 * k + lane >= hi ? 0.f : a, b);
+    }
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
+    for (int k = 0; k < kDeep; ++k) {
+      const unsigned long long all = units_of(__reduce_add_sync(0xffffffffu, w[k].hi), __reduce_add_sync(0xffffffffu, w[k].lo));
+      if (before + all > target) {
+        unsigned long long upto = units_of(w[k].hi, w[k].lo);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        return i + 32 * k + __ffs(__ballot_sync(0xffffffffu, before + upto > target)) - 1;
       }
-      const uint32_t past = __ballot_sync(0xffffffffu, before + upto > target);
-      if (past) return i + 32 * k + __ffs(past) - 1;
-      before += __shfl_sync(0xffffffffu, upto, 31);
+      before += all;
     }
   }
   return -1;

@@ -111,9 +111,9 @@ cudaError_t launch_evict(const EvictParams& p, int kvf, int sms, cudaStream_t st
   cudaError_t err;
   if (C <= kFewSlots) {
     const auto few = [&](auto kernel) { return launch(kernel, dim3((unsigned)(p.batch * kHkv)), kFewThreads, 0, 1, stream, e); };
-    err = C <= kFewThreads ? few(select_few_kernel<1>) : C <= 4 * kFewThreads ? few(select_few_kernel<4>)
-          : C <= 8 * kFewThreads ? few(select_few_kernel<8>) : C <= 16 * kFewThreads ? few(select_few_kernel<16>)
-                                                             : few(select_few_kernel<32>);
+    err = C <= 2 * kFewThreads   ? few(select_few_kernel<2>)
+          : C <= 8 * kFewThreads ? few(select_few_kernel<8>)
+                                 : few(select_few_kernel<16>);
   } else {
     // CTAs a head: one wave of them, 8 at most (each adds to the cluster's barriers and
     // to the histograms that every one reads), as many as hold the weights if need be

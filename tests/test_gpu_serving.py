@@ -9,7 +9,13 @@ Bounds, each derived from the arithmetic and not from a run:
   weights   exp(s - max) / sum is off by 2 |ds| (its own score and the sum's) and
             2^-19 (exp2, the sum, the division)
   outputs   those, half a step of q's type for the weight where it meets V, all times
-            sum of weight * |V|, and half a step of the output's type
+            sum of weight * |V|, and half a step of the output's type.  Where the weights
+            are fp16 (any cache but a bf16 one) they lie on the grid of 2^-24 below its
+            normal numbers: off by 2^-25 at most, where the largest weight is 2^7 or more
+            (the running maximum never lies above the row's), so the outputs by 2^-32
+            times the sum of |V| over the slots.  int8: the weights are held times the V
+            scales, with the largest one's power of two above it in the maximum, so by
+            2^-31 times the largest scale times the sum of |codes|
   tokens, lengths, kept slots and moved rows: equal
 """
 import math
@@ -147,7 +153,8 @@ def prefill_case(fmt, dtype, rows, capacity, page=0, seed=0, pad=3, q_scale=1.0,
             0, nb, (sample,), generator=torch.Generator().manual_seed(seed + b)).tolist()})
         for j in picks:
             ref, a, e = attend64(q[at + j] * q_scale, K[b], V[b], L - nb + j + 1)
-            bound = half * ref.abs() + (half + 2 * e + 2 ** -18) * a + tiny * half
+            grid = 0.0 if fmt == "bf16" else 2 ** -31 * L * float(127 * sc[b, 1].abs().max() if fmt == "i8" else V[b].abs().max())
+            bound = half * ref.abs() + (half + 2 * e + 2 ** -18) * a + tiny * half + grid
             err = (out[at + j].double() - ref).abs()
             assert (err <= bound).all(), \
                 f"row {b} query {j}: worst {float((err / bound).max()):.3f} of the bound, {float(err.max()):.3e}"
@@ -491,3 +498,326 @@ def test_evict_special_weights(library):
     kept = gq.evict_kv(kv, lens, w, 250, 10, 5, out=out, out_lengths=ol)
     for h in range(HKV):
         assert kept[0, h].tolist() == kept64(w[0, h].tolist(), 500, 250, 10, 5)
+
+
+# ------------------------------------------- edges, and all of them together
+
+
+def test_prefill_masked_values(library):
+    """Infinities and NaN in slots that a query does not see never reach it; in slots
+    that it sees they do, at every chunk size around the tiles' and units' edges."""
+    for fmt, dtype in (("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e2m1", "f16")):
+        n, L, C = 70, 300, 384
+        kv, sc = new_cache(fmt, 1, C, 4)
+        ks, vs = scale_of(fmt)
+        bad = [L - n + 3, L - n + 40, L - 1]  # slots of the chunk itself
+        for t in bad:
+            if fmt in TD:
+                kv[0, 1, :, t, 5] = float("nan") if t != L - 1 else float("inf")
+            elif fmt == "e4m3":
+                kv[0, 1, :, t, 5] = 0x7F
+            else:
+                sc[0, 1, :, t, 0] = 0x7F  # dims 0..15
+        for plane in (0, 1):  # behind the length: anything
+            if fmt in TD:
+                kv[0, plane, :, L:] = float("nan")
+            elif fmt == "e4m3":
+                kv[0, plane, :, L:] = 0xFF
+            else:
+                sc[0, plane, :, L:] = 0x7F
+        if fmt in TD:
+            kv[0, 0, 2, L - 10] = float("nan")  # a key of one head
+        q = torch.randn((n, HQ, D), generator=gen(5), device=DEV).to(TD[dtype])
+        starts = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+        out = gq.gqa_prefill(q, kv, starts, lens, k_scale=ks, v_scale=vs, kv_scales=sc)
+        K, V = (values(kv[:, p], None if sc is None else sc[:, p], fmt, s)[0] for p, s in ((0, ks), (1, vs)))
+        dims = range(16) if fmt == "e2m1" else (5,)
+        for j in range(n):
+            end = L - n + j + 1
+            head_nan = fmt in TD and end > L - 10
+            for d in dims:
+                seen = [t for t in bad if t < end]
+                col = out[j, :, d].float()
+                want_nan = any(not (fmt in TD and t == L - 1) for t in seen)
+                rows = [h for h in range(HQ) if not (head_nan and 8 <= h < 12)]
+                if want_nan:
+                    assert torch.isnan(col[rows]).all()
+                elif seen:
+                    assert torch.isposinf(col[rows]).all()
+                else:
+                    assert torch.isfinite(col[rows]).all()
+            if head_nan:
+                assert torch.isnan(out[j, 8:12].float()).all()
+            clean = [d for d in range(D) if d not in dims]
+            ref, a, e = attend64(q[j], torch.nan_to_num(K, nan=0.0, posinf=0.0), torch.nan_to_num(V, nan=0.0, posinf=0.0), end)
+            rows = [h for h in range(HQ) if not (head_nan and 8 <= h < 12)]
+            half = torch.finfo(TD[dtype]).eps / 2
+            bound = half * ref.abs() + (half + 2 * e + 2 ** -18) * a + 2 ** -24
+            err = (out[j].double() - ref).abs()
+            assert (err[rows][:, clean] <= bound[rows][:, clean]).all()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("bf16", "bf16"), ("i8", "bf16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("mag", [1e-6, 30.0])
+def test_prefill_magnitudes(library, fmt, dtype, mag):
+    if dtype == "f16":
+        mag = min(max(mag, 1e-3), 30.0)
+    prefill_case(fmt, dtype, [(40, 300), (130, 130)], 300, seed=6, mag=mag, sample=20)
+
+
+def test_prefill_scales_apart(library):
+    """int8 rows whose V scales differ by powers of two over a tile, zero among them."""
+    def edit(kv, sc):
+        e = torch.randint(-30, 6, sc.shape[2:], generator=gen(1), device=DEV).float()
+        sc[:, 1] = torch.exp2(e).to(torch.bfloat16)
+        sc[:, 1, :, ::17] = 0
+    prefill_case("i8", "bf16", [(60, 500)], 512, seed=7, sample=30, edit=edit)
+    prefill_case("i8", "f16", [(60, 500)], 512, seed=7, sample=30, edit=lambda kv, sc: sc[:, 1].fill_(2.0 ** -20))
+
+
+def test_prefill_out_of_contract(library):
+    """Lengths and starts out of order are clamped and told; nothing outside is touched."""
+    kv, _ = new_cache("bf16", 3, 256, 8)
+    q = torch.randn((50, HQ, D), generator=gen(9), device=DEV).to(torch.bfloat16)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    out = torch.full_like(q, 3.0)
+    starts = torch.tensor([-5, 20, 40, 60], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([10, 1000, -3], dtype=torch.int32, device=DEV)  # below its chunk, above the capacity, negative
+    gq.gqa_prefill(q, kv, starts, lens, out=out, workspace=ws)
+    assert gq.get_status(ws) == gq.api.FLAG_LENGTH_CLAMPED
+    assert not out[:10].any() and not out[40:].any()  # queries without a slot: zero rows
+    want = gq.gqa_prefill(q[10:40].contiguous(), kv, torch.tensor([0, 10, 30, 30], dtype=torch.int32, device=DEV),
+                          torch.tensor([10, 256, 0], dtype=torch.int32, device=DEV))
+    assert torch.equal(out[10:40], want)
+    pool, _, table = paged(kv, None, 64, 3, 256)
+    table[1, 2] = 10 ** 6
+    gq.gqa_prefill_paged(q, pool, table, torch.tensor([0, 0, 50, 50], dtype=torch.int32, device=DEV),
+                         torch.full((3,), 256, dtype=torch.int32, device=DEV), out=out, workspace=ws)
+    assert gq.get_status(ws) == gq.api.FLAG_PAGE_CLAMPED
+
+
+def test_prefill_many_launches(library):
+    """Launches back to back give the same bits each time and no wait runs out."""
+    rows = [(0, 100), (513, 4000), (64, 64), (1, 4096), (300, 2000), (1024, 1024)]
+    kv, _ = new_cache("bf16", len(rows), 4096, 10)
+    n = torch.tensor([r[0] for r in rows])
+    starts = torch.cat((torch.zeros(1, dtype=torch.int64), n.cumsum(0))).to(torch.int32).to(DEV)
+    lens = torch.tensor([r[1] for r in rows], dtype=torch.int32, device=DEV)
+    q = torch.randn((int(n.sum()), HQ, D), generator=gen(11), device=DEV).to(torch.bfloat16)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    first = gq.gqa_prefill(q, kv, starts, lens, workspace=ws)
+    outs = [torch.empty_like(q) for _ in range(4)]
+    for o in outs:
+        o.copy_(first)
+    for k in range(400):
+        gq.gqa_prefill(q, kv, starts, lens, out=outs[k % 4], workspace=ws)
+    assert gq.get_status(ws) == 0
+    for o in outs:
+        assert torch.equal(o, first)
+
+
+def test_prefill_equals_decode(library):
+    """One token a row: within the decode's own rounding of the decode call."""
+    B, C = 5, 700
+    kv, _ = new_cache("f16", B, C, 12)
+    lens = torch.tensor([1, 700, 128, 129, 333], dtype=torch.int32, device=DEV)
+    q = torch.randn((B, HQ, D), generator=gen(13), device=DEV).to(torch.float16)
+    a = gq.gqa_prefill(q, kv, torch.arange(B + 1, dtype=torch.int32, device=DEV), lens)
+    b = gq.gqa_decode(q, kv, lens)
+    assert ((a.float() - b.float()).abs() <= 2 ** -9 * (1 + b.float().abs())).all()
+
+
+def test_long_offsets(library):
+    """Element offsets past 32 bits: the last rows of a large cache."""
+    if torch.cuda.get_device_properties(0).total_memory < 40 << 30:
+        pytest.skip("needs 40 GB")
+    B, C = 9, 131072
+    kv = torch.zeros((B, 2, HKV, C, D), dtype=torch.bfloat16, device=DEV)  # 4.8 GB, 2.4e9 elements
+    kv[B - 1] = torch.randn((2, HKV, C, D), generator=gen(14), device=DEV).to(torch.bfloat16)
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    lens[B - 1] = C
+    starts = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    starts[B] = 33
+    q = torch.randn((33, HQ, D), generator=gen(15), device=DEV).to(torch.bfloat16)
+    out = gq.gqa_prefill(q, kv, starts, lens)
+    K, V = kv[B - 1, 0].double(), kv[B - 1, 1].double()
+    half = torch.finfo(torch.bfloat16).eps / 2
+    for j in (0, 32):
+        ref, a, e = attend64(q[j], K, V, C - 33 + j + 1)
+        assert ((out[j].double() - ref).abs() <= half * ref.abs() + (half + 2 * e + 2 ** -18) * a + 2 ** -126).all()
+    w = torch.zeros((B, HKV, C), device=DEV)
+    gq.accumulate_weights(q[:B].contiguous(), kv, lens, w)
+    ref, e = weights64(q[B - 1][None], K, C, 1)
+    assert ((w[B - 1].double() - ref).abs() <= e + 2 ** -126).all()
+    out_lens = lens.clone()
+    small = torch.zeros((B, 2, HKV, 600, D), dtype=torch.bfloat16, device=DEV)
+    kept = gq.evict_kv(kv, lens, w, 600, 8, 4, out=small, out_lengths=out_lens)
+    for h in (0, 7):
+        at = torch.tensor(kept64(w[B - 1, h].tolist(), C, 600, 8, 4), device=DEV)
+        assert torch.equal(kept[B - 1, h].long(), at)
+        assert torch.equal(small[B - 1, :, h], kv[B - 1, :, h][:, at])
+
+
+def serving_state(fmt="bf16", dtype="bf16", B=4, C=512, seed=20):
+    kv, sc = new_cache(fmt, B, C, seed)
+    g = gen(seed + 1)
+    n = 40
+    return dict(kv=kv, sc=sc, B=B, C=C, q=torch.randn((B * n, HQ, D), generator=g, device=DEV).to(TD[dtype]),
+                starts=torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV),
+                lens=torch.tensor([512, 40, 300, 401][:B], dtype=torch.int32, device=DEV))
+
+
+def run_together(s, ws):
+    """A chunk attended, a window's weights summed, its drafts judged, the cache cut."""
+    B, C = s["B"], s["C"]
+    ks, vs = scale_of("e2m1") if s["sc"] is not None else (1.0, 1.0)
+    out = gq.gqa_prefill(s["q"], s["kv"], s["starts"], s["lens"], k_scale=ks, v_scale=vs, kv_scales=s["sc"], out=ws["out"],
+                         workspace=ws["prefill"])
+    w = gq.accumulate_weights(s["q"].view(B, -1, HQ, D)[:, :2].contiguous(), s["kv"], s["lens"], ws["w"], k_scale=ks,
+                              kv_scales=s["sc"], add=False, workspace=ws["weights"])
+    tokens, accepted = gq.verify_drafts(ws["p"], ws["d"], ws["u"], draft_probs=ws["dq"], sequence_lengths=s["lens"],
+                                        out_lengths=ws["len1"], tokens=ws["tokens"], accepted=ws["accepted"])
+    kept = gq.evict_kv(s["kv"], ws["len1"], w, 100, 16, 4, out=ws["kv"], out_scales=ws["sc"], out_lengths=ws["len2"],
+                       out_weights=ws["w2"], kept=ws["kept"], kv_scales=s["sc"], workspace=ws["evict"])
+    return [out, w, tokens, accepted, ws["len1"], kept, ws["kv"], ws["len2"], ws["w2"]]
+
+
+def together_buffers(s, seed=30):
+    B, C = s["B"], s["C"]
+    fmt = "e2m1" if s["sc"] is not None else "bf16"
+    p, d, u, q, _ = draft_inputs(B, 3, 997, "f32", seed=seed)
+    kv, sc = new_cache(fmt, B, 100, 40)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    return dict(out=torch.zeros_like(s["q"]), w=torch.zeros((B, HKV, C), device=DEV), p=p, d=d, u=u, dq=q,
+                tokens=torch.zeros((B, 3), **i32), accepted=torch.zeros(B, **i32), len1=torch.zeros(B, **i32),
+                len2=torch.zeros(B, **i32), kv=kv, sc=sc, w2=torch.zeros((B, HKV, 100), device=DEV),
+                kept=torch.zeros((B, HKV, 100), **i32),
+                prefill=torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV),
+                weights=torch.zeros(gq.weights_workspace_size(B, C, 2), dtype=torch.uint8, device=DEV),
+                evict=torch.zeros(gq.evict_workspace_size(B, 100), dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_together_graphs_and_streams(library, fmt):
+    s = serving_state(fmt)
+    ws = together_buffers(s)
+    want = [x.clone() for x in run_together(s, ws)]
+    # the same through a captured graph, replayed after its inputs changed and back
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run_together(s, ws)
+    q = s["q"].clone()
+    s["q"].mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(got[0], want[0])
+    s["q"].copy_(q)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    # two streams at once, a set of buffers each, and the side streams' tensors made there
+    other = [(torch.cuda.Stream(), together_buffers(s)) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, w in other:
+            with torch.cuda.stream(st):
+                run_together(s, w)
+    torch.cuda.synchronize()
+    for _, w in other:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            again = run_together(s, w)
+        torch.cuda.synchronize()
+        for a, b in zip(again, want):
+            assert torch.equal(a, b)
+
+
+def test_chain(library):
+    """A prompt written in two chunks and attended, a step's drafts judged and the lengths
+    shortened, the weights summed over steps, the cache cut in place and decoded."""
+    B, C, dt = 2, 640, torch.bfloat16
+    g = gen(50)
+    kv = torch.zeros((B, 2, HKV, C, D), dtype=dt, device=DEV)
+    w_norm = torch.ones(D, dtype=dt, device=DEV)
+    done = torch.zeros(B, dtype=torch.int32, device=DEV)
+    for n in ([100, 33], [300, 200]):
+        rows = torch.repeat_interleave(torch.arange(B), torch.tensor(n)).to(torch.int32).to(DEV)
+        slots = torch.cat([torch.arange(k) for k in n]).to(torch.int32).to(DEV) + done[rows.long()]
+        x = torch.randn((sum(n), HQ + 2 * HKV, D), generator=g, device=DEV).to(dt)
+        q = gq.write_kv(x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], w_norm, w_norm, slots, rows, slots, kv)
+        done = done + torch.tensor(n, dtype=torch.int32, device=DEV)
+        starts = torch.tensor([0, n[0], sum(n)], dtype=torch.int32, device=DEV)
+        out = gq.gqa_prefill(q, kv, starts, done)
+        half = torch.finfo(dt).eps / 2
+        for b in range(B):
+            for j in (0, n[b] - 1):
+                i = int(starts[b]) + j
+                ref, a, e = attend64(q[i], kv[b, 0].double(), kv[b, 1].double(), int(done[b]) - n[b] + j + 1)
+                assert ((out[i].double() - ref).abs() <= half * ref.abs() + (half + 2 * e + 2 ** -18) * a + 2 ** -126).all()
+    weights = torch.zeros((B, HKV, C), device=DEV)
+    total = torch.zeros((B, HKV, C), dtype=torch.float64, device=DEV)
+    bound = total.clone()
+    for step in range(3):
+        qs = torch.randn((B, 1, HQ, D), generator=g, device=DEV).to(dt)
+        gq.accumulate_weights(qs, kv, done, weights)
+        for b in range(B):
+            L = int(done[b])
+            x, e = weights64(qs[b], kv[b, 0].double(), L, 1)
+            total[b, :, :L] += x
+            bound[b, :, :L] += e + 2 ** -23 * total[b, :, :L]
+    assert ((weights.double() - total).abs() <= bound + 2 ** -126).all()
+    before, old, lens0 = kv.clone(), weights.clone(), done.clone()
+    kept = gq.evict_kv(kv, done, weights, 128, recent=32, first=4)
+    check_evicted("bf16", before, None, old, lens0, 128, 32, 4, kv, None, weights, done, kept, clean_w=False)
+    q1 = torch.randn((B, HQ, D), generator=g, device=DEV).to(dt)
+    o = gq.gqa_decode(q1, kv, done)
+    for b in range(B):
+        k, v = (torch.stack([before[b, p, h][kept[b, h].long()] for h in range(HKV)]).double() for p in (0, 1))
+        ref, _, _ = attend64(q1[b], k, v, 128)
+        assert ((o[b].double() - ref).abs() <= 3e-2 * (1 + ref.abs())).all()
+
+
+def test_refusals(library):
+    kv, _ = new_cache("bf16", 2, 64, 60)
+    q = torch.zeros((10, HQ, D), dtype=torch.bfloat16, device=DEV)
+    starts = torch.tensor([0, 5, 10], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([64, 64], dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        gq.gqa_prefill(q, kv, starts[:2], lens)
+    with pytest.raises(ValueError):
+        gq.gqa_prefill(q.view(10, HQ // 2, 2 * D), kv, starts, lens)
+    with pytest.raises(gq.GqaError, match="dtype of q"):
+        gq.gqa_prefill(q.half(), kv, starts, lens)
+    with pytest.raises(gq.GqaError, match="WORKSPACE"):
+        gq.gqa_prefill(q, kv, starts, lens, workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(gq.GqaError, match="overlaps"):
+        gq.gqa_prefill(q, kv, starts, lens, out=q)
+    with pytest.raises(gq.GqaError, match="q_scale"):
+        gq.gqa_prefill(q, kv, starts, lens, q_scale=float("nan"))
+    assert gq.gqa_prefill(q[:0], kv, torch.zeros_like(starts), lens).shape == (0, HQ, D)
+    p, d, u, dq, n = draft_inputs(2, 3, 50, "f32")
+    for bad in (dict(drafts=d[:, :1].contiguous()), dict(uniforms=u.double()), dict(draft_probs=dq.half()),
+                dict(out_lengths=n), dict(probs=p.transpose(1, 2))):
+        with pytest.raises(ValueError):
+            gq.verify_drafts(**{**dict(probs=p, drafts=d, uniforms=u), **bad})
+    with pytest.raises(gq.GqaError, match="strides"):
+        gq.verify_drafts(p[:1].expand(2, 3, 50), d, u)
+    w = torch.zeros((2, HKV, 64), device=DEV)
+    with pytest.raises(ValueError):
+        gq.accumulate_weights(q[:2], kv, lens, w[:, :, :32])
+    with pytest.raises(ValueError):
+        gq.accumulate_weights(q.view(2, 5, HQ, D), kv, lens, w)
+    with pytest.raises(gq.GqaError, match="first and recent"):
+        gq.evict_kv(kv, lens, w, 10, recent=8, first=4)
+    with pytest.raises(ValueError):
+        gq.evict_kv(kv, lens, w, 10, out_lengths=lens)
+    with pytest.raises(ValueError):
+        gq.evict_kv(kv, lens, w, 10, out=torch.zeros_like(kv))
+    with pytest.raises(gq.GqaError, match="slots a row"):
+        gq.evict_kv(kv, lens, w, 10, out=torch.zeros_like(kv[:, :, :, :8]).contiguous(), out_lengths=lens.clone())
+    with pytest.raises(gq.GqaError, match="overlaps"):
+        gq.evict_kv(kv, lens, w, 10, out=kv, out_lengths=lens.clone())
+    with pytest.raises(gq.GqaError, match="overlaps"):
+        gq.evict_kv(kv, lens, w, 10, out=torch.zeros_like(kv), out_lengths=lens)
