@@ -234,36 +234,46 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t address, uint32_t lead) {
 __host__ __device__ constexpr uint32_t tc_idesc(bool bf16, bool b_mn) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_mn ? 1u << 16 : 0u) | (128u >> 3) << 17 | (128u >> 4) << 24;
 }
-// One lane of a converged warp, always the same.  The whole warp runs the code around
-// a product, so that its operands stay in uniform registers; the lane issues it.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t one;
+// The products are issued by a converged warp: its elected lane (always the same one)
+// issues them, and the operands, the same in every lane, stay in uniform registers.  A
+// step's products are one block of code: the warp shares its scheduler with two softmax
+// warps, and every instruction between two products costs it some ten cycles.
+//
+// S = Q K^T over 128 dims: eight products of 16 dims, four to a 64-dim half.
+__device__ __forceinline__ void tc_qk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(one));
-  return one != 0;
+      "{\n\t.reg .pred e, no, yes;\n\t.reg .b64 x, y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 no, 0, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, no;\n\t"
+      "add.u64 x, %1, 2;\n\tadd.u64 y, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 4;\n\tadd.u64 y, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 6;\n\tadd.u64 y, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 1024;\n\tadd.u64 y, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 1026;\n\tadd.u64 y, %2, 1026;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 1028;\n\tadd.u64 y, %2, 1028;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t"
+      "add.u64 x, %1, 1030;\n\tadd.u64 y, %2, 1030;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, yes;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
+      : "memory");
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  if (elect_lane())
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"((uint32_t)add)
-        : "memory");
-}
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  if (elect_lane())
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"((uint32_t)add)
-        : "memory");
+// O += P V over 64 slots: four products of 16 slots, P in TMEM; `add` 0: the first one
+// writes O.
+__device__ __forceinline__ void tc_pv(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred e, first, yes;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 first, %4, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, first;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.u64 y, %2, 128;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.u64 y, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.u64 y, %2, 384;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, yes;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      : "memory");
 }
 // The barrier is arrived at when every product issued so far by the elected lane is done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  if (elect_lane())
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+      : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -314,7 +324,8 @@ struct PfShared {
   // are between a load and its product).  A barrier is waited on in every one of its
   // phases by whoever waits on it: a parity says nothing about a phase further on.
   uint64_t k_full[4], v_full[4], v_fixed[4];
-  uint64_t kv_empty[kPfSlots], raw_full[3], raw_empty[3];
+  // A tile's K and the V of the tile before were used (tile & 3).
+  uint64_t used[4], raw_full[3], raw_empty[3];
   PfCursor cursor[kPfThreads / 32];
   uint32_t tmem;
   uint16_t odd[8];  // a part's number + 1 where a value was taken out of V (a stale one only costs time)
@@ -432,11 +443,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       mbar_init(&sm.p_full[i][1], kPfRows);
       mbar_init(&sm.o_full[i], 1);
     }
-    for (int i = 0; i < kPfSlots; ++i) mbar_init(&sm.kv_empty[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&sm.k_full[i], kNarrow ? 2 : 1);
       mbar_init(&sm.v_full[i], kNarrow ? 2 : 1);
       mbar_init(&sm.v_fixed[i], 2);
+      mbar_init(&sm.used[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&sm.raw_full[i], scale_row_bytes(KVF) > 0 ? 2 : 1);
@@ -732,57 +743,56 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const uint64_t q0 = tc_desc(smem_addr(sm.q[0]), 16), k0 = tc_desc(smem_addr(sm.kv[0]), 16),
                      v0 = tc_desc(smem_addr(sm.kv[0]), kPfTileBytes / 2);
       // (a descriptor's address counts 16 bytes in its lowest 14 bits; all of shared memory fits)
-      const auto qk = [&](int t, int slot) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t off = ((k >> 2) * (kPfTileBytes / 2) + (k & 3) * 32) >> 4;
-          tc_mma_ss(tmem + t * 128, q0 + (uint32_t)(t * (kPfTileBytes >> 4)) + off,
-                    k0 + (uint32_t)(slot * (kPfTileBytes >> 4)) + off, kQk, k > 0);
-        }
+      constexpr uint32_t kTile = kPfTileBytes >> 4;
+      // a lane that gives up a wait goes on with the others to the end of the tile
+      const auto await = [&](uint64_t* bar, uint32_t parity) {
+        if (!pf_wait(bar, parity)) ok = false;
       };
-      const auto pv = [&](int t, int slot, int half, bool add) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 4 * half + i;
-          tc_mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, v0 + (uint32_t)(slot * (kPfTileBytes >> 4) + k * 128), kPv,
-                    add || k > 0);
-        }
-      };
-      int k_no = 0, v_no = 0;  // tiles whose K, V came to be used
+      uint32_t tile = 0, k_slot = 0, v_slot = 1;  // the tile whose K comes next; its slot, V's of the tile before
       uint32_t q_phase = 0, p_phase = 0;
       while (ok && sg.next(p)) {
         const int nq = sg.rows_of_q(), n = sg.j1 - sg.j0;
         for (int j = -1; ok && j < n; ++j) {
-          const int k_slot = 2 * k_no % kSlots, v_slot = (2 * v_no + 1) % kSlots;
           if (j >= 0) {
-            uint64_t* there = kNarrow ? &sm.v_full[v_no & 3] : &sm.v_fixed[v_no & 3];
-            if (!wait(there, v_no >> 2 & 1)) break;
+            const uint32_t v_no = tile - 1;
+            await(kNarrow ? &sm.v_full[v_no & 3] : &sm.v_fixed[v_no & 3], v_no >> 2 & 1);
           }
-          for (int t = 0; t < nq; ++t) {
+          const uint64_t kd = k0 + k_slot * kTile, vd = v0 + v_slot * kTile;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= nq) break;
             if (j >= 0) {
-              if (!wait(&sm.p_full[t][0], p_phase >> t & 1)) break;
+              const uint32_t parity = p_phase >> t & 1;
+              await(&sm.p_full[t][0], parity);
               tc_fence_after();
-              pv(t, v_slot, 0, j > 0);
-              if (!wait(&sm.p_full[t][1], p_phase >> t & 1)) break;
-              p_phase ^= 1u << t;
+              tc_pv(tmem + 256 + t * 128, tmem + t * 128, vd, kPv, j > 0);
+              await(&sm.p_full[t][1], parity);
               tc_fence_after();
-              pv(t, v_slot, 1, true);
+              tc_pv(tmem + 256 + t * 128, tmem + t * 128 + 32, vd + 512, kPv, 1);
               if (j == n - 1) tc_commit(&sm.o_full[t]);
-              if (t == nq - 1) tc_commit(&sm.kv_empty[v_slot]);
             } else {
-              if (!wait(&sm.q_full[t], q_phase >> t & 1)) break;
-              q_phase ^= 1u << t;
+              await(&sm.q_full[t], q_phase >> t & 1);
               tc_fence_after();
             }
             if (j + 1 < n) {
-              if (t == 0 && !wait(&sm.k_full[k_no & 3], k_no >> 2 & 1)) break;
-              qk(t, k_slot);
+              if (t == 0) await(&sm.k_full[tile & 3], tile >> 2 & 1);
+              tc_qk(tmem + t * 128, q0 + t * kTile, kd, kQk);
               tc_commit(&sm.s_full[t]);
-              if (t == nq - 1) tc_commit(&sm.kv_empty[k_slot]);
             }
           }
-          if (j >= 0) ++v_no;
-          if (j + 1 < n) ++k_no;
+          if (j >= 0) {
+            p_phase ^= (1u << nq) - 1;
+            v_slot = v_slot + 2 >= kSlots ? v_slot + 2 - kSlots : v_slot + 2;
+          } else {
+            q_phase ^= (1u << nq) - 1;
+          }
+          if (j + 1 < n) {
+            // K of this tile and V of the one before are done with
+            tc_commit(&sm.used[tile & 3]);
+            k_slot = k_slot + 2 >= kSlots ? k_slot + 2 - kSlots : k_slot + 2;
+            ++tile;
+          }
+          ok = __all_sync(0xffffffffu, ok);
         }
       }
       if (!ok) {  // products in flight end before the block's memory is given up
@@ -795,6 +805,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // -------------------------------------------------------- K and V tiles
     uint32_t item = 0, seg = 0;
     int tile_no = 0;
+    // The slot of item i (tile i / 2's K, or its V) held item i - kSlots, which is free
+    // when the first product of tile (i - kSlots + 1) / 2 with its K is done.  (Every
+    // tile's barrier is waited on, one after another.)
+    uint32_t freed = 0;  // tiles whose barrier was waited on
+    const auto slot_free = [&](uint32_t i) {
+      while (ok && i >= (uint32_t)kSlots && freed <= (i - kSlots + 1) / 2) {
+        wait(&sm.used[freed & 3], freed >> 2 & 1);
+        ++freed;
+      }
+      return ok;
+    };
     if constexpr (kNarrow) {
       // One warp has the tiles loaded as they lie; two widen them, four rows at a time, a
       // lane 16 elements, eight lanes a row.  (The first widening a quarter too was
@@ -900,7 +921,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const int slot = (int)(item % kSlots), raw = (int)(item % kRaws);
               const uint8_t* bytes = sm.kv[kSlots] + raw * kRawBytes;
               uint8_t* dst = sm.kv[slot];
-              if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
+              if (!wait(&sm.raw_full[raw], item / kRaws & 1) || !slot_free(item)) break;
               // slots past the length, and values that some query does not see
               const bool tail = t0 + kPfTile > len, check = !kI8 && plane == 1 && t0 + kPfTile - 1 > first_seen;
               bool odd = false;
@@ -966,7 +987,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (warp == 9) {
               // by TMA, in boxes of `box` rows: one, or a page's each; pages past the
               // length are left out
-              if (!wait(&sm.kv_empty[slot], (item / kSlots & 1) ^ 1)) break;
+              if (!slot_free(item)) break;
               const int pg = plane * kHkv + sg.g;
               int row = -1;
               if (p.c.block_table == nullptr) {
