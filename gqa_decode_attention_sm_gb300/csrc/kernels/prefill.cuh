@@ -23,6 +23,14 @@
 // row into fp16's range, so these calls have fp16 products whatever q's type is.
 // int8 scales multiply the columns of S and of P.
 //
+// Measured (GB300, in a CUDA graph): 8192 bf16 tokens 350 us, 1573 TFLOP/s, 0.81 of the
+// library GEMM's burst rate, at clocks that the power limit has already lowered; 512
+// tokens over 131072 slots in pages 740 us, 1484.  A tile pair takes 4 products of 512
+// tensor clocks; the rest is the chain S -> maximum -> 2^x -> P of a row (1380 clocks),
+// the issuing warp's steps and the latency between the two, of which the other tile
+// covers a part.  K and V come from L2 mostly: 152 CTAs ask for 64 KB each tile.  Narrow
+// caches are bound by the two widening warps (1700 clocks a K or V tile of e2m1).
+//
 // All rows' tiles form one stream that the resident CTAs (one an SM) cut into equal
 // runs, whatever the lengths are; a unit cut by a run's end leaves FP32 partials (two a
 // CTA at most) that a second kernel merges.
@@ -42,11 +50,11 @@ constexpr int kPfTileBytes = kPfTile * kD * 2;
 constexpr int kPfSlots = 5;
 constexpr int kPfMaxCtas = 160;
 // Balancing, measured on prompts of 8192 tokens, 16 ragged chunks over 8192 and 512 tokens
-// over 131072 slots: a unit counted as 1, 2, 3, 4 tiles more than it has 460 / 474 / 816,
-// 429 / 434 / 828, 432 / 430 / 816, 436 / 437 / 827 us; 17 tokens over 1024 slots in
-// runs of 1, 2, 3 tiles at least 28, 19, 22 us.
+// over 131072 slots: a unit counted as 1, 2, 3, 4, 5 tiles more than it has 401 / 449 / 776,
+// 375 / 426 / 787, 354 / 400 / 781, 350 / 375 / 740, 352 / 381 / 729 us; 17 tokens over
+// 1024 slots in runs of 1, 2, 3 tiles at least 28, 19, 22 us (with an earlier merge).
 constexpr int kPfMinRun = 2;         // K/V tiles a CTA takes at least
-constexpr int kPfUnitCost = 2;       // what a unit costs besides its tiles (q, the first product, the output), in tiles
+constexpr int kPfUnitCost = 4;       // what a unit costs besides its tiles (q, the first product, the output), in tiles
 constexpr int kPfFewTiles = 4;       // tiles a CTA up to which that is not counted (every CTA then has about one piece)
 constexpr float kPfLift = 7.f;       // log2 of the weight of a row's maximum
 constexpr float kPfGrow = 8.f;       // growth of the maximum that a row is rescaled for
