@@ -764,7 +764,9 @@ def evict_workspace_size(batch: int, keep: int) -> int:
 
 def _workspace(workspace, nbytes, device):
     if workspace is None:
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace[:256].zero_()  # the header (status flags); the rest is written before it is read
+        return workspace
     _require(workspace, "workspace", None, (torch.uint8,), device)
     return workspace
 

@@ -172,61 +172,70 @@ struct PfCursor {
 struct PfPlan {
   long long total, run;  // positions in all and a CTA's
   int cost;              // a unit's besides its tiles
+  int b;                 // run c begins at position `rem` of row b's (if it begins before `total`)
+  long long rem;
+};
+struct PfScan {
+  long long tiles[32], units[32], rem;
+  int b;
 };
 
-// Every thread of the block calls it.
-__device__ __forceinline__ PfPlan pf_plan(const PrefillParams& p, long long* s_sum) {
+// The plan, and where run c begins.  Every thread of the block calls it; each has an
+// equal part of the rows.
+__device__ __forceinline__ PfPlan pf_plan(const PrefillParams& p, int c, PfScan& s) {
+  const int warps = (int)blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int per = (p.c.batch + (int)blockDim.x - 1) / (int)blockDim.x;
+  const int b0 = min(p.c.batch, (int)threadIdx.x * per), b1 = min(p.c.batch, b0 + per);
   long long tiles = 0, units = 0;
-  for (int b = threadIdx.x; b < p.c.batch; b += blockDim.x) {
+  for (int b = b0; b < b1; ++b) {
     const PfRow r = pf_row(p, b);
     tiles += r.positions(0);
     units += kHkv * r.units();
   }
+  const long long my_tiles = tiles, my_units = units;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-    units += __shfl_xor_sync(0xffffffffu, units, o);
+  for (int o = 1; o < 32; o <<= 1) {  // up to this lane
+    const long long x = __shfl_up_sync(0xffffffffu, tiles, o), y = __shfl_up_sync(0xffffffffu, units, o);
+    if (lane >= o) {
+      tiles += x;
+      units += y;
+    }
   }
-  if ((threadIdx.x & 31) == 0) {
-    s_sum[threadIdx.x / 32 * 2] = tiles;
-    s_sum[threadIdx.x / 32 * 2 + 1] = units;
+  if (lane == 31) {
+    s.tiles[warp] = tiles;
+    s.units[warp] = units;
   }
   __syncthreads();
-  tiles = units = 0;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-    tiles += s_sum[2 * w];
-    units += s_sum[2 * w + 1];
+  long long all_tiles = 0, all_units = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) {
+      tiles += all_tiles;
+      units += all_units;
+    }
+    all_tiles += s.tiles[w];
+    all_units += s.units[w];
   }
   PfPlan plan;
-  plan.cost = tiles > (long long)kPfFewTiles * p.ctas ? kPfUnitCost : 0;
-  plan.total = tiles + plan.cost * units;
+  plan.cost = all_tiles > (long long)kPfFewTiles * p.ctas ? kPfUnitCost : 0;
+  plan.total = all_tiles + plan.cost * all_units;
   plan.run = max((plan.total + p.ctas - 1) / p.ctas, (long long)kPfMinRun);
-  __syncthreads();
-  return plan;
-}
-
-// The row that holds position `at` < total, and the position within it: warp-wide.
-__device__ __forceinline__ int pf_find_row(const PrefillParams& p, long long at, int cost, long long& rem) {
-  const int lane = threadIdx.x & 31;
-  long long before = 0;
-  for (int b0 = 0; b0 < p.c.batch; b0 += 32) {
-    const long long mine = b0 + lane < p.c.batch ? pf_row(p, b0 + lane).positions(cost) : 0;
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
+  // the thread whose rows hold the position says which it is
+  const long long at = c * plan.run, upto = tiles + plan.cost * units, before = upto - my_tiles - plan.cost * my_units;
+  if (before <= at && at < upto) {
+    long long rem = at - before;
+    int b = b0;
+    for (; b < b1 - 1; ++b) {
+      const long long n = pf_row(p, b).positions(plan.cost);
+      if (rem < n) break;
+      rem -= n;
     }
-    const uint32_t past = __ballot_sync(0xffffffffu, before + upto > at);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      rem = at - before - __shfl_sync(0xffffffffu, upto - mine, k);
-      return b0 + k;
-    }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    s.b = b;
+    s.rem = rem;
   }
-  rem = 0;
-  return p.c.batch;
+  __syncthreads();
+  plan.b = s.b;
+  plan.rem = s.rem;
+  return plan;
 }
 
 // ---- tcgen05 ---------------------------------------------------------------
@@ -466,20 +475,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     fence_barrier_init();
   }
   pdl_wait_prior_grid();
-  const PfPlan plan = pf_plan(p, reinterpret_cast<long long*>(sm.q[0]));
+  const PfPlan plan = pf_plan(p, (int)blockIdx.x, *reinterpret_cast<PfScan*>(sm.q[0]));
   const long long begin = (long long)blockIdx.x * plan.run;
   if (begin >= plan.total) return;  // (all of the block)
   if (warp == 0) {
-    long long rem;
-    const int b = pf_find_row(p, begin, plan.cost, rem);
     if (lane < kPfThreads / 32) {
       PfCursor& c = sm.cursor[lane];
-      c.b = b;
-      c.row = pf_row(p, b);
+      c.b = plan.b;
+      c.row = pf_row(p, plan.b);
       c.left = min(plan.run, plan.total - begin);
       c.begun = 0;
       c.cost = plan.cost;
-      pf_locate(c.row, rem, c.cost, c.g, c.m, c.j0);
+      pf_locate(c.row, plan.rem, c.cost, c.g, c.m, c.j0);
     }
   } else if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
@@ -564,6 +571,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         *reinterpret_cast<uint4*>(sm.q[t] + pf_piece((warp & 3) * 32 + 2 * i + (lane >> 4), piece)) = x[i];
+      // (a q_scale of 0: the least normal number, so that a hidden slot's -inf stays one)
+      scale = fmaxf(scale, 0x1p-126f);
       proxy_fence();
       mbar_arrive(&sm.q_full[t]);
     };
@@ -1073,33 +1082,29 @@ constexpr int kMergeDims = kD / (kMergeThreads / 32);  // of a row that a thread
 // the first run that does.
 template <int QF>
 __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  __shared__ long long s_sum[2 * kMergeThreads / 32];
+  __shared__ PfScan s_scan;
   __shared__ PfCursor s_unit;
   __shared__ int s_pieces;  // 0: nothing to do
   __shared__ long long s_begin;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const PfPlan plan = pf_plan(p, s_sum);
   const int c = (int)blockIdx.x + 1;
+  const PfPlan plan = pf_plan(p, c, s_scan);
   const long long at = c * plan.run;
   if (at >= plan.total) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    long long rem;
-    const int b = pf_find_row(p, at, plan.cost, rem);
-    if (lane == 0) {
-      PfCursor u;
-      u.b = b;
-      u.row = pf_row(p, b);
-      int j;
-      pf_locate(u.row, rem, plan.cost, u.g, u.m, j);
-      u.all = u.row.tiles(u.m);
-      const long long begin = at - j;  // the position of the unit's first tile
-      s_begin = begin;
-      // inside the unit, and no earlier run's begin is
-      s_pieces = j > 0 && at - plan.run <= begin ? (int)((begin + u.all - 1) / plan.run - begin / plan.run) + 1 : 0;
-      s_unit = u;
-    }
+  if (threadIdx.x == 0) {
+    PfCursor u;
+    u.b = plan.b;
+    u.row = pf_row(p, plan.b);
+    int j;
+    pf_locate(u.row, plan.rem, plan.cost, u.g, u.m, j);
+    u.all = u.row.tiles(u.m);
+    const long long begin = at - j;  // the position of the unit's first tile
+    s_begin = begin;
+    // inside the unit, and no earlier run's begin is
+    s_pieces = j > 0 && at - plan.run <= begin ? (int)((begin + u.all - 1) / plan.run - begin / plan.run) + 1 : 0;
+    s_unit = u;
   }
   __syncthreads();
   if (s_pieces == 0) return;

@@ -558,6 +558,23 @@ def test_prefill_masked_values(library):
             assert (err[rows][:, clean] <= bound[rows][:, clean]).all()
 
 
+@pytest.mark.parametrize("fmt,dtype", FORMATS)
+def test_prefill_small_caches(library, fmt, dtype):
+    # caches of fewer rows than a tile has, odd capacities
+    prefill_case(fmt, dtype, [(1, 1)], 1, seed=11)
+    prefill_case(fmt, dtype, [(2, 3), (3, 3), (0, 0)], 3, seed=12)
+    prefill_case(fmt, dtype, [(40, 77)], 77, seed=13, q_scale=0.37)
+    prefill_case(fmt, dtype, [(5, 16)], 16, page=16, seed=14, q_scale=0.0)
+
+
+def test_prefill_many_rows(library):
+    # more rows than a block has threads, most of them short, some without tokens
+    rows = [((7 * b) % 3, 1 + (5 * b) % 40) for b in range(1000)]
+    rows = [(min(n, L), L) for n, L in rows]
+    prefill_case("bf16", "bf16", rows, 41, seed=15, sample=1)
+    prefill_case("e4m3", "bf16", [(90, 100), (0, 100)] * 150, 100, seed=16, sample=1)
+
+
 @pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("bf16", "bf16"), ("i8", "bf16"), ("e4m3", "bf16")])
 @pytest.mark.parametrize("mag", [1e-6, 30.0])
 def test_prefill_magnitudes(library, fmt, dtype, mag):
