@@ -838,3 +838,19 @@ def test_refusals(library):
         gq.evict_kv(kv, lens, w, 10, out=kv, out_lengths=lens.clone())
     with pytest.raises(gq.GqaError, match="overlaps"):
         gq.evict_kv(kv, lens, w, 10, out=torch.zeros_like(kv), out_lengths=lens)
+
+
+def test_weights_nan_key(library):
+    """A NaN key makes every weight of the rows that see it NaN, and hidden slots' none."""
+    for C in (300, 40000):  # on chip and in two launches
+        kv, _ = new_cache("f16", 1, C, 61)
+        kv[0, 0, 3, C - 2] = float("nan")
+        q = torch.randn((1, 2, HQ, D), generator=gen(62), device=DEV).half()
+        q[0, :, 12] *= 40  # (weights that underflow beside the largest)
+        lens = torch.tensor([C - 1], dtype=torch.int32, device=DEV)  # the last slot is behind the length
+        w = gq.accumulate_weights(q, kv, lens, torch.zeros((1, HKV, C), device=DEV))
+        assert torch.isfinite(w[0, [0, 1, 2, 4, 5, 6, 7]]).all() and w[0, 3, C - 1] == 0
+        assert torch.isnan(w[0, 3, :C - 1]).all()  # token 1 sees the NaN key
+        lens.fill_(C - 2)  # now no token sees it
+        w = gq.accumulate_weights(q, kv, lens, torch.zeros((1, HKV, C), device=DEV))
+        assert torch.isfinite(w).all()
