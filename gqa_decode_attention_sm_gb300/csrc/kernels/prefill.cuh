@@ -28,8 +28,13 @@
 // tokens over 131072 slots in pages 740 us, 1484.  A tile pair takes 4 products of 512
 // tensor clocks; the rest is the chain S -> maximum -> 2^x -> P of a row (1380 clocks),
 // the issuing warp's steps and the latency between the two, of which the other tile
-// covers a part.  K and V come from L2 mostly: 152 CTAs ask for 64 KB each tile.  Narrow
-// caches are bound by the two widening warps (1700 clocks a K or V tile of e2m1).
+// covers a part.  152 CTAs ask for 64 KB each tile: of one long row's K and V most comes
+// from L2; 16 rows' units lie too far apart for it (1.65 GB from HBM in 390 us, 4.2
+// TB/s), which costs no more than 5 %: the same chunks over one row's pages take 374 and
+// 376 us or, of longer rows, 596 and 626.  Narrow caches are bound by the two widening
+// warps: of 1980 clocks a K or V tile of e2m1 they widen for 1560 and wait for 370 (raw
+// codes read one step ahead: 729 us before and after; a third warp: 1108 us, its
+// registers are the softmax's).
 //
 // All rows' tiles form one stream that the resident CTAs (one an SM) cut into equal
 // runs, whatever the lengths are; a unit cut by a run's end leaves FP32 partials (two a
