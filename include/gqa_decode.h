@@ -596,7 +596,8 @@ gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride,
  * a query that sees no slot gives no weight.  Pointers 16-byte aligned (int8
  * scales 2, e2m1 scales 8, lens 4).  The workspace holds
  * gqa_weights_workspace_size(batch, capacity, q_len) bytes (0: invalid sizes).
- * Two launches, no allocation, no host sync. */
+ * One launch where a row's scores fit on chip and the batch fills the GPU or the
+ * capacity is at most 8192, else two; no allocation, no host sync. */
 size_t gqa_weights_workspace_size(int batch, int capacity, int q_len);
 gqa_status_t gqa_accumulate_weights(const void* q, gqa_dtype_t q_dtype, const void* kv,
                                     gqa_kv_format_t kv_format, const void* kv_scales, const int32_t* lens,
