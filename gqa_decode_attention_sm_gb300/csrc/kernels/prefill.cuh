@@ -612,9 +612,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         const int visible = seen - j * kPfTile + 1;  // columns of this tile that the row sees
         const bool masked = __any_sync(0xffffffffu, visible < kPfTile);
+        uint32_t big = 0;  // int8: the largest V scale that the row sees in this tile, a pair's in 15 bits each
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 128; ++k) s[k] = k < visible ? s[k] : -INFINITY;
+          if constexpr (kI8) {
+#pragma unroll
+            for (int k = 0; k < 128; k += 2) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(scales[1] + k) & 0x7fff7fffu;
+              big = __vmaxu2(big, k + 1 < visible ? w : (k < visible ? w & 0xffffu : 0u));
+            }
+          }
+        } else if constexpr (kI8) {
+#pragma unroll
+          for (int k = 0; k < 128; k += 2) big = __vmaxu2(big, *reinterpret_cast<const uint32_t*>(scales[1] + k) & 0x7fff7fffu);
         }
         float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -625,10 +636,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * scale;
         if constexpr (kI8) {
           // int8: P holds weights times V scales, so the largest of these counts too, by
-          // its exponent (-60 at least: the weights' sum stays in range)
-          uint32_t big = 0;
-#pragma unroll
-          for (int k = 0; k < 128; k += 2) big = __vmaxu2(big, *reinterpret_cast<const uint32_t*>(scales[1] + k) & 0x7fff7fffu);
+          // its exponent (-60 at least: the weights' sum stays in range).  Of the slots that
+          // the row sees only: a later token's scale may be anything.
           const int lg = (int)(max(big & 0xffffu, big >> 16) >> 7) - 126;
           top += (float)max(lg, -60);
         }

@@ -532,8 +532,12 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
  * row and sets it too.  Formats, scales and q_scale as gqa_decode_verify, but no
  * rule on the capacity of an int8 or e2m1 cache.  Scores, maximum and sum are
  * FP32; each softmax weight is rounded where it meets V, to bf16 over a bf16 cache,
- * else to fp16 (by 2^-12 of itself down to 2^-21 of the largest, by 2^-32 of the
- * largest below; int8: times its V scale).  A value (or key) that a query does not see never reaches its output, whatever it holds.
+ * else to fp16 (by 2^-11 of itself down to 2^-21 of the largest, by 2^-32 of the
+ * largest below).  int8: what is rounded is the weight times its slot's V scale, and
+ * the largest weight times the largest V scale that the query sees (2^-61 at least)
+ * takes the largest's place: by 2^-11 of itself down to 2^-20 of that product, by
+ * 2^-31 of it below.  A value, key or scale that a query does not see never reaches its
+ * output, whatever it holds.
  * q, kv, out and the workspace 16-byte aligned (int8 scales 2, e2m1 scales 8);
  * nothing written overlaps anything else.  The workspace holds
  * gqa_prefill_workspace_size() bytes whatever the sizes; its header as
