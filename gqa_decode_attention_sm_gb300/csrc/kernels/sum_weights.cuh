@@ -220,7 +220,9 @@ __device__ __forceinline__ void score_rows(const WeightParams& p, int q_len, int
               l[nt][e] *= ex2(m[nt][e] - top);
               m[nt][e] = top;
             }
-            if (t <= seen && t < end) l[nt][e] += ex2(sv[e] - m[nt][e]);  // (a NaN score makes a NaN sum)
+            // (-inf: a hidden slot, or a score of no weight wherever it lies, also where the
+            // maximum is -inf still; a NaN score makes a NaN sum)
+            if (sv[e] != -INFINITY) l[nt][e] += ex2(sv[e] - m[nt][e]);
           }
         }
       }

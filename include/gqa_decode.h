@@ -597,7 +597,9 @@ gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride,
  * weights float [batch, 8, capacity]: for t < lens[b], w is added to it (add != 0)
  * or written (add = 0); slots at and past the length keep what they hold.  FP32
  * throughout.  Formats as gqa_decode_verify (no rule on the capacity), lengths too;
- * a query that sees no slot gives no weight.  Pointers 16-byte aligned (int8
+ * a score of minus infinity gives its slot none, and a query that sees no slot, or
+ * none but such, gives no weight at all; a NaN score makes NaN of the weights that
+ * its head's query gives.  Pointers 16-byte aligned (int8
  * scales 2, e2m1 scales 8, lens 4).  The workspace holds
  * gqa_weights_workspace_size(batch, capacity, q_len) bytes (0: invalid sizes).
  * One launch where a row's scores fit on chip and the batch fills the GPU or the

@@ -70,3 +70,61 @@ def test_prefill_hidden_int8_scales(library, n, L, page, dtype):  # noqa: F811
                 continue
             err = (out[j].double() - ref).abs()
             assert (err <= bound).all(), f"{what}: query {j}, worst {float((err / bound).max()):.3f} of the bound"
+
+
+# ------------------------------------------------- weight sums: infinite scores
+
+
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("bf16", "bf16"), ("i8", "bf16")])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("C", [300, 40000])  # on chip and in two launches
+def test_weights_of_minus_infinity(library, fmt, dtype, T, C):  # noqa: F811
+    """A score of minus infinity gives its slot no weight and leaves the others theirs,
+    wherever it lies: a lane's first slot, a whole slab of a warp, or the last."""
+    L = C - 3
+    g = gen(12)
+    q = torch.randn((1, T, HQ, D), generator=g, device=DEV).to(TD[dtype])
+    q[..., 0] = 1.0 + torch.rand(q.shape[:-1], generator=g, device=DEV).to(TD[dtype])
+    for at in ([0], [0, 8], list(range(16)), list(range(32)), [5, 17, 100, L - T], list(range(130, 290)), [L // 2]):
+        kv, sc = new_cache(fmt, 1, C, 13)
+        if fmt == "i8":
+            sc[0, 0, :, at] = INF
+            kv[0, 0, :, at] = 0
+            kv[0, 0, :, at, 0] = -1
+            # (0 * inf is no number in the values; codes 0 add nothing to the score)
+        else:
+            kv[0, 0, :, at, 0] = -INF
+        lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+        got = gq.accumulate_weights(q, kv, lens, torch.zeros((1, HKV, C), device=DEV), kv_scales=sc, add=False)
+        K = torch.nan_to_num(values(kv[:, 0], None if sc is None else sc[:, 0], fmt, 1.0)[0], nan=0.0, neginf=0.0)
+        w, e = (torch.zeros((HKV, L), dtype=torch.float64, device=DEV) for _ in range(2))
+        for j in range(T):
+            end = L - T + 1 + j
+            k = K[:, :end].repeat_interleave(4, 0)
+            s = torch.einsum("hd,htd->ht", q[0, j].double(), k) / math.sqrt(128.0)
+            m = torch.einsum("hd,htd->ht", q[0, j].double().abs(), k.abs()).amax(-1, keepdim=True) / math.sqrt(128.0)
+            ds = 2 ** -16 * m + 2 ** -22 * s.abs().amax(-1, keepdim=True)
+            s[:, [t for t in at if t < end]] = -INF
+            x = torch.softmax(s, -1)
+            w[:, :end] += x.view(HKV, 4, end).sum(1)
+            e[:, :end] += (x * (2 * ds + 2 ** -19)).view(HKV, 4, end).sum(1)
+        assert not got[0][:, at].any()
+        assert ((got[0, :, :L].double() - w).abs() <= e + 2 ** -126).all()
+
+
+def test_weights_of_minus_infinity_alone(library):  # noqa: F811
+    """A query whose scores are all minus infinity gives no weight (its softmax has no
+    value), and a NaN score among them still makes NaN of the row's."""
+    for C in (40, 40000):
+        kv, _ = new_cache("f16", 2, C, 14)
+        kv[:, 0, 2, :, 0] = -INF
+        kv[1, 0, 2, C // 2, 0] = NAN
+        q = torch.rand((2, HQ, D), generator=gen(15), device=DEV).half() + 0.5
+        lens = torch.full((2,), C, dtype=torch.int32, device=DEV)
+        w = gq.accumulate_weights(q, kv, lens, torch.full((2, HKV, C), 2.0, device=DEV))
+        assert (w[0, 2] == 2.0).all()
+        assert torch.isnan(w[1, 2, C // 2]) and not (w[1, 2] > 2.0).any()
+        others = [h for h in range(HKV) if h != 2]
+        # (2 + w is rounded to FP32: by 2^-22 of itself, a head's sum by no more)
+        total = (w[:, others].double() - 2.0).sum(-1)
+        assert ((total - 4.0).abs() <= C * 2.0 ** -22 + 4 * 2.0 ** -12).all()
