@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const __grid
         exact = s_above[2] != 0u;
         __syncthreads();
       }
-      // exact: as many as needed at or above t
-      threshold = exact ? t - 1u : t;
+      // exact: as many as needed at or above t, which is 0 where the least and the largest
+      // weight differ in their first bit and every number is kept: all but key 0, which is NaN's
+      threshold = exact ? max(t, 1u) - 1u : t;
       need = exact ? 0u : need - over;
     }
   }

@@ -128,3 +128,43 @@ def test_weights_of_minus_infinity_alone(library):  # noqa: F811
         # (2 + w is rounded to FP32: by 2^-22 of itself, a head's sum by no more)
         total = (w[:, others].double() - 2.0).sum(-1)
         assert ((total - 4.0).abs() <= C * 2.0 ** -22 + 4 * 2.0 ** -12).all()
+
+
+# ------------------------------------------------------ eviction: kinds of weights
+
+
+@pytest.mark.parametrize("C", [300, 1024, 3000, 8000, 9000])
+def test_evict_as_many_numbers_as_needed(library, C):  # noqa: F811
+    """Weights of both signs, and NaN, with as many numbers as are needed, one fewer, one more."""
+    first, recent, L = 4, 9, C - 5
+    hi = L - recent
+    keep = C // 3
+    need = keep - first - recent
+    g = gen(C)
+    for extra in (0, -1, 1):
+        w = torch.randn((2, HKV, C), generator=g, device=DEV)
+        w[0, 1] = -w[0, 1].abs()                       # negative ones of every size
+        w[0, 2] = -1.0                                 # one negative value
+        w[0, 3] = w[0, 3].sign()                       # two values
+        w[0, 4] = torch.where(w[0, 4] > 0, INF, -INF)
+        w[0, 5] = torch.where(w[0, 5] > 0, 0.0, -0.0)
+        w[0, 6] = w[0, 6].abs()
+        w[0, 7] = (w[0, 7] * 1e4).floor() * 1e-45      # subnormal, both signs
+        w[1] *= 10.0 ** torch.randint(-30, 30, (HKV, C), generator=g, device=DEV)
+        for b in range(2):
+            for h in range(HKV):
+                between = torch.randperm(hi - first, generator=g, device=DEV) + first
+                w[b, h, between[need + extra:]] = NAN
+        kv, _ = new_cache("f16", 2, C, 16)
+        lens = torch.full((2,), L, dtype=torch.int32, device=DEV)
+        out, ol = torch.zeros((2, 2, HKV, keep, D), dtype=torch.float16, device=DEV), torch.zeros_like(lens)
+        ws = torch.zeros(gq.evict_workspace_size(2, keep), dtype=torch.uint8, device=DEV)
+        kept = torch.full((2, HKV, keep), -9, dtype=torch.int32, device=DEV)
+        gq.evict_kv(kv, lens, w, keep, recent, first, out=out, out_lengths=ol, kept=kept, workspace=ws)
+        assert gq.get_status(ws) == 0
+        for b in range(2):
+            for h in range(HKV):
+                want = kept64(w[b, h].tolist(), L, keep, recent, first)
+                same = kept[b, h].tolist() == want  # (no diff of long lists)
+                assert same, f"row {b} head {h}, {need + extra} numbers for {need}"
+                assert torch.equal(out[b, :, h], kv[b, :, h][:, want])
