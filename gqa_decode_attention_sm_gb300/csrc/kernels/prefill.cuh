@@ -481,6 +481,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   }
   pdl_wait_prior_grid();
   const PfPlan plan = pf_plan(p, (int)blockIdx.x, *reinterpret_cast<PfScan*>(sm.q[0]));
+  // lengths and starts that are out of order are told once, also where no row has a token
+  if (blockIdx.x == 0 && p.c.flags) {
+    for (int b = tid; b < p.c.batch; b += kPfThreads) {
+      const int at = __ldg(p.chunk_starts + b), end = __ldg(p.chunk_starts + b + 1), len = __ldg(p.lens + b);
+      if (at < 0 || end < at || end > p.tokens || len < 0 || len > p.c.capacity || len < end - at)
+        atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
+    }
+  }
   const long long begin = (long long)blockIdx.x * plan.run;
   if (begin >= plan.total) return;  // (all of the block)
   if (warp == 0) {
@@ -497,14 +505,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
-  }
-  // lengths and starts that are out of order are told once
-  if (blockIdx.x == 0 && p.c.flags) {
-    for (int b = tid; b < p.c.batch; b += kPfThreads) {
-      const int at = __ldg(p.chunk_starts + b), end = __ldg(p.chunk_starts + b + 1), len = __ldg(p.lens + b);
-      if (at < 0 || end < at || end > p.tokens || len < 0 || len > p.c.capacity || len < end - at)
-        atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
-    }
   }
   __syncthreads();
   tc_fence_after();

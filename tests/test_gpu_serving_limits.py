@@ -72,6 +72,25 @@ def test_prefill_hidden_int8_scales(library, n, L, page, dtype):  # noqa: F811
             assert (err <= bound).all(), f"{what}: query {j}, worst {float((err / bound).max()):.3f} of the bound"
 
 
+# --------------------------------------------- calls without a token, and flags
+
+
+@pytest.mark.parametrize("starts,lens", [([10, 0, 0], [5, 5]), ([0, 0, 0], [-1, 5]), ([0, 0, 0], [5, 65]),
+                                         ([4, 4, 3], [9, 9]), ([20, 20, 20], [9, 9])])
+def test_prefill_flags_without_tokens(library, starts, lens):  # noqa: F811
+    """What is out of contract is told also where no row has a token."""
+    kv, _ = new_cache("bf16", 2, 64, 8)
+    q = torch.randn((12, HQ, D), generator=gen(9), device=DEV).to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    gq.gqa_prefill(q, kv, torch.tensor(starts, **i32), torch.tensor(lens, **i32), out=out, workspace=ws)
+    assert gq.get_status(ws) == gq.api.FLAG_LENGTH_CLAMPED
+    assert (out == 3.0).all()
+    gq.gqa_prefill(q, kv, torch.zeros(3, **i32), torch.tensor([5, 0], **i32), out=out, workspace=ws)
+    assert gq.get_status(ws) == 0
+
+
 # ------------------------------------------------- weight sums: infinite scores
 
 
