@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import importlib
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -744,19 +745,27 @@ def read_kv_paged(kv_pages, block_table, sequence_lengths, starts=None, out=None
                  workspace)
 
 
+def _int32(x, name):
+    """A whole number that the C interface's int holds."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} {x} is outside [-2^31, 2^31)")
+    return x
+
+
 def prefill_workspace_size() -> int:
     return int(_lib.load().gqa_prefill_workspace_size())
 
 
 def weights_workspace_size(batch: int, capacity: int, q_len: int = 1) -> int:
-    n = _lib.load().gqa_weights_workspace_size(batch, capacity, q_len)
+    n = _lib.load().gqa_weights_workspace_size(_int32(batch, "batch"), _int32(capacity, "capacity"), _int32(q_len, "q_len"))
     if n == 0:
         raise ValueError("invalid batch/capacity/q_len")
     return int(n)
 
 
 def evict_workspace_size(batch: int, keep: int) -> int:
-    n = _lib.load().gqa_evict_workspace_size(batch, keep)
+    n = _lib.load().gqa_evict_workspace_size(_int32(batch, "batch"), _int32(keep, "keep"))
     if n == 0:
         raise ValueError("invalid batch/keep")
     return int(n)
@@ -779,8 +788,8 @@ def _cache_args(kv, block_table, paged, kv_scales, device):
     _require_scales(kv_scales, "kv_scales", kv, kvf)
     if paged:
         _require_table(block_table, None, kv.device)
-    batch = block_table.shape[0] if paged else kv.shape[0]
-    capacity = block_table.shape[1] * kv.shape[3] if paged else kv.shape[3]
+    batch = _int32(block_table.shape[0] if paged else kv.shape[0], "batch")
+    capacity = _int32(block_table.shape[1] * kv.shape[3] if paged else kv.shape[3], "capacity")
     return kvf, _ptr(kv_scales) if kvf in (KV_I8, KV_E2M1) else None, batch, capacity
 
 
@@ -877,7 +886,7 @@ def verify_drafts(probs, drafts, uniforms, draft_probs=None, sequence_lengths=No
         raise TypeError("probs must be a torch.Tensor")
     if not probs.is_cuda or probs.dim() != 3 or probs.dtype not in _PROB:
         raise ValueError("probs must be a CUDA fp32/fp16/bf16 tensor [batch, T, vocab]")
-    B, T, V = probs.shape
+    B, T, V = (_int32(n, name) for n, name in zip(probs.shape, ("batch", "window", "vocab")))
     dev = probs.device
     ps = _prob_strides(probs, "probs", (B, T, V), probs.dtype, dev)
     _require(drafts, "drafts", (B, T - 1), (torch.int32,), dev)
@@ -975,7 +984,7 @@ def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, firs
     _require(kv, "kv_pages" if paged else "kv", None, tuple(_KVF))
     dev = kv.device
     kvf, sc, B, C = _cache_args(kv, block_table, paged, kv_scales, dev)
-    keep = int(keep)
+    keep, recent, first = _int32(keep, "keep"), _int32(recent, "recent"), _int32(first, "first")
     _require(sequence_lengths, "sequence_lengths", (B,), (torch.int32,), dev)
     _require(weights, "weights", (B, HKV, C), (torch.float32,), dev)
     in_place = out is None and out_table is None
@@ -988,6 +997,7 @@ def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, firs
         osc, out_capacity = _ptr(out_scales) if kvf in (KV_I8, KV_E2M1) else None, out.shape[3]
     if out_table is not None:
         _require_table(out_table, B, dev)
+        _int32(out_table.shape[1] * kv.shape[3], "slots of out_table")
     if in_place:
         if out_lengths is not None or out_weights is not None or out_scales is not None:
             raise ValueError("an eviction in place has no out_lengths, out_weights or out_scales")
@@ -1000,7 +1010,7 @@ def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, firs
         _require(out_weights, "out_weights", None, (torch.float32,), dev)
         if out_weights.dim() != 3 or out_weights.shape[:2] != (B, HKV):
             raise ValueError(f"out_weights must be [{B}, {HKV}, slots], got {tuple(out_weights.shape)}")
-        wcap = out_weights.shape[2]
+        wcap = _int32(out_weights.shape[2], "slots of out_weights")
     nbytes = evict_workspace_size(B, keep)
     if kept is None:
         kept = torch.empty((B, HKV, keep), dtype=torch.int32, device=dev)
@@ -1009,7 +1019,7 @@ def _evict(kv, block_table, paged, sequence_lengths, weights, keep, recent, firs
     lib = _lib.load()
     ol = None if in_place else _ptr(out_lengths)
     ow = None if out_weights is None else _ptr(out_weights)
-    tail = (wcap, keep, int(recent), int(first), _ptr(workspace), workspace.numel())
+    tail = (wcap, keep, recent, first, _ptr(workspace), workspace.numel())
     with _current(dev):
         if paged:
             _lib.check(lib.gqa_evict_kv_paged(

@@ -187,3 +187,27 @@ def test_evict_as_many_numbers_as_needed(library, C):  # noqa: F811
                 same = kept[b, h].tolist() == want  # (no diff of long lists)
                 assert same, f"row {b} head {h}, {need + extra} numbers for {need}"
                 assert torch.equal(out[b, :, h], kv[b, :, h][:, want])
+
+
+# -------------------------------------------------- sizes past what an int holds
+
+
+def test_sizes_past_an_int(library):  # noqa: F811
+    kv, _ = new_cache("bf16", 1, 64, 60)
+    lens = torch.tensor([64], dtype=torch.int32, device=DEV)
+    w = torch.zeros((1, HKV, 64), device=DEV)
+    for bad in (dict(recent=2 ** 32 + 2), dict(first=2 ** 32), dict(recent=-2 ** 32 + 1), dict(first=2 ** 31)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            gq.evict_kv(kv, lens, w, 10, **bad)
+        with pytest.raises(ValueError, match="2\\^31"):
+            gq.evict_kv_paged(kv, torch.zeros((1, 1), dtype=torch.int32, device=DEV), lens, w, 10, **bad)
+    for bad in (dict(recent=1.5), dict(first="1")):
+        with pytest.raises(TypeError):
+            gq.evict_kv(kv, lens, w, 10, **bad)
+    assert int(lens) == 64
+    with pytest.raises(ValueError, match="2\\^31"):
+        gq.evict_kv(kv, lens, w, 2 ** 32 + 8)
+    with pytest.raises(ValueError, match="2\\^31"):  # (8 GB)
+        gq.verify_drafts(torch.zeros((1, 1, 2 ** 32 + 5), dtype=torch.float16, device=DEV),
+                         torch.zeros((1, 0), dtype=torch.int32, device=DEV), torch.zeros((1, 1), device=DEV))
+    torch.cuda.empty_cache()
