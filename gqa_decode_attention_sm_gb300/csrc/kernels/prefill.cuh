@@ -10,8 +10,8 @@
 // tile's softmax runs the tensor cores work on the other.  The products of one thread
 // run in order, so "S0' is there" says that O0 is complete, and a row's O may be
 // rescaled then without another barrier.  It is rescaled only when its maximum grows
-// by more than 8 (weights up to 2^15: with a maximum at 2^7, small weights of an fp16
-// P stay normal numbers down to 2^-21 of the largest).
+// by more than 8 (weights of an fp16 P up to 2^15: with a maximum at 2^7, small ones stay
+// normal numbers down to 2^-21 of the largest; of a bf16 P up to 1).
 //
 // K and V tiles go through a ring of five 32 KB slots in the 128-byte swizzled layout.
 // 16-bit caches come by TMA (a box of 128 rows, or of a page's), and two warps look at
@@ -61,8 +61,12 @@ constexpr int kPfMaxCtas = 160;
 constexpr int kPfMinRun = 2;         // K/V tiles a CTA takes at least
 constexpr int kPfUnitCost = 4;       // what a unit costs besides its tiles (q, the first product, the output), in tiles
 constexpr int kPfFewTiles = 4;       // tiles a CTA up to which that is not counted (every CTA then has about one piece)
-constexpr float kPfLift = 7.f;       // log2 of the weight of a row's maximum
 constexpr float kPfGrow = 8.f;       // growth of the maximum that a row is rescaled for
+// log2 of the weight of a row's maximum.  fp16: 7, so that weights down to 2^-21 of the
+// largest are normal numbers, and 2^(7 + 8) is one too.  bf16 has FP32's range: -8, so that
+// no weight is above 1 and a row's sum of weight * |V| no larger than with the exact
+// maximum (V may be as large as the type's largest).
+__host__ __device__ constexpr float pf_lift(bool bf16) { return bf16 ? -kPfGrow : 7.f; }
 
 struct PrefillParams {
   CacheView c;
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
           }
         }
-        const float minus = kPfLift - (m == -INFINITY ? 0.f : m);
+        const float minus = pf_lift(MF == kQBF16) - (m == -INFINITY ? 0.f : m);
         const float2 scale2 = make_float2(scale, scale), minus2 = make_float2(minus, minus);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll

@@ -531,7 +531,8 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
  * GQA_FLAG_LENGTH_CLAMPED; a query with no slot (n above the length) gets a zero
  * row and sets it too.  Formats, scales and q_scale as gqa_decode_verify, but no
  * rule on the capacity of an int8 or e2m1 cache.  Scores, maximum and sum are
- * FP32; each softmax weight is rounded where it meets V, to bf16 over a bf16 cache,
+ * FP32 (the sum over the slots of weight * |V|, the largest weight being 1, has to be
+ * below FP32's largest number); each softmax weight is rounded where it meets V, to bf16 over a bf16 cache,
  * else to fp16 (by 2^-11 of itself down to 2^-21 of the largest, by 2^-32 of the
  * largest below).  int8: what is rounded is the weight times its slot's V scale, and
  * the largest weight times the largest V scale that the query sees (2^-61 at least)

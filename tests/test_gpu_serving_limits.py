@@ -72,6 +72,33 @@ def test_prefill_hidden_int8_scales(library, n, L, page, dtype):  # noqa: F811
             assert (err <= bound).all(), f"{what}: query {j}, worst {float((err / bound).max()):.3f} of the bound"
 
 
+# ------------------------------------------------ prompt attention: large values
+
+
+@pytest.mark.parametrize("n,L", [(70, 300), (40, 20000), (5, 129)])
+def test_prefill_largest_bf16_values(library, n, L):  # noqa: F811
+    """bf16 values up to the type's largest: weights are held at 1 or less, so a row's
+    sum of weight * |V| stays what FP32 holds."""
+    kv, _ = new_cache("bf16", 1, L, 5)
+    q = torch.randn((n, HQ, D), generator=gen(6), device=DEV).to(torch.bfloat16)
+    starts, lens = torch.tensor([0, n], dtype=torch.int32, device=DEV), torch.tensor([L], dtype=torch.int32, device=DEV)
+    half = 2.0 ** -8
+    big = torch.finfo(torch.bfloat16).max
+    for what in ("one", "all"):
+        x = kv.clone()
+        if what == "one":
+            x[0, 1, :, 3] = big
+            x[0, 1, :, L - n + 1, ::2] = -big
+        else:
+            x[0, 1] *= 2.0 ** 108  # (20000 * 2^108 * 5 < 2^127)
+        out = gq.gqa_prefill(q, x, starts, lens)
+        for j in (0, 1, n // 2, n - 1):
+            ref, a, e = attend64(q[j], x[0, 0].double(), x[0, 1].double(), L - n + j + 1)
+            assert float(ref.abs().max()) < big / 2
+            err = (out[j].double() - ref).abs()
+            assert (err <= half * ref.abs() + (half + 2 * e + 2 ** -18) * a).all(), f"{what}: query {j}"
+
+
 # --------------------------------------------- calls without a token, and flags
 
 
