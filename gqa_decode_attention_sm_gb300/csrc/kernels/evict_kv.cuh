@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
   const int lane = threadIdx.x % kPer, first = chunk * kRows;
   const int32_t* kept = p.kept + (size_t)unit * p.keep;
   const float* w = p.weights + (size_t)unit * p.src.capacity;
+  bool strayed = false;
   uint4 x[kIter];
   uint2 sc[kIter];
   float wt[kIter];
@@ -450,7 +451,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
   for (int k = 0; k < kIter; ++k) {
     const int at = first + k * kStep + threadIdx.x / kPer;
     if (at >= n) continue;
-    const int t = min(max(kept[at], 0), p.src.capacity - 1);  // (a slot, whatever the caller's kept was written with since)
+    // a slot of the row, as the select kernel wrote it; another one (the caller's other
+    // work, or a mistake here) is left inside the row and told
+    const int said = kept[at];
+    const int t = min(max(said, 0), L - 1);
+    strayed |= t != said;
     const size_t row = cache_row(p.src, b, pg, t);
     x[k] = *(reinterpret_cast<const uint4*>(p.src.kv) + row * kPer + lane);
     if (lane == 0) {
@@ -491,6 +496,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
       if (plane == 0 && p.out_weights) p.out_weights[(size_t)unit * p.weights_capacity + at] = wt[k];
     }
   }
+  if (strayed && p.flags) atomicOr(p.flags, GQA_FLAG_BOUNDS);
   // slots behind the kept ones start their sums at zero (in place: those that held tokens)
   if (plane == 0 && p.out_weights) {
     const int end = chunk < p.chunks - 1 ? first + kRows : (p.in_place ? L : p.weights_capacity);

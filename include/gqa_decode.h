@@ -108,8 +108,9 @@ typedef enum {
 #define GQA_FLAG_WAIT_TIMEOUT 0x2u    /* a pipeline wait gave up; outputs are invalid */
 #define GQA_FLAG_PAGE_CLAMPED 0x4u    /* a block-table entry was outside [0, num_pages) (decode: clamped; append: not written) */
 #define GQA_FLAG_SLOT_CLAMPED 0x8u    /* gqa_append_kv: a slot outside [0, capacity), not written */
-#define GQA_FLAG_BOUNDS 0x10u         /* checked builds only (GQA_CHECKED): an access fell outside its
-                                         buffer and was redirected inside it; the library has a bug */
+#define GQA_FLAG_BOUNDS 0x10u         /* checked builds (GQA_CHECKED): an access fell outside its buffer and was
+                                         redirected inside it; the library has a bug.  Any build: an eviction's
+                                         list of kept slots was no longer what the call had written */
 
 /* Name of a status code (static string). */
 const char* gqa_status_string(gqa_status_t status);
@@ -532,13 +533,14 @@ gqa_status_t gqa_read_kv_paged(const void* kv_pages, gqa_kv_format_t kv_format, 
  * row and sets it too.  Formats, scales and q_scale as gqa_decode_verify, but no
  * rule on the capacity of an int8 or e2m1 cache.  Scores, maximum and sum are
  * FP32 (the sum over the slots of weight * |V|, the largest weight being 1, has to be
- * below FP32's largest number); each softmax weight is rounded where it meets V, to bf16 over a bf16 cache,
- * else to fp16 (by 2^-11 of itself down to 2^-21 of the largest, by 2^-32 of the
- * largest below).  int8: what is rounded is the weight times its slot's V scale, and
- * the largest weight times the largest V scale that the query sees (2^-61 at least)
- * takes the largest's place: by 2^-11 of itself down to 2^-20 of that product, by
- * 2^-31 of it below.  A value, key or scale that a query does not see never reaches its
- * output, whatever it holds.
+ * below FP32's largest number); each softmax weight is rounded where it meets V, to
+ * bf16 over a bf16 cache, else to fp16 (by 2^-11 of itself down to 2^-21 of the
+ * largest, by 2^-32 of the largest below).  int8: what is rounded is the weight times
+ * its slot's V scale, and the largest weight times the largest V scale that the query
+ * sees (2^-61 at least; 2^100 at most, above it small weights are lost) takes the
+ * largest's place: by 2^-11 of itself down to 2^-20 of that product, by 2^-31 of it
+ * below.  A value, key or scale that a query does not see never reaches its output,
+ * whatever it holds.
  * q, kv, out and the workspace 16-byte aligned (int8 scales 2, e2m1 scales 8);
  * nothing written overlaps anything else.  The workspace holds
  * gqa_prefill_workspace_size() bytes whatever the sizes; its header as
