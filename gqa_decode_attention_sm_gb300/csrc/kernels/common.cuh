@@ -87,8 +87,8 @@ __host__ __device__ inline int split_count(int capacity, int num_splits, int kv_
 
 // Checked builds (compiled with -DGQA_CHECKED; the product library is not):
 // every global-memory access whose place is computed (cache rows and scales,
-// partial results, outputs, and in the write and read-back kernels every load and
-// store) is tested against the extent of its buffer first.  One outside it sets
+// partial results, outputs, and in the write, read-back and serving kernels every load
+// and store) is tested against the extent of its buffer first.  One outside it sets
 // GQA_FLAG_BOUNDS in the status word and is redirected to an address inside the
 // buffer (or left out), so a bad index is reported and nothing faults.  The tests run their cases through such a
 // build and require the flag never to be set.
@@ -113,6 +113,23 @@ __device__ __forceinline__ T* in_buffer(T* p, size_t bytes, const void* base, si
     }
   }
   return p;
+}
+
+// Element i of a row of `width` in an array of `rows` of them, the same way.
+template <class T>
+__device__ __forceinline__ T* cell(T* row, int i, size_t width, T* base, size_t rows, uint32_t* flags) {
+  if constexpr (kChecked) {
+    if (i < 0 || (size_t)i >= width || !in_extent(base, rows * width * sizeof(T), row + i, sizeof(T))) {
+      if (flags) atomicOr(flags, GQA_FLAG_BOUNDS);
+      return base;
+    }
+  }
+  return row + i;
+}
+// Element i of n.
+template <class T>
+__device__ __forceinline__ T* item(T* base, int i, int n, uint32_t* flags) {
+  return cell(base, i, (size_t)n, base, 1, flags);
 }
 
 // Default bound of a pipeline wait (a healthy wait lasts microseconds).

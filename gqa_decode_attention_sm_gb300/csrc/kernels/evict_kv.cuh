@@ -53,6 +53,16 @@ struct EvictParams {
   int in_place;
   int cluster;  // CTAs that share a head
   int held;  // weights a CTA of the select kernel holds in shared memory (0: reads them each time)
+  __device__ __forceinline__ int32_t* kept_at(int32_t* row, int i) const {  // row: kept + unit * keep
+    return cell(row, i, (size_t)keep, kept, (size_t)batch * kHkv, flags);
+  }
+  __device__ __forceinline__ float* out_weight(int unit, int i) const {
+    return cell(out_weights + (size_t)unit * weights_capacity, i, (size_t)weights_capacity, out_weights, (size_t)batch * kHkv, flags);
+  }
+  __device__ __forceinline__ uint32_t* read_flag(int up, int i) const {  // up: unit * 2 + plane
+    return cell(read_flags + (size_t)up * chunks, i, (size_t)chunks, read_flags, (size_t)batch * kHkv * 2, flags);
+  }
+  __device__ __forceinline__ int32_t* old_len(int b) const { return item(old_lens, b, batch, flags); }
 };
 
 // Integers in the order of the weights; NaN below everything, both zeros one.
@@ -79,18 +89,21 @@ __device__ __forceinline__ uint32_t head_ld(const uint32_t* p, int S, int rank) 
 // flags cleared, the slots that are kept anyway.  Returns the slots held; `keep` or
 // fewer need no choice.
 __device__ __forceinline__ int select_begin(const EvictParams& p, int unit, int first, int step) {
-  const int b = unit / kHkv, L = clamp_length(__ldg(p.lens + b), p.src.capacity, p.flags, unit % kHkv == 0 && first == 0);
-  int32_t* kept = p.kept + (size_t)unit * p.keep;
-  if (first == 0 && unit % kHkv == 0) p.old_lens[b] = L;
+  const int b = unit / kHkv;
+  const int L = clamp_length(__ldg(item(p.lens, b, p.batch, p.flags)), p.src.capacity, p.flags,
+                             unit % kHkv == 0 && first == 0);
+  int32_t* const kept = p.kept + (size_t)unit * p.keep;
+  if (first == 0 && unit % kHkv == 0) *p.old_len(b) = L;
   if (p.in_place) {
-    for (int i = first; i < 2 * p.chunks; i += step) p.read_flags[(size_t)unit * 2 * p.chunks + i] = 0u;
+    for (int i = first; i < 2 * p.chunks; i += step)
+      *cell(p.read_flags + (size_t)unit * 2 * p.chunks, i, (size_t)2 * p.chunks, p.read_flags, (size_t)p.batch * kHkv, p.flags) = 0u;
     if (unit == 0 && first == 0) *p.ticket = 0u;
   }
   if (L <= p.keep) {
-    for (int i = first; i < p.keep; i += step) kept[i] = i < L ? i : -1;
+    for (int i = first; i < p.keep; i += step) *p.kept_at(kept, i) = i < L ? i : -1;
   } else {  // first + recent <= keep < L
     for (int i = first; i < p.first + p.recent; i += step)
-      kept[i < p.first ? i : p.keep - p.recent + (i - p.first)] = i < p.first ? i : L - p.recent + (i - p.first);
+      *p.kept_at(kept, i < p.first ? i : p.keep - p.recent + (i - p.first)) = i < p.first ? i : L - p.recent + (i - p.first);
   }
   return L;
 }
@@ -251,7 +264,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const __grid
   above = __reduce_add_sync(0xffffffffu, lane < warp ? s_above[lane % kWarps] : 0u);
   equal = __reduce_add_sync(0xffffffffu, lane < warp ? s_equal[lane % kWarps] : 0u);
   above += min(equal, need);  // those on the threshold that the warps before keep
-  int32_t* kept = p.kept + (size_t)unit * p.keep;
+  int32_t* const kept = p.kept + (size_t)unit * p.keep;
   const uint32_t before = (1u << lane) - 1;
 #pragma unroll
   for (int i = 0; i < K; ++i) {
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) select_few_kernel(const __grid
     }
     if (chosen >> lane & 1) {
       const uint32_t to = (uint32_t)p.first + above + __popc(chosen & before);
-      if (to < (uint32_t)p.keep) kept[to] = at + 32 * i;  // (always; every address here is held in bounds)
+      if (kChecked || to < (uint32_t)p.keep) *p.kept_at(kept, (int)to) = at + 32 * i;  // (always; held in bounds)
     }
     above += __popc(chosen);
   }
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_
   const int C = p.src.capacity;
   const int L = select_begin(p, unit, rank * kSelectThreads + tid, S * kSelectThreads);
   if (L <= p.keep) return;  // (the same in every CTA of the cluster)
-  int32_t* kept = p.kept + (size_t)unit * p.keep;
+  int32_t* const kept = p.kept + (size_t)unit * p.keep;
   const int lo = p.first, hi = L - p.recent;
   const float* w = p.weights + (size_t)unit * C;
   const size_t w_extent = (size_t)p.batch * kHkv * C * 4;
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kv_kernel(const __grid_
     const uint32_t rank_eq = equal + __popc(eq & before);
     if (in && (x > threshold || (x == threshold && rank_eq < need))) {
       const uint32_t at = (uint32_t)p.first + above + __popc(gt & before) + min(rank_eq, need);
-      if (at < (uint32_t)p.keep) kept[at] = lo + i + lane;  // (always; every address here is held in bounds)
+      if (kChecked || at < (uint32_t)p.keep) *p.kept_at(kept, (int)at) = lo + i + lane;  // (always; held in bounds)
     }
     above += __popc(gt);
     equal += __popc(eq);
@@ -436,12 +449,13 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
   }
   const int chunk = (int)(job % (uint32_t)p.chunks);
   const int up = (int)(job / (uint32_t)p.chunks), plane = up & 1, unit = up >> 1, b = unit / kHkv;
-  const int L = min(max(p.old_lens[b], 0), p.src.capacity), n = min(L, p.keep);
+  const int L = min(max(*p.old_len(b), 0), p.src.capacity), n = min(L, p.keep);
   const int pg = plane * kHkv + unit % kHkv;
-  if (unit % kHkv == 0 && plane == 0 && chunk == 0 && threadIdx.x == 0) p.out_lens[b] = n;
+  if (unit % kHkv == 0 && plane == 0 && chunk == 0 && threadIdx.x == 0)
+    *item(p.out_lens, b, p.batch, p.flags) = n;
   if (p.in_place && L <= p.keep) return;  // nothing moves
   const int lane = threadIdx.x % kPer, first = chunk * kRows;
-  const int32_t* kept = p.kept + (size_t)unit * p.keep;
+  int32_t* const kept = p.kept + (size_t)unit * p.keep;
   const float* w = p.weights + (size_t)unit * p.src.capacity;
   bool strayed = false;
   uint4 x[kIter];
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
     if (at >= n) continue;
     // a slot of the row, as the select kernel wrote it; another one (the caller's other
     // work, or a mistake here) is left inside the row and told
-    const int said = kept[at];
+    const int said = *p.kept_at(kept, at);
     const int t = min(max(said, 0), L - 1);
     strayed |= t != said;
     const size_t row = cache_row(p.src, b, pg, t);
@@ -461,17 +475,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
     if (lane == 0) {
       if constexpr (KVF == kKvI8) sc[k].x = static_cast<const uint16_t*>(p.src.scales)[row];
       if constexpr (KVF == kKvE2M1) sc[k] = static_cast<const uint2*>(p.src.scales)[row];
-      if (plane == 0 && p.out_weights) wt[k] = w[t];
+      if (plane == 0 && p.out_weights)
+        wt[k] = *cell(w, t, (size_t)p.src.capacity, p.weights, (size_t)p.batch * kHkv, p.flags);
     }
   }
   if (p.in_place) {
-    uint32_t* read = p.read_flags + (size_t)up * p.chunks;
     __threadfence();  // this thread's reads come before the flag
     __syncthreads();
-    if (threadIdx.x == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(read + chunk), "r"(1u) : "memory");
+    if (threadIdx.x == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p.read_flag(up, chunk)), "r"(1u) : "memory");
     const uint64_t deadline = global_timer_ns() + kWaitBudgetNs;
     for (int c = threadIdx.x; c < chunk; c += kMoveThreads)
-      while (load_acquire(read + c) == 0u)
+      while (load_acquire(p.read_flag(up, c)) == 0u)
         if (global_timer_ns() > deadline) {
           s_late = 1;
           break;
@@ -493,7 +507,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
     if (lane == 0) {
       if constexpr (KVF == kKvI8) static_cast<uint16_t*>(const_cast<void*>(p.dst.scales))[row] = (uint16_t)sc[k].x;
       if constexpr (KVF == kKvE2M1) static_cast<uint2*>(const_cast<void*>(p.dst.scales))[row] = sc[k];
-      if (plane == 0 && p.out_weights) p.out_weights[(size_t)unit * p.weights_capacity + at] = wt[k];
+      if (plane == 0 && p.out_weights) *p.out_weight(unit, at) = wt[k];
     }
   }
   if (strayed && p.flags) atomicOr(p.flags, GQA_FLAG_BOUNDS);
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kv_kernel(const __grid_cons
   if (plane == 0 && p.out_weights) {
     const int end = chunk < p.chunks - 1 ? first + kRows : (p.in_place ? L : p.weights_capacity);
     for (int at = max(first, n) + threadIdx.x; at < end; at += kMoveThreads)
-      p.out_weights[(size_t)unit * p.weights_capacity + at] = 0.f;
+      *p.out_weight(unit, at) = 0.f;
   }
   // (kept[] of a row shorter than `keep` ends in -1, written by the select kernel)
 }

@@ -68,6 +68,8 @@ constexpr float kPfGrow = 8.f;       // growth of the maximum that a row is resc
 // maximum (V may be as large as the type's largest).
 __host__ __device__ constexpr float pf_lift(bool bf16) { return bf16 ? -kPfGrow : 7.f; }
 
+constexpr size_t kPfTokenBytes = kHq * kD * 2;  // of a token of q or out
+
 struct PrefillParams {
   CacheView c;
   const void* q;                // [tokens, 32, 128]
@@ -80,6 +82,25 @@ struct PrefillParams {
   int box;                      // rows loaded together: a tile's, or a page's if it is smaller
   float scale_log2, v_scale;
 };
+
+// Checked: a piece's partial output, and a row's maximum and sum.
+__device__ __forceinline__ float* pf_part(const PrefillParams& p, float* at) {
+  return in_buffer(at, 4, p.part_o, (size_t)2 * p.ctas * kD * 2 * kPfRows * 4, p.c.flags);
+}
+__device__ __forceinline__ float2* pf_part_ml(const PrefillParams& p, float2* at) {
+  return in_buffer(at, 8, p.part_ml, (size_t)2 * p.ctas * 2 * kPfRows * 8, p.c.flags);
+}
+// The cache's row that a box starts at.  (A contiguous cache's last boxes may reach past its
+// last row, and past a row's length start behind it: the copy fills those with zeros.)
+__device__ __forceinline__ int pf_box_row(const PrefillParams& p, size_t row, bool held) {
+  if constexpr (kChecked) {
+    if (held && row >= p.c.rows) {
+      if (p.c.flags) atomicOr(p.c.flags, GQA_FLAG_BOUNDS);
+      return 0;
+    }
+  }
+  return (int)row;
+}
 
 // ---- the schedule ----------------------------------------------------------
 
@@ -107,9 +128,10 @@ struct PfRow {
 
 __device__ __forceinline__ PfRow pf_row(const PrefillParams& p, int b) {
   PfRow r;
-  r.at = min(max(__ldg(p.chunk_starts + b), 0), p.tokens);
-  r.n = min(max(__ldg(p.chunk_starts + b + 1), r.at), p.tokens) - r.at;
-  r.len = min(max(__ldg(p.lens + b), 0), p.c.capacity);
+  const auto start = [&](int i) { return __ldg(item(p.chunk_starts, i, p.c.batch + 1, p.c.flags)); };
+  r.at = min(max(start(b), 0), p.tokens);
+  r.n = min(max(start(b + 1), r.at), p.tokens) - r.at;
+  r.len = min(max(__ldg(item(p.lens, b, p.c.batch, p.c.flags)), 0), p.c.capacity);
   r.base = r.len - r.n;
   return r;
 }
@@ -551,8 +573,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int row = (warp & 3) * 32 + 2 * i + (lane >> 4), tok = sg.m * kPfTokens + t * 32 + row / 4;
         x[i] = make_uint4(0, 0, 0, 0);
         if (tok < sg.row.n)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                      ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + piece);
+          x[i] = __ldg(in_buffer(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                                ((size_t)(sg.row.at + tok) * kHq + 4 * sg.g + (row & 3)) * kD) + piece,
+                                 16, p.q, p.tokens * kPfTokenBytes, p.c.flags));
       }
       if constexpr (kNarrow && QF == kQBF16) {
         // by a power of two into fp16's range: a row's largest |q| into [2^14, 2^15)
@@ -761,15 +784,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (r / 4 < tokens) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + out_at + (size_t)(r / 4) * kHq * kD) + 4 * k + (lane & 3);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i * (kD / 8)] = c[i];
+            for (int i = 0; i < 4; ++i) *in_buffer(dst + i * (kD / 8), 16, p.out, p.tokens * kPfTokenBytes, p.c.flags) = c[i];
           }
         } else {
           float* dst = p.part_o + ((size_t)slot * kD + 32 * k) * (2 * kPfRows) + t * kPfRows + r;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) dst[i * (2 * kPfRows)] = __uint_as_float(o[i]);
+          for (int i = 0; i < 32; ++i) *pf_part(p, dst + i * (2 * kPfRows)) = __uint_as_float(o[i]);
         }
       }
-      if (!whole) p.part_ml[(size_t)slot * (2 * kPfRows) + t * kPfRows + r] = make_float2(m, l);
+      if (!whole) *pf_part_ml(p, p.part_ml + (size_t)slot * (2 * kPfRows) + t * kPfRows + r) = make_float2(m, l);
     }
   } else if (warp == 8) {
     // ----------------------------------------------------------- products
@@ -863,7 +886,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const auto page_of = [&](int j) {  // of the lane's box
         const int t = j * kPfTile + lane * p.box;
         return lane < kPfTile / p.box && t < l_len
-                   ? __ldg(p.c.block_table + (size_t)la.b * p.c.max_pages + (t >> p.c.page_log2))
+                   ? __ldg(cell(p.c.block_table + (size_t)la.b * p.c.max_pages, t >> p.c.page_log2, (size_t)p.c.max_pages,
+                                p.c.block_table, (size_t)p.c.batch, p.c.flags))
                    : 0;
       };
       const auto load = [&]() {  // false: the run's end
@@ -887,9 +911,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         l_row = -1;
         if (p.c.block_table == nullptr) {
-          if (lane == 0) l_row = (int)(((size_t)la.b * 2 * kHkv + pg) * p.c.capacity + t0);
+          if (lane == 0) l_row = pf_box_row(p, ((size_t)la.b * 2 * kHkv + pg) * p.c.capacity + t0, t0 < l_len);
         } else if (lane < kPfTile / p.box && t0 + lane * p.box < l_len) {
-          l_row = (int)((((size_t)ids * 2 * kHkv + pg) << p.c.page_log2) + ((t0 + lane * p.box) & ((1 << p.c.page_log2) - 1)));
+          l_row = pf_box_row(p, (((size_t)ids * 2 * kHkv + pg) << p.c.page_log2) + ((t0 + lane * p.box) & ((1 << p.c.page_log2) - 1)),
+                             true);
         }
         if (!wait(&sm.raw_empty[raw], (l_item / kRaws & 1) ^ 1)) return false;
         const uint32_t some = __ballot_sync(0xffffffffu, l_row >= 0);
@@ -1026,7 +1051,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const int pg = plane * kHkv + sg.g;
               int row = -1;
               if (p.c.block_table == nullptr) {
-                if (lane == 0) row = (int)(((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0);
+                if (lane == 0) row = pf_box_row(p, ((size_t)sg.b * 2 * kHkv + pg) * p.c.capacity + t0, t0 < len);
               } else if (lane < kPfTile / p.box && t0 + lane * p.box < len) {
                 row = (int)cache_row(p.c, sg.b, pg, t0 + lane * p.box);
               }
@@ -1138,7 +1163,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
     float x[2 * kSide];
 #pragma unroll
     for (int k = 0; k < 2 * kSide; ++k)
-      x[k] = k0 + k < s_pieces ? p.part_ml[(size_t)slot_of(k0 + k) * (2 * kPfRows) + row].x : -INFINITY;
+      x[k] = k0 + k < s_pieces ? pf_part_ml(p, p.part_ml + (size_t)slot_of(k0 + k) * (2 * kPfRows) + row)->x : -INFINITY;
 #pragma unroll
     for (int k = 0; k < 2 * kSide; ++k) m = fmaxf(m, x[k]);
   }
@@ -1153,10 +1178,10 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
       ml[k] = make_float2(-INFINITY, 0.f);
       if (k0 + k < s_pieces) {
         const int slot = slot_of(k0 + k);
-        ml[k] = p.part_ml[(size_t)slot * (2 * kPfRows) + row];
-        const float* src = p.part_o + ((size_t)slot * kD + kMergeDims * warp) * (2 * kPfRows) + row;
+        ml[k] = *pf_part_ml(p, p.part_ml + (size_t)slot * (2 * kPfRows) + row);
+        float* src = p.part_o + ((size_t)slot * kD + kMergeDims * warp) * (2 * kPfRows) + row;
 #pragma unroll
-        for (int i = 0; i < kMergeDims; ++i) y[k][i] = src[i * (2 * kPfRows)];
+        for (int i = 0; i < kMergeDims; ++i) y[k][i] = *pf_part(p, src + i * (2 * kPfRows));
       }
     }
 #pragma unroll
@@ -1177,7 +1202,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefill_merge_kernel(const __gr
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = round2<QF>(o[8 * i + 2 * e] * f, o[8 * i + 2 * e + 1] * f);
-    dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    *in_buffer(dst + i, 16, p.out, p.tokens * kPfTokenBytes, p.c.flags) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

@@ -126,7 +126,8 @@ __device__ __forceinline__ void score_rows(const WeightParams& p, int q_len, int
     for (int i = 0; i < 4; ++i) {
       uint4 x = make_uint4(0, 0, 0, 0);
       if (col < cols)
-        x = __ldg(reinterpret_cast<const uint4*>(src + (8 * i / kRun) * 4 * kRun + c * kRun + 8 * i % kRun));
+        x = __ldg(in_buffer(reinterpret_cast<const uint4*>(src + (8 * i / kRun) * 4 * kRun + c * kRun + 8 * i % kRun), 16, p.q,
+                            (size_t)p.c.batch * q_len * kHq * kD * 2, p.c.flags));
       q[nt][4 * i] = x.x;
       q[nt][4 * i + 1] = x.y;
       q[nt][4 * i + 2] = x.z;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_co
   pdl_wait_prior_grid();
   const int b = blockIdx.z, g = blockIdx.y, C = p.c.capacity, cols = 4 * q_len;
   const bool tell = blockIdx.x == 0 && g == 0 && threadIdx.x == 0;
-  const int len = clamp_length(__ldg(p.lens + b), C, p.c.flags, tell);
+  const int len = clamp_length(__ldg(item(p.lens, b, p.c.batch, p.c.flags)), C, p.c.flags, tell);
   if (len < q_len && tell && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
   const int begin = blockIdx.x * p.chunk, end = min(len, begin + p.chunk);
   if (begin >= len) return;
@@ -267,7 +268,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_kv_kernel(const __grid_co
   score_rows<KVF, QF, NT>(p, q_len, b, g, len, begin, end, s_stats, [&](int t, int col, float2 s) {
     *reinterpret_cast<float2*>(in_buffer(out + (size_t)t * cols + col, 8, p.scores, extent, p.c.flags)) = s;
   });
-  if (threadIdx.x < cols) p.stats[(unit * p.chunks + blockIdx.x) * cols + threadIdx.x] = s_stats[0][threadIdx.x];
+  if (threadIdx.x < cols)
+    *cell(p.stats + (unit * p.chunks + blockIdx.x) * cols, (int)threadIdx.x, (size_t)cols, p.stats,
+          (size_t)p.c.batch * kHkv * p.chunks, p.c.flags) = s_stats[0][threadIdx.x];
 }
 
 // A cluster of CTAs a (row, KV head); a CTA's slots are an equal part of the
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kScoreThreads) fused_weights_kernel(const __gr
   const size_t unit = blockIdx.x / S;
   const int b = (int)(unit / kHkv), g = (int)(unit % kHkv), C = p.c.capacity, cols = 4 * q_len;
   const bool tell = rank == 0 && g == 0 && threadIdx.x == 0;
-  const int len = clamp_length(__ldg(p.lens + b), C, p.c.flags, tell);
+  const int len = clamp_length(__ldg(item(p.lens, b, p.c.batch, p.c.flags)), C, p.c.flags, tell);
   if (len < q_len && tell && p.c.flags) atomicOr(p.c.flags, GQA_FLAG_LENGTH_CLAMPED);
   if (len == 0) return;  // (all of the cluster)
   const int part = ((len + S - 1) / S + kSlab - 1) / kSlab * kSlab;
@@ -333,21 +336,24 @@ __global__ void __launch_bounds__(kSumThreads) sum_weights_kernel(const __grid_c
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const int b = blockIdx.z, g = blockIdx.y, C = p.c.capacity;
-  const int len = min(max(__ldg(p.lens + b), 0), C);
+  const int len = min(max(__ldg(item(p.lens, b, p.c.batch, p.c.flags)), 0), C);
   const int begin = blockIdx.x * kSumSlots, end = min(len, begin + kSumSlots);
   if (begin >= len) return;
   const size_t unit = (size_t)b * kHkv + g;
   const int used = (len + p.chunk - 1) / p.chunk;
-  const float2* stats = p.stats + unit * p.chunks * COLS;
+  float2* const stats = p.stats + unit * p.chunks * COLS;
+  const auto stat = [&](int k, int col) {
+    return cell(stats + (size_t)k * COLS, col, COLS, p.stats, (size_t)p.c.batch * kHkv * p.chunks, p.c.flags);
+  };
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   for (int col = warp; col < COLS; col += kSumThreads / 32) {
     float m = -INFINITY;
-    for (int k = lane; k < used; k += 32) m = fmaxf(m, stats[(size_t)k * COLS + col].x);
+    for (int k = lane; k < used; k += 32) m = fmaxf(m, stat(k, col)->x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
     for (int k = lane; k < used; k += 32) {
-      const float2 x = stats[(size_t)k * COLS + col];
+      const float2 x = *stat(k, col);
       if (x.y != 0.f) l += x.y * ex2(x.x - m);  // (a NaN sum is not 0)
     }
 #pragma unroll
@@ -360,7 +366,8 @@ __global__ void __launch_bounds__(kSumThreads) sum_weights_kernel(const __grid_c
   __syncthreads();
   const size_t extent = (size_t)p.c.batch * kHkv * C * 4;
   for (int t = begin + threadIdx.x; t < end; t += kSumThreads) {
-    const float4* src = reinterpret_cast<const float4*>(p.scores + (unit * C + t) * COLS);
+    const float4* src = reinterpret_cast<const float4*>(
+        in_buffer(p.scores + (unit * C + t) * COLS, COLS * 4, p.scores, (size_t)p.c.batch * kHkv * C * COLS * 4, p.c.flags));
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < COLS / 4; ++j) {

@@ -41,6 +41,15 @@ struct DraftParams {
   uint32_t* flags;
   int batch, window, vocab;
   size_t p_bytes, q_bytes;  // extents, for checked builds
+  __device__ __forceinline__ const int32_t* draft(int b, int j) const {
+    return cell(drafts + (long long)b * (window - 1), j, (size_t)window - 1, drafts, (size_t)batch, flags);
+  }
+  __device__ __forceinline__ const float* uniform(int b, int j) const {
+    return cell(uniforms + (long long)b * window, j, (size_t)window, uniforms, (size_t)batch, flags);
+  }
+  __device__ __forceinline__ int32_t* token(int b, int j) const {
+    return cell(tokens + (long long)b * window, j, (size_t)window, tokens, (size_t)batch, flags);
+  }
 };
 
 template <int PF>
@@ -216,12 +225,12 @@ __global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const _
   const long long pb = (long long)b * p.p_batch, qb = (long long)b * p.q_batch;
   if (warp == 0) {
     // every CTA of the cluster judges the drafts; lane j draft j
-    const int d = lane < T - 1 ? __ldg(p.drafts + (long long)b * (T - 1) + lane) : -1;
+    const int d = lane < T - 1 ? __ldg(p.draft(b, lane)) : -1;
     const bool given = d >= 0 && d < V;
     if (lane < T - 1 && d >= V && rank == 0 && p.flags) atomicOr(p.flags, GQA_FLAG_SLOT_CLAMPED);
     bool taken = false;
     if (given) {
-      const float u = __ldg(p.uniforms + (long long)b * T + lane);
+      const float u = __ldg(p.uniform(b, lane));
       const float pd = prob_at<PF>(p.probs, pb + lane * p.p_token + d, p, p.p_bytes);
       const float qd = p.draft_probs ? prob_at<PF>(p.draft_probs, qb + lane * p.q_token + d, p, p.q_bytes) : 1.f;
       taken = (double)u * (double)qd < (double)pd;  // (the product of two floats is exact)
@@ -233,21 +242,22 @@ __global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const _
       s_refused = n < T - 1 && (all_given >> n & 1);
     }
     if (rank == 0) {
-      if (lane < T && lane != n) p.tokens[(long long)b * T + lane] = lane < n ? d : -1;
+      if (lane < T && lane != n) *p.token(b, lane) = lane < n ? d : -1;
       if (lane == 0) {
-        p.accepted[b] = n;
-        if (p.out_lens) p.out_lens[b] = max(p.lens[b] - (T - 1) + n, 0);
+        *item(p.accepted, b, p.batch, p.flags) = n;
+        if (p.out_lens)
+          *item(p.out_lens, b, p.batch, p.flags) = max(*item(p.lens, b, p.batch, p.flags) - (T - 1) + n, 0);
       }
     }
   }
   __syncthreads();
   const int n = s_n;
-  const float u = __ldg(p.uniforms + (long long)b * T + T - 1);
+  const float u = __ldg(p.uniform(b, T - 1));
   DraftRow r;
   r.p0 = pb + n * p.p_token;
   r.q0 = qb + n * p.q_token;
   r.q = s_refused && p.draft_probs != nullptr;
-  r.without = s_refused && p.draft_probs == nullptr ? __ldg(p.drafts + (long long)b * (T - 1) + n) : -1;
+  r.without = s_refused && p.draft_probs == nullptr ? __ldg(p.draft(b, n)) : -1;
   // the warps' runs: consecutive tokens, in whole groups of 32 * 16 bytes
   const int runs = S * kDraftWarps, unit = 32 * ProbTraits<PF>::kVec;
   const int per = ((V + runs - 1) / runs + unit - 1) / unit * unit;
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const _
       continue;
     }
     if (total == 0) {  // no weight at all (zeros, NaN): no token
-      if (rank == 0 && threadIdx.x == 0) p.tokens[(long long)b * T + n] = -1;
+      if (rank == 0 && threadIdx.x == 0) *p.token(b, n) = -1;
       return;
     }
     // floor(total * u), u in units of 2^-24; 128-bit product
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const _
     const unsigned long long target = (total * k) >> 24 | __umul64hi(total, k) << 40;
     if (target >= before && target - before < mine) {
       const int pick = find_token<PF>(p, r, lo, hi, target - before);
-      if (lane == 0) p.tokens[(long long)b * T + n] = pick;
+      if (lane == 0) *p.token(b, n) = pick;
     }
     return;
   }
