@@ -1561,8 +1561,7 @@ gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride, 
                         {workspace, (size_t)GQA_WORKSPACE_HEADER_BYTES}};
   gqa_status_t st = no_aliasing(ins, outs);
   if (st != GQA_OK) return st;
-  int sms = 0;
-  st = current_device_ready(&sms);
+  st = current_device_ready(nullptr);
   if (st != GQA_OK) return st;
   DraftParams p = {};
   p.probs = probs;
@@ -1584,7 +1583,7 @@ gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride, 
   p.p_bytes = p_bytes;
   p.q_bytes = q_bytes;
   const int pf = prob_type == GQA_PROB_F32 ? kPF32 : (prob_type == GQA_PROB_BF16 ? kPBF16 : kPF16);
-  const cudaError_t e = launch_verify_drafts(p, pf, sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_verify_drafts(p, pf, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "draft verification kernel launch");
   return GQA_OK;
 }

@@ -1,6 +1,6 @@
 // The rows of a cache, contiguous or paged, as the kernels that take a prompt's
-// chunk, sum softmax weights or move rows address them, and a row's elements
-// widened to the 16-bit type that the tensor cores multiply.
+// chunk, sum softmax weights or move rows address them, and a narrow row's elements
+// widened to fp16.
 #pragma once
 
 #include "common.cuh"
@@ -52,30 +52,17 @@ __device__ __forceinline__ int clamp_length(int raw, int capacity, uint32_t* fla
   return len;
 }
 
-// f16x2 -> the same two values in QF (exact for what 8 and 4 bits hold).
-template <int QF>
-__device__ __forceinline__ uint32_t f16x2_to(uint32_t h2) {
-  if constexpr (QF == kQF16) return h2;
-  const float2 f = f16x2_to_f32x2(h2);
-  return round2<kQBF16>(f.x, f.y);
-}
-
-// Sixteen consecutive elements of a narrow row as pairs of QF: e4m3 values and int8
-// codes (16 bytes, exact in fp16 and bf16), or e2m1 codes times their e4m3 scale (8
-// bytes; 2 + 4 significand bits and exponents -10..11, exact in both).
-template <int KVF, int QF>
+// Sixteen consecutive elements of a narrow row as pairs of fp16, exactly: e4m3 values and
+// int8 codes (16 bytes), or e2m1 codes times their e4m3 scale (8 bytes; 2 + 4 significand
+// bits and exponents -10..11).
+template <int KVF>
 __device__ __forceinline__ void widen16(const uint32_t* w, uint32_t scale, uint32_t (&d)[8]) {
   if constexpr (KVF == kKvE4M3) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = f16x2_to<QF>(e4m3x2_to_f16x2((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+    for (int i = 0; i < 8; ++i) d[i] = e4m3x2_to_f16x2((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
   } else if constexpr (KVF == kKvI8) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t lo, hi;
-      i8x4_to_f16x2x2(w[i], lo, hi);
-      d[2 * i] = f16x2_to<QF>(lo);
-      d[2 * i + 1] = f16x2_to<QF>(hi);
-    }
+    for (int i = 0; i < 4; ++i) i8x4_to_f16x2x2(w[i], d[2 * i], d[2 * i + 1]);
   } else {
     const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(scale | scale << 8));
 #pragma unroll
@@ -85,17 +72,12 @@ __device__ __forceinline__ void widen16(const uint32_t* w, uint32_t scale, uint3
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[j]), *reinterpret_cast<const __half2*>(&s2));
-        d[4 * i + j] = f16x2_to<QF>(*reinterpret_cast<const uint32_t*>(&y));
+        d[4 * i + j] = *reinterpret_cast<const uint32_t*>(&y);
       }
     }
   }
 }
 
 __device__ __forceinline__ float bf16_bits_to_f32(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-
-template <int QF>
-__device__ __forceinline__ float2 pair_to_f32x2(uint32_t w) {
-  return QF == kQF16 ? f16x2_to_f32x2(w) : bf16x2_to_f32x2(w);
-}
 
 }  // namespace gqa

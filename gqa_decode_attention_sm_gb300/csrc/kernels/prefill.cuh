@@ -450,7 +450,7 @@ __device__ __forceinline__ void row8(const CacheView& c, size_t row, int i, floa
       w[0] = v.x;
       w[1] = v.y;
     }
-    widen16<KVF, kQF16>(w, group, d);
+    widen16<KVF>(w, group, d);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 f = f16x2_to_f32x2(d[k]);
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (!wait(&sm.o_full[t], o_phase)) break;
       o_phase ^= 1;
       tc_fence_after();
-      const bool odd = sm.odd[part & 7] == (uint16_t)(part + 1);
+      const bool odd = !kI8 && sm.odd[part & 7] == (uint16_t)(part + 1);  // (a code of int8 is a number)
       const int slot = 2 * (int)blockIdx.x + (j0 > 0 ? 0 : 1);
       const float f = l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll 1
@@ -742,20 +742,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         __syncwarp();
         tc_ld32(o, o_at + 32 * k);
         tc_wait_ld();
-        if (odd) {
-          // values taken out of V: into the rows that see their slots
-          for (int u = hidden; u <= min(seen, j1 * kPfTile - 1); ++u) {
-            const size_t vrow = cache_row(p.c, b, kHkv + g, u);
+        if constexpr (!kI8) {
+          if (odd) {
+            // values taken out of V: into the rows that see their slots
+            for (int u = hidden; u <= min(seen, j1 * kPfTile - 1); ++u) {
+              const size_t vrow = cache_row(p.c, b, kHkv + g, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float y[8];
-              row8<KVF>(p.c, vrow, 4 * k + i, y);
+              for (int i = 0; i < 4; ++i) {
+                float y[8];
+                row8<KVF>(p.c, vrow, 4 * k + i, y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (!(fabsf(y[e]) <= 3.4e38f)) o[8 * i + e] = __float_as_uint(__uint_as_float(o[8 * i + e]) + y[e]);
+                for (int e = 0; e < 8; ++e)
+                  if (!(fabsf(y[e]) <= 3.4e38f)) o[8 * i + e] = __float_as_uint(__uint_as_float(o[8 * i + e]) + y[e]);
+              }
             }
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (whole) {
           // four lanes hold a token's four heads: turned about, so that they store 64
@@ -995,11 +997,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                   if constexpr (KVF == kKvE2M1) {
                     const uint2 v = *reinterpret_cast<const uint2*>(bytes + row * 64 + piece * 8);
                     const uint32_t w[2] = {v.x, v.y};
-                    widen16<KVF, kQF16>(w, bytes[kPfTile * 64 + row * 8 + piece], d[i]);
+                    widen16<KVF>(w, bytes[kPfTile * 64 + row * 8 + piece], d[i]);
                   } else {
                     const uint4 v = *reinterpret_cast<const uint4*>(bytes + row * 128 + piece * 16);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    widen16<KVF, kQF16>(w, 0, d[i]);
+                    widen16<KVF>(w, 0, d[i]);
                   }
                 }
                 if (tail || check) {

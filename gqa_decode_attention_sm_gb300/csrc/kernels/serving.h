@@ -15,7 +15,7 @@ namespace gqa {
 cudaError_t serving_setup();  // once a device
 cudaError_t prefill_setup();  // once a device
 cudaError_t launch_prefill(const PrefillParams& p, int kvf, int qf, cudaStream_t stream);
-cudaError_t launch_verify_drafts(const DraftParams& p, int pf, int sms, cudaStream_t stream);
+cudaError_t launch_verify_drafts(const DraftParams& p, int pf, cudaStream_t stream);
 cudaError_t launch_sum_weights(const WeightParams& p, int kvf, int qf, int q_len, int sms, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, int kvf, int sms, cudaStream_t stream);
 

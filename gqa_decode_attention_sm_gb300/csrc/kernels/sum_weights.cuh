@@ -72,8 +72,7 @@ struct RowPart {
     if constexpr (KVF == kKvI8) scale = __ldg(static_cast<const uint16_t*>(c.scales) + row);
     if constexpr (KVF == kKvE2M1) scale = __ldg(static_cast<const uint16_t*>(c.scales) + row * 4 + part);
   }
-  // its 16 pairs
-  template <int QF>
+  // its 16 pairs, a narrow row's in fp16
   __device__ __forceinline__ void pairs(uint32_t (&d)[16]) const {
     if constexpr (!is_narrow(KVF)) {
 #pragma unroll
@@ -92,7 +91,7 @@ struct RowPart {
         uint32_t w[kW], o[8];
 #pragma unroll
         for (int j = 0; j < kW; ++j) w[j] = all[KVF == kKvE2M1 ? 2 * i + j : j];
-        widen16<KVF, QF>(w, KVF == kKvE2M1 ? (scale >> (8 * i)) & 0xff : 0u, o);
+        widen16<KVF>(w, KVF == kKvE2M1 ? (scale >> (8 * i)) & 0xff : 0u, o);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[8 * i + j] = o[j];
       }
@@ -190,7 +189,7 @@ __device__ __forceinline__ void score_rows(const WeightParams& p, int q_len, int
       float row_scale[2] = {1.f, 1.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        next[u][k].template pairs<MF>(a[k]);
+        next[u][k].pairs(a[k]);
         if constexpr (KVF == kKvI8) row_scale[k] = bf16_bits_to_f32((uint16_t)next[u][k].scale);
       }
       if (t0 + kStep < end) {

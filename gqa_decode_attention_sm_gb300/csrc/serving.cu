@@ -37,7 +37,7 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, in
 
 }  // namespace
 
-cudaError_t launch_verify_drafts(const DraftParams& p, int pf, int sms, cudaStream_t stream) {
+cudaError_t launch_verify_drafts(const DraftParams& p, int pf, cudaStream_t stream) {
   constexpr int S = kDraftCluster;
   const dim3 grid((unsigned)(p.batch * S));
   switch (pf) {
