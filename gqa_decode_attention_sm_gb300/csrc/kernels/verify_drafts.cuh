@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kDraftThreads, 4) verify_drafts_kernel(const _
       if (lane == 0) {
         *item(p.accepted, b, p.batch, p.flags) = n;
         if (p.out_lens)
-          *item(p.out_lens, b, p.batch, p.flags) = max(*item(p.lens, b, p.batch, p.flags) - (T - 1) + n, 0);
+          *item(p.out_lens, b, p.batch, p.flags) = max(max(*item(p.lens, b, p.batch, p.flags), 0) - (T - 1) + n, 0);  // (no overflow)
       }
     }
   }

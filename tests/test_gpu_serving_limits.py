@@ -9,8 +9,8 @@ import pytest
 import torch
 
 import gqa_decode_attention_sm_gb300 as gq
-from test_gpu_serving import (D, DEV, HKV, HQ, TD, attend64, gen, kept64, library, new_cache,  # noqa: F401
-                              paged, values)
+from test_gpu_serving import (D, DEV, HKV, HQ, TD, attend64, draft_inputs, gen, kept64, library,  # noqa: F401
+                              new_cache, paged, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -238,3 +238,16 @@ def test_sizes_past_an_int(library):  # noqa: F811
         gq.verify_drafts(torch.zeros((1, 1, 2 ** 32 + 5), dtype=torch.float16, device=DEV),
                          torch.zeros((1, 0), dtype=torch.int32, device=DEV), torch.zeros((1, 1), device=DEV))
     torch.cuda.empty_cache()
+
+
+# -------------------------------------------------- drafts: lengths and large sums
+
+
+def test_drafts_lengths_below_zero(library):  # noqa: F811
+    """max(length - (T - 1) + n, 0) of any int, without overflow."""
+    p, d, u, q, _ = draft_inputs(6, 4, 50, "f32", seed=80)
+    low = -2 ** 31
+    lens = torch.tensor([low, low + 1, low + 2, -1, 0, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    tokens, accepted = gq.verify_drafts(p, d, u, draft_probs=q, sequence_lengths=lens)
+    assert lens[:4].tolist() == [0] * 4
+    assert int(lens[4]) == 0 and int(lens[5]) == 2 ** 31 - 1 - 3 + int(accepted[5])
