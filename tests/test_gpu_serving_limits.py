@@ -251,3 +251,82 @@ def test_drafts_lengths_below_zero(library):  # noqa: F811
     tokens, accepted = gq.verify_drafts(p, d, u, draft_probs=q, sequence_lengths=lens)
     assert lens[:4].tolist() == [0] * 4
     assert int(lens[4]) == 0 and int(lens[5]) == 2 ** 31 - 1 - 3 + int(accepted[5])
+
+
+# ----------------------------------------------------------------- largest sizes
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_drafts_largest_vocabulary(library, dtype):  # noqa: F811
+    """2^24 tokens, and terms of 2^38 units each (their sum is 2^62)."""
+    V = 1 << 24
+    d, u = torch.zeros((3, 0), dtype=torch.int32, device=DEV), torch.tensor([[0.0], [0.3], [1 - 2.0 ** -24]], device=DEV)
+    p = torch.ones((3, 1, V), dtype=TD[dtype], device=DEV)
+    tokens, accepted = gq.verify_drafts(p, d, u)
+    assert tokens[:, 0].tolist() == [int(math.floor(float(x) * 2 ** 24)) for x in u]
+    p = torch.rand((3, 1, V), generator=gen(81), device=DEV).to(TD[dtype])
+    tokens, _ = gq.verify_drafts(p, d, u)
+    w = (p[:, 0].float().clamp(0, 1).double() * 2.0 ** 38).round().long()
+    upto = w.cumsum(1)
+    for b in range(3):
+        target = int(upto[b, -1]) * int(math.floor(float(u[b, 0]) * 2 ** 24)) >> 24
+        assert int(tokens[b, 0]) == int(torch.searchsorted(upto[b], target, right=True))
+
+
+@pytest.mark.parametrize("C", [65536, 400032])  # above 393216 slots the weights are read again each time
+def test_evict_long_rows(library, C):  # noqa: F811
+    kv, _ = new_cache("e4m3", 1, C, 82)
+    w = torch.rand((1, HKV, C), generator=gen(83), device=DEV)
+    w[0, 1] = (w[0, 1] * 8).floor()  # ties over all of the row
+    w[0, 2, ::3] = NAN
+    w[0, 3] -= 0.5
+    L, keep, recent, first = C - 77, C // 5, 300, 7
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    out = torch.zeros((1, 2, HKV, keep, D), dtype=torch.uint8, device=DEV)
+    ol, ow = torch.zeros_like(lens), torch.zeros((1, HKV, keep), device=DEV)
+    ws = torch.zeros(gq.evict_workspace_size(1, keep), dtype=torch.uint8, device=DEV)
+    kept = gq.evict_kv(kv, lens, w, keep, recent, first, out=out, out_lengths=ol, out_weights=ow, workspace=ws)
+    assert gq.get_status(ws) == 0 and int(ol) == keep
+    key = torch.where(torch.isnan(w[0, :, :L]), -INF, w[0, :, :L])
+    key[:, :first] = INF
+    key[:, L - recent:] = INF
+    order = torch.sort(key, dim=-1, descending=True, stable=True).indices[:, :keep]
+    want = torch.sort(order, dim=-1).values
+    assert torch.equal(kept[0].long(), want)
+    assert torch.equal(out[0], kv[0].gather(2, want[None, :, :, None].expand(2, HKV, keep, D)))
+    assert torch.equal(ow[0].view(torch.int32), w[0].gather(1, want).view(torch.int32))
+    # in place: the same slots
+    gq.evict_kv(kv, lens, w, keep, recent, first, kept=kept, workspace=ws)
+    assert gq.get_status(ws) == 0 and int(lens) == keep and torch.equal(kept[0].long(), want)
+    assert torch.equal(kv[:, :, :, :keep], out)
+
+
+def test_evict_keep_past_the_capacity(library):  # noqa: F811
+    """More slots asked for than the cache has: all stay."""
+    kv, _ = new_cache("bf16", 2, 50, 84)
+    w = torch.rand((2, HKV, 50), generator=gen(85), device=DEV)
+    lens = torch.tensor([50, 17], dtype=torch.int32, device=DEV)
+    out, ol = torch.zeros((2, 2, HKV, 130, D), dtype=torch.bfloat16, device=DEV), torch.zeros_like(lens)
+    ow = torch.full((2, HKV, 140), 5.0, device=DEV)
+    kept = gq.evict_kv(kv, lens, w, 120, 100, 20, out=out, out_lengths=ol, out_weights=ow)
+    before, old = kv.clone(), w.clone()
+    same = gq.evict_kv(kv, lens, w, 120, 100, 20)
+    assert torch.equal(kept, same) and torch.equal(kv, before) and torch.equal(w, old) and lens.tolist() == [50, 17]
+    for b, n in enumerate((50, 17)):
+        assert kept[b].tolist() == [list(range(n)) + [-1] * (120 - n)] * HKV and int(ol[b]) == n
+        assert torch.equal(out[b, :, :, :n], kv[b, :, :, :n]) and not out[b, :, :, n:].any()
+        assert torch.equal(ow[b, :, :n], w[b, :, :n]) and not ow[b, :, n:].any()
+
+
+def test_prefill_padding_in_front(library):  # noqa: F811
+    """The first chunk may start behind padding."""
+    kv, _ = new_cache("f16", 2, 200, 86)
+    q = torch.randn((100, HQ, D), generator=gen(87), device=DEV).half()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lens = torch.tensor([150, 199], **i32)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    out = torch.full_like(q, 3.0)
+    gq.gqa_prefill(q, kv, torch.tensor([13, 50, 90], **i32), lens, out=out, workspace=ws)
+    assert gq.get_status(ws) == 0 and (out[:13] == 3.0).all() and (out[90:] == 3.0).all()
+    want = gq.gqa_prefill(q[13:90].contiguous(), kv, torch.tensor([0, 37, 77], **i32), lens)
+    assert torch.equal(out[13:90], want)
