@@ -23,18 +23,20 @@
 // row into fp16's range, so these calls have fp16 products whatever q's type is.
 // int8 scales multiply the columns of S and of P.
 //
-// Measured (GB300, in a CUDA graph): 8192 bf16 tokens 350 us, 1573 TFLOP/s, 0.81 of the
-// library GEMM's burst rate, at clocks that the power limit has already lowered; 512
-// tokens over 131072 slots in pages 740 us, 1484.  A tile pair takes 4 products of 512
-// tensor clocks; the rest is the chain S -> maximum -> 2^x -> P of a row (1380 clocks),
-// the issuing warp's steps and the latency between the two, of which the other tile
-// covers a part.  152 CTAs ask for 64 KB each tile: of one long row's K and V most comes
+// Measured (GB300, calls back to back; ranges are GPUs and the clock that the power limit
+// leaves): 8192 bf16 tokens 350 to 385 us, 1430 to 1573 TFLOP/s, 0.73 to 0.81 of the
+// library GEMM's burst rate; 512 tokens over 131072 slots in pages 740 to 866 us.  A tile
+// pair takes 4 products of 512 tensor clocks; the rest is the chain S -> maximum -> 2^x ->
+// P of a row (1380 clocks), the issuing warp's steps and the latency between the two, of
+// which the other tile covers a part.  152 CTAs ask for 64 KB each tile: of one long row's K and V most comes
 // from L2; 16 rows' units lie too far apart for it (1.65 GB from HBM in 390 us, 4.2
 // TB/s), which costs no more than 5 %: the same chunks over one row's pages take 374 and
 // 376 us or, of longer rows, 596 and 626.  Narrow caches are bound by the two widening
-// warps: of 1980 clocks a K or V tile of e2m1 they widen for 1560 and wait for 370 (raw
-// codes read one step ahead: 729 us before and after; a third warp: 1108 us, its
-// registers are the softmax's).
+// warps: of 2260 clocks a K or V tile of e2m1 they widen for 1690 and wait for 390, of
+// e4m3's 2090 for 1560 and 380 (raw codes read one step ahead: 729 us before and after; a
+// third warp: 1108 us, its registers are the softmax's).  int8's softmax threads have two
+// scale products more a column, and its raw tiles (two, each told only when the next
+// one's copies are issued) keep the widening warps waiting for 1050 of 3440 clocks.
 //
 // All rows' tiles form one stream that the resident CTAs (one an SM) cut into equal
 // runs, whatever the lengths are; a unit cut by a run's end leaves FP32 partials (two a

@@ -1,6 +1,8 @@
 // The attention of chunks of new tokens, in a translation unit of its own.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "gqa_decode.h"
 #include "kernels/serving.h"
 
@@ -8,11 +10,12 @@ namespace gqa {
 
 namespace {
 
-// The driver's encoder of tensor maps, looked up once (no link to the driver library).
+// The driver's encoder of tensor maps, looked up at a device's first call (no link to the
+// driver library; two devices' first calls may meet, and find the same).
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-Encode g_encode = nullptr;
+std::atomic<Encode> g_encode{nullptr};
 
 // A cache's rows in boxes of `box`: of a 16-bit cache 64 elements wide and swizzled, of
 // a narrow one whole rows as they are.
@@ -22,13 +25,13 @@ cudaError_t encode_rows(CUtensorMap* map, const CacheView& c, int kvf, int box) 
   if (is_narrow(kvf)) {
     const cuuint64_t width = (cuuint64_t)kv_row_bytes(kvf), dims[2] = {width, c.rows}, strides[1] = {width};
     const cuuint32_t tile[2] = {(cuuint32_t)width, (cuuint32_t)box};
-    r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.kv), dims, strides, tile, steps,
+    r = g_encode.load()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.kv), dims, strides, tile, steps,
                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   } else {
     const cuuint64_t dims[2] = {kD, c.rows}, strides[1] = {2 * kD};
     const cuuint32_t tile[2] = {kD / 2, (cuuint32_t)box};
-    r = g_encode(map, kvf == kKvBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+    r = g_encode.load()(map, kvf == kKvBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                  const_cast<void*>(c.kv), dims, strides, tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
@@ -67,7 +70,7 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& map, cudaStream_
 static_assert(sizeof(PfShared) <= 227 * 1024, "shared memory of a CTA");
 
 cudaError_t prefill_setup() {
-  if (!g_encode) {
+  if (!g_encode.load()) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
     const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
