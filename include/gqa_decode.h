@@ -604,7 +604,8 @@ gqa_status_t gqa_verify_drafts(const void* probs, long long probs_batch_stride,
  * none but such, gives no weight at all; a NaN score makes NaN of the weights that
  * its head's query gives.  Pointers 16-byte aligned (int8
  * scales 2, e2m1 scales 8, lens 4).  The workspace holds
- * gqa_weights_workspace_size(batch, capacity, q_len) bytes (0: invalid sizes).
+ * gqa_weights_workspace_size(batch, capacity, q_len) bytes (0: invalid sizes), the
+ * scores of the whole capacity among them, whichever way the call takes.
  * One launch where a row's scores fit on chip and the batch fills the GPU or the
  * capacity is at most 8192, else two; no allocation, no host sync. */
 size_t gqa_weights_workspace_size(int batch, int capacity, int q_len);
