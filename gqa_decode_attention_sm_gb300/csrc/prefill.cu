@@ -19,23 +19,31 @@ std::atomic<Encode> g_encode{nullptr};
 
 // A cache's rows in boxes of `box`: of a 16-bit cache 64 elements wide and swizzled, of
 // a narrow one whole rows as they are.
-cudaError_t encode_rows(CUtensorMap* map, const CacheView& c, int kvf, int box) {
+CUresult encode(CUtensorMap* map, const CacheView& c, int kvf, int box) {
   const cuuint32_t steps[2] = {1, 1};
-  CUresult r;
   if (is_narrow(kvf)) {
     const cuuint64_t width = (cuuint64_t)kv_row_bytes(kvf), dims[2] = {width, c.rows}, strides[1] = {width};
     const cuuint32_t tile[2] = {(cuuint32_t)width, (cuuint32_t)box};
-    r = g_encode.load()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.kv), dims, strides, tile, steps,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  } else {
-    const cuuint64_t dims[2] = {kD, c.rows}, strides[1] = {2 * kD};
-    const cuuint32_t tile[2] = {kD / 2, (cuuint32_t)box};
-    r = g_encode.load()(map, kvf == kKvBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                 const_cast<void*>(c.kv), dims, strides, tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return g_encode.load()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(c.kv), dims, strides, tile, steps,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   }
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint64_t dims[2] = {kD, c.rows}, strides[1] = {2 * kD};
+  const cuuint32_t tile[2] = {kD / 2, (cuuint32_t)box};
+  return g_encode.load()(map, kvf == kKvBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                         const_cast<void*>(c.kv), dims, strides, tile, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+cudaError_t encode_rows(CUtensorMap* map, const CacheView& c, int kvf, int box) {
+  if (encode(map, c, kvf, box) == CUDA_SUCCESS) return cudaSuccess;
+  // A thread that has not called the runtime yet has no current context, which the
+  // driver's encoder asks for; setting the device that it has gives it one.
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return encode(map, c, kvf, box) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int KVF, int QF>

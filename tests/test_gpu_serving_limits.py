@@ -4,13 +4,14 @@ does not see, infinite scores, weights of every kind, calls without a token (GPU
 Bounds as in test_gpu_serving.py, with what each test says of its own.
 """
 import math
+import threading
 
 import pytest
 import torch
 
 import gqa_decode_attention_sm_gb300 as gq
 from test_gpu_serving import (D, DEV, HKV, HQ, TD, attend64, draft_inputs, gen, kept64, library,  # noqa: F401
-                              new_cache, paged, values)
+                              new_cache, paged, run_together, serving_state, together_buffers, values)
 
 pytestmark = pytest.mark.gpu
 
@@ -330,3 +331,89 @@ def test_prefill_padding_in_front(library):  # noqa: F811
     assert gq.get_status(ws) == 0 and (out[:13] == 3.0).all() and (out[90:] == 3.0).all()
     want = gq.gqa_prefill(q[13:90].contiguous(), kv, torch.tensor([0, 37, 77], **i32), lens)
     assert torch.equal(out[13:90], want)
+
+
+# ------------------------------------------------------------------ fresh threads
+
+
+def in_thread(f):
+    """f() in a thread that has made no call of the GPU before; what it raised."""
+    raised = []
+
+    def run():
+        try:
+            f()
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    return raised
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_first_call_of_a_thread(library, fmt):  # noqa: F811
+    """Each call as a thread's first work on the GPU, with every buffer given, so that
+    nothing before it gives the thread a context."""
+    s = serving_state(fmt)
+    ws = together_buffers(s)
+    fill = ws["kv"].clone()  # (slots past the new length keep it)
+    want = [x.clone() for x in run_together(s, ws)]
+    B = s["B"]
+    ks, vs = (0.4, 0.7) if fmt == "e2m1" else (1.0, 1.0)
+    q = s["q"].view(B, -1, HQ, D)[:, :2].contiguous()
+    torch.cuda.synchronize()
+    calls = [
+        lambda: gq.gqa_prefill(s["q"], s["kv"], s["starts"], s["lens"], k_scale=ks, v_scale=vs, kv_scales=s["sc"], out=ws["out"],
+                               workspace=ws["prefill"]),
+        lambda: gq.accumulate_weights(q, s["kv"], s["lens"], ws["w"], k_scale=ks, kv_scales=s["sc"], add=False,
+                                      workspace=ws["weights"]),
+        lambda: gq.verify_drafts(ws["p"], ws["d"], ws["u"], draft_probs=ws["dq"], sequence_lengths=s["lens"],
+                                 out_lengths=ws["len1"], tokens=ws["tokens"], accepted=ws["accepted"]),
+        lambda: gq.evict_kv(s["kv"], ws["len1"], ws["w"], 100, 16, 4, out=ws["kv"], out_scales=ws["sc"],
+                            out_lengths=ws["len2"], out_weights=ws["w2"], kept=ws["kept"], kv_scales=s["sc"],
+                            workspace=ws["evict"]),
+    ]
+    for x in (ws["out"], ws["w"], ws["tokens"], ws["accepted"], ws["len1"], ws["kept"], ws["len2"], ws["w2"]):
+        x.zero_()
+    ws["kv"].copy_(fill)
+    torch.cuda.synchronize()
+    for call in calls:
+        assert not in_thread(call)
+    got = [ws["out"], ws["w"], ws["tokens"], ws["accepted"], ws["len1"], ws["kept"], ws["kv"], ws["len2"], ws["w2"]]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_threads_at_once(library):  # noqa: F811
+    """Four threads, each on a stream and with buffers of its own, all calls many times."""
+    s = serving_state("bf16")
+    want = [x.clone() for x in run_together(s, together_buffers(s))]
+    buffers = [together_buffers(s) for _ in range(4)]
+    torch.cuda.synchronize()
+    raised, barrier = [], threading.Barrier(4)
+
+    def work(ws):
+        try:
+            stream = torch.cuda.Stream()
+            barrier.wait(30)
+            with torch.cuda.stream(stream):
+                for _ in range(25):
+                    run_together(s, ws)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            raised.append(e)
+    threads = [threading.Thread(target=work, args=(ws,)) for ws in buffers]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not raised
+    for ws in buffers:
+        got = [ws["out"], ws["w"], ws["tokens"], ws["accepted"], ws["len1"], ws["kept"], ws["kv"], ws["len2"], ws["w2"]]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        for name in ("prefill", "weights", "evict"):
+            assert gq.get_status(ws[name]) == 0
