@@ -274,6 +274,46 @@ def test_drafts_largest_vocabulary(library, dtype):  # noqa: F811
         assert int(tokens[b, 0]) == int(torch.searchsorted(upto[b], target, right=True))
 
 
+def test_drafts_rows_far_apart(library):  # noqa: F811
+    """Rows 2^32 elements apart, at an odd 16-bit offset."""
+    V, apart = 3001, 2 ** 32 + 1
+    p, d, u, q, lens = draft_inputs(2, 3, V, "f16", seed=88)
+    want = gq.verify_drafts(p, d, u, draft_probs=q, sequence_lengths=lens.clone())
+    far = torch.empty(apart + 4 * V, dtype=torch.float16, device=DEV)  # 8 GB
+    wide = far.as_strided((2, 3, V), (apart, V + 2, 1), 1)
+    wide.copy_(p)
+    got = gq.verify_drafts(wide, d, u, draft_probs=q, sequence_lengths=lens)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del far, wide
+    torch.cuda.empty_cache()
+
+
+def test_prefill_many_tokens(library):  # noqa: F811
+    """More than 2^31 elements of q and out (4.9 GB each)."""
+    B, n = 600, 1000
+    kv = torch.randn((1, 2, HKV, n, D), generator=gen(89), device=DEV).to(torch.bfloat16)
+    pool = torch.zeros((2 * 16, 2, HKV, 64, D), dtype=torch.bfloat16, device=DEV)
+    for k in range(16):  # (every row has the same pages)
+        part = kv[0, :, :, 64 * k:64 * (k + 1)]
+        pool[k, :, :, :part.shape[2]] = part
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.arange(16, **i32).repeat(B, 1)
+    q = torch.empty((B * n, HQ, D), dtype=torch.bfloat16, device=DEV)
+    for b in range(B):
+        q[b * n:(b + 1) * n] = torch.randn((n, HQ, D), generator=gen(b), device=DEV).to(torch.bfloat16)
+    out = torch.empty_like(q)
+    ws = torch.zeros(gq.prefill_workspace_size(), dtype=torch.uint8, device=DEV)
+    gq.gqa_prefill_paged(q, pool, table, torch.arange(0, B * n + 1, n, **i32), torch.full((B,), n, **i32), out=out, workspace=ws)
+    assert gq.get_status(ws) == 0
+    half = 2.0 ** -8
+    K, V = kv[0, 0].double(), kv[0, 1].double()
+    for t in (0, n - 1, 524287, 524288, 524289, B * n - n, B * n - 1):
+        ref, a, e = attend64(q[t], K, V, t % n + 1)
+        assert ((out[t].double() - ref).abs() <= half * ref.abs() + (half + 2 * e + 2 ** -18) * a + 2 ** -126).all(), t
+    del q, out
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("C", [65536, 400032])  # above 393216 slots the weights are read again each time
 def test_evict_long_rows(library, C):  # noqa: F811
     kv, _ = new_cache("e4m3", 1, C, 82)
@@ -417,3 +457,67 @@ def test_threads_at_once(library):  # noqa: F811
             assert torch.equal(a, b)
         for name in ("prefill", "weights", "evict"):
             assert gq.get_status(ws[name]) == 0
+
+
+# ------------------------------------------------- block tables past the length
+
+
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("fmt", ["bf16", "i8", "e2m1"])
+def test_table_entries_past_the_length(library, fmt, page):  # noqa: F811
+    """Entries that no slot in use needs may hold anything: they are neither read from nor told."""
+    B, C = 3, 1024
+    kv, sc = new_cache(fmt, B, C, 90)
+    pool, psc, table = paged(kv, sc, page, B, C, 91)
+    lens = torch.tensor([1, 3 * page + 1, 2 * page], dtype=torch.int32, device=DEV).clamp(max=C)
+    wild = table.clone()
+    for b, L in enumerate(lens.tolist()):
+        wild[b, -(-L // page):] = torch.tensor([-1, 2 ** 31 - 1, -2 ** 31, 10 ** 6], dtype=torch.int32,
+                                               device=DEV).repeat(C)[:C // page - -(-L // page)]
+    n = [1, 20, 33]
+    n[2] = min(n[2], int(lens[2]))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, n[0], n[0] + n[1], sum(n)], **i32)
+    q = torch.randn((sum(n), HQ, D), generator=gen(92), device=DEV).to(torch.bfloat16)
+    w0, keep = torch.rand((B, HKV, C), generator=gen(93), device=DEV), 2 * page - 3
+    got = []
+    for t in (table, wild):
+        ws = [torch.zeros(k, dtype=torch.uint8, device=DEV) for k in (
+            gq.prefill_workspace_size(), gq.weights_workspace_size(B, C, 1), gq.evict_workspace_size(B, keep))]
+        out = gq.gqa_prefill_paged(q, pool, t, starts, lens, kv_scales=psc, workspace=ws[0])
+        w = gq.accumulate_weights_paged(q[:B], pool, t, lens, w0.clone(), kv_scales=psc, workspace=ws[1])
+        p2, s2, l2 = pool.clone(), None if psc is None else psc.clone(), lens.clone()
+        kept = gq.evict_kv_paged(p2, t, l2, w, keep, 5, 2, kv_scales=s2, workspace=ws[2])
+        assert [gq.get_status(x) for x in ws] == [0, 0, 0]
+        got.append([out, w, kept, p2.view(torch.uint8), l2])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------- types of the bytes
+
+
+def test_float8_types(library):  # noqa: F811
+    """A cache of torch.float8_e4m3fn, and e2m1 scales of it, as the same bytes in uint8."""
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lens, starts = torch.tensor([200, 77], **i32), torch.tensor([0, 30, 100], **i32)
+    q = torch.randn((100, HQ, D), generator=gen(95), device=DEV).to(torch.bfloat16)
+    for fmt in ("e4m3", "e2m1"):
+        kv, sc = new_cache(fmt, 2, 200, 94)
+        w0 = torch.rand((2, HKV, 200), generator=gen(96), device=DEV)
+        got = []
+        for as8 in (False, True):
+            f8 = torch.float8_e4m3fn
+            x = kv.view(f8) if as8 and fmt == "e4m3" else kv
+            s = sc.view(f8) if as8 and sc is not None else sc
+            out = gq.gqa_prefill(q, x, starts, lens, kv_scales=s)
+            w = gq.accumulate_weights(q[:2], x, lens, w0.clone(), kv_scales=s)
+            y, ys = torch.zeros_like(x[:, :, :, :50]), None if s is None else torch.zeros_like(s[:, :, :, :50])
+            ol = torch.zeros_like(lens)
+            kept = gq.evict_kv(x, lens, w, 50, 5, 2, out=y, out_scales=ys, out_lengths=ol, kv_scales=s)
+            got.append([out, w, y.view(torch.uint8), kept, ol] + ([] if ys is None else [ys.view(torch.uint8)]))
+            if as8 and fmt == "e4m3":
+                with pytest.raises(ValueError):
+                    gq.evict_kv(x, lens, w, 50, 5, 2, out=torch.zeros_like(kv[:, :, :, :50]), out_lengths=ol)
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
